@@ -47,30 +47,30 @@ def _compact(name, **k):
 def listed():
     return [
         # one short chat, 4 query heads on one KV head, pages of 16: a call whose latency counts
-        _decode("decode, one short stream", q_heads=4, kv_heads=1, window=128, page=16, idx=0),
+        _decode("decode: one short stream", q_heads=4, kv_heads=1, window=128, page=16, idx=0),
         # four ragged streams, the new token stored by the call
-        _decode("decode, four streams", streams=4, longest=9001, store=True),
+        _decode("decode: four streams", streams=4, longest=9001, store=True),
         # a full launch of long streams: bound by the window's K and V bytes
-        _decode("decode, 64 long streams", streams=64, longest=40956, window=4096, store=True),
+        _decode("decode: 64 long streams", streams=64, longest=40956, window=4096, store=True),
         # the same in the e4m3 page format
-        _decode("decode, e4m3 pages", format="e4m3", streams=32, longest=24000, window=4096, page=128),
+        _decode("decode: e4m3 pages", format="e4m3", streams=32, longest=24000, window=4096, page=128),
         # speculative decoding: four draft tokens a stream, an odd window, pages that end inside a tile
-        _decode("decode, draft windows", streams=8, longest=16384, new=4, window=2047, sinks=3, page=48, store=True),
+        _decode("decode: draft windows", streams=8, longest=16384, new=4, window=2047, sinks=3, page=48, store=True),
         # short ragged prompt chunks on pages of 20
-        _prefill("prefill, short chunks", streams=3, longest=1000, new=40, q_heads=4, kv_heads=1, window=500, sinks=1,
+        _prefill("prefill: short chunks", streams=3, longest=1000, new=40, q_heads=4, kv_heads=1, window=500, sinks=1,
                  page=20, idx=0),
         # a 512-token chunk on a long context
-        _prefill("prefill, chunk at 31000", longest=31512, window=4096),
+        _prefill("prefill: chunk at 31000", longest=31512, window=4096),
         # a whole prompt of 8192 tokens
-        _prefill("prefill, whole prompt", longest=8192, new=8192),
+        _prefill("prefill: whole prompt", longest=8192, new=8192),
         # a fork of four streams in the middle of a page: the tails' rows
-        _copy("copy, tails of a fork", positions=77),
+        _copy("copy: tails of a fork", positions=77),
         # whole pages of 7.9 MB each
-        _copy("copy, whole pages", pages=96),
+        _copy("copy: whole pages", pages=96),
         # a small arena of e4m3 pages made dense again
-        _compact("compact, small pages", format="e4m3", layers=4, page=16, streams=4, each=40, moves=50),
+        _compact("compact: small pages", format="e4m3", layers=4, page=16, streams=4, each=40, moves=50),
         # a serving arena: 16 streams, 300 pages moved down and every table rewritten
-        _compact("compact, serving arena", streams=16, each=40, moves=300),
+        _compact("compact: serving arena", streams=16, each=40, moves=300),
     ]
 
 
