@@ -193,13 +193,43 @@ int pkv_arena_info(pkv_arena *arena, int32_t *n_pages, int32_t *n_free, int64_t 
 int pkv_pages_take(pkv_arena *arena, int32_t n, int32_t *ids_out);
 /* Give pages back.  With `defer` nonzero the pages return once the work
  * queued on `stream` so far has finished (an event is recorded); with defer
- * == 0 they return now and the caller asserts the stream has drained.
- * EINVAL for an id outside the arena or not taken (nothing changes then). */
+ * == 0 they return now and the caller asserts the stream has drained.  A page
+ * with several holders (pkv_pages_fork) loses one and is free once it has
+ * none.  EINVAL for an id outside the arena, not taken, listed twice, or
+ * whose holders have all given it already (nothing changes then). */
 int pkv_pages_give(pkv_arena *arena, const int32_t *ids, int32_t n, cudaStream_t stream,
                    int32_t defer);
 /* Fill a pkv_pg for a stream of this arena; dev_table holds n_table ids. */
 int pkv_arena_pg(const pkv_arena *arena, const int32_t *dev_table, int32_t n_table,
                  pkv_pg *out);
+
+/* Fork a stream of `len` positions (an addition: the pages have no sharing).
+ * ids: its n = ceil(len / page_pos) pages in logical order, -1 for a page
+ * already given back (behind a window).  Every whole page gets one more
+ * holder and goes into ids_out as it is (-1 stays -1); a last page that `len`
+ * ends inside is not shared: the fork takes a fresh page for it (the lowest
+ * free id), and *copy_src, *copy_dst and *copy_pos say which page's first
+ * copy_pos positions to copy into it (pkv_pages_copy) before the fork is
+ * read; they are -1, -1 and 0 when len is whole pages.  EAGAIN when that page
+ * is not to be had, EINVAL for an id outside the arena, not held, listed
+ * twice, a wrong n, or a last page that is -1 with len inside it; nothing
+ * changes then.  Stores into a shared page change it for every holder: only
+ * whole pages are shared, and a stream writes behind its length. */
+int pkv_pages_fork(pkv_arena *arena, const int32_t *ids, int32_t n, int32_t len, int32_t *ids_out,
+                   int32_t *copy_src, int32_t *copy_dst, int32_t *copy_pos);
+/* Holders of each page, those whose give is pending no longer counted: 0 for
+ * a free page or a run's.  EINVAL for an id outside the arena. */
+int pkv_pages_holders(pkv_arena *arena, const int32_t *ids, int32_t n, int32_t *holders_out);
+/* Plan a compaction (an addition): the held KV pages with the highest ids
+ * move to the lowest free ids below them, at most max_moves of them; src_out
+ * and dst_out (room for max_moves each) get *n_out moves, the highest page
+ * first.  The arena's books change at once: dst has src's holders, and src is
+ * held once more, by the caller, who queues the copies (pkv_pages_copy) and
+ * the tables' rewrite (pkv_tables_remap) on the streams' stream, renames the
+ * pages in its own lists, and gives the src ids back with `defer` set.  Run
+ * pages and pages being given back stay where they are. */
+int pkv_arena_compact(pkv_arena *arena, int32_t max_moves, int32_t *src_out, int32_t *dst_out,
+                      int32_t *n_out);
 
 /* Event operations used for deferred release; the default is CUDA events.
  * record: 0 and *ev set on success; query: 0 done, 1 pending, <0 failed. */
@@ -261,6 +291,34 @@ int pkv_store(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int
  * [sum len/4][Di].  Restoring is pkv_store with n_new = len. */
 int pkv_gather(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
                int32_t kind, void *out, int32_t *dev_status, cudaStream_t stream);
+
+/* ---- page copies (an addition: forks and compaction) -------------------------
+ * Copy pages inside the arena at `base` (n_pages pages of page_pos positions
+ * of `layout`): page src[i] to page dst[i] for i < n, all layers; with n_pos
+ * non-NULL only its first n_pos[i] positions (0 .. page_pos): their K, V and
+ * indexer rows (codes and scales for an e4m3 layout) and the pooled rows of
+ * their n_pos[i]/4 whole blocks, every other byte of the page left as it was.
+ * Bytes move unchanged.  src, dst and n_pos are host arrays, read before the
+ * call returns.  A src may repeat (a fan-out); EINVAL for an id outside the
+ * arena, a dst that repeats or is also a src, n_pos out of range, a base that
+ * is not 16-byte aligned, or a page whose one layer is over 32 GB.  The call may queue several kernels; they let
+ * the next kernel on the stream start only once their rows are visible, as
+ * pkv_store does. */
+int pkv_pages_copy(const pkv_layout *layout, int32_t page_pos, void *base, int32_t n_pages,
+                   const int32_t *src, const int32_t *dst, const int32_t *n_pos, int32_t n,
+                   cudaStream_t stream);
+
+/* ---- table rewrite (an addition: compaction) ----------------------------------
+ * In each of n_tables device page tables (tables[t], n_table[t] entries),
+ * every entry equal to some src[i] becomes dst[i]; other entries (also ids
+ * outside the arena, as of pages given back) stay.  All arrays are host
+ * arrays, read before the call returns; the tables are device memory.  EINVAL
+ * for a negative id, a src or dst that repeats, a dst that is also a src, or
+ * a table that is NULL or not 4-byte aligned while it has entries.  A table
+ * may be listed twice.  The kernels let the next kernel on the stream start
+ * only once the entries are visible, so a decode may follow directly. */
+int pkv_tables_remap(int32_t *const *tables, const int32_t *n_table, int32_t n_tables,
+                     const int32_t *src, const int32_t *dst, int32_t n_moves, cudaStream_t stream);
 
 /* ---- pooling (#1169: fn_qsa_pool reads indexer keys once per block of
  * four and writes pooled rows through the table) ------------------------------

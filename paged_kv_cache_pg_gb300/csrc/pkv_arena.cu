@@ -1,7 +1,9 @@
 // The page arena of the C ABI (host only): KV pages handed out lowest id
 // first, runs of consecutive pages claimed from the top, both given back
 // either at once or once the caller's stream has drained (an event polled,
-// never waited on).
+// never waited on).  KV pages count their holders, so that forked streams
+// share whole pages; a compaction moves the highest KV pages to the lowest
+// free ids.
 #include <algorithm>
 #include <map>
 #include <mutex>
@@ -19,6 +21,8 @@ struct pkv_arena {
     int32_t n_pages = 0;
     void *base = nullptr;
     std::vector<uint8_t> taken;  // 1 = a KV page, 2 = a run's page; held or pending release
+    std::vector<int32_t> holders;  // of a KV page: streams that hold it, pending gives included
+    std::vector<int32_t> going;    // of those, gives that wait for their stream
     std::map<int32_t, int32_t> runs;  // first id -> pages of each run held now
     int32_t n_free = 0;
     int32_t low = 0;  // no free page below this id
@@ -63,6 +67,37 @@ void free_page(pkv_arena *a, int32_t id) {
     if (id < a->low) a->low = id;
 }
 
+// One holder of a page less: a KV page is free once it has none, a run's
+// page at once.
+void drop_holder(pkv_arena *a, int32_t id) {
+    if (a->taken[id] == 1 && --a->holders[id] > 0) return;
+    free_page(a, id);
+}
+
+// Holders whose give is not under way (0: free, a run's page, or going).
+int32_t live_holders(const pkv_arena *a, int32_t id) {
+    return a->taken[id] == 1 ? a->holders[id] - a->going[id] : 0;
+}
+
+bool held_once_each(const pkv_arena *a, const std::vector<int32_t> &sorted) {
+    for (size_t i = 0; i < sorted.size(); ++i) {
+        if (sorted[i] < 0 || sorted[i] >= a->n_pages || live_holders(a, sorted[i]) < 1) return false;
+        if (i && sorted[i] == sorted[i - 1]) return false;
+    }
+    return true;
+}
+
+// The lowest free page (there is one: n_free > 0), taken by one holder.
+int32_t take_lowest(pkv_arena *a) {
+    int32_t id = a->low;
+    while (a->taken[id]) ++id;
+    a->taken[id] = 1;
+    a->holders[id] = 1;
+    a->n_free--;
+    a->low = id + 1;
+    return id;
+}
+
 // Move releases whose stream work has finished back to the free pages.
 int poll_pending(pkv_arena *a) {
     int rc = PKV_OK;
@@ -72,7 +107,10 @@ int poll_pending(pkv_arena *a) {
         int q = a->ops.query(a->ops.ctx, p.ev);
         if (q == 0) {
             a->ops.destroy(a->ops.ctx, p.ev);
-            for (int32_t id : p.ids) free_page(a, id);
+            for (int32_t id : p.ids) {
+                if (a->taken[id] == 1) a->going[id]--;
+                drop_holder(a, id);
+            }
         } else {
             if (q < 0) rc = PKV_ECUDA;
             if (keep != i) a->pending[keep] = std::move(p);
@@ -103,6 +141,8 @@ extern "C" int pkv_arena_create(const pkv_layout *layout, int32_t page_pos, void
     a->n_pages = static_cast<int32_t>(n);
     a->base = dev_base;
     a->taken.assign(static_cast<size_t>(n), 0);
+    a->holders.assign(static_cast<size_t>(n), 0);
+    a->going.assign(static_cast<size_t>(n), 0);
     a->n_free = a->n_pages;
     a->ops = kCudaOps;
     *out = a;
@@ -143,15 +183,7 @@ extern "C" int pkv_pages_take(pkv_arena *a, int32_t n, int32_t *ids_out) {
     int rc = poll_pending(a);
     if (rc) return rc;
     if (n > a->n_free) return PKV_EAGAIN;
-    int32_t got = 0;
-    for (int32_t id = a->low; id < a->n_pages && got < n; ++id) {
-        if (!a->taken[id]) {
-            a->taken[id] = 1;
-            ids_out[got++] = id;
-        }
-    }
-    a->n_free -= got;
-    a->low = got ? ids_out[got - 1] + 1 : a->low;
+    for (int32_t i = 0; i < n; ++i) ids_out[i] = take_lowest(a);
     return PKV_OK;
 }
 
@@ -162,21 +194,83 @@ extern "C" int pkv_pages_give(pkv_arena *a, const int32_t *ids, int32_t n, cudaS
     // every id must be in range, held, and listed once
     std::vector<int32_t> v(ids, ids + n);
     std::sort(v.begin(), v.end());
-    for (int32_t i = 0; i < n; ++i) {
-        if (v[i] < 0 || v[i] >= a->n_pages || a->taken[v[i]] != 1) return PKV_EINVAL;
-        if (i && v[i] == v[i - 1]) return PKV_EINVAL;
-    }
-    for (auto &p : a->pending)
-        for (int32_t id : p.ids)
-            if (std::binary_search(v.begin(), v.end(), id)) return PKV_EINVAL;
+    if (!held_once_each(a, v)) return PKV_EINVAL;
     if (n == 0) return PKV_OK;
     if (!defer) {
-        for (int32_t id : v) free_page(a, id);
+        for (int32_t id : v) drop_holder(a, id);
         return PKV_OK;
     }
     void *ev = nullptr;
     if (a->ops.record(a->ops.ctx, stream, &ev) != 0) return PKV_ECUDA;
+    for (int32_t id : v) a->going[id]++;
     a->pending.push_back({ev, std::move(v)});
+    return PKV_OK;
+}
+
+// ---- sharing and compaction -----------------------------------------------------
+
+extern "C" int pkv_pages_fork(pkv_arena *a, const int32_t *ids, int32_t n, int32_t len,
+                              int32_t *ids_out, int32_t *copy_src, int32_t *copy_dst,
+                              int32_t *copy_pos) {
+    if (!a || n < 0 || len < 0 || !copy_src || !copy_dst || !copy_pos) return PKV_EINVAL;
+    if (n > 0 && (!ids || !ids_out)) return PKV_EINVAL;
+    if (n != len / a->page_pos + (len % a->page_pos ? 1 : 0)) return PKV_EINVAL;
+    std::lock_guard<std::mutex> g(a->mu);
+    int rc = poll_pending(a);
+    if (rc) return rc;
+    const int32_t tail = len % a->page_pos;
+    try {
+        std::vector<int32_t> v;
+        for (int32_t i = 0; i < n; ++i)
+            if (ids[i] != -1) v.push_back(ids[i]);
+        std::sort(v.begin(), v.end());
+        if (!held_once_each(a, v) || (tail && ids[n - 1] == -1)) return PKV_EINVAL;
+    } catch (...) {  // no host memory for the sorted list
+        return PKV_EINVAL;
+    }
+    if (tail && a->n_free < 1) return PKV_EAGAIN;
+    const int32_t last = tail ? ids[n - 1] : -1;
+    for (int32_t i = 0; i < n; ++i) {
+        ids_out[i] = ids[i];
+        if (ids[i] != -1 && !(tail && i == n - 1)) a->holders[ids[i]]++;
+    }
+    *copy_src = last;
+    *copy_dst = -1;
+    *copy_pos = tail;
+    if (tail) *copy_dst = ids_out[n - 1] = take_lowest(a);
+    return PKV_OK;
+}
+
+extern "C" int pkv_pages_holders(pkv_arena *a, const int32_t *ids, int32_t n, int32_t *holders_out) {
+    if (!a || n < 0 || (n > 0 && (!ids || !holders_out))) return PKV_EINVAL;
+    std::lock_guard<std::mutex> g(a->mu);
+    int rc = poll_pending(a);
+    if (rc) return rc;
+    for (int32_t i = 0; i < n; ++i)
+        if (ids[i] < 0 || ids[i] >= a->n_pages) return PKV_EINVAL;
+    for (int32_t i = 0; i < n; ++i) holders_out[i] = live_holders(a, ids[i]);
+    return PKV_OK;
+}
+
+extern "C" int pkv_arena_compact(pkv_arena *a, int32_t max_moves, int32_t *src_out,
+                                 int32_t *dst_out, int32_t *n_out) {
+    if (!a || max_moves < 0 || !n_out || (max_moves > 0 && (!src_out || !dst_out))) return PKV_EINVAL;
+    std::lock_guard<std::mutex> g(a->mu);
+    int rc = poll_pending(a);
+    if (rc) return rc;
+    int32_t moves = 0, dst = a->low;
+    for (int32_t src = a->n_pages - 1; moves < max_moves; --src) {
+        while (dst < src && a->taken[dst]) ++dst;
+        if (dst >= src) break;  // no free page below the highest one left
+        if (live_holders(a, src) < 1) continue;
+        a->taken[dst] = 1;
+        a->holders[dst] = live_holders(a, src);
+        a->holders[src] = a->going[src] + 1;  // the caller's, beside the gives under way
+        a->n_free--;
+        src_out[moves] = src;
+        dst_out[moves++] = dst;
+    }
+    *n_out = moves;
     return PKV_OK;
 }
 

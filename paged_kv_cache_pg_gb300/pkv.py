@@ -60,7 +60,8 @@ EXPORTS = [
     "pkv_layout_page_elems", "pkv_pg_row", "pkv_arena_create", "pkv_arena_destroy",
     "pkv_arena_info", "pkv_pages_take", "pkv_pages_give", "pkv_arena_pg",
     "pkv_arena_set_event_ops", "pkv_run_pages", "pkv_run_take", "pkv_run_give", "pkv_run_map",
-    "pkv_store", "pkv_gather", "pkv_pool", "pkv_decode_ws_size",
+    "pkv_pages_fork", "pkv_pages_holders", "pkv_arena_compact", "pkv_pages_copy",
+    "pkv_tables_remap", "pkv_store", "pkv_gather", "pkv_pool", "pkv_decode_ws_size",
     "pkv_decode", "pkv_decode_static", "pkv_block_scores", "pkv_topk", "pkv_sparse_ws_size",
     "pkv_sparse_decode", "pkv_prefill_ws_size", "pkv_prefill", "pkv_diag_wait_runs_out",
     "pkv_diag_cta_wait_runs_out",
@@ -92,6 +93,12 @@ def load(path: Optional[str] = None):
         "pkv_pages_give": [vp, vp, i32, vp, i32],
         "pkv_arena_pg": [vp, vp, i32, PP],
         "pkv_arena_set_event_ops": [vp, ctypes.POINTER(EventOps)],
+        "pkv_pages_fork": [vp, vp, i32, i32, vp, ctypes.POINTER(i32), ctypes.POINTER(i32),
+                           ctypes.POINTER(i32)],
+        "pkv_pages_holders": [vp, vp, i32, vp],
+        "pkv_arena_compact": [vp, i32, vp, vp, ctypes.POINTER(i32)],
+        "pkv_pages_copy": [LP, i32, vp, i32, vp, vp, vp, i32, vp],
+        "pkv_tables_remap": [vp, vp, i32, vp, vp, i32, vp],
         "pkv_run_pages": [vp, ctypes.c_uint64, ctypes.POINTER(i32)],
         "pkv_run_take": [vp, i32, ctypes.POINTER(i32)],
         "pkv_run_give": [vp, i32, i32, vp, i32],
@@ -143,8 +150,32 @@ def _stream(stream) -> Optional[int]:
 
 
 def _seqs(seqs: Sequence[Seq]):
+    if isinstance(seqs, ctypes.Array):
+        return seqs, len(seqs)
     arr = (Seq * max(1, len(seqs)))(*seqs)
     return arr, len(seqs)
+
+
+def _here(what: str, *tensors, dtype=None):
+    """Device addresses of tensors that a kernel of the current device may
+    touch as one block each: contiguous tensors on that device (of `dtype`
+    when given); None and addresses given as ints are taken as they are."""
+    dev, out = None, []
+    for t in tensors:
+        if t is not None and not isinstance(t, int):
+            if dev is None and t.get_device() >= 0:
+                import torch
+                dev = torch.cuda.current_device()
+            if t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+                raise PkvError(EINVAL, f"{what}: not a contiguous tensor of the type on the current device")
+            t = t.data_ptr()
+        out.append(t)
+    return out
+
+
+def _host_i32(a):
+    import numpy as np
+    return np.ascontiguousarray(a, dtype=np.int32)
 
 
 # ---- descriptors ------------------------------------------------------------
@@ -173,6 +204,13 @@ def pg(base, table, page_elems_: int, page_pos: int, n_pages: int = 1,
 
 def seq(pg_: Pg, length: int, n_new: int) -> Seq:
     return Seq(pg_, length, n_new)
+
+
+def batch(seqs: Sequence[Seq]):
+    """The streams of a launch as one ctypes array, for programs that keep it
+    between calls (its entries' len and n_new may be changed in place).  Every
+    call that takes a list of streams takes it as well."""
+    return (Seq * len(seqs))(*seqs)
 
 
 def pg_row(lay: Layout, pg_: Pg, host_table, layer: int, kind: int, head: int, pos: int) -> int:
@@ -226,6 +264,36 @@ class Arena:
         _check(self._lib.pkv_pages_give(self._h, ids.ctypes.data, ids.size, st, int(defer)),
                "pkv_pages_give")
 
+    def fork(self, ids, length: int):
+        """Share a stream's pages with a new one: (its ids, copy), where copy
+        is None or (src, dst, n_pos) of the last page, which is its own."""
+        import numpy as np
+        ids = _host_i32(ids)
+        out = np.empty(max(1, ids.size), dtype=np.int32)
+        s, d, n = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
+        _check(self._lib.pkv_pages_fork(self._h, ids.ctypes.data, ids.size, length, out.ctypes.data,
+                                        ctypes.byref(s), ctypes.byref(d), ctypes.byref(n)),
+               "pkv_pages_fork")
+        return out[:ids.size], ((s.value, d.value, n.value) if n.value else None)
+
+    def holders(self, ids):
+        import numpy as np
+        ids = _host_i32(ids)
+        out = np.zeros(max(1, ids.size), dtype=np.int32)
+        _check(self._lib.pkv_pages_holders(self._h, ids.ctypes.data, ids.size, out.ctypes.data),
+               "pkv_pages_holders")
+        return out[:ids.size]
+
+    def compact(self, max_moves: int):
+        """Plan up to max_moves moves of high pages to low holes: (src, dst).
+        The caller copies the pages, rewrites the tables and gives src back."""
+        import numpy as np
+        src, dst = (np.zeros(max(1, max_moves), dtype=np.int32) for _ in range(2))
+        n = ctypes.c_int32()
+        _check(self._lib.pkv_arena_compact(self._h, max_moves, src.ctypes.data, dst.ctypes.data,
+                                           ctypes.byref(n)), "pkv_arena_compact")
+        return src[:n.value], dst[:n.value]
+
     def run_pages(self, run_bytes: int) -> int:
         k = ctypes.c_int32()
         _check(self._lib.pkv_run_pages(self._h, run_bytes, ctypes.byref(k)), "pkv_run_pages")
@@ -274,6 +342,35 @@ def gather(lay, seqs, layer, kind, out, status=None, stream=None):
     arr, n = _seqs(seqs)
     _check(load().pkv_gather(ctypes.byref(lay), arr, n, layer, kind, _ptr(out), _ptr(status),
                              _stream(stream)), "pkv_gather")
+
+
+def pages_copy(lay, page_pos: int, memory, n_pages: int, src, dst, n_pos=None, stream=None):
+    """Copy pages src[i] to dst[i] of the arena at `memory`, whole or their
+    first n_pos[i] positions; src, dst, n_pos: host integers."""
+    src, dst = _host_i32(src), _host_i32(dst)
+    if src.size != dst.size or (n_pos is not None and len(n_pos) != src.size):
+        raise PkvError(EINVAL, "pkv_pages_copy: lists of different lengths")
+    n_pos = None if n_pos is None else _host_i32(n_pos)
+    base, = _here("pkv_pages_copy", memory)
+    if base is not memory and memory.numel() * memory.element_size() < 2 * n_pages * page_elems(lay, page_pos):
+        raise PkvError(EINVAL, "pkv_pages_copy: the memory holds fewer pages")
+    _check(load().pkv_pages_copy(ctypes.byref(lay), page_pos, base, n_pages, src.ctypes.data, dst.ctypes.data,
+                                 None if n_pos is None else n_pos.ctypes.data, src.size,
+                                 _stream(stream)), "pkv_pages_copy")
+
+
+def tables_remap(tables, src, dst, stream=None):
+    """Rewrite device page tables after a compaction: entries src[i] become
+    dst[i].  tables: int32 device tensors; src, dst: host integers."""
+    src, dst = _host_i32(src), _host_i32(dst)
+    if src.size != dst.size:
+        raise PkvError(EINVAL, "pkv_tables_remap: lists of different lengths")
+    import torch
+    n = len(tables)
+    ptrs = (ctypes.c_void_p * max(1, n))(*_here("pkv_tables_remap", *tables, dtype=torch.int32))
+    sizes = (ctypes.c_int32 * max(1, n))(*[t.numel() for t in tables])
+    _check(load().pkv_tables_remap(ptrs, sizes, n, src.ctypes.data, dst.ctypes.data, src.size,
+                                   _stream(stream)), "pkv_tables_remap")
 
 
 def pool(lay, seqs, layer, status=None, stream=None):
