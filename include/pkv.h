@@ -367,6 +367,39 @@ int pkv_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, in
                const void *ik_new, void *out, void *ws, size_t ws_bytes, int32_t *dev_status,
                cudaStream_t stream);
 
+/* ---- windowed decode: a sliding window and sinks (an addition) ---------------
+ * pkv_decode for streams that keep only a window of their context: the query
+ * at position p reads the keys j <= p with j > p - window or j < n_sink (the
+ * newest `window` positions, its own among them, and the first n_sink).
+ * window >= 1, n_sink >= 0; a window as long as the stream is pkv_decode's
+ * attention.  Both formats; n_new * (n_q_heads/H) <= 32 per stream; q, out,
+ * k_new, v_new, ik_new, the fused store and the ordering of cached rows as
+ * for pkv_decode (the sinks and the window's rows below len - n_new - 32 are
+ * read before the previous kernel has finished).
+ * Rows that no query of the stream reads may hold anything, NaN included, and
+ * table entries of pages without a row that one reads are not looked at: such
+ * pages may have been given back (pkv_window_dead_pages).  A row that some of
+ * the stream's new tokens read and others do not must hold finite values.
+ * Partials of windows of more than about 5,000 keys go to ws (device, >=
+ * pkv_window_decode_ws_size bytes, 0 for shorter ones, 256-byte aligned, no
+ * initialization, one ws per in-flight call).  A stream's bits depend only on
+ * its own rows, length and new tokens, the window and n_sink: paged output
+ * equals contiguous output, and other streams of the call change nothing.
+ * EINVAL for a window or n_sink out of range, and as for pkv_decode. */
+int pkv_window_decode_ws_size(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs,
+                              int32_t n_q_heads, int32_t window, int32_t n_sink, size_t *bytes);
+int pkv_window_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
+                      int32_t n_q_heads, int32_t window, int32_t n_sink, const void *q,
+                      const void *k_new, const void *v_new, const void *ik_new, void *out, void *ws,
+                      size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
+
+/* Logical pages [*first, *end) of a stream of `len` positions that no query at
+ * position len or later reads (all their positions lie behind the sinks and
+ * the window): they may be given back once the stream's queued work is done,
+ * and their table entries are not read again.  Empty: *first == *end. */
+int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t n_sink,
+                          int32_t *first, int32_t *end);
+
 /* ---- chunked prefill on the tensor cores (#1170, maintainer notes on the
  * Qwen slice: contiguous tensor-core attention for flat batches, a page-run
  * path for paged or mixed batches; #1169 maintainer reply: the grouped prompt

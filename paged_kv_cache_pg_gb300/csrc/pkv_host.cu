@@ -133,7 +133,7 @@ std::vector<std::pair<MapKey, RowMap>> g_maps;  // encoded maps, most recent las
 int row_map(DecodeMaps &maps, int &n_maps, const void *base, uint64_t rows, bool bytes8,
             bool tile, int box_rows, int box_chunks) {
     if (rows == 0 || rows > (1ull << 31) || !aligned16(base)) return -1;
-    if (tile ? (bytes8 || (box_rows != 64 && box_rows != 128) || (box_chunks != 2 && box_chunks != 4))
+    if (tile ? (bytes8 || (box_rows != 16 && box_rows != 64 && box_rows != 128) || (box_chunks != 2 && box_chunks != 4))
              : (box_rows != 16 || box_chunks != 1))
         return -1;
     RowMap m;
@@ -220,6 +220,28 @@ void plan_maps(Common &c, const pkv_layout *L, const pkv_seq *seqs, DecodeMaps &
             if (pg.page_pos % 64 == 0)
                 d.tma_v = static_cast<int16_t>(row_map(maps, n_maps, pg.base, rows, false, true, 64, 4));
         }
+    }
+}
+
+void plan_window_maps(Common &c, const pkv_layout *L, const pkv_seq *seqs, DecodeMaps &maps) {
+    int n_maps = 0;
+    const bool fp8 = fp8_of(L);
+    const int64_t row = fp8 ? 128 : 256;  // 16-bit elements of a row
+    for (int s = 0; s < c.n_seqs; ++s) {
+        SeqDev &d = c.seq[s];
+        d.tma = -1;
+        d.tma_k = d.tma_v = -1;
+        const pkv_pg &pg = seqs[s].pg;
+        const int64_t layer_off = (int64_t)c.layer * layer_elems_f(fp8, L->n_kv_heads, L->idx_dim, pg.page_pos);
+        // a 16-key tile of whole rows in one page, every page and this layer's
+        // block starting on a row
+        if (d.ncols == 0 || pg.page_pos % 16 != 0 || pg.page_elems % row != 0 || layer_off % row != 0) continue;
+        const uint64_t rows = (uint64_t)(pg.table ? pg.n_pages : 1) * pg.page_elems / row;
+        if (fp8)
+            d.tma = row_map(maps, n_maps, pg.base, rows, true);
+        else
+            d.tma_k = static_cast<int16_t>(row_map(maps, n_maps, pg.base, rows, false, true, 16, 4));
+        d.layer_row = layer_off / row;
     }
 }
 
@@ -478,6 +500,68 @@ extern "C" int pkv_decode_static(const pkv_layout *L, const pkv_seq *seqs, int32
                          static_cast<uint16_t *>(out), static_cast<float *>(scratch),
                          static_cast<const uint16_t *>(k_new), static_cast<const uint16_t *>(v_new),
                          k_new ? static_cast<const uint16_t *>(ik_new) : nullptr, stream);
+}
+
+// ---- windowed decode ---------------------------------------------------------
+
+static int window_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
+                         int32_t n_q_heads, int32_t window, int32_t n_sink, int32_t *dev_status,
+                         Common *c, DecodePlan *plan) {
+    int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, c);
+    if (rc) return rc;
+    if (window < 1 || n_sink < 0) return PKV_EINVAL;
+    return plan_window(*c, window, n_sink, plan);
+}
+
+extern "C" int pkv_window_decode_ws_size(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs,
+                                         int32_t n_q_heads, int32_t window, int32_t n_sink,
+                                         size_t *bytes) {
+    if (!bytes) return PKV_EINVAL;
+    Common c;
+    DecodePlan plan;
+    int rc = window_common(L, seqs, n_seqs, 0, n_q_heads, window, n_sink, nullptr, &c, &plan);
+    if (rc) return rc;
+    *bytes = plan.ws_bytes;
+    return PKV_OK;
+}
+
+extern "C" int pkv_window_decode(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs,
+                                 int32_t layer, int32_t n_q_heads, int32_t window, int32_t n_sink,
+                                 const void *q, const void *k_new, const void *v_new,
+                                 const void *ik_new, void *out, void *ws, size_t ws_bytes,
+                                 int32_t *dev_status, cudaStream_t stream) {
+    Common c;
+    DecodePlan plan;
+    int rc = window_common(L, seqs, n_seqs, layer, n_q_heads, window, n_sink, dev_status, &c, &plan);
+    if (rc) return rc;
+    if (plan.total_items == 0) return PKV_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out)) return PKV_EINVAL;
+    if ((k_new == nullptr) != (v_new == nullptr)) return PKV_EINVAL;
+    if (k_new) {
+        if (!aligned16(k_new) || !aligned16(v_new)) return PKV_EINVAL;
+        if (L->idx_dim && (!ik_new || !aligned16(ik_new))) return PKV_EINVAL;
+    }
+    if (plan.ws_bytes > 0 &&
+        (!ws || ws_bytes < plan.ws_bytes || (reinterpret_cast<uintptr_t>(ws) & 255u)))
+        return PKV_EINVAL;
+    DecodeMaps maps;  // copied into the launch's parameters
+    plan_window_maps(c, L, seqs, maps);
+    return launch_window(c, plan, maps, window, n_sink, static_cast<const uint16_t *>(q),
+                         static_cast<uint16_t *>(out), static_cast<float *>(ws),
+                         static_cast<const uint16_t *>(k_new), static_cast<const uint16_t *>(v_new),
+                         k_new && L->idx_dim ? static_cast<const uint16_t *>(ik_new) : nullptr, stream);
+}
+
+extern "C" int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t n_sink,
+                                     int32_t *first, int32_t *end) {
+    if (!first || !end || !page_pos_ok(page_pos) || len < 0 || window < 1 || n_sink < 0) return PKV_EINVAL;
+    // whole pages of positions from n_sink on that the next query (at len) no longer reads
+    const int64_t lo = std::max<int64_t>(0, (int64_t)len + 1 - window);
+    const int64_t f = ((int64_t)n_sink + page_pos - 1) / page_pos;
+    const int64_t e = std::max<int64_t>(f, lo / page_pos);
+    *first = static_cast<int32_t>(f);
+    *end = static_cast<int32_t>(e);
+    return PKV_OK;
 }
 
 extern "C" int pkv_sparse_ws_size(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs,

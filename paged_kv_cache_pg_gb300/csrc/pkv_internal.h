@@ -61,7 +61,7 @@ struct DecodeMaps {
 // or -1 when none can be made (no driver entry point, or maps full).
 // bytes8: rows of 256 bytes (e4m3 codes, boxes of 128 x 16) instead of 256
 // bf16 elements (boxes of 64 x 16); tile: the 3D tile view of bf16 rows,
-// boxes of {64, box_rows, box_chunks} (box_rows 64 or 128, box_chunks 2 or 4).
+// boxes of {64, box_rows, box_chunks} (box_rows 16, 64 or 128, box_chunks 2 or 4).
 int row_map(DecodeMaps &maps, int &n_maps, const void *base, uint64_t rows, bool bytes8,
             bool tile = false, int box_rows = 16, int box_chunks = 1);
 
@@ -128,6 +128,28 @@ __host__ __device__ inline int64_t off8_scale(bool v, int32_t h_kv, int32_t ptok
                                               int32_t row) {
     return 2 * (int64_t)h_kv * ptok * kHeadDim + (v ? 4 * (int64_t)h_kv * ptok : 0) +
            4 * ((int64_t)head * ptok + row);
+}
+
+// The keys that the queries of one stream read through a sliding window with
+// sinks: positions 0 .. n_sink-1 and lo .. len-1, lo the first position in
+// the first query's window.  Counted as virtual keys 0 .. nkeys-1 in whole
+// tiles: virtual key v is position v below sink_end (the sinks' tiles) and
+// position v + shift from there on (shift a multiple of the tile, 0 where the
+// window's first tile follows the sinks').  Tiles at the sinks' end and the
+// window's start may hold positions between n_sink and lo, which no query sees.
+struct WindowSpan {
+    int32_t lo, sink_end, shift, nkeys;
+};
+__host__ __device__ inline WindowSpan window_span(int32_t len, int32_t n_new, int32_t window,
+                                                  int32_t n_sink, int32_t tile) {
+    WindowSpan w;
+    w.lo = len - n_new + 1 - window;  // len - n_new >= 0 and window >= 1: no overflow
+    if (w.lo < 0) w.lo = 0;
+    const int32_t lo_t = w.lo / tile * tile;
+    w.sink_end = n_sink < lo_t ? (n_sink + tile - 1) / tile * tile : lo_t;
+    w.shift = lo_t - w.sink_end;
+    w.nkeys = len - w.shift;
+    return w;
 }
 
 // Runs set() on the current device until it succeeds there once: a kernel's
@@ -209,6 +231,17 @@ int launch_combine(const Common &c, const DecodePlan &plan, const uint16_t *q, u
 int launch_decode8(const Common &c, const DecodePlan &plan, const DecodeMaps &maps,
                    const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
                    const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
+
+// Windowed decode (pkv_window.cu): CTAs of a cluster for a window, plan and
+// launch; partials of long windows use the decode layout and its combine.
+int window_cluster(int32_t window, int32_t n_sink);
+int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan);
+// Row maps of the streams: 3D boxes of 16 rows over all dims (bf16, in
+// tma_k) or the e4m3 code rows' 2D boxes (in tma).
+void plan_window_maps(Common &c, const pkv_layout *layout, const pkv_seq *seqs, DecodeMaps &maps);
+int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &maps, int32_t window,
+                  int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
+                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 
 // Fixed scratch of pkv_decode_static (pkv_decode.cu): its size, and its
 // device address on the current device (looked up on the first call there).

@@ -1,0 +1,872 @@
+// Decode attention over a sliding window with sinks: a query at position p
+// reads the keys j <= p with j > p - window or j < n_sink.
+//
+// The keys that some query of a stream reads are its first n_sink positions
+// and a run that ends at its newest one.  They are counted through as virtual
+// keys (WindowSpan): the sinks' 16-key tiles, then the window's, so the rows
+// between them are never touched and their pages may be gone.  A tile's keys
+// that no query of the stream sees take the row of a neighbouring key that
+// one sees, so that nothing stale (a NaN, a page that is gone) reaches an MMA.
+//
+// A split of a (stream, KV head) is a cluster of up to eight CTAs, each with
+// an equal run of the split's tiles.  A CTA is a producer warp, which fills a
+// ring of 16-key stages (one 3D TMA copy for K and one for V where a page
+// holds the tile, else key by key with cp.async), and consumer warps that
+// compute S^T = K Q^T and O^T += V^T P^T with warp MMAs (one query token has
+// at most 32 query columns here, 8 to an MMA; the tensor cores' 128-row tiles
+// would stand nearly empty) with an online softmax per column.  The consumers
+// merge through shared memory and the cluster's CTAs through distributed
+// shared memory, in the order of the keys, so a window of up to
+// kSplitTiles x 8 x 16 keys is one launch with no workspace; longer ones
+// write split partials for the decode's combine kernel.
+//
+// The bytes of K and V bound a full batch: two CTAs share an SM, so one
+// streams while the other starts or merges.
+#include <algorithm>
+#include <cuda_fp16.h>
+
+#include "pkv_dev.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kTile = 16;                    // keys a stage
+constexpr int kMaxCols = 32;                 // query columns of one unit
+constexpr int kMaxCluster = 8;
+constexpr int kSplitTiles = 40;              // tiles of a CTA's run at most
+constexpr int kMaxPages = kSplitTiles * kTile / 4 + 4;  // pages a CTA's run can touch
+constexpr int kFreshGuard = 32;              // see decode_partial: rows a kernel just before may write
+constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
+
+constexpr int kPlane = 2048;                 // bf16: one 64-dim chunk of 16 rows
+constexpr int kCfgHalf16 = 4 * kPlane;       // bf16: 16 rows of K (or V)
+constexpr int kHalf8 = kTile * 128;          // e4m3: one 128-byte half of 16 code rows
+constexpr int kCfgHalf8 = 2 * kHalf8;
+
+// Shapes of the two page formats' CTAs.  bf16: eight consumer warps, a pair a
+// tile (each sums O over half the dims).  e4m3: four, one a tile.
+template <bool kFp8>
+struct Cfg {
+    static constexpr int half = kFp8 ? kCfgHalf8 : kCfgHalf16;   // K or V bytes of a stage
+    static constexpr int stage = 2 * half;
+    static constexpr int slots = kFp8 ? 12 : 6;
+    static constexpr int pair = kFp8 ? 1 : 2;                    // warps on one tile and column group
+    static constexpr int consumers = kFp8 ? 4 : 8;
+    static constexpr int threads = consumers * 32 + 32;
+    static constexpr int teams = consumers / pair;               // tiles (x column groups) at once
+    static constexpr int row = kFp8 ? kHeadDim + 12 : kHeadDim + 4;  // floats of a merge row
+    static constexpr int off_scl = slots * stage;                // e4m3: 16 K and 16 V scales a stage
+    static constexpr int off_page = off_scl + (kFp8 ? slots * 128 : 0);
+    static constexpr int off_bar = off_page + kMaxPages * 8;
+    static constexpr int bytes = off_bar + 2 * slots * 8 + 16;
+    static constexpr int smem = bytes + 1024;                    // with alignment slack
+    // after the last tile the stages hold the merge rows, then the CTA's sum
+    static constexpr int off_ml = 32 * row * 4;
+    static constexpr int off_sum = (off_ml + 32 * 8 + 127) / 128 * 128;
+    static constexpr int off_sum_ml = off_sum + kMaxCols * kHeadDim * 4;
+    static_assert(off_sum_ml + kMaxCols * 8 <= slots * stage, "merge buffers reuse the stages");
+    static_assert(off_page % 8 == 0 && off_bar % 8 == 0, "aligned");
+};
+
+struct WinArgs {
+    const uint16_t *q;
+    uint16_t *out;
+    float *ws;
+    const uint16_t *k_new;  // fused store of the new tokens, or null
+    const uint16_t *v_new;
+    const uint16_t *ik_new;
+    int32_t window, n_sink, cluster;
+};
+
+// ---- cluster helpers ----------------------------------------------------------
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster meet.  A warp whose lanes took different paths
+// (the producer's) may still be split behind a CTA barrier, and a warp that
+// arrives in two parts would count twice: the warp is joined first, and the
+// forms without .aligned do not need it to be.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float4 peer_ld4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 peer_ld2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// ---- small helpers --------------------------------------------------------------
+__device__ __forceinline__ float max_rows(float v) {  // over the lanes that share lane & 3
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float sum_rows(float v) {
+    v += __shfl_xor_sync(0xffffffffu, v, 4);
+    v += __shfl_xor_sync(0xffffffffu, v, 8);
+    return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
+
+// Byte offset of 16-byte chunk c of row r inside a staged K or V tile: planes
+// of 16 rows x 128 B with the TMA's 128-byte swizzle (bf16: four planes of 64
+// dims, e4m3: two of 128).
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+    return (c >> 3) * 2048 + r * 128 + ((((c & 7) ^ (r & 7))) << 4);
+}
+
+// Two e4m3 codes (low byte first) to an f16 pair, exactly.
+__device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
+    return r;
+}
+__device__ __forceinline__ void mma_half(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ void cp_async4(void *dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// s = 2^e x mant with mant in [1, 2); a zero or subnormal scale gives weight 0.
+__device__ __forceinline__ void split_scale(float s, float &e, float &mant) {
+    const uint32_t b = __float_as_uint(s);
+    const int ex = static_cast<int>((b >> 23) & 0xffu);
+    const bool normal = ex != 0 && ex != 0xff;
+    e = normal ? static_cast<float>(ex - 127) : -INFINITY;
+    mant = normal ? __uint_as_float((b & 0x007fffffu) | 0x3f800000u) : 0.f;
+}
+
+// ---- one CTA's run of keys --------------------------------------------------------
+struct Run {
+    WindowSpan sp;
+    int s, kvh, split;
+    int key0, key1;        // virtual keys of this CTA
+    int ntiles;
+    int qbase;
+    int sink_page, win_page, n_sink_pages, n_pages;  // the page list: sinks' pages, then the window's
+};
+
+__device__ __forceinline__ Run locate(const Common &c, const WinArgs &a, uint32_t rank) {
+    Run u;
+    const int item = static_cast<int>(blockIdx.x) / a.cluster;
+    u.s = find_seq(c.n_seqs, item, [&](int t) { return c.seq[t].work_off; });
+    const SeqDev &sd = c.seq[u.s];
+    const int r = item - sd.work_off;
+    u.kvh = r / sd.nsplit;
+    u.split = r - u.kvh * sd.nsplit;
+    u.sp = window_span(sd.len, sd.n_new, a.window, a.n_sink, kTile);
+    u.key0 = min(u.sp.nkeys, (u.split * a.cluster + static_cast<int>(rank)) * sd.split_len);
+    u.key1 = min(u.sp.nkeys, u.key0 + sd.split_len);
+    u.ntiles = (u.key1 - u.key0 + kTile - 1) / kTile;
+    u.qbase = sd.len - sd.n_new;
+    u.sink_page = u.win_page = u.n_sink_pages = u.n_pages = 0;
+    if (sd.table && u.ntiles > 0) {
+        if (u.key0 < u.sp.sink_end) {
+            u.sink_page = u.key0 / sd.ptok;
+            u.n_sink_pages = min(min(u.key1, u.sp.sink_end), a.n_sink) - 1;
+            u.n_sink_pages = u.n_sink_pages / sd.ptok - u.sink_page + 1;
+            u.n_pages = u.n_sink_pages;
+        }
+        if (u.key1 > u.sp.sink_end) {
+            // the first seen position: the sinks may reach into the window's first tile
+            int p0 = max(u.key0, u.sp.sink_end) + u.sp.shift;
+            if (p0 >= a.n_sink) p0 = max(p0, u.sp.lo);
+            const int p1 = u.key1 - 1 + u.sp.shift;
+            u.win_page = p0 / sd.ptok;
+            u.n_pages += p1 / sd.ptok - u.win_page + 1;
+        }
+    }
+    return u;
+}
+
+// Position of virtual key v.
+__device__ __forceinline__ int pos_of(const WindowSpan &sp, int v) {
+    return v + (v >= sp.sink_end ? sp.shift : 0);
+}
+
+struct Ctx {
+    uint8_t *stages;
+    float *scl;          // e4m3: [slot][32] K then V scales
+    int64_t *pages;      // offsets of the run's pages (-1: outside the arena)
+    uint64_t *full, *empty;
+    volatile int *abort_flag;
+};
+
+// Where one staged key's rows come from (per lane; lanes 16.. repeat 0..15).
+struct KeySrc {
+    int pos;          // the position read
+    int row;          // its row inside the page
+    int64_t page;     // its page's offset (elements)
+    bool seen;        // some query sees the key (else pos is a neighbour's)
+    bool fresh;       // the row comes from the new tokens' input
+    bool bad;         // its page id was outside the arena
+};
+
+__device__ __forceinline__ KeySrc key_src(const SeqDev &sd, const WinArgs &a, const Run &u, const Ctx &x,
+                                          int t, int lane) {
+    KeySrc k;
+    const int v = u.key0 + t * kTile + (lane & 15);
+    const int p = pos_of(u.sp, v);
+    k.seen = v < u.key1 && (p < a.n_sink || p >= u.sp.lo);
+    // the last position of the run, the last sink, or the window's first position
+    k.pos = k.seen ? p : v >= u.key1 ? pos_of(u.sp, u.key1 - 1) : v < u.sp.sink_end ? a.n_sink - 1 : u.sp.lo;
+    k.row = k.pos;
+    k.page = 0;
+    k.bad = false;
+    if (sd.table) {
+        const int page = k.pos / sd.ptok;
+        k.row = k.pos - page * sd.ptok;
+        k.page = x.pages[min(v, u.key1 - 1) < u.sp.sink_end ? page - u.sink_page
+                                                           : u.n_sink_pages + page - u.win_page];
+        if (k.page < 0) {
+            k.bad = true;
+            k.page = 0;
+        }
+    }
+    k.fresh = a.k_new != nullptr && k.pos >= u.qbase;
+    return k;
+}
+
+// Stage bf16 tile t into `slot` (the producer warp); the copies complete on
+// `bar`, and new rows are stored into the cache too.
+__device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const SeqDev &sd, const Run &u,
+                                        const Ctx &x, const void *map, int t, int slot, uint64_t *bar,
+                                        int lane, uint64_t pol) {
+    const int H = c.n_kv_heads;
+    const int64_t v_gap = (int64_t)H * sd.ptok * kHeadDim;  // V row - K row
+    const KeySrc k = key_src(sd, a, u, x, t, lane);
+    const int64_t krow = k.page + off_k(sd.ptok, u.kvh, k.row);
+    uint8_t *kst = x.stages + slot * Cfg<false>::stage, *vst = kst + Cfg<false>::half;
+    if (map != nullptr && __all_sync(0xffffffffu, k.seen && !k.fresh)) {
+        if (lane == 0) {
+            const int y = static_cast<int>(sd.layer_row + krow / kHeadDim);
+            mbar_arrive_expect_tx(bar, Cfg<false>::stage);
+            tma_load_3d(kst, map, 0, y, 0, bar, pol);
+            tma_load_3d(vst, map, 0, y + static_cast<int>(v_gap / kHeadDim), 0, bar, pol);
+        }
+        return;
+    }
+    const uint16_t *ksrc, *vsrc;
+    if (k.fresh) {
+        const int64_t r = ((int64_t)sd.tok_off + (k.pos - u.qbase)) * H + u.kvh;
+        ksrc = a.k_new + r * kHeadDim;
+        vsrc = a.v_new + r * kHeadDim;
+    } else {
+        ksrc = sd.layer_base + krow;
+        vsrc = ksrc + v_gap;
+    }
+    const int64_t kp = reinterpret_cast<int64_t>(ksrc), vp = reinterpret_cast<int64_t>(vsrc);
+#pragma unroll 4
+    for (int r = 0; r < kTile; ++r) {
+        const uint16_t *kr = reinterpret_cast<const uint16_t *>(shfl64(kp, r));
+        const uint16_t *vr = reinterpret_cast<const uint16_t *>(shfl64(vp, r));
+        cp_async16(kst + swz(r, lane), kr + lane * 8, pol);
+        cp_async16(vst + swz(r, lane), vr + lane * 8, pol);
+    }
+    cp_async_mbar_arrive(bar);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    unsigned todo = __ballot_sync(0xffffffffu, k.fresh && k.seen && !k.bad && lane < kTile);
+    while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const int p = __shfl_sync(0xffffffffu, k.pos, src), prow = __shfl_sync(0xffffffffu, k.row, src);
+        const int64_t kr = shfl64(krow, src), pg = shfl64(k.page, src);
+        const int64_t r = (int64_t)sd.tok_off + (p - u.qbase);
+        uint16_t *dst = const_cast<uint16_t *>(sd.layer_base) + kr;
+        const uint4 kv = __ldg(reinterpret_cast<const uint4 *>(a.k_new + (r * H + u.kvh) * kHeadDim) + lane);
+        const uint4 vv = __ldg(reinterpret_cast<const uint4 *>(a.v_new + (r * H + u.kvh) * kHeadDim) + lane);
+        reinterpret_cast<uint4 *>(dst)[lane] = kv;
+        reinterpret_cast<uint4 *>(dst + v_gap)[lane] = vv;
+        if (u.kvh == 0 && a.ik_new != nullptr && lane < c.idx_dim / 8) {
+            // the indexer-key row of the same position, written once (KV head 0)
+            uint16_t *idst = const_cast<uint16_t *>(sd.layer_base) + pg + off_ik(H, c.idx_dim, sd.ptok, prow);
+            reinterpret_cast<uint4 *>(idst)[lane] =
+                __ldg(reinterpret_cast<const uint4 *>(a.ik_new + r * c.idx_dim) + lane);
+        }
+    }
+}
+
+// The same for e4m3 pages: 16 code rows of K and V and their scales.  New rows
+// are quantized here (the rule of pkv_store) into the stage and the cache.
+__device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const SeqDev &sd, const Run &u,
+                                       const Ctx &x, const void *map, int t, int slot, uint64_t *bar,
+                                       int lane, uint64_t pol) {
+    const int H = c.n_kv_heads;
+    const KeySrc k = key_src(sd, a, u, x, t, lane);
+    const uint8_t *base = reinterpret_cast<const uint8_t *>(sd.layer_base);
+    const int64_t pg = 2 * k.page;
+    const int64_t kc = pg + off8_code(false, H, sd.ptok, u.kvh, k.row);
+    const int64_t vc = pg + off8_code(true, H, sd.ptok, u.kvh, k.row);
+    uint8_t *st = x.stages + slot * Cfg<true>::stage;
+    uint8_t *sc = reinterpret_cast<uint8_t *>(x.scl) + slot * 128;
+    constexpr int kCodes = Cfg<true>::half;
+    if (map != nullptr && __all_sync(0xffffffffu, k.seen && !k.fresh)) {
+        // one page holds the 16 keys: their code rows and scales are runs
+        if (lane == 0) {
+            const int yk = static_cast<int>(sd.layer_row + kc / 256), yv = static_cast<int>(sd.layer_row + vc / 256);
+            mbar_arrive_expect_tx(bar, Cfg<true>::stage + 128);
+            tma_load_2d(st, map, 0, yk, bar, pol);
+            tma_load_2d(st + kHalf8, map, 128, yk, bar, pol);
+            tma_load_2d(st + kCodes, map, 0, yv, bar, pol);
+            tma_load_2d(st + kCodes + kHalf8, map, 128, yv, bar, pol);
+            bulk_g2s(sc, base + pg + off8_scale(false, H, sd.ptok, u.kvh, k.row), 64, bar, pol);
+            bulk_g2s(sc + 64, base + pg + off8_scale(true, H, sd.ptok, u.kvh, k.row), 64, bar, pol);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int item = lane + 32 * i, rr = item >> 4, ch = item & 15;
+        const int64_t krr = shfl64(kc, rr), vrr = shfl64(vc, rr);
+        if (!__shfl_sync(0xffffffffu, k.fresh, rr)) {
+            cp_async16(st + swz(rr, ch), base + krr + 16 * ch, pol);
+            cp_async16(st + kCodes + swz(rr, ch), base + vrr + 16 * ch, pol);
+        }
+    }
+    if (!k.fresh) cp_async4(sc + 4 * lane, base + pg + off8_scale(lane >= 16, H, sd.ptok, u.kvh, k.row));
+    // rows whose source is a new token: quantized by the whole warp, one at a
+    // time; one that no query sees only needs finite codes
+    unsigned todo = __ballot_sync(0xffffffffu, k.fresh && lane < kTile);
+    while (todo) {
+        const int rr = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const bool seen = __shfl_sync(0xffffffffu, k.seen, rr);
+        if (!seen) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+                *reinterpret_cast<uint2 *>(st + v * kCodes + swz(rr, lane >> 1) + (lane & 1) * 8) = make_uint2(0u, 0u);
+            if (lane < 2) reinterpret_cast<float *>(sc)[16 * lane + rr] = 0.f;
+            continue;
+        }
+        const int p = __shfl_sync(0xffffffffu, k.pos, rr), row = __shfl_sync(0xffffffffu, k.row, rr);
+        const bool write = !__shfl_sync(0xffffffffu, k.bad, rr);
+        const int64_t pg_rr = shfl64(pg, rr);
+        const int64_t tr = (int64_t)sd.tok_off + (p - u.qbase);  // its packed input row
+        const bool ik_row = write && u.kvh == 0 && a.ik_new != nullptr && lane < c.idx_dim / 8;
+        const uint4 in_k = __ldg(reinterpret_cast<const uint4 *>(a.k_new + (tr * H + u.kvh) * kHeadDim) + lane);
+        const uint4 in_v = __ldg(reinterpret_cast<const uint4 *>(a.v_new + (tr * H + u.kvh) * kHeadDim) + lane);
+        const uint4 in_ik = ik_row ? __ldg(reinterpret_cast<const uint4 *>(a.ik_new + tr * c.idx_dim) + lane)
+                                   : make_uint4(0u, 0u, 0u, 0u);
+        uint8_t *lb = const_cast<uint8_t *>(base) + pg_rr;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            uint2 codes;
+            const float scale = quantize_row8(v ? in_v : in_k, &codes);
+            *reinterpret_cast<uint2 *>(st + v * kCodes + swz(rr, lane >> 1) + (lane & 1) * 8) = codes;
+            if (lane == 0) reinterpret_cast<float *>(sc)[16 * v + rr] = scale;
+            if (write) {
+                *reinterpret_cast<uint2 *>(lb + off8_code(v, H, sd.ptok, u.kvh, row) + 8 * lane) = codes;
+                if (lane == 0) *reinterpret_cast<float *>(lb + off8_scale(v, H, sd.ptok, u.kvh, row)) = scale;
+            }
+        }
+        if (ik_row)
+            reinterpret_cast<uint4 *>(lb + 2 * off_ik_f(true, H, c.idx_dim, sd.ptok, row))[lane] = in_ik;
+    }
+    cp_async_mbar_arrive(bar);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+}
+
+// Whether the query at position p (-1: a padding column) sees position kp.
+__device__ __forceinline__ bool sees(int p, int kp, int window, int n_sink) {
+    return kp <= p && (kp > p - window || kp < n_sink);
+}
+
+template <bool kFp8>
+__global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
+    window_partial(const __grid_constant__ Common c, const __grid_constant__ DecodeMaps maps,
+                   const __grid_constant__ WinArgs a) {
+    using F = Cfg<kFp8>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Ctx x;
+    x.stages = smem;
+    x.scl = reinterpret_cast<float *>(smem + F::off_scl);
+    x.pages = reinterpret_cast<int64_t *>(smem + F::off_page);
+    x.full = reinterpret_cast<uint64_t *>(smem + F::off_bar);
+    x.empty = x.full + F::slots;
+    x.abort_flag = reinterpret_cast<volatile int *>(x.empty + F::slots);
+    constexpr int S = F::slots;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cluster_rank();
+    const Run u = locate(c, a, rank);
+    const SeqDev &sd = c.seq[u.s];
+    const int ncols = sd.ncols, G = c.group;
+    const int ncg = (ncols + 7) >> 3;           // column groups of 8
+    // Tiles at once (key slices), a divisor of the slots: each slot then always
+    // belongs to one slice, which takes every phase of its barrier.  (A slice
+    // that skipped a phase could not tell the tile before its own, not landed
+    // yet, from its own: both leave the barrier the same parity.)
+    int ks_n = F::teams / ncg;
+    while (S % ks_n) --ks_n;
+    const int team = warp / F::pair, dh = kFp8 ? 0 : (warp & 1);
+    const int cg = team % ncg, ks = team / ncg;
+    const bool active = warp < F::consumers && ks < ks_n;
+
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&x.full[i], 1);
+            mbar_init(&x.empty[i], F::pair * ncg);
+        }
+        *x.abort_flag = 0;
+        fence_mbar_init();
+    }
+    for (int j = tid; j < u.n_pages; j += F::threads) {
+        const int p = j < u.n_sink_pages ? u.sink_page + j : u.win_page + (j - u.n_sink_pages);
+        // small pages between the sinks and the window may lie inside one tile:
+        // no row of theirs is read
+        if ((int64_t)p * sd.ptok >= a.n_sink && (int64_t)(p + 1) * sd.ptok <= u.sp.lo) continue;
+        const int id = __ldg(sd.table + p);
+        const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(sd.n_pages);
+        if (!ok && c.status) atomicOr(c.status, PKV_DEV_BAD_PAGE);
+        x.pages[j] = ok ? (int64_t)id * sd.ps : -1;
+    }
+    __syncthreads();
+    // nothing this CTA writes is read by the next kernel before its own wait
+    // (a decode reads no row within kFreshGuard of its new tokens early)
+    if (tid == 0) pdl_trigger();
+
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[kFp8 ? 16 : 8][4];
+#pragma unroll
+    for (int i = 0; i < (kFp8 ? 16 : 8); ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+
+    int issued = 0;  // tiles the producer has staged
+    if (warp == F::consumers) {
+        // ---------------- producer ----------------
+        const uint64_t pol = policy_evict_first();
+        const int tma = kFp8 ? sd.tma : sd.tma_k;
+        const void *map = tma >= 0 ? &maps.map[tma] : nullptr;
+        // cached rows more than kFreshGuard below the new tokens do not depend
+        // on the previous kernel: their tiles stream before the wait
+        const int early_end = u.qbase - kFreshGuard;
+        bool waited = false;
+        for (int t = 0; t < u.ntiles; ++t, ++issued) {
+            const int slot = t % S;
+            if (t >= S && !__all_sync(0xffffffffu, mbar_wait(&x.empty[slot], ((t / S) - 1) & 1, c.status))) {
+                *x.abort_flag = 1;
+                break;
+            }
+            if (!waited && pos_of(u.sp, u.key0 + t * kTile) + kTile > early_end) {
+                pdl_wait();
+                waited = true;
+            }
+            fence_proxy_async_smem();  // the slot's last reads come before the next tile's writes
+            if constexpr (kFp8) stage8(c, a, sd, u, x, map, t, slot, &x.full[slot], lane, pol);
+            else stage16(c, a, sd, u, x, map, t, slot, &x.full[slot], lane, pol);
+            __syncwarp();
+        }
+        if (!waited) pdl_wait();
+    } else if (active) {
+        // ---------------- consumers ----------------
+        const int g = lane >> 2, c4 = lane & 3;
+        const int bcol = cg * 8 + g;
+        const uint16_t *qr = nullptr;
+        if (bcol < ncols) {
+            const int j = bcol / G;
+            qr = a.q + (((int64_t)sd.tok_off + j) * c.n_q_heads + u.kvh * G + (bcol - j * G)) * kHeadDim;
+        }
+        asm volatile("" ::"l"(qr));
+        pdl_wait();
+        uint32_t qf[16][2];
+        if constexpr (kFp8) {
+            // dims 64 c4 .. 64 c4 + 63 of the row, converted to f16 once
+            uint4 w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                w[i] = qr ? __ldg(reinterpret_cast<const uint4 *>(qr + 64 * c4) + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                qf[2 * i][0] = bits_of(__floats2half2_rn(bf16_lo(w[i].x), bf16_hi(w[i].x)));
+                qf[2 * i][1] = bits_of(__floats2half2_rn(bf16_lo(w[i].y), bf16_hi(w[i].y)));
+                qf[2 * i + 1][0] = bits_of(__floats2half2_rn(bf16_lo(w[i].z), bf16_hi(w[i].z)));
+                qf[2 * i + 1][1] = bits_of(__floats2half2_rn(bf16_lo(w[i].w), bf16_hi(w[i].w)));
+            }
+        } else {
+#pragma unroll
+            for (int kk = 0; kk < 16; ++kk) {
+                const int d = kk * 16 + 2 * c4;
+                qf[kk][0] = qr ? __ldg(reinterpret_cast<const uint32_t *>(qr + d)) : 0u;
+                qf[kk][1] = qr ? __ldg(reinterpret_cast<const uint32_t *>(qr + d + 8)) : 0u;
+            }
+        }
+        // the positions of this lane's two columns (-1: padding)
+        const int c0 = cg * 8 + 2 * c4;
+        const int p0 = c0 < ncols ? u.qbase + c0 / G : -1;
+        const int p1 = c0 + 1 < ncols ? u.qbase + (c0 + 1) / G : -1;
+        const uint32_t s_base = smem_u32(x.stages);
+        const int kr_ = (lane & 7) + 8 * ((lane >> 3) & 1), kcb = lane >> 4;
+        const int vr_ = (lane & 7) + 8 * (lane >> 4), vcb = (lane >> 3) & 1;
+        float uo[2] = {-INFINITY, -INFINITY};  // e4m3: O's own reference (logit + V-scale exponent)
+
+        for (int t = ks; t < u.ntiles; t += ks_n) {
+            const int slot = t % S;
+            if (!__all_sync(0xffffffffu, mbar_wait(&x.full[slot], (t / S) & 1, c.status))) {
+                *x.abort_flag = 1;
+                break;
+            }
+            const int ka = pos_of(u.sp, u.key0 + t * kTile) + g, kb = ka + 8;
+            const bool a0 = sees(p0, ka, a.window, a.n_sink), a1 = sees(p1, ka, a.window, a.n_sink);
+            const bool b0 = sees(p0, kb, a.window, a.n_sink), b1 = sees(p1, kb, a.window, a.n_sink);
+            float sx[4];
+            if constexpr (kFp8) {
+                const uint8_t *st = x.stages + slot * F::stage;
+                float sacc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 w0 = *reinterpret_cast<const uint4 *>(st + swz(g, 4 * c4 + i));
+                    const uint4 w1 = *reinterpret_cast<const uint4 *>(st + swz(g + 8, 4 * c4 + i));
+                    const uint32_t y0[4] = {w0.x, w0.y, w0.z, w0.w}, y1[4] = {w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        mma_half(sacc, f16_of_codes(y0[j] & 0xffffu), f16_of_codes(y1[j] & 0xffffu),
+                                 f16_of_codes(y0[j] >> 16), f16_of_codes(y1[j] >> 16), qf[4 * i + j][0],
+                                 qf[4 * i + j][1]);
+                }
+                const float ska = x.scl[slot * 32 + g] * kScaleLog2, skb = x.scl[slot * 32 + g + 8] * kScaleLog2;
+                sx[0] = a0 ? sacc[0] * ska : -INFINITY;
+                sx[1] = a1 ? sacc[1] * ska : -INFINITY;
+                sx[2] = b0 ? sacc[2] * skb : -INFINITY;
+                sx[3] = b1 ? sacc[3] * skb : -INFINITY;
+            } else {
+                const uint32_t kbs = s_base + slot * F::stage;
+                float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int kk = 0; kk < 16; kk += 2) {
+                    uint32_t x0, x1, x2, x3;
+                    ldsm_x4(kbs + swz(kr_, 2 * kk + kcb), x0, x1, x2, x3);
+                    mma_bf16(sa, x0, x1, x2, x3, qf[kk][0], qf[kk][1]);
+                    ldsm_x4(kbs + swz(kr_, 2 * (kk + 1) + kcb), x0, x1, x2, x3);
+                    mma_bf16(sb, x0, x1, x2, x3, qf[kk + 1][0], qf[kk + 1][1]);
+                }
+                sx[0] = a0 ? (sa[0] + sb[0]) * kScaleLog2 : -INFINITY;
+                sx[1] = a1 ? (sa[1] + sb[1]) * kScaleLog2 : -INFINITY;
+                sx[2] = b0 ? (sa[2] + sb[2]) * kScaleLog2 : -INFINITY;
+                sx[3] = b1 ? (sa[3] + sb[3]) * kScaleLog2 : -INFINITY;
+            }
+            // online softmax of the two columns
+            const float n0 = fmaxf(m[0], max_rows(fmaxf(sx[0], sx[2])));
+            const float n1 = fmaxf(m[1], max_rows(fmaxf(sx[1], sx[3])));
+            const float o0 = n0 == -INFINITY ? 0.f : n0, o1 = n1 == -INFINITY ? 0.f : n1;
+            const float al0 = ex2(m[0] - o0), al1 = ex2(m[1] - o1);  // 0 while nothing was summed
+            const float e0 = ex2(sx[0] - o0), e1 = ex2(sx[1] - o1), e2 = ex2(sx[2] - o0), e3 = ex2(sx[3] - o1);
+            l[0] = l[0] * al0 + (e0 + e2);
+            l[1] = l[1] * al1 + (e1 + e3);
+            m[0] = n0;
+            m[1] = n1;
+            if constexpr (kFp8) {
+                // a V scale 2^E x mant goes into the key's weight, with a running
+                // maximum of logit + E as O's reference: weights in [0, 2), split
+                // into f16 hi + lo parts (about 22 significant bits)
+                float ea, ma, eb, mb;
+                split_scale(x.scl[slot * 32 + 16 + g], ea, ma);
+                split_scale(x.scl[slot * 32 + 16 + g + 8], eb, mb);
+                const float y0 = sx[0] + ea, y1 = sx[1] + ea, y2 = sx[2] + eb, y3 = sx[3] + eb;
+                const float nu0 = fmaxf(uo[0], max_rows(fmaxf(y0, y2))), nu1 = fmaxf(uo[1], max_rows(fmaxf(y1, y3)));
+                const float v0 = nu0 == -INFINITY ? 0.f : nu0, v1 = nu1 == -INFINITY ? 0.f : nu1;
+                const float be0 = ex2(uo[0] - v0), be1 = ex2(uo[1] - v1);
+                uo[0] = nu0;
+                uo[1] = nu1;
+                const float q0 = ex2(y0 - v0) * ma, q1 = ex2(y1 - v1) * ma;
+                const float q2 = ex2(y2 - v0) * mb, q3 = ex2(y3 - v1) * mb;
+                const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
+                const __half2 l01 = __floats2half2_rn(q0 - __low2float(h01), q1 - __high2float(h01));
+                const __half2 l23 = __floats2half2_rn(q2 - __low2float(h23), q3 - __high2float(h23));
+                const uint32_t b0h = movmatrix_t(bits_of(h01)), b1h = movmatrix_t(bits_of(h23));
+                const uint32_t b0l = movmatrix_t(bits_of(l01)), b1l = movmatrix_t(bits_of(l23));
+                // V codes of keys 2c, 2c+1, 2c+8, 2c+9, dims 32g .. 32g+31
+                uint32_t w[4][8];
+                const uint8_t *vb = x.stages + slot * F::stage + F::half;
+                const int kr[4] = {2 * c4, 2 * c4 + 1, 2 * c4 + 8, 2 * c4 + 9};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 z0 = *reinterpret_cast<const uint4 *>(vb + swz(kr[i], 2 * g));
+                    const uint4 z1 = *reinterpret_cast<const uint4 *>(vb + swz(kr[i], 2 * g + 1));
+                    w[i][0] = z0.x;
+                    w[i][1] = z0.y;
+                    w[i][2] = z0.z;
+                    w[i][3] = z0.w;
+                    w[i][4] = z1.x;
+                    w[i][5] = z1.y;
+                    w[i][6] = z1.z;
+                    w[i][7] = z1.w;
+                }
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    acc[i][0] *= be0;
+                    acc[i][1] *= be1;
+                    acc[i][2] *= be0;
+                    acc[i][3] *= be1;
+                    const int wi = i >> 1, b = 2 * (i & 1);
+                    const uint32_t sel0 = b | ((4 + b) << 4), sel1 = (b + 1) | ((5 + b) << 4);
+                    const uint32_t z0 = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel0));
+                    const uint32_t z1 = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel1));
+                    const uint32_t z2 = f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel0));
+                    const uint32_t z3 = f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel1));
+                    mma_half(acc[i], z0, z1, z2, z3, b0h, b1h);
+                    mma_half(acc[i], z0, z1, z2, z3, b0l, b1l);
+                }
+            } else {
+                // P as a bf16 pair hi + lo (lo = p - hi exactly): about 16
+                // significant bits of the weights reach the float32 accumulator
+                const uint32_t h01 = pack_bf16(e0, e1), h23 = pack_bf16(e2, e3);
+                const uint32_t l01 = pack_bf16(e0 - bf16_lo(h01), e1 - bf16_hi(h01));
+                const uint32_t l23 = pack_bf16(e2 - bf16_lo(h23), e3 - bf16_hi(h23));
+                const uint32_t pb0 = movmatrix_t(h01), pb1 = movmatrix_t(h23);
+                const uint32_t pc0 = movmatrix_t(l01), pc1 = movmatrix_t(l23);
+                const uint32_t vbs = s_base + slot * F::stage + F::half;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    acc[i][0] *= al0;
+                    acc[i][1] *= al1;
+                    acc[i][2] *= al0;
+                    acc[i][3] *= al1;
+                    uint32_t y0, y1, y2, y3;
+                    ldsm_x4_t(vbs + swz(vr_, 2 * (8 * dh + i) + vcb), y0, y1, y2, y3);
+                    mma_bf16(acc[i], y0, y1, y2, y3, pb0, pb1);
+                    mma_bf16(acc[i], y0, y1, y2, y3, pc0, pc1);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&x.empty[slot]);
+        }
+        l[0] = sum_rows(l[0]);
+        l[1] = sum_rows(l[1]);
+        if constexpr (kFp8) {
+            // O from its own reference back to the logits' maximum
+            const float f0 = uo[0] == -INFINITY ? 0.f : ex2(uo[0] - m[0]);
+            const float f1 = uo[1] == -INFINITY ? 0.f : ex2(uo[1] - m[1]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                acc[i][0] *= f0;
+                acc[i][1] *= f1;
+                acc[i][2] *= f0;
+                acc[i][3] *= f1;
+            }
+        }
+    }
+    __syncthreads();  // every staged tile is consumed (or the CTA gave up)
+    const bool failed = *x.abort_flag != 0;
+    // after a wait that ran out, every copy issued lands before the memory goes
+    if (failed)
+        for (int j = max(0, issued - S); j < issued; ++j) mbar_wait(&x.full[j % S], (j / S) & 1, nullptr);
+
+    // ---- merge the CTA's key slices, in order ----
+    const int NC = ncg * 8;
+    float *mbuf = reinterpret_cast<float *>(x.stages);               // [ks][NC][row]
+    float *mlb = reinterpret_cast<float *>(x.stages + F::off_ml);    // [ks][NC][2]
+    float *sum = reinterpret_cast<float *>(x.stages + F::off_sum);   // [ncols][256]
+    float *sum_ml = reinterpret_cast<float *>(x.stages + F::off_sum_ml);
+    if (active && !failed) {
+        const int g = lane >> 2, c0 = cg * 8 + 2 * (lane & 3);
+        float *b0 = mbuf + (ks * NC + c0) * F::row, *b1 = b0 + F::row;
+        if constexpr (kFp8) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int d = 33 * g + 2 * i;  // dim 32 g + 2 i, skewed by g against bank conflicts
+                b0[d] = acc[i][0];
+                b1[d] = acc[i][1];
+                b0[d + 1] = acc[i][2];
+                b1[d + 1] = acc[i][3];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int d = (8 * dh + i) * 16 + g;
+                b0[d] = acc[i][0];
+                b1[d] = acc[i][1];
+                b0[d + 8] = acc[i][2];
+                b1[d + 8] = acc[i][3];
+            }
+        }
+        if (dh == 0 && g == 0) {
+            float *ml = mlb + (ks * NC + c0) * 2;
+            ml[0] = m[0];
+            ml[1] = l[0];
+            ml[2] = m[1];
+            ml[3] = l[1];
+        }
+    }
+    __syncthreads();
+    for (int idx = tid; idx < ncols * (kHeadDim / 4); idx += F::threads) {
+        const int col = idx / (kHeadDim / 4), d = 4 * (idx - col * (kHeadDim / 4));
+        const int ds = kFp8 ? d + (d >> 5) : d;
+        float M = -INFINITY;
+        for (int k = 0; k < ks_n; ++k) M = fmaxf(M, mlb[(k * NC + col) * 2]);
+        float L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < ks_n; ++k) {
+            const float w = M == -INFINITY ? 0.f : ex2(mlb[(k * NC + col) * 2] - M);
+            const float *v = mbuf + (k * NC + col) * F::row + ds;
+            L += w * mlb[(k * NC + col) * 2 + 1];
+            O.x += w * v[0];
+            O.y += w * v[1];
+            O.z += w * v[2];
+            O.w += w * v[3];
+        }
+        *reinterpret_cast<float4 *>(sum + col * kHeadDim + d) = O;
+        if (d == 0) *reinterpret_cast<float2 *>(sum_ml + 2 * col) = make_float2(M, L);
+    }
+    // ---- then the cluster's CTAs, in order ----
+    cluster_sync();
+    const bool single = sd.nsplit == 1;
+    float *part_acc = a.ws + sd.ws_off;
+    float *part_ml = part_acc + (int64_t)c.n_kv_heads * sd.nsplit * ncols * kHeadDim;
+    const int64_t pidx = ((int64_t)u.kvh * sd.nsplit + u.split) * ncols;
+    if (!failed) {
+        for (int idx = static_cast<int>(rank) * F::threads + tid; idx < ncols * (kHeadDim / 4);
+             idx += a.cluster * F::threads) {
+            const int col = idx / (kHeadDim / 4), d = 4 * (idx - col * (kHeadDim / 4));
+            float2 ml[kMaxCluster];
+            float4 v[kMaxCluster];
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < a.cluster) {
+                    ml[k] = peer_ld2(peer_addr(sum_ml + 2 * col, k));
+                    v[k] = peer_ld4(peer_addr(sum + col * kHeadDim + d, k));
+                }
+            }
+            float M = -INFINITY, L = 0.f;
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, ml[k].x);
+            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kMaxCluster; ++k) {
+                const float w = M == -INFINITY ? 0.f : ex2(ml[k].x - M);
+                L += w * ml[k].y;
+                O.x += w * v[k].x;
+                O.y += w * v[k].y;
+                O.z += w * v[k].z;
+                O.w += w * v[k].w;
+            }
+            if (single) {
+                const bool any = L > 0.f;
+                const float lz = any ? L : 1.f;
+                const int j = col / G;
+                uint2 pk;
+                pk.x = pack_bf16(any ? O.x / lz : 0.f, any ? O.y / lz : 0.f);
+                pk.y = pack_bf16(any ? O.z / lz : 0.f, any ? O.w / lz : 0.f);
+                *reinterpret_cast<uint2 *>(
+                    a.out + (((int64_t)sd.tok_off + j) * c.n_q_heads + u.kvh * G + (col - j * G)) * kHeadDim + d) = pk;
+            } else {
+                *reinterpret_cast<float4 *>(part_acc + (pidx + col) * kHeadDim + d) = O;
+                if (d == 0) *reinterpret_cast<float2 *>(part_ml + (pidx + col) * 2) = make_float2(M, L);
+            }
+        }
+    }
+    cluster_sync();  // the peers have read this CTA's sums
+}
+
+}  // namespace
+
+// A split is a cluster of CTAs that share its tiles, its size set by the
+// window alone (so a stream's bits do not depend on its batch): eight tiles a
+// CTA before another one joins, eight CTAs at most.
+int window_cluster(int32_t window, int32_t n_sink) {
+    const int64_t tiles = ((int64_t)window + n_sink) / kTile + 2;
+    int cs = 1;
+    while (cs < kMaxCluster && tiles > 8 * cs) cs *= 2;
+    return cs;
+}
+
+// Splits only where a CTA's run would pass kSplitTiles tiles.
+int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
+    int64_t items = 0;
+    int32_t comb = 0;
+    int64_t floats = 0;
+    const int cs = window_cluster(window, n_sink);
+    for (int s = 0; s < c.n_seqs; ++s) {
+        SeqDev &d = c.seq[s];
+        d.work_off = static_cast<int32_t>(items);
+        d.comb_off = comb;
+        d.ws_off = floats;
+        d.ncols = d.n_new * c.group;
+        if (d.ncols > kMaxCols) return PKV_EINVAL;
+        d.nsplit = 1;
+        d.split_len = kTile;
+        if (d.ncols == 0) continue;
+        const WindowSpan sp = window_span(d.len, d.n_new, window, n_sink, kTile);
+        const int tiles = (sp.nkeys + kTile - 1) / kTile;
+        d.nsplit = (tiles + cs * kSplitTiles - 1) / (cs * kSplitTiles);
+        if (d.nsplit > 2048) return PKV_EINVAL;
+        const int per = (tiles + d.nsplit * cs - 1) / (d.nsplit * cs);
+        d.split_len = per * kTile;
+        items += (int64_t)c.n_kv_heads * d.nsplit;
+        if (d.nsplit > 1) {
+            comb += c.n_kv_heads * d.ncols * comb_ctas(d.nsplit);
+            floats += (int64_t)c.n_kv_heads * d.nsplit * d.ncols * (kHeadDim + 2);
+            floats = (floats + 63) / 64 * 64;
+        }
+    }
+    if (items * cs > INT32_MAX) return PKV_EINVAL;
+    plan->total_items = static_cast<int32_t>(items);
+    plan->total_comb = comb;
+    plan->ws_bytes = static_cast<size_t>(floats) * 4;
+    return PKV_OK;
+}
+
+int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &maps, int32_t window,
+                  int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
+                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream) {
+    static std::atomic<uint64_t> attr_done{0};
+    if (once_per_device(attr_done, [] {
+            const void *fns[] = {reinterpret_cast<const void *>(window_partial<false>),
+                                 reinterpret_cast<const void *>(window_partial<true>)};
+            const int bytes[] = {Cfg<false>::smem, Cfg<true>::smem};
+            for (int i = 0; i < 2; ++i) {
+                if (cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]) != cudaSuccess)
+                    return PKV_ECUDA;
+                if (cudaFuncSetAttribute(fns[i], cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared) != cudaSuccess)
+                    return PKV_ECUDA;
+            }
+            return PKV_OK;
+        }) != PKV_OK)
+        return PKV_ECUDA;
+    const WinArgs a{q, out, ws, k_new, v_new, ik_new, window, n_sink, window_cluster(window, n_sink)};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.total_items) * a.cluster);
+    cfg.blockDim = dim3(c.kv_fp8 ? Cfg<true>::threads : Cfg<false>::threads);
+    cfg.dynamicSmemBytes = c.kv_fp8 ? Cfg<true>::smem : Cfg<false>::smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    if (cudaLaunchKernelEx(&cfg, c.kv_fp8 ? window_partial<true> : window_partial<false>, c, maps, a) != cudaSuccess)
+        return PKV_ECUDA;
+    if (plan.total_comb > 0) return launch_combine(c, plan, q, out, ws, stream);
+    return PKV_OK;
+}
+
+}  // namespace pkv

@@ -64,7 +64,8 @@ EXPORTS = [
     "pkv_tables_remap", "pkv_store", "pkv_gather", "pkv_pool", "pkv_decode_ws_size",
     "pkv_decode", "pkv_decode_static", "pkv_block_scores", "pkv_topk", "pkv_sparse_ws_size",
     "pkv_sparse_decode", "pkv_prefill_ws_size", "pkv_prefill", "pkv_diag_wait_runs_out",
-    "pkv_diag_cta_wait_runs_out",
+    "pkv_diag_cta_wait_runs_out", "pkv_window_decode_ws_size", "pkv_window_decode",
+    "pkv_window_dead_pages",
 ]
 
 
@@ -109,6 +110,9 @@ def load(path: Optional[str] = None):
         "pkv_decode_ws_size": [LP, SP, i32, i32, ctypes.POINTER(sz)],
         "pkv_decode": [LP, SP, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, vp],
         "pkv_decode_static": [LP, SP, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp],
+        "pkv_window_decode_ws_size": [LP, SP, i32, i32, i32, i32, ctypes.POINTER(sz)],
+        "pkv_window_decode": [LP, SP, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, vp],
+        "pkv_window_dead_pages": [i32, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)],
         "pkv_prefill_ws_size": [LP, SP, i32, i32, ctypes.POINTER(sz)],
         "pkv_prefill": [LP, SP, i32, i32, i32, vp, vp, vp, sz, vp, vp],
         "pkv_block_scores": [LP, SP, i32, i32, i32, vp, vp, i32, vp, vp],
@@ -411,6 +415,35 @@ def prefill(lay, seqs, layer, n_q_heads, q, out, ws, status=None, stream=None):
     ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(load().pkv_prefill(ctypes.byref(lay), arr, n, layer, n_q_heads, _ptr(q), _ptr(out),
                               _ptr(ws), ws_bytes, _ptr(status), _stream(stream)), "pkv_prefill")
+
+
+def window_decode_ws_size(lay, seqs, n_q_heads, window, n_sink) -> int:
+    arr, n = _seqs(seqs)
+    out = ctypes.c_size_t()
+    _check(load().pkv_window_decode_ws_size(ctypes.byref(lay), arr, n, n_q_heads, window, n_sink,
+                                            ctypes.byref(out)), "pkv_window_decode_ws_size")
+    return out.value
+
+
+def window_decode(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws=None, status=None,
+                  stream=None, k_new=None, v_new=None, ik_new=None):
+    """Decode attention over the newest `window` positions and the first
+    n_sink; with k_new/v_new (and ik_new) the new rows are stored too."""
+    arr, n = _seqs(seqs)
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    q, k_new, v_new, ik_new, out, ws, status = _here("pkv_window_decode", q, k_new, v_new, ik_new, out,
+                                                     ws, status)
+    _check(load().pkv_window_decode(ctypes.byref(lay), arr, n, layer, n_q_heads, window, n_sink, q,
+                                    k_new, v_new, ik_new, out, ws, ws_bytes, status,
+                                    _stream(stream)), "pkv_window_decode")
+
+
+def window_dead_pages(page_pos: int, length: int, window: int, n_sink: int):
+    """Logical pages [first, end) that no query at position `length` or later reads."""
+    first, end = ctypes.c_int32(), ctypes.c_int32()
+    _check(load().pkv_window_dead_pages(page_pos, length, window, n_sink, ctypes.byref(first),
+                                        ctypes.byref(end)), "pkv_window_dead_pages")
+    return first.value, end.value
 
 
 STATIC_SCRATCH_BYTES = 4 << 20

@@ -1,0 +1,89 @@
+"""Windowed attention: its refusals, workspace sizes and dead pages, without a GPU."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from paged_kv_cache_pg_gb300 import build, pkv
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return pkv.load()
+
+
+def _seq(lay, length=600, n_new=1, ptok=16, n_table=50, n_pages=64, base=0x10000):
+    return pkv.seq(pkv.Pg(base, 0x20000, pkv.page_elems(lay, ptok), ptok, n_pages, n_table, 0), length, n_new)
+
+
+def _call(lay, seqs, window=100, n_sink=4, hq=4, layer=0, q=0x1000, out=0x1000, k=None, v=None, ik=None, ws=None,
+          ws_bytes=0):
+    arr, n = pkv._seqs(seqs)
+    return pkv.load().pkv_window_decode(ctypes.byref(lay), arr, n, layer, hq, window, n_sink, q, k, v, ik, out, ws,
+                                        ws_bytes, None, None)
+
+
+def _ws(lay, seqs, window, n_sink, hq=4):
+    return pkv.window_decode_ws_size(lay, seqs, hq, window, n_sink)
+
+
+@pytest.mark.parametrize("fmt", [pkv.KV_BF16, pkv.KV_E4M3])
+def test_refusals_before_launch(fmt):
+    lay = pkv.layout(2, 2, 256, 128, fmt)
+    s = _seq(lay)
+    for kw in (dict(window=0), dict(window=-5), dict(n_sink=-1), dict(hq=3), dict(layer=2), dict(q=None), dict(out=None),
+               dict(q=0x1008), dict(out=0x1008), dict(k=0x1000), dict(v=0x1000), dict(k=0x1000, v=0x1000),
+               dict(k=0x1000, v=0x1000, ik=0x1008), dict(k=0x1008, v=0x1000, ik=0x1000), dict(hq=66)):
+        assert _call(lay, [s], **kw) == pkv.EINVAL, kw
+    assert _call(lay, [_seq(lay, n_new=17)]) == pkv.EINVAL            # 34 query columns
+    assert _call(lay, [_seq(lay, length=801)]) == pkv.EINVAL          # past the table
+    assert _call(lay, [_seq(lay, n_new=601)]) == pkv.EINVAL
+    assert _call(lay, [s] * 65) == pkv.EINVAL
+    assert _call(lay, []) == pkv.OK                                    # nothing launched
+    assert _call(lay, [_seq(lay, n_new=0), _seq(lay, length=0, n_new=0)]) == pkv.OK
+    out = ctypes.c_size_t()
+    arr, n = pkv._seqs([s])
+    assert pkv.load().pkv_window_decode_ws_size(ctypes.byref(lay), arr, n, 4, 0, 0, ctypes.byref(out)) == pkv.EINVAL
+    assert pkv.load().pkv_window_decode_ws_size(ctypes.byref(lay), arr, n, 4, 1, 0, None) == pkv.EINVAL
+
+
+def test_short_windows_need_no_workspace_and_long_ones_are_checked():
+    lay = pkv.layout(1, 2)
+    s = _seq(lay, length=40000, ptok=256, n_table=200, n_pages=200)
+    assert _ws(lay, [s], 4096, 64) == 0
+    need = _ws(lay, [s], 20000, 4)
+    assert need > 0
+    assert _ws(lay, [s, s], 20000, 4) == 2 * need
+    assert _call(lay, [s], 20000) == pkv.EINVAL
+    assert _call(lay, [s], 20000, ws=0x1000, ws_bytes=need - 4) == pkv.EINVAL
+    assert _call(lay, [s], 20000, ws=0x1080, ws_bytes=need) == pkv.EINVAL
+    # the largest window and sink counts do not overflow
+    assert _ws(lay, [s], 2**31 - 1, 2**31 - 1) == _ws(lay, [s], 40000, 0)
+
+
+def test_dead_pages_are_exactly_those_no_later_query_reads():
+    rng = np.random.default_rng(2)
+    for _ in range(400):
+        ptok = int(rng.choice([4, 16, 20, 48]))
+        length, window, sinks = (int(rng.integers(0, 300)), int(rng.integers(1, 120)), int(rng.integers(0, 70)))
+        first, end = pkv.window_dead_pages(ptok, length, window, sinks)
+        j = np.arange(0, length + ptok)
+        read = (j < sinks) | (j > length - window)
+        dead = [p for p in range(length // ptok + 1) if not read[p * ptok:(p + 1) * ptok].any()]
+        assert list(range(first, end)) == dead, (ptok, length, window, sinks)
+    assert pkv.window_dead_pages(16, 1000, 2**31 - 1, 0) == (0, 0)
+    a, b = pkv.window_dead_pages(16, 1000, 1, 2**31 - 1)
+    assert a == b
+    for bad in ((18, 1, 1, 0), (0, 1, 1, 0), (16, -1, 1, 0), (16, 1, 0, 0), (16, 1, 1, -1)):
+        with pytest.raises(pkv.PkvError) as e:
+            pkv.window_dead_pages(*bad)
+        assert e.value.code == pkv.EINVAL
+
+
+def test_calls_take_only_contiguous_tensors_of_the_device():
+    import torch
+    lay = pkv.layout(1, 1, 256, 0)
+    with pytest.raises(pkv.PkvError) as e:
+        pkv.window_decode(lay, [_seq(lay)], 0, 4, 100, 4, torch.zeros(4, 256, dtype=torch.bfloat16), 0x1000, stream=0)
+    assert e.value.code == pkv.EINVAL
