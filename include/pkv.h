@@ -393,6 +393,27 @@ int pkv_window_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_s
                       const void *k_new, const void *v_new, const void *ik_new, void *out, void *ws,
                       size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
 
+/* The same for chunks (pkv_prefill with a window): each stream's n_new queries
+ * at its newest positions, any number of them, whose rows are in the cache
+ * already.  bf16 pages.  A first kernel copies the rows that the chunk reads
+ * (the sinks, and the first query's window on) out of their pages into ws, K
+ * as it is and V in fp16; both products run as tcgen05 MMAs with float32
+ * accumulation, P in fp16 (11 significant bits).  So a V entry is exact for
+ * magnitudes 2^-14 to 65,280, rounded to fp16's 2^-24 grid below that, and one
+ * beyond 65,504 makes the output non-finite and sets PKV_DEV_RANGE.  Rows
+ * that no query of the chunk reads and their pages' table entries are not
+ * looked at; a row that some of the chunk's queries read and others do not
+ * must hold finite values.  ws: device, >= pkv_window_prefill_ws_size bytes,
+ * 256-byte aligned, no initialization, one ws per in-flight call.  Paged
+ * output equals contiguous output, and other streams of the call change
+ * nothing, bit for bit.  EINVAL for a window or n_sink out of range, an e4m3
+ * layout, and as for pkv_prefill. */
+int pkv_window_prefill_ws_size(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs,
+                               int32_t n_q_heads, int32_t window, int32_t n_sink, size_t *bytes);
+int pkv_window_prefill(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
+                       int32_t n_q_heads, int32_t window, int32_t n_sink, const void *q, void *out,
+                       void *ws, size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
+
 /* Logical pages [*first, *end) of a stream of `len` positions that no query at
  * position len or later reads (all their positions lie behind the sinks and
  * the window): they may be given back once the stream's queued work is done,

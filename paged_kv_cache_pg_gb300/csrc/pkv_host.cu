@@ -552,6 +552,45 @@ extern "C" int pkv_window_decode(const pkv_layout *L, const pkv_seq *seqs, int32
                          k_new && L->idx_dim ? static_cast<const uint16_t *>(ik_new) : nullptr, stream);
 }
 
+static int window_chunk_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
+                               int32_t n_q_heads, int32_t window, int32_t n_sink, int32_t *dev_status,
+                               Common *c, DecodePlan *plan) {
+    int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, c);
+    if (rc) return rc;
+    if (window < 1 || n_sink < 0 || c->kv_fp8) return PKV_EINVAL;
+    int nsm = 0;
+    rc = sm_count(&nsm);
+    if (rc) return rc;
+    return plan_window_prefill(*c, window, n_sink, nsm, plan);
+}
+
+extern "C" int pkv_window_prefill_ws_size(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs,
+                                          int32_t n_q_heads, int32_t window, int32_t n_sink,
+                                          size_t *bytes) {
+    if (!bytes) return PKV_EINVAL;
+    Common c;
+    DecodePlan plan;
+    int rc = window_chunk_common(L, seqs, n_seqs, 0, n_q_heads, window, n_sink, nullptr, &c, &plan);
+    if (rc) return rc;
+    *bytes = plan.ws_bytes;
+    return PKV_OK;
+}
+
+extern "C" int pkv_window_prefill(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs,
+                                  int32_t layer, int32_t n_q_heads, int32_t window, int32_t n_sink,
+                                  const void *q, void *out, void *ws, size_t ws_bytes,
+                                  int32_t *dev_status, cudaStream_t stream) {
+    Common c;
+    DecodePlan plan;
+    int rc = window_chunk_common(L, seqs, n_seqs, layer, n_q_heads, window, n_sink, dev_status, &c, &plan);
+    if (rc) return rc;
+    if (plan.total_items == 0) return PKV_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out)) return PKV_EINVAL;
+    if (!ws || ws_bytes < plan.ws_bytes || (reinterpret_cast<uintptr_t>(ws) & 255u)) return PKV_EINVAL;
+    return launch_window_prefill(c, plan, window, n_sink, static_cast<const uint16_t *>(q),
+                                 static_cast<uint16_t *>(out), static_cast<float *>(ws), stream);
+}
+
 extern "C" int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t n_sink,
                                      int32_t *first, int32_t *end) {
     if (!first || !end || !page_pos_ok(page_pos) || len < 0 || window < 1 || n_sink < 0) return PKV_EINVAL;

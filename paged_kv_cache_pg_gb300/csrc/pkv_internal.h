@@ -243,6 +243,12 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
                   int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
                   const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 
+// Windowed chunk attention (pkv_window_prefill.cu): plan and launch (gather,
+// chunk kernel, and the combine of split calls).
+int plan_window_prefill(Common &c, int32_t window, int32_t n_sink, int nsm, DecodePlan *plan);
+int launch_window_prefill(const Common &c, const DecodePlan &plan, int32_t window, int32_t n_sink,
+                          const uint16_t *q, uint16_t *out, float *ws, cudaStream_t stream);
+
 // Fixed scratch of pkv_decode_static (pkv_decode.cu): its size, and its
 // device address on the current device (looked up on the first call there).
 constexpr size_t kStaticScratchBytes = 4u << 20;

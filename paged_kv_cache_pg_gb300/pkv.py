@@ -65,7 +65,7 @@ EXPORTS = [
     "pkv_decode", "pkv_decode_static", "pkv_block_scores", "pkv_topk", "pkv_sparse_ws_size",
     "pkv_sparse_decode", "pkv_prefill_ws_size", "pkv_prefill", "pkv_diag_wait_runs_out",
     "pkv_diag_cta_wait_runs_out", "pkv_window_decode_ws_size", "pkv_window_decode",
-    "pkv_window_dead_pages",
+    "pkv_window_prefill_ws_size", "pkv_window_prefill", "pkv_window_dead_pages",
 ]
 
 
@@ -112,6 +112,8 @@ def load(path: Optional[str] = None):
         "pkv_decode_static": [LP, SP, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp],
         "pkv_window_decode_ws_size": [LP, SP, i32, i32, i32, i32, ctypes.POINTER(sz)],
         "pkv_window_decode": [LP, SP, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, vp],
+        "pkv_window_prefill_ws_size": [LP, SP, i32, i32, i32, i32, ctypes.POINTER(sz)],
+        "pkv_window_prefill": [LP, SP, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp, vp],
         "pkv_window_dead_pages": [i32, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)],
         "pkv_prefill_ws_size": [LP, SP, i32, i32, ctypes.POINTER(sz)],
         "pkv_prefill": [LP, SP, i32, i32, i32, vp, vp, vp, sz, vp, vp],
@@ -436,6 +438,25 @@ def window_decode(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws=None, 
     _check(load().pkv_window_decode(ctypes.byref(lay), arr, n, layer, n_q_heads, window, n_sink, q,
                                     k_new, v_new, ik_new, out, ws, ws_bytes, status,
                                     _stream(stream)), "pkv_window_decode")
+
+
+def window_prefill_ws_size(lay, seqs, n_q_heads, window, n_sink) -> int:
+    arr, n = _seqs(seqs)
+    out = ctypes.c_size_t()
+    _check(load().pkv_window_prefill_ws_size(ctypes.byref(lay), arr, n, n_q_heads, window, n_sink,
+                                             ctypes.byref(out)), "pkv_window_prefill_ws_size")
+    return out.value
+
+
+def window_prefill(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws, status=None,
+                   stream=None):
+    """Chunk attention on the tensor cores over the newest `window` positions
+    of each query and the first n_sink (the chunk already stored)."""
+    arr, n = _seqs(seqs)
+    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    q, out, ws, status = _here("pkv_window_prefill", q, out, ws, status)
+    _check(load().pkv_window_prefill(ctypes.byref(lay), arr, n, layer, n_q_heads, window, n_sink, q,
+                                     out, ws, ws_bytes, status, _stream(stream)), "pkv_window_prefill")
 
 
 def window_dead_pages(page_pos: int, length: int, window: int, n_sink: int):

@@ -87,3 +87,26 @@ def test_calls_take_only_contiguous_tensors_of_the_device():
     with pytest.raises(pkv.PkvError) as e:
         pkv.window_decode(lay, [_seq(lay)], 0, 4, 100, 4, torch.zeros(4, 256, dtype=torch.bfloat16), 0x1000, stream=0)
     assert e.value.code == pkv.EINVAL
+
+
+# ---- the chunk form ------------------------------------------------------------
+
+def _chunk(lay, seqs, window=100, n_sink=4, hq=4, layer=0, q=0x1000, out=0x1000, ws=0x1000, ws_bytes=1 << 40):
+    arr, n = pkv._seqs(seqs)
+    return pkv.load().pkv_window_prefill(ctypes.byref(lay), arr, n, layer, hq, window, n_sink, q, out, ws, ws_bytes,
+                                         None, None)
+
+
+def test_chunk_refusals_before_launch():
+    # with a stream that has queries the call asks for the SM count before it
+    # checks its pointers: every answer here is a refusal either way
+    lay = pkv.layout(2, 2, 256, 128)
+    s = _seq(lay, n_new=30)
+    for kw in (dict(window=0), dict(window=-1), dict(n_sink=-1), dict(hq=3), dict(layer=2)):
+        assert _chunk(lay, [s], **kw) == pkv.EINVAL, kw
+    assert _chunk(pkv.layout(2, 2, 256, 128, pkv.KV_E4M3), [_seq(pkv.layout(2, 2, 256, 128, pkv.KV_E4M3))]) == pkv.EINVAL
+    for kw in (dict(q=None), dict(out=None), dict(q=0x1008), dict(out=0x1008), dict(ws=None), dict(ws=0x1080), dict(ws_bytes=64)):
+        assert _chunk(lay, [s], **kw) != pkv.OK, kw
+    assert _chunk(lay, [_seq(lay, n_new=601)]) == pkv.EINVAL
+    assert _chunk(lay, [_seq(lay, length=801, n_new=30)]) == pkv.EINVAL
+    assert pkv.load().pkv_window_prefill_ws_size(ctypes.byref(lay), pkv._seqs([s])[0], 1, 4, 100, 4, None) == pkv.EINVAL
