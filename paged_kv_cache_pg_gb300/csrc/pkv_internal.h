@@ -60,8 +60,8 @@ struct DecodeMaps {
 // Index of the map for [base, base + rows*512 B) in `maps` (added if new),
 // or -1 when none can be made (no driver entry point, or maps full).
 // bytes8: rows of 256 bytes (e4m3 codes, boxes of 128 x 16) instead of 256
-// bf16 elements (boxes of 64 x 16); tile: the 3D tile view of bf16 rows,
-// boxes of {64, box_rows, box_chunks} (box_rows 16, 64 or 128, box_chunks 2 or 4).
+// bf16 elements (boxes of 64 x 16); tile: the 3D tile view, of code rows boxes
+// of {128, 16, 2}, of bf16 rows boxes of {64, box_rows, box_chunks} (box_rows 16, 64 or 128, box_chunks 2 or 4).
 int row_map(DecodeMaps &maps, int &n_maps, const void *base, uint64_t rows, bool bytes8,
             bool tile = false, int box_rows = 16, int box_chunks = 1);
 
@@ -232,12 +232,10 @@ int launch_decode8(const Common &c, const DecodePlan &plan, const DecodeMaps &ma
                    const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
                    const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 
-// Windowed decode (pkv_window.cu): CTAs of a cluster for a window, plan and
-// launch; partials of long windows use the decode layout and its combine.
-int window_cluster(int32_t window, int32_t n_sink);
+// Windowed decode (pkv_window.cu): CTAs that share a split, plan and launch.
+int window_pieces(int32_t window, int32_t n_sink);
 int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan);
-// Row maps of the streams: 3D boxes of 16 rows over all dims (bf16, in
-// tma_k) or the e4m3 code rows' 2D boxes (in tma).
+// Row maps of the streams (in tma): 3D boxes of 16 whole rows, bf16 or codes.
 void plan_window_maps(Common &c, const pkv_layout *layout, const pkv_seq *seqs, DecodeMaps &maps);
 int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &maps, int32_t window,
                   int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,

@@ -32,9 +32,18 @@ namespace {
 
 constexpr int kTile = 16;                    // keys a stage
 constexpr int kMaxCols = 32;                 // query columns of one unit
-constexpr int kMaxCluster = 8;
+constexpr int kMaxPieces = 8;           // CTAs that share a split
 constexpr int kSplitTiles = 40;              // tiles of a CTA's run at most
 constexpr int kMaxPages = kSplitTiles * kTile / 4 + 4;  // pages a CTA's run can touch
+// CTAs of a call up to which a split's CTAs are clustered (two fill an SM).
+// Past it a cluster waits for eight free places on neighbouring SMs while
+// other places stand empty: 64 streams of 4,096-key windows took 116 us
+// clustered and XX us as single CTAs with a combine kernel; four streams of
+// 1,024-key windows YY us clustered and ZZ us with the second kernel.
+#ifndef PKV_WINDOW_CLUSTER_CTAS
+#define PKV_WINDOW_CLUSTER_CTAS 304
+#endif
+constexpr int kClusterCtas = PKV_WINDOW_CLUSTER_CTAS;
 constexpr int kFreshGuard = 32;              // see decode_partial: rows a kernel just before may write
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
 
@@ -75,15 +84,12 @@ struct WinArgs {
     const uint16_t *k_new;  // fused store of the new tokens, or null
     const uint16_t *v_new;
     const uint16_t *ik_new;
-    int32_t window, n_sink, cluster;
+    int32_t window, n_sink;
+    int32_t pieces;     // CTAs that share a split
+    int32_t clustered;  // they are a cluster and merge among themselves
 };
 
 // ---- cluster helpers ----------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 // All threads of the cluster meet.  A warp whose lanes took different paths
 // (the producer's) may still be split behind a CTA barrier, and a warp that
 // arrives in two parts would count twice: the warp is joined first, and the
@@ -168,16 +174,16 @@ struct Run {
     int sink_page, win_page, n_sink_pages, n_pages;  // the page list: sinks' pages, then the window's
 };
 
-__device__ __forceinline__ Run locate(const Common &c, const WinArgs &a, uint32_t rank) {
+__device__ __forceinline__ Run locate(const Common &c, const WinArgs &a, int rank) {
     Run u;
-    const int item = static_cast<int>(blockIdx.x) / a.cluster;
+    const int item = static_cast<int>(blockIdx.x) / a.pieces;
     u.s = find_seq(c.n_seqs, item, [&](int t) { return c.seq[t].work_off; });
     const SeqDev &sd = c.seq[u.s];
     const int r = item - sd.work_off;
     u.kvh = r / sd.nsplit;
     u.split = r - u.kvh * sd.nsplit;
     u.sp = window_span(sd.len, sd.n_new, a.window, a.n_sink, kTile);
-    u.key0 = min(u.sp.nkeys, (u.split * a.cluster + static_cast<int>(rank)) * sd.split_len);
+    u.key0 = min(u.sp.nkeys, (u.split * a.pieces + rank) * sd.split_len);
     u.key1 = min(u.sp.nkeys, u.key0 + sd.split_len);
     u.ntiles = (u.key1 - u.key0 + kTile - 1) / kTile;
     u.qbase = sd.len - sd.n_new;
@@ -249,25 +255,15 @@ __device__ __forceinline__ KeySrc key_src(const SeqDev &sd, const WinArgs &a, co
     return k;
 }
 
-// Stage bf16 tile t into `slot` (the producer warp); the copies complete on
-// `bar`, and new rows are stored into the cache too.
+// Stage bf16 tile t into `slot` key by key (the producer warp); the copies
+// complete on `bar`, and new rows are stored into the cache too.
 __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const SeqDev &sd, const Run &u,
-                                        const Ctx &x, const void *map, int t, int slot, uint64_t *bar,
-                                        int lane, uint64_t pol) {
+                                        const Ctx &x, int t, int slot, uint64_t *bar, int lane, uint64_t pol) {
     const int H = c.n_kv_heads;
     const int64_t v_gap = (int64_t)H * sd.ptok * kHeadDim;  // V row - K row
     const KeySrc k = key_src(sd, a, u, x, t, lane);
     const int64_t krow = k.page + off_k(sd.ptok, u.kvh, k.row);
     uint8_t *kst = x.stages + slot * Cfg<false>::stage, *vst = kst + Cfg<false>::half;
-    if (map != nullptr && __all_sync(0xffffffffu, k.seen && !k.fresh)) {
-        if (lane == 0) {
-            const int y = static_cast<int>(sd.layer_row + krow / kHeadDim);
-            mbar_arrive_expect_tx(bar, Cfg<false>::stage);
-            tma_load_3d(kst, map, 0, y, 0, bar, pol);
-            tma_load_3d(vst, map, 0, y + static_cast<int>(v_gap / kHeadDim), 0, bar, pol);
-        }
-        return;
-    }
     const uint16_t *ksrc, *vsrc;
     if (k.fresh) {
         const int64_t r = ((int64_t)sd.tok_off + (k.pos - u.qbase)) * H + u.kvh;
@@ -312,8 +308,7 @@ __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const
 // The same for e4m3 pages: 16 code rows of K and V and their scales.  New rows
 // are quantized here (the rule of pkv_store) into the stage and the cache.
 __device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const SeqDev &sd, const Run &u,
-                                       const Ctx &x, const void *map, int t, int slot, uint64_t *bar,
-                                       int lane, uint64_t pol) {
+                                       const Ctx &x, int t, int slot, uint64_t *bar, int lane, uint64_t pol) {
     const int H = c.n_kv_heads;
     const KeySrc k = key_src(sd, a, u, x, t, lane);
     const uint8_t *base = reinterpret_cast<const uint8_t *>(sd.layer_base);
@@ -323,20 +318,6 @@ __device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const 
     uint8_t *st = x.stages + slot * Cfg<true>::stage;
     uint8_t *sc = reinterpret_cast<uint8_t *>(x.scl) + slot * 128;
     constexpr int kCodes = Cfg<true>::half;
-    if (map != nullptr && __all_sync(0xffffffffu, k.seen && !k.fresh)) {
-        // one page holds the 16 keys: their code rows and scales are runs
-        if (lane == 0) {
-            const int yk = static_cast<int>(sd.layer_row + kc / 256), yv = static_cast<int>(sd.layer_row + vc / 256);
-            mbar_arrive_expect_tx(bar, Cfg<true>::stage + 128);
-            tma_load_2d(st, map, 0, yk, bar, pol);
-            tma_load_2d(st + kHalf8, map, 128, yk, bar, pol);
-            tma_load_2d(st + kCodes, map, 0, yv, bar, pol);
-            tma_load_2d(st + kCodes + kHalf8, map, 128, yv, bar, pol);
-            bulk_g2s(sc, base + pg + off8_scale(false, H, sd.ptok, u.kvh, k.row), 64, bar, pol);
-            bulk_g2s(sc + 64, base + pg + off8_scale(true, H, sd.ptok, u.kvh, k.row), 64, bar, pol);
-        }
-        return;
-    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int item = lane + 32 * i, rr = item >> 4, ch = item & 15;
@@ -390,6 +371,55 @@ __device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const 
     if (lane == 0) mbar_arrive(bar);
 }
 
+// One query column's softmax over some keys: maximum, sum, and O of four dims.
+struct Sum {
+    float m, l;
+    float4 o;
+};
+
+// The sum over a split's pieces, in order; ml(k) and acc(k) load piece k's.
+template <typename FM, typename FO>
+__device__ __forceinline__ Sum merge_pieces(int n, FM ml_of, FO acc_of) {
+    float2 ml[kMaxPieces];
+    float4 v[kMaxPieces];
+#pragma unroll
+    for (int k = 0; k < kMaxPieces; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (k < n) {
+            ml[k] = ml_of(k);
+            v[k] = acc_of(k);
+        }
+    }
+    Sum r;
+    r.m = -INFINITY;
+    r.l = 0.f;
+    r.o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kMaxPieces; ++k) r.m = fmaxf(r.m, ml[k].x);
+#pragma unroll
+    for (int k = 0; k < kMaxPieces; ++k) {
+        const float w = r.m == -INFINITY ? 0.f : ex2(ml[k].x - r.m);
+        // fused explicitly: both kernels that merge round alike
+        r.l = fmaf(w, ml[k].y, r.l);
+        r.o.x = fmaf(w, v[k].x, r.o.x);
+        r.o.y = fmaf(w, v[k].y, r.o.y);
+        r.o.z = fmaf(w, v[k].z, r.o.z);
+        r.o.w = fmaf(w, v[k].w, r.o.w);
+    }
+    return r;
+}
+
+// Four dims of an output row (zeros where no key was seen).
+__device__ __forceinline__ void write_out(uint16_t *out, const Sum &r) {
+    const bool any = r.l > 0.f;
+    const float l = any ? r.l : 1.f;
+    uint2 pk;
+    pk.x = pack_bf16(any ? __fdiv_rn(r.o.x, l) : 0.f, any ? __fdiv_rn(r.o.y, l) : 0.f);
+    pk.y = pack_bf16(any ? __fdiv_rn(r.o.z, l) : 0.f, any ? __fdiv_rn(r.o.w, l) : 0.f);
+    *reinterpret_cast<uint2 *>(out) = pk;
+}
+
 // Whether the query at position p (-1: a padding column) sees position kp.
 __device__ __forceinline__ bool sees(int p, int kp, int window, int n_sink) {
     return kp <= p && (kp > p - window || kp < n_sink);
@@ -412,10 +442,10 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     constexpr int S = F::slots;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t rank = cluster_rank();
+    const int rank = static_cast<int>(blockIdx.x) % a.pieces;  // its place in a cluster too
     const Run u = locate(c, a, rank);
     const SeqDev &sd = c.seq[u.s];
-    const int ncols = sd.ncols, G = c.group;
+    const int ncols = sd.ncols, G = c.group, H = c.n_kv_heads;
     const int ncg = (ncols + 7) >> 3;           // column groups of 8
     // Tiles at once (key slices), a divisor of the slots: each slot then always
     // belongs to one slice, which takes every phase of its barrier.  (A slice
@@ -459,25 +489,72 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     if (warp == F::consumers) {
         // ---------------- producer ----------------
         const uint64_t pol = policy_evict_first();
-        const int tma = kFp8 ? sd.tma : sd.tma_k;
-        const void *map = tma >= 0 ? &maps.map[tma] : nullptr;
+        const void *map = sd.tma >= 0 ? &maps.map[sd.tma] : nullptr;
+        const int v_rows = H * sd.ptok;       // map rows from a K row to its V row
         // cached rows more than kFreshGuard below the new tokens do not depend
         // on the previous kernel: their tiles stream before the wait
         const int early_end = u.qbase - kFreshGuard;
         bool waited = false;
+        int yk = -1;            // lane i: map row of tile t0 + i's first K row, -1: not a run of cached rows
+        int64_t sc = 0;         // e4m3: byte offset of its K scales
         for (int t = 0; t < u.ntiles; ++t, ++issued) {
-            const int slot = t % S;
-            if (t >= S && !__all_sync(0xffffffffu, mbar_wait(&x.empty[slot], ((t / S) - 1) & 1, c.status))) {
-                *x.abort_flag = 1;
-                break;
+            if ((t & 31) == 0) {
+                // the next 32 tiles' rows, a tile a lane: looked up one by one
+                // they would take the warp longer than a tile takes to arrive
+                const int v0 = u.key0 + (t + lane) * kTile, p0 = pos_of(u.sp, v0);
+                yk = -1;
+                if (map != nullptr && v0 + kTile <= u.key1 &&
+                    (p0 >= u.sp.lo || p0 + kTile <= a.n_sink || a.n_sink >= u.sp.lo) &&
+                    (a.k_new == nullptr || p0 + kTile <= u.qbase)) {
+                    int row = p0;
+                    int64_t pg = 0;
+                    if (sd.table) {
+                        const int page = p0 / sd.ptok;
+                        row = p0 - page * sd.ptok;
+                        pg = x.pages[v0 < u.sp.sink_end ? page - u.sink_page : u.n_sink_pages + page - u.win_page];
+                        if (pg < 0) pg = 0;  // reported when it was looked up
+                    }
+                    if constexpr (kFp8) {
+                        yk = static_cast<int>(sd.layer_row + (2 * pg + off8_code(false, H, sd.ptok, u.kvh, row)) / kHeadDim);
+                        sc = 2 * pg + off8_scale(false, H, sd.ptok, u.kvh, row);
+                    } else {
+                        yk = static_cast<int>(sd.layer_row + (pg + off_k(sd.ptok, u.kvh, row)) / kHeadDim);
+                    }
+                }
+            }
+            const int slot = t % S, y = __shfl_sync(0xffffffffu, yk, t & 31);
+            uint64_t *const bar = &x.full[slot];
+            if (t >= S) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&x.empty[slot], ((t / S) - 1) & 1, c.status))) {
+                    *x.abort_flag = 1;
+                    break;
+                }
+                fence_proxy_async_smem();  // the slot's last reads come before the next tile's writes
             }
             if (!waited && pos_of(u.sp, u.key0 + t * kTile) + kTile > early_end) {
                 pdl_wait();
                 waited = true;
             }
-            fence_proxy_async_smem();  // the slot's last reads come before the next tile's writes
-            if constexpr (kFp8) stage8(c, a, sd, u, x, map, t, slot, &x.full[slot], lane, pol);
-            else stage16(c, a, sd, u, x, map, t, slot, &x.full[slot], lane, pol);
+            if (y >= 0) {
+                // one page holds the 16 keys: a copy of K, one of V, and with
+                // e4m3 pages one of each scale run
+                uint8_t *const kst = x.stages + slot * F::stage;
+                const int64_t s0 = kFp8 ? shfl64(sc, t & 31) : 0;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, F::stage + (kFp8 ? 128 : 0));
+                    tma_load_3d(kst, map, 0, y, 0, bar, pol);
+                    tma_load_3d(kst + F::half, map, 0, y + v_rows, 0, bar, pol);
+                    if constexpr (kFp8) {
+                        const uint8_t *base = reinterpret_cast<const uint8_t *>(sd.layer_base) + s0;
+                        bulk_g2s(x.scl + slot * 32, base, 64, bar, pol);
+                        bulk_g2s(x.scl + slot * 32 + 16, base + 4 * (int64_t)v_rows, 64, bar, pol);
+                    }
+                }
+            } else if constexpr (kFp8) {
+                stage8(c, a, sd, u, x, t, slot, bar, lane, pol);
+            } else {
+                stage16(c, a, sd, u, x, t, slot, bar, lane, pol);
+            }
             __syncwarp();
         }
         if (!waited) pdl_wait();
@@ -731,80 +808,93 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         *reinterpret_cast<float4 *>(sum + col * kHeadDim + d) = O;
         if (d == 0) *reinterpret_cast<float2 *>(sum_ml + 2 * col) = make_float2(M, L);
     }
-    // ---- then the cluster's CTAs, in order ----
+    // ---- then the split's CTAs, in order: in a cluster here, else window_combine ----
+    if (!a.clustered && a.pieces > 1) {
+        __syncthreads();
+        if (failed) return;
+        // partials of a piece: O [column][256], then (m, l) [column]
+        const int64_t piece = ((int64_t)u.kvh * sd.nsplit + u.split) * a.pieces + rank;
+        float *acc_out = a.ws + sd.ws_off + piece * ncols * kHeadDim;
+        float *ml_out = a.ws + sd.ws_off + ((int64_t)H * sd.nsplit * a.pieces * kHeadDim + piece * 2) * ncols;
+        for (int idx = tid; idx < ncols * (kHeadDim / 4); idx += F::threads)
+            reinterpret_cast<float4 *>(acc_out)[idx] = reinterpret_cast<const float4 *>(sum)[idx];
+        for (int idx = tid; idx < 2 * ncols; idx += F::threads) ml_out[idx] = sum_ml[idx];
+        return;
+    }
     cluster_sync();
-    const bool single = sd.nsplit == 1;
-    float *part_acc = a.ws + sd.ws_off;
-    float *part_ml = part_acc + (int64_t)c.n_kv_heads * sd.nsplit * ncols * kHeadDim;
-    const int64_t pidx = ((int64_t)u.kvh * sd.nsplit + u.split) * ncols;
     if (!failed) {
-        for (int idx = static_cast<int>(rank) * F::threads + tid; idx < ncols * (kHeadDim / 4);
-             idx += a.cluster * F::threads) {
+        for (int idx = rank * F::threads + tid; idx < ncols * (kHeadDim / 4); idx += a.pieces * F::threads) {
             const int col = idx / (kHeadDim / 4), d = 4 * (idx - col * (kHeadDim / 4));
-            float2 ml[kMaxCluster];
-            float4 v[kMaxCluster];
-#pragma unroll
-            for (int k = 0; k < kMaxCluster; ++k) {
-                ml[k] = make_float2(-INFINITY, 0.f);
-                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (k < a.cluster) {
-                    ml[k] = peer_ld2(peer_addr(sum_ml + 2 * col, k));
-                    v[k] = peer_ld4(peer_addr(sum + col * kHeadDim + d, k));
-                }
-            }
-            float M = -INFINITY, L = 0.f;
-#pragma unroll
-            for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, ml[k].x);
-            float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int k = 0; k < kMaxCluster; ++k) {
-                const float w = M == -INFINITY ? 0.f : ex2(ml[k].x - M);
-                L += w * ml[k].y;
-                O.x += w * v[k].x;
-                O.y += w * v[k].y;
-                O.z += w * v[k].z;
-                O.w += w * v[k].w;
-            }
-            if (single) {
-                const bool any = L > 0.f;
-                const float lz = any ? L : 1.f;
-                const int j = col / G;
-                uint2 pk;
-                pk.x = pack_bf16(any ? O.x / lz : 0.f, any ? O.y / lz : 0.f);
-                pk.y = pack_bf16(any ? O.z / lz : 0.f, any ? O.w / lz : 0.f);
-                *reinterpret_cast<uint2 *>(
-                    a.out + (((int64_t)sd.tok_off + j) * c.n_q_heads + u.kvh * G + (col - j * G)) * kHeadDim + d) = pk;
-            } else {
-                *reinterpret_cast<float4 *>(part_acc + (pidx + col) * kHeadDim + d) = O;
-                if (d == 0) *reinterpret_cast<float2 *>(part_ml + (pidx + col) * 2) = make_float2(M, L);
-            }
+            const Sum r = merge_pieces(
+                a.pieces, [&](int k) { return peer_ld2(peer_addr(sum_ml + 2 * col, k)); },
+                [&](int k) { return peer_ld4(peer_addr(sum + col * kHeadDim + d, k)); });
+            const int j = col / G;
+            write_out(a.out + (((int64_t)sd.tok_off + j) * c.n_q_heads + u.kvh * G + (col - j * G)) * kHeadDim + d, r);
         }
     }
     cluster_sync();  // the peers have read this CTA's sums
 }
 
+// Merge of the pieces' partials for calls whose CTAs are not clustered: 64
+// threads a query column, four dims each, the pieces of a split in order as a
+// cluster merges them, then the splits in order.
+constexpr int kCombThreads = 256;
+__global__ void __launch_bounds__(kCombThreads)
+    window_combine(const __grid_constant__ Common c, const __grid_constant__ WinArgs a, int32_t total) {
+    pdl_trigger();  // the next kernel waits for this grid before it reads what it writes
+    const int i = static_cast<int>(blockIdx.x) * (kCombThreads / 64) + (threadIdx.x >> 6);
+    if (i >= total) return;
+    const int s = find_seq(c.n_seqs, i, [&](int t) { return c.seq[t].comb_off; });
+    const SeqDev &sd = c.seq[s];
+    const int r = i - sd.comb_off, ncols = sd.ncols, unit = r / ncols, col = r - unit * ncols, G = c.group;
+    const int d = 4 * (threadIdx.x & 63), j = col / G;
+    const int64_t p0 = (int64_t)unit * sd.nsplit * a.pieces;
+    const float *acc = a.ws + sd.ws_off + (p0 * ncols + col) * kHeadDim + d;
+    const float *ml = a.ws + sd.ws_off + (int64_t)c.n_kv_heads * sd.nsplit * a.pieces * ncols * kHeadDim + (p0 * ncols + col) * 2;
+    uint16_t *out = a.out + (((int64_t)sd.tok_off + j) * c.n_q_heads + unit * G + (col - j * G)) * kHeadDim + d;
+    asm volatile("" ::"l"(acc), "l"(ml), "l"(out));
+    pdl_wait();
+    Sum t;
+    for (int sp = 0; sp < sd.nsplit; ++sp) {
+        const Sum x = merge_pieces(
+            a.pieces, [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(ml + (int64_t)(sp * a.pieces + k) * ncols * 2)); },
+            [&](int k) { return __ldcg(reinterpret_cast<const float4 *>(acc + (int64_t)(sp * a.pieces + k) * ncols * kHeadDim)); });
+        if (sp == 0) {
+            t = x;
+        } else {
+            const float M = fmaxf(t.m, x.m);
+            const float wt = M == -INFINITY ? 0.f : ex2(t.m - M), wx = M == -INFINITY ? 0.f : ex2(x.m - M);
+            t.l = wt * t.l + wx * x.l;
+            t.o.x = wt * t.o.x + wx * x.o.x;
+            t.o.y = wt * t.o.y + wx * x.o.y;
+            t.o.z = wt * t.o.z + wx * x.o.z;
+            t.o.w = wt * t.o.w + wx * x.o.w;
+            t.m = M;
+        }
+    }
+    write_out(out, t);
+}
+
 }  // namespace
 
-// A split is a cluster of CTAs that share its tiles, its size set by the
-// window alone (so a stream's bits do not depend on its batch): eight tiles a
-// CTA before another one joins, eight CTAs at most.
-int window_cluster(int32_t window, int32_t n_sink) {
+// CTAs that share a split, by the window alone (a stream's bits must not
+// depend on its batch): eight tiles a CTA before another one joins.
+int window_pieces(int32_t window, int32_t n_sink) {
     const int64_t tiles = ((int64_t)window + n_sink) / kTile + 2;
-    int cs = 1;
-    while (cs < kMaxCluster && tiles > 8 * cs) cs *= 2;
-    return cs;
+    int n = 1;
+    while (n < kMaxPieces && tiles > 8 * n) n *= 2;
+    return n;
 }
 
 // Splits only where a CTA's run would pass kSplitTiles tiles.
 int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
-    int64_t items = 0;
-    int32_t comb = 0;
-    int64_t floats = 0;
-    const int cs = window_cluster(window, n_sink);
+    int64_t items = 0, cols = 0, floats = 0;
+    const int pieces = window_pieces(window, n_sink);
+    bool split = false;
     for (int s = 0; s < c.n_seqs; ++s) {
         SeqDev &d = c.seq[s];
         d.work_off = static_cast<int32_t>(items);
-        d.comb_off = comb;
+        d.comb_off = static_cast<int32_t>(cols);
         d.ws_off = floats;
         d.ncols = d.n_new * c.group;
         if (d.ncols > kMaxCols) return PKV_EINVAL;
@@ -813,21 +903,20 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
         if (d.ncols == 0) continue;
         const WindowSpan sp = window_span(d.len, d.n_new, window, n_sink, kTile);
         const int tiles = (sp.nkeys + kTile - 1) / kTile;
-        d.nsplit = (tiles + cs * kSplitTiles - 1) / (cs * kSplitTiles);
-        if (d.nsplit > 2048) return PKV_EINVAL;
-        const int per = (tiles + d.nsplit * cs - 1) / (d.nsplit * cs);
+        d.nsplit = (tiles + pieces * kSplitTiles - 1) / (pieces * kSplitTiles);
+        const int per = (tiles + d.nsplit * pieces - 1) / (d.nsplit * pieces);
         d.split_len = per * kTile;
+        split |= d.nsplit > 1;
         items += (int64_t)c.n_kv_heads * d.nsplit;
-        if (d.nsplit > 1) {
-            comb += c.n_kv_heads * d.ncols * comb_ctas(d.nsplit);
-            floats += (int64_t)c.n_kv_heads * d.nsplit * d.ncols * (kHeadDim + 2);
-            floats = (floats + 63) / 64 * 64;
-        }
+        cols += (int64_t)c.n_kv_heads * d.ncols;
+        floats += (int64_t)c.n_kv_heads * d.nsplit * pieces * d.ncols * (kHeadDim + 2);
+        floats = (floats + 63) / 64 * 64;
     }
-    if (items * cs > INT32_MAX) return PKV_EINVAL;
+    if (items * pieces > INT32_MAX) return PKV_EINVAL;
+    const bool combine = pieces > 1 && (split || items * pieces > kClusterCtas);
     plan->total_items = static_cast<int32_t>(items);
-    plan->total_comb = comb;
-    plan->ws_bytes = static_cast<size_t>(floats) * 4;
+    plan->total_comb = combine ? static_cast<int32_t>(cols) : 0;
+    plan->ws_bytes = combine ? static_cast<size_t>(floats) * 4 : 0;
     return PKV_OK;
 }
 
@@ -846,12 +935,15 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
                                          cudaSharedmemCarveoutMaxShared) != cudaSuccess)
                     return PKV_ECUDA;
             }
-            return PKV_OK;
+            // an SM left with a small carveout could not take a CTA of the next call
+            return cuda_rc(cudaFuncSetAttribute(window_combine, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                cudaSharedmemCarveoutMaxShared));
         }) != PKV_OK)
         return PKV_ECUDA;
-    const WinArgs a{q, out, ws, k_new, v_new, ik_new, window, n_sink, window_cluster(window, n_sink)};
+    WinArgs a{q, out, ws, k_new, v_new, ik_new, window, n_sink, window_pieces(window, n_sink), 0};
+    a.clustered = plan.total_comb == 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.total_items) * a.cluster);
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.total_items) * a.pieces);
     cfg.blockDim = dim3(c.kv_fp8 ? Cfg<true>::threads : Cfg<false>::threads);
     cfg.dynamicSmemBytes = c.kv_fp8 ? Cfg<true>::smem : Cfg<false>::smem;
     cfg.stream = stream;
@@ -859,14 +951,16 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.cluster;
+    attr[1].val.clusterDim.x = a.clustered ? a.pieces : 1;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, c.kv_fp8 ? window_partial<true> : window_partial<false>, c, maps, a) != cudaSuccess)
         return PKV_ECUDA;
-    if (plan.total_comb > 0) return launch_combine(c, plan, q, out, ws, stream);
-    return PKV_OK;
+    if (a.clustered) return PKV_OK;
+    const int per = kCombThreads / 64;
+    return launch_status(launch_pdl(window_combine, static_cast<unsigned>((plan.total_comb + per - 1) / per),
+                                    kCombThreads, 0, stream, c, a, plan.total_comb));
 }
 
 }  // namespace pkv

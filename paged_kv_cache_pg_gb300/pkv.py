@@ -146,10 +146,23 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_current = None  # (torch, current device's raw stream by device index), once torch is needed
+
+
+def _torch_streams():
+    global _current
+    if _current is None:
+        import torch
+        # the raw handle without building a Stream object (about 3 us of a call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current = (torch, raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+    return _current
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        torch, raw = _current or _torch_streams()
+        return raw(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -168,20 +181,29 @@ def _here(what: str, *tensors, dtype=None):
     when given); None and addresses given as ints are taken as they are."""
     dev, out = None, []
     for t in tensors:
-        if t is not None and not isinstance(t, int):
-            if dev is None and t.get_device() >= 0:
-                import torch
-                dev = torch.cuda.current_device()
-            if t.get_device() != dev or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+        if t is not None and type(t) is not int:
+            at = t.get_device()
+            if dev is None and at >= 0:
+                dev = (_current or _torch_streams())[0].cuda.current_device()
+            if at != dev or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
                 raise PkvError(EINVAL, f"{what}: not a contiguous tensor of the type on the current device")
             t = t.data_ptr()
         out.append(t)
     return out
 
 
+_np = None
+
+
 def _host_i32(a):
-    import numpy as np
-    return np.ascontiguousarray(a, dtype=np.int32)
+    """A contiguous int32 numpy array of host integers, and its address."""
+    global _np
+    if _np is None:
+        import numpy
+        _np = numpy
+    if type(a) is not _np.ndarray or a.dtype != _np.int32 or not a.flags.c_contiguous:
+        a = _np.ascontiguousarray(a, dtype=_np.int32)
+    return a, a.__array_interface__["data"][0]
 
 
 # ---- descriptors ------------------------------------------------------------
@@ -274,19 +296,19 @@ class Arena:
         """Share a stream's pages with a new one: (its ids, copy), where copy
         is None or (src, dst, n_pos) of the last page, which is its own."""
         import numpy as np
-        ids = _host_i32(ids)
+        ids, at = _host_i32(ids)
         out = np.empty(max(1, ids.size), dtype=np.int32)
         s, d, n = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
-        _check(self._lib.pkv_pages_fork(self._h, ids.ctypes.data, ids.size, length, out.ctypes.data,
+        _check(self._lib.pkv_pages_fork(self._h, at, ids.size, length, out.ctypes.data,
                                         ctypes.byref(s), ctypes.byref(d), ctypes.byref(n)),
                "pkv_pages_fork")
         return out[:ids.size], ((s.value, d.value, n.value) if n.value else None)
 
     def holders(self, ids):
         import numpy as np
-        ids = _host_i32(ids)
+        ids, at = _host_i32(ids)
         out = np.zeros(max(1, ids.size), dtype=np.int32)
-        _check(self._lib.pkv_pages_holders(self._h, ids.ctypes.data, ids.size, out.ctypes.data),
+        _check(self._lib.pkv_pages_holders(self._h, at, ids.size, out.ctypes.data),
                "pkv_pages_holders")
         return out[:ids.size]
 
@@ -353,30 +375,30 @@ def gather(lay, seqs, layer, kind, out, status=None, stream=None):
 def pages_copy(lay, page_pos: int, memory, n_pages: int, src, dst, n_pos=None, stream=None):
     """Copy pages src[i] to dst[i] of the arena at `memory`, whole or their
     first n_pos[i] positions; src, dst, n_pos: host integers."""
-    src, dst = _host_i32(src), _host_i32(dst)
-    if src.size != dst.size or (n_pos is not None and len(n_pos) != src.size):
+    (src, ps), (dst, pd) = _host_i32(src), _host_i32(dst)
+    n_pos, pn = (None, None) if n_pos is None else _host_i32(n_pos)
+    n = src.size
+    if dst.size != n or (n_pos is not None and n_pos.size != n):
         raise PkvError(EINVAL, "pkv_pages_copy: lists of different lengths")
-    n_pos = None if n_pos is None else _host_i32(n_pos)
     base, = _here("pkv_pages_copy", memory)
-    if base is not memory and memory.numel() * memory.element_size() < 2 * n_pages * page_elems(lay, page_pos):
+    if base is not memory and memory.nbytes < 2 * n_pages * page_elems(lay, page_pos):
         raise PkvError(EINVAL, "pkv_pages_copy: the memory holds fewer pages")
-    _check(load().pkv_pages_copy(ctypes.byref(lay), page_pos, base, n_pages, src.ctypes.data, dst.ctypes.data,
-                                 None if n_pos is None else n_pos.ctypes.data, src.size,
+    _check(load().pkv_pages_copy(ctypes.byref(lay), page_pos, base, n_pages, ps, pd, pn, n,
                                  _stream(stream)), "pkv_pages_copy")
 
 
 def tables_remap(tables, src, dst, stream=None):
     """Rewrite device page tables after a compaction: entries src[i] become
     dst[i].  tables: int32 device tensors; src, dst: host integers."""
-    src, dst = _host_i32(src), _host_i32(dst)
+    (src, ps), (dst, pd) = _host_i32(src), _host_i32(dst)
     if src.size != dst.size:
         raise PkvError(EINVAL, "pkv_tables_remap: lists of different lengths")
-    import torch
+    torch = (_current or _torch_streams())[0]
     n = len(tables)
     ptrs = (ctypes.c_void_p * max(1, n))(*_here("pkv_tables_remap", *tables, dtype=torch.int32))
     sizes = (ctypes.c_int32 * max(1, n))(*[t.numel() for t in tables])
-    _check(load().pkv_tables_remap(ptrs, sizes, n, src.ctypes.data, dst.ctypes.data, src.size,
-                                   _stream(stream)), "pkv_tables_remap")
+    _check(load().pkv_tables_remap(ptrs, sizes, n, ps, pd, src.size, _stream(stream)),
+           "pkv_tables_remap")
 
 
 def pool(lay, seqs, layer, status=None, stream=None):
@@ -432,7 +454,7 @@ def window_decode(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws=None, 
     """Decode attention over the newest `window` positions and the first
     n_sink; with k_new/v_new (and ik_new) the new rows are stored too."""
     arr, n = _seqs(seqs)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    ws_bytes = 0 if ws is None else ws.nbytes
     q, k_new, v_new, ik_new, out, ws, status = _here("pkv_window_decode", q, k_new, v_new, ik_new, out,
                                                      ws, status)
     _check(load().pkv_window_decode(ctypes.byref(lay), arr, n, layer, n_q_heads, window, n_sink, q,
@@ -453,7 +475,7 @@ def window_prefill(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws, stat
     """Chunk attention on the tensor cores over the newest `window` positions
     of each query and the first n_sink (the chunk already stored)."""
     arr, n = _seqs(seqs)
-    ws_bytes = 0 if ws is None else ws.numel() * ws.element_size()
+    ws_bytes = 0 if ws is None else ws.nbytes
     q, out, ws, status = _here("pkv_window_prefill", q, out, ws, status)
     _check(load().pkv_window_prefill(ctypes.byref(lay), arr, n, layer, n_q_heads, window, n_sink, q,
                                      out, ws, ws_bytes, status, _stream(stream)), "pkv_window_prefill")

@@ -114,10 +114,18 @@ def test_full_launches_back_to_back_give_the_same_bits(fmt):
     q = t.randn(B, hq, 256, device="cuda").to(t.bfloat16)
     status = t.zeros(1, dtype=t.int32, device="cuda")
     outs = [t.zeros_like(q) for _ in range(40)]
+    ws = t.empty(pkv.window_decode_ws_size(lay, seqs, hq, 4096, 4) // 4, dtype=t.float32, device="cuda")
     for o in outs:
-        pkv.window_decode(lay, seqs, 0, hq, 4096, 4, q, o, status=status)
+        pkv.window_decode(lay, seqs, 0, hq, 4096, 4, q, o, ws, status=status)
     assert int(status) == 0 and outs[0].isfinite().all()
     assert all(t.equal(o, outs[0]) for o in outs)
+    # a stream alone takes the clustered kernel, the batch the combine: the same bits
+    assert pkv.window_decode_ws_size(lay, seqs, hq, 4096, 4) > 0
+    for i in (0, 17, 63):
+        alone = t.zeros_like(q[i:i + 1])
+        assert pkv.window_decode_ws_size(lay, seqs[i:i + 1], hq, 4096, 4) == 0
+        pkv.window_decode(lay, seqs[i:i + 1], 0, hq, 4096, 4, q[i:i + 1], alone)
+        assert t.equal(alone, outs[0][i:i + 1])
 
 
 @pytest.mark.parametrize("fmt", FMT)
