@@ -32,9 +32,10 @@ namespace {
 
 constexpr int kTile = 16;                    // keys a stage
 constexpr int kMaxCols = 32;                 // query columns of one unit
-constexpr int kMaxPieces = 8;           // CTAs that share a split
+constexpr int kMaxPieces = 8;           // pieces of a split
+constexpr int kMaxSlices = 4;           // key slices of a CTA
 constexpr int kSplitTiles = 40;              // tiles of a CTA's run at most
-constexpr int kMaxPages = kSplitTiles * kTile / 4 + 4;  // pages a CTA's run can touch
+constexpr int kMaxPages = kMaxPieces * kSplitTiles * kTile / 4 + 4;  // pages a CTA's run can touch
 // CTAs of a call up to which a split's CTAs are clustered (two fill an SM).
 // Past it a cluster waits for eight free places on neighbouring SMs while
 // other places stand empty: 64 streams of 4,096-key windows took 116 us
@@ -52,17 +53,18 @@ constexpr int kCfgHalf16 = 4 * kPlane;       // bf16: 16 rows of K (or V)
 constexpr int kHalf8 = kTile * 128;          // e4m3: one 128-byte half of 16 code rows
 constexpr int kCfgHalf8 = 2 * kHalf8;
 
-// Shapes of the two page formats' CTAs.  bf16: eight consumer warps, a pair a
-// tile (each sums O over half the dims).  e4m3: four, one a tile.
+// Shapes of the two page formats' CTAs: four consumer warps, each on a tile (and
+// column group) of its own with O over all dims in registers.  (Eight, a pair
+// a tile with half the dims each, computed S twice and left 96 registers a
+// thread: too few to load ahead of the MMAs, 2,100 cycles a tile.)
+constexpr int kConsumers = 4;
 template <bool kFp8>
 struct Cfg {
     static constexpr int half = kFp8 ? kCfgHalf8 : kCfgHalf16;   // K or V bytes of a stage
     static constexpr int stage = 2 * half;
     static constexpr int slots = kFp8 ? 12 : 6;
-    static constexpr int pair = kFp8 ? 1 : 2;                    // warps on one tile and column group
-    static constexpr int consumers = kFp8 ? 4 : 8;
+    static constexpr int consumers = kConsumers;
     static constexpr int threads = consumers * 32 + 32;
-    static constexpr int teams = consumers / pair;               // tiles (x column groups) at once
     static constexpr int row = kFp8 ? kHeadDim + 12 : kHeadDim + 4;  // floats of a merge row
     static constexpr int off_scl = slots * stage;                // e4m3: 16 K and 16 V scales a stage
     static constexpr int off_page = off_scl + (kFp8 ? slots * 128 : 0);
@@ -85,9 +87,17 @@ struct WinArgs {
     const uint16_t *v_new;
     const uint16_t *ik_new;
     int32_t window, n_sink;
-    int32_t pieces;     // CTAs that share a split
-    int32_t clustered;  // they are a cluster and merge among themselves
+    int32_t pieces;     // pieces of a split
+    int32_t run;        // pieces of a CTA; 0: one, and the split's CTAs are a cluster
 };
+
+// Key slices of a CTA (tiles it works on at once): a divisor of its slots.
+__host__ __device__ inline int slices_of(bool fp8, int ncols) {
+    const int ncg = (ncols + 7) >> 3, slots = fp8 ? Cfg<true>::slots : Cfg<false>::slots;
+    int n = kConsumers / ncg;
+    while (slots % n) --n;
+    return n;
+}
 
 // ---- cluster helpers ----------------------------------------------------------
 // All threads of the cluster meet.  A warp whose lanes took different paths
@@ -168,27 +178,30 @@ __device__ __forceinline__ void split_scale(float s, float &e, float &mant) {
 struct Run {
     WindowSpan sp;
     int s, kvh, split;
-    int key0, key1;        // virtual keys of this CTA
-    int ntiles;
+    int piece, n_pieces;   // its pieces of the split
+    int key0, key1;        // their virtual keys
+    int per;               // tiles of a piece
     int qbase;
     int sink_page, win_page, n_sink_pages, n_pages;  // the page list: sinks' pages, then the window's
 };
 
-__device__ __forceinline__ Run locate(const Common &c, const WinArgs &a, int rank) {
+__device__ __forceinline__ Run locate(const Common &c, const WinArgs &a) {
     Run u;
-    const int item = static_cast<int>(blockIdx.x) / a.pieces;
+    u.n_pieces = max(1, a.run);
+    const int per_split = a.pieces / u.n_pieces, b = static_cast<int>(blockIdx.x), item = b / per_split;
     u.s = find_seq(c.n_seqs, item, [&](int t) { return c.seq[t].work_off; });
     const SeqDev &sd = c.seq[u.s];
     const int r = item - sd.work_off;
     u.kvh = r / sd.nsplit;
     u.split = r - u.kvh * sd.nsplit;
+    u.piece = (b - item * per_split) * u.n_pieces;
     u.sp = window_span(sd.len, sd.n_new, a.window, a.n_sink, kTile);
-    u.key0 = min(u.sp.nkeys, (u.split * a.pieces + rank) * sd.split_len);
-    u.key1 = min(u.sp.nkeys, u.key0 + sd.split_len);
-    u.ntiles = (u.key1 - u.key0 + kTile - 1) / kTile;
+    u.per = sd.split_len / kTile;
+    u.key0 = min(u.sp.nkeys, (u.split * a.pieces + u.piece) * sd.split_len);
+    u.key1 = min(u.sp.nkeys, u.key0 + u.n_pieces * sd.split_len);
     u.qbase = sd.len - sd.n_new;
     u.sink_page = u.win_page = u.n_sink_pages = u.n_pages = 0;
-    if (sd.table && u.ntiles > 0) {
+    if (sd.table && u.key1 > u.key0) {
         if (u.key0 < u.sp.sink_end) {
             u.sink_page = u.key0 / sd.ptok;
             u.n_sink_pages = min(min(u.key1, u.sp.sink_end), a.n_sink) - 1;
@@ -231,9 +244,9 @@ struct KeySrc {
 };
 
 __device__ __forceinline__ KeySrc key_src(const SeqDev &sd, const WinArgs &a, const Run &u, const Ctx &x,
-                                          int t, int lane) {
+                                          int v0, int lane) {
     KeySrc k;
-    const int v = u.key0 + t * kTile + (lane & 15);
+    const int v = v0 + (lane & 15);
     const int p = pos_of(u.sp, v);
     k.seen = v < u.key1 && (p < a.n_sink || p >= u.sp.lo);
     // the last position of the run, the last sink, or the window's first position
@@ -255,13 +268,13 @@ __device__ __forceinline__ KeySrc key_src(const SeqDev &sd, const WinArgs &a, co
     return k;
 }
 
-// Stage bf16 tile t into `slot` key by key (the producer warp); the copies
+// Stage the bf16 tile of virtual keys v0 .. into `slot` key by key (the producer warp); the copies
 // complete on `bar`, and new rows are stored into the cache too.
 __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const SeqDev &sd, const Run &u,
-                                        const Ctx &x, int t, int slot, uint64_t *bar, int lane, uint64_t pol) {
+                                        const Ctx &x, int v0, int slot, uint64_t *bar, int lane, uint64_t pol) {
     const int H = c.n_kv_heads;
     const int64_t v_gap = (int64_t)H * sd.ptok * kHeadDim;  // V row - K row
-    const KeySrc k = key_src(sd, a, u, x, t, lane);
+    const KeySrc k = key_src(sd, a, u, x, v0, lane);
     const int64_t krow = k.page + off_k(sd.ptok, u.kvh, k.row);
     uint8_t *kst = x.stages + slot * Cfg<false>::stage, *vst = kst + Cfg<false>::half;
     const uint16_t *ksrc, *vsrc;
@@ -308,9 +321,9 @@ __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const
 // The same for e4m3 pages: 16 code rows of K and V and their scales.  New rows
 // are quantized here (the rule of pkv_store) into the stage and the cache.
 __device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const SeqDev &sd, const Run &u,
-                                       const Ctx &x, int t, int slot, uint64_t *bar, int lane, uint64_t pol) {
+                                       const Ctx &x, int v0, int slot, uint64_t *bar, int lane, uint64_t pol) {
     const int H = c.n_kv_heads;
-    const KeySrc k = key_src(sd, a, u, x, t, lane);
+    const KeySrc k = key_src(sd, a, u, x, v0, lane);
     const uint8_t *base = reinterpret_cast<const uint8_t *>(sd.layer_base);
     const int64_t pg = 2 * k.page;
     const int64_t kc = pg + off8_code(false, H, sd.ptok, u.kvh, k.row);
@@ -377,13 +390,14 @@ struct Sum {
     float4 o;
 };
 
-// The sum over a split's pieces, in order; ml(k) and acc(k) load piece k's.
-template <typename FM, typename FO>
-__device__ __forceinline__ Sum merge_pieces(int n, FM ml_of, FO acc_of) {
-    float2 ml[kMaxPieces];
-    float4 v[kMaxPieces];
+// The sum over n partials in order (a piece's slices, a split's pieces);
+// ml_of(k) and acc_of(k) load partial k.
+template <int kMax, typename FM, typename FO>
+__device__ __forceinline__ Sum merge_parts(int n, FM ml_of, FO acc_of) {
+    float2 ml[kMax];
+    float4 v[kMax];
 #pragma unroll
-    for (int k = 0; k < kMaxPieces; ++k) {
+    for (int k = 0; k < kMax; ++k) {
         ml[k] = make_float2(-INFINITY, 0.f);
         v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k < n) {
@@ -396,9 +410,9 @@ __device__ __forceinline__ Sum merge_pieces(int n, FM ml_of, FO acc_of) {
     r.l = 0.f;
     r.o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int k = 0; k < kMaxPieces; ++k) r.m = fmaxf(r.m, ml[k].x);
+    for (int k = 0; k < kMax; ++k) r.m = fmaxf(r.m, ml[k].x);
 #pragma unroll
-    for (int k = 0; k < kMaxPieces; ++k) {
+    for (int k = 0; k < kMax; ++k) {
         const float w = r.m == -INFINITY ? 0.f : ex2(ml[k].x - r.m);
         // fused explicitly: both kernels that merge round alike
         r.l = fmaf(w, ml[k].y, r.l);
@@ -442,25 +456,25 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     constexpr int S = F::slots;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = static_cast<int>(blockIdx.x) % a.pieces;  // its place in a cluster too
-    const Run u = locate(c, a, rank);
+    const Run u = locate(c, a);
     const SeqDev &sd = c.seq[u.s];
     const int ncols = sd.ncols, G = c.group, H = c.n_kv_heads;
     const int ncg = (ncols + 7) >> 3;           // column groups of 8
-    // Tiles at once (key slices), a divisor of the slots: each slot then always
-    // belongs to one slice, which takes every phase of its barrier.  (A slice
-    // that skipped a phase could not tell the tile before its own, not landed
-    // yet, from its own: both leave the barrier the same parity.)
-    int ks_n = F::teams / ncg;
-    while (S % ks_n) --ks_n;
-    const int team = warp / F::pair, dh = kFp8 ? 0 : (warp & 1);
-    const int cg = team % ncg, ks = team / ncg;
+    // Tiles at once.  A piece's tile t belongs to key slice t % ks_n, and a
+    // piece takes whole rounds of the slices (empty tiles fill its last one),
+    // so each slot always belongs to one slice, which takes every phase of its
+    // barrier.  (A slice that skipped a phase could not tell the tile before
+    // its own, not landed yet, from its own: both leave the same parity.)
+    const int ks_n = slices_of(kFp8, ncols);
+    const int round = (u.per + ks_n - 1) / ks_n * ks_n;  // a piece's tiles, empty ones among them
+    const int ntiles = a.run > 0 || u.key1 > u.key0 ? u.n_pieces * round : 0;
+    const int cg = warp % ncg, ks = warp / ncg;
     const bool active = warp < F::consumers && ks < ks_n;
 
     if (tid == 0) {
         for (int i = 0; i < S; ++i) {
             mbar_init(&x.full[i], 1);
-            mbar_init(&x.empty[i], F::pair * ncg);
+            mbar_init(&x.empty[i], ncg);
         }
         *x.abort_flag = 0;
         fence_mbar_init();
@@ -481,9 +495,9 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     if (tid == 0) pdl_trigger();
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float acc[kFp8 ? 16 : 8][4];
+    float acc[16][4];  // O^T: 16 tiles of 16 dims, this lane's two columns
 #pragma unroll
-    for (int i = 0; i < (kFp8 ? 16 : 8); ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
 
     int issued = 0;  // tiles the producer has staged
     if (warp == F::consumers) {
@@ -495,15 +509,18 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         // on the previous kernel: their tiles stream before the wait
         const int early_end = u.qbase - kFreshGuard;
         bool waited = false;
-        int yk = -1;            // lane i: map row of tile t0 + i's first K row, -1: not a run of cached rows
+        int first = -1;         // lane i: first virtual key of tile t0 + i, -1: an empty tile
+        int yk = -1;            // map row of its first K row, -1: not a run of cached rows
         int64_t sc = 0;         // e4m3: byte offset of its K scales
-        for (int t = 0; t < u.ntiles; ++t, ++issued) {
+        for (int t = 0; t < ntiles; ++t, ++issued) {
             if ((t & 31) == 0) {
                 // the next 32 tiles' rows, a tile a lane: looked up one by one
                 // they would take the warp longer than a tile takes to arrive
-                const int v0 = u.key0 + (t + lane) * kTile, p0 = pos_of(u.sp, v0);
+                const int pc = (t + lane) / round, tp = t + lane - pc * round;
+                const int v0 = u.key0 + (pc * u.per + tp) * kTile, p0 = pos_of(u.sp, v0);
+                first = tp < u.per && v0 < u.key1 ? v0 : -1;
                 yk = -1;
-                if (map != nullptr && v0 + kTile <= u.key1 &&
+                if (map != nullptr && first >= 0 && v0 + kTile <= u.key1 &&
                     (p0 >= u.sp.lo || p0 + kTile <= a.n_sink || a.n_sink >= u.sp.lo) &&
                     (a.k_new == nullptr || p0 + kTile <= u.qbase)) {
                     int row = p0;
@@ -523,6 +540,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                 }
             }
             const int slot = t % S, y = __shfl_sync(0xffffffffu, yk, t & 31);
+            const int v0 = __shfl_sync(0xffffffffu, first, t & 31);
             uint64_t *const bar = &x.full[slot];
             if (t >= S) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&x.empty[slot], ((t / S) - 1) & 1, c.status))) {
@@ -531,7 +549,11 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                 }
                 fence_proxy_async_smem();  // the slot's last reads come before the next tile's writes
             }
-            if (!waited && pos_of(u.sp, u.key0 + t * kTile) + kTile > early_end) {
+            if (v0 < 0) {
+                if (lane == 0) mbar_arrive(bar);
+                continue;
+            }
+            if (!waited && pos_of(u.sp, v0) + kTile > early_end) {
                 pdl_wait();
                 waited = true;
             }
@@ -551,9 +573,9 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                     }
                 }
             } else if constexpr (kFp8) {
-                stage8(c, a, sd, u, x, t, slot, bar, lane, pol);
+                stage8(c, a, sd, u, x, v0, slot, bar, lane, pol);
             } else {
-                stage16(c, a, sd, u, x, t, slot, bar, lane, pol);
+                stage16(c, a, sd, u, x, v0, slot, bar, lane, pol);
             }
             __syncwarp();
         }
@@ -600,13 +622,66 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         const int vr_ = (lane & 7) + 8 * (lane >> 4), vcb = (lane >> 3) & 1;
         float uo[2] = {-INFINITY, -INFINITY};  // e4m3: O's own reference (logit + V-scale exponent)
 
-        for (int t = ks; t < u.ntiles; t += ks_n) {
-            const int slot = t % S;
-            if (!__all_sync(0xffffffffu, mbar_wait(&x.full[slot], (t / S) & 1, c.status))) {
+        // A piece's sums are complete: l over the key rows, O on the logits'
+        // maximum.  They stay in registers for the cluster's merge, or go to
+        // the workspace, O [slice of the unit][column][256], then (m, l), and
+        // the next piece starts anew.
+        auto finish_piece = [&](int pc) {
+            l[0] = sum_rows(l[0]);
+            l[1] = sum_rows(l[1]);
+            if constexpr (kFp8) {
+                const float f0 = uo[0] == -INFINITY ? 0.f : ex2(uo[0] - m[0]);
+                const float f1 = uo[1] == -INFINITY ? 0.f : ex2(uo[1] - m[1]);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    acc[i][0] *= f0;
+                    acc[i][1] *= f1;
+                    acc[i][2] *= f0;
+                    acc[i][3] *= f1;
+                }
+            }
+            if (a.run == 0) return;
+            const int64_t n_part = (int64_t)sd.nsplit * a.pieces * ks_n;  // of a unit
+            const int64_t part = u.kvh * n_part + (int64_t)(u.split * a.pieces + u.piece + pc) * ks_n + ks;
+            float *o = a.ws + sd.ws_off + (part * ncols + c0) * kHeadDim;
+            float *ml = a.ws + sd.ws_off + (int64_t)H * n_part * ncols * kHeadDim + (part * ncols + c0) * 2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (c0 + e < ncols) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        if constexpr (kFp8) {
+                            *reinterpret_cast<float2 *>(o + e * kHeadDim + 32 * g + 2 * i) = make_float2(acc[i][e], acc[i][e + 2]);
+                        } else {
+                            o[e * kHeadDim + 16 * i + g] = acc[i][e];
+                            o[e * kHeadDim + 16 * i + g + 8] = acc[i][e + 2];
+                        }
+                    }
+                    if (g == 0) *reinterpret_cast<float2 *>(ml + 2 * e) = make_float2(m[e], l[e]);
+                }
+            }
+            m[0] = m[1] = uo[0] = uo[1] = -INFINITY;
+            l[0] = l[1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        };
+
+        const int n_pieces = ntiles > 0 ? u.n_pieces : 0;
+        bool ok = true;
+        for (int pc = 0; ok && pc < n_pieces; ++pc) {
+        for (int tp = ks; tp < round; tp += ks_n) {
+            const int t = pc * round + tp, slot = t % S;
+            ok = __all_sync(0xffffffffu, mbar_wait(&x.full[slot], (t / S) & 1, c.status));
+            if (!ok) {
                 *x.abort_flag = 1;
                 break;
             }
-            const int ka = pos_of(u.sp, u.key0 + t * kTile) + g, kb = ka + 8;
+            const int v0 = u.key0 + (pc * u.per + tp) * kTile;
+            if (tp >= u.per || v0 >= u.key1) {
+                if (lane == 0) mbar_arrive(&x.empty[slot]);
+                continue;
+            }
+            const int ka = pos_of(u.sp, v0) + g, kb = ka + 8;
             const bool a0 = sees(p0, ka, a.window, a.n_sink), a1 = sees(p1, ka, a.window, a.n_sink);
             const bool b0 = sees(p0, kb, a.window, a.n_sink), b1 = sees(p1, kb, a.window, a.n_sink);
             float sx[4];
@@ -630,15 +705,20 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                 sx[2] = b0 ? sacc[2] * skb : -INFINITY;
                 sx[3] = b1 ? sacc[3] * skb : -INFINITY;
             } else {
+                // two accumulator chains, four K fragments loaded before their MMAs
                 const uint32_t kbs = s_base + slot * F::stage;
                 float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int kk = 0; kk < 16; kk += 2) {
-                    uint32_t x0, x1, x2, x3;
-                    ldsm_x4(kbs + swz(kr_, 2 * kk + kcb), x0, x1, x2, x3);
-                    mma_bf16(sa, x0, x1, x2, x3, qf[kk][0], qf[kk][1]);
-                    ldsm_x4(kbs + swz(kr_, 2 * (kk + 1) + kcb), x0, x1, x2, x3);
-                    mma_bf16(sb, x0, x1, x2, x3, qf[kk + 1][0], qf[kk + 1][1]);
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t f[4][4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ldsm_x4(kbs + h * kPlane + swz(kr_, 2 * j + kcb), f[j][0], f[j][1], f[j][2], f[j][3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t(&x4)[4] = f[j];
+                        mma_bf16((j & 1) ? sb : sa, x4[0], x4[1], x4[2], x4[3], qf[4 * h + j][0], qf[4 * h + j][1]);
+                    }
                 }
                 sx[0] = a0 ? (sa[0] + sb[0]) * kScaleLog2 : -INFINITY;
                 sx[1] = a1 ? (sa[1] + sb[1]) * kScaleLog2 : -INFINITY;
@@ -692,12 +772,17 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                     w[i][6] = z1.z;
                     w[i][7] = z1.w;
                 }
+                if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {  // some reference grew
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        acc[i][0] *= be0;
+                        acc[i][1] *= be1;
+                        acc[i][2] *= be0;
+                        acc[i][3] *= be1;
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    acc[i][0] *= be0;
-                    acc[i][1] *= be1;
-                    acc[i][2] *= be0;
-                    acc[i][3] *= be1;
                     const int wi = i >> 1, b = 2 * (i & 1);
                     const uint32_t sel0 = b | ((4 + b) << 4), sel1 = (b + 1) | ((5 + b) << 4);
                     const uint32_t z0 = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel0));
@@ -708,6 +793,15 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                     mma_half(acc[i], z0, z1, z2, z3, b0l, b1l);
                 }
             } else {
+                if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {  // some maximum grew
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        acc[i][0] *= al0;
+                        acc[i][1] *= al1;
+                        acc[i][2] *= al0;
+                        acc[i][3] *= al1;
+                    }
+                }
                 // P as a bf16 pair hi + lo (lo = p - hi exactly): about 16
                 // significant bits of the weights reach the float32 accumulator
                 const uint32_t h01 = pack_bf16(e0, e1), h23 = pack_bf16(e2, e3);
@@ -717,33 +811,27 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                 const uint32_t pc0 = movmatrix_t(l01), pc1 = movmatrix_t(l23);
                 const uint32_t vbs = s_base + slot * F::stage + F::half;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    acc[i][0] *= al0;
-                    acc[i][1] *= al1;
-                    acc[i][2] *= al0;
-                    acc[i][3] *= al1;
-                    uint32_t y0, y1, y2, y3;
-                    ldsm_x4_t(vbs + swz(vr_, 2 * (8 * dh + i) + vcb), y0, y1, y2, y3);
-                    mma_bf16(acc[i], y0, y1, y2, y3, pb0, pb1);
-                    mma_bf16(acc[i], y0, y1, y2, y3, pc0, pc1);
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t f[4][4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        ldsm_x4_t(vbs + h * kPlane + swz(vr_, 2 * j + vcb), f[j][0], f[j][1], f[j][2], f[j][3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t(&x4)[4] = f[j];
+                        mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], pb0, pb1);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t(&x4)[4] = f[j];
+                        mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], pc0, pc1);
+                    }
                 }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&x.empty[slot]);
         }
-        l[0] = sum_rows(l[0]);
-        l[1] = sum_rows(l[1]);
-        if constexpr (kFp8) {
-            // O from its own reference back to the logits' maximum
-            const float f0 = uo[0] == -INFINITY ? 0.f : ex2(uo[0] - m[0]);
-            const float f1 = uo[1] == -INFINITY ? 0.f : ex2(uo[1] - m[1]);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                acc[i][0] *= f0;
-                acc[i][1] *= f1;
-                acc[i][2] *= f0;
-                acc[i][3] *= f1;
-            }
+        finish_piece(pc);
         }
     }
     __syncthreads();  // every staged tile is consumed (or the CTA gave up)
@@ -751,6 +839,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     // after a wait that ran out, every copy issued lands before the memory goes
     if (failed)
         for (int j = max(0, issued - S); j < issued; ++j) mbar_wait(&x.full[j % S], (j / S) & 1, nullptr);
+    if (a.run > 0) return;  // window_combine merges the slices and pieces
 
     // ---- merge the CTA's key slices, in order ----
     const int NC = ncg * 8;
@@ -772,15 +861,15 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int d = (8 * dh + i) * 16 + g;
+            for (int i = 0; i < 16; ++i) {
+                const int d = 16 * i + g;
                 b0[d] = acc[i][0];
                 b1[d] = acc[i][1];
                 b0[d + 8] = acc[i][2];
                 b1[d + 8] = acc[i][3];
             }
         }
-        if (dh == 0 && g == 0) {
+        if (g == 0) {
             float *ml = mlb + (ks * NC + c0) * 2;
             ml[0] = m[0];
             ml[1] = l[0];
@@ -792,40 +881,21 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     for (int idx = tid; idx < ncols * (kHeadDim / 4); idx += F::threads) {
         const int col = idx / (kHeadDim / 4), d = 4 * (idx - col * (kHeadDim / 4));
         const int ds = kFp8 ? d + (d >> 5) : d;
-        float M = -INFINITY;
-        for (int k = 0; k < ks_n; ++k) M = fmaxf(M, mlb[(k * NC + col) * 2]);
-        float L = 0.f;
-        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < ks_n; ++k) {
-            const float w = M == -INFINITY ? 0.f : ex2(mlb[(k * NC + col) * 2] - M);
-            const float *v = mbuf + (k * NC + col) * F::row + ds;
-            L += w * mlb[(k * NC + col) * 2 + 1];
-            O.x += w * v[0];
-            O.y += w * v[1];
-            O.z += w * v[2];
-            O.w += w * v[3];
-        }
-        *reinterpret_cast<float4 *>(sum + col * kHeadDim + d) = O;
-        if (d == 0) *reinterpret_cast<float2 *>(sum_ml + 2 * col) = make_float2(M, L);
+        const Sum r = merge_parts<kMaxSlices>(
+            ks_n, [&](int k) { return *reinterpret_cast<const float2 *>(mlb + (k * NC + col) * 2); },
+            [&](int k) {
+                const float *v = mbuf + (k * NC + col) * F::row + ds;
+                return make_float4(v[0], v[1], v[2], v[3]);
+            });
+        *reinterpret_cast<float4 *>(sum + col * kHeadDim + d) = r.o;
+        if (d == 0) *reinterpret_cast<float2 *>(sum_ml + 2 * col) = make_float2(r.m, r.l);
     }
-    // ---- then the split's CTAs, in order: in a cluster here, else window_combine ----
-    if (!a.clustered && a.pieces > 1) {
-        __syncthreads();
-        if (failed) return;
-        // partials of a piece: O [column][256], then (m, l) [column]
-        const int64_t piece = ((int64_t)u.kvh * sd.nsplit + u.split) * a.pieces + rank;
-        float *acc_out = a.ws + sd.ws_off + piece * ncols * kHeadDim;
-        float *ml_out = a.ws + sd.ws_off + ((int64_t)H * sd.nsplit * a.pieces * kHeadDim + piece * 2) * ncols;
-        for (int idx = tid; idx < ncols * (kHeadDim / 4); idx += F::threads)
-            reinterpret_cast<float4 *>(acc_out)[idx] = reinterpret_cast<const float4 *>(sum)[idx];
-        for (int idx = tid; idx < 2 * ncols; idx += F::threads) ml_out[idx] = sum_ml[idx];
-        return;
-    }
+    // ---- then the cluster's CTAs, in order ----
     cluster_sync();
     if (!failed) {
-        for (int idx = rank * F::threads + tid; idx < ncols * (kHeadDim / 4); idx += a.pieces * F::threads) {
+        for (int idx = u.piece * F::threads + tid; idx < ncols * (kHeadDim / 4); idx += a.pieces * F::threads) {
             const int col = idx / (kHeadDim / 4), d = 4 * (idx - col * (kHeadDim / 4));
-            const Sum r = merge_pieces(
+            const Sum r = merge_parts<kMaxPieces>(
                 a.pieces, [&](int k) { return peer_ld2(peer_addr(sum_ml + 2 * col, k)); },
                 [&](int k) { return peer_ld4(peer_addr(sum + col * kHeadDim + d, k)); });
             const int j = col / G;
@@ -835,9 +905,9 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     cluster_sync();  // the peers have read this CTA's sums
 }
 
-// Merge of the pieces' partials for calls whose CTAs are not clustered: 64
-// threads a query column, four dims each, the pieces of a split in order as a
-// cluster merges them, then the splits in order.
+// Merge of the slices' partials for calls whose CTAs are not clustered: 64
+// threads a query column, four dims each; a piece's slices, the split's pieces
+// and the splits in order, as a clustered CTA and its cluster merge them.
 constexpr int kCombThreads = 256;
 __global__ void __launch_bounds__(kCombThreads)
     window_combine(const __grid_constant__ Common c, const __grid_constant__ WinArgs a, int32_t total) {
@@ -847,18 +917,27 @@ __global__ void __launch_bounds__(kCombThreads)
     const int s = find_seq(c.n_seqs, i, [&](int t) { return c.seq[t].comb_off; });
     const SeqDev &sd = c.seq[s];
     const int r = i - sd.comb_off, ncols = sd.ncols, unit = r / ncols, col = r - unit * ncols, G = c.group;
-    const int d = 4 * (threadIdx.x & 63), j = col / G;
-    const int64_t p0 = (int64_t)unit * sd.nsplit * a.pieces;
-    const float *acc = a.ws + sd.ws_off + (p0 * ncols + col) * kHeadDim + d;
-    const float *ml = a.ws + sd.ws_off + (int64_t)c.n_kv_heads * sd.nsplit * a.pieces * ncols * kHeadDim + (p0 * ncols + col) * 2;
+    const int d = 4 * (threadIdx.x & 63), j = col / G, ks_n = slices_of(c.kv_fp8 != 0, ncols);
+    const int64_t n_part = (int64_t)sd.nsplit * a.pieces * ks_n;
+    const float *acc = a.ws + sd.ws_off + (unit * n_part * ncols + col) * kHeadDim + d;
+    const float *ml = a.ws + sd.ws_off + (int64_t)c.n_kv_heads * n_part * ncols * kHeadDim + (unit * n_part * ncols + col) * 2;
     uint16_t *out = a.out + (((int64_t)sd.tok_off + j) * c.n_q_heads + unit * G + (col - j * G)) * kHeadDim + d;
     asm volatile("" ::"l"(acc), "l"(ml), "l"(out));
     pdl_wait();
     Sum t;
     for (int sp = 0; sp < sd.nsplit; ++sp) {
-        const Sum x = merge_pieces(
-            a.pieces, [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(ml + (int64_t)(sp * a.pieces + k) * ncols * 2)); },
-            [&](int k) { return __ldcg(reinterpret_cast<const float4 *>(acc + (int64_t)(sp * a.pieces + k) * ncols * kHeadDim)); });
+        Sum pieces[kMaxPieces];
+#pragma unroll
+        for (int p = 0; p < kMaxPieces; ++p) {
+            if (p < a.pieces) {
+                const int64_t p0 = (int64_t)(sp * a.pieces + p) * ks_n;
+                pieces[p] = merge_parts<kMaxSlices>(
+                    ks_n, [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(ml + (p0 + k) * ncols * 2)); },
+                    [&](int k) { return __ldcg(reinterpret_cast<const float4 *>(acc + (p0 + k) * ncols * kHeadDim)); });
+            }
+        }
+        const Sum x = merge_parts<kMaxPieces>(
+            a.pieces, [&](int p) { return make_float2(pieces[p].m, pieces[p].l); }, [&](int p) { return pieces[p].o; });
         if (sp == 0) {
             t = x;
         } else {
@@ -877,8 +956,8 @@ __global__ void __launch_bounds__(kCombThreads)
 
 }  // namespace
 
-// CTAs that share a split, by the window alone (a stream's bits must not
-// depend on its batch): eight tiles a CTA before another one joins.
+// Pieces of a split, by the window alone (a stream's bits must not depend on
+// its batch): eight tiles a piece before there is another.
 int window_pieces(int32_t window, int32_t n_sink) {
     const int64_t tiles = ((int64_t)window + n_sink) / kTile + 2;
     int n = 1;
@@ -886,7 +965,7 @@ int window_pieces(int32_t window, int32_t n_sink) {
     return n;
 }
 
-// Splits only where a CTA's run would pass kSplitTiles tiles.
+// Splits only where a piece would pass kSplitTiles tiles.
 int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
     int64_t items = 0, cols = 0, floats = 0;
     const int pieces = window_pieces(window, n_sink);
@@ -909,7 +988,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
         split |= d.nsplit > 1;
         items += (int64_t)c.n_kv_heads * d.nsplit;
         cols += (int64_t)c.n_kv_heads * d.ncols;
-        floats += (int64_t)c.n_kv_heads * d.nsplit * pieces * d.ncols * (kHeadDim + 2);
+        floats += (int64_t)c.n_kv_heads * d.nsplit * pieces * slices_of(c.kv_fp8 != 0, d.ncols) * d.ncols * (kHeadDim + 2);
         floats = (floats + 63) / 64 * 64;
     }
     if (items * pieces > INT32_MAX) return PKV_EINVAL;
@@ -941,9 +1020,12 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
         }) != PKV_OK)
         return PKV_ECUDA;
     WinArgs a{q, out, ws, k_new, v_new, ik_new, window, n_sink, window_pieces(window, n_sink), 0};
-    a.clustered = plan.total_comb == 0;
+    const bool clustered = plan.total_comb == 0;
+    // one wave of CTAs where the pieces allow it
+    if (!clustered)
+        for (a.run = 1; a.run < a.pieces && (int64_t)plan.total_items * a.pieces / a.run > kClusterCtas;) a.run *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.total_items) * a.pieces);
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.total_items) * (a.pieces / std::max(1, a.run)));
     cfg.blockDim = dim3(c.kv_fp8 ? Cfg<true>::threads : Cfg<false>::threads);
     cfg.dynamicSmemBytes = c.kv_fp8 ? Cfg<true>::smem : Cfg<false>::smem;
     cfg.stream = stream;
@@ -951,13 +1033,13 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = a.clustered ? a.pieces : 1;
+    attr[1].val.clusterDim.x = clustered ? a.pieces : 1;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, c.kv_fp8 ? window_partial<true> : window_partial<false>, c, maps, a) != cudaSuccess)
         return PKV_ECUDA;
-    if (a.clustered) return PKV_OK;
+    if (clustered) return PKV_OK;
     const int per = kCombThreads / 64;
     return launch_status(launch_pdl(window_combine, static_cast<unsigned>((plan.total_comb + per - 1) / per),
                                     kCombThreads, 0, stream, c, a, plan.total_comb));
