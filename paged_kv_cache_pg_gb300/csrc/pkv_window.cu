@@ -687,23 +687,38 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             float sx[4];
             if constexpr (kFp8) {
                 const uint8_t *st = x.stages + slot * F::stage;
-                float sacc[4] = {0.f, 0.f, 0.f, 0.f};
+                // two accumulator chains, the whole K fragment loaded before its MMAs
+                float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+                uint4 w0[4], w1[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint4 w0 = *reinterpret_cast<const uint4 *>(st + swz(g, 4 * c4 + i));
-                    const uint4 w1 = *reinterpret_cast<const uint4 *>(st + swz(g + 8, 4 * c4 + i));
-                    const uint32_t y0[4] = {w0.x, w0.y, w0.z, w0.w}, y1[4] = {w1.x, w1.y, w1.z, w1.w};
+                    w0[i] = *reinterpret_cast<const uint4 *>(st + swz(g, 4 * c4 + i));
+                    w1[i] = *reinterpret_cast<const uint4 *>(st + swz(g + 8, 4 * c4 + i));
+                }
+                // a step's codes widen while the step before is multiplied
+                uint32_t fr[3][4];
+                auto widen = [&](int st_) {
+                    const uint4 q0 = w0[st_ >> 2], q1 = w1[st_ >> 2];
+                    const uint32_t e0 = (st_ & 3) == 0 ? q0.x : (st_ & 3) == 1 ? q0.y : (st_ & 3) == 2 ? q0.z : q0.w;
+                    const uint32_t e1 = (st_ & 3) == 0 ? q1.x : (st_ & 3) == 1 ? q1.y : (st_ & 3) == 2 ? q1.z : q1.w;
+                    uint32_t(&o)[4] = fr[st_ % 3];
+                    o[0] = f16_of_codes(e0);
+                    o[1] = f16_of_codes(e1);
+                    o[2] = f16_of_codes(e0 >> 16);
+                    o[3] = f16_of_codes(e1 >> 16);
+                };
+                widen(0);
+                widen(1);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_half(sacc, f16_of_codes(y0[j] & 0xffffu), f16_of_codes(y1[j] & 0xffffu),
-                                 f16_of_codes(y0[j] >> 16), f16_of_codes(y1[j] >> 16), qf[4 * i + j][0],
-                                 qf[4 * i + j][1]);
+                for (int j = 0; j < 16; ++j) {
+                    if (j < 14) widen(j + 2);
+                    mma_half((j & 1) ? sb : sa, fr[j % 3][0], fr[j % 3][1], fr[j % 3][2], fr[j % 3][3], qf[j][0], qf[j][1]);
                 }
                 const float ska = x.scl[slot * 32 + g] * kScaleLog2, skb = x.scl[slot * 32 + g + 8] * kScaleLog2;
-                sx[0] = a0 ? sacc[0] * ska : -INFINITY;
-                sx[1] = a1 ? sacc[1] * ska : -INFINITY;
-                sx[2] = b0 ? sacc[2] * skb : -INFINITY;
-                sx[3] = b1 ? sacc[3] * skb : -INFINITY;
+                sx[0] = a0 ? (sa[0] + sb[0]) * ska : -INFINITY;
+                sx[1] = a1 ? (sa[1] + sb[1]) * ska : -INFINITY;
+                sx[2] = b0 ? (sa[2] + sb[2]) * skb : -INFINITY;
+                sx[3] = b1 ? (sa[3] + sb[3]) * skb : -INFINITY;
             } else {
                 // two accumulator chains, four K fragments loaded before their MMAs
                 const uint32_t kbs = s_base + slot * F::stage;
@@ -781,16 +796,23 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                         acc[i][3] *= be1;
                     }
                 }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
+                uint32_t z[3][4];
+                auto widen_v = [&](int i) {  // keys' codes of dims 32g + 2i and + 1, paired
                     const int wi = i >> 1, b = 2 * (i & 1);
                     const uint32_t sel0 = b | ((4 + b) << 4), sel1 = (b + 1) | ((5 + b) << 4);
-                    const uint32_t z0 = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel0));
-                    const uint32_t z1 = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel1));
-                    const uint32_t z2 = f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel0));
-                    const uint32_t z3 = f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel1));
-                    mma_half(acc[i], z0, z1, z2, z3, b0h, b1h);
-                    mma_half(acc[i], z0, z1, z2, z3, b0l, b1l);
+                    uint32_t(&o)[4] = z[i % 3];
+                    o[0] = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel0));
+                    o[1] = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel1));
+                    o[2] = f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel0));
+                    o[3] = f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel1));
+                };
+                widen_v(0);
+                widen_v(1);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    if (i < 14) widen_v(i + 2);
+                    mma_half(acc[i], z[i % 3][0], z[i % 3][1], z[i % 3][2], z[i % 3][3], b0h, b1h);
+                    mma_half(acc[i], z[i % 3][0], z[i % 3][1], z[i % 3][2], z[i % 3][3], b0l, b1l);
                 }
             } else {
                 if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {  // some maximum grew
