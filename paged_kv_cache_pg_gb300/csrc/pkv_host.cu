@@ -133,7 +133,7 @@ std::vector<std::pair<MapKey, RowMap>> g_maps;  // encoded maps, most recent las
 int row_map(DecodeMaps &maps, int &n_maps, const void *base, uint64_t rows, bool bytes8,
             bool tile, int box_rows, int box_chunks) {
     if (rows == 0 || rows > (1ull << 31) || !aligned16(base)) return -1;
-    if (tile ? (bytes8 ? (box_rows != 16 || box_chunks != 2)
+    if (tile ? (bytes8 ? ((box_rows != 16 && box_rows != 32) || box_chunks != 2)
                        : ((box_rows != 16 && box_rows != 64 && box_rows != 128) || (box_chunks != 2 && box_chunks != 4)))
              : (box_rows != 16 || box_chunks != 1))
         return -1;
@@ -157,16 +157,26 @@ int row_map(DecodeMaps &maps, int &n_maps, const void *base, uint64_t rows, bool
         // 256 bytes, boxes of 128 x 16 (both 128-byte inner boxes).  The tile
         // view: dims {64, rows, 4 column chunks}, strides 512 B (a row) and
         // 128 B (a chunk), boxes of {64, box_rows, box_chunks}; of code rows
-        // {128, rows, 2 halves}, strides 256 B and 128 B.
+        // {128, 2 halves, rows}, strides 128 B and 256 B, boxes of whole rows.
         cuuint64_t dims[3] = {256, rows, 1};
         cuuint64_t strides[2] = {bytes8 ? 256u : 512u, 0};
         cuuint32_t box[3] = {bytes8 ? 128u : 64u, 16, 1};
         if (tile) {
-            dims[0] = bytes8 ? 128 : 64;
-            dims[2] = bytes8 ? 2 : 4;
-            strides[1] = 128;
-            box[1] = static_cast<cuuint32_t>(box_rows);
-            box[2] = static_cast<cuuint32_t>(box_chunks);
+            if (bytes8) {
+                dims[0] = 128;
+                dims[1] = 2;
+                dims[2] = rows;
+                strides[0] = 128;
+                strides[1] = 256;
+                box[1] = static_cast<cuuint32_t>(box_chunks);
+                box[2] = static_cast<cuuint32_t>(box_rows);
+            } else {
+                dims[0] = 64;
+                dims[2] = 4;
+                strides[1] = 128;
+                box[1] = static_cast<cuuint32_t>(box_rows);
+                box[2] = static_cast<cuuint32_t>(box_chunks);
+            }
         }
         cuuint32_t estr[3] = {1, 1, 1};
         CUresult r = fn(reinterpret_cast<CUtensorMap *>(m.bytes),
@@ -235,11 +245,11 @@ void plan_window_maps(Common &c, const pkv_layout *L, const pkv_seq *seqs, Decod
         d.tma_k = d.tma_v = -1;
         const pkv_pg &pg = seqs[s].pg;
         const int64_t layer_off = (int64_t)c.layer * layer_elems_f(fp8, L->n_kv_heads, L->idx_dim, pg.page_pos);
-        // a 16-key tile of whole rows in one page, every page and this layer's
-        // block starting on a row
+        // runs of 16 (or 32) whole rows in one page, every page and this
+        // layer's block starting on a row
         if (d.ncols == 0 || pg.page_pos % 16 != 0 || pg.page_elems % row != 0 || layer_off % row != 0) continue;
         const uint64_t rows = (uint64_t)(pg.table ? pg.n_pages : 1) * pg.page_elems / row;
-        d.tma = row_map(maps, n_maps, pg.base, rows, fp8, true, 16, fp8 ? 2 : 4);
+        d.tma = row_map(maps, n_maps, pg.base, rows, fp8, true, fp8 && window_wide(d) ? 32 : 16, fp8 ? 2 : 4);
         d.layer_row = layer_off / row;
     }
 }

@@ -235,7 +235,10 @@ int launch_decode8(const Common &c, const DecodePlan &plan, const DecodeMaps &ma
 // Windowed decode (pkv_window.cu): CTAs that share a split, plan and launch.
 int window_pieces(int32_t window, int32_t n_sink);
 int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan);
-// Row maps of the streams (in tma): 3D boxes of 16 whole rows, bf16 or codes.
+// Row maps of the streams (in tma): 3D boxes of 16 whole bf16 rows, or of 32
+// code rows where a page holds every run of 32 positions from a multiple of 32
+// (16 else).
+__host__ __device__ inline bool window_wide(const SeqDev &d) { return d.table == nullptr || d.ptok % 32 == 0; }
 void plan_window_maps(Common &c, const pkv_layout *layout, const pkv_seq *seqs, DecodeMaps &maps);
 int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &maps, int32_t window,
                   int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,

@@ -30,12 +30,11 @@
 namespace pkv {
 namespace {
 
-constexpr int kTile = 16;                    // keys a stage
 constexpr int kMaxCols = 32;                 // query columns of one unit
 constexpr int kMaxPieces = 8;           // pieces of a split
 constexpr int kMaxSlices = 4;           // key slices of a CTA
-constexpr int kSplitTiles = 40;              // tiles of a CTA's run at most
-constexpr int kMaxPages = kMaxPieces * kSplitTiles * kTile / 4 + 4;  // pages a CTA's run can touch
+constexpr int kSplitKeys = 640;              // keys of a piece at most
+constexpr int kMaxPages = kMaxPieces * kSplitKeys / 4 + 4;  // pages a CTA's run can touch
 // CTAs of a call up to which a split's CTAs are clustered (two fill an SM).
 // Past it a cluster waits for eight free places on neighbouring SMs while
 // other places stand empty: 64 streams of 4,096-key windows took 116 us
@@ -49,9 +48,6 @@ constexpr int kFreshGuard = 32;              // see decode_partial: rows a kerne
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
 
 constexpr int kPlane = 2048;                 // bf16: one 64-dim chunk of 16 rows
-constexpr int kCfgHalf16 = 4 * kPlane;       // bf16: 16 rows of K (or V)
-constexpr int kHalf8 = kTile * 128;          // e4m3: one 128-byte half of 16 code rows
-constexpr int kCfgHalf8 = 2 * kHalf8;
 
 // Shapes of the two page formats' CTAs: four consumer warps, each on a tile (and
 // column group) of its own with O over all dims in registers.  (Eight, a pair
@@ -60,14 +56,16 @@ constexpr int kCfgHalf8 = 2 * kHalf8;
 constexpr int kConsumers = 4;
 template <bool kFp8>
 struct Cfg {
-    static constexpr int half = kFp8 ? kCfgHalf8 : kCfgHalf16;   // K or V bytes of a stage
+    static constexpr int tile = kFp8 ? 32 : 16;                  // keys a stage
+    static constexpr int half = 8192;                            // K or V bytes of a stage
     static constexpr int stage = 2 * half;
-    static constexpr int slots = kFp8 ? 12 : 6;
+    static constexpr int slots = 6;
+    static_assert(half == tile * kHeadDim * (kFp8 ? 1 : 2), "whole rows");
     static constexpr int consumers = kConsumers;
     static constexpr int threads = consumers * 32 + 32;
     static constexpr int row = kFp8 ? kHeadDim + 12 : kHeadDim + 4;  // floats of a merge row
-    static constexpr int off_scl = slots * stage;                // e4m3: 16 K and 16 V scales a stage
-    static constexpr int off_page = off_scl + (kFp8 ? slots * 128 : 0);
+    static constexpr int off_scl = slots * stage;                // e4m3: 32 K and 32 V scales a stage
+    static constexpr int off_page = off_scl + (kFp8 ? slots * 256 : 0);
     static constexpr int off_bar = off_page + kMaxPages * 8;
     static constexpr int bytes = off_bar + 2 * slots * 8 + 16;
     static constexpr int smem = bytes + 1024;                    // with alignment slack
@@ -89,6 +87,7 @@ struct WinArgs {
     int32_t window, n_sink;
     int32_t pieces;     // pieces of a split
     int32_t run;        // pieces of a CTA; 0: one, and the split's CTAs are a cluster
+    int32_t even;       // splits of each stream where all have as many, else 0
 };
 
 // Key slices of a CTA (tiles it works on at once): a divisor of its slots.
@@ -140,22 +139,29 @@ __device__ __forceinline__ float sum_rows(float v) {
     return v + __shfl_xor_sync(0xffffffffu, v, 16);
 }
 
-// Byte offset of 16-byte chunk c of row r inside a staged K or V tile: planes
-// of 16 rows x 128 B with the TMA's 128-byte swizzle (bf16: four planes of 64
-// dims, e4m3: two of 128).
+// Byte offset of 16-byte chunk c of row r inside a staged K or V tile, with the
+// TMA's 128-byte swizzle.  bf16: four planes of 64 dims, each 16 rows x 128 B.
 __device__ __forceinline__ uint32_t swz(int r, int c) {
-    return (c >> 3) * 2048 + r * 128 + ((((c & 7) ^ (r & 7))) << 4);
+    return (c >> 3) * kPlane + r * 128 + ((((c & 7) ^ (r & 7))) << 4);
+}
+// e4m3: whole rows of 256 B, each two lines of 128 B.
+__device__ __forceinline__ uint32_t swz8(int r, int c) {
+    const int line = 2 * r + (c >> 3);
+    return line * 128 + ((((c & 7) ^ (line & 7))) << 4);
 }
 
-// Two e4m3 codes (low byte first) to an f16 pair, exactly.
-__device__ __forceinline__ uint32_t f16_of_codes(uint32_t two) {
-    uint32_t r;
-    asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, t;\n\t}" : "=r"(r) : "r"(two));
-    return r;
+// Four e4m3 codes (low byte first) to two f16 pairs, exactly.
+__device__ __forceinline__ void f16_of_codes(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
+// D (16x8 f32) += A (16x16 f16, row) B (16x8 f16, col).  Not volatile: it only
+// reads its registers, and the compiler may place it among the conversions.
 __device__ __forceinline__ void mma_half(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -185,13 +191,15 @@ struct Run {
     int sink_page, win_page, n_sink_pages, n_pages;  // the page list: sinks' pages, then the window's
 };
 
+template <int kTile>
 __device__ __forceinline__ Run locate(const Common &c, const WinArgs &a) {
     Run u;
     u.n_pieces = max(1, a.run);
     const int per_split = a.pieces / u.n_pieces, b = static_cast<int>(blockIdx.x), item = b / per_split;
-    u.s = find_seq(c.n_seqs, item, [&](int t) { return c.seq[t].work_off; });
+    // (a search through the streams' offsets costs a CTA of a full launch 1.5 us)
+    u.s = a.even ? item / a.even : find_seq(c.n_seqs, item, [&](int t) { return c.seq[t].work_off; });
     const SeqDev &sd = c.seq[u.s];
-    const int r = item - sd.work_off;
+    const int r = a.even ? item - u.s * a.even : item - sd.work_off;
     u.kvh = r / sd.nsplit;
     u.split = r - u.kvh * sd.nsplit;
     u.piece = (b - item * per_split) * u.n_pieces;
@@ -227,13 +235,13 @@ __device__ __forceinline__ int pos_of(const WindowSpan &sp, int v) {
 
 struct Ctx {
     uint8_t *stages;
-    float *scl;          // e4m3: [slot][32] K then V scales
+    float *scl;          // e4m3: [slot][2][32] K then V scales
     int64_t *pages;      // offsets of the run's pages (-1: outside the arena)
     uint64_t *full, *empty;
     volatile int *abort_flag;
 };
 
-// Where one staged key's rows come from (per lane; lanes 16.. repeat 0..15).
+// Where one staged key's rows come from (per lane; bf16: lanes 16.. repeat 0..15).
 struct KeySrc {
     int pos;          // the position read
     int row;          // its row inside the page
@@ -243,10 +251,11 @@ struct KeySrc {
     bool bad;         // its page id was outside the arena
 };
 
+template <int kTile>
 __device__ __forceinline__ KeySrc key_src(const SeqDev &sd, const WinArgs &a, const Run &u, const Ctx &x,
                                           int v0, int lane) {
     KeySrc k;
-    const int v = v0 + (lane & 15);
+    const int v = v0 + (lane & (kTile - 1));
     const int p = pos_of(u.sp, v);
     k.seen = v < u.key1 && (p < a.n_sink || p >= u.sp.lo);
     // the last position of the run, the last sink, or the window's first position
@@ -274,7 +283,7 @@ __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const
                                         const Ctx &x, int v0, int slot, uint64_t *bar, int lane, uint64_t pol) {
     const int H = c.n_kv_heads;
     const int64_t v_gap = (int64_t)H * sd.ptok * kHeadDim;  // V row - K row
-    const KeySrc k = key_src(sd, a, u, x, v0, lane);
+    const KeySrc k = key_src<16>(sd, a, u, x, v0, lane);
     const int64_t krow = k.page + off_k(sd.ptok, u.kvh, k.row);
     uint8_t *kst = x.stages + slot * Cfg<false>::stage, *vst = kst + Cfg<false>::half;
     const uint16_t *ksrc, *vsrc;
@@ -288,7 +297,7 @@ __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const
     }
     const int64_t kp = reinterpret_cast<int64_t>(ksrc), vp = reinterpret_cast<int64_t>(vsrc);
 #pragma unroll 4
-    for (int r = 0; r < kTile; ++r) {
+    for (int r = 0; r < 16; ++r) {
         const uint16_t *kr = reinterpret_cast<const uint16_t *>(shfl64(kp, r));
         const uint16_t *vr = reinterpret_cast<const uint16_t *>(shfl64(vp, r));
         cp_async16(kst + swz(r, lane), kr + lane * 8, pol);
@@ -297,7 +306,7 @@ __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const
     cp_async_mbar_arrive(bar);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    unsigned todo = __ballot_sync(0xffffffffu, k.fresh && k.seen && !k.bad && lane < kTile);
+    unsigned todo = __ballot_sync(0xffffffffu, k.fresh && k.seen && !k.bad && lane < 16);
     while (todo) {
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
@@ -318,32 +327,35 @@ __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const
     }
 }
 
-// The same for e4m3 pages: 16 code rows of K and V and their scales.  New rows
+// The same for e4m3 pages: 32 code rows of K and V and their scales.  New rows
 // are quantized here (the rule of pkv_store) into the stage and the cache.
 __device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const SeqDev &sd, const Run &u,
                                        const Ctx &x, int v0, int slot, uint64_t *bar, int lane, uint64_t pol) {
     const int H = c.n_kv_heads;
-    const KeySrc k = key_src(sd, a, u, x, v0, lane);
+    const KeySrc k = key_src<32>(sd, a, u, x, v0, lane);
     const uint8_t *base = reinterpret_cast<const uint8_t *>(sd.layer_base);
     const int64_t pg = 2 * k.page;
     const int64_t kc = pg + off8_code(false, H, sd.ptok, u.kvh, k.row);
     const int64_t vc = pg + off8_code(true, H, sd.ptok, u.kvh, k.row);
     uint8_t *st = x.stages + slot * Cfg<true>::stage;
-    uint8_t *sc = reinterpret_cast<uint8_t *>(x.scl) + slot * 128;
+    uint8_t *sc = reinterpret_cast<uint8_t *>(x.scl) + slot * 256;
     constexpr int kCodes = Cfg<true>::half;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
         const int item = lane + 32 * i, rr = item >> 4, ch = item & 15;
         const int64_t krr = shfl64(kc, rr), vrr = shfl64(vc, rr);
         if (!__shfl_sync(0xffffffffu, k.fresh, rr)) {
-            cp_async16(st + swz(rr, ch), base + krr + 16 * ch, pol);
-            cp_async16(st + kCodes + swz(rr, ch), base + vrr + 16 * ch, pol);
+            cp_async16(st + swz8(rr, ch), base + krr + 16 * ch, pol);
+            cp_async16(st + kCodes + swz8(rr, ch), base + vrr + 16 * ch, pol);
         }
     }
-    if (!k.fresh) cp_async4(sc + 4 * lane, base + pg + off8_scale(lane >= 16, H, sd.ptok, u.kvh, k.row));
+    if (!k.fresh) {
+        cp_async4(sc + 4 * lane, base + pg + off8_scale(false, H, sd.ptok, u.kvh, k.row));
+        cp_async4(sc + 128 + 4 * lane, base + pg + off8_scale(true, H, sd.ptok, u.kvh, k.row));
+    }
     // rows whose source is a new token: quantized by the whole warp, one at a
     // time; one that no query sees only needs finite codes
-    unsigned todo = __ballot_sync(0xffffffffu, k.fresh && lane < kTile);
+    unsigned todo = __ballot_sync(0xffffffffu, k.fresh);
     while (todo) {
         const int rr = __ffs(todo) - 1;
         todo &= todo - 1;
@@ -351,8 +363,8 @@ __device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const 
         if (!seen) {
 #pragma unroll
             for (int v = 0; v < 2; ++v)
-                *reinterpret_cast<uint2 *>(st + v * kCodes + swz(rr, lane >> 1) + (lane & 1) * 8) = make_uint2(0u, 0u);
-            if (lane < 2) reinterpret_cast<float *>(sc)[16 * lane + rr] = 0.f;
+                *reinterpret_cast<uint2 *>(st + v * kCodes + swz8(rr, lane >> 1) + (lane & 1) * 8) = make_uint2(0u, 0u);
+            if (lane < 2) reinterpret_cast<float *>(sc)[32 * lane + rr] = 0.f;
             continue;
         }
         const int p = __shfl_sync(0xffffffffu, k.pos, rr), row = __shfl_sync(0xffffffffu, k.row, rr);
@@ -369,8 +381,8 @@ __device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const 
         for (int v = 0; v < 2; ++v) {
             uint2 codes;
             const float scale = quantize_row8(v ? in_v : in_k, &codes);
-            *reinterpret_cast<uint2 *>(st + v * kCodes + swz(rr, lane >> 1) + (lane & 1) * 8) = codes;
-            if (lane == 0) reinterpret_cast<float *>(sc)[16 * v + rr] = scale;
+            *reinterpret_cast<uint2 *>(st + v * kCodes + swz8(rr, lane >> 1) + (lane & 1) * 8) = codes;
+            if (lane == 0) reinterpret_cast<float *>(sc)[32 * v + rr] = scale;
             if (write) {
                 *reinterpret_cast<uint2 *>(lb + off8_code(v, H, sd.ptok, u.kvh, row) + 8 * lane) = codes;
                 if (lane == 0) *reinterpret_cast<float *>(lb + off8_scale(v, H, sd.ptok, u.kvh, row)) = scale;
@@ -456,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     constexpr int S = F::slots;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Run u = locate(c, a);
+    const Run u = locate<F::tile>(c, a);
     const SeqDev &sd = c.seq[u.s];
     const int ncols = sd.ncols, G = c.group, H = c.n_kv_heads;
     const int ncg = (ncols + 7) >> 3;           // column groups of 8
@@ -505,38 +517,43 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         const uint64_t pol = policy_evict_first();
         const void *map = sd.tma >= 0 ? &maps.map[sd.tma] : nullptr;
         const int v_rows = H * sd.ptok;       // map rows from a K row to its V row
+        const bool wide = window_wide(sd);    // e4m3: a copy takes the tile's 32 rows, else 16
         // cached rows more than kFreshGuard below the new tokens do not depend
         // on the previous kernel: their tiles stream before the wait
         const int early_end = u.qbase - kFreshGuard;
         bool waited = false;
         int first = -1;         // lane i: first virtual key of tile t0 + i, -1: an empty tile
-        int yk = -1;            // map row of its first K row, -1: not a run of cached rows
-        int64_t sc = 0;         // e4m3: byte offset of its K scales
+        int yk = -1, yk2 = 0;   // map rows of its first K row and its 17th, -1: not runs of cached rows
+        int64_t sc = 0, sc2 = 0;  // e4m3: byte offsets of those rows' K scales
         for (int t = 0; t < ntiles; ++t, ++issued) {
             if ((t & 31) == 0) {
                 // the next 32 tiles' rows, a tile a lane: looked up one by one
                 // they would take the warp longer than a tile takes to arrive
                 const int pc = (t + lane) / round, tp = t + lane - pc * round;
-                const int v0 = u.key0 + (pc * u.per + tp) * kTile, p0 = pos_of(u.sp, v0);
+                const int v0 = u.key0 + (pc * u.per + tp) * F::tile, p0 = pos_of(u.sp, v0);
                 first = tp < u.per && v0 < u.key1 ? v0 : -1;
                 yk = -1;
-                if (map != nullptr && first >= 0 && v0 + kTile <= u.key1 &&
-                    (p0 >= u.sp.lo || p0 + kTile <= a.n_sink || a.n_sink >= u.sp.lo) &&
-                    (a.k_new == nullptr || p0 + kTile <= u.qbase)) {
-                    int row = p0;
-                    int64_t pg = 0;
-                    if (sd.table) {
-                        const int page = p0 / sd.ptok;
-                        row = p0 - page * sd.ptok;
-                        pg = x.pages[v0 < u.sp.sink_end ? page - u.sink_page : u.n_sink_pages + page - u.win_page];
-                        if (pg < 0) pg = 0;  // reported when it was looked up
-                    }
-                    if constexpr (kFp8) {
-                        yk = static_cast<int>(sd.layer_row + (2 * pg + off8_code(false, H, sd.ptok, u.kvh, row)) / kHeadDim);
-                        sc = 2 * pg + off8_scale(false, H, sd.ptok, u.kvh, row);
-                    } else {
-                        yk = static_cast<int>(sd.layer_row + (pg + off_k(sd.ptok, u.kvh, row)) / kHeadDim);
-                    }
+                if (map != nullptr && first >= 0 && v0 + F::tile <= u.key1 &&
+                    (p0 >= u.sp.lo || p0 + F::tile <= a.n_sink || a.n_sink >= u.sp.lo) &&
+                    (a.k_new == nullptr || p0 + F::tile <= u.qbase)) {
+                    auto look = [&](int p, int &y, int64_t &scale) {
+                        int row = p;
+                        int64_t pg = 0;
+                        if (sd.table) {
+                            const int page = p / sd.ptok;
+                            row = p - page * sd.ptok;
+                            pg = x.pages[v0 < u.sp.sink_end ? page - u.sink_page : u.n_sink_pages + page - u.win_page];
+                            if (pg < 0) pg = 0;  // reported when it was looked up
+                        }
+                        if constexpr (kFp8) {
+                            y = static_cast<int>(sd.layer_row + (2 * pg + off8_code(false, H, sd.ptok, u.kvh, row)) / kHeadDim);
+                            scale = 2 * pg + off8_scale(false, H, sd.ptok, u.kvh, row);
+                        } else {
+                            y = static_cast<int>(sd.layer_row + (pg + off_k(sd.ptok, u.kvh, row)) / kHeadDim);
+                        }
+                    };
+                    look(p0, yk, sc);
+                    if (kFp8 && !wide) look(p0 + 16, yk2, sc2);
                 }
             }
             const int slot = t % S, y = __shfl_sync(0xffffffffu, yk, t & 31);
@@ -553,23 +570,34 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                 if (lane == 0) mbar_arrive(bar);
                 continue;
             }
-            if (!waited && pos_of(u.sp, v0) + kTile > early_end) {
+            if (!waited && pos_of(u.sp, v0) + F::tile > early_end) {
                 pdl_wait();
                 waited = true;
             }
             if (y >= 0) {
-                // one page holds the 16 keys: a copy of K, one of V, and with
-                // e4m3 pages one of each scale run
+                // a page holds the keys (e4m3: or a page each of their halves): a
+                // copy of K and one of V, and with e4m3 pages of their scales
                 uint8_t *const kst = x.stages + slot * F::stage;
-                const int64_t s0 = kFp8 ? shfl64(sc, t & 31) : 0;
+                const int64_t s0 = kFp8 ? shfl64(sc, t & 31) : 0, s1 = kFp8 && !wide ? shfl64(sc2, t & 31) : 0;
+                const int y2 = kFp8 && !wide ? __shfl_sync(0xffffffffu, yk2, t & 31) : 0;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bar, F::stage + (kFp8 ? 128 : 0));
-                    tma_load_3d(kst, map, 0, y, 0, bar, pol);
-                    tma_load_3d(kst + F::half, map, 0, y + v_rows, 0, bar, pol);
+                    mbar_arrive_expect_tx(bar, F::stage + (kFp8 ? 256 : 0));
                     if constexpr (kFp8) {
-                        const uint8_t *base = reinterpret_cast<const uint8_t *>(sd.layer_base) + s0;
-                        bulk_g2s(x.scl + slot * 32, base, 64, bar, pol);
-                        bulk_g2s(x.scl + slot * 32 + 16, base + 4 * (int64_t)v_rows, 64, bar, pol);
+                        const uint8_t *base = reinterpret_cast<const uint8_t *>(sd.layer_base);
+                        float *const scl = x.scl + slot * 64;
+                        tma_load_3d(kst, map, 0, 0, y, bar, pol);
+                        tma_load_3d(kst + F::half, map, 0, 0, y + v_rows, bar, pol);
+                        bulk_g2s(scl, base + s0, wide ? 128 : 64, bar, pol);
+                        bulk_g2s(scl + 32, base + s0 + 4 * (int64_t)v_rows, wide ? 128 : 64, bar, pol);
+                        if (!wide) {
+                            tma_load_3d(kst + F::half / 2, map, 0, 0, y2, bar, pol);
+                            tma_load_3d(kst + F::half + F::half / 2, map, 0, 0, y2 + v_rows, bar, pol);
+                            bulk_g2s(scl + 16, base + s1, 64, bar, pol);
+                            bulk_g2s(scl + 48, base + s1 + 4 * (int64_t)v_rows, 64, bar, pol);
+                        }
+                    } else {
+                        tma_load_3d(kst, map, 0, y, 0, bar, pol);
+                        tma_load_3d(kst + F::half, map, 0, y + v_rows, 0, bar, pol);
                     }
                 }
             } else if constexpr (kFp8) {
@@ -676,161 +704,179 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                 *x.abort_flag = 1;
                 break;
             }
-            const int v0 = u.key0 + (pc * u.per + tp) * kTile;
+            const int v0 = u.key0 + (pc * u.per + tp) * F::tile;
             if (tp >= u.per || v0 >= u.key1) {
                 if (lane == 0) mbar_arrive(&x.empty[slot]);
                 continue;
             }
-            const int ka = pos_of(u.sp, v0) + g, kb = ka + 8;
-            const bool a0 = sees(p0, ka, a.window, a.n_sink), a1 = sees(p1, ka, a.window, a.n_sink);
-            const bool b0 = sees(p0, kb, a.window, a.n_sink), b1 = sees(p1, kb, a.window, a.n_sink);
-            float sx[4];
-            if constexpr (kFp8) {
-                const uint8_t *st = x.stages + slot * F::stage;
-                // two accumulator chains, the whole K fragment loaded before its MMAs
+            const uint8_t *const st = x.stages + slot * F::stage;
+            const float *const scl = x.scl + slot * 64;  // e4m3
+            // S^T of the tile's keys and this lane's two columns: rows g and g + 8
+            // of each 16 keys, in log2 units, -inf where the column's query does
+            // not see the key
+            constexpr int kSub = F::tile / 16;
+            float sx[kSub][4];
+#pragma unroll
+            for (int u16 = 0; u16 < kSub; ++u16) {
                 float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-                uint4 w0[4], w1[4];
+                float fa = kScaleLog2, fb = kScaleLog2;
+                if constexpr (kFp8) {
+                    // two accumulator chains, a quarter of the dims at a time
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w0[i] = *reinterpret_cast<const uint4 *>(st + swz(g, 4 * c4 + i));
-                    w1[i] = *reinterpret_cast<const uint4 *>(st + swz(g + 8, 4 * c4 + i));
-                }
-                // a step's codes widen while the step before is multiplied
-                uint32_t fr[3][4];
-                auto widen = [&](int st_) {
-                    const uint4 q0 = w0[st_ >> 2], q1 = w1[st_ >> 2];
-                    const uint32_t e0 = (st_ & 3) == 0 ? q0.x : (st_ & 3) == 1 ? q0.y : (st_ & 3) == 2 ? q0.z : q0.w;
-                    const uint32_t e1 = (st_ & 3) == 0 ? q1.x : (st_ & 3) == 1 ? q1.y : (st_ & 3) == 2 ? q1.z : q1.w;
-                    uint32_t(&o)[4] = fr[st_ % 3];
-                    o[0] = f16_of_codes(e0);
-                    o[1] = f16_of_codes(e1);
-                    o[2] = f16_of_codes(e0 >> 16);
-                    o[3] = f16_of_codes(e1 >> 16);
-                };
-                widen(0);
-                widen(1);
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 w0 = *reinterpret_cast<const uint4 *>(st + swz8(16 * u16 + g, 4 * c4 + i));
+                        const uint4 w1 = *reinterpret_cast<const uint4 *>(st + swz8(16 * u16 + g + 8, 4 * c4 + i));
+                        uint32_t z[4][4];
+                        f16_of_codes(w0.x, z[0][0], z[0][2]);
+                        f16_of_codes(w1.x, z[0][1], z[0][3]);
+                        f16_of_codes(w0.y, z[1][0], z[1][2]);
+                        f16_of_codes(w1.y, z[1][1], z[1][3]);
+                        f16_of_codes(w0.z, z[2][0], z[2][2]);
+                        f16_of_codes(w1.z, z[2][1], z[2][3]);
+                        f16_of_codes(w0.w, z[3][0], z[3][2]);
+                        f16_of_codes(w1.w, z[3][1], z[3][3]);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    if (j < 14) widen(j + 2);
-                    mma_half((j & 1) ? sb : sa, fr[j % 3][0], fr[j % 3][1], fr[j % 3][2], fr[j % 3][3], qf[j][0], qf[j][1]);
-                }
-                const float ska = x.scl[slot * 32 + g] * kScaleLog2, skb = x.scl[slot * 32 + g + 8] * kScaleLog2;
-                sx[0] = a0 ? (sa[0] + sb[0]) * ska : -INFINITY;
-                sx[1] = a1 ? (sa[1] + sb[1]) * ska : -INFINITY;
-                sx[2] = b0 ? (sa[2] + sb[2]) * skb : -INFINITY;
-                sx[3] = b1 ? (sa[3] + sb[3]) * skb : -INFINITY;
-            } else {
-                // two accumulator chains, four K fragments loaded before their MMAs
-                const uint32_t kbs = s_base + slot * F::stage;
-                float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+                        for (int j = 0; j < 4; ++j)
+                            mma_half((j & 1) ? sb : sa, z[j][0], z[j][1], z[j][2], z[j][3], qf[4 * i + j][0], qf[4 * i + j][1]);
+                    }
+                    fa *= scl[16 * u16 + g];
+                    fb *= scl[16 * u16 + g + 8];
+                } else {
+                    // two accumulator chains, four K fragments loaded before their MMAs
+                    const uint32_t kbs = s_base + slot * F::stage;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t f[4][4];
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t f[4][4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ldsm_x4(kbs + h * kPlane + swz(kr_, 2 * j + kcb), f[j][0], f[j][1], f[j][2], f[j][3]);
+                        for (int j = 0; j < 4; ++j)
+                            ldsm_x4(kbs + h * kPlane + swz(kr_, 2 * j + kcb), f[j][0], f[j][1], f[j][2], f[j][3]);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t(&x4)[4] = f[j];
-                        mma_bf16((j & 1) ? sb : sa, x4[0], x4[1], x4[2], x4[3], qf[4 * h + j][0], qf[4 * h + j][1]);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t(&x4)[4] = f[j];
+                            mma_bf16((j & 1) ? sb : sa, x4[0], x4[1], x4[2], x4[3], qf[4 * h + j][0], qf[4 * h + j][1]);
+                        }
                     }
                 }
-                sx[0] = a0 ? (sa[0] + sb[0]) * kScaleLog2 : -INFINITY;
-                sx[1] = a1 ? (sa[1] + sb[1]) * kScaleLog2 : -INFINITY;
-                sx[2] = b0 ? (sa[2] + sb[2]) * kScaleLog2 : -INFINITY;
-                sx[3] = b1 ? (sa[3] + sb[3]) * kScaleLog2 : -INFINITY;
+                const int ka = pos_of(u.sp, v0) + 16 * u16 + g, kb = ka + 8;
+                sx[u16][0] = sees(p0, ka, a.window, a.n_sink) ? (sa[0] + sb[0]) * fa : -INFINITY;
+                sx[u16][1] = sees(p1, ka, a.window, a.n_sink) ? (sa[1] + sb[1]) * fa : -INFINITY;
+                sx[u16][2] = sees(p0, kb, a.window, a.n_sink) ? (sa[2] + sb[2]) * fb : -INFINITY;
+                sx[u16][3] = sees(p1, kb, a.window, a.n_sink) ? (sa[3] + sb[3]) * fb : -INFINITY;
             }
             // online softmax of the two columns
-            const float n0 = fmaxf(m[0], max_rows(fmaxf(sx[0], sx[2])));
-            const float n1 = fmaxf(m[1], max_rows(fmaxf(sx[1], sx[3])));
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int u16 = 0; u16 < kSub; ++u16) {
+                t0 = fmaxf(t0, fmaxf(sx[u16][0], sx[u16][2]));
+                t1 = fmaxf(t1, fmaxf(sx[u16][1], sx[u16][3]));
+            }
+            const float n0 = fmaxf(m[0], max_rows(t0)), n1 = fmaxf(m[1], max_rows(t1));
             const float o0 = n0 == -INFINITY ? 0.f : n0, o1 = n1 == -INFINITY ? 0.f : n1;
             const float al0 = ex2(m[0] - o0), al1 = ex2(m[1] - o1);  // 0 while nothing was summed
-            const float e0 = ex2(sx[0] - o0), e1 = ex2(sx[1] - o1), e2 = ex2(sx[2] - o0), e3 = ex2(sx[3] - o1);
-            l[0] = l[0] * al0 + (e0 + e2);
-            l[1] = l[1] * al1 + (e1 + e3);
             m[0] = n0;
             m[1] = n1;
+            l[0] *= al0;
+            l[1] *= al1;
+            // the weights of O, as two parts (hi + lo) in the MMAs' B layout
+            uint32_t wh[kSub][2], wl[kSub][2];
+            float be0 = al0, be1 = al1;  // what O is rescaled by
             if constexpr (kFp8) {
                 // a V scale 2^E x mant goes into the key's weight, with a running
                 // maximum of logit + E as O's reference: weights in [0, 2), split
                 // into f16 hi + lo parts (about 22 significant bits)
-                float ea, ma, eb, mb;
-                split_scale(x.scl[slot * 32 + 16 + g], ea, ma);
-                split_scale(x.scl[slot * 32 + 16 + g + 8], eb, mb);
-                const float y0 = sx[0] + ea, y1 = sx[1] + ea, y2 = sx[2] + eb, y3 = sx[3] + eb;
-                const float nu0 = fmaxf(uo[0], max_rows(fmaxf(y0, y2))), nu1 = fmaxf(uo[1], max_rows(fmaxf(y1, y3)));
-                const float v0 = nu0 == -INFINITY ? 0.f : nu0, v1 = nu1 == -INFINITY ? 0.f : nu1;
-                const float be0 = ex2(uo[0] - v0), be1 = ex2(uo[1] - v1);
+                float e[kSub][2], mt[kSub][2], r0 = -INFINITY, r1 = -INFINITY;
+#pragma unroll
+                for (int u16 = 0; u16 < kSub; ++u16) {
+                    split_scale(scl[32 + 16 * u16 + g], e[u16][0], mt[u16][0]);
+                    split_scale(scl[32 + 16 * u16 + g + 8], e[u16][1], mt[u16][1]);
+                    l[0] += ex2(sx[u16][0] - o0) + ex2(sx[u16][2] - o0);
+                    l[1] += ex2(sx[u16][1] - o1) + ex2(sx[u16][3] - o1);
+                    r0 = fmaxf(r0, fmaxf(sx[u16][0] + e[u16][0], sx[u16][2] + e[u16][1]));
+                    r1 = fmaxf(r1, fmaxf(sx[u16][1] + e[u16][0], sx[u16][3] + e[u16][1]));
+                }
+                const float nu0 = fmaxf(uo[0], max_rows(r0)), nu1 = fmaxf(uo[1], max_rows(r1));
+                const float z0 = nu0 == -INFINITY ? 0.f : nu0, z1 = nu1 == -INFINITY ? 0.f : nu1;
+                be0 = ex2(uo[0] - z0);
+                be1 = ex2(uo[1] - z1);
                 uo[0] = nu0;
                 uo[1] = nu1;
-                const float q0 = ex2(y0 - v0) * ma, q1 = ex2(y1 - v1) * ma;
-                const float q2 = ex2(y2 - v0) * mb, q3 = ex2(y3 - v1) * mb;
-                const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
-                const __half2 l01 = __floats2half2_rn(q0 - __low2float(h01), q1 - __high2float(h01));
-                const __half2 l23 = __floats2half2_rn(q2 - __low2float(h23), q3 - __high2float(h23));
-                const uint32_t b0h = movmatrix_t(bits_of(h01)), b1h = movmatrix_t(bits_of(h23));
-                const uint32_t b0l = movmatrix_t(bits_of(l01)), b1l = movmatrix_t(bits_of(l23));
-                // V codes of keys 2c, 2c+1, 2c+8, 2c+9, dims 32g .. 32g+31
-                uint32_t w[4][8];
-                const uint8_t *vb = x.stages + slot * F::stage + F::half;
-                const int kr[4] = {2 * c4, 2 * c4 + 1, 2 * c4 + 8, 2 * c4 + 9};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 z0 = *reinterpret_cast<const uint4 *>(vb + swz(kr[i], 2 * g));
-                    const uint4 z1 = *reinterpret_cast<const uint4 *>(vb + swz(kr[i], 2 * g + 1));
-                    w[i][0] = z0.x;
-                    w[i][1] = z0.y;
-                    w[i][2] = z0.z;
-                    w[i][3] = z0.w;
-                    w[i][4] = z1.x;
-                    w[i][5] = z1.y;
-                    w[i][6] = z1.z;
-                    w[i][7] = z1.w;
-                }
-                if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {  // some reference grew
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        acc[i][0] *= be0;
-                        acc[i][1] *= be1;
-                        acc[i][2] *= be0;
-                        acc[i][3] *= be1;
-                    }
-                }
-                uint32_t z[3][4];
-                auto widen_v = [&](int i) {  // keys' codes of dims 32g + 2i and + 1, paired
-                    const int wi = i >> 1, b = 2 * (i & 1);
-                    const uint32_t sel0 = b | ((4 + b) << 4), sel1 = (b + 1) | ((5 + b) << 4);
-                    uint32_t(&o)[4] = z[i % 3];
-                    o[0] = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel0));
-                    o[1] = f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel1));
-                    o[2] = f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel0));
-                    o[3] = f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel1));
-                };
-                widen_v(0);
-                widen_v(1);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    if (i < 14) widen_v(i + 2);
-                    mma_half(acc[i], z[i % 3][0], z[i % 3][1], z[i % 3][2], z[i % 3][3], b0h, b1h);
-                    mma_half(acc[i], z[i % 3][0], z[i % 3][1], z[i % 3][2], z[i % 3][3], b0l, b1l);
+                for (int u16 = 0; u16 < kSub; ++u16) {
+                    const float q0 = ex2(sx[u16][0] + e[u16][0] - z0) * mt[u16][0], q1 = ex2(sx[u16][1] + e[u16][0] - z1) * mt[u16][0];
+                    const float q2 = ex2(sx[u16][2] + e[u16][1] - z0) * mt[u16][1], q3 = ex2(sx[u16][3] + e[u16][1] - z1) * mt[u16][1];
+                    const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
+                    const __half2 l01 = __floats2half2_rn(q0 - __low2float(h01), q1 - __high2float(h01));
+                    const __half2 l23 = __floats2half2_rn(q2 - __low2float(h23), q3 - __high2float(h23));
+                    wh[u16][0] = movmatrix_t(bits_of(h01));
+                    wh[u16][1] = movmatrix_t(bits_of(h23));
+                    wl[u16][0] = movmatrix_t(bits_of(l01));
+                    wl[u16][1] = movmatrix_t(bits_of(l23));
                 }
             } else {
-                if (__any_sync(0xffffffffu, al0 != 1.f || al1 != 1.f)) {  // some maximum grew
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        acc[i][0] *= al0;
-                        acc[i][1] *= al1;
-                        acc[i][2] *= al0;
-                        acc[i][3] *= al1;
-                    }
-                }
                 // P as a bf16 pair hi + lo (lo = p - hi exactly): about 16
                 // significant bits of the weights reach the float32 accumulator
+                const float e0 = ex2(sx[0][0] - o0), e1 = ex2(sx[0][1] - o1), e2 = ex2(sx[0][2] - o0), e3 = ex2(sx[0][3] - o1);
+                l[0] += e0 + e2;
+                l[1] += e1 + e3;
                 const uint32_t h01 = pack_bf16(e0, e1), h23 = pack_bf16(e2, e3);
-                const uint32_t l01 = pack_bf16(e0 - bf16_lo(h01), e1 - bf16_hi(h01));
-                const uint32_t l23 = pack_bf16(e2 - bf16_lo(h23), e3 - bf16_hi(h23));
-                const uint32_t pb0 = movmatrix_t(h01), pb1 = movmatrix_t(h23);
-                const uint32_t pc0 = movmatrix_t(l01), pc1 = movmatrix_t(l23);
+                wh[0][0] = movmatrix_t(h01);
+                wh[0][1] = movmatrix_t(h23);
+                wl[0][0] = movmatrix_t(pack_bf16(e0 - bf16_lo(h01), e1 - bf16_hi(h01)));
+                wl[0][1] = movmatrix_t(pack_bf16(e2 - bf16_lo(h23), e3 - bf16_hi(h23)));
+            }
+            if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {  // some reference grew
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    acc[i][0] *= be0;
+                    acc[i][1] *= be1;
+                    acc[i][2] *= be0;
+                    acc[i][3] *= be1;
+                }
+            }
+            // O^T += V^T P^T
+            if constexpr (kFp8) {
+#pragma unroll
+                for (int u16 = 0; u16 < kSub; ++u16) {
+                    // V codes of keys 2c, 2c+1, 2c+8, 2c+9, dims 32g .. 32g+31
+                    uint32_t w[4][8];
+                    const uint8_t *vb = st + F::half;
+                    const int kr[4] = {2 * c4, 2 * c4 + 1, 2 * c4 + 8, 2 * c4 + 9};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 z0 = *reinterpret_cast<const uint4 *>(vb + swz8(16 * u16 + kr[i], 2 * g));
+                        const uint4 z1 = *reinterpret_cast<const uint4 *>(vb + swz8(16 * u16 + kr[i], 2 * g + 1));
+                        w[i][0] = z0.x;
+                        w[i][1] = z0.y;
+                        w[i][2] = z0.z;
+                        w[i][3] = z0.w;
+                        w[i][4] = z1.x;
+                        w[i][5] = z1.y;
+                        w[i][6] = z1.z;
+                        w[i][7] = z1.w;
+                    }
+                    // four dim tiles at a time: a hi and a lo product of one
+                    // tile follow each other at the MMA's latency
+#pragma unroll
+                    for (int i4 = 0; i4 < 16; i4 += 4) {
+                        uint32_t z[4][4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // codes of dims 32g + 2 (i4 + i) and + 1: {key, next key}
+                            // of the first dim, then of the second
+                            const int wi = (i4 + i) >> 1, b = 2 * (i & 1);
+                            const uint32_t sel = b | ((4 + b) << 4) | ((b + 1) << 8) | ((5 + b) << 12);
+                            f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel), z[i][0], z[i][1]);
+                            f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel), z[i][2], z[i][3]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_half(acc[i4 + i], z[i][0], z[i][1], z[i][2], z[i][3], wh[u16][0], wh[u16][1]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mma_half(acc[i4 + i], z[i][0], z[i][1], z[i][2], z[i][3], wl[u16][0], wl[u16][1]);
+                    }
+                }
+            } else {
                 const uint32_t vbs = s_base + slot * F::stage + F::half;
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
@@ -841,12 +887,12 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t(&x4)[4] = f[j];
-                        mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], pb0, pb1);
+                        mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], wh[0][0], wh[0][1]);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t(&x4)[4] = f[j];
-                        mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], pc0, pc1);
+                        mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], wl[0][0], wl[0][1]);
                     }
                 }
             }
@@ -927,19 +973,22 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     cluster_sync();  // the peers have read this CTA's sums
 }
 
-// Merge of the slices' partials for calls whose CTAs are not clustered: 64
-// threads a query column, four dims each; a piece's slices, the split's pieces
-// and the splits in order, as a clustered CTA and its cluster merge them.
+// Merge of the slices' partials for calls whose CTAs are not clustered: a CTA a
+// query column, four groups of 64 threads (four dims each) that take every
+// fourth piece; a piece's slices, the split's pieces and the splits in order,
+// as a clustered CTA and its cluster merge them.
 constexpr int kCombThreads = 256;
 __global__ void __launch_bounds__(kCombThreads)
-    window_combine(const __grid_constant__ Common c, const __grid_constant__ WinArgs a, int32_t total) {
+    window_combine(const __grid_constant__ Common c, const __grid_constant__ WinArgs a) {
+    __shared__ float2 sh_ml[kMaxPieces];
+    __shared__ float4 sh_o[kMaxPieces][64];
     pdl_trigger();  // the next kernel waits for this grid before it reads what it writes
-    const int i = static_cast<int>(blockIdx.x) * (kCombThreads / 64) + (threadIdx.x >> 6);
-    if (i >= total) return;
+    const int i = static_cast<int>(blockIdx.x);
     const int s = find_seq(c.n_seqs, i, [&](int t) { return c.seq[t].comb_off; });
     const SeqDev &sd = c.seq[s];
     const int r = i - sd.comb_off, ncols = sd.ncols, unit = r / ncols, col = r - unit * ncols, G = c.group;
-    const int d = 4 * (threadIdx.x & 63), j = col / G, ks_n = slices_of(c.kv_fp8 != 0, ncols);
+    const int grp = threadIdx.x >> 6, d4 = threadIdx.x & 63, d = 4 * d4, j = col / G;
+    const int ks_n = slices_of(c.kv_fp8 != 0, ncols);
     const int64_t n_part = (int64_t)sd.nsplit * a.pieces * ks_n;
     const float *acc = a.ws + sd.ws_off + (unit * n_part * ncols + col) * kHeadDim + d;
     const float *ml = a.ws + sd.ws_off + (int64_t)c.n_kv_heads * n_part * ncols * kHeadDim + (unit * n_part * ncols + col) * 2;
@@ -948,49 +997,52 @@ __global__ void __launch_bounds__(kCombThreads)
     pdl_wait();
     Sum t;
     for (int sp = 0; sp < sd.nsplit; ++sp) {
-        Sum pieces[kMaxPieces];
-#pragma unroll
-        for (int p = 0; p < kMaxPieces; ++p) {
-            if (p < a.pieces) {
-                const int64_t p0 = (int64_t)(sp * a.pieces + p) * ks_n;
-                pieces[p] = merge_parts<kMaxSlices>(
-                    ks_n, [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(ml + (p0 + k) * ncols * 2)); },
-                    [&](int k) { return __ldcg(reinterpret_cast<const float4 *>(acc + (p0 + k) * ncols * kHeadDim)); });
+        for (int p = grp; p < a.pieces; p += kCombThreads / 64) {
+            const int64_t p0 = (int64_t)(sp * a.pieces + p) * ks_n;
+            const Sum x = merge_parts<kMaxSlices>(
+                ks_n, [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(ml + (p0 + k) * ncols * 2)); },
+                [&](int k) { return __ldcg(reinterpret_cast<const float4 *>(acc + (p0 + k) * ncols * kHeadDim)); });
+            sh_o[p][d4] = x.o;
+            if (d4 == 0) sh_ml[p] = make_float2(x.m, x.l);
+        }
+        __syncthreads();
+        if (grp == 0) {
+            const Sum x = merge_parts<kMaxPieces>(
+                a.pieces, [&](int p) { return sh_ml[p]; }, [&](int p) { return sh_o[p][d4]; });
+            if (sp == 0) {
+                t = x;
+            } else {
+                const float M = fmaxf(t.m, x.m);
+                const float wt = M == -INFINITY ? 0.f : ex2(t.m - M), wx = M == -INFINITY ? 0.f : ex2(x.m - M);
+                t.l = wt * t.l + wx * x.l;
+                t.o.x = wt * t.o.x + wx * x.o.x;
+                t.o.y = wt * t.o.y + wx * x.o.y;
+                t.o.z = wt * t.o.z + wx * x.o.z;
+                t.o.w = wt * t.o.w + wx * x.o.w;
+                t.m = M;
             }
         }
-        const Sum x = merge_parts<kMaxPieces>(
-            a.pieces, [&](int p) { return make_float2(pieces[p].m, pieces[p].l); }, [&](int p) { return pieces[p].o; });
-        if (sp == 0) {
-            t = x;
-        } else {
-            const float M = fmaxf(t.m, x.m);
-            const float wt = M == -INFINITY ? 0.f : ex2(t.m - M), wx = M == -INFINITY ? 0.f : ex2(x.m - M);
-            t.l = wt * t.l + wx * x.l;
-            t.o.x = wt * t.o.x + wx * x.o.x;
-            t.o.y = wt * t.o.y + wx * x.o.y;
-            t.o.z = wt * t.o.z + wx * x.o.z;
-            t.o.w = wt * t.o.w + wx * x.o.w;
-            t.m = M;
-        }
+        if (sp + 1 < sd.nsplit) __syncthreads();  // the sums are read before the next split's
     }
-    write_out(out, t);
+    if (grp == 0) write_out(out, t);
 }
 
 }  // namespace
 
 // Pieces of a split, by the window alone (a stream's bits must not depend on
-// its batch): eight tiles a piece before there is another.
+// its batch): 128 keys a piece before there is another.
 int window_pieces(int32_t window, int32_t n_sink) {
-    const int64_t tiles = ((int64_t)window + n_sink) / kTile + 2;
+    const int64_t keys = (int64_t)window + n_sink + 32;
     int n = 1;
-    while (n < kMaxPieces && tiles > 8 * n) n *= 2;
+    while (n < kMaxPieces && keys > 128 * n) n *= 2;
     return n;
 }
 
-// Splits only where a piece would pass kSplitTiles tiles.
+// Splits only where a piece would pass kSplitKeys keys.
 int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
     int64_t items = 0, cols = 0, floats = 0;
     const int pieces = window_pieces(window, n_sink);
+    const int tile = c.kv_fp8 ? Cfg<true>::tile : Cfg<false>::tile;
     bool split = false;
     for (int s = 0; s < c.n_seqs; ++s) {
         SeqDev &d = c.seq[s];
@@ -1000,13 +1052,12 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
         d.ncols = d.n_new * c.group;
         if (d.ncols > kMaxCols) return PKV_EINVAL;
         d.nsplit = 1;
-        d.split_len = kTile;
+        d.split_len = tile;
         if (d.ncols == 0) continue;
-        const WindowSpan sp = window_span(d.len, d.n_new, window, n_sink, kTile);
-        const int tiles = (sp.nkeys + kTile - 1) / kTile;
-        d.nsplit = (tiles + pieces * kSplitTiles - 1) / (pieces * kSplitTiles);
-        const int per = (tiles + d.nsplit * pieces - 1) / (d.nsplit * pieces);
-        d.split_len = per * kTile;
+        const WindowSpan sp = window_span(d.len, d.n_new, window, n_sink, tile);
+        d.nsplit = (sp.nkeys - 1) / (pieces * kSplitKeys) + 1;
+        const int per = (sp.nkeys - 1) / (d.nsplit * pieces) + 1;  // keys of a piece
+        d.split_len = (per + tile - 1) / tile * tile;
         split |= d.nsplit > 1;
         items += (int64_t)c.n_kv_heads * d.nsplit;
         cols += (int64_t)c.n_kv_heads * d.ncols;
@@ -1041,7 +1092,12 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
                                                 cudaSharedmemCarveoutMaxShared));
         }) != PKV_OK)
         return PKV_ECUDA;
-    WinArgs a{q, out, ws, k_new, v_new, ik_new, window, n_sink, window_pieces(window, n_sink), 0};
+    WinArgs a{q, out, ws, k_new, v_new, ik_new, window, n_sink, window_pieces(window, n_sink), 0, 0};
+    if (plan.total_items % c.n_seqs == 0) {
+        a.even = plan.total_items / c.n_seqs;
+        for (int s = 0; s < c.n_seqs; ++s)
+            if (c.seq[s].work_off != s * a.even) a.even = 0;
+    }
     const bool clustered = plan.total_comb == 0;
     // one wave of CTAs where the pieces allow it
     if (!clustered)
@@ -1062,9 +1118,8 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
     if (cudaLaunchKernelEx(&cfg, c.kv_fp8 ? window_partial<true> : window_partial<false>, c, maps, a) != cudaSuccess)
         return PKV_ECUDA;
     if (clustered) return PKV_OK;
-    const int per = kCombThreads / 64;
-    return launch_status(launch_pdl(window_combine, static_cast<unsigned>((plan.total_comb + per - 1) / per),
-                                    kCombThreads, 0, stream, c, a, plan.total_comb));
+    return launch_status(
+        launch_pdl(window_combine, static_cast<unsigned>(plan.total_comb), kCombThreads, 0, stream, c, a));
 }
 
 }  // namespace pkv
