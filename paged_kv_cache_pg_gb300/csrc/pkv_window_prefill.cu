@@ -155,6 +155,11 @@ __device__ __forceinline__ int row_of(const Gathered &g, const Keys &k, int v) {
     return g.win + (k.lo - g.lo) + (v - k.sink_end);
 }
 
+// The lowest n of 64 bits.
+__device__ __forceinline__ uint64_t below(int n) {
+    return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
 // bf16 bits of a float rounded up (toward +infinity).
 __device__ __forceinline__ uint16_t bf16_up(float x) {
     uint32_t u = __float_as_uint(x);
@@ -233,6 +238,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         uint16_t *const red = reinterpret_cast<uint16_t *>(smem + kOffRed);
         uint8_t *const p_row = smem + hf * kPRegion + r * 128;
+        // positions fit 31 bits, sums of two of them clamped to 30 do
+        constexpr int kFar = 1 << 30;
+        const int n_sink = min(a.n_sink, kFar);
         uint32_t T = 0, it = 0;  // tiles and items so far
         bool ok = true;
         for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x, ++it) {
@@ -240,8 +248,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const SeqDev &sd = c.seq[t.s];
             // rows past the M-tile's end take no mask: their Q rows are
             // zero, so their scores are finite, and they are never written
-            const int qpos = r < t.rows ? sd.len - sd.n_new + (t.col0 + r) / G : INT_MAX;
-            const int win0 = r < t.rows ? qpos - a.window : INT_MIN;  // keys above it are in the row's window
+            const int qpos = r < t.rows ? sd.len - sd.n_new + (t.col0 + r) / G : kFar;
+            const int win0 = r < t.rows ? max(qpos - a.window, -kFar) : -kFar;  // keys above it are in the row's window
             float m_raw = -INFINITY, m_used = -INFINITY, l = 0.f;
             for (int n = 0; n < t.ntiles; ++n, ++T) {
                 if (!(ok = wait_warp(kSFull, T))) break;
@@ -254,18 +262,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int kp0 = v0 - t.k.sink_end + t.k.lo;            // its position, in the window's part
                 float x[64];
                 const bool all = v0 >= t.k.sink_end
-                                     ? kp0 + 63 <= qpos && (kp0 > win0 || kp0 + 63 < a.n_sink)
+                                     ? kp0 + 63 <= qpos && (kp0 > win0 || kp0 + 63 < n_sink)
                                      : v0 + 63 < t.k.slim;
                 if (__all_sync(0xffffffffu, all)) {
 #pragma unroll
                     for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(sv[j]);
                 } else {
+                    // one bit a key: the sinks' runs hold positions below slim,
+                    // the window's part positions up to qpos that are in the
+                    // row's window or among the sinks (compared key by key this
+                    // took 3 to 4 us a tile, a fifth of a nine-tile item)
+                    const uint64_t part = below(t.k.sink_end - v0);
+                    const uint64_t see = (part & below(t.k.slim - v0)) |
+                                         (~part & below(qpos - kp0 + 1) & (~below(win0 - kp0 + 1) | below(n_sink - kp0)));
+                    const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-                    for (int j = 0; j < 64; ++j) {
-                        const int kp = kp0 + j;
-                        const bool see = v0 + j >= t.k.sink_end ? kp <= qpos && (kp > win0 || kp < a.n_sink)
-                                                                : v0 + j < t.k.slim;
-                        x[j] = see ? __uint_as_float(sv[j]) : -INFINITY;
+                    for (int j = 0; j < 32; ++j) {
+                        x[j] = (see0 >> j) & 1u ? __uint_as_float(sv[j]) : -INFINITY;
+                        x[j + 32] = (see1 >> j) & 1u ? __uint_as_float(sv[j + 32]) : -INFINITY;
                     }
                 }
                 // this half's max as eight interleaved chains, then the row's
@@ -348,43 +362,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col = t.col0 + r, j = col / G;
             return ((int64_t)c.seq[t.s].tok_off + j) * c.n_q_heads + t.kvh * G + (col - j * G);
         };
-        auto store_q = [&](const Item &t) {
+        // A half of the row's Q (128 dims) from global memory, and into TMEM
+        uint4 qv[16];
+        auto load_q = [&](const Item &t, int half) {
             const bool row_ok = r < t.rows;
-            const uint16_t *src = a.q + (row_ok ? q_row(t) : 0) * kHeadDim;
-#pragma unroll 1
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t qv[32];
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (row_ok ? q_row(t) : 0) * kHeadDim + 128 * half);
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
-                    const uint4 v = row_ok ? __ldg(reinterpret_cast<const uint4 *>(src + 64 * ch + 2 * j))
-                                           : make_uint4(0, 0, 0, 0);
-                    qv[j] = v.x;
-                    qv[j + 1] = v.y;
-                    qv[j + 2] = v.z;
-                    qv[j + 3] = v.w;
+            for (int j = 0; j < 16; ++j) qv[j] = row_ok ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+        };
+        auto put_q = [&](int half) {
+#pragma unroll
+            for (int ch = 0; ch < 2; ++ch) {
+                uint32_t w[32];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    w[4 * j] = qv[8 * ch + j].x;
+                    w[4 * j + 1] = qv[8 * ch + j].y;
+                    w[4 * j + 2] = qv[8 * ch + j].z;
+                    w[4 * j + 3] = qv[8 * ch + j].w;
                 }
                 __syncwarp();
-                tmem_st32(lane_base + kQCol + 32 * ch, qv);
+                tmem_st32(lane_base + kQCol + 64 * half + 32 * ch, w);
             }
+        };
+        auto q_stored = [&]() {
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
             mbar_arrive(&bars[kQFull]);
         };
         uint32_t it = 0;
         Item t = item_at(c, a, blockIdx.x);
-        store_q(t);
+        load_q(t, 0);
+        put_q(0);
+        load_q(t, 1);
+        put_q(1);
+        q_stored();
         for (int i = blockIdx.x; i < a.n_items; i += gridDim.x, ++it) {
             const int next = i + gridDim.x;
             Item t2 = t;
             if (next < a.n_items) {
+                // the first half waits in registers for the last product that
+                // reads this item's Q, the second in L2
                 t2 = item_at(c, a, next);
+                load_q(t2, 0);
                 if (r < t2.rows)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + q_row(t2) * kHeadDim + 64 * j));
+                    for (int j = 0; j < 2; ++j)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.q + q_row(t2) * kHeadDim + 128 + 64 * j));
                 if (!wait_warp(kQEmpty, it)) break;
                 tc_fence_after();
-                store_q(t2);
+                put_q(0);
+                load_q(t2, 1);
+                put_q(1);
+                q_stored();
             }
             if (!wait_warp(kSums, it)) break;
             if (!wait_warp(kOLast, it)) break;
@@ -457,6 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_commit(&bars[kEmpty + q % kSlots]);  // free once these MMAs are done
                 ++q;
             };
+            // a descriptor's address is its low 14 bits in units of 16 bytes, and
+            // shared memory ends below 256 KB: offsets are added to the low word
+            const uint64_t desc_k = smem_desc(0, 16, 1024), desc_v = smem_desc(0, kVRegion, 1024);
+            const uint64_t desc_p = smem_desc(sbase, 16, 1024);
             auto issue_s = [&](uint32_t tile, bool last) -> bool {
                 if (tile > 0 && !wait(kSEmpty, tile - 1)) return false;
                 tc_fence_after();
@@ -464,12 +498,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int hh = 0; hh < 2; ++hh) {
                     uint32_t kb;
                     if (!take(kb)) return false;
+                    const uint64_t dk = desc_k + (kb >> 4);
 #pragma unroll
-                    for (int k8 = 0; k8 < 8; ++k8) {
-                        const uint32_t kbb = kb + (k8 >> 2) * kKRegion + (k8 & 3) * 32;
-                        tc_mma_ts(tmem + kSCol, tmem + kQCol + (8 * hh + k8) * 8, smem_desc(kbb, 16, 1024), idesc_s,
+                    for (int k8 = 0; k8 < 8; ++k8)
+                        tc_mma_ts(tmem + kSCol, tmem + kQCol + (8 * hh + k8) * 8,
+                                  dk + (((k8 >> 2) * kKRegion + (k8 & 3) * 32) >> 4), idesc_s,
                                   (hh > 0 || k8 > 0) ? 1u : 0u);
-                    }
                     give();
                 }
                 tc_commit(&bars[kSFull]);
@@ -493,10 +527,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int hh = 0; hh < 2; ++hh) {
                         uint32_t vb;
                         if (!(ok = take(vb))) break;
+                        const uint64_t dp = desc_p + (hh * kPRegion >> 4), dv = desc_v + (vb >> 4);
 #pragma unroll
                         for (int k4 = 0; k4 < 4; ++k4)
-                            tc_mma(tmem + kOCol, smem_desc(sbase + hh * kPRegion + k4 * 32, 16, 1024),
-                                   smem_desc(vb + k4 * 2048, kVRegion, 1024), idesc_o,
+                            tc_mma(tmem + kOCol, dp + (k4 * 32 >> 4), dv + (k4 * 2048 >> 4), idesc_o,
                                    (n > 0 || hh > 0 || k4 > 0) ? 1u : 0u);
                         give();
                     }
