@@ -134,7 +134,7 @@ int row_map(DecodeMaps &maps, int &n_maps, const void *base, uint64_t rows, bool
             bool tile, int box_rows, int box_chunks) {
     if (rows == 0 || rows > (1ull << 31) || !aligned16(base)) return -1;
     if (tile ? (bytes8 ? ((box_rows != 16 && box_rows != 32) || box_chunks != 2)
-                       : ((box_rows != 16 && box_rows != 64 && box_rows != 128) || (box_chunks != 2 && box_chunks != 4)))
+                       : ((box_rows & 15) || box_rows < 16 || box_rows > 128 || (box_chunks & 3) > 2 || box_chunks < 1 || box_chunks > 4))
              : (box_rows != 16 || box_chunks != 1))
         return -1;
     RowMap m;

@@ -20,8 +20,10 @@
 // tiles) and one item's start and end would take as long as its tiles.
 //   warps 0-7   softmax: two threads a row, each on 64 of a tile's keys
 //   warps 8-11  edge: the next item's Q into tensor memory, this item's O out
-//   warp 12     issues the MMAs
-//   warps 13,14 fill one ring of six 32 KB slots with K and V by TMA
+//   warp 12     issues the S products, warp 15 the PV products (one thread for
+//               both kept the tensor pipe waiting while it waited on barriers
+//               and committed: 2.0 us a tile against XX)
+//   warps 13,14 fill a ring of six 16 KB slots each, K and V, by TMA
 // Per tile: S = Q K^T -> TMEM, P = softmax numerators in fp16 -> shared
 // memory, O += P V -> TMEM.  Q sits in TMEM (the S product's A operand), and
 // the next item's Q goes there while this item's last tile is in the softmax
@@ -40,23 +42,27 @@ constexpr int kRun = 16;             // rows of a run (sinks are padded to whole
 constexpr int kThreads = 512;
 constexpr int kSoftThreads = 256;
 constexpr int kEdgeThreads = 128;
-constexpr int kWarpMma = 12, kWarpK = 13, kWarpV = 14;
+constexpr int kWarpS = 12, kWarpV = 14, kWarpPv = 15;  // warp 13 fills the K ring
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kQCol = 0, kSCol = 128, kOCol = 256;
 constexpr int kKRegion = kN * 128;   // one 64-dim region of 128 K rows
-constexpr int kVRegion = 64 * 128;   // one 64-dim region of 64 V rows
-constexpr int kSlotBytes = 2 * kKRegion;  // a tile's K over 128 dims, or V of 64 keys
-constexpr int kSlots = 6;
+constexpr int kVKeys = 32;            // keys of a V slot
+constexpr int kVRegion = kVKeys * 128;  // one 64-dim region of its rows
+constexpr int kSlotBytes = kKRegion; // K of the tile's keys over 64 dims, or V of 32 keys
+constexpr int kSlots = 6;            // of each ring
 constexpr int kPRegion = kM * 128;   // 64 keys of the 128 P rows
-constexpr int kOffRing = 2 * kPRegion;
-constexpr int kOffRed = kOffRing + kSlots * kSlotBytes;   // [tile parity][half][row] bf16 row maxima
+constexpr int kOffK = 2 * kPRegion, kOffV = kOffK + kSlots * kSlotBytes;
+static_assert(4 * kVRegion == kSlotBytes, "a V slot is 32 keys of four regions");
+constexpr int kOffRed = kOffV + kSlots * kSlotBytes;   // [tile parity][half][row] bf16 row maxima
 constexpr int kOffSum = kOffRed + 2 * 2 * kM * 2;         // [half][row] float sums of an item
 constexpr int kOffMax = kOffSum + 2 * kM * 4;             // [row] bf16 maxima of an item
 constexpr int kOffBar = kOffMax + kM * 2;
 enum Bars {
-    kFull = 0,
-    kEmpty = kSlots,
-    kSFull = 2 * kSlots,  // S of a tile is in TMEM
+    kKFull = 0,            // a ring's slots: filled, and free again
+    kKEmpty = kSlots,
+    kVFull = 2 * kSlots,
+    kVEmpty = 3 * kSlots,
+    kSFull = 4 * kSlots,  // S of a tile is in TMEM
     kSEmpty,              // ... and has been read
     kPFull,               // P of a tile is in shared memory
     kODone,               // a tile's PV product is done
@@ -66,8 +72,8 @@ enum Bars {
     kOFree,               // ... and its O, sums and maxima have been read
     kSums,                // an item's sums and maxima are in shared memory
     kRed,                 // a tile's half-row maxima are in shared memory
-    kDrain,
-    kNumBars
+    kDrain,               // a failed issuer's products are done (S, PV)
+    kNumBars = kDrain + 2
 };
 constexpr int kSmem = kOffBar + kNumBars * 8 + 16;
 static_assert(kSmem <= 232448, "above the 227 KB a CTA may hold");
@@ -149,6 +155,12 @@ __device__ __forceinline__ Item item_at(const Common &c, const ChunkArgs &a, int
     return t;
 }
 
+// V slots of the tile of virtual keys v0 .. (keys past `total` have no weight;
+// a tile past it, all masked, takes one).
+__device__ __forceinline__ int v_slots(int v0, int total) {
+    return max(1, min(kN / kVKeys, (total - v0 + kVKeys - 1) / kVKeys));
+}
+
 // Gathered row of virtual key v of an item.
 __device__ __forceinline__ int row_of(const Gathered &g, const Keys &k, int v) {
     if (v < k.sink_end || g.win == g.lo) return v < k.sink_end ? v : k.lo + (v - k.sink_end);
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const int H = c.n_kv_heads, G = c.group;
     if (tid == 0) {
-        for (int i = 0; i < kSFull; ++i) mbar_init(&bars[i], 1);
+        for (int i = 0; i < kSFull; ++i) mbar_init(&bars[i], 1);  // both rings
         mbar_init(&bars[kSFull], 1);
         mbar_init(&bars[kSEmpty], kSoftThreads);
         mbar_init(&bars[kPFull], kSoftThreads);
@@ -200,13 +212,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars[kSums], kSoftThreads);
         mbar_init(&bars[kRed], kSoftThreads);
         mbar_init(&bars[kDrain], 1);
+        mbar_init(&bars[kDrain + 1], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     // tcgen05 alloc, dealloc, ld and st are warp-collective (.sync.aligned):
     // every one follows a __syncwarp, because a CTA barrier does not
     // reconverge a warp whose lanes took different paths before it
-    if (warp == kWarpMma) {
+    if (warp == kWarpS) {
         __syncwarp();
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
                      "r"(kTmemCols)
@@ -353,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (hf == 0) reinterpret_cast<uint16_t *>(smem + kOffMax)[r] = bf16_up(m_raw);
             mbar_arrive(&bars[kSums]);
         }
-    } else if (warp < kWarpMma) {
+    } else if (warp < kWarpS) {
         // ------- edge: Q into TMEM columns 0-127 (bf16 pairs), O out -------
         pdl_wait();
         const int r = lane + 32 * (warp & 3);
@@ -468,92 +481,99 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!finite && c.status) atomicOr(c.status, PKV_DEV_RANGE);
             t = t2;
         }
-    } else if (warp == kWarpMma) {
+    } else if (warp == kWarpS || warp == kWarpPv) {
         if (lane == 0) {
             // ---------------- MMA issue ----------------
             // operands written by threads (Q, P) were fenced by their writers
-            // before they arrived
-            const uint32_t idesc_s = mma_idesc(kN, false);
-            const uint32_t idesc_o = mma_idesc(kHeadDim, true, true);
+            // before they arrived.  A descriptor's address is its low 14 bits in
+            // units of 16 bytes, and shared memory ends below 256 KB: offsets
+            // are added to it.
             uint32_t q = 0, T = 0, it = 0;  // slots, tiles and items so far
             bool ok = true;
-            auto take = [&](uint32_t &addr) -> bool {
-                if (!wait(kFull + q % kSlots, q / kSlots)) return false;
+            auto take = [&](int full, int ring, uint32_t &addr) -> bool {
+                if (!wait(full + q % kSlots, q / kSlots)) return false;
                 tc_fence_after();
-                addr = sbase + kOffRing + (q % kSlots) * kSlotBytes;
+                addr = sbase + ring + (q % kSlots) * kSlotBytes;
                 return true;
             };
-            auto give = [&]() {
-                tc_commit(&bars[kEmpty + q % kSlots]);  // free once these MMAs are done
+            auto give = [&](int empty) {
+                tc_commit(&bars[empty + q % kSlots]);  // free once these MMAs are done
                 ++q;
             };
-            // a descriptor's address is its low 14 bits in units of 16 bytes, and
-            // shared memory ends below 256 KB: offsets are added to the low word
-            const uint64_t desc_k = smem_desc(0, 16, 1024), desc_v = smem_desc(0, kVRegion, 1024);
-            const uint64_t desc_p = smem_desc(sbase, 16, 1024);
-            auto issue_s = [&](uint32_t tile, bool last) -> bool {
-                if (tile > 0 && !wait(kSEmpty, tile - 1)) return false;
-                tc_fence_after();
-#pragma unroll 1
-                for (int hh = 0; hh < 2; ++hh) {
-                    uint32_t kb;
-                    if (!take(kb)) return false;
-                    const uint64_t dk = desc_k + (kb >> 4);
-#pragma unroll
-                    for (int k8 = 0; k8 < 8; ++k8)
-                        tc_mma_ts(tmem + kSCol, tmem + kQCol + (8 * hh + k8) * 8,
-                                  dk + (((k8 >> 2) * kKRegion + (k8 & 3) * 32) >> 4), idesc_s,
-                                  (hh > 0 || k8 > 0) ? 1u : 0u);
-                    give();
-                }
-                tc_commit(&bars[kSFull]);
-                if (last) tc_commit(&bars[kQEmpty]);
-                return true;
-            };
-            int ntiles = item_at(c, a, blockIdx.x).ntiles, next_tiles = 0;
-            for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x, ++it, ntiles = next_tiles) {
-                ok = wait(kQFull, it);
-                tc_fence_after();
-                if (ok) ok = issue_s(T, ntiles == 1);
-                // looked up here, while the first product runs
-                if (i + (int)gridDim.x < a.n_items) next_tiles = item_at(c, a, i + gridDim.x).ntiles;
-                for (int n = 0; ok && n < ntiles; ++n, ++T) {
-                    if (n + 1 < ntiles && !(ok = issue_s(T + 1, n + 2 == ntiles))) break;
-                    if (!(ok = wait(kPFull, T))) break;
-                    if (n == 0 && it > 0 && !(ok = wait(kOFree, it - 1))) break;
+            if (warp == kWarpS) {
+                const uint32_t idesc = mma_idesc(kN, false);
+                const uint64_t desc_k = smem_desc(0, 16, 1024);
+                int ntiles = item_at(c, a, blockIdx.x).ntiles, next_tiles = 0;
+                for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x, ++it, ntiles = next_tiles) {
+                    ok = wait(kQFull, it);
                     tc_fence_after();
-                    // O += P V over the tile's two key-half slots
+                    for (int n = 0; ok && n < ntiles; ++n, ++T) {
+                        if (T > 0 && !(ok = wait(kSEmpty, T - 1))) break;
+                        tc_fence_after();
+                        // S = Q K^T, 64 dims a slot
 #pragma unroll 1
-                    for (int hh = 0; hh < 2; ++hh) {
-                        uint32_t vb;
-                        if (!(ok = take(vb))) break;
-                        const uint64_t dp = desc_p + (hh * kPRegion >> 4), dv = desc_v + (vb >> 4);
+                        for (int qt = 0; qt < 4; ++qt) {
+                            uint32_t kb;
+                            if (!(ok = take(kKFull, kOffK, kb))) break;
+                            const uint64_t dk = desc_k + (kb >> 4);
 #pragma unroll
-                        for (int k4 = 0; k4 < 4; ++k4)
-                            tc_mma(tmem + kOCol, dp + (k4 * 32 >> 4), dv + (k4 * 2048 >> 4), idesc_o,
-                                   (n > 0 || hh > 0 || k4 > 0) ? 1u : 0u);
-                        give();
+                            for (int k4 = 0; k4 < 4; ++k4)
+                                tc_mma_ts(tmem + kSCol, tmem + kQCol + (4 * qt + k4) * 8, dk + (k4 * 32 >> 4), idesc,
+                                          (qt > 0 || k4 > 0) ? 1u : 0u);
+                            give(kKEmpty);
+                        }
+                        if (!ok) break;
+                        tc_commit(&bars[kSFull]);
+                        if (n + 1 == ntiles) tc_commit(&bars[kQEmpty]);
+                        // looked up here, while the first product runs
+                        if (n == 0 && i + (int)gridDim.x < a.n_items) next_tiles = item_at(c, a, i + gridDim.x).ntiles;
                     }
-                    if (!ok) break;
-                    tc_commit(&bars[kODone]);
-                    if (n + 1 == ntiles) tc_commit(&bars[kOLast]);
+                }
+            } else {
+                const uint32_t idesc = mma_idesc(kHeadDim, true, true);
+                const uint64_t desc_v = smem_desc(0, kVRegion, 1024), desc_p = smem_desc(sbase, 16, 1024);
+                Item t = item_at(c, a, blockIdx.x);
+                for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x, ++it) {
+                    const int ntiles = t.ntiles, key0 = t.key0, total = t.k.total;
+                    for (int n = 0; ok && n < ntiles; ++n, ++T) {
+                        const int nv = v_slots(key0 + n * kN, total);
+                        if (!(ok = wait(kPFull, T))) break;
+                        if (n == 0 && it > 0 && !(ok = wait(kOFree, it - 1))) break;
+                        tc_fence_after();
+                        // O += P V, 32 keys a slot
+#pragma unroll 1
+                        for (int vs = 0; vs < nv; ++vs) {
+                            uint32_t vb;
+                            if (!(ok = take(kVFull, kOffV, vb))) break;
+                            const uint64_t dp = desc_p + (((vs >> 1) * kPRegion + (vs & 1) * 64) >> 4), dv = desc_v + (vb >> 4);
+#pragma unroll
+                            for (int k2 = 0; k2 < 2; ++k2)
+                                tc_mma(tmem + kOCol, dp + (k2 * 32 >> 4), dv + (k2 * 2048 >> 4), idesc,
+                                       (n > 0 || vs > 0 || k2 > 0) ? 1u : 0u);
+                            give(kVEmpty);
+                        }
+                        if (!ok) break;
+                        tc_commit(&bars[kODone]);
+                        if (n + 1 == ntiles) tc_commit(&bars[kOLast]);
+                        if (n == 0 && i + (int)gridDim.x < a.n_items) t = item_at(c, a, i + gridDim.x);
+                    }
                 }
             }
             if (!ok) {  // no product is in flight when the tensor memory goes
-                tc_commit(&bars[kDrain]);
-                mbar_wait(&bars[kDrain], 0, nullptr);
+                const int drain = kDrain + (warp == kWarpPv);
+                tc_commit(&bars[drain]);
+                mbar_wait(&bars[drain], 0, nullptr);
             }
         }
-    } else if (warp == kWarpK || warp == kWarpV) {
-        // ------- producers: K slots (two halves of the dims) and V slots (two halves of the keys) -------
-        // The MMAs take an item's slots in the order K(0), then K(m), V(m-1)
-        // for m = 1 .., and V(last); each producer knows its places in it.
+    } else {
+        // ------- producers of K slots (64 dims each) and V slots (32 keys each) -------
         pdl_wait();
         const bool is_v = warp == kWarpV;
         const uint64_t pol = policy_evict_normal();  // neighbouring M-tiles read the same rows
         const void *const map = &maps.map[is_v ? a.map_v : a.map_k];
         const void *const map_run = &maps.map[a.map_run];
-        uint32_t q0 = 0;
+        const int full0 = is_v ? kVFull : kKFull, empty0 = is_v ? kVEmpty : kKEmpty, ring = is_v ? kOffV : kOffK;
+        uint32_t q = 0;
         bool ok = true;
         for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x) {
             const Item t = item_at(c, a, i);
@@ -564,38 +584,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (a split past the item's keys copies the first ones, all masked)
                 const int v0 = (t.key0 < t.k.total ? t.key0 : 0) + m * kN;
                 const bool mixed = v0 < t.k.sink_end && v0 + kN > t.k.sink_end;
-                auto row_at = [&](int v) { return base + row_of(g, t.k, v); };
-                for (int hh = 0; hh < 2; ++hh) {
-                    const uint32_t q = q0 + (is_v ? (m + 1 < t.ntiles ? 4 * m + 4 + hh : 4 * m + 2 + hh)
-                                                  : (m == 0 ? hh : 4 * m - 2 + hh));
+                const int n_slots = is_v ? v_slots(t.key0 + m * kN, t.k.total) : 4;
+                for (int j = 0; j < n_slots; ++j, ++q) {
                     const uint32_t slot = q % kSlots;
-                    if (q >= kSlots && !(ok = wait_warp(kEmpty + slot, q / kSlots - 1))) break;
-                    uint64_t *const full = &bars[kFull + slot];
-                    uint8_t *const dst = smem + kOffRing + slot * kSlotBytes;
+                    if (q >= kSlots && !(ok = wait_warp(empty0 + slot, q / kSlots - 1))) break;
+                    uint64_t *const full = &bars[full0 + slot];
+                    uint8_t *const dst = smem + ring + slot * kSlotBytes;
                     if (lane == 0) mbar_arrive_expect_tx(full, kSlotBytes);
                     __syncwarp();
                     if (!mixed) {
                         if (lane == 0) {
-                            if (is_v) tma_load_3d(dst, map, 0, row_at(v0 + 64 * hh), 0, full, pol);
-                            else tma_load_3d(dst, map, 0, row_at(v0), 2 * hh, full, pol);
+                            if (is_v) tma_load_3d(dst, map, 0, base + row_of(g, t.k, v0 + kVKeys * j), 0, full, pol);
+                            else tma_load_3d(dst, map, 0, base + row_of(g, t.k, v0), j, full, pol);
                         }
-                    } else if (lane < 16) {
+                    } else if (lane < 8) {
                         // the sinks' last tile: 16-row runs, one 64-dim box a lane
                         if (is_v) {
                             const int rn = lane >> 2, ch = lane & 3;
                             tma_load_2d(dst + ch * kVRegion + rn * 2048, map_run, 64 * ch,
-                                        row_at(v0 + 64 * hh + 16 * rn), full, pol);
+                                        base + row_of(g, t.k, v0 + kVKeys * j + 16 * rn), full, pol);
                         } else {
-                            const int rn = lane >> 1, ch = lane & 1;
-                            tma_load_2d(dst + ch * kKRegion + rn * 2048, map_run, 64 * (2 * hh + ch),
-                                        row_at(v0 + 16 * rn), full, pol);
+                            tma_load_2d(dst + lane * 2048, map_run, 64 * j, base + row_of(g, t.k, v0 + 16 * lane), full, pol);
                         }
                     }
                     __syncwarp();
                     last_q = static_cast<int>(q);
                 }
             }
-            q0 += 4 * t.ntiles;
         }
     }
 
@@ -605,8 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // (this producer's last slots; no later phase has been armed)
     if (*abort_flag)
         for (int k = last_q; k >= 0 && k > last_q - kSlots; --k)
-            mbar_wait(&bars[kFull + k % kSlots], (k / kSlots) & 1, nullptr);
-    if (warp == kWarpMma) {
+            mbar_wait(&bars[(warp == kWarpV ? kVFull : kKFull) + k % kSlots], (k / kSlots) & 1, nullptr);
+    if (warp == kWarpS) {
         __syncwarp();  // lane 0 issued the MMAs, lanes 1-31 went straight here
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
@@ -754,8 +769,8 @@ int launch_window_prefill(const Common &c, const DecodePlan &plan, int32_t windo
     // (the maps' type is bf16; a copy moves fp16 rows' bits unchanged)
     DecodeMaps maps;
     int n_maps = 0;
-    a.map_k = row_map(maps, n_maps, a.rows16, static_cast<uint64_t>(2 * rows), false, true, 128, 2);
-    a.map_v = row_map(maps, n_maps, a.rows16, static_cast<uint64_t>(2 * rows), false, true, 64, 4);
+    a.map_k = row_map(maps, n_maps, a.rows16, static_cast<uint64_t>(2 * rows), false, true, kN, 1);
+    a.map_v = row_map(maps, n_maps, a.rows16, static_cast<uint64_t>(2 * rows), false, true, kVKeys, 4);
     a.map_run = row_map(maps, n_maps, a.rows16, static_cast<uint64_t>(2 * rows), false);
     if (a.map_k < 0 || a.map_v < 0 || a.map_run < 0) return PKV_ECUDA;
     const int64_t warps = 2 * rows / kRun;
