@@ -274,25 +274,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int v0 = t.key0 + n * kN + 64 * hf;             // this thread's first virtual key
                 const int kp0 = v0 - t.k.sink_end + t.k.lo;            // its position, in the window's part
                 float x[64];
+#pragma unroll
+                for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(sv[j]);
                 const bool all = v0 >= t.k.sink_end
                                      ? kp0 + 63 <= qpos && (kp0 > win0 || kp0 + 63 < n_sink)
                                      : v0 + 63 < t.k.slim;
-                if (__all_sync(0xffffffffu, all)) {
-#pragma unroll
-                    for (int j = 0; j < 64; ++j) x[j] = __uint_as_float(sv[j]);
-                } else {
+                if (!__all_sync(0xffffffffu, all)) {
                     // one bit a key: the sinks' runs hold positions below slim,
                     // the window's part positions up to qpos that are in the
-                    // row's window or among the sinks (compared key by key this
-                    // took 3 to 4 us a tile, a fifth of a nine-tile item)
+                    // row's window or among the sinks.  Compared key by key this
+                    // took 3 to 4 us a tile, a fifth of a nine-tile item; 16 keys
+                    // that every row of the warp sees are left alone.
                     const uint64_t part = below(t.k.sink_end - v0);
                     const uint64_t see = (part & below(t.k.slim - v0)) |
                                          (~part & below(qpos - kp0 + 1) & (~below(win0 - kp0 + 1) | below(n_sink - kp0)));
-                    const uint32_t see0 = static_cast<uint32_t>(see), see1 = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        x[j] = (see0 >> j) & 1u ? __uint_as_float(sv[j]) : -INFINITY;
-                        x[j + 32] = (see1 >> j) & 1u ? __uint_as_float(sv[j + 32]) : -INFINITY;
+                    for (int j16 = 0; j16 < 4; ++j16) {
+                        const uint32_t m16 = static_cast<uint32_t>(see >> (16 * j16)) & 0xffffu;
+                        if (!__all_sync(0xffffffffu, m16 == 0xffffu)) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if (!(m16 & (1u << j))) x[16 * j16 + j] = -INFINITY;
+                        }
                     }
                 }
                 // this half's max as eight interleaved chains, then the row's
