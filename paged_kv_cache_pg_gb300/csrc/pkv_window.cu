@@ -35,15 +35,16 @@ constexpr int kMaxPieces = 8;           // pieces of a split
 constexpr int kMaxSlices = 4;           // key slices of a CTA
 constexpr int kSplitKeys = 640;              // keys of a piece at most
 constexpr int kMaxPages = kMaxPieces * kSplitKeys / 4 + 4;  // pages a CTA's run can touch
-// CTAs of a call up to which a split's CTAs are clustered (two fill an SM).
-// Past it a cluster waits for eight free places on neighbouring SMs while
-// other places stand empty: 64 streams of 4,096-key windows took 116 us
-// clustered and XX us as single CTAs with a combine kernel; four streams of
-// 1,024-key windows YY us clustered and ZZ us with the second kernel.
-#ifndef PKV_WINDOW_CLUSTER_CTAS
-#define PKV_WINDOW_CLUSTER_CTAS 304
-#endif
-constexpr int kClusterCtas = PKV_WINDOW_CLUSTER_CTAS;
+// bf16 calls of more CTAs than this (two fill an SM) run them unclustered, each
+// on one to eight pieces, and merge in a second kernel: a cluster waits for
+// eight free places on neighbouring SMs, and each CTA starts and merges anew.
+// Measured, clustered against unclustered, windows of 512 keys: 32 streams (512
+// CTAs) 18.4 us against 14.6, 48 streams 27.4 against 23.3, 16 streams (256
+// CTAs) 9.4 against 11.0; of 4,096 keys: 24 streams 43.9 us against 37.9, 64
+// streams 98.5 against 97, 16 streams 24.1 against 26.7.  e4m3 calls are bound
+// by their conversions instead and stay clustered (32 streams of 4,096 keys
+// 43.8 us against 45.2).
+constexpr int kClusterCtas = 304;
 constexpr int kFreshGuard = 32;              // see decode_partial: rows a kernel just before may write
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
 
@@ -1065,7 +1066,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
         floats = (floats + 63) / 64 * 64;
     }
     if (items * pieces > INT32_MAX) return PKV_EINVAL;
-    const bool combine = pieces > 1 && (split || items * pieces > kClusterCtas);
+    const bool combine = pieces > 1 && (split || (!c.kv_fp8 && items * pieces > kClusterCtas));
     plan->total_items = static_cast<int32_t>(items);
     plan->total_comb = combine ? static_cast<int32_t>(cols) : 0;
     plan->ws_bytes = combine ? static_cast<size_t>(floats) * 4 : 0;
@@ -1099,9 +1100,19 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
             if (c.seq[s].work_off != s * a.even) a.even = 0;
     }
     const bool clustered = plan.total_comb == 0;
-    // one wave of CTAs where the pieces allow it
-    if (!clustered)
-        for (a.run = 1; a.run < a.pieces && (int64_t)plan.total_items * a.pieces / a.run > kClusterCtas;) a.run *= 2;
+    // pieces of a CTA: the least of waves x (pieces + half a piece's time to
+    // start), the larger run where two are alike
+    if (!clustered) {
+        const int64_t ctas = (int64_t)plan.total_items * a.pieces;
+        int64_t best = INT64_MAX;
+        for (int run = 1; run <= a.pieces; run *= 2) {
+            const int64_t cost = ((ctas / run + kClusterCtas - 1) / kClusterCtas) * (2 * run + 1);
+            if (cost <= best) {
+                best = cost;
+                a.run = run;
+            }
+        }
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(plan.total_items) * (a.pieces / std::max(1, a.run)));
     cfg.blockDim = dim3(c.kv_fp8 ? Cfg<true>::threads : Cfg<false>::threads);

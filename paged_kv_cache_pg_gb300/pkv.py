@@ -203,6 +203,8 @@ def _host_i32(a):
         _np = numpy
     if type(a) is not _np.ndarray or a.dtype != _np.int32 or not a.flags.c_contiguous:
         a = _np.ascontiguousarray(a, dtype=_np.int32)
+    if a.flags.writeable and a.size:  # the cheaper way to its address
+        return a, ctypes.addressof(ctypes.c_char.from_buffer(a))
     return a, a.__array_interface__["data"][0]
 
 
