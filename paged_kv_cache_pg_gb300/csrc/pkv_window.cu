@@ -30,7 +30,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kMaxCols = 32;                 // query columns of one unit
+constexpr int kMaxCols = 32;                 // query columns of a (stream, KV head)
+constexpr int kBlockCols = 16;               // ... of a CTA
 constexpr int kMaxPieces = 8;           // pieces of a split
 constexpr int kMaxSlices = 4;           // key slices of a CTA
 constexpr int kSplitKeys = 640;              // keys of a piece at most
@@ -48,6 +49,7 @@ constexpr int kClusterCtas = 304;
 constexpr int kFreshGuard = 32;              // see decode_partial: rows a kernel just before may write
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
 
+constexpr int kJoinBytes = 8192;             // O of a warp's 8 columns, in its registers' layout
 constexpr int kPlane = 2048;                 // bf16: one 64-dim chunk of 16 rows
 
 // Shapes of the two page formats' CTAs: four consumer warps, each on a tile (and
@@ -67,15 +69,17 @@ struct Cfg {
     static constexpr int row = kFp8 ? kHeadDim + 12 : kHeadDim + 4;  // floats of a merge row
     static constexpr int off_scl = slots * stage;                // e4m3: 32 K and 32 V scales a stage
     static constexpr int off_page = off_scl + (kFp8 ? slots * 256 : 0);
-    static constexpr int off_bar = off_page + kMaxPages * 8;
+    static constexpr int off_join = off_page + kMaxPages * 4;    // a piece's slices: 8 KB of O, then (m, l)
+    static constexpr int off_join_ml = off_join + kJoinBytes;
+    static constexpr int off_bar = off_join_ml + kMaxSlices * kBlockCols * 8;
     static constexpr int bytes = off_bar + 2 * slots * 8 + 16;
     static constexpr int smem = bytes + 1024;                    // with alignment slack
     // after the last tile the stages hold the merge rows, then the CTA's sum
     static constexpr int off_ml = 32 * row * 4;
     static constexpr int off_sum = (off_ml + 32 * 8 + 127) / 128 * 128;
-    static constexpr int off_sum_ml = off_sum + kMaxCols * kHeadDim * 4;
-    static_assert(off_sum_ml + kMaxCols * 8 <= slots * stage, "merge buffers reuse the stages");
-    static_assert(off_page % 8 == 0 && off_bar % 8 == 0, "aligned");
+    static constexpr int off_sum_ml = off_sum + kBlockCols * kHeadDim * 4;
+    static_assert(off_sum_ml + kBlockCols * 8 <= slots * stage, "merge buffers reuse the stages");
+    static_assert(off_join % 16 == 0 && off_bar % 8 == 0, "aligned");
 };
 
 struct WinArgs {
@@ -91,9 +95,12 @@ struct WinArgs {
     int32_t even;       // splits of each stream where all have as many, else 0
 };
 
+// CTAs that share a (stream, KV head)'s columns.
+__host__ __device__ inline int col_blocks(int ncols) { return (ncols + kBlockCols - 1) / kBlockCols; }
+
 // Key slices of a CTA (tiles it works on at once): a divisor of its slots.
 __host__ __device__ inline int slices_of(bool fp8, int ncols) {
-    const int ncg = (ncols + 7) >> 3, slots = fp8 ? Cfg<true>::slots : Cfg<false>::slots;
+    const int ncg = ((ncols < kBlockCols ? ncols : kBlockCols) + 7) >> 3, slots = fp8 ? Cfg<true>::slots : Cfg<false>::slots;
     int n = kConsumers / ncg;
     while (slots % n) --n;
     return n;
@@ -126,6 +133,11 @@ __device__ __forceinline__ float2 peer_ld2(uint32_t a) {
     float2 v;
     asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
     return v;
+}
+
+// The active consumer warps of a CTA meet (n threads).
+__device__ __forceinline__ void join_sync(int n) {
+    asm volatile("bar.sync 1, %0;" ::"r"(n) : "memory");
 }
 
 // ---- small helpers --------------------------------------------------------------
@@ -185,6 +197,7 @@ __device__ __forceinline__ void split_scale(float s, float &e, float &mant) {
 struct Run {
     WindowSpan sp;
     int s, kvh, split;
+    int col0;              // its first query column
     int piece, n_pieces;   // its pieces of the split
     int key0, key1;        // their virtual keys
     int per;               // tiles of a piece
@@ -201,8 +214,10 @@ __device__ __forceinline__ Run locate(const Common &c, const WinArgs &a) {
     u.s = a.even ? item / a.even : find_seq(c.n_seqs, item, [&](int t) { return c.seq[t].work_off; });
     const SeqDev &sd = c.seq[u.s];
     const int r = a.even ? item - u.s * a.even : item - sd.work_off;
-    u.kvh = r / sd.nsplit;
-    u.split = r - u.kvh * sd.nsplit;
+    const int blocks = col_blocks(sd.ncols), q = r / blocks;
+    u.col0 = (r - q * blocks) * kBlockCols;
+    u.kvh = q / sd.nsplit;
+    u.split = q - u.kvh * sd.nsplit;
     u.piece = (b - item * per_split) * u.n_pieces;
     u.sp = window_span(sd.len, sd.n_new, a.window, a.n_sink, kTile);
     u.per = sd.split_len / kTile;
@@ -237,7 +252,7 @@ __device__ __forceinline__ int pos_of(const WindowSpan &sp, int v) {
 struct Ctx {
     uint8_t *stages;
     float *scl;          // e4m3: [slot][2][32] K then V scales
-    int64_t *pages;      // offsets of the run's pages (-1: outside the arena)
+    int32_t *pages;      // ids of the run's pages (-1: outside the arena)
     uint64_t *full, *empty;
     volatile int *abort_flag;
 };
@@ -267,12 +282,10 @@ __device__ __forceinline__ KeySrc key_src(const SeqDev &sd, const WinArgs &a, co
     if (sd.table) {
         const int page = k.pos / sd.ptok;
         k.row = k.pos - page * sd.ptok;
-        k.page = x.pages[min(v, u.key1 - 1) < u.sp.sink_end ? page - u.sink_page
-                                                           : u.n_sink_pages + page - u.win_page];
-        if (k.page < 0) {
-            k.bad = true;
-            k.page = 0;
-        }
+        const int id = x.pages[min(v, u.key1 - 1) < u.sp.sink_end ? page - u.sink_page
+                                                                  : u.n_sink_pages + page - u.win_page];
+        k.bad = id < 0;
+        k.page = max(id, 0) * sd.ps;
     }
     k.fresh = a.k_new != nullptr && k.pos >= u.qbase;
     return k;
@@ -307,7 +320,7 @@ __device__ __forceinline__ void stage16(const Common &c, const WinArgs &a, const
     cp_async_mbar_arrive(bar);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    unsigned todo = __ballot_sync(0xffffffffu, k.fresh && k.seen && !k.bad && lane < 16);
+    unsigned todo = __ballot_sync(0xffffffffu, k.fresh && k.seen && !k.bad && lane < 16 && u.col0 == 0);
     while (todo) {
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
@@ -369,7 +382,7 @@ __device__ __forceinline__ void stage8(const Common &c, const WinArgs &a, const 
             continue;
         }
         const int p = __shfl_sync(0xffffffffu, k.pos, rr), row = __shfl_sync(0xffffffffu, k.row, rr);
-        const bool write = !__shfl_sync(0xffffffffu, k.bad, rr);
+        const bool write = u.col0 == 0 && !__shfl_sync(0xffffffffu, k.bad, rr);
         const int64_t pg_rr = shfl64(pg, rr);
         const int64_t tr = (int64_t)sd.tok_off + (p - u.qbase);  // its packed input row
         const bool ik_row = write && u.kvh == 0 && a.ik_new != nullptr && lane < c.idx_dim / 8;
@@ -452,7 +465,7 @@ __device__ __forceinline__ bool sees(int p, int kp, int window, int n_sink) {
     return kp <= p && (kp > p - window || kp < n_sink);
 }
 
-template <bool kFp8>
+template <bool kFp8, bool kRuns>
 __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     window_partial(const __grid_constant__ Common c, const __grid_constant__ DecodeMaps maps,
                    const __grid_constant__ WinArgs a) {
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     Ctx x;
     x.stages = smem;
     x.scl = reinterpret_cast<float *>(smem + F::off_scl);
-    x.pages = reinterpret_cast<int64_t *>(smem + F::off_page);
+    x.pages = reinterpret_cast<int32_t *>(smem + F::off_page);
     x.full = reinterpret_cast<uint64_t *>(smem + F::off_bar);
     x.empty = x.full + F::slots;
     x.abort_flag = reinterpret_cast<volatile int *>(x.empty + F::slots);
@@ -472,7 +485,8 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     const Run u = locate<F::tile>(c, a);
     const SeqDev &sd = c.seq[u.s];
     const int ncols = sd.ncols, G = c.group, H = c.n_kv_heads;
-    const int ncg = (ncols + 7) >> 3;           // column groups of 8
+    const int nc = min(ncols - u.col0, kBlockCols);  // this CTA's columns
+    const int ncg = (nc + 7) >> 3;                   // in groups of 8
     // Tiles at once.  A piece's tile t belongs to key slice t % ks_n, and a
     // piece takes whole rounds of the slices (empty tiles fill its last one),
     // so each slot always belongs to one slice, which takes every phase of its
@@ -480,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     // its own, not landed yet, from its own: both leave the same parity.)
     const int ks_n = slices_of(kFp8, ncols);
     const int round = (u.per + ks_n - 1) / ks_n * ks_n;  // a piece's tiles, empty ones among them
-    const int ntiles = a.run > 0 || u.key1 > u.key0 ? u.n_pieces * round : 0;
+    const int ntiles = kRuns || u.key1 > u.key0 ? u.n_pieces * round : 0;
     const int cg = warp % ncg, ks = warp / ncg;
     const bool active = warp < F::consumers && ks < ks_n;
 
@@ -500,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         const int id = __ldg(sd.table + p);
         const bool ok = static_cast<uint32_t>(id) < static_cast<uint32_t>(sd.n_pages);
         if (!ok && c.status) atomicOr(c.status, PKV_DEV_BAD_PAGE);
-        x.pages[j] = ok ? (int64_t)id * sd.ps : -1;
+        x.pages[j] = ok ? id : -1;
     }
     __syncthreads();
     // nothing this CTA writes is read by the next kernel before its own wait
@@ -543,8 +557,8 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                         if (sd.table) {
                             const int page = p / sd.ptok;
                             row = p - page * sd.ptok;
-                            pg = x.pages[v0 < u.sp.sink_end ? page - u.sink_page : u.n_sink_pages + page - u.win_page];
-                            if (pg < 0) pg = 0;  // reported when it was looked up
+                            const int id = x.pages[v0 < u.sp.sink_end ? page - u.sink_page : u.n_sink_pages + page - u.win_page];
+                            pg = max(id, 0) * sd.ps;  // (-1 was reported when it was looked up)
                         }
                         if constexpr (kFp8) {
                             y = static_cast<int>(sd.layer_row + (2 * pg + off8_code(false, H, sd.ptok, u.kvh, row)) / kHeadDim);
@@ -612,7 +626,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     } else if (active) {
         // ---------------- consumers ----------------
         const int g = lane >> 2, c4 = lane & 3;
-        const int bcol = cg * 8 + g;
+        const int bcol = u.col0 + cg * 8 + g;
         const uint16_t *qr = nullptr;
         if (bcol < ncols) {
             const int j = bcol / G;
@@ -643,7 +657,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             }
         }
         // the positions of this lane's two columns (-1: padding)
-        const int c0 = cg * 8 + 2 * c4;
+        const int c0 = u.col0 + cg * 8 + 2 * c4;
         const int p0 = c0 < ncols ? u.qbase + c0 / G : -1;
         const int p1 = c0 + 1 < ncols ? u.qbase + (c0 + 1) / G : -1;
         const uint32_t s_base = smem_u32(x.stages);
@@ -652,9 +666,12 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         float uo[2] = {-INFINITY, -INFINITY};  // e4m3: O's own reference (logit + V-scale exponent)
 
         // A piece's sums are complete: l over the key rows, O on the logits'
-        // maximum.  They stay in registers for the cluster's merge, or go to
-        // the workspace, O [slice of the unit][column][256], then (m, l), and
-        // the next piece starts anew.
+        // maximum.  They stay in registers for the cluster's merge, or the
+        // piece's slices join into slice 0's (as merge_parts would), which go
+        // to the workspace, O [piece of the unit][column][256], then (m, l),
+        // and the next piece starts anew.  The slices hand O over lane by lane,
+        // 8 KB at a time; written out one by one they are two or three times
+        // the traffic (64 streams of 4,096 keys 99.0 us against 92.3).
         auto finish_piece = [&](int pc) {
             l[0] = sum_rows(l[0]);
             l[1] = sum_rows(l[1]);
@@ -669,24 +686,83 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                     acc[i][3] *= f1;
                 }
             }
-            if (a.run == 0) return;
-            const int64_t n_part = (int64_t)sd.nsplit * a.pieces * ks_n;  // of a unit
-            const int64_t part = u.kvh * n_part + (int64_t)(u.split * a.pieces + u.piece + pc) * ks_n + ks;
-            float *o = a.ws + sd.ws_off + (part * ncols + c0) * kHeadDim;
-            float *ml = a.ws + sd.ws_off + (int64_t)H * n_part * ncols * kHeadDim + (part * ncols + c0) * 2;
+            if constexpr (!kRuns) return;
+            const int cl = cg * 8 + 2 * c4;  // this lane's first column in the CTA
+            float4 *const jml = reinterpret_cast<float4 *>(smem + F::off_join_ml);  // [slice][two columns]
+            float4 *const jo = reinterpret_cast<float4 *>(smem + F::off_join) + cg * 8 * 32 + lane;
+            if (g == 0) jml[(ks * kBlockCols + cl) / 2] = make_float4(m[0], l[0], m[1], l[1]);
+            join_sync(ncg * ks_n * 32);
+            if (ks == 0) {
+                const float4 own = make_float4(m[0], l[0], m[1], l[1]);
+                for (int k = 1; k < ks_n; ++k) {
+                    const float4 ml = jml[(k * kBlockCols + cl) / 2];
+                    m[0] = fmaxf(m[0], ml.x);
+                    m[1] = fmaxf(m[1], ml.z);
+                }
+                const float w0 = m[0] == -INFINITY ? 0.f : ex2(own.x - m[0]);
+                const float w1 = m[1] == -INFINITY ? 0.f : ex2(own.z - m[1]);
+                l[0] = fmaf(w0, own.y, 0.f);
+                l[1] = fmaf(w1, own.w, 0.f);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                if (c0 + e < ncols) {
+                for (int i = 0; i < 16; ++i) {
+                    acc[i][0] = fmaf(w0, acc[i][0], 0.f);
+                    acc[i][1] = fmaf(w1, acc[i][1], 0.f);
+                    acc[i][2] = fmaf(w0, acc[i][2], 0.f);
+                    acc[i][3] = fmaf(w1, acc[i][3], 0.f);
+                }
+            }
+            for (int k = 1; k < ks_n; ++k) {
+                float w0 = 0.f, w1 = 0.f;
+                if (ks == 0) {
+                    const float4 ml = jml[(k * kBlockCols + cl) / 2];
+                    w0 = m[0] == -INFINITY ? 0.f : ex2(ml.x - m[0]);
+                    w1 = m[1] == -INFINITY ? 0.f : ex2(ml.z - m[1]);
+                    l[0] = fmaf(w0, ml.y, l[0]);
+                    l[1] = fmaf(w1, ml.w, l[1]);
+                }
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        if constexpr (kFp8) {
-                            *reinterpret_cast<float2 *>(o + e * kHeadDim + 32 * g + 2 * i) = make_float2(acc[i][e], acc[i][e + 2]);
-                        } else {
-                            o[e * kHeadDim + 16 * i + g] = acc[i][e];
-                            o[e * kHeadDim + 16 * i + g + 8] = acc[i][e + 2];
+                for (int h = 0; h < 2; ++h) {  // 8 tiles of 16 dims at a time
+                    if (k > 1 || h > 0) join_sync(ncg * ks_n * 32);  // the part before has been read
+                    if (ks == k) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float(&t)[4] = acc[8 * h + i];
+                            jo[i * 32] = make_float4(t[0], t[1], t[2], t[3]);
                         }
                     }
-                    if (g == 0) *reinterpret_cast<float2 *>(ml + 2 * e) = make_float2(m[e], l[e]);
+                    join_sync(ncg * ks_n * 32);
+                    if (ks == 0) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float4 v = jo[i * 32];
+                            float(&t)[4] = acc[8 * h + i];
+                            t[0] = fmaf(w0, v.x, t[0]);
+                            t[1] = fmaf(w1, v.y, t[1]);
+                            t[2] = fmaf(w0, v.z, t[2]);
+                            t[3] = fmaf(w1, v.w, t[3]);
+                        }
+                    }
+                }
+            }
+            if (ks == 0) {
+                const int64_t n_part = (int64_t)sd.nsplit * a.pieces;  // of a unit
+                const int64_t part = u.kvh * n_part + u.split * a.pieces + u.piece + pc;
+                float *o = a.ws + sd.ws_off + (part * ncols + c0) * kHeadDim;
+                float *ml = a.ws + sd.ws_off + (int64_t)H * n_part * ncols * kHeadDim + (part * ncols + c0) * 2;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (c0 + e < ncols) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if constexpr (kFp8) {
+                                *reinterpret_cast<float2 *>(o + e * kHeadDim + 32 * g + 2 * i) = make_float2(acc[i][e], acc[i][e + 2]);
+                            } else {
+                                o[e * kHeadDim + 16 * i + g] = acc[i][e];
+                                o[e * kHeadDim + 16 * i + g + 8] = acc[i][e + 2];
+                            }
+                        }
+                        if (g == 0) *reinterpret_cast<float2 *>(ml + 2 * e) = make_float2(m[e], l[e]);
+                    }
                 }
             }
             m[0] = m[1] = uo[0] = uo[1] = -INFINITY;
@@ -695,10 +771,11 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         };
 
-        const int n_pieces = ntiles > 0 ? u.n_pieces : 0;
+        const int n_pieces = kRuns ? u.n_pieces : ntiles > 0 ? 1 : 0;
         bool ok = true;
-        for (int pc = 0; ok && pc < n_pieces; ++pc) {
-        for (int tp = ks; tp < round; tp += ks_n) {
+        // (after a wait that ran out the warp still meets the others at each piece's end)
+        for (int pc = 0; pc < n_pieces; ++pc) {
+        for (int tp = ks; ok && tp < round; tp += ks_n) {
             const int t = pc * round + tp, slot = t % S;
             ok = __all_sync(0xffffffffu, mbar_wait(&x.full[slot], (t / S) & 1, c.status));
             if (!ok) {
@@ -908,13 +985,13 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     // after a wait that ran out, every copy issued lands before the memory goes
     if (failed)
         for (int j = max(0, issued - S); j < issued; ++j) mbar_wait(&x.full[j % S], (j / S) & 1, nullptr);
-    if (a.run > 0) return;  // window_combine merges the slices and pieces
+    if (kRuns) return;  // window_combine merges the slices and pieces
 
     // ---- merge the CTA's key slices, in order ----
     const int NC = ncg * 8;
     float *mbuf = reinterpret_cast<float *>(x.stages);               // [ks][NC][row]
     float *mlb = reinterpret_cast<float *>(x.stages + F::off_ml);    // [ks][NC][2]
-    float *sum = reinterpret_cast<float *>(x.stages + F::off_sum);   // [ncols][256]
+    float *sum = reinterpret_cast<float *>(x.stages + F::off_sum);   // [nc][256]
     float *sum_ml = reinterpret_cast<float *>(x.stages + F::off_sum_ml);
     if (active && !failed) {
         const int g = lane >> 2, c0 = cg * 8 + 2 * (lane & 3);
@@ -947,7 +1024,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         }
     }
     __syncthreads();
-    for (int idx = tid; idx < ncols * (kHeadDim / 4); idx += F::threads) {
+    for (int idx = tid; idx < nc * (kHeadDim / 4); idx += F::threads) {
         const int col = idx / (kHeadDim / 4), d = 4 * (idx - col * (kHeadDim / 4));
         const int ds = kFp8 ? d + (d >> 5) : d;
         const Sum r = merge_parts<kMaxSlices>(
@@ -962,22 +1039,22 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     // ---- then the cluster's CTAs, in order ----
     cluster_sync();
     if (!failed) {
-        for (int idx = u.piece * F::threads + tid; idx < ncols * (kHeadDim / 4); idx += a.pieces * F::threads) {
+        for (int idx = u.piece * F::threads + tid; idx < nc * (kHeadDim / 4); idx += a.pieces * F::threads) {
             const int col = idx / (kHeadDim / 4), d = 4 * (idx - col * (kHeadDim / 4));
             const Sum r = merge_parts<kMaxPieces>(
                 a.pieces, [&](int k) { return peer_ld2(peer_addr(sum_ml + 2 * col, k)); },
                 [&](int k) { return peer_ld4(peer_addr(sum + col * kHeadDim + d, k)); });
-            const int j = col / G;
-            write_out(a.out + (((int64_t)sd.tok_off + j) * c.n_q_heads + u.kvh * G + (col - j * G)) * kHeadDim + d, r);
+            const int j = (u.col0 + col) / G, h = u.col0 + col - j * G;
+            write_out(a.out + (((int64_t)sd.tok_off + j) * c.n_q_heads + u.kvh * G + h) * kHeadDim + d, r);
         }
     }
     cluster_sync();  // the peers have read this CTA's sums
 }
 
-// Merge of the slices' partials for calls whose CTAs are not clustered: a CTA a
-// query column, four groups of 64 threads (four dims each) that take every
-// fourth piece; a piece's slices, the split's pieces and the splits in order,
-// as a clustered CTA and its cluster merge them.
+// Merge of the pieces' partials for calls whose CTAs are not clustered: a CTA a
+// query column, four groups of 64 threads (four dims each) that load every
+// fourth piece; the split's pieces and the splits in order, as a cluster merges
+// its CTAs' sums.
 constexpr int kCombThreads = 256;
 __global__ void __launch_bounds__(kCombThreads)
     window_combine(const __grid_constant__ Common c, const __grid_constant__ WinArgs a) {
@@ -989,8 +1066,7 @@ __global__ void __launch_bounds__(kCombThreads)
     const SeqDev &sd = c.seq[s];
     const int r = i - sd.comb_off, ncols = sd.ncols, unit = r / ncols, col = r - unit * ncols, G = c.group;
     const int grp = threadIdx.x >> 6, d4 = threadIdx.x & 63, d = 4 * d4, j = col / G;
-    const int ks_n = slices_of(c.kv_fp8 != 0, ncols);
-    const int64_t n_part = (int64_t)sd.nsplit * a.pieces * ks_n;
+    const int64_t n_part = (int64_t)sd.nsplit * a.pieces;
     const float *acc = a.ws + sd.ws_off + (unit * n_part * ncols + col) * kHeadDim + d;
     const float *ml = a.ws + sd.ws_off + (int64_t)c.n_kv_heads * n_part * ncols * kHeadDim + (unit * n_part * ncols + col) * 2;
     uint16_t *out = a.out + (((int64_t)sd.tok_off + j) * c.n_q_heads + unit * G + (col - j * G)) * kHeadDim + d;
@@ -999,12 +1075,9 @@ __global__ void __launch_bounds__(kCombThreads)
     Sum t;
     for (int sp = 0; sp < sd.nsplit; ++sp) {
         for (int p = grp; p < a.pieces; p += kCombThreads / 64) {
-            const int64_t p0 = (int64_t)(sp * a.pieces + p) * ks_n;
-            const Sum x = merge_parts<kMaxSlices>(
-                ks_n, [&](int k) { return __ldcg(reinterpret_cast<const float2 *>(ml + (p0 + k) * ncols * 2)); },
-                [&](int k) { return __ldcg(reinterpret_cast<const float4 *>(acc + (p0 + k) * ncols * kHeadDim)); });
-            sh_o[p][d4] = x.o;
-            if (d4 == 0) sh_ml[p] = make_float2(x.m, x.l);
+            const int64_t p0 = (int64_t)sp * a.pieces + p;
+            sh_o[p][d4] = __ldcg(reinterpret_cast<const float4 *>(acc + p0 * ncols * kHeadDim));
+            if (d4 == 0) sh_ml[p] = __ldcg(reinterpret_cast<const float2 *>(ml + p0 * ncols * 2));
         }
         __syncthreads();
         if (grp == 0) {
@@ -1060,9 +1133,9 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
         const int per = (sp.nkeys - 1) / (d.nsplit * pieces) + 1;  // keys of a piece
         d.split_len = (per + tile - 1) / tile * tile;
         split |= d.nsplit > 1;
-        items += (int64_t)c.n_kv_heads * d.nsplit;
+        items += (int64_t)c.n_kv_heads * d.nsplit * col_blocks(d.ncols);
         cols += (int64_t)c.n_kv_heads * d.ncols;
-        floats += (int64_t)c.n_kv_heads * d.nsplit * pieces * slices_of(c.kv_fp8 != 0, d.ncols) * d.ncols * (kHeadDim + 2);
+        floats += (int64_t)c.n_kv_heads * d.nsplit * pieces * d.ncols * (kHeadDim + 2);
         floats = (floats + 63) / 64 * 64;
     }
     if (items * pieces > INT32_MAX) return PKV_EINVAL;
@@ -1078,10 +1151,12 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
                   const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     if (once_per_device(attr_done, [] {
-            const void *fns[] = {reinterpret_cast<const void *>(window_partial<false>),
-                                 reinterpret_cast<const void *>(window_partial<true>)};
-            const int bytes[] = {Cfg<false>::smem, Cfg<true>::smem};
-            for (int i = 0; i < 2; ++i) {
+            const void *fns[] = {reinterpret_cast<const void *>(window_partial<false, false>),
+                                 reinterpret_cast<const void *>(window_partial<false, true>),
+                                 reinterpret_cast<const void *>(window_partial<true, false>),
+                                 reinterpret_cast<const void *>(window_partial<true, true>)};
+            const int bytes[] = {Cfg<false>::smem, Cfg<false>::smem, Cfg<true>::smem, Cfg<true>::smem};
+            for (int i = 0; i < 4; ++i) {
                 if (cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]) != cudaSuccess)
                     return PKV_ECUDA;
                 if (cudaFuncSetAttribute(fns[i], cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -1126,7 +1201,9 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, c.kv_fp8 ? window_partial<true> : window_partial<false>, c, maps, a) != cudaSuccess)
+    auto *const fn = c.kv_fp8 ? (clustered ? window_partial<true, false> : window_partial<true, true>)
+                              : (clustered ? window_partial<false, false> : window_partial<false, true>);
+    if (cudaLaunchKernelEx(&cfg, fn, c, maps, a) != cudaSuccess)
         return PKV_ECUDA;
     if (clustered) return PKV_OK;
     return launch_status(
