@@ -515,7 +515,7 @@ extern "C" int pkv_decode_static(const pkv_layout *L, const pkv_seq *seqs, int32
 
 static int window_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
                          int32_t n_q_heads, int32_t window, int32_t n_sink, int32_t *dev_status,
-                         Common *c, DecodePlan *plan) {
+                         Common *c, WindowPlan *plan) {
     int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, c);
     if (rc) return rc;
     if (window < 1 || n_sink < 0) return PKV_EINVAL;
@@ -527,7 +527,7 @@ extern "C" int pkv_window_decode_ws_size(const pkv_layout *L, const pkv_seq *seq
                                          size_t *bytes) {
     if (!bytes) return PKV_EINVAL;
     Common c;
-    DecodePlan plan;
+    WindowPlan plan;
     int rc = window_common(L, seqs, n_seqs, 0, n_q_heads, window, n_sink, nullptr, &c, &plan);
     if (rc) return rc;
     *bytes = plan.ws_bytes;
@@ -540,10 +540,10 @@ extern "C" int pkv_window_decode(const pkv_layout *L, const pkv_seq *seqs, int32
                                  const void *ik_new, void *out, void *ws, size_t ws_bytes,
                                  int32_t *dev_status, cudaStream_t stream) {
     Common c;
-    DecodePlan plan;
+    WindowPlan plan;
     int rc = window_common(L, seqs, n_seqs, layer, n_q_heads, window, n_sink, dev_status, &c, &plan);
     if (rc) return rc;
-    if (plan.total_items == 0) return PKV_OK;
+    if (plan.items == 0) return PKV_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out)) return PKV_EINVAL;
     if ((k_new == nullptr) != (v_new == nullptr)) return PKV_EINVAL;
     if (k_new) {

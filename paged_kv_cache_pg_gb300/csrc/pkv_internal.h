@@ -233,15 +233,24 @@ int launch_decode8(const Common &c, const DecodePlan &plan, const DecodeMaps &ma
                    const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
                    const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 
-// Windowed decode (pkv_window.cu): CTAs that share a split, plan and launch.
-int window_pieces(int32_t window, int32_t n_sink);
-int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan);
+// Windowed decode (pkv_window.cu): plan and launch.
+struct WindowPlan {
+    int32_t items;      // (stream, KV head, split, column block)s
+    int32_t pieces;     // pieces of a split
+    int32_t run;        // pieces of a CTA; 0: one, and a split's CTAs are a cluster
+    int32_t ctas;       // CTAs of the partial kernel
+    int32_t comb;       // CTAs of the combine kernel (run > 0)
+    bool wide;          // a CTA takes all of a KV head's columns
+    int64_t stash_off;  // floats of partials in the workspace, before the stash
+    size_t ws_bytes;
+};
+int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan);
 // Row maps of the streams (in tma): 3D boxes of 16 whole bf16 rows, or of 32
 // code rows where a page holds every run of 32 positions from a multiple of 32
 // (16 else).
 __host__ __device__ inline bool window_wide(const SeqDev &d) { return d.table == nullptr || d.ptok % 32 == 0; }
 void plan_window_maps(Common &c, const pkv_layout *layout, const pkv_seq *seqs, DecodeMaps &maps);
-int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &maps, int32_t window,
+int launch_window(const Common &c, const WindowPlan &plan, const DecodeMaps &maps, int32_t window,
                   int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
                   const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 

@@ -31,7 +31,7 @@ namespace pkv {
 namespace {
 
 constexpr int kMaxCols = 32;                 // query columns of a (stream, KV head)
-constexpr int kBlockCols = 16;               // ... of a CTA
+constexpr int kBlockCols = 16;               // ... of a CTA of small calls
 constexpr int kMaxPieces = 8;           // pieces of a split
 constexpr int kMaxSlices = 4;           // key slices of a CTA
 constexpr int kSplitKeys = 640;              // keys of a piece at most
@@ -40,11 +40,12 @@ constexpr int kMaxPages = kMaxPieces * kSplitKeys / 4 + 4;  // pages a CTA's run
 // on one to eight pieces, and merge in a second kernel: a cluster waits for
 // eight free places on neighbouring SMs, and each CTA starts and merges anew.
 // Measured, clustered against unclustered, windows of 512 keys: 32 streams (512
-// CTAs) 18.4 us against 14.6, 48 streams 27.4 against 23.3, 16 streams (256
-// CTAs) 9.4 against 11.0; of 4,096 keys: 24 streams 43.9 us against 37.9, 64
-// streams 98.5 against 97, 16 streams 24.1 against 26.7.  e4m3 calls are bound
-// by their conversions instead and stay clustered (32 streams of 4,096 keys
-// 43.8 us against 45.2).
+// CTAs) 18.3 us against 16.6, 48 streams 27.2 against 26.0, 16 streams (256
+// CTAs) 9.4 against 11.2; of 4,096 keys: 24 streams 44.0 us against 38.3, 64
+// streams 96.7 against 92.9, 16 streams 24.2 against 26.5.  Calls that their
+// arithmetic bounds stay clustered: e4m3 ones (48 streams of 4,096 keys 64.2 us
+// against 79.9), and those whose CTAs take more than 16 columns (64 streams of
+// 32 columns and 4,096 keys 146.6 us against 161.8).
 constexpr int kClusterCtas = 304;
 constexpr int kFreshGuard = 32;              // see decode_partial: rows a kernel just before may write
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
@@ -77,8 +78,8 @@ struct Cfg {
     // after the last tile the stages hold the merge rows, then the CTA's sum
     static constexpr int off_ml = 32 * row * 4;
     static constexpr int off_sum = (off_ml + 32 * 8 + 127) / 128 * 128;
-    static constexpr int off_sum_ml = off_sum + kBlockCols * kHeadDim * 4;
-    static_assert(off_sum_ml + kBlockCols * 8 <= slots * stage, "merge buffers reuse the stages");
+    static constexpr int off_sum_ml = off_sum + kMaxCols * kHeadDim * 4;
+    static_assert(off_sum_ml + kMaxCols * 8 <= slots * stage, "merge buffers reuse the stages");
     static_assert(off_join % 16 == 0 && off_bar % 8 == 0, "aligned");
 };
 
@@ -86,6 +87,7 @@ struct WinArgs {
     const uint16_t *q;
     uint16_t *out;
     float *ws;
+    float4 *stash;          // wide calls: a first pass's sums, kStash a CTA
     const uint16_t *k_new;  // fused store of the new tokens, or null
     const uint16_t *v_new;
     const uint16_t *ik_new;
@@ -96,9 +98,14 @@ struct WinArgs {
 };
 
 // CTAs that share a (stream, KV head)'s columns.
-__host__ __device__ inline int col_blocks(int ncols) { return (ncols + kBlockCols - 1) / kBlockCols; }
+__host__ __device__ inline int col_blocks(bool wide, int ncols) {
+    const int block = wide ? kMaxCols : kBlockCols;
+    return (ncols + block - 1) / block;
+}
+constexpr int kStash = kConsumers * 17 * 32;  // float4 a CTA: O and (m, l) of each lane
 
-// Key slices of a CTA (tiles it works on at once): a divisor of its slots.
+// Key slices of a piece (the tiles that a CTA of kBlockCols columns works on at
+// once): a divisor of the slots.
 __host__ __device__ inline int slices_of(bool fp8, int ncols) {
     const int ncg = ((ncols < kBlockCols ? ncols : kBlockCols) + 7) >> 3, slots = fp8 ? Cfg<true>::slots : Cfg<false>::slots;
     int n = kConsumers / ncg;
@@ -205,7 +212,7 @@ struct Run {
     int sink_page, win_page, n_sink_pages, n_pages;  // the page list: sinks' pages, then the window's
 };
 
-template <int kTile>
+template <int kTile, bool kWide>
 __device__ __forceinline__ Run locate(const Common &c, const WinArgs &a) {
     Run u;
     u.n_pieces = max(1, a.run);
@@ -214,7 +221,7 @@ __device__ __forceinline__ Run locate(const Common &c, const WinArgs &a) {
     u.s = a.even ? item / a.even : find_seq(c.n_seqs, item, [&](int t) { return c.seq[t].work_off; });
     const SeqDev &sd = c.seq[u.s];
     const int r = a.even ? item - u.s * a.even : item - sd.work_off;
-    const int blocks = col_blocks(sd.ncols), q = r / blocks;
+    const int blocks = col_blocks(kWide, sd.ncols), q = r / blocks;
     u.col0 = (r - q * blocks) * kBlockCols;
     u.kvh = q / sd.nsplit;
     u.split = q - u.kvh * sd.nsplit;
@@ -465,7 +472,7 @@ __device__ __forceinline__ bool sees(int p, int kp, int window, int n_sink) {
     return kp <= p && (kp > p - window || kp < n_sink);
 }
 
-template <bool kFp8, bool kRuns>
+template <bool kFp8, bool kRuns, bool kWide>
 __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     window_partial(const __grid_constant__ Common c, const __grid_constant__ DecodeMaps maps,
                    const __grid_constant__ WinArgs a) {
@@ -482,18 +489,22 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     constexpr int S = F::slots;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const Run u = locate<F::tile>(c, a);
+    const Run u = locate<F::tile, kWide>(c, a);
     const SeqDev &sd = c.seq[u.s];
     const int ncols = sd.ncols, G = c.group, H = c.n_kv_heads;
-    const int nc = min(ncols - u.col0, kBlockCols);  // this CTA's columns
+    const int nc = min(ncols - u.col0, kWide ? kMaxCols : kBlockCols);  // this CTA's columns
     const int ncg = (nc + 7) >> 3;                   // in groups of 8
-    // Tiles at once.  A piece's tile t belongs to key slice t % ks_n, and a
-    // piece takes whole rounds of the slices (empty tiles fill its last one),
-    // so each slot always belongs to one slice, which takes every phase of its
-    // barrier.  (A slice that skipped a phase could not tell the tile before
-    // its own, not landed yet, from its own: both leave the same parity.)
-    const int ks_n = slices_of(kFp8, ncols);
-    const int round = (u.per + ks_n - 1) / ks_n * ks_n;  // a piece's tiles, empty ones among them
+    // A piece's tile t belongs to key slice t % slices.  A CTA takes all slices
+    // at once, ks_n tiles in its warps together, or (more than kBlockCols
+    // columns) one slice after the other in two passes.  A piece takes whole
+    // rounds of the slices (empty tiles fill its last one), so each slot always
+    // belongs to the same warps, which take every phase of its barrier.  (One
+    // that skipped a phase could not tell the tile before its own, not landed
+    // yet, from its own: both leave the same parity.)
+    const int slices = slices_of(kFp8, ncols);
+    const int passes = kWide && ncols > kBlockCols ? 2 : 1, ks_n = passes == 1 ? slices : 1;
+    const int round = (u.per + slices - 1) / slices * slices;  // a piece's tiles, empty ones among them
+    const int pass_tiles = passes == 1 ? round : round / 2;
     const int ntiles = kRuns || u.key1 > u.key0 ? u.n_pieces * round : 0;
     const int cg = warp % ncg, ks = warp / ncg;
     const bool active = warp < F::consumers && ks < ks_n;
@@ -544,7 +555,8 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             if ((t & 31) == 0) {
                 // the next 32 tiles' rows, a tile a lane: looked up one by one
                 // they would take the warp longer than a tile takes to arrive
-                const int pc = (t + lane) / round, tp = t + lane - pc * round;
+                const int w = (t + lane) / pass_tiles, j = t + lane - w * pass_tiles;
+                const int pc = passes == 1 ? w : w >> 1, tp = passes == 1 ? j : 2 * j + (w & 1);
                 const int v0 = u.key0 + (pc * u.per + tp) * F::tile, p0 = pos_of(u.sp, v0);
                 first = tp < u.per && v0 < u.key1 ? v0 : -1;
                 yk = -1;
@@ -672,7 +684,13 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         // and the next piece starts anew.  The slices hand O over lane by lane,
         // 8 KB at a time; written out one by one they are two or three times
         // the traffic (64 streams of 4,096 keys 99.0 us against 92.3).
-        auto finish_piece = [&](int pc) {
+        auto reset = [&] {
+            m[0] = m[1] = uo[0] = uo[1] = -INFINITY;
+            l[0] = l[1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+        };
+        auto finish_pass = [&](int pc, int pass) {
             l[0] = sum_rows(l[0]);
             l[1] = sum_rows(l[1]);
             if constexpr (kFp8) {
@@ -686,7 +704,35 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                     acc[i][3] *= f1;
                 }
             }
+            if (kWide && passes > 1) {
+                // slice 0's sums wait in the workspace for slice 1's, each lane its own
+                float4 *const st = a.stash + (int64_t)blockIdx.x * kStash + warp * (17 * 32) + lane;
+                if (pass == 0) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) st[i * 32] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+                    st[16 * 32] = make_float4(m[0], l[0], m[1], l[1]);
+                    reset();
+                    return;
+                }
+                const float4 ml = st[16 * 32];
+                const float M0 = fmaxf(ml.x, m[0]), M1 = fmaxf(ml.z, m[1]);
+                const float w0 = M0 == -INFINITY ? 0.f : ex2(ml.x - M0), w1 = M1 == -INFINITY ? 0.f : ex2(ml.z - M1);
+                const float x0 = M0 == -INFINITY ? 0.f : ex2(m[0] - M0), x1 = M1 == -INFINITY ? 0.f : ex2(m[1] - M1);
+                l[0] = fmaf(x0, l[0], fmaf(w0, ml.y, 0.f));
+                l[1] = fmaf(x1, l[1], fmaf(w1, ml.w, 0.f));
+                m[0] = M0;
+                m[1] = M1;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float4 v = st[i * 32];
+                    acc[i][0] = fmaf(x0, acc[i][0], fmaf(w0, v.x, 0.f));
+                    acc[i][1] = fmaf(x1, acc[i][1], fmaf(w1, v.y, 0.f));
+                    acc[i][2] = fmaf(x0, acc[i][2], fmaf(w0, v.z, 0.f));
+                    acc[i][3] = fmaf(x1, acc[i][3], fmaf(w1, v.w, 0.f));
+                }
+            }
             if constexpr (!kRuns) return;
+            if (!kWide || ks_n > 1) {
             const int cl = cg * 8 + 2 * c4;  // this lane's first column in the CTA
             float4 *const jml = reinterpret_cast<float4 *>(smem + F::off_join_ml);  // [slice][two columns]
             float4 *const jo = reinterpret_cast<float4 *>(smem + F::off_join) + cg * 8 * 32 + lane;
@@ -744,6 +790,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                     }
                 }
             }
+            }
             if (ks == 0) {
                 const int64_t n_part = (int64_t)sd.nsplit * a.pieces;  // of a unit
                 const int64_t part = u.kvh * n_part + u.split * a.pieces + u.piece + pc;
@@ -765,18 +812,16 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                     }
                 }
             }
-            m[0] = m[1] = uo[0] = uo[1] = -INFINITY;
-            l[0] = l[1] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+            reset();
         };
 
         const int n_pieces = kRuns ? u.n_pieces : ntiles > 0 ? 1 : 0;
         bool ok = true;
         // (after a wait that ran out the warp still meets the others at each piece's end)
-        for (int pc = 0; pc < n_pieces; ++pc) {
-        for (int tp = ks; ok && tp < round; tp += ks_n) {
-            const int t = pc * round + tp, slot = t % S;
+        for (int w = 0; w < n_pieces * passes; ++w) {
+        const int pc = passes == 1 ? w : w >> 1, pass = w - pc * passes;
+        for (int tp = pass + ks; ok && tp < round; tp += slices) {
+            const int t = w * pass_tiles + (passes == 1 ? tp : tp >> 1), slot = t % S;
             ok = __all_sync(0xffffffffu, mbar_wait(&x.full[slot], (t / S) & 1, c.status));
             if (!ok) {
                 *x.abort_flag = 1;
@@ -977,7 +1022,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             __syncwarp();
             if (lane == 0) mbar_arrive(&x.empty[slot]);
         }
-        finish_piece(pc);
+        finish_pass(pc, pass);
         }
     }
     __syncthreads();  // every staged tile is consumed (or the CTA gave up)
@@ -1101,28 +1146,40 @@ __global__ void __launch_bounds__(kCombThreads)
     if (grp == 0) write_out(out, t);
 }
 
+using WindowKernel = void (*)(Common, DecodeMaps, WinArgs);
+template <bool kFp8>
+WindowKernel window_kernel_of(bool runs, bool wide) {
+    return runs ? (wide ? window_partial<kFp8, true, true> : window_partial<kFp8, true, false>)
+                : (wide ? window_partial<kFp8, false, true> : window_partial<kFp8, false, false>);
+}
+WindowKernel window_kernel(bool fp8, bool runs, bool wide) {
+    return fp8 ? window_kernel_of<true>(runs, wide) : window_kernel_of<false>(runs, wide);
+}
+
 }  // namespace
 
 // Pieces of a split, by the window alone (a stream's bits must not depend on
 // its batch): 128 keys a piece before there is another.
-int window_pieces(int32_t window, int32_t n_sink) {
+static int window_pieces(int32_t window, int32_t n_sink) {
     const int64_t keys = (int64_t)window + n_sink + 32;
     int n = 1;
     while (n < kMaxPieces && keys > 128 * n) n *= 2;
     return n;
 }
 
-// Splits only where a piece would pass kSplitKeys keys.
-int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
-    int64_t items = 0, cols = 0, floats = 0;
+// Splits only where a piece would pass kSplitKeys keys.  A call of streams with
+// more than kBlockCols columns gives each kBlockCols a CTA while the CTAs fit
+// the GPU at once, else all of them one: the bits are the same.  Four draft
+// tokens of 8 heads, windows of 2,047 keys, 16 columns a CTA against 32: 8
+// streams 15.4 us against 21.7, 16 streams (512 CTAs against 256) 30.9 against
+// 25.0, 64 streams (which read twice the bytes from L2) 118 against 100.5.
+int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
     const int pieces = window_pieces(window, n_sink);
     const int tile = c.kv_fp8 ? Cfg<true>::tile : Cfg<false>::tile;
-    bool split = false;
+    bool split = false, wide = false;
+    int64_t items = 0, cols = 0, floats = 0;
     for (int s = 0; s < c.n_seqs; ++s) {
         SeqDev &d = c.seq[s];
-        d.work_off = static_cast<int32_t>(items);
-        d.comb_off = static_cast<int32_t>(cols);
-        d.ws_off = floats;
         d.ncols = d.n_new * c.group;
         if (d.ncols > kMaxCols) return PKV_EINVAL;
         d.nsplit = 1;
@@ -1133,33 +1190,58 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, DecodePlan *plan) {
         const int per = (sp.nkeys - 1) / (d.nsplit * pieces) + 1;  // keys of a piece
         d.split_len = (per + tile - 1) / tile * tile;
         split |= d.nsplit > 1;
-        items += (int64_t)c.n_kv_heads * d.nsplit * col_blocks(d.ncols);
+        wide |= d.ncols > kBlockCols;
+        items += (int64_t)c.n_kv_heads * d.nsplit * col_blocks(false, d.ncols);
+    }
+    wide = wide && items * pieces > kClusterCtas;
+    items = 0;
+    for (int s = 0; s < c.n_seqs; ++s) {
+        SeqDev &d = c.seq[s];
+        d.work_off = static_cast<int32_t>(items);
+        d.comb_off = static_cast<int32_t>(cols);
+        d.ws_off = floats;
+        if (d.ncols == 0) continue;
+        items += (int64_t)c.n_kv_heads * d.nsplit * col_blocks(wide, d.ncols);
         cols += (int64_t)c.n_kv_heads * d.ncols;
         floats += (int64_t)c.n_kv_heads * d.nsplit * pieces * d.ncols * (kHeadDim + 2);
         floats = (floats + 63) / 64 * 64;
     }
     if (items * pieces > INT32_MAX) return PKV_EINVAL;
-    const bool combine = pieces > 1 && (split || (!c.kv_fp8 && items * pieces > kClusterCtas));
-    plan->total_items = static_cast<int32_t>(items);
-    plan->total_comb = combine ? static_cast<int32_t>(cols) : 0;
-    plan->ws_bytes = combine ? static_cast<size_t>(floats) * 4 : 0;
+    const bool combine = pieces > 1 && (split || (!c.kv_fp8 && !wide && items * pieces > kClusterCtas));
+    plan->items = static_cast<int32_t>(items);
+    plan->comb = combine ? static_cast<int32_t>(cols) : 0;
+    plan->pieces = pieces;
+    plan->wide = wide;
+    plan->run = 0;
+    // pieces of a CTA: the least of waves x (pieces + half a piece's time to
+    // start), the larger run where two are alike
+    if (combine) {
+        int64_t best = INT64_MAX;
+        for (int run = 1; run <= pieces; run *= 2) {
+            const int64_t cost = ((items * pieces / run + kClusterCtas - 1) / kClusterCtas) * (2 * run + 1);
+            if (cost <= best) {
+                best = cost;
+                plan->run = run;
+            }
+        }
+    }
+    plan->ctas = static_cast<int32_t>(items * (pieces / std::max(1, plan->run)));
+    plan->stash_off = combine ? floats : 0;
+    plan->ws_bytes = static_cast<size_t>(plan->stash_off) * 4 + (wide ? (size_t)plan->ctas * kStash * sizeof(float4) : 0);
     return PKV_OK;
 }
 
-int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &maps, int32_t window,
+int launch_window(const Common &c, const WindowPlan &plan, const DecodeMaps &maps, int32_t window,
                   int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
                   const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     if (once_per_device(attr_done, [] {
-            const void *fns[] = {reinterpret_cast<const void *>(window_partial<false, false>),
-                                 reinterpret_cast<const void *>(window_partial<false, true>),
-                                 reinterpret_cast<const void *>(window_partial<true, false>),
-                                 reinterpret_cast<const void *>(window_partial<true, true>)};
-            const int bytes[] = {Cfg<false>::smem, Cfg<false>::smem, Cfg<true>::smem, Cfg<true>::smem};
-            for (int i = 0; i < 4; ++i) {
-                if (cudaFuncSetAttribute(fns[i], cudaFuncAttributeMaxDynamicSharedMemorySize, bytes[i]) != cudaSuccess)
+            for (int i = 0; i < 8; ++i) {
+                const void *fn = reinterpret_cast<const void *>(window_kernel(i & 1, i & 2, i & 4));
+                const int bytes = i & 1 ? Cfg<true>::smem : Cfg<false>::smem;
+                if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
                     return PKV_ECUDA;
-                if (cudaFuncSetAttribute(fns[i], cudaFuncAttributePreferredSharedMemoryCarveout,
+                if (cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
                                          cudaSharedmemCarveoutMaxShared) != cudaSuccess)
                     return PKV_ECUDA;
             }
@@ -1168,28 +1250,16 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
                                                 cudaSharedmemCarveoutMaxShared));
         }) != PKV_OK)
         return PKV_ECUDA;
-    WinArgs a{q, out, ws, k_new, v_new, ik_new, window, n_sink, window_pieces(window, n_sink), 0, 0};
-    if (plan.total_items % c.n_seqs == 0) {
-        a.even = plan.total_items / c.n_seqs;
+    WinArgs a{q, out, ws, reinterpret_cast<float4 *>(ws + plan.stash_off), k_new, v_new, ik_new, window, n_sink,
+              plan.pieces, plan.run, 0};
+    if (plan.items % c.n_seqs == 0) {
+        a.even = plan.items / c.n_seqs;
         for (int s = 0; s < c.n_seqs; ++s)
             if (c.seq[s].work_off != s * a.even) a.even = 0;
     }
-    const bool clustered = plan.total_comb == 0;
-    // pieces of a CTA: the least of waves x (pieces + half a piece's time to
-    // start), the larger run where two are alike
-    if (!clustered) {
-        const int64_t ctas = (int64_t)plan.total_items * a.pieces;
-        int64_t best = INT64_MAX;
-        for (int run = 1; run <= a.pieces; run *= 2) {
-            const int64_t cost = ((ctas / run + kClusterCtas - 1) / kClusterCtas) * (2 * run + 1);
-            if (cost <= best) {
-                best = cost;
-                a.run = run;
-            }
-        }
-    }
+    const bool clustered = plan.run == 0;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(plan.total_items) * (a.pieces / std::max(1, a.run)));
+    cfg.gridDim = dim3(static_cast<unsigned>(plan.ctas));
     cfg.blockDim = dim3(c.kv_fp8 ? Cfg<true>::threads : Cfg<false>::threads);
     cfg.dynamicSmemBytes = c.kv_fp8 ? Cfg<true>::smem : Cfg<false>::smem;
     cfg.stream = stream;
@@ -1201,13 +1271,12 @@ int launch_window(const Common &c, const DecodePlan &plan, const DecodeMaps &map
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    auto *const fn = c.kv_fp8 ? (clustered ? window_partial<true, false> : window_partial<true, true>)
-                              : (clustered ? window_partial<false, false> : window_partial<false, true>);
+    auto *const fn = window_kernel(c.kv_fp8 != 0, !clustered, plan.wide);
     if (cudaLaunchKernelEx(&cfg, fn, c, maps, a) != cudaSuccess)
         return PKV_ECUDA;
     if (clustered) return PKV_OK;
     return launch_status(
-        launch_pdl(window_combine, static_cast<unsigned>(plan.total_comb), kCombThreads, 0, stream, c, a));
+        launch_pdl(window_combine, static_cast<unsigned>(plan.comb), kCombThreads, 0, stream, c, a));
 }
 
 }  // namespace pkv

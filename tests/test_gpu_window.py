@@ -143,6 +143,35 @@ def test_paged_equals_contiguous_and_alone_equals_in_batch(fmt):
         assert np.array_equal(run(w, 0, hq, q[i:i + 1]), rows[i])
 
 
+# (lens, new tokens, q heads, kv heads, window, sinks) of calls that give a KV
+# head's 17 to 32 query columns one CTA: several pieces, splits, one piece
+WIDE = [([int(x) for x in np.linspace(40, 2300, 24)], [4, 3, 2, 1] * 6, 16, 2, 1500, 4),
+        ([9100, 8000, 9005, 7000, 8800, 9216, 8191, 30], [4, 4, 3, 4, 1, 4, 4, 4], 16, 2, 9000, 0),
+        ([int(x) for x in np.linspace(5, 200, 64)], [4, 3] * 32, 32, 4, 60, 1)]
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("case", range(len(WIDE)))
+def test_many_draft_windows(case, fmt):
+    t = torch()
+    lens, n_new, hq, hkv, window, sinks = WIDE[case]
+    lay = pkv.layout(1, hkv, 256, 0, fmt)
+    streams = streams_of(lens, hkv, seed=400)
+    q = queries_of(n_new, hq, seed=400)
+    a = Windowed(lay, streams, n_new, window, sinks, 48, seed=1, fused=True)
+    b = Windowed(lay, streams, n_new, window, sinks, 48, seed=1, fused=True)
+    pkv.store(lay, b.seqs(), 0, *b.new_rows(0))
+    got = run(a, 0, hq, q, fused=True)
+    assert np.array_equal(got, run(b, 0, hq, q))
+    assert t.equal(a.bufs[0], b.bufs[0])
+    rows = np.split(got, np.cumsum(n_new)[:-1])
+    for i in sorted({0, 1, 2, 3, 5, len(lens) - 1}):
+        w = Windowed(lay, streams[i:i + 1], n_new[i:i + 1], window, sinks, 16, seed=i)
+        ok, report = within_tol(rows[i], w.reference(0, q[i:i + 1]))
+        assert ok, report
+        assert np.array_equal(run(w, 0, hq, q[i:i + 1]), rows[i])   # alone, a CTA takes 16 columns
+
+
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("ptok", [16, 20, 64])
 @pytest.mark.parametrize("idx", [0, 128])
