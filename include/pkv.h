@@ -30,10 +30,11 @@
  *     and wait for it before touching anything it may write.  Two things are
  *     read before that wait: page tables, and the rows of cached positions
  *     more than 32 below a stream's new tokens (below len - n_new - 32) in
- *     pkv_decode / pkv_decode_static.  So those must not
+ *     pkv_decode / pkv_decode_static / pkv_window_decode.  So those must not
  *     be written by the kernel immediately before on the stream, unless that
- *     kernel is pkv_store, which makes its rows visible before letting the
- *     next kernel start.  A pkv_decode with k_new writes only its own new
+ *     kernel is pkv_store, pkv_pages_copy or pkv_tables_remap, which make
+ *     what they write visible before letting the next kernel start.  A
+ *     pkv_decode or pkv_window_decode with k_new writes only its own new
  *     rows (at most 32 a stream), which for a stream decoding in order lie
  *     within the 32 positions below the next call's new tokens, so decode
  *     calls of the same stream and layer may follow each other directly.
@@ -380,9 +381,10 @@ int pkv_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, in
  * table entries of pages without a row that one reads are not looked at: such
  * pages may have been given back (pkv_window_dead_pages).  A row that some of
  * the stream's new tokens read and others do not must hold finite values.
- * Partials of windows of more than about 5,000 keys go to ws (device, >=
- * pkv_window_decode_ws_size bytes, 0 for shorter ones, 256-byte aligned, no
- * initialization, one ws per in-flight call).  A stream's bits depend only on
+ * Partials of large calls (more than 304 CTAs of up to 640 keys and 16 query
+ * columns each) and of windows of more than about 5,000 keys go to ws (device,
+ * >= pkv_window_decode_ws_size bytes, which is 0 for other calls, 256-byte
+ * aligned, no initialization, one ws per in-flight call).  A stream's bits depend only on
  * its own rows, length and new tokens, the window and n_sink: paged output
  * equals contiguous output, and other streams of the call change nothing.
  * EINVAL for a window or n_sink out of range, and as for pkv_decode. */

@@ -8,20 +8,31 @@
 // that no query of the stream sees take the row of a neighbouring key that
 // one sees, so that nothing stale (a NaN, a page that is gone) reaches an MMA.
 //
-// A split of a (stream, KV head) is a cluster of up to eight CTAs, each with
-// an equal run of the split's tiles.  A CTA is a producer warp, which fills a
-// ring of 16-key stages (one 3D TMA copy for K and one for V where a page
-// holds the tile, else key by key with cp.async), and consumer warps that
-// compute S^T = K Q^T and O^T += V^T P^T with warp MMAs (one query token has
-// at most 32 query columns here, 8 to an MMA; the tensor cores' 128-row tiles
-// would stand nearly empty) with an online softmax per column.  The consumers
-// merge through shared memory and the cluster's CTAs through distributed
-// shared memory, in the order of the keys, so a window of up to
-// kSplitTiles x 8 x 16 keys is one launch with no workspace; longer ones
-// write split partials for the decode's combine kernel.
+// The keys of a (stream, KV head) are cut into up to eight pieces, by the
+// window alone, a CTA each; the pieces are one split, or more where a piece
+// would pass 640 keys.  A CTA is a producer warp, which fills a ring of six
+// 16 KB stages (16 bf16 keys or 32 e4m3 keys: one 3D TMA copy for K and one for
+// V where a page holds them, else key by key with cp.async), and four consumer
+// warps that compute S^T = K Q^T and O^T += V^T P^T with warp MMAs (8 query
+// columns to an MMA, 16 a CTA; the tensor cores' 128-row tiles would stand
+// nearly empty) with an online softmax per column, each warp on a tile and a
+// column group of its own.  The tiles of a piece are dealt to two or three key
+// slices; slices, pieces and splits merge in the order of the keys.
 //
-// The bytes of K and V bound a full batch: two CTAs share an SM, so one
-// streams while the other starts or merges.
+// A split's CTAs are a cluster that merges through distributed shared memory:
+// one launch, no workspace.  Calls of more CTAs than the GPU holds, and windows
+// of several splits, run unclustered instead, a CTA on one or more pieces, and
+// window_combine merges the pieces from the workspace.  Calls of many draft
+// windows give a CTA 32 columns.  All of them round alike: a stream's bits do
+// not depend on its batch.
+//
+// What bounds it: the bytes of K and V where there are many (64 streams of
+// 4,096 bf16 keys: 539 MB in 92.3 us, 5.84 TB/s); whole waves of CTAs, two on
+// an SM, below that (32 streams of 4,096 e4m3 keys are 512 CTAs in two waves of
+// 21 us; a copy of the kernel without its MMAs and conversions takes 37.2 us of
+// 42.9); and for a few streams the launch, the first tile's way in and the
+// merge (one stream of 128 keys 7.0 us, four of 1,024 keys 8.0 us).  Two CTAs
+// share an SM, so one streams while the other starts or merges.
 #include <algorithm>
 #include <cuda_fp16.h>
 
@@ -32,8 +43,8 @@ namespace {
 
 constexpr int kMaxCols = 32;                 // query columns of a (stream, KV head)
 constexpr int kBlockCols = 16;               // ... of a CTA of small calls
-constexpr int kMaxPieces = 8;           // pieces of a split
-constexpr int kMaxSlices = 4;           // key slices of a CTA
+constexpr int kMaxPieces = 8;                // pieces of a split
+constexpr int kMaxSlices = 3;                // key slices of a piece
 constexpr int kSplitKeys = 640;              // keys of a piece at most
 constexpr int kMaxPages = kMaxPieces * kSplitKeys / 4 + 4;  // pages a CTA's run can touch
 // bf16 calls of more CTAs than this (two fill an SM) run them unclustered, each
@@ -42,12 +53,12 @@ constexpr int kMaxPages = kMaxPieces * kSplitKeys / 4 + 4;  // pages a CTA's run
 // Measured, clustered against unclustered, windows of 512 keys: 32 streams (512
 // CTAs) 18.3 us against 16.6, 48 streams 27.2 against 26.0, 16 streams (256
 // CTAs) 9.4 against 11.2; of 4,096 keys: 24 streams 44.0 us against 38.3, 64
-// streams 96.7 against 92.9, 16 streams 24.2 against 26.5.  Calls that their
-// arithmetic bounds stay clustered: e4m3 ones (48 streams of 4,096 keys 64.2 us
-// against 79.9), and those whose CTAs take more than 16 columns (64 streams of
-// 32 columns and 4,096 keys 146.6 us against 161.8).
+// streams 96.7 against 92.9, 16 streams 24.2 against 26.5.  e4m3
+// calls stay clustered (48 streams of 4,096 keys 64.2 us against 79.9), and so
+// do those whose CTAs take more than 16 columns (64 streams of 32 columns and
+// 4,096 keys 146.6 us against 161.8).
 constexpr int kClusterCtas = 304;
-constexpr int kFreshGuard = 32;              // see decode_partial: rows a kernel just before may write
+constexpr int kFreshGuard = 32;              // rows below the new tokens that a kernel just before may write
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
 
 constexpr int kJoinBytes = 8192;             // O of a warp's 8 columns, in its registers' layout
@@ -109,6 +120,7 @@ constexpr int kStash = kConsumers * 17 * 32;  // float4 a CTA: O and (m, l) of e
 __host__ __device__ inline int slices_of(bool fp8, int ncols) {
     const int ncg = ((ncols < kBlockCols ? ncols : kBlockCols) + 7) >> 3, slots = fp8 ? Cfg<true>::slots : Cfg<false>::slots;
     int n = kConsumers / ncg;
+    n = n > kMaxSlices ? kMaxSlices : n;
     while (slots % n) --n;
     return n;
 }
@@ -802,7 +814,8 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
                             if constexpr (kFp8) {
-                                *reinterpret_cast<float2 *>(o + e * kHeadDim + 32 * g + 2 * i) = make_float2(acc[i][e], acc[i][e + 2]);
+                                *reinterpret_cast<float2 *>(o + e * kHeadDim + 32 * g + 2 * i) =
+                                    make_float2(acc[i][e], acc[i][e + 2]);
                             } else {
                                 o[e * kHeadDim + 16 * i + g] = acc[i][e];
                                 o[e * kHeadDim + 16 * i + g + 8] = acc[i][e + 2];
@@ -819,210 +832,214 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         bool ok = true;
         // (after a wait that ran out the warp still meets the others at each piece's end)
         for (int w = 0; w < n_pieces * passes; ++w) {
-        const int pc = passes == 1 ? w : w >> 1, pass = w - pc * passes;
-        for (int tp = pass + ks; ok && tp < round; tp += slices) {
-            const int t = w * pass_tiles + (passes == 1 ? tp : tp >> 1), slot = t % S;
-            ok = __all_sync(0xffffffffu, mbar_wait(&x.full[slot], (t / S) & 1, c.status));
-            if (!ok) {
-                *x.abort_flag = 1;
-                break;
-            }
-            const int v0 = u.key0 + (pc * u.per + tp) * F::tile;
-            if (tp >= u.per || v0 >= u.key1) {
-                if (lane == 0) mbar_arrive(&x.empty[slot]);
-                continue;
-            }
-            const uint8_t *const st = x.stages + slot * F::stage;
-            const float *const scl = x.scl + slot * 64;  // e4m3
-            // S^T of the tile's keys and this lane's two columns: rows g and g + 8
-            // of each 16 keys, in log2 units, -inf where the column's query does
-            // not see the key
-            constexpr int kSub = F::tile / 16;
-            float sx[kSub][4];
+            const int pc = passes == 1 ? w : w >> 1, pass = w - pc * passes;
+            for (int tp = pass + ks; ok && tp < round; tp += slices) {
+                const int t = w * pass_tiles + (passes == 1 ? tp : tp >> 1), slot = t % S;
+                ok = __all_sync(0xffffffffu, mbar_wait(&x.full[slot], (t / S) & 1, c.status));
+                if (!ok) {
+                    *x.abort_flag = 1;
+                    break;
+                }
+                const int v0 = u.key0 + (pc * u.per + tp) * F::tile;
+                if (tp >= u.per || v0 >= u.key1) {
+                    if (lane == 0) mbar_arrive(&x.empty[slot]);
+                    continue;
+                }
+                const uint8_t *const st = x.stages + slot * F::stage;
+                const float *const scl = x.scl + slot * 64;  // e4m3
+                // S^T of the tile's keys and this lane's two columns: rows g and g + 8
+                // of each 16 keys, in log2 units, -inf where the column's query does
+                // not see the key
+                constexpr int kSub = F::tile / 16;
+                float sx[kSub][4];
 #pragma unroll
-            for (int u16 = 0; u16 < kSub; ++u16) {
-                float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-                float fa = kScaleLog2, fb = kScaleLog2;
-                if constexpr (kFp8) {
-                    // two accumulator chains, a quarter of the dims at a time
+                for (int u16 = 0; u16 < kSub; ++u16) {
+                    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+                    float fa = kScaleLog2, fb = kScaleLog2;
+                    if constexpr (kFp8) {
+                        // two accumulator chains, a quarter of the dims at a time
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 w0 = *reinterpret_cast<const uint4 *>(st + swz8(16 * u16 + g, 4 * c4 + i));
-                        const uint4 w1 = *reinterpret_cast<const uint4 *>(st + swz8(16 * u16 + g + 8, 4 * c4 + i));
-                        uint32_t z[4][4];
-                        f16_of_codes(w0.x, z[0][0], z[0][2]);
-                        f16_of_codes(w1.x, z[0][1], z[0][3]);
-                        f16_of_codes(w0.y, z[1][0], z[1][2]);
-                        f16_of_codes(w1.y, z[1][1], z[1][3]);
-                        f16_of_codes(w0.z, z[2][0], z[2][2]);
-                        f16_of_codes(w1.z, z[2][1], z[2][3]);
-                        f16_of_codes(w0.w, z[3][0], z[3][2]);
-                        f16_of_codes(w1.w, z[3][1], z[3][3]);
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 w0 = *reinterpret_cast<const uint4 *>(st + swz8(16 * u16 + g, 4 * c4 + i));
+                            const uint4 w1 = *reinterpret_cast<const uint4 *>(st + swz8(16 * u16 + g + 8, 4 * c4 + i));
+                            uint32_t z[4][4];
+                            f16_of_codes(w0.x, z[0][0], z[0][2]);
+                            f16_of_codes(w1.x, z[0][1], z[0][3]);
+                            f16_of_codes(w0.y, z[1][0], z[1][2]);
+                            f16_of_codes(w1.y, z[1][1], z[1][3]);
+                            f16_of_codes(w0.z, z[2][0], z[2][2]);
+                            f16_of_codes(w1.z, z[2][1], z[2][3]);
+                            f16_of_codes(w0.w, z[3][0], z[3][2]);
+                            f16_of_codes(w1.w, z[3][1], z[3][3]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            mma_half((j & 1) ? sb : sa, z[j][0], z[j][1], z[j][2], z[j][3], qf[4 * i + j][0], qf[4 * i + j][1]);
+                            for (int j = 0; j < 4; ++j)
+                                mma_half((j & 1) ? sb : sa, z[j][0], z[j][1], z[j][2], z[j][3], qf[4 * i + j][0],
+                                         qf[4 * i + j][1]);
+                        }
+                        fa *= scl[16 * u16 + g];
+                        fb *= scl[16 * u16 + g + 8];
+                    } else {
+                        // two accumulator chains, four K fragments loaded before their MMAs
+                        const uint32_t kbs = s_base + slot * F::stage;
+#pragma unroll
+                        for (int h = 0; h < 4; ++h) {
+                            uint32_t f[4][4];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                ldsm_x4(kbs + h * kPlane + swz(kr_, 2 * j + kcb), f[j][0], f[j][1], f[j][2], f[j][3]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t(&x4)[4] = f[j];
+                                mma_bf16((j & 1) ? sb : sa, x4[0], x4[1], x4[2], x4[3], qf[4 * h + j][0], qf[4 * h + j][1]);
+                            }
+                        }
                     }
-                    fa *= scl[16 * u16 + g];
-                    fb *= scl[16 * u16 + g + 8];
+                    const int ka = pos_of(u.sp, v0) + 16 * u16 + g, kb = ka + 8;
+                    sx[u16][0] = sees(p0, ka, a.window, a.n_sink) ? (sa[0] + sb[0]) * fa : -INFINITY;
+                    sx[u16][1] = sees(p1, ka, a.window, a.n_sink) ? (sa[1] + sb[1]) * fa : -INFINITY;
+                    sx[u16][2] = sees(p0, kb, a.window, a.n_sink) ? (sa[2] + sb[2]) * fb : -INFINITY;
+                    sx[u16][3] = sees(p1, kb, a.window, a.n_sink) ? (sa[3] + sb[3]) * fb : -INFINITY;
+                }
+                // online softmax of the two columns
+                float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+                for (int u16 = 0; u16 < kSub; ++u16) {
+                    t0 = fmaxf(t0, fmaxf(sx[u16][0], sx[u16][2]));
+                    t1 = fmaxf(t1, fmaxf(sx[u16][1], sx[u16][3]));
+                }
+                const float n0 = fmaxf(m[0], max_rows(t0)), n1 = fmaxf(m[1], max_rows(t1));
+                const float o0 = n0 == -INFINITY ? 0.f : n0, o1 = n1 == -INFINITY ? 0.f : n1;
+                const float al0 = ex2(m[0] - o0), al1 = ex2(m[1] - o1);  // 0 while nothing was summed
+                m[0] = n0;
+                m[1] = n1;
+                l[0] *= al0;
+                l[1] *= al1;
+                // the weights of O, as two parts (hi + lo) in the MMAs' B layout
+                uint32_t wh[kSub][2], wl[kSub][2];
+                float be0 = al0, be1 = al1;  // what O is rescaled by
+                if constexpr (kFp8) {
+                    // a V scale 2^E x mant goes into the key's weight, with a running
+                    // maximum of logit + E as O's reference: weights in [0, 2), split
+                    // into f16 hi + lo parts (about 22 significant bits)
+                    float e[kSub][2], mt[kSub][2], r0 = -INFINITY, r1 = -INFINITY;
+#pragma unroll
+                    for (int u16 = 0; u16 < kSub; ++u16) {
+                        split_scale(scl[32 + 16 * u16 + g], e[u16][0], mt[u16][0]);
+                        split_scale(scl[32 + 16 * u16 + g + 8], e[u16][1], mt[u16][1]);
+                        l[0] += ex2(sx[u16][0] - o0) + ex2(sx[u16][2] - o0);
+                        l[1] += ex2(sx[u16][1] - o1) + ex2(sx[u16][3] - o1);
+                        r0 = fmaxf(r0, fmaxf(sx[u16][0] + e[u16][0], sx[u16][2] + e[u16][1]));
+                        r1 = fmaxf(r1, fmaxf(sx[u16][1] + e[u16][0], sx[u16][3] + e[u16][1]));
+                    }
+                    const float nu0 = fmaxf(uo[0], max_rows(r0)), nu1 = fmaxf(uo[1], max_rows(r1));
+                    const float z0 = nu0 == -INFINITY ? 0.f : nu0, z1 = nu1 == -INFINITY ? 0.f : nu1;
+                    be0 = ex2(uo[0] - z0);
+                    be1 = ex2(uo[1] - z1);
+                    uo[0] = nu0;
+                    uo[1] = nu1;
+#pragma unroll
+                    for (int u16 = 0; u16 < kSub; ++u16) {
+                        const float q0 = ex2(sx[u16][0] + e[u16][0] - z0) * mt[u16][0];
+                        const float q1 = ex2(sx[u16][1] + e[u16][0] - z1) * mt[u16][0];
+                        const float q2 = ex2(sx[u16][2] + e[u16][1] - z0) * mt[u16][1];
+                        const float q3 = ex2(sx[u16][3] + e[u16][1] - z1) * mt[u16][1];
+                        const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
+                        const __half2 l01 = __floats2half2_rn(q0 - __low2float(h01), q1 - __high2float(h01));
+                        const __half2 l23 = __floats2half2_rn(q2 - __low2float(h23), q3 - __high2float(h23));
+                        wh[u16][0] = movmatrix_t(bits_of(h01));
+                        wh[u16][1] = movmatrix_t(bits_of(h23));
+                        wl[u16][0] = movmatrix_t(bits_of(l01));
+                        wl[u16][1] = movmatrix_t(bits_of(l23));
+                    }
                 } else {
-                    // two accumulator chains, four K fragments loaded before their MMAs
-                    const uint32_t kbs = s_base + slot * F::stage;
+                    // P as a bf16 pair hi + lo (lo = p - hi exactly): about 16
+                    // significant bits of the weights reach the float32 accumulator
+                    const float e0 = ex2(sx[0][0] - o0), e1 = ex2(sx[0][1] - o1);
+                    const float e2 = ex2(sx[0][2] - o0), e3 = ex2(sx[0][3] - o1);
+                    l[0] += e0 + e2;
+                    l[1] += e1 + e3;
+                    const uint32_t h01 = pack_bf16(e0, e1), h23 = pack_bf16(e2, e3);
+                    wh[0][0] = movmatrix_t(h01);
+                    wh[0][1] = movmatrix_t(h23);
+                    wl[0][0] = movmatrix_t(pack_bf16(e0 - bf16_lo(h01), e1 - bf16_hi(h01)));
+                    wl[0][1] = movmatrix_t(pack_bf16(e2 - bf16_lo(h23), e3 - bf16_hi(h23)));
+                }
+                if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {  // some reference grew
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        acc[i][0] *= be0;
+                        acc[i][1] *= be1;
+                        acc[i][2] *= be0;
+                        acc[i][3] *= be1;
+                    }
+                }
+                // O^T += V^T P^T
+                if constexpr (kFp8) {
+#pragma unroll
+                    for (int u16 = 0; u16 < kSub; ++u16) {
+                        // V codes of keys 2c, 2c+1, 2c+8, 2c+9, dims 32g .. 32g+31
+                        uint32_t w[4][8];
+                        const uint8_t *vb = st + F::half;
+                        const int kr[4] = {2 * c4, 2 * c4 + 1, 2 * c4 + 8, 2 * c4 + 9};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const uint4 z0 = *reinterpret_cast<const uint4 *>(vb + swz8(16 * u16 + kr[i], 2 * g));
+                            const uint4 z1 = *reinterpret_cast<const uint4 *>(vb + swz8(16 * u16 + kr[i], 2 * g + 1));
+                            w[i][0] = z0.x;
+                            w[i][1] = z0.y;
+                            w[i][2] = z0.z;
+                            w[i][3] = z0.w;
+                            w[i][4] = z1.x;
+                            w[i][5] = z1.y;
+                            w[i][6] = z1.z;
+                            w[i][7] = z1.w;
+                        }
+                        // four dim tiles at a time: a hi and a lo product of one
+                        // tile follow each other at the MMA's latency
+#pragma unroll
+                        for (int i4 = 0; i4 < 16; i4 += 4) {
+                            uint32_t z[4][4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                // codes of dims 32g + 2 (i4 + i) and + 1: {key, next key}
+                                // of the first dim, then of the second
+                                const int wi = (i4 + i) >> 1, b = 2 * (i & 1);
+                                const uint32_t sel = b | ((4 + b) << 4) | ((b + 1) << 8) | ((5 + b) << 12);
+                                f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel), z[i][0], z[i][1]);
+                                f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel), z[i][2], z[i][3]);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_half(acc[i4 + i], z[i][0], z[i][1], z[i][2], z[i][3], wh[u16][0], wh[u16][1]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_half(acc[i4 + i], z[i][0], z[i][1], z[i][2], z[i][3], wl[u16][0], wl[u16][1]);
+                        }
+                    }
+                } else {
+                    const uint32_t vbs = s_base + slot * F::stage + F::half;
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
                         uint32_t f[4][4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            ldsm_x4(kbs + h * kPlane + swz(kr_, 2 * j + kcb), f[j][0], f[j][1], f[j][2], f[j][3]);
+                            ldsm_x4_t(vbs + h * kPlane + swz(vr_, 2 * j + vcb), f[j][0], f[j][1], f[j][2], f[j][3]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t(&x4)[4] = f[j];
-                            mma_bf16((j & 1) ? sb : sa, x4[0], x4[1], x4[2], x4[3], qf[4 * h + j][0], qf[4 * h + j][1]);
+                            mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], wh[0][0], wh[0][1]);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t(&x4)[4] = f[j];
+                            mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], wl[0][0], wl[0][1]);
                         }
                     }
                 }
-                const int ka = pos_of(u.sp, v0) + 16 * u16 + g, kb = ka + 8;
-                sx[u16][0] = sees(p0, ka, a.window, a.n_sink) ? (sa[0] + sb[0]) * fa : -INFINITY;
-                sx[u16][1] = sees(p1, ka, a.window, a.n_sink) ? (sa[1] + sb[1]) * fa : -INFINITY;
-                sx[u16][2] = sees(p0, kb, a.window, a.n_sink) ? (sa[2] + sb[2]) * fb : -INFINITY;
-                sx[u16][3] = sees(p1, kb, a.window, a.n_sink) ? (sa[3] + sb[3]) * fb : -INFINITY;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x.empty[slot]);
             }
-            // online softmax of the two columns
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int u16 = 0; u16 < kSub; ++u16) {
-                t0 = fmaxf(t0, fmaxf(sx[u16][0], sx[u16][2]));
-                t1 = fmaxf(t1, fmaxf(sx[u16][1], sx[u16][3]));
-            }
-            const float n0 = fmaxf(m[0], max_rows(t0)), n1 = fmaxf(m[1], max_rows(t1));
-            const float o0 = n0 == -INFINITY ? 0.f : n0, o1 = n1 == -INFINITY ? 0.f : n1;
-            const float al0 = ex2(m[0] - o0), al1 = ex2(m[1] - o1);  // 0 while nothing was summed
-            m[0] = n0;
-            m[1] = n1;
-            l[0] *= al0;
-            l[1] *= al1;
-            // the weights of O, as two parts (hi + lo) in the MMAs' B layout
-            uint32_t wh[kSub][2], wl[kSub][2];
-            float be0 = al0, be1 = al1;  // what O is rescaled by
-            if constexpr (kFp8) {
-                // a V scale 2^E x mant goes into the key's weight, with a running
-                // maximum of logit + E as O's reference: weights in [0, 2), split
-                // into f16 hi + lo parts (about 22 significant bits)
-                float e[kSub][2], mt[kSub][2], r0 = -INFINITY, r1 = -INFINITY;
-#pragma unroll
-                for (int u16 = 0; u16 < kSub; ++u16) {
-                    split_scale(scl[32 + 16 * u16 + g], e[u16][0], mt[u16][0]);
-                    split_scale(scl[32 + 16 * u16 + g + 8], e[u16][1], mt[u16][1]);
-                    l[0] += ex2(sx[u16][0] - o0) + ex2(sx[u16][2] - o0);
-                    l[1] += ex2(sx[u16][1] - o1) + ex2(sx[u16][3] - o1);
-                    r0 = fmaxf(r0, fmaxf(sx[u16][0] + e[u16][0], sx[u16][2] + e[u16][1]));
-                    r1 = fmaxf(r1, fmaxf(sx[u16][1] + e[u16][0], sx[u16][3] + e[u16][1]));
-                }
-                const float nu0 = fmaxf(uo[0], max_rows(r0)), nu1 = fmaxf(uo[1], max_rows(r1));
-                const float z0 = nu0 == -INFINITY ? 0.f : nu0, z1 = nu1 == -INFINITY ? 0.f : nu1;
-                be0 = ex2(uo[0] - z0);
-                be1 = ex2(uo[1] - z1);
-                uo[0] = nu0;
-                uo[1] = nu1;
-#pragma unroll
-                for (int u16 = 0; u16 < kSub; ++u16) {
-                    const float q0 = ex2(sx[u16][0] + e[u16][0] - z0) * mt[u16][0], q1 = ex2(sx[u16][1] + e[u16][0] - z1) * mt[u16][0];
-                    const float q2 = ex2(sx[u16][2] + e[u16][1] - z0) * mt[u16][1], q3 = ex2(sx[u16][3] + e[u16][1] - z1) * mt[u16][1];
-                    const __half2 h01 = __floats2half2_rn(q0, q1), h23 = __floats2half2_rn(q2, q3);
-                    const __half2 l01 = __floats2half2_rn(q0 - __low2float(h01), q1 - __high2float(h01));
-                    const __half2 l23 = __floats2half2_rn(q2 - __low2float(h23), q3 - __high2float(h23));
-                    wh[u16][0] = movmatrix_t(bits_of(h01));
-                    wh[u16][1] = movmatrix_t(bits_of(h23));
-                    wl[u16][0] = movmatrix_t(bits_of(l01));
-                    wl[u16][1] = movmatrix_t(bits_of(l23));
-                }
-            } else {
-                // P as a bf16 pair hi + lo (lo = p - hi exactly): about 16
-                // significant bits of the weights reach the float32 accumulator
-                const float e0 = ex2(sx[0][0] - o0), e1 = ex2(sx[0][1] - o1), e2 = ex2(sx[0][2] - o0), e3 = ex2(sx[0][3] - o1);
-                l[0] += e0 + e2;
-                l[1] += e1 + e3;
-                const uint32_t h01 = pack_bf16(e0, e1), h23 = pack_bf16(e2, e3);
-                wh[0][0] = movmatrix_t(h01);
-                wh[0][1] = movmatrix_t(h23);
-                wl[0][0] = movmatrix_t(pack_bf16(e0 - bf16_lo(h01), e1 - bf16_hi(h01)));
-                wl[0][1] = movmatrix_t(pack_bf16(e2 - bf16_lo(h23), e3 - bf16_hi(h23)));
-            }
-            if (__any_sync(0xffffffffu, be0 != 1.f || be1 != 1.f)) {  // some reference grew
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    acc[i][0] *= be0;
-                    acc[i][1] *= be1;
-                    acc[i][2] *= be0;
-                    acc[i][3] *= be1;
-                }
-            }
-            // O^T += V^T P^T
-            if constexpr (kFp8) {
-#pragma unroll
-                for (int u16 = 0; u16 < kSub; ++u16) {
-                    // V codes of keys 2c, 2c+1, 2c+8, 2c+9, dims 32g .. 32g+31
-                    uint32_t w[4][8];
-                    const uint8_t *vb = st + F::half;
-                    const int kr[4] = {2 * c4, 2 * c4 + 1, 2 * c4 + 8, 2 * c4 + 9};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint4 z0 = *reinterpret_cast<const uint4 *>(vb + swz8(16 * u16 + kr[i], 2 * g));
-                        const uint4 z1 = *reinterpret_cast<const uint4 *>(vb + swz8(16 * u16 + kr[i], 2 * g + 1));
-                        w[i][0] = z0.x;
-                        w[i][1] = z0.y;
-                        w[i][2] = z0.z;
-                        w[i][3] = z0.w;
-                        w[i][4] = z1.x;
-                        w[i][5] = z1.y;
-                        w[i][6] = z1.z;
-                        w[i][7] = z1.w;
-                    }
-                    // four dim tiles at a time: a hi and a lo product of one
-                    // tile follow each other at the MMA's latency
-#pragma unroll
-                    for (int i4 = 0; i4 < 16; i4 += 4) {
-                        uint32_t z[4][4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // codes of dims 32g + 2 (i4 + i) and + 1: {key, next key}
-                            // of the first dim, then of the second
-                            const int wi = (i4 + i) >> 1, b = 2 * (i & 1);
-                            const uint32_t sel = b | ((4 + b) << 4) | ((b + 1) << 8) | ((5 + b) << 12);
-                            f16_of_codes(__byte_perm(w[0][wi], w[1][wi], sel), z[i][0], z[i][1]);
-                            f16_of_codes(__byte_perm(w[2][wi], w[3][wi], sel), z[i][2], z[i][3]);
-                        }
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_half(acc[i4 + i], z[i][0], z[i][1], z[i][2], z[i][3], wh[u16][0], wh[u16][1]);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_half(acc[i4 + i], z[i][0], z[i][1], z[i][2], z[i][3], wl[u16][0], wl[u16][1]);
-                    }
-                }
-            } else {
-                const uint32_t vbs = s_base + slot * F::stage + F::half;
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    uint32_t f[4][4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        ldsm_x4_t(vbs + h * kPlane + swz(vr_, 2 * j + vcb), f[j][0], f[j][1], f[j][2], f[j][3]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t(&x4)[4] = f[j];
-                        mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], wh[0][0], wh[0][1]);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t(&x4)[4] = f[j];
-                        mma_bf16(acc[4 * h + j], x4[0], x4[1], x4[2], x4[3], wl[0][0], wl[0][1]);
-                    }
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&x.empty[slot]);
-        }
-        finish_pass(pc, pass);
+            finish_pass(pc, pass);
         }
     }
     __syncthreads();  // every staged tile is consumed (or the CTA gave up)
