@@ -171,8 +171,10 @@ __global__ void __launch_bounds__(kMapThreads) remap_kernel(const __grid_constan
 // distinct_src the src ids too.
 bool moves_ok(const int32_t *src, const int32_t *dst, int32_t n, int64_t limit, bool distinct_src) {
     std::vector<int32_t> s(src, src + n), d(dst, dst + n);
-    std::sort(s.begin(), s.end());
-    std::sort(d.begin(), d.end());
+    for (auto *v : {&s, &d}) {  // (a compaction plans its moves in order)
+        if (v->front() > v->back()) std::reverse(v->begin(), v->end());
+        if (!std::is_sorted(v->begin(), v->end())) std::sort(v->begin(), v->end());
+    }
     if (s.front() < 0 || d.front() < 0 || s.back() >= limit || d.back() >= limit) return false;
     if (std::adjacent_find(d.begin(), d.end()) != d.end()) return false;
     if (distinct_src && std::adjacent_find(s.begin(), s.end()) != s.end()) return false;
@@ -217,7 +219,8 @@ int copy_pages(const pkv_layout *L, int32_t page_pos, void *base, int32_t n_page
             a.first[a.n++] = static_cast<int32_t>(pieces);
             pieces += more;
         }
-        if (a.n == 0) break;  // nothing left but copies of no positions
+        if (a.n == 0 && i < n) return PKV_EINVAL;  // a page of more pieces than a grid has
+        if (a.n == 0) break;                       // nothing left but copies of no positions
         const cudaError_t e =
             launch_pdl(copy_kernel, static_cast<unsigned>(pieces), kCopyThreads, 0, stream, a);
         if (e != cudaSuccess) return PKV_ECUDA;
@@ -229,8 +232,10 @@ int remap_tables(int32_t *const *tables, const int32_t *n_table, int32_t n_table
                  const int32_t *dst, int32_t n_moves, cudaStream_t stream) {
     if (!moves_ok(src, dst, n_moves, INT64_MAX, true)) return PKV_EINVAL;
     std::vector<int32_t> order(static_cast<size_t>(n_moves));
-    for (int32_t i = 0; i < n_moves; ++i) order[i] = i;
-    std::sort(order.begin(), order.end(), [&](int32_t x, int32_t y) { return src[x] < src[y]; });
+    const bool down = src[0] > src[n_moves - 1];
+    for (int32_t i = 0; i < n_moves; ++i) order[i] = down ? n_moves - 1 - i : i;
+    const auto before = [&](int32_t x, int32_t y) { return src[x] < src[y]; };
+    if (!std::is_sorted(order.begin(), order.end(), before)) std::sort(order.begin(), order.end(), before);
     MapArgs a;
     // no dst is a src, so the groups of moves may follow each other in any order
     for (int32_t m0 = 0; m0 < n_moves; m0 += kMoves) {

@@ -146,7 +146,7 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
-_current = None  # (torch, current device's raw stream by device index), once torch is needed
+_current = None  # (torch, the current device, its raw stream by device index), once torch is needed
 
 
 def _torch_streams():
@@ -155,14 +155,17 @@ def _torch_streams():
         import torch
         # the raw handle without building a Stream object (about 3 us of a call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        _current = (torch, raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        if torch.cuda.is_available():
+            torch.cuda.init()
+        _current = (torch, getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
+                    raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
     return _current
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        torch, raw = _current or _torch_streams()
-        return raw(torch.cuda.current_device())
+        _, device, raw = _current or _torch_streams()
+        return raw(device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -184,7 +187,7 @@ def _here(what: str, *tensors, dtype=None):
         if t is not None and type(t) is not int:
             at = t.get_device()
             if dev is None and at >= 0:
-                dev = (_current or _torch_streams())[0].cuda.current_device()
+                dev = (_current or _torch_streams())[1]()
             if at != dev or not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
                 raise PkvError(EINVAL, f"{what}: not a contiguous tensor of the type on the current device")
             t = t.data_ptr()
