@@ -47,17 +47,19 @@ constexpr int kMaxPieces = 8;                // pieces of a split
 constexpr int kMaxSlices = 3;                // key slices of a piece
 constexpr int kSplitKeys = 640;              // keys of a piece at most
 constexpr int kMaxPages = kMaxPieces * kSplitKeys / 4 + 4;  // pages a CTA's run can touch
-// bf16 calls of more CTAs than this (two fill an SM) run them unclustered, each
-// on one to eight pieces, and merge in a second kernel: a cluster waits for
-// eight free places on neighbouring SMs, and each CTA starts and merges anew.
-// Measured, clustered against unclustered, windows of 512 keys: 32 streams (512
-// CTAs) 18.3 us against 16.6, 48 streams 27.2 against 26.0, 16 streams (256
-// CTAs) 9.4 against 11.2; of 4,096 keys: 24 streams 44.0 us against 38.3, 64
-// streams 96.7 against 92.9, 16 streams 24.2 against 26.5.  e4m3
-// calls stay clustered (48 streams of 4,096 keys 64.2 us against 79.9), and so
-// do those whose CTAs take more than 16 columns (64 streams of 32 columns and
-// 4,096 keys 146.6 us against 161.8).
-constexpr int kClusterCtas = 304;
+constexpr int kCtas = 304;                   // that the GPU holds at once, two an SM
+// What a call of clusters costs against one of runs (CTAs on one to eight
+// pieces each, merged by a second kernel), in keys of a wave of CTAs: a wave
+// takes its CTAs' keys and kStartKeys (start, first tile, merge), and runs take
+// kCombKeys more.  A run's keys count 9/10 where the bytes bound the call (a
+// wave that is not full is faster) and 12/10 with e4m3 pages and CTAs of more
+// than 16 columns, which the latencies of a tile bound.  Measured, clusters
+// against the runs that this picks or would pick: bf16, windows of 4,096 keys,
+// 16 streams 23.9 us against 25.8, 24 streams 43.4 against 37.5, 64 streams 95.4
+// against 86.5; of 512 keys, 64 streams 35.4 against 24.2; e4m3, 4,096 keys, 24
+// streams 38.7 against 41.2, 48 streams 63.9 against 76.6, 64 streams 85.0
+// against 78.1; of 512 keys, 32 streams 22.8 against 19.6.
+constexpr int kStartKeys = 300, kCombKeys = 100;
 constexpr int kFreshGuard = 32;              // rows below the new tokens that a kernel just before may write
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
 
@@ -106,6 +108,7 @@ struct WinArgs {
     int32_t pieces;     // pieces of a split
     int32_t run;        // pieces of a CTA; 0: one, and the split's CTAs are a cluster
     int32_t even;       // splits of each stream where all have as many, else 0
+    int32_t even_cols;  // query columns (all KV heads) of each stream, likewise
 };
 
 // CTAs that share a (stream, KV head)'s columns.
@@ -1114,20 +1117,20 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
 }
 
 // Merge of the pieces' partials for calls whose CTAs are not clustered: a CTA a
-// query column, four groups of 64 threads (four dims each) that load every
-// fourth piece; the split's pieces and the splits in order, as a cluster merges
-// its CTAs' sums.
-constexpr int kCombThreads = 256;
+// query column, a thread four dims; the split's pieces and the splits in order,
+// as a cluster merges its CTAs' sums.  A thread loads all pieces of a split
+// together, and a CTA is small (no shared memory, two warps) so that it can
+// start beside the last partial CTAs.
+constexpr int kCombThreads = kHeadDim / 4;
 __global__ void __launch_bounds__(kCombThreads)
     window_combine(const __grid_constant__ Common c, const __grid_constant__ WinArgs a) {
-    __shared__ float2 sh_ml[kMaxPieces];
-    __shared__ float4 sh_o[kMaxPieces][64];
     pdl_trigger();  // the next kernel waits for this grid before it reads what it writes
     const int i = static_cast<int>(blockIdx.x);
-    const int s = find_seq(c.n_seqs, i, [&](int t) { return c.seq[t].comb_off; });
+    const int s = a.even_cols ? i / a.even_cols : find_seq(c.n_seqs, i, [&](int t) { return c.seq[t].comb_off; });
     const SeqDev &sd = c.seq[s];
-    const int r = i - sd.comb_off, ncols = sd.ncols, unit = r / ncols, col = r - unit * ncols, G = c.group;
-    const int grp = threadIdx.x >> 6, d4 = threadIdx.x & 63, d = 4 * d4, j = col / G;
+    const int r = a.even_cols ? i - s * a.even_cols : i - sd.comb_off;
+    const int ncols = sd.ncols, unit = r / ncols, col = r - unit * ncols, G = c.group;
+    const int d = 4 * static_cast<int>(threadIdx.x), j = col / G;
     const int64_t n_part = (int64_t)sd.nsplit * a.pieces;
     const float *acc = a.ws + sd.ws_off + (unit * n_part * ncols + col) * kHeadDim + d;
     const float *ml = a.ws + sd.ws_off + (int64_t)c.n_kv_heads * n_part * ncols * kHeadDim + (unit * n_part * ncols + col) * 2;
@@ -1136,31 +1139,24 @@ __global__ void __launch_bounds__(kCombThreads)
     pdl_wait();
     Sum t;
     for (int sp = 0; sp < sd.nsplit; ++sp) {
-        for (int p = grp; p < a.pieces; p += kCombThreads / 64) {
-            const int64_t p0 = (int64_t)sp * a.pieces + p;
-            sh_o[p][d4] = __ldcg(reinterpret_cast<const float4 *>(acc + p0 * ncols * kHeadDim));
-            if (d4 == 0) sh_ml[p] = __ldcg(reinterpret_cast<const float2 *>(ml + p0 * ncols * 2));
+        const int64_t p0 = (int64_t)sp * a.pieces;
+        const Sum x = merge_parts<kMaxPieces>(
+            a.pieces, [&](int p) { return __ldcg(reinterpret_cast<const float2 *>(ml + (p0 + p) * ncols * 2)); },
+            [&](int p) { return __ldcg(reinterpret_cast<const float4 *>(acc + (p0 + p) * ncols * kHeadDim)); });
+        if (sp == 0) {
+            t = x;
+        } else {
+            const float M = fmaxf(t.m, x.m);
+            const float wt = M == -INFINITY ? 0.f : ex2(t.m - M), wx = M == -INFINITY ? 0.f : ex2(x.m - M);
+            t.l = wt * t.l + wx * x.l;
+            t.o.x = wt * t.o.x + wx * x.o.x;
+            t.o.y = wt * t.o.y + wx * x.o.y;
+            t.o.z = wt * t.o.z + wx * x.o.z;
+            t.o.w = wt * t.o.w + wx * x.o.w;
+            t.m = M;
         }
-        __syncthreads();
-        if (grp == 0) {
-            const Sum x = merge_parts<kMaxPieces>(
-                a.pieces, [&](int p) { return sh_ml[p]; }, [&](int p) { return sh_o[p][d4]; });
-            if (sp == 0) {
-                t = x;
-            } else {
-                const float M = fmaxf(t.m, x.m);
-                const float wt = M == -INFINITY ? 0.f : ex2(t.m - M), wx = M == -INFINITY ? 0.f : ex2(x.m - M);
-                t.l = wt * t.l + wx * x.l;
-                t.o.x = wt * t.o.x + wx * x.o.x;
-                t.o.y = wt * t.o.y + wx * x.o.y;
-                t.o.z = wt * t.o.z + wx * x.o.z;
-                t.o.w = wt * t.o.w + wx * x.o.w;
-                t.m = M;
-            }
-        }
-        if (sp + 1 < sd.nsplit) __syncthreads();  // the sums are read before the next split's
     }
-    if (grp == 0) write_out(out, t);
+    write_out(out, t);
 }
 
 using WindowKernel = void (*)(Common, DecodeMaps, WinArgs);
@@ -1194,7 +1190,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
     const int pieces = window_pieces(window, n_sink);
     const int tile = c.kv_fp8 ? Cfg<true>::tile : Cfg<false>::tile;
     bool split = false, wide = false;
-    int64_t items = 0, cols = 0, floats = 0;
+    int64_t items = 0, cols = 0, floats = 0, keys = 0;
     for (int s = 0; s < c.n_seqs; ++s) {
         SeqDev &d = c.seq[s];
         d.ncols = d.n_new * c.group;
@@ -1210,7 +1206,8 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
         wide |= d.ncols > kBlockCols;
         items += (int64_t)c.n_kv_heads * d.nsplit * col_blocks(false, d.ncols);
     }
-    wide = wide && items * pieces > kClusterCtas;
+    const bool many = items * pieces > kCtas;
+    wide = wide && many;
     items = 0;
     for (int s = 0; s < c.n_seqs; ++s) {
         SeqDev &d = c.seq[s];
@@ -1220,31 +1217,35 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
         if (d.ncols == 0) continue;
         items += (int64_t)c.n_kv_heads * d.nsplit * col_blocks(wide, d.ncols);
         cols += (int64_t)c.n_kv_heads * d.ncols;
+        keys += (int64_t)c.n_kv_heads * col_blocks(wide, d.ncols) * window_span(d.len, d.n_new, window, n_sink, tile).nkeys;
         floats += (int64_t)c.n_kv_heads * d.nsplit * pieces * d.ncols * (kHeadDim + 2);
         floats = (floats + 63) / 64 * 64;
     }
     if (items * pieces > INT32_MAX) return PKV_EINVAL;
-    const bool combine = pieces > 1 && (split || (!c.kv_fp8 && !wide && items * pieces > kClusterCtas));
+    // the least cost: a cluster a split, or runs of pieces (which have to merge splits)
+    const int64_t per = items ? keys / (items * pieces) : 0;  // keys of a piece
+    const auto waves = [&](int run) { return (items * pieces / run + kCtas - 1) / kCtas; };
+    int64_t best = split ? INT64_MAX : waves(1) * (per + kStartKeys) * 10;
+    plan->run = 0;
+    for (int run = 1; pieces > 1 && run <= pieces; run *= 2) {
+        const int64_t cost = waves(run) * (run * per * (c.kv_fp8 || wide ? 12 : 9) + kStartKeys * 10) + kCombKeys * 10;
+        if (cost < best) {
+            best = cost;
+            plan->run = run;
+        }
+    }
+    const bool combine = plan->run > 0;
     plan->items = static_cast<int32_t>(items);
     plan->comb = combine ? static_cast<int32_t>(cols) : 0;
     plan->pieces = pieces;
     plan->wide = wide;
-    plan->run = 0;
-    // pieces of a CTA: the least of waves x (pieces + half a piece's time to
-    // start), the larger run where two are alike
-    if (combine) {
-        int64_t best = INT64_MAX;
-        for (int run = 1; run <= pieces; run *= 2) {
-            const int64_t cost = ((items * pieces / run + kClusterCtas - 1) / kClusterCtas) * (2 * run + 1);
-            if (cost <= best) {
-                best = cost;
-                plan->run = run;
-            }
-        }
-    }
     plan->ctas = static_cast<int32_t>(items * (pieces / std::max(1, plan->run)));
-    plan->stash_off = combine ? floats : 0;
-    plan->ws_bytes = static_cast<size_t>(plan->stash_off) * 4 + (wide ? (size_t)plan->ctas * kStash * sizeof(float4) : 0);
+    // sized for either kind of call, so that the size for a stream's longest
+    // length covers every shorter one
+    const bool some = pieces > 1 && (split || many);
+    plan->stash_off = some ? floats : 0;
+    plan->ws_bytes = static_cast<size_t>(plan->stash_off) * 4 +
+                     (wide ? static_cast<size_t>(items * pieces) * kStash * sizeof(float4) : 0);
     return PKV_OK;
 }
 
@@ -1268,11 +1269,12 @@ int launch_window(const Common &c, const WindowPlan &plan, const DecodeMaps &map
         }) != PKV_OK)
         return PKV_ECUDA;
     WinArgs a{q, out, ws, reinterpret_cast<float4 *>(ws + plan.stash_off), k_new, v_new, ik_new, window, n_sink,
-              plan.pieces, plan.run, 0};
-    if (plan.items % c.n_seqs == 0) {
-        a.even = plan.items / c.n_seqs;
-        for (int s = 0; s < c.n_seqs; ++s)
-            if (c.seq[s].work_off != s * a.even) a.even = 0;
+              plan.pieces, plan.run, 0, 0};
+    if (plan.items % c.n_seqs == 0) a.even = plan.items / c.n_seqs;
+    if (plan.comb % c.n_seqs == 0) a.even_cols = plan.comb / c.n_seqs;
+    for (int s = 0; s < c.n_seqs; ++s) {
+        if (c.seq[s].work_off != s * a.even) a.even = 0;
+        if (c.seq[s].comb_off != s * a.even_cols) a.even_cols = 0;
     }
     const bool clustered = plan.run == 0;
     cudaLaunchConfig_t cfg = {};

@@ -110,3 +110,21 @@ def test_chunk_refusals_before_launch():
     assert _chunk(lay, [_seq(lay, n_new=601)]) == pkv.EINVAL
     assert _chunk(lay, [_seq(lay, length=801, n_new=30)]) == pkv.EINVAL
     assert pkv.load().pkv_window_prefill_ws_size(ctypes.byref(lay), pkv._seqs([s])[0], 1, 4, 100, 4, None) == pkv.EINVAL
+
+
+@pytest.mark.parametrize("fmt", [pkv.KV_BF16, pkv.KV_E4M3])
+@pytest.mark.parametrize("streams,hq,window", [(24, 16, 4096), (64, 16, 512), (7, 8, 9000), (64, 64, 60), (40, 16, 2047)])
+def test_the_workspace_of_the_longest_lengths_covers_shorter_ones(fmt, streams, hq, window):
+    rng = np.random.default_rng(streams + hq)
+    lay = pkv.layout(1, 2 if hq < 64 else 4, 256, 0, fmt)
+    group = hq // lay.n_kv_heads
+
+    def size(lens, new):
+        page = pkv.pg(1 << 20, None, pkv.page_elems(lay, 20000), 20000)
+        return pkv.window_decode_ws_size(lay, [pkv.seq(page, int(n), int(m)) for n, m in zip(lens, new)], hq, window, 4)
+
+    top_new = max(1, 32 // group)
+    most = size([20000] * streams, [top_new] * streams)
+    for _ in range(200):
+        lens = np.exp(rng.uniform(np.log(top_new), np.log(20000), streams)).astype(int).clip(top_new)
+        assert size(lens, rng.integers(0, top_new + 1, streams)) <= most
