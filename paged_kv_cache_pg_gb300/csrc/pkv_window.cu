@@ -20,18 +20,19 @@
 // slices; slices, pieces and splits merge in the order of the keys.
 //
 // A split's CTAs are a cluster that merges through distributed shared memory:
-// one launch, no workspace.  Calls of more CTAs than the GPU holds, and windows
-// of several splits, run unclustered instead, a CTA on one or more pieces, and
-// window_combine merges the pieces from the workspace.  Calls of many draft
+// one launch, no workspace.  Windows of several splits, and calls of more CTAs
+// than the GPU holds where a cost model says so, run unclustered instead, a CTA
+// on one or more pieces, and window_combine merges the pieces from the
+// workspace.  Calls of many draft
 // windows give a CTA 32 columns.  All of them round alike: a stream's bits do
 // not depend on its batch.
 //
 // What bounds it: the bytes of K and V where there are many (64 streams of
-// 4,096 bf16 keys: 539 MB in 92.3 us, 5.84 TB/s); whole waves of CTAs, two on
+// 4,096 bf16 keys: 539 MB in 87.4 us, 6.16 TB/s); whole waves of CTAs, two on
 // an SM, below that (32 streams of 4,096 e4m3 keys are 512 CTAs in two waves of
 // 21 us; a copy of the kernel without its MMAs and conversions takes 37.2 us of
-// 42.9); and for a few streams the launch, the first tile's way in and the
-// merge (one stream of 128 keys 7.0 us, four of 1,024 keys 8.0 us).  Two CTAs
+// 42.3); and for a few streams the launch, the first tile's way in and the
+// merge (one stream of 128 keys 6.6 us, four of 1,024 keys 7.6 us).  Two CTAs
 // share an SM, so one streams while the other starts or merges.
 #include <algorithm>
 #include <cuda_fp16.h>
