@@ -140,9 +140,14 @@ extern "C" int pkv_arena_create(const pkv_layout *layout, int32_t page_pos, void
     a->page_elems = ps;
     a->n_pages = static_cast<int32_t>(n);
     a->base = dev_base;
-    a->taken.assign(static_cast<size_t>(n), 0);
-    a->holders.assign(static_cast<size_t>(n), 0);
-    a->going.assign(static_cast<size_t>(n), 0);
+    try {
+        a->taken.assign(static_cast<size_t>(n), 0);
+        a->holders.assign(static_cast<size_t>(n), 0);
+        a->going.assign(static_cast<size_t>(n), 0);
+    } catch (...) {  // no host memory for the books of so many pages
+        delete a;
+        return PKV_EINVAL;
+    }
     a->n_free = a->n_pages;
     a->ops = kCudaOps;
     *out = a;
@@ -192,7 +197,13 @@ extern "C" int pkv_pages_give(pkv_arena *a, const int32_t *ids, int32_t n, cudaS
     if (!a || n < 0 || (n > 0 && !ids)) return PKV_EINVAL;
     std::lock_guard<std::mutex> g(a->mu);
     // every id must be in range, held, and listed once
-    std::vector<int32_t> v(ids, ids + n);
+    std::vector<int32_t> v;
+    try {
+        v.assign(ids, ids + n);
+        if (defer) a->pending.reserve(a->pending.size() + 1);
+    } catch (...) {  // no host memory for the sorted list
+        return PKV_EINVAL;
+    }
     std::sort(v.begin(), v.end());
     if (!held_once_each(a, v)) return PKV_EINVAL;
     if (n == 0) return PKV_OK;

@@ -544,9 +544,6 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         x.pages[j] = ok ? id : -1;
     }
     __syncthreads();
-    // nothing this CTA writes is read by the next kernel before its own wait
-    // (a decode reads no row within kFreshGuard of its new tokens early)
-    if (tid == 0) pdl_trigger();
 
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     float acc[16][4];  // O^T: 16 tiles of 16 dims, this lane's two columns
@@ -662,6 +659,11 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         }
         asm volatile("" ::"l"(qr));
         pdl_wait();
+        // The next kernel may start: the kernel before this one is done, and of
+        // what this one writes a decode reads no row before its own wait (none
+        // within kFreshGuard of its new tokens).  Let go before the wait, calls
+        // of 32 new tokens could have read rows of the last call but one.
+        if (tid == 0) pdl_trigger();
         uint32_t qf[16][2];
         if constexpr (kFp8) {
             // dims 64 c4 .. 64 c4 + 63 of the row, converted to f16 once

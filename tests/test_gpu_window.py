@@ -297,3 +297,63 @@ def test_token_by_token_with_pages_given_back():
         ok, report = within_tol(host_u16(o), attend(kf, vf, q, start + 1 + i, window, sinks))
         assert ok, (i, report)
     assert int(status) == 0 and dead >= 7
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_calls_of_32_tokens_follow_each_other_directly(fmt):
+    # each call stores 32 rows, and the next reads cached rows more than 32 below
+    # its own new ones before the call has finished
+    t = torch()
+    T, hkv, ptok, steps = 1024, 2, 16, 32
+    lay = pkv.layout(1, hkv, 256, 0, fmt)
+    ps, per = pkv.page_elems(lay, ptok), T // ptok
+    g = t.Generator(device="cuda").manual_seed(5)
+    table = t.randperm(per, device="cuda", generator=g).to(t.int32)
+    k, v, q = (t.randn(T, hkv, 256, device="cuda", generator=g).to(t.bfloat16) for _ in range(3))
+    outs = []
+    for wait in (True, False):
+        mem = t.full((per, ps), 0x7FC1, dtype=t.int16, device="cuda")
+        out = t.zeros_like(q)
+        status = t.zeros(1, dtype=t.int32, device="cuda")
+        calls = []
+        for i in range(steps):
+            at = slice(32 * i, 32 * i + 32)
+            seqs = pkv.batch([pkv.seq(pkv.pg(mem, table, ps, ptok, per), 32 * i + 32, 32)])
+            calls.append((seqs, q[at].contiguous(), out[at], k[at].contiguous(), v[at].contiguous()))
+        t.cuda.synchronize()
+
+        def run_all():
+            for seqs, qi, oi, ki, vi in calls:
+                pkv.window_decode(lay, seqs, 0, hkv, 200, 4, qi, oi, None, status=status, k_new=ki, v_new=vi)
+                if wait:
+                    t.cuda.synchronize()
+
+        if wait:
+            run_all()
+        else:
+            graph = t.cuda.CUDAGraph()
+            with t.cuda.graph(graph):
+                run_all()
+            for _ in range(5):
+                mem.fill_(0x7FC1)
+                out.zero_()
+                graph.replay()
+        t.cuda.synchronize()
+        assert int(status) == 0
+        outs.append((out.clone(), mem))
+    assert t.equal(outs[0][0], outs[1][0]) and t.equal(outs[0][1], outs[1][1])
+    assert outs[0][0].isfinite().all()
+
+
+@pytest.mark.parametrize("fmt", FMT)
+def test_more_contiguous_streams_than_copy_maps(fmt):
+    lens, hq, hkv, window, sinks = [int(x) for x in np.linspace(3, 700, 40)], 16, 2, 300, 4
+    lay = pkv.layout(1, hkv, 256, 0, fmt)
+    streams = streams_of(lens, hkv, seed=500)
+    q = queries_of([1] * 40, hq, seed=500)
+    a = Windowed(lay, streams, [1] * 40, window, sinks, None)
+    b = Windowed(lay, streams, [1] * 40, window, sinks, 32, seed=3)
+    got = run(a, 0, hq, q)
+    ok, report = within_tol(got, a.reference(0, q))
+    assert ok, report
+    assert np.array_equal(got, run(b, 0, hq, q))
