@@ -24,19 +24,22 @@
 //               both kept the tensor pipe waiting while it waited on barriers
 //               and committed: a prompt of 8,192 at a window of 1,024 took 157 us,
 //               and takes 144)
-//   warps 13,14 fill a ring of six 16 KB slots each, K and V, by TMA
-// Per tile: S = Q K^T -> TMEM, P = softmax numerators in fp16 -> shared
-// memory, O += P V -> TMEM.  Q sits in TMEM (the S product's A operand), and
-// the next item's Q goes there while this item's last tile is in the softmax
+//   warps 13,14 fill a ring of five 16 KB slots each, K and V, by TMA
+// Per tile: S = Q K^T -> TMEM, P = softmax numerators in fp16 -> shared memory
+// (two buffers: a tile's P is written while the last tile's product runs), O +=
+// P V -> TMEM.  Q sits in TMEM (the S product's A operand), and the next item's
+// Q goes there, a half at a time, while this item's last tile is in the softmax
 // and its PV product; O is read while the next item's first tile is scored.
 // O is rescaled only when a row's maximum grows by more than 2^8.
 //
-// What bounds it: the tensor pipe and its operands' way through shared memory,
-// about 1.7 us a tile of 128 keys where 1.4 us is this card's rate for its two
-// products, and the masked parts of the tiles at both ends of a window.  8,192
-// queries at a window of 1,024 (129 GFLOP that some query sees): 144 us, 896
-// TFLOP/s; 512 queries at 31,000 with a window of 4,096 (34 GFLOP in 64 items,
-// split over the SMs): 57 us, 7 of them the gather and 6 the combine.
+// What bounds it: the operands' way through shared memory.  A 128-key tile
+// brings 128 KB of K and V in, its products read 160 KB and P takes 64, about
+// 2,800 cycles of the memory's width beside 2,600 of the products; a tile takes
+// 3,400 (1.75 us).  Beside that the end of an item costs about a tile and a half
+// (its masked tiles, its O out, the next item's masked start).  8,192 queries at
+// a window of 1,024 (129 GFLOP that some query sees): 141 us, 914 TFLOP/s; 512
+// queries at 31,000 with a window of 4,096 (34 GFLOP in 64 items, split over the
+// SMs): 54 us, 6 of them the gather and 6 the combine.
 #include <algorithm>
 #include <climits>
 
@@ -57,9 +60,10 @@ constexpr int kKRegion = kN * 128;   // one 64-dim region of 128 K rows
 constexpr int kVKeys = 32;            // keys of a V slot
 constexpr int kVRegion = kVKeys * 128;  // one 64-dim region of its rows
 constexpr int kSlotBytes = kKRegion; // K of the tile's keys over 64 dims, or V of 32 keys
-constexpr int kSlots = 6;            // of each ring
+constexpr int kSlots = 5;            // of each ring
 constexpr int kPRegion = kM * 128;   // 64 keys of the 128 P rows
-constexpr int kOffK = 2 * kPRegion, kOffV = kOffK + kSlots * kSlotBytes;
+constexpr int kPBuf = 2 * kPRegion;  // P of a tile; two tiles' buffers
+constexpr int kOffK = 2 * kPBuf, kOffV = kOffK + kSlots * kSlotBytes;
 static_assert(4 * kVRegion == kSlotBytes, "a V slot is 32 keys of four regions");
 constexpr int kOffRed = kOffV + kSlots * kSlotBytes;   // [tile parity][half][row] bf16 row maxima
 constexpr int kOffSum = kOffRed + 2 * 2 * kM * 2;         // [half][row] float sums of an item
@@ -72,10 +76,10 @@ enum Bars {
     kVEmpty = 3 * kSlots,
     kSFull = 4 * kSlots,  // S of a tile is in TMEM
     kSEmpty,              // ... and has been read
-    kPFull,               // P of a tile is in shared memory
-    kODone,               // a tile's PV product is done
-    kQFull,               // an item's Q is in TMEM
-    kQEmpty,              // ... and its last S product is done
+    kPFull,               // P of an even or odd tile is in shared memory (two barriers)
+    kODone = kPFull + 2,  // an even or odd tile's PV product is done (two barriers)
+    kQFull = kODone + 2,               // a half of an item's Q is in TMEM (two barriers)
+    kQEmpty = kQFull + 2, // ... and its last S product is done
     kOLast,               // an item's last PV product is done
     kOFree,               // ... and its O, sums and maxima have been read
     kSums,                // an item's sums and maxima are in shared memory
@@ -180,6 +184,33 @@ __device__ __forceinline__ uint64_t below(int n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
+// Transpose over each four lanes: word j of lane i goes to word i of lane j.
+// Rows that lie one a lane are so read and written 64 bytes of a row at a time
+// by four lanes (16 bytes of 32 rows an instruction, as the lanes hold them,
+// kept the load and store units of an item's Q and O busy for 8,000 cycles).
+__device__ __forceinline__ uint4 shfl_xor16(const uint4 &v, int m) {
+    return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                      __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
+}
+__device__ __forceinline__ uint4 pick(bool b, const uint4 &x, const uint4 &y) {
+    return make_uint4(b ? x.x : y.x, b ? x.y : y.y, b ? x.z : y.z, b ? x.w : y.w);
+}
+__device__ __forceinline__ void quad_transpose(uint4 *v, int lane) {
+    const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+    for (int p = 0; p < 4; p += 2) {
+        const uint4 got = shfl_xor16(pick(b0, v[p], v[p + 1]), 1);
+        v[p] = pick(b0, got, v[p]);
+        v[p + 1] = pick(b0, v[p + 1], got);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const uint4 got = shfl_xor16(pick(b1, v[p], v[p + 2]), 2);
+        v[p] = pick(b1, got, v[p]);
+        v[p + 2] = pick(b1, v[p + 2], got);
+    }
+}
+
 // bf16 bits of a float rounded up (toward +infinity).
 __device__ __forceinline__ uint16_t bf16_up(float x) {
     uint32_t u = __float_as_uint(x);
@@ -212,8 +243,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars[kSFull], 1);
         mbar_init(&bars[kSEmpty], kSoftThreads);
         mbar_init(&bars[kPFull], kSoftThreads);
+        mbar_init(&bars[kPFull + 1], kSoftThreads);
         mbar_init(&bars[kODone], 1);
+        mbar_init(&bars[kODone + 1], 1);
         mbar_init(&bars[kQFull], kEdgeThreads);
+        mbar_init(&bars[kQFull + 1], kEdgeThreads);
         mbar_init(&bars[kQEmpty], 1);
         mbar_init(&bars[kOLast], 1);
         mbar_init(&bars[kOFree], kEdgeThreads);
@@ -326,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // correct this thread's half of O: the previous tile's
                     // products must be in it first (some row of the warp had a
                     // maximum before, so this is not the item's first tile)
-                    if (!(ok = wait_warp(kODone, T - 1))) break;
+                    if (!(ok = wait_warp(kODone + ((T - 1) & 1), (T - 1) >> 1))) break;
                     tc_fence_after();
                     const float m_new = fmaxf(m_used, mx);
                     const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
@@ -360,15 +394,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p16[j / 2] = pack_f16(p0, p1);
                 }
                 l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-                // the P rows are free once the last tile's products are done
-                if (T > 0 && !(ok = wait_warp(kODone, T - 1))) break;
+                // this buffer's P rows are free once the products of the tile
+                // before the last are done
+                if (T > 1 && !(ok = wait_warp(kODone + (T & 1), (T >> 1) - 1))) break;
 #pragma unroll
                 for (int ch = 0; ch < 8; ++ch)
-                    *reinterpret_cast<uint4 *>(p_row + ((ch ^ (r & 7)) << 4)) =
+                    *reinterpret_cast<uint4 *>(p_row + (T & 1) * kPBuf + ((ch ^ (r & 7)) << 4)) =
                         make_uint4(p16[4 * ch], p16[4 * ch + 1], p16[4 * ch + 2], p16[4 * ch + 3]);
                 fence_async_smem();
                 tc_fence_before();
-                mbar_arrive(&bars[kPFull]);
+                mbar_arrive(&bars[kPFull + (T & 1)]);
             }
             if (!ok) break;
             // the row's sum (this thread's half) and maximum, for the edge warps
@@ -386,13 +421,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int col = t.col0 + r, j = col / G;
             return ((int64_t)c.seq[t.s].tok_off + j) * c.n_q_heads + t.kvh * G + (col - j * G);
         };
-        // A half of the row's Q (128 dims) from global memory, and into TMEM
+        // A half of the rows' Q (128 dims) from global memory, and into TMEM
+        const int quad = lane & ~3, word = lane & 3;
         uint4 qv[16];
         auto load_q = [&](const Item &t, int half) {
-            const bool row_ok = r < t.rows;
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + (row_ok ? q_row(t) : 0) * kHeadDim + 128 * half);
+            const int64_t mine = r < t.rows ? q_row(t) : -1;
+            int64_t row[4];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) qv[j] = row_ok ? __ldg(src + j) : make_uint4(0, 0, 0, 0);
+            for (int i = 0; i < 4; ++i) row[i] = shfl64(mine, quad + i);
+#pragma unroll
+            for (int j = 0; j < 16; j += 4)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    qv[j + i] = row[i] >= 0 ? __ldg(reinterpret_cast<const uint4 *>(a.q + row[i] * kHeadDim + 128 * half) + j + word)
+                                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int j = 0; j < 16; j += 4) quad_transpose(qv + j, lane);
         };
         auto put_q = [&](int half) {
 #pragma unroll
@@ -408,11 +452,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 tmem_st32(lane_base + kQCol + 64 * half + 32 * ch, w);
             }
-        };
-        auto q_stored = [&]() {
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             tc_fence_before();
-            mbar_arrive(&bars[kQFull]);
+            mbar_arrive(&bars[kQFull + half]);
         };
         uint32_t it = 0;
         Item t = item_at(c, a, blockIdx.x);
@@ -420,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         put_q(0);
         load_q(t, 1);
         put_q(1);
-        q_stored();
         for (int i = blockIdx.x; i < a.n_items; i += gridDim.x, ++it) {
             const int next = i + gridDim.x;
             Item t2 = t;
@@ -438,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 put_q(0);
                 load_q(t2, 1);
                 put_q(1);
-                q_stored();
             }
             if (!wait_warp(kSums, it)) break;
             if (!wait_warp(kOLast, it)) break;
@@ -449,47 +489,58 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float l = sums[r] + sums[kM + r];
             const float m = bf16_float(reinterpret_cast<const uint16_t *>(smem + kOffMax)[r]) * kScaleLog2;
             const float inv = l > 0.f ? 1.f / l : 0.f;
-            uint16_t *orow = a.out + (row_ok ? q_row(t) : 0) * kHeadDim;
             const int64_t prow = ((int64_t)t.kvh * sd.nsplit + t.split) * sd.ncols + t.col0 + r;
+            const int64_t mine = !row_ok ? -1 : single ? q_row(t) : prow;  // output row, or the partials'
+            int64_t row[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) row[j] = shfl64(mine, quad + j);
             float *part_acc = a.ws + sd.ws_off;
             float *part_ml = part_acc + (int64_t)H * sd.nsplit * sd.ncols * kHeadDim;
-            bool finite = true;  // a V entry beyond fp16's range makes O infinite or NaN
+            float odd = 0.f;  // NaN once a sum is not finite: a V entry beyond fp16's range
 #pragma unroll 1
             for (int ch = 0; ch < 8; ++ch) {
                 uint32_t o[32];
-                __syncwarp();  // rows past the tile's end skipped the stores below
+                __syncwarp();
                 tmem_ld32(lane_base + kOCol + 32 * ch, o);
                 if (ch == 7) {  // the next item's first PV product may write O
                     tc_fence_before();
                     mbar_arrive(&bars[kOFree]);
                 }
-                if (!row_ok) continue;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) finite &= fabsf(__uint_as_float(o[j])) <= 3.402823466e38f;
+                for (int j = 0; j < 32; ++j) odd = fmaf(__uint_as_float(o[j]), 0.f, odd);
                 if (single) {
+                    uint4 v[4];
 #pragma unroll
-                    for (int j = 0; j < 32; j += 8) {
-                        uint4 v;
-                        v.x = pack_bf16(__uint_as_float(o[j]) * inv, __uint_as_float(o[j + 1]) * inv);
-                        v.y = pack_bf16(__uint_as_float(o[j + 2]) * inv, __uint_as_float(o[j + 3]) * inv);
-                        v.z = pack_bf16(__uint_as_float(o[j + 4]) * inv, __uint_as_float(o[j + 5]) * inv);
-                        v.w = pack_bf16(__uint_as_float(o[j + 6]) * inv, __uint_as_float(o[j + 7]) * inv);
-                        *reinterpret_cast<uint4 *>(orow + 32 * ch + j) = v;
+                    for (int j = 0; j < 4; ++j) {
+                        v[j].x = pack_bf16(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
+                        v[j].y = pack_bf16(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
+                        v[j].z = pack_bf16(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
+                        v[j].w = pack_bf16(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
                     }
-                } else {
-                    float *dst = part_acc + prow * kHeadDim + 32 * ch;
+                    quad_transpose(v, lane);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<float4 *>(dst + j) =
-                            make_float4(__uint_as_float(o[j]), __uint_as_float(o[j + 1]),
-                                        __uint_as_float(o[j + 2]), __uint_as_float(o[j + 3]));
+                    for (int j = 0; j < 4; ++j)
+                        if (row[j] >= 0) *(reinterpret_cast<uint4 *>(a.out + row[j] * kHeadDim + 32 * ch) + word) = v[j];
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            v[j] = make_uint4(o[16 * h + 4 * j], o[16 * h + 4 * j + 1], o[16 * h + 4 * j + 2], o[16 * h + 4 * j + 3]);
+                        quad_transpose(v, lane);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (row[j] >= 0)
+                                *(reinterpret_cast<uint4 *>(part_acc + row[j] * kHeadDim + 32 * ch + 16 * h) + word) = v[j];
+                    }
                 }
             }
             if (row_ok && !single) {
                 part_ml[prow * 2 + 0] = m;
                 part_ml[prow * 2 + 1] = l;
             }
-            if (!finite && c.status) atomicOr(c.status, PKV_DEV_RANGE);
+            if (row_ok && odd != 0.f && c.status) atomicOr(c.status, PKV_DEV_RANGE);
             t = t2;
         }
     } else if (warp == kWarpS || warp == kWarpPv) {
@@ -516,14 +567,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint64_t desc_k = smem_desc(0, 16, 1024);
                 int ntiles = item_at(c, a, blockIdx.x).ntiles, next_tiles = 0;
                 for (int i = blockIdx.x; ok && i < a.n_items; i += gridDim.x, ++it, ntiles = next_tiles) {
-                    ok = wait(kQFull, it);
-                    tc_fence_after();
                     for (int n = 0; ok && n < ntiles; ++n, ++T) {
                         if (T > 0 && !(ok = wait(kSEmpty, T - 1))) break;
                         tc_fence_after();
                         // S = Q K^T, 64 dims a slot
 #pragma unroll 1
                         for (int qt = 0; qt < 4; ++qt) {
+                            if (n == 0 && qt % 2 == 0 && !(ok = wait(kQFull + qt / 2, it))) break;
                             uint32_t kb;
                             if (!(ok = take(kKFull, kOffK, kb))) break;
                             const uint64_t dk = desc_k + (kb >> 4);
@@ -548,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int ntiles = t.ntiles, key0 = t.key0, total = t.k.total;
                     for (int n = 0; ok && n < ntiles; ++n, ++T) {
                         const int nv = v_slots(key0 + n * kN, total);
-                        if (!(ok = wait(kPFull, T))) break;
+                        if (!(ok = wait(kPFull + (T & 1), T >> 1))) break;
                         if (n == 0 && it > 0 && !(ok = wait(kOFree, it - 1))) break;
                         tc_fence_after();
                         // O += P V, 32 keys a slot
@@ -556,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int vs = 0; vs < nv; ++vs) {
                             uint32_t vb;
                             if (!(ok = take(kVFull, kOffV, vb))) break;
-                            const uint64_t dp = desc_p + (((vs >> 1) * kPRegion + (vs & 1) * 64) >> 4), dv = desc_v + (vb >> 4);
+                            const uint64_t dp = desc_p + (((T & 1) * kPBuf + (vs >> 1) * kPRegion + (vs & 1) * 64) >> 4), dv = desc_v + (vb >> 4);
 #pragma unroll
                             for (int k2 = 0; k2 < 2; ++k2)
                                 tc_mma(tmem + kOCol, dp + (k2 * 32 >> 4), dv + (k2 * 2048 >> 4), idesc,
@@ -564,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             give(kVEmpty);
                         }
                         if (!ok) break;
-                        tc_commit(&bars[kODone]);
+                        tc_commit(&bars[kODone + (T & 1)]);
                         if (n + 1 == ntiles) tc_commit(&bars[kOLast]);
                         if (n == 0 && i + (int)gridDim.x < a.n_items) t = item_at(c, a, i + gridDim.x);
                     }
