@@ -23,7 +23,7 @@
 //   warp 12     issues the S products, warp 15 the PV products (one thread for
 //               both kept the tensor pipe waiting while it waited on barriers
 //               and committed: a prompt of 8,192 at a window of 1,024 took 157 us,
-//               and takes 144)
+//               against 144)
 //   warps 13,14 fill a ring of five 16 KB slots each, K and V, by TMA
 // Per tile: S = Q K^T -> TMEM, P = softmax numerators in fp16 -> shared memory
 // (two buffers: a tile's P is written while the last tile's product runs), O +=
@@ -33,9 +33,9 @@
 // O is rescaled only when a row's maximum grows by more than 2^8.
 //
 // What bounds it: the operands' way through shared memory.  A 128-key tile
-// brings 128 KB of K and V in, its products read 160 KB and P takes 64, about
-// 2,800 cycles of the memory's width beside 2,600 of the products; a tile takes
-// 3,400 (1.75 us).  Beside that the end of an item costs about a tile and a half
+// brings 128 KB of K and V in, 32 KB of P are written and the products read
+// 160 KB, 2,500 cycles of the memory's width beside 2,600 of the products; a
+// tile takes 3,400 (1.75 us).  Beside that the end of an item costs about a tile and a half
 // (its masked tiles, its O out, the next item's masked start).  8,192 queries at
 // a window of 1,024 (129 GFLOP that some query sees): 141 us, 914 TFLOP/s; 512
 // queries at 31,000 with a window of 4,096 (34 GFLOP in 64 items, split over the
