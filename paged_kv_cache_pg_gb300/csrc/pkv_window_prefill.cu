@@ -37,9 +37,9 @@
 // 160 KB, 2,500 cycles of the memory's width beside 2,600 of the products; a
 // tile takes 3,400 (1.75 us).  Beside that the end of an item costs about a tile and a half
 // (its masked tiles, its O out, the next item's masked start).  8,192 queries at
-// a window of 1,024 (129 GFLOP that some query sees): 141 us, 914 TFLOP/s; 512
+// a window of 1,024 (129 GFLOP that some query sees): 136 us, 952 TFLOP/s; 512
 // queries at 31,000 with a window of 4,096 (34 GFLOP in 64 items, split over the
-// SMs): 54 us, 6 of them the gather and 6 the combine.
+// SMs): 53 us, 6 of them the gather and 6 the combine.
 #include <algorithm>
 #include <climits>
 
@@ -182,6 +182,34 @@ __device__ __forceinline__ int row_of(const Gathered &g, const Keys &k, int v) {
 // The lowest n of 64 bits.
 __device__ __forceinline__ uint64_t below(int n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
+}
+
+// Two float32 operations an instruction, each rounded as alone: the softmax and
+// edge warps' issue slots count (a prompt of 8,192 took 141.0 us with single
+// ones, 135.9 with these).
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
 }
 
 // Transpose over each four lanes: word j of lane i goes to word i of lane j.
@@ -384,16 +412,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // offset is 0 while every score so far was masked).  fp16: 11
                 // significant bits, weights at most 2^8 with the lazy rescale
                 const float m_off = m_used == -INFINITY ? 0.f : m_used;
-                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 scale = make_float2(kScaleLog2, kScaleLog2), off = make_float2(-m_off, -m_off);
+                float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                 uint32_t p16[32];
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {
-                    const float p0 = ex2(fmaf(x[j], kScaleLog2, -m_off));
-                    const float p1 = ex2(fmaf(x[j + 1], kScaleLog2, -m_off));
-                    ps[(j >> 1) & 3] += p0 + p1;
-                    p16[j / 2] = pack_f16(p0, p1);
+                    float2 p = fma2(make_float2(x[j], x[j + 1]), scale, off);
+                    p.x = ex2(p.x);
+                    p.y = ex2(p.y);
+                    ps[(j >> 1) & 1] = add2(ps[(j >> 1) & 1], p);
+                    p16[j / 2] = pack_f16(p.x, p.y);
                 }
-                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
                 // this buffer's P rows are free once the products of the tile
                 // before the last are done
                 if (T > 1 && !(ok = wait_warp(kODone + (T & 1), (T >> 1) - 1))) break;
@@ -496,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j) row[j] = shfl64(mine, quad + j);
             float *part_acc = a.ws + sd.ws_off;
             float *part_ml = part_acc + (int64_t)H * sd.nsplit * sd.ncols * kHeadDim;
-            float odd = 0.f;  // NaN once a sum is not finite: a V entry beyond fp16's range
+            float2 odd = make_float2(0.f, 0.f);  // NaN once a sum is not finite: a V entry beyond fp16's range
 #pragma unroll 1
             for (int ch = 0; ch < 8; ++ch) {
                 uint32_t o[32];
@@ -507,15 +537,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(&bars[kOFree]);
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) odd = fmaf(__uint_as_float(o[j]), 0.f, odd);
+                for (int j = 0; j < 32; j += 2)
+                    odd = fma2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), make_float2(0.f, 0.f), odd);
                 if (single) {
                     uint4 v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        v[j].x = pack_bf16(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
-                        v[j].y = pack_bf16(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
-                        v[j].z = pack_bf16(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
-                        v[j].w = pack_bf16(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = 8 * j + 2 * e;
+                            const float2 z = mul2(make_float2(__uint_as_float(o[k]), __uint_as_float(o[k + 1])), make_float2(inv, inv));
+                            w[e] = pack_bf16(z.x, z.y);
+                        }
+                        v[j] = make_uint4(w[0], w[1], w[2], w[3]);
                     }
                     quad_transpose(v, lane);
 #pragma unroll
@@ -540,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 part_ml[prow * 2 + 0] = m;
                 part_ml[prow * 2 + 1] = l;
             }
-            if (row_ok && odd != 0.f && c.status) atomicOr(c.status, PKV_DEV_RANGE);
+            if (row_ok && odd.x + odd.y != 0.f && c.status) atomicOr(c.status, PKV_DEV_RANGE);
             t = t2;
         }
     } else if (warp == kWarpS || warp == kWarpPv) {
