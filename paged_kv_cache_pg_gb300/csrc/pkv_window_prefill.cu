@@ -37,7 +37,7 @@
 // 160 KB, 2,500 cycles of the memory's width beside 2,600 of the products; a
 // tile takes 3,400 (1.75 us).  Beside that the end of an item costs about a tile and a half
 // (its masked tiles, its O out, the next item's masked start).  8,192 queries at
-// a window of 1,024 (129 GFLOP that some query sees): 136 us, 952 TFLOP/s; 512
+// a window of 1,024 (129 GFLOP that some query sees): 135 us, 956 TFLOP/s; 512
 // queries at 31,000 with a window of 4,096 (34 GFLOP in 64 items, split over the
 // SMs): 53 us, 6 of them the gather and 6 the combine.
 #include <algorithm>
@@ -353,20 +353,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // one bit a key: the sinks' runs hold positions below slim,
                     // the window's part positions up to qpos that are in the
                     // row's window or among the sinks.  Compared key by key this
-                    // took 3 to 4 us a tile, a fifth of a nine-tile item; 16 keys
-                    // that every row of the warp sees are left alone.
+                    // took 3 to 4 us a tile, a fifth of a nine-tile item.  (Leaving
+                    // 16 keys alone that every row sees cost the other tiles more
+                    // than it saved these.)
                     const uint64_t part = below(t.k.sink_end - v0);
                     const uint64_t see = (part & below(t.k.slim - v0)) |
                                          (~part & below(qpos - kp0 + 1) & (~below(win0 - kp0 + 1) | below(n_sink - kp0)));
+                    const uint32_t lo = static_cast<uint32_t>(see), hi = static_cast<uint32_t>(see >> 32);
 #pragma unroll
-                    for (int j16 = 0; j16 < 4; ++j16) {
-                        const uint32_t m16 = static_cast<uint32_t>(see >> (16 * j16)) & 0xffffu;
-                        if (!__all_sync(0xffffffffu, m16 == 0xffffu)) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                if (!(m16 & (1u << j))) x[16 * j16 + j] = -INFINITY;
-                        }
-                    }
+                    for (int j = 0; j < 64; ++j)
+                        if (!((j < 32 ? lo : hi) & (1u << (j & 31)))) x[j] = -INFINITY;
                 }
                 // this half's max as eight interleaved chains, then the row's
                 // from the partner thread; both take it rounded up to bf16 (a
