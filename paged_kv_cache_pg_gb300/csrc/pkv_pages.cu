@@ -6,8 +6,8 @@
 // one piece, each of its threads kUnits units a CTA's width apart, all loaded
 // before any is stored, so an SM holds its resident CTAs' pieces in flight.
 // Measured: 96 pages of 7.9 MB (1,513 MB read and written) 226 us, 6.68 TB/s,
-// 98 % of a plain copy's rate; four pages' first 77 positions (19 MB) 8.6 us,
-// of which the host's call is most.
+// 98 % of a plain copy's rate; four pages' first 77 positions (19 MB) 5.9 us,
+// half of it the launch.
 // A whole page is one run of bytes.  A page's first n positions are, for each
 // layer, the first n rows of each K, V and indexer part, and the first n/4
 // pooled rows: the piece's units are counted over those rows only, and each
@@ -140,7 +140,9 @@ struct MapArgs {
     int32_t src[kMoves], dst[kMoves];  // src ascending
 };
 
-// A thread an entry; the moves, sorted by src, are searched in shared memory.
+// A thread an entry; the moves, sorted by src, are searched in shared memory.  A
+// few thousand entries are one wave of CTAs, bound by the launch (5 us a call with
+// its checks, four tables of 40 entries and 50 moves).
 __global__ void __launch_bounds__(kMapThreads) remap_kernel(const __grid_constant__ MapArgs a) {
     __shared__ int32_t src[kMoves], dst[kMoves];
     for (int i = threadIdx.x; i < a.n; i += kMapThreads) {

@@ -8,6 +8,7 @@ raises instead of falling back to anything.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Optional, Sequence
@@ -195,20 +196,24 @@ def _here(what: str, *tensors, dtype=None):
     return out
 
 
-_np = None
+_np = _i32 = None
 
 
-def _host_i32(a):
-    """A contiguous int32 numpy array of host integers, and its address."""
-    global _np
+def _host_i32(what: str, a):
+    """Host integers as int32: how many, and their bytes (which ctypes passes
+    as an address, sooner than it finds an array's).  Refuses a value that is
+    not a 32-bit integer."""
+    global _np, _i32
     if _np is None:
         import numpy
-        _np = numpy
-    if type(a) is not _np.ndarray or a.dtype != _np.int32 or not a.flags.c_contiguous:
-        a = _np.ascontiguousarray(a, dtype=_np.int32)
-    if a.flags.writeable and a.size:  # the cheaper way to its address
-        return a, ctypes.addressof(ctypes.c_char.from_buffer(a))
-    return a, a.__array_interface__["data"][0]
+        _np, _i32 = numpy, numpy.dtype(numpy.int32)
+    if type(a) is not _np.ndarray or a.dtype is not _i32:
+        given = _np.asarray(a)
+        with _np.errstate(invalid="ignore"):
+            a = given.astype(_np.int32)
+        if not _np.array_equal(a, given):
+            raise PkvError(EINVAL, f"{what}: not 32-bit integers")
+    return a.size, a.tobytes()
 
 
 # ---- descriptors ------------------------------------------------------------
@@ -301,21 +306,20 @@ class Arena:
         """Share a stream's pages with a new one: (its ids, copy), where copy
         is None or (src, dst, n_pos) of the last page, which is its own."""
         import numpy as np
-        ids, at = _host_i32(ids)
-        out = np.empty(max(1, ids.size), dtype=np.int32)
+        n_ids, ids = _host_i32("pkv_pages_fork", ids)
+        out = np.empty(max(1, n_ids), dtype=np.int32)
         s, d, n = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
-        _check(self._lib.pkv_pages_fork(self._h, at, ids.size, length, out.ctypes.data,
+        _check(self._lib.pkv_pages_fork(self._h, ids, n_ids, length, out.ctypes.data,
                                         ctypes.byref(s), ctypes.byref(d), ctypes.byref(n)),
                "pkv_pages_fork")
-        return out[:ids.size], ((s.value, d.value, n.value) if n.value else None)
+        return out[:n_ids], ((s.value, d.value, n.value) if n.value else None)
 
     def holders(self, ids):
         import numpy as np
-        ids, at = _host_i32(ids)
-        out = np.zeros(max(1, ids.size), dtype=np.int32)
-        _check(self._lib.pkv_pages_holders(self._h, at, ids.size, out.ctypes.data),
-               "pkv_pages_holders")
-        return out[:ids.size]
+        n, ids = _host_i32("pkv_pages_holders", ids)
+        out = np.zeros(max(1, n), dtype=np.int32)
+        _check(self._lib.pkv_pages_holders(self._h, ids, n, out.ctypes.data), "pkv_pages_holders")
+        return out[:n]
 
     def compact(self, max_moves: int):
         """Plan up to max_moves moves of high pages to low holes: (src, dst).
@@ -380,29 +384,28 @@ def gather(lay, seqs, layer, kind, out, status=None, stream=None):
 def pages_copy(lay, page_pos: int, memory, n_pages: int, src, dst, n_pos=None, stream=None):
     """Copy pages src[i] to dst[i] of the arena at `memory`, whole or their
     first n_pos[i] positions; src, dst, n_pos: host integers."""
-    (src, ps), (dst, pd) = _host_i32(src), _host_i32(dst)
-    n_pos, pn = (None, None) if n_pos is None else _host_i32(n_pos)
-    n = src.size
-    if dst.size != n or (n_pos is not None and n_pos.size != n):
+    (n, src), (n_dst, dst) = _host_i32("pkv_pages_copy", src), _host_i32("pkv_pages_copy", dst)
+    n_n_pos, n_pos = (n, None) if n_pos is None else _host_i32("pkv_pages_copy", n_pos)
+    if n_dst != n or n_n_pos != n:
         raise PkvError(EINVAL, "pkv_pages_copy: lists of different lengths")
     base, = _here("pkv_pages_copy", memory)
     if base is not memory and memory.nbytes < 2 * n_pages * page_elems(lay, page_pos):
         raise PkvError(EINVAL, "pkv_pages_copy: the memory holds fewer pages")
-    _check(load().pkv_pages_copy(ctypes.byref(lay), page_pos, base, n_pages, ps, pd, pn, n,
+    _check(load().pkv_pages_copy(ctypes.byref(lay), page_pos, base, n_pages, src, dst, n_pos, n,
                                  _stream(stream)), "pkv_pages_copy")
 
 
 def tables_remap(tables, src, dst, stream=None):
     """Rewrite device page tables after a compaction: entries src[i] become
     dst[i].  tables: int32 device tensors; src, dst: host integers."""
-    (src, ps), (dst, pd) = _host_i32(src), _host_i32(dst)
-    if src.size != dst.size:
+    (n_moves, src), (n_dst, dst) = _host_i32("pkv_tables_remap", src), _host_i32("pkv_tables_remap", dst)
+    if n_moves != n_dst:
         raise PkvError(EINVAL, "pkv_tables_remap: lists of different lengths")
     torch = (_current or _torch_streams())[0]
     n = len(tables)
-    ptrs = (ctypes.c_void_p * max(1, n))(*_here("pkv_tables_remap", *tables, dtype=torch.int32))
-    sizes = (ctypes.c_int32 * max(1, n))(*[t.numel() for t in tables])
-    _check(load().pkv_tables_remap(ptrs, sizes, n, ps, pd, src.size, _stream(stream)),
+    ptrs = array.array("Q", _here("pkv_tables_remap", *tables, dtype=torch.int32)).tobytes()
+    sizes = array.array("i", [t.numel() for t in tables]).tobytes()
+    _check(load().pkv_tables_remap(ptrs, sizes, n, src, dst, n_moves, _stream(stream)),
            "pkv_tables_remap")
 
 

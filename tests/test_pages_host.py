@@ -279,3 +279,14 @@ def test_calls_take_only_contiguous_tensors_of_the_device():
     lay = pkv.layout(1, 1, 256, 0)
     assert _code(pkv.pages_copy, lay, 16, torch.zeros(1 << 16, dtype=torch.int16), 2, [0], [1], stream=0) == pkv.EINVAL
     assert _code(pkv.tables_remap, [torch.zeros(4, dtype=torch.int32)], [0], [1], stream=0) == pkv.EINVAL
+
+
+@pytest.mark.parametrize("bad", [[1 << 32], np.array([5 + (1 << 32)]), [1.5], [float("nan")], [-(1 << 31) - 1]])
+def test_lists_of_other_than_32_bit_integers_are_refused(bad):
+    lay = pkv.layout(1, 1, 256, 0)
+    for call in (lambda: pkv.pages_copy(lay, 16, 0x1000, 8, bad, [1], stream=0),
+                 lambda: pkv.pages_copy(lay, 16, 0x1000, 8, [1], [2], n_pos=bad, stream=0),
+                 lambda: pkv.tables_remap([], bad, [1], stream=0)):
+        with pytest.raises(pkv.PkvError) as e:
+            call()
+        assert e.value.code == pkv.EINVAL
