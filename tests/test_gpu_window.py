@@ -143,20 +143,22 @@ def test_paged_equals_contiguous_and_alone_equals_in_batch(fmt):
         assert np.array_equal(run(w, 0, hq, q[i:i + 1]), rows[i])
 
 
-# (lens, new tokens, q heads, kv heads, window, sinks) of calls that give a KV
-# head's 17 to 32 query columns one CTA: several pieces, splits, one piece
-WIDE = [([int(x) for x in np.linspace(40, 2300, 24)], [4, 3, 2, 1] * 6, 16, 2, 1500, 4),
-        ([9100, 8000, 9005, 7000, 8800, 9216, 8191, 30], [4, 4, 3, 4, 1, 4, 4, 4], 16, 2, 9000, 0),
-        ([int(x) for x in np.linspace(5, 200, 64)], [4, 3] * 32, 32, 4, 60, 1)]
+# (lens, new tokens, q heads, kv heads, window, sinks, indexer dim) of calls that
+# give a KV head's 17 to 32 query columns one CTA: several pieces, splits, one
+# piece; the last one's columns are two CTAs
+WIDE = [([int(x) for x in np.linspace(40, 2300, 24)], [4, 3, 2, 1] * 6, 16, 2, 1500, 4, 128),
+        ([9100, 8000, 9005, 7000, 8800, 9216, 8191, 30], [4, 4, 3, 4, 1, 4, 4, 4], 16, 2, 9000, 0, 0),
+        ([int(x) for x in np.linspace(5, 200, 64)], [4, 3, 0, 2] * 16, 32, 4, 60, 1, 0),
+        ([700, 37, 150], [4, 3, 4], 16, 2, 300, 5, 128)]
 
 
 @pytest.mark.parametrize("fmt", FMT)
 @pytest.mark.parametrize("case", range(len(WIDE)))
 def test_many_draft_windows(case, fmt):
     t = torch()
-    lens, n_new, hq, hkv, window, sinks = WIDE[case]
-    lay = pkv.layout(1, hkv, 256, 0, fmt)
-    streams = streams_of(lens, hkv, seed=400)
+    lens, n_new, hq, hkv, window, sinks, idx = WIDE[case]
+    lay = pkv.layout(1, hkv, 256, idx, fmt)
+    streams = streams_of(lens, hkv, idx, seed=400)
     q = queries_of(n_new, hq, seed=400)
     a = Windowed(lay, streams, n_new, window, sinks, 48, seed=1, fused=True)
     b = Windowed(lay, streams, n_new, window, sinks, 48, seed=1, fused=True)
@@ -166,6 +168,8 @@ def test_many_draft_windows(case, fmt):
     assert t.equal(a.bufs[0], b.bufs[0])
     rows = np.split(got, np.cumsum(n_new)[:-1])
     for i in sorted({0, 1, 2, 3, 5, len(lens) - 1}):
+        if i >= len(lens) or n_new[i] == 0:
+            continue
         w = Windowed(lay, streams[i:i + 1], n_new[i:i + 1], window, sinks, 16, seed=i)
         ok, report = within_tol(rows[i], w.reference(0, q[i:i + 1]))
         assert ok, report
