@@ -16,7 +16,7 @@
 // warps that compute S^T = K Q^T and O^T += V^T P^T with warp MMAs (8 query
 // columns to an MMA, 16 a CTA; the tensor cores' 128-row tiles would stand
 // nearly empty) with an online softmax per column, each warp on a tile and a
-// column group of its own.  The tiles of a piece are dealt to two or three key
+// column group of its own.  The tiles of a piece are dealt to two or four key
 // slices; slices, pieces and splits merge in the order of the keys.
 //
 // A split's CTAs are a cluster that merges through distributed shared memory:
@@ -45,7 +45,7 @@ namespace {
 constexpr int kMaxCols = 32;                 // query columns of a (stream, KV head)
 constexpr int kBlockCols = 16;               // ... of a CTA of small calls
 constexpr int kMaxPieces = 8;                // pieces of a split
-constexpr int kMaxSlices = 3;                // key slices of a piece
+constexpr int kMaxSlices = 4;                // key slices of a piece
 constexpr int kSplitKeys = 640;              // keys of a piece at most
 constexpr int kMaxPages = kMaxPieces * kSplitKeys / 4 + 4;  // pages a CTA's run can touch
 constexpr int kCtas = 304;                   // that the GPU holds at once, two an SM
@@ -78,6 +78,7 @@ struct Cfg {
     static constexpr int half = 8192;                            // K or V bytes of a stage
     static constexpr int stage = 2 * half;
     static constexpr int slots = 6;
+    static constexpr int bars = 2 * slots;                       // a tile's barriers: t % bars, its slot t % slots
     static_assert(half == tile * kHeadDim * (kFp8 ? 1 : 2), "whole rows");
     static constexpr int consumers = kConsumers;
     static constexpr int threads = consumers * 32 + 32;
@@ -87,7 +88,7 @@ struct Cfg {
     static constexpr int off_join = off_page + kMaxPages * 4;    // a piece's slices: 8 KB of O, then (m, l)
     static constexpr int off_join_ml = off_join + kJoinBytes;
     static constexpr int off_bar = off_join_ml + kMaxSlices * kBlockCols * 8;
-    static constexpr int bytes = off_bar + 2 * slots * 8 + 16;
+    static constexpr int bytes = off_bar + 2 * bars * 8 + 16;
     static constexpr int smem = bytes + 1024;                    // with alignment slack
     // after the last tile the stages hold the merge rows, then the CTA's sum
     static constexpr int off_ml = 32 * row * 4;
@@ -119,15 +120,17 @@ __host__ __device__ inline int col_blocks(bool wide, int ncols) {
 }
 constexpr int kStash = kConsumers * 17 * 32;  // float4 a CTA: O and (m, l) of each lane
 
-// Key slices of a piece (the tiles that a CTA of kBlockCols columns works on at
-// once): a divisor of the slots.
-__host__ __device__ inline int slices_of(bool fp8, int ncols) {
-    const int ncg = ((ncols < kBlockCols ? ncols : kBlockCols) + 7) >> 3, slots = fp8 ? Cfg<true>::slots : Cfg<false>::slots;
-    int n = kConsumers / ncg;
-    n = n > kMaxSlices ? kMaxSlices : n;
-    while (slots % n) --n;
-    return n;
+// Key slices of a piece: the tiles that a CTA of kBlockCols columns works on at
+// once.  Each of a tile's barriers always belongs to one slice, which takes
+// every phase of it: the slices divide their number.  (A slice that skipped a
+// phase could not tell the tile before its own, not landed yet, from its own:
+// both leave the same parity.)
+__host__ __device__ inline int slices_of(int ncols) {
+    const int ncg = ((ncols < kBlockCols ? ncols : kBlockCols) + 7) >> 3;
+    return kConsumers / ncg;
 }
+static_assert(Cfg<false>::bars % kMaxSlices == 0 && Cfg<true>::bars % kMaxSlices == 0 && kConsumers == kMaxSlices,
+              "1, 2 or 4 slices, each with barriers of its own");
 
 // ---- cluster helpers ----------------------------------------------------------
 // All threads of the cluster meet.  A warp whose lanes took different paths
@@ -500,9 +503,9 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     x.scl = reinterpret_cast<float *>(smem + F::off_scl);
     x.pages = reinterpret_cast<int32_t *>(smem + F::off_page);
     x.full = reinterpret_cast<uint64_t *>(smem + F::off_bar);
-    x.empty = x.full + F::slots;
-    x.abort_flag = reinterpret_cast<volatile int *>(x.empty + F::slots);
-    constexpr int S = F::slots;
+    x.empty = x.full + F::bars;
+    x.abort_flag = reinterpret_cast<volatile int *>(x.empty + F::bars);
+    constexpr int S = F::slots, B = F::bars;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const Run u = locate<F::tile, kWide>(c, a);
@@ -513,11 +516,8 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     // A piece's tile t belongs to key slice t % slices.  A CTA takes all slices
     // at once, ks_n tiles in its warps together, or (more than kBlockCols
     // columns) one slice after the other in two passes.  A piece takes whole
-    // rounds of the slices (empty tiles fill its last one), so each slot always
-    // belongs to the same warps, which take every phase of its barrier.  (One
-    // that skipped a phase could not tell the tile before its own, not landed
-    // yet, from its own: both leave the same parity.)
-    const int slices = slices_of(kFp8, ncols);
+    // rounds of the slices: empty tiles fill its last one.
+    const int slices = slices_of(ncols);
     const int passes = kWide && ncols > kBlockCols ? 2 : 1, ks_n = passes == 1 ? slices : 1;
     const int round = (u.per + slices - 1) / slices * slices;  // a piece's tiles, empty ones among them
     const int pass_tiles = passes == 1 ? round : round / 2;
@@ -526,7 +526,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     const bool active = warp < F::consumers && ks < ks_n;
 
     if (tid == 0) {
-        for (int i = 0; i < S; ++i) {
+        for (int i = 0; i < B; ++i) {
             mbar_init(&x.full[i], 1);
             mbar_init(&x.empty[i], ncg);
         }
@@ -598,9 +598,9 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             }
             const int slot = t % S, y = __shfl_sync(0xffffffffu, yk, t & 31);
             const int v0 = __shfl_sync(0xffffffffu, first, t & 31);
-            uint64_t *const bar = &x.full[slot];
+            uint64_t *const bar = &x.full[t % B];
             if (t >= S) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&x.empty[slot], ((t / S) - 1) & 1, c.status))) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&x.empty[(t - S) % B], ((t - S) / B) & 1, c.status))) {
                     *x.abort_flag = 1;
                     break;
                 }
@@ -841,14 +841,14 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             const int pc = passes == 1 ? w : w >> 1, pass = w - pc * passes;
             for (int tp = pass + ks; ok && tp < round; tp += slices) {
                 const int t = w * pass_tiles + (passes == 1 ? tp : tp >> 1), slot = t % S;
-                ok = __all_sync(0xffffffffu, mbar_wait(&x.full[slot], (t / S) & 1, c.status));
+                ok = __all_sync(0xffffffffu, mbar_wait(&x.full[t % B], (t / B) & 1, c.status));
                 if (!ok) {
                     *x.abort_flag = 1;
                     break;
                 }
                 const int v0 = u.key0 + (pc * u.per + tp) * F::tile;
                 if (tp >= u.per || v0 >= u.key1) {
-                    if (lane == 0) mbar_arrive(&x.empty[slot]);
+                    if (lane == 0) mbar_arrive(&x.empty[t % B]);
                     continue;
                 }
                 const uint8_t *const st = x.stages + slot * F::stage;
@@ -1043,7 +1043,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&x.empty[slot]);
+                if (lane == 0) mbar_arrive(&x.empty[t % B]);
             }
             finish_pass(pc, pass);
         }
@@ -1052,7 +1052,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     const bool failed = *x.abort_flag != 0;
     // after a wait that ran out, every copy issued lands before the memory goes
     if (failed)
-        for (int j = max(0, issued - S); j < issued; ++j) mbar_wait(&x.full[j % S], (j / S) & 1, nullptr);
+        for (int j = max(0, issued - S); j < issued; ++j) mbar_wait(&x.full[j % B], (j / B) & 1, nullptr);
     if (kRuns) return;  // window_combine merges the slices and pieces
 
     // ---- merge the CTA's key slices, in order ----
