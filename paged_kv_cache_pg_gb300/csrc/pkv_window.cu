@@ -28,12 +28,12 @@
 // not depend on its batch.
 //
 // What bounds it: the bytes of K and V where there are many (64 streams of
-// 4,096 bf16 keys: 539 MB in 87.4 us, 6.16 TB/s); whole waves of CTAs, two on
-// an SM, below that (32 streams of 4,096 e4m3 keys are 512 CTAs in two waves of
-// 21 us; a copy of the kernel without its MMAs and conversions takes 37.2 us of
-// 42.3); and for a few streams the launch, the first tile's way in and the
-// merge (one stream of 128 keys 6.6 us, four of 1,024 keys 7.6 us).  Two CTAs
-// share an SM, so one streams while the other starts or merges.
+// 4,096 bf16 keys: 539 MB in 86.0 us, 6.26 TB/s); whole waves of CTAs, two on
+// an SM, and a tile's chain of latencies below that (32 streams of 4,096 e4m3
+// keys: 137 MB in 37.1 us, 256 CTAs of two pieces on the 304 places); and for a
+// few streams the launch, the first tile's way in and the merge (one stream of
+// 128 keys 6.6 us, four of 1,024 keys 7.6 us).  Two CTAs share an SM, so one
+// streams while the other starts or merges.
 #include <algorithm>
 #include <cuda_fp16.h>
 
@@ -53,13 +53,14 @@ constexpr int kCtas = 304;                   // that the GPU holds at once, two 
 // pieces each, merged by a second kernel), in keys of a wave of CTAs: a wave
 // takes its CTAs' keys and kStartKeys (start, first tile, merge), and runs take
 // kCombKeys more.  A run's keys count 9/10 where the bytes bound the call (a
-// wave that is not full is faster) and 12/10 with e4m3 pages and CTAs of more
-// than 16 columns, which the latencies of a tile bound.  Measured, clusters
-// against the runs that this picks or would pick: bf16, windows of 4,096 keys,
-// 16 streams 23.9 us against 25.8, 24 streams 43.4 against 37.5, 64 streams 95.4
-// against 86.5; of 512 keys, 64 streams 35.4 against 24.2; e4m3, 4,096 keys, 24
-// streams 38.7 against 41.2, 48 streams 63.9 against 76.6, 64 streams 85.0
-// against 78.1; of 512 keys, 32 streams 22.8 against 19.6.
+// wave that is not full is faster) and 12/10 with CTAs of more than 16 columns
+// and e4m3 pages of more than 8, which the latencies of a tile bound.  Measured,
+// clusters against runs, those picked first: bf16, one token, windows of 4,096
+// keys, 16 streams 23.9 us against 25.8; runs against clusters, 24 streams 36.6
+// against 43.4, 64 streams 84.8 against 95.4; of 512 keys, 64 streams 24.4
+// against 35.4; e4m3, 4,096 keys, 32 streams 37.4 against 40.1; with two tokens
+// (16 columns) clusters against runs, 24 streams 50.7 against 55.6; bf16, four
+// tokens (32 columns), 24 streams 69.7 against 72.0.
 constexpr int kStartKeys = 300, kCombKeys = 100;
 constexpr int kFreshGuard = 32;              // rows below the new tokens that a kernel just before may write
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
@@ -1192,7 +1193,7 @@ static int window_pieces(int32_t window, int32_t n_sink) {
 int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
     const int pieces = window_pieces(window, n_sink);
     const int tile = c.kv_fp8 ? Cfg<true>::tile : Cfg<false>::tile;
-    bool split = false, wide = false;
+    bool split = false, wide = false, over8 = false;
     int64_t items = 0, cols = 0, floats = 0, keys = 0;
     for (int s = 0; s < c.n_seqs; ++s) {
         SeqDev &d = c.seq[s];
@@ -1207,6 +1208,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
         d.split_len = (per + tile - 1) / tile * tile;
         split |= d.nsplit > 1;
         wide |= d.ncols > kBlockCols;
+        over8 |= d.ncols > 8;
         items += (int64_t)c.n_kv_heads * d.nsplit * col_blocks(false, d.ncols);
     }
     const bool many = items * pieces > kCtas;
@@ -1231,7 +1233,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
     int64_t best = split ? INT64_MAX : waves(1) * (per + kStartKeys) * 10;
     plan->run = 0;
     for (int run = 1; pieces > 1 && run <= pieces; run *= 2) {
-        const int64_t cost = waves(run) * (run * per * (c.kv_fp8 || wide ? 12 : 9) + kStartKeys * 10) + kCombKeys * 10;
+        const int64_t cost = waves(run) * (run * per * (wide || (c.kv_fp8 && over8) ? 12 : 9) + kStartKeys * 10) + kCombKeys * 10;
         if (cost < best) {
             best = cost;
             plan->run = run;
