@@ -388,7 +388,8 @@ int pkv_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, in
  * stream's longest length and most new tokens covers all shorter and fewer.  A stream's bits depend only on
  * its own rows, length and new tokens, the window and n_sink: paged output
  * equals contiguous output, and other streams of the call change nothing.
- * EINVAL for a window or n_sink out of range, and as for pkv_decode. */
+ * EINVAL for a window or n_sink out of range, a stream of more than 2^29
+ * positions, and as for pkv_decode. */
 int pkv_window_decode_ws_size(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs,
                               int32_t n_q_heads, int32_t window, int32_t n_sink, size_t *bytes);
 int pkv_window_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
@@ -409,8 +410,8 @@ int pkv_window_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_s
  * must hold finite values.  ws: device, >= pkv_window_prefill_ws_size bytes,
  * 256-byte aligned, no initialization, one ws per in-flight call.  Paged
  * output equals contiguous output, and other streams of the call change
- * nothing, bit for bit.  EINVAL for a window or n_sink out of range, an e4m3
- * layout, and as for pkv_prefill. */
+ * nothing, bit for bit.  EINVAL for a window or n_sink out of range, a stream
+ * of more than 2^29 positions, an e4m3 layout, and as for pkv_prefill. */
 int pkv_window_prefill_ws_size(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs,
                                int32_t n_q_heads, int32_t window, int32_t n_sink, size_t *bytes);
 int pkv_window_prefill(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,

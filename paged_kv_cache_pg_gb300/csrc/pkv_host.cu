@@ -519,6 +519,8 @@ static int window_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seq
     int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, c);
     if (rc) return rc;
     if (window < 1 || n_sink < 0) return PKV_EINVAL;
+    for (int s = 0; s < c->n_seqs; ++s)
+        if (c->seq[s].len > 1 << 29) return PKV_EINVAL;  // keys rounded up to tiles stay 32-bit
     return plan_window(*c, window, n_sink, plan);
 }
 
@@ -567,6 +569,9 @@ static int window_chunk_common(const pkv_layout *L, const pkv_seq *seqs, int32_t
     int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, c);
     if (rc) return rc;
     if (window < 1 || n_sink < 0 || c->kv_fp8) return PKV_EINVAL;
+    for (int s = 0; s < c->n_seqs; ++s)
+        if (c->seq[s].len > 1 << 29 || (int64_t)c->seq[s].n_new * c->group > INT32_MAX / 2)
+            return PKV_EINVAL;  // gathered rows and query columns are 32-bit
     int nsm = 0;
     rc = sm_count(&nsm);
     if (rc) return rc;

@@ -1197,8 +1197,8 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
     int64_t items = 0, cols = 0, floats = 0, keys = 0;
     for (int s = 0; s < c.n_seqs; ++s) {
         SeqDev &d = c.seq[s];
+        if ((int64_t)d.n_new * c.group > kMaxCols) return PKV_EINVAL;
         d.ncols = d.n_new * c.group;
-        if (d.ncols > kMaxCols) return PKV_EINVAL;
         d.nsplit = 1;
         d.split_len = tile;
         if (d.ncols == 0) continue;
@@ -1227,12 +1227,13 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
         floats = (floats + 63) / 64 * 64;
     }
     if (items * pieces > INT32_MAX) return PKV_EINVAL;
+    const bool some = pieces > 1 && (split || many);  // calls that may run as runs of pieces
     // the least cost: a cluster a split, or runs of pieces (which have to merge splits)
     const int64_t per = items ? keys / (items * pieces) : 0;  // keys of a piece
     const auto waves = [&](int run) { return (items * pieces / run + kCtas - 1) / kCtas; };
     int64_t best = split ? INT64_MAX : waves(1) * (per + kStartKeys) * 10;
     plan->run = 0;
-    for (int run = 1; pieces > 1 && run <= pieces; run *= 2) {
+    for (int run = 1; some && run <= pieces; run *= 2) {
         const int64_t cost = waves(run) * (run * per * (wide || (c.kv_fp8 && over8) ? 12 : 9) + kStartKeys * 10) + kCombKeys * 10;
         if (cost < best) {
             best = cost;
@@ -1247,7 +1248,6 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
     plan->ctas = static_cast<int32_t>(items * (pieces / std::max(1, plan->run)));
     // sized for either kind of call, so that the size for a stream's longest
     // length covers every shorter one
-    const bool some = pieces > 1 && (split || many);
     plan->stash_off = some ? floats : 0;
     plan->ws_bytes = static_cast<size_t>(plan->stash_off) * 4 +
                      (wide ? static_cast<size_t>(items * pieces) * kStash * sizeof(float4) : 0);

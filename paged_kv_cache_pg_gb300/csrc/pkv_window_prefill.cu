@@ -795,7 +795,6 @@ int plan_window_prefill(Common &c, int32_t window, int32_t n_sink, int nsm, Deco
         d.nsplit = 1;
         d.split_len = kN;
         if (d.ncols == 0) continue;
-        if ((int64_t)d.n_new * c.group > INT32_MAX / 2) return PKV_EINVAL;
         const int mtiles = (d.ncols + kM - 1) / kM;
         // at most: a window, the queries of an M-tile, the sinks' runs
         const int64_t span = std::min<int64_t>(d.n_new, kM / c.group + 2);

@@ -128,3 +128,14 @@ def test_the_workspace_of_the_longest_lengths_covers_shorter_ones(fmt, streams, 
     for _ in range(200):
         lens = np.exp(rng.uniform(np.log(top_new), np.log(20000), streams)).astype(int).clip(top_new)
         assert size(lens, rng.integers(0, top_new + 1, streams)) <= most
+
+
+def test_more_queries_or_positions_than_32_bits_count_are_refused():
+    # 2^28 new tokens of 16 heads a KV head: 2^32 query columns; a stream of 2^29 + 4 positions
+    lay = pkv.layout(1, 1, 256, 0)
+    for length, n_new in ((1 << 28, 1 << 28), ((1 << 29) + 4, 1)):
+        seqs = [pkv.seq(pkv.Pg(0x10000, 0, pkv.page_elems(lay, length), length, 1, 0, 0), length, n_new)]
+        for size in (pkv.window_decode_ws_size, pkv.window_prefill_ws_size):
+            with pytest.raises(pkv.PkvError) as e:
+                size(lay, seqs, 16, 100, 0)
+            assert e.value.code == pkv.EINVAL
