@@ -385,9 +385,10 @@ int pkv_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, in
  * columns each) and of windows of more than about 5,000 keys go to ws (device,
  * >= pkv_window_decode_ws_size bytes, which is 0 for other calls, 256-byte
  * aligned, no initialization, one ws per in-flight call).  The size for a
- * stream's longest length and most new tokens covers all shorter and fewer.  A stream's bits depend only on
- * its own rows, length and new tokens, the window and n_sink: paged output
- * equals contiguous output, and other streams of the call change nothing.
+ * stream's longest length and most new tokens covers all shorter and fewer.
+ * A stream's bits depend only on its own rows, length and new tokens, the
+ * window and n_sink: paged output equals contiguous output, and other streams
+ * of the call change nothing.
  * EINVAL for a window or n_sink out of range, a stream of more than 2^29
  * positions, and as for pkv_decode. */
 int pkv_window_decode_ws_size(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs,

@@ -361,3 +361,20 @@ def test_more_contiguous_streams_than_copy_maps(fmt):
     ok, report = within_tol(got, a.reference(0, q))
     assert ok, report
     assert np.array_equal(got, run(b, 0, hq, q))
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("streams", [2, 24])
+def test_output_rows_behind_the_last_stream_stay(fmt, streams):
+    t = torch()
+    lens, hq, hkv, window, sinks = [200 + i for i in range(streams)], 16, 2, 1100, 4
+    lay = pkv.layout(1, hkv, 256, 0, fmt)
+    w = Windowed(lay, streams_of(lens, hkv, seed=600), [3] * streams, window, sinks, 16)
+    seqs, rows = w.seqs(), 3 * streams
+    q = dev_u16(np.concatenate(queries_of([3] * streams, hq, seed=600)))
+    out = t.full((rows + 5, hq, 256), 0x7FC1, dtype=q.dtype, device="cuda")
+    size = pkv.window_decode_ws_size(lay, seqs, hq, window, sinks)
+    ws = t.full((size // 4 + 64,), 7.5, dtype=t.float32, device="cuda")
+    pkv.window_decode(lay, seqs, 0, hq, window, sinks, q, out, ws)
+    assert (out[rows:] == 0x7FC1).all() and (ws[size // 4:] == 7.5).all()
+    assert not (out[:rows] == 0x7FC1).any()

@@ -235,3 +235,19 @@ def test_prompt_in_chunks_then_tokens_in_a_small_arena():
         assert ok, (at, n, report)
         at, step = at + n, step + 1
     assert int(status) == 0 and dead > 20
+
+
+@pytest.mark.parametrize("lens,n_new,window", [([300, 64], [40, 64], 100), ([1100], [20], 900)])
+def test_output_rows_behind_the_last_stream_stay(lens, n_new, window):
+    t = torch()
+    hq, hkv, sinks, rows = 8, 2, 4, sum(n_new)
+    lay = pkv.layout(1, hkv, 256, 0)
+    w = Windowed(lay, streams_of(lens, hkv, seed=700), n_new, window, sinks, 20)
+    seqs = w.seqs()
+    q = dev_u16(np.concatenate(queries_of(n_new, hq, seed=700)))
+    out = t.full((rows + 200, hq, 256), 0x7FC1, dtype=q.dtype, device="cuda")
+    size = pkv.window_prefill_ws_size(lay, seqs, hq, window, sinks)
+    ws = t.full((size // 4 + 64,), 7.5, dtype=t.float32, device="cuda")
+    pkv.window_prefill(lay, seqs, 0, hq, window, sinks, q, out, ws)
+    assert (out[rows:] == 0x7FC1).all() and (ws[size // 4:] == 7.5).all()
+    assert not (out[:rows] == 0x7FC1).any()
