@@ -696,19 +696,19 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         const int vr_ = (lane & 7) + 8 * (lane >> 4), vcb = (lane >> 3) & 1;
         float uo[2] = {-INFINITY, -INFINITY};  // e4m3: O's own reference (logit + V-scale exponent)
 
-        // A piece's sums are complete: l over the key rows, O on the logits'
-        // maximum.  They stay in registers for the cluster's merge, or the
-        // piece's slices join into slice 0's (as merge_parts would), which go
-        // to the workspace, O [piece of the unit][column][256], then (m, l),
-        // and the next piece starts anew.  The slices hand O over lane by lane,
-        // 8 KB at a time; written out one by one they are two or three times
-        // the traffic (64 streams of 4,096 keys 99.0 us against 92.3).
         auto reset = [&] {
             m[0] = m[1] = uo[0] = uo[1] = -INFINITY;
             l[0] = l[1] = 0.f;
 #pragma unroll
             for (int i = 0; i < 16; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
         };
+        // The sums of a piece (or of a slice of it, in two passes) are complete:
+        // l over the key rows, O on the logits' maximum.  They stay in registers for the cluster's merge, or the
+        // piece's slices join into slice 0's (as merge_parts would), which go
+        // to the workspace, O [piece of the unit][column][256], then (m, l),
+        // and the next piece starts anew.  The slices hand O over lane by lane,
+        // 8 KB at a time; written out one by one they are two to four times
+        // the traffic (64 streams of 4,096 keys 99.0 us against 92.3).
         auto finish_pass = [&](int pc, int pass) {
             l[0] = sum_rows(l[0]);
             l[1] = sum_rows(l[1]);
