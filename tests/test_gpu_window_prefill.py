@@ -251,3 +251,40 @@ def test_output_rows_behind_the_last_stream_stay(lens, n_new, window):
     pkv.window_prefill(lay, seqs, 0, hq, window, sinks, q, out, ws)
     assert (out[rows:] == 0x7FC1).all() and (ws[size // 4:] == 7.5).all()
     assert not (out[:rows] == 0x7FC1).any()
+
+
+def test_calls_on_two_streams_at_once():
+    # a chunk and decodes on one stream, the same with other inputs on a second: each
+    # with its own workspaces, and the results of running them one after the other
+    t = torch()
+    hq, hkv, window, sinks = 16, 2, 512, 4
+    lay = pkv.layout(1, hkv, 256, 0)
+    sets = []
+    for k in range(2):
+        dec = Windowed(lay, streams_of([600 + 7 * i for i in range(24)], hkv, seed=800 + 40 * k), [1] * 24, window, sinks, 16)
+        pre = Windowed(lay, streams_of([900, 333], hkv, seed=880 + k), [256, 100], window, sinks, 16)
+        dq, pq = (dev_u16(np.concatenate(queries_of(w.n_new, hq, seed=900 + k))) for w in (dec, pre))
+        dseq, pseq = pkv.batch(dec.seqs()), pkv.batch(pre.seqs())
+        size = pkv.window_decode_ws_size(lay, dseq, hq, window, sinks)
+        dws = t.empty(max(64, size // 4), dtype=t.float32, device="cuda")
+        sets.append((dec, pre, dq, pq, dseq, pseq, dws, workspace(lay, pseq, hq, window, sinks)))
+
+    def calls(k, stream):
+        _, _, dq, pq, dseq, pseq, dws, pws = sets[k]
+        outs = []
+        for _ in range(12):
+            outs += [t.zeros_like(dq), t.zeros_like(pq)]
+            stream.wait_stream(t.cuda.default_stream())
+            pkv.window_decode(lay, dseq, 0, hq, window, sinks, dq, outs[-2], dws, stream=stream)
+            pkv.window_prefill(lay, pseq, 0, hq, window, sinks, pq, outs[-1], pws, stream=stream)
+        return outs
+
+    alone = []
+    for k in range(2):
+        alone.append(calls(k, t.cuda.default_stream()))
+        t.cuda.synchronize()
+    side = [t.cuda.Stream(), t.cuda.Stream()]
+    both = [calls(k, side[k]) for k in range(2)]
+    t.cuda.synchronize()
+    for k in range(2):
+        assert all(t.equal(x, alone[k][i % 2]) for i, x in enumerate(alone[k] + both[k]))
