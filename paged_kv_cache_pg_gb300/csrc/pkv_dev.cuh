@@ -260,12 +260,15 @@ __device__ __forceinline__ void pdl_trigger() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Let the next kernel start once this thread's writes are visible device
-// wide: for kernels writing cache rows, which the next kernel may read
-// before its grid-dependency wait.
+// Let the next kernel start once the CTA's writes are visible device wide: for
+// kernels writing cache rows or page tables, which the next kernel may read
+// before its grid-dependency wait.  A CTA counts as triggered at the first
+// trigger of any of its threads, so one thread triggers once all have fenced
+// their writes.  Every thread of the CTA (1D) calls it.
 __device__ __forceinline__ void pdl_trigger_after_writes() {
     __threadfence();
-    pdl_trigger();
+    __syncthreads();
+    if (threadIdx.x == 0) pdl_trigger();
 }
 
 // A 64-bit value from lane `src` of the warp.
