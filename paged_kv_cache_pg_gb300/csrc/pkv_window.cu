@@ -1184,7 +1184,16 @@ static int window_pieces(int32_t window, int32_t n_sink) {
     return n;
 }
 
-// Splits only where a piece would pass kSplitKeys keys.  A call of streams with
+// The most virtual keys of a stream of up to `len` positions and n_new new
+// tokens.  The count itself goes up and down by a tile with the length (the
+// window starts anywhere in its first tile), this never goes down: splits by it
+// need no more workspace for a shorter stream.
+static int64_t most_keys(int32_t len, int32_t n_new, int32_t window, int32_t n_sink, int32_t tile) {
+    const int64_t sinks = ((int64_t)n_sink + tile - 1) / tile * tile;
+    return std::min<int64_t>(len, sinks + ((int64_t)window + n_new - 1) + (tile - 1));
+}
+
+// Splits only where a piece could pass kSplitKeys keys.  A call of streams with
 // more than kBlockCols columns gives each kBlockCols a CTA while the CTAs fit
 // the GPU at once, else all of them one: the bits are the same.  Four draft
 // tokens of 8 heads, windows of 2,047 keys, 16 columns a CTA against 32: 8
@@ -1203,7 +1212,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
         d.split_len = tile;
         if (d.ncols == 0) continue;
         const WindowSpan sp = window_span(d.len, d.n_new, window, n_sink, tile);
-        d.nsplit = (sp.nkeys - 1) / (pieces * kSplitKeys) + 1;
+        d.nsplit = static_cast<int32_t>((most_keys(d.len, d.n_new, window, n_sink, tile) - 1) / (pieces * kSplitKeys) + 1);
         const int per = (sp.nkeys - 1) / (d.nsplit * pieces) + 1;  // keys of a piece
         d.split_len = (per + tile - 1) / tile * tile;
         split |= d.nsplit > 1;
@@ -1247,7 +1256,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
     plan->wide = wide;
     plan->ctas = static_cast<int32_t>(items * (pieces / std::max(1, plan->run)));
     // sized for either kind of call, so that the size for a stream's longest
-    // length covers every shorter one
+    // length and most new tokens covers every shorter one and fewer
     plan->stash_off = some ? floats : 0;
     plan->ws_bytes = static_cast<size_t>(plan->stash_off) * 4 +
                      (wide ? static_cast<size_t>(items * pieces) * kStash * sizeof(float4) : 0);
