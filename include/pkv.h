@@ -380,7 +380,8 @@ int pkv_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, in
  * Rows that no query of the stream reads may hold anything, NaN included, and
  * table entries of pages without a row that one reads are not looked at: such
  * pages may have been given back (pkv_window_dead_pages).  A row that some of
- * the stream's new tokens read and others do not must hold finite values.
+ * the stream's new tokens read and others do not must hold finite values.  A NaN
+ * that is read (or a score beyond float32) comes out as NaN, with no status bit.
  * Partials of large calls (more than 304 CTAs of up to 640 keys and 16 query
  * columns each) and of windows of more than about 5,000 keys go to ws (device,
  * >= pkv_window_decode_ws_size bytes, which is 0 for other calls, 256-byte

@@ -477,13 +477,13 @@ __device__ __forceinline__ Sum merge_parts(int n, FM ml_of, FO acc_of) {
     return r;
 }
 
-// Four dims of an output row (zeros where no key was seen).
+// Four dims of an output row.  A query sees its own position at least, so l is
+// 0 only where every score is -infinity: NaN then, as where a score or a row that
+// is read is NaN.
 __device__ __forceinline__ void write_out(uint16_t *out, const Sum &r) {
-    const bool any = r.l > 0.f;
-    const float l = any ? r.l : 1.f;
     uint2 pk;
-    pk.x = pack_bf16(any ? __fdiv_rn(r.o.x, l) : 0.f, any ? __fdiv_rn(r.o.y, l) : 0.f);
-    pk.y = pack_bf16(any ? __fdiv_rn(r.o.z, l) : 0.f, any ? __fdiv_rn(r.o.w, l) : 0.f);
+    pk.x = pack_bf16(__fdiv_rn(r.o.x, r.l), __fdiv_rn(r.o.y, r.l));
+    pk.y = pack_bf16(__fdiv_rn(r.o.z, r.l), __fdiv_rn(r.o.w, r.l));
     *reinterpret_cast<uint2 *>(out) = pk;
 }
 

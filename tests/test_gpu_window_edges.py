@@ -6,7 +6,7 @@ import pytest
 from paged_kv_cache_pg_gb300 import pkv, synth
 
 from gpu_setup import dev_u16, host_u16, torch, within_tol
-from window_setup import Windowed, queries_of, streams_of
+from window_setup import Windowed, attend, queries_of, streams_of, values
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,52 @@ def test_one_workspace_for_every_length_near_a_split_s_border(fmt):
         ok, report = within_tol(host_u16(out), w.reference(0, q))
         assert ok, (n, report)
     assert int(status) == 0 and ws[size // 4:].isnan().all()
+
+
+
+def run(w, hq, q_list):
+    t = torch()
+    seqs = w.seqs()
+    q = dev_u16(np.concatenate(q_list))
+    out = t.zeros_like(q)
+    size = pkv.window_decode_ws_size(w.lay, seqs, hq, w.window, w.sinks)
+    ws = t.full((max(64, size // 4),), float("nan"), dtype=t.float32, device="cuda") if size else None
+    pkv.window_decode(w.lay, seqs, 0, hq, w.window, w.sinks, q, out, ws)
+    return host_u16(out)
+
+
+NAN, INF, NINF = 0x7FC1, 0x7F80, 0xFF80
+# what KV head 0 of the first stream (or its heads' queries) holds, as (tensor,
+# position from the stream's end, dim, bits); each is read by the query
+BAD = [[("k", 50, 3, NAN)], [("v", 50, 3, NAN)], [("k", 1, 3, NAN)], [("q", 0, 5, NAN)], [("k", 50, 3, INF)],
+       [("q", 0, 5, INF)], [("v", 1, 3, INF), ("v", 50, 3, NINF)], [("k", p, 0, NAN) for p in range(1, 301)]]
+
+
+@pytest.mark.parametrize("fmt", FMT)
+@pytest.mark.parametrize("case", range(len(BAD)))
+@pytest.mark.parametrize("window,streams", [(100, 1), (100, 40), (2000, 40), (6000, 2)])
+def test_what_is_not_finite_where_it_is_read_is_not_finite_in_the_output(window, streams, case, fmt):
+    hq, hkv, sinks, length = 8, 2, 4, 300 if window < 2000 else 6200
+    grp = hq // hkv
+    lay = pkv.layout(1, hkv, 256, 0, fmt)
+    ss = streams_of([length] + [200] * (streams - 1), hkv, seed=61)
+    q = queries_of([1] * streams, hq, seed=62)
+    clean = Windowed(lay, ss, [1] * streams, window, sinks, 16, seed=5).reference(0, q)
+    for what, back, dim, bits in BAD[case]:
+        if what == "q":
+            q[0][0, :grp, dim] = bits
+        else:
+            getattr(ss[0], what)[0][length - back, 0, dim] = bits
+    w = Windowed(lay, ss, [1] * streams, window, sinks, 16, seed=5)
+    got = run(w, hq, q)
+    with np.errstate(all="ignore"):
+        want = attend(values(ss[0].k[0], fmt), values(ss[0].v[0], fmt), q[0], length, window, sinks)
+    odd = (got[0, :grp] & 0x7F80) == 0x7F80
+    dims = sorted({d for what, _, d, _ in BAD[case] if what == "v"})
+    if dims:                  # of e4m3 rows the other dims share the scale that is not finite
+        assert odd[:, dims].all() and (fmt == pkv.KV_E4M3 or odd.sum() == odd[:, dims].sum())
+    else:                     # a score of -inf (an infinite key against the query's sign) is a weight of 0
+        assert np.array_equal(odd, ~np.isfinite(want[0, :grp])) and odd.any()
+    rest = np.concatenate([got[0, grp:].ravel(), got[1:].ravel()])
+    ok, report = within_tol(rest, np.concatenate([clean[0, grp:].ravel(), clean[1:].ravel()]))
+    assert ok, report
