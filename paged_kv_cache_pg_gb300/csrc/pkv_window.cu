@@ -211,13 +211,14 @@ __device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cas
 __device__ __forceinline__ void cp_async4(void *dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
-// s = 2^e x mant with mant in [1, 2); a zero or subnormal scale gives weight 0.
+// s = 2^e x mant with mant in [1, 2); a zero or subnormal scale gives weight 0, one
+// that is not finite gives NaN (its zero codes are NaN, and a row that holds an
+// infinity has no other codes but NaN).
 __device__ __forceinline__ void split_scale(float s, float &e, float &mant) {
     const uint32_t b = __float_as_uint(s);
     const int ex = static_cast<int>((b >> 23) & 0xffu);
-    const bool normal = ex != 0 && ex != 0xff;
-    e = normal ? static_cast<float>(ex - 127) : -INFINITY;
-    mant = normal ? __uint_as_float((b & 0x007fffffu) | 0x3f800000u) : 0.f;
+    e = ex != 0 ? static_cast<float>(ex - 127) : -INFINITY;
+    mant = ex == 0xff ? __uint_as_float(0x7fffffffu) : ex != 0 ? __uint_as_float((b & 0x007fffffu) | 0x3f800000u) : 0.f;
 }
 
 // ---- one CTA's run of keys --------------------------------------------------------

@@ -89,3 +89,18 @@ def test_what_is_not_finite_where_it_is_read_is_not_finite_in_the_output(window,
     rest = np.concatenate([got[0, grp:].ravel(), got[1:].ravel()])
     ok, report = within_tol(rest, np.concatenate([clean[0, grp:].ravel(), clean[1:].ravel()]))
     assert ok, report
+
+
+def test_e4m3_rows_whose_scale_is_not_finite():
+    # a V scale of inf or NaN set in the cache: not a weight of zero
+    t = torch()
+    lay = pkv.layout(1, 1, 256, 0, pkv.KV_E4M3)
+    s = streams_of([120], 1, seed=8)
+    q = queries_of([1], 4)
+    for pos in (3, 64, 119):
+        for value in (float("inf"), float("nan")):
+            w = Windowed(lay, s, [1], 60, 4, 16, seed=2)
+            table = next(x for x in w.keep if x.dtype == t.int32).cpu().numpy()[:-1]
+            at = pkv.pg_row(lay, w.pgs[0], table, 0, pkv.VS, 0, pos)
+            w._body(0).view(t.uint8)[at:at + 4].view(t.float32)[0] = value
+            assert ((run(w, 4, q) & 0x7F80) == 0x7F80).all(), (pos, value)
