@@ -382,6 +382,10 @@ int pkv_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, in
  * pages may have been given back (pkv_window_dead_pages).  A row that some of
  * the stream's new tokens read and others do not must hold finite values.  A NaN
  * that is read (or a score beyond float32) comes out as NaN, with no status bit.
+ * Arithmetic: bf16 products with P as two bf16 parts (about 16 significant bits);
+ * with an e4m3 layout fp16 products of the codes, exact, and of the query, scaled
+ * by a power of two to fp16's range (an element is exact down to 2^-28 of the
+ * row's largest), weights as two fp16 parts; sums in float32.
  * Partials of large calls (more than 304 CTAs of up to 640 keys and 16 query
  * columns each) and of windows of more than about 5,000 keys go to ws (device,
  * >= pkv_window_decode_ws_size bytes, which is 0 for other calls, 256-byte

@@ -667,18 +667,35 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         // of 32 new tokens could have read rows of the last call but one.
         if (tid == 0) pdl_trigger();
         uint32_t qf[16][2];
+        float qs0 = kScaleLog2, qs1 = kScaleLog2;  // e4m3: what a score of this lane's two columns is scaled by
         if constexpr (kFp8) {
-            // dims 64 c4 .. 64 c4 + 63 of the row, converted to f16 once
+            // dims 64 c4 .. 64 c4 + 63 of the row, converted to f16 once.  bf16 has
+            // the wider range: a power of two first takes the row's largest element
+            // to 2^14 .. 2^15, exactly, and goes into the scores' scale
             uint4 w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                w[i] = qr ? __ldg(reinterpret_cast<const uint4 *>(qr + 64 * c4) + i) : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t top = 0u;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                qf[2 * i][0] = bits_of(__floats2half2_rn(bf16_lo(w[i].x), bf16_hi(w[i].x)));
-                qf[2 * i][1] = bits_of(__floats2half2_rn(bf16_lo(w[i].y), bf16_hi(w[i].y)));
-                qf[2 * i + 1][0] = bits_of(__floats2half2_rn(bf16_lo(w[i].z), bf16_hi(w[i].z)));
-                qf[2 * i + 1][1] = bits_of(__floats2half2_rn(bf16_lo(w[i].w), bf16_hi(w[i].w)));
+                w[i] = qr ? __ldg(reinterpret_cast<const uint4 *>(qr + 64 * c4) + i) : make_uint4(0u, 0u, 0u, 0u);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                             __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+            }
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int ex = static_cast<int>(max(top >> 16, top & 0xffffu) >> 7);  // biased exponent
+            // (zeros, and rows with an infinity or NaN, stay as they are)
+            const int e = ex == 0 || ex == 0xff ? 0 : max(ex - 127 - 14, -100);
+            const float dn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+            const float up = kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            qs0 = __shfl_sync(0xffffffffu, up, 8 * c4);
+            qs1 = __shfl_sync(0xffffffffu, up, 8 * c4 + 4);
+            const auto pair = [&](uint32_t x) { return bits_of(__floats2half2_rn(dn * bf16_lo(x), dn * bf16_hi(x))); };
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                qf[2 * i][0] = pair(w[i].x);
+                qf[2 * i][1] = pair(w[i].y);
+                qf[2 * i + 1][0] = pair(w[i].z);
+                qf[2 * i + 1][1] = pair(w[i].w);
             }
         } else {
 #pragma unroll
@@ -863,7 +880,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
 #pragma unroll
                 for (int u16 = 0; u16 < kSub; ++u16) {
                     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-                    float fa = kScaleLog2, fb = kScaleLog2;
+                    float ka_scl = 1.f, kb_scl = 1.f;  // e4m3: the keys' scales
                     if constexpr (kFp8) {
                         // two accumulator chains, a quarter of the dims at a time
 #pragma unroll
@@ -884,8 +901,8 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                                 mma_half((j & 1) ? sb : sa, z[j][0], z[j][1], z[j][2], z[j][3], qf[4 * i + j][0],
                                          qf[4 * i + j][1]);
                         }
-                        fa *= scl[16 * u16 + g];
-                        fb *= scl[16 * u16 + g + 8];
+                        ka_scl = scl[16 * u16 + g];
+                        kb_scl = scl[16 * u16 + g + 8];
                     } else {
                         // two accumulator chains, four K fragments loaded before their MMAs
                         const uint32_t kbs = s_base + slot * F::stage;
@@ -903,10 +920,10 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                         }
                     }
                     const int ka = pos_of(u.sp, v0) + 16 * u16 + g, kb = ka + 8;
-                    sx[u16][0] = sees(p0, ka, a.window, a.n_sink) ? (sa[0] + sb[0]) * fa : -INFINITY;
-                    sx[u16][1] = sees(p1, ka, a.window, a.n_sink) ? (sa[1] + sb[1]) * fa : -INFINITY;
-                    sx[u16][2] = sees(p0, kb, a.window, a.n_sink) ? (sa[2] + sb[2]) * fb : -INFINITY;
-                    sx[u16][3] = sees(p1, kb, a.window, a.n_sink) ? (sa[3] + sb[3]) * fb : -INFINITY;
+                    sx[u16][0] = sees(p0, ka, a.window, a.n_sink) ? ((sa[0] + sb[0]) * ka_scl) * qs0 : -INFINITY;
+                    sx[u16][1] = sees(p1, ka, a.window, a.n_sink) ? ((sa[1] + sb[1]) * ka_scl) * qs1 : -INFINITY;
+                    sx[u16][2] = sees(p0, kb, a.window, a.n_sink) ? ((sa[2] + sb[2]) * kb_scl) * qs0 : -INFINITY;
+                    sx[u16][3] = sees(p1, kb, a.window, a.n_sink) ? ((sa[3] + sb[3]) * kb_scl) * qs1 : -INFINITY;
                 }
                 // online softmax of the two columns
                 float t0 = -INFINITY, t1 = -INFINITY;

@@ -104,3 +104,17 @@ def test_e4m3_rows_whose_scale_is_not_finite():
             at = pkv.pg_row(lay, w.pgs[0], table, 0, pkv.VS, 0, pos)
             w._body(0).view(t.uint8)[at:at + 4].view(t.float32)[0] = value
             assert ((run(w, 4, q) & 0x7F80) == 0x7F80).all(), (pos, value)
+
+
+def test_e4m3_queries_beyond_fp16():
+    # queries of bf16's range against keys as small or large the other way: the
+    # scores, and so the outputs, are those of the definition
+    lay = pkv.layout(1, 2, 256, 0, pkv.KV_E4M3)
+    for e in (-40, -18, 14, 20, 60):
+        ss = streams_of([200, 90], 2, seed=70)
+        for s in ss:
+            s.k[0] = synth.scale_pow2(s.k[0], -e)
+        q = [synth.scale_pow2(x, e) for x in queries_of([2, 1], 8, seed=71)]
+        w = Windowed(lay, ss, [2, 1], 64, 4, 16, seed=1)
+        ok, report = within_tol(run(w, 8, q), w.reference(0, q))
+        assert ok, (e, report)
