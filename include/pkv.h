@@ -75,11 +75,12 @@ extern "C" {
 #define PKV_DEV_TIMEOUT 2u  /* a pipeline wait ran past its time limit     */
 #define PKV_DEV_SMEM 4u     /* a kernel's shared memory was not at the
                                alignment its layout needs; it did nothing  */
-#define PKV_DEV_RANGE 8u    /* the tensor-core attention (pkv_prefill, and
-                               a decode call's tensor-core route) summed a
-                               non-finite value: a V entry beyond fp16's
-                               range (|v| > 65,504) in a call whose PV
-                               product runs in fp16, or non-finite inputs */
+#define PKV_DEV_RANGE 8u    /* the tensor-core attention (pkv_prefill, a decode
+                               call's tensor-core route, pkv_window_prefill)
+                               summed a non-finite value: a V entry beyond
+                               fp16's range (|v| > 65,504) in a call whose PV
+                               product runs in fp16, or non-finite inputs; or
+                               pkv_window_prefill met scores beyond 4.6e7  */
 
 /* kinds of rows (pkv_pg_row, pkv_gather) */
 #define PKV_K 0
@@ -410,8 +411,9 @@ int pkv_window_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_s
  * as it is and V in fp16; both products run as tcgen05 MMAs with float32
  * accumulation, P in fp16 (11 significant bits).  So a V entry is exact for
  * magnitudes 2^-14 to 65,280, rounded to fp16's 2^-24 grid below that, and one
- * beyond 65,504 makes the output non-finite and sets PKV_DEV_RANGE.  Rows
- * that no query of the chunk reads and their pages' table entries are not
+ * beyond 65,504 makes the output non-finite and sets PKV_DEV_RANGE, as does a
+ * largest score (q.k / 16) of a query beyond 4.6e7, where float32 steps over
+ * whole units.  Rows that no query of the chunk reads and their pages' table entries are not
  * looked at; a row that some of the chunk's queries read and others do not
  * must hold finite values.  ws: device, >= pkv_window_prefill_ws_size bytes,
  * 256-byte aligned, no initialization, one ws per in-flight call.  Paged

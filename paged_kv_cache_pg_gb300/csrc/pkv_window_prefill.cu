@@ -65,10 +65,9 @@ constexpr int kPRegion = kM * 128;   // 64 keys of the 128 P rows
 constexpr int kPBuf = 2 * kPRegion;  // P of a tile; two tiles' buffers
 constexpr int kOffK = 2 * kPBuf, kOffV = kOffK + kSlots * kSlotBytes;
 static_assert(4 * kVRegion == kSlotBytes, "a V slot is 32 keys of four regions");
-constexpr int kOffRed = kOffV + kSlots * kSlotBytes;   // [tile parity][half][row] bf16 row maxima
-constexpr int kOffSum = kOffRed + 2 * 2 * kM * 2;         // [half][row] float sums of an item
-constexpr int kOffMax = kOffSum + 2 * kM * 4;             // [row] bf16 maxima of an item
-constexpr int kOffBar = kOffMax + kM * 2;
+constexpr int kOffRed = kOffV + kSlots * kSlotBytes;   // [tile parity][half][row] row maxima
+constexpr int kOffSum = kOffRed + 2 * 2 * kM * 4;         // [row] sums of an item
+constexpr int kOffBar = kOffSum + kM * 4;
 enum Bars {
     kKFull = 0,            // a ring's slots: filled, and free again
     kKEmpty = kSlots,
@@ -81,8 +80,8 @@ enum Bars {
     kQFull = kODone + 2,               // a half of an item's Q is in TMEM (two barriers)
     kQEmpty = kQFull + 2, // ... and its last S product is done
     kOLast,               // an item's last PV product is done
-    kOFree,               // ... and its O, sums and maxima have been read
-    kSums,                // an item's sums and maxima are in shared memory
+    kOFree,               // ... and its O and sums have been read
+    kSums,                // an item's sums are in shared memory
     kRed,                 // a tile's half-row maxima are in shared memory
     kDrain,               // a failed issuer's products are done (S, PV)
     kNumBars = kDrain + 2
@@ -91,6 +90,10 @@ constexpr int kSmem = kOffBar + kNumBars * 8 + 16;
 static_assert(kSmem <= 232448, "above the 227 KB a CTA may hold");
 constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(256)
 constexpr float kRescale = 8.f;  // rescale O when the max grows by more than 2^8
+// Row maxima beyond this (log2 units) are reported: float32 steps of 4 and more
+// lie between scores there, and the reference's own rounding, up to half a step,
+// would take P out of fp16's range.
+constexpr float kFarScore = 67108864.f;  // 2^26
 
 struct ChunkArgs {
     const uint16_t *q;
@@ -99,6 +102,7 @@ struct ChunkArgs {
     uint16_t *rows16;   // the gathered rows: K, then V in fp16
     int64_t n_rows;     // rows of each
     int32_t window, n_sink, n_items;
+    int32_t split;      // whether some stream's M-tiles are split
     int32_t map_k, map_v, map_run;
     int32_t row0[PKV_MAX_SEQS];  // first gathered row of the stream (KV head 0)
 };
@@ -239,14 +243,6 @@ __device__ __forceinline__ void quad_transpose(uint4 *v, int lane) {
     }
 }
 
-// bf16 bits of a float rounded up (toward +infinity).
-__device__ __forceinline__ uint16_t bf16_up(float x) {
-    uint32_t u = __float_as_uint(x);
-    if (!(u >> 31)) u += 0xffffu;
-    return static_cast<uint16_t>(u >> 16);
-}
-__device__ __forceinline__ float bf16_float(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
-
 __global__ void __launch_bounds__(kThreads, 1)
     window_chunk(const __grid_constant__ Common c, const __grid_constant__ DecodeMaps maps,
                  const __grid_constant__ ChunkArgs a) {
@@ -286,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
+    if (tid < kM) reinterpret_cast<float *>(smem + kOffSum)[tid] = 0.f;
     // tcgen05 alloc, dealloc, ld and st are warp-collective (.sync.aligned):
     // every one follows a __syncwarp, because a CTA barrier does not
     // reconverge a warp whose lanes took different paths before it
@@ -319,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------- softmax: row r (TMEM lane r) by two threads, keys 64 hf .. 64 hf + 63 of a tile -------
         const int r = lane + 32 * (warp & 3), hf = warp >> 2;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        uint16_t *const red = reinterpret_cast<uint16_t *>(smem + kOffRed);
+        float *const red = reinterpret_cast<float *>(smem + kOffRed);
         uint8_t *const p_row = smem + hf * kPRegion + r * 128;
         // positions fit 31 bits, sums of two of them clamped to 30 do
         constexpr int kFar = 1 << 30;
@@ -333,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // zero, so their scores are finite, and they are never written
             const int qpos = r < t.rows ? sd.len - sd.n_new + (t.col0 + r) / G : kFar;
             const int win0 = r < t.rows ? max(qpos - a.window, -kFar) : -kFar;  // keys above it are in the row's window
-            float m_raw = -INFINITY, m_used = -INFINITY, l = 0.f;
+            float m_used = -INFINITY, l = 0.f;
             for (int n = 0; n < t.ntiles; ++n, ++T) {
                 if (!(ok = wait_warp(kSFull, T))) break;
                 tc_fence_after();
@@ -365,20 +362,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!((j < 32 ? lo : hi) & (1u << (j & 31)))) x[j] = -INFINITY;
                 }
                 // this half's max as eight interleaved chains, then the row's
-                // from the partner thread; both take it rounded up to bf16 (a
-                // softmax reference need not be exact, only the same for both)
+                // from the partner thread, in float32 (a reference above the
+                // maximum, by a coarser rounding of large scores, takes P out of
+                // fp16's range)
                 float m8[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) m8[j] = x[j];
 #pragma unroll
                 for (int j = 8; j < 64; ++j) m8[j & 7] = fmaxf(m8[j & 7], x[j]);
-                const uint16_t lmx = bf16_up(fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
-                                                   fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7]))));
+                const float lmx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])),
+                                        fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
                 red[((T & 1) * 2 + hf) * kM + r] = lmx;
                 mbar_arrive(&bars[kRed]);
                 if (!(ok = wait_warp(kRed, T))) break;
-                const float raw = fmaxf(bf16_float(lmx), bf16_float(red[((T & 1) * 2 + (hf ^ 1)) * kM + r]));
-                const float mx = raw * kScaleLog2;  // log2 units; -inf when the whole row of the tile is masked
+                const float mx = fmaxf(lmx, red[((T & 1) * 2 + (hf ^ 1)) * kM + r]) * kScaleLog2;  // log2 units; -inf when the whole row of the tile is masked
                 const bool grow = m_used != -INFINITY && mx > m_used + kRescale;
                 if (__any_sync(0xffffffffu, grow)) {
                     // correct this thread's half of O: the previous tile's
@@ -398,11 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     l *= alpha;
-                    m_raw = fmaxf(m_raw, raw);
                     m_used = m_new;
                 } else if (m_used == -INFINITY) {
-                    m_raw = raw;  // nothing accumulated yet: O is still zero
-                    m_used = mx;
+                    m_used = mx;  // nothing accumulated yet: O is still zero
                 }
                 // p = 2^(s * scale - m); a masked score is -inf and gives 0 (the
                 // offset is 0 while every score so far was masked).  fp16: 11
@@ -432,11 +427,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(&bars[kPFull + (T & 1)]);
             }
             if (!ok) break;
-            // the row's sum (this thread's half) and maximum, for the edge warps
+            // the row's sum, for the edge warps, from zero (two terms: the same in
+            // either order)
             if (it > 0 && !(ok = wait_warp(kOFree, it - 1))) break;
-            reinterpret_cast<float *>(smem + kOffSum)[hf * kM + r] = l;
-            if (hf == 0) reinterpret_cast<uint16_t *>(smem + kOffMax)[r] = bf16_up(m_raw);
+            atomicAdd(reinterpret_cast<float *>(smem + kOffSum) + r, l);
             mbar_arrive(&bars[kSums]);
+            if (hf == 0) {
+                // (rows past the M-tile's end score 0)
+                if (m_used != -INFINITY && fabsf(m_used) > kFarScore && c.status) atomicOr(c.status, PKV_DEV_RANGE);
+                if (a.split) {
+                    // a split's maximum, to the workspace (the scores came of tiles
+                    // copied behind the grid-dependency wait: the last call is done
+                    // with it).  The item is looked up anew: kept along the tiles it
+                    // would not fit the registers
+                    int again = i;
+                    asm volatile("" : "+r"(again));
+                    const Item e = item_at(c, a, again);
+                    const SeqDev &se = c.seq[e.s];
+                    float *const part_ml = a.ws + se.ws_off + (int64_t)H * se.nsplit * se.ncols * kHeadDim;
+                    if (se.nsplit > 1 && r < e.rows)
+                        part_ml[2 * (((int64_t)e.kvh * se.nsplit + e.split) * se.ncols + e.col0 + r)] = m_used;
+                }
+            }
         }
     } else if (warp < kWarpS) {
         // ------- edge: Q into TMEM columns 0-127 (bf16 pairs), O out -------
@@ -511,9 +523,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             const SeqDev &sd = c.seq[t.s];
             const bool row_ok = r < t.rows, single = sd.nsplit == 1;
-            const float *sums = reinterpret_cast<const float *>(smem + kOffSum);
-            const float l = sums[r] + sums[kM + r];
-            const float m = bf16_float(reinterpret_cast<const uint16_t *>(smem + kOffMax)[r]) * kScaleLog2;
+            float *const sum = reinterpret_cast<float *>(smem + kOffSum) + r;
+            const float l = *sum;
+            *sum = 0.f;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const int64_t prow = ((int64_t)t.kvh * sd.nsplit + t.split) * sd.ncols + t.col0 + r;
             const int64_t mine = !row_ok ? -1 : single ? q_row(t) : prow;  // output row, or the partials'
@@ -567,10 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (row_ok && !single) {
-                part_ml[prow * 2 + 0] = m;
-                part_ml[prow * 2 + 1] = l;
-            }
+            if (row_ok && !single) part_ml[prow * 2 + 1] = l;  // (its maximum: the softmax warps)
             if (row_ok && odd.x + odd.y != 0.f && c.status) atomicOr(c.status, PKV_DEV_RANGE);
             t = t2;
         }
@@ -846,6 +855,7 @@ int launch_window_prefill(const Common &c, const DecodePlan &plan, int32_t windo
     a.window = window;
     a.n_sink = n_sink;
     a.n_items = plan.total_items;
+    a.split = plan.total_comb > 0;
     int64_t rows = 0;
     for (int s = 0; s < PKV_MAX_SEQS; ++s) {
         a.row0[s] = -1;
