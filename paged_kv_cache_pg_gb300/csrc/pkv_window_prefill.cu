@@ -41,6 +41,7 @@
 // queries at 31,000 with a window of 4,096 (34 GFLOP in 64 items, split over the
 // SMs): 53 us, 6 of them the gather and 6 the combine.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 
 #include "pkv_tc.cuh"
@@ -438,7 +439,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (a.split) {
                     // a split's maximum, to the workspace (the scores came of tiles
                     // copied behind the grid-dependency wait: the last call is done
-                    // with it).  The item is looked up anew: kept along the tiles it
+                    // with it); a finite one for NaN and infinity, whose sums the
+                    // combine takes as they are.  The item is looked up anew: kept along the tiles it
                     // would not fit the registers
                     int again = i;
                     asm volatile("" : "+r"(again));
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const SeqDev &se = c.seq[e.s];
                     float *const part_ml = a.ws + se.ws_off + (int64_t)H * se.nsplit * se.ncols * kHeadDim;
                     if (se.nsplit > 1 && r < e.rows)
-                        part_ml[2 * (((int64_t)e.kvh * se.nsplit + e.split) * se.ncols + e.col0 + r)] = m_used;
+                        part_ml[2 * (((int64_t)e.kvh * se.nsplit + e.split) * se.ncols + e.col0 + r)] = fminf(m_used, FLT_MAX);
                 }
             }
         }
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *const sum = reinterpret_cast<float *>(smem + kOffSum) + r;
             const float l = *sum;
             *sum = 0.f;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = 1.f / l;  // (0 only where every score is -infinity: NaN)
             const int64_t prow = ((int64_t)t.kvh * sd.nsplit + t.split) * sd.ncols + t.col0 + r;
             const int64_t mine = !row_ok ? -1 : single ? q_row(t) : prow;  // output row, or the partials'
             int64_t row[4];
@@ -579,8 +581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (row_ok && !single) part_ml[prow * 2 + 1] = l;  // (its maximum: the softmax warps)
-            if (row_ok && odd.x + odd.y != 0.f && c.status) atomicOr(c.status, PKV_DEV_RANGE);
+            // (its maximum: the softmax warps.  A sum that is NaN comes with an O
+            // that is, which the combine divides only by a sum above zero)
+            if (row_ok && !single) part_ml[prow * 2 + 1] = l == l ? l : 1.f;
+            if (row_ok && (odd.x + odd.y != 0.f || (single && !(l > 0.f))) && c.status) atomicOr(c.status, PKV_DEV_RANGE);
             t = t2;
         }
     } else if (warp == kWarpS || warp == kWarpPv) {

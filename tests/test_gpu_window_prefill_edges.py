@@ -6,7 +6,7 @@ import pytest
 from paged_kv_cache_pg_gb300 import pkv
 
 from gpu_setup import dev_u16, host_u16, torch, within_tol
-from window_setup import Windowed, queries_of, streams_of
+from window_setup import Windowed, attend, queries_of, streams_of, values
 
 pytestmark = pytest.mark.gpu
 
@@ -82,4 +82,36 @@ def test_scores_with_a_large_common_part(shift, lens, n_new, window):
         q.append(bf16_of(x))
     w = Windowed(lay, ss, n_new, window, sinks, 16, seed=2)
     ok, report = within_tol(run(w, hq, q), w.reference(0, q))
+    assert ok, report
+
+
+NAN, INF, NINF = 0x7FC1, 0x7F80, 0xFF80
+# what KV head 0 of the first stream (or all queries of its heads) holds, as
+# (tensor, position from the stream's end, dim, bits); every query reads it
+BAD = [[("k", 50, 3, NAN)], [("v", 50, 3, NAN)], [("q", 0, 5, NAN)], [("k", 50, 3, INF)], [("q", 0, 5, INF)],
+       [("v", 50, 3, INF), ("v", 40, 3, NINF)], [("k", p, 0, NAN) for p in range(1, 301)]]
+
+
+@pytest.mark.parametrize("case", range(len(BAD)))
+@pytest.mark.parametrize("lens,n_new,window", [([300, 64], [20, 64], 100), ([2600], [20], 2400)])
+def test_what_is_not_finite_where_it_is_read_is_not_finite_in_the_output(lens, n_new, window, case):
+    hq, hkv, sinks = 8, 2, 4
+    grp = hq // hkv
+    lay = pkv.layout(1, hkv, 256, 0)
+    ss = streams_of(lens, hkv, seed=61)
+    q = queries_of(n_new, hq, seed=62)
+    clean = Windowed(lay, ss, n_new, window, sinks, 16, seed=5).reference(0, q)
+    for what, back, dim, bits in BAD[case]:
+        if what == "q":
+            q[0][:, :grp, dim] = bits
+        else:
+            getattr(ss[0], what)[0][lens[0] - back, 0, dim] = bits
+    got = run(Windowed(lay, ss, n_new, window, sinks, 16, seed=5), hq, q, expect=pkv.DEV_RANGE)
+    with np.errstate(all="ignore"):
+        want = attend(values(ss[0].k[0], 0), values(ss[0].v[0], 0), q[0], lens[0], window, sinks)
+    n = n_new[0]
+    odd = (got[:n, :grp] & 0x7F80) == 0x7F80
+    assert np.array_equal(odd, ~np.isfinite(want[:, :grp])) and odd.any()
+    rest = np.concatenate([got[:n, grp:].ravel(), got[n:].ravel()])
+    ok, report = within_tol(rest, np.concatenate([clean[:n, grp:].ravel(), clean[n:].ravel()]))
     assert ok, report
