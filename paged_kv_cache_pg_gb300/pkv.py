@@ -11,6 +11,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 from . import build as _build
@@ -112,9 +113,9 @@ def load(path: Optional[str] = None):
         "pkv_decode": [LP, SP, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, vp],
         "pkv_decode_static": [LP, SP, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp],
         "pkv_window_decode_ws_size": [LP, SP, i32, i32, i32, i32, ctypes.POINTER(sz)],
-        "pkv_window_decode": [LP, SP, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, vp],
+        "pkv_window_decode": [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, vp],
         "pkv_window_prefill_ws_size": [LP, SP, i32, i32, i32, i32, ctypes.POINTER(sz)],
-        "pkv_window_prefill": [LP, SP, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp, vp],
+        "pkv_window_prefill": [vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, sz, vp, vp],
         "pkv_window_dead_pages": [i32, i32, i32, i32, ctypes.POINTER(i32), ctypes.POINTER(i32)],
         "pkv_prefill_ws_size": [LP, SP, i32, i32, ctypes.POINTER(sz)],
         "pkv_prefill": [LP, SP, i32, i32, i32, vp, vp, vp, sz, vp, vp],
@@ -156,10 +157,12 @@ def _torch_streams():
         import torch
         # the raw handle without building a Stream object (about 3 us of a call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         if torch.cuda.is_available():
             torch.cuda.init()
-        _current = (torch, getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
-                    raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+        else:
+            device = lambda: -2   # of no tensor
+        _current = (torch, device, raw or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
     return _current
 
 
@@ -194,6 +197,74 @@ def _here(what: str, *tensors, dtype=None):
             t = t.data_ptr()
         out.append(t)
     return out
+
+
+_counts = {}  # streams of a launch: reader of their new tokens
+_types = None  # types of 16-bit rows; the status word's
+
+
+def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sink: int, q, out, ws, status, stream,
+            chunk: bool, k=None, v=None, ik=None):
+    """A windowed call.  Tensors have to be contiguous, on the current device, of
+    the rows' type and as long as the launch's packed rows; rows given as ints
+    (addresses) are taken as they are.  Written out for each tensor: a small
+    call takes the GPU no longer than its arguments take here."""
+    global _types
+    if _types is None:
+        torch = (_current or _torch_streams())[0]
+        _types = frozenset((torch.bfloat16, torch.int16, torch.uint16)), torch.int32
+    arr, n = _seqs(seqs)
+    if arr._type_ is not Seq:
+        raise PkvError(EINVAL, f"{what}: the streams are not pkv_seq structures")
+    read = _counts.get(n)
+    if read is None:
+        at = Seq.n_new.offset
+        read = _counts[n] = struct.Struct("=" + f"{at}xi{ctypes.sizeof(Seq) - at - 4}x" * n).unpack_from
+    new = read(arr)[0] if n == 1 else sum(read(arr)) if n else 0
+    types, word = _types
+    dev, ws_bytes, rows = (_current or _torch_streams())[1](), 0, 512 * n_q_heads * new
+    if type(q) is not int and q is not None:
+        if q.get_device() != dev or q.dtype not in types or q.nbytes < rows or not q.is_contiguous():
+            _refuse(what, "q")
+        q = q.data_ptr()
+    if type(out) is not int and out is not None:
+        if out.get_device() != dev or out.dtype not in types or out.nbytes < rows or not out.is_contiguous():
+            _refuse(what, "out")
+        out = out.data_ptr()
+    if k is not None or v is not None:
+        rows = 512 * lay.n_kv_heads * new
+    if k is not None and type(k) is not int:
+        if k.get_device() != dev or k.dtype not in types or k.nbytes < rows or not k.is_contiguous():
+            _refuse(what, "k_new")
+        k = k.data_ptr()
+    if v is not None and type(v) is not int:
+        if v.get_device() != dev or v.dtype not in types or v.nbytes < rows or not v.is_contiguous():
+            _refuse(what, "v_new")
+        v = v.data_ptr()
+    if ik is not None and type(ik) is not int:
+        if ik.get_device() != dev or ik.dtype not in types or ik.nbytes < 2 * lay.idx_dim * new or not ik.is_contiguous():
+            _refuse(what, "ik_new")
+        ik = ik.data_ptr()
+    if ws is not None:  # (an address would say nothing of its size)
+        if type(ws) is int or ws.get_device() != dev or not ws.is_contiguous():
+            _refuse(what, "the workspace")
+        ws_bytes, ws = ws.nbytes, ws.data_ptr()
+    if status is not None and type(status) is not int:
+        if status.get_device() != dev or status.dtype is not word or status.nbytes < 4:
+            _refuse(what, "the status")
+        status = status.data_ptr()
+    lib, lay_at, seqs_at = load(), ctypes.addressof(lay), ctypes.addressof(arr)
+    if chunk:
+        rc = lib.pkv_window_prefill(lay_at, seqs_at, n, layer, n_q_heads, window, n_sink, q, out, ws, ws_bytes, status,
+                                    _stream(stream))
+    else:
+        rc = lib.pkv_window_decode(lay_at, seqs_at, n, layer, n_q_heads, window, n_sink, q, k, v, ik, out, ws, ws_bytes,
+                                   status, _stream(stream))
+    _check(rc, what)
+
+
+def _refuse(what: str, name: str):
+    raise PkvError(EINVAL, f"{what}: {name} is not a contiguous tensor of its type, long enough, on the current device")
 
 
 _np = _i32 = None
@@ -403,6 +474,8 @@ def tables_remap(tables, src, dst, stream=None):
         raise PkvError(EINVAL, "pkv_tables_remap: lists of different lengths")
     torch = (_current or _torch_streams())[0]
     n = len(tables)
+    if any(type(t) is int for t in tables):
+        raise PkvError(EINVAL, "pkv_tables_remap: the tables are tensors")
     ptrs = array.array("Q", _here("pkv_tables_remap", *tables, dtype=torch.int32)).tobytes()
     sizes = array.array("i", [t.numel() for t in tables]).tobytes()
     _check(load().pkv_tables_remap(ptrs, sizes, n, src, dst, n_moves, _stream(stream)),
@@ -461,13 +534,8 @@ def window_decode(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws=None, 
                   stream=None, k_new=None, v_new=None, ik_new=None):
     """Decode attention over the newest `window` positions and the first
     n_sink; with k_new/v_new (and ik_new) the new rows are stored too."""
-    arr, n = _seqs(seqs)
-    ws_bytes = 0 if ws is None else ws.nbytes
-    q, k_new, v_new, ik_new, out, ws, status = _here("pkv_window_decode", q, k_new, v_new, ik_new, out,
-                                                     ws, status)
-    _check(load().pkv_window_decode(ctypes.byref(lay), arr, n, layer, n_q_heads, window, n_sink, q,
-                                    k_new, v_new, ik_new, out, ws, ws_bytes, status,
-                                    _stream(stream)), "pkv_window_decode")
+    _window("pkv_window_decode", lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws, status, stream, False,
+            k_new, v_new, ik_new)
 
 
 def window_prefill_ws_size(lay, seqs, n_q_heads, window, n_sink) -> int:
@@ -482,11 +550,7 @@ def window_prefill(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws, stat
                    stream=None):
     """Chunk attention on the tensor cores over the newest `window` positions
     of each query and the first n_sink (the chunk already stored)."""
-    arr, n = _seqs(seqs)
-    ws_bytes = 0 if ws is None else ws.nbytes
-    q, out, ws, status = _here("pkv_window_prefill", q, out, ws, status)
-    _check(load().pkv_window_prefill(ctypes.byref(lay), arr, n, layer, n_q_heads, window, n_sink, q,
-                                     out, ws, ws_bytes, status, _stream(stream)), "pkv_window_prefill")
+    _window("pkv_window_prefill", lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws, status, stream, True)
 
 
 def window_dead_pages(page_pos: int, length: int, window: int, n_sink: int):
