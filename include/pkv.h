@@ -229,7 +229,8 @@ int pkv_pages_holders(pkv_arena *arena, const int32_t *ids, int32_t n, int32_t *
  * held once more, by the caller, who queues the copies (pkv_pages_copy) and
  * the tables' rewrite (pkv_tables_remap) on the streams' stream, renames the
  * pages in its own lists, and gives the src ids back with `defer` set.  Run
- * pages and pages being given back stay where they are. */
+ * pages, pages being given back and the src of an earlier plan, until it has
+ * been given back, stay where they are. */
 int pkv_arena_compact(pkv_arena *arena, int32_t max_moves, int32_t *src_out, int32_t *dst_out,
                       int32_t *n_out);
 

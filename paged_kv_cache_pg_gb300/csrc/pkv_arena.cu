@@ -23,6 +23,7 @@ struct pkv_arena {
     std::vector<uint8_t> taken;  // 1 = a KV page, 2 = a run's page; held or pending release
     std::vector<int32_t> holders;  // of a KV page: streams that hold it, pending gives included
     std::vector<int32_t> going;    // of those, gives that wait for their stream
+    std::vector<uint8_t> vacated;  // a compaction has moved the page; it waits for its last give
     std::map<int32_t, int32_t> runs;  // first id -> pages of each run held now
     int32_t n_free = 0;
     int32_t low = 0;  // no free page below this id
@@ -62,7 +63,7 @@ void cuda_destroy(void *, void *ev) { cudaEventDestroy(static_cast<cudaEvent_t>(
 const pkv_event_ops kCudaOps = {cuda_record, cuda_query, cuda_destroy, nullptr};
 
 void free_page(pkv_arena *a, int32_t id) {
-    a->taken[id] = 0;
+    a->taken[id] = a->vacated[id] = 0;
     a->n_free++;
     if (id < a->low) a->low = id;
 }
@@ -144,6 +145,7 @@ extern "C" int pkv_arena_create(const pkv_layout *layout, int32_t page_pos, void
         a->taken.assign(static_cast<size_t>(n), 0);
         a->holders.assign(static_cast<size_t>(n), 0);
         a->going.assign(static_cast<size_t>(n), 0);
+        a->vacated.assign(static_cast<size_t>(n), 0);
     } catch (...) {  // no host memory for the books of so many pages
         delete a;
         return PKV_EINVAL;
@@ -273,10 +275,11 @@ extern "C" int pkv_arena_compact(pkv_arena *a, int32_t max_moves, int32_t *src_o
     for (int32_t src = a->n_pages - 1; moves < max_moves; --src) {
         while (dst < src && a->taken[dst]) ++dst;
         if (dst >= src) break;  // no free page below the highest one left
-        if (live_holders(a, src) < 1) continue;
+        if (live_holders(a, src) < 1 || a->vacated[src]) continue;
         a->taken[dst] = 1;
         a->holders[dst] = live_holders(a, src);
         a->holders[src] = a->going[src] + 1;  // the caller's, beside the gives under way
+        a->vacated[src] = 1;
         a->n_free--;
         src_out[moves] = src;
         dst_out[moves++] = dst;
