@@ -15,7 +15,8 @@
 // lanes) and copies a whole 16-row page run by 2D TMA, or key by key with
 // cp.async.  Cached rows more than 32 positions below the new tokens stream
 // before the grid-dependency wait, and every dense CTA lets the next kernel
-// start at entry; tiles past the slots are prefetched into L2.  The warps
+// start at entry (behind the wait when it stores new rows: 3,045 GB/s over the
+// page sweep against 3,027); tiles past the slots are prefetched into L2.  The warps
 // compute S^T = K Q^T and O^T += V^T P^T with warp MMAs (bf16 in, float32
 // accumulate), keep an online softmax per query column, and merge their key
 // slices in a fixed order.  Splits have a fixed length set by the stream's
@@ -390,9 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
     __syncthreads();
-    // dense: nothing this CTA writes is read by the next kernel before its own
-    // wait (a decode reads no row within kFreshGuard of its new tokens early)
-    if (!kSparse && tid == 0) pdl_trigger();
+    // dense: the next kernel may start at once; it reads no row early that this
+    // one writes (none within kFreshGuard of its new tokens).  A call that stores
+    // lets go behind its wait: let go here, rows of the call before it, or of one
+    // before that, could still be on their way when the next kernel reads them
+    if (!kSparse && tid == 0 && a.k_new == nullptr) pdl_trigger();
 
     const uint64_t pol = policy_evict_first();
     // Rows of cached positions more than kFreshGuard below the new tokens do
@@ -424,6 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         (active && bcol < ncols) ? a.q + q_row<kSparse>(c, sd, u, bcol) * kHeadDim : nullptr;
     asm volatile("" ::"l"(qr));
     if (!waited) pdl_wait();
+    if (!kSparse && tid == 0 && a.k_new != nullptr) pdl_trigger();
 
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float acc[8][4];  // O^T for dims 128*dh .. 128*dh+127

@@ -274,9 +274,10 @@ __global__ void __maxnreg__(192)
         }
     };
 
-    // nothing this CTA writes is read by the next kernel before its own wait
-    // (a decode reads no row within 32 positions of its new tokens early)
-    if (tid == 0) pdl_trigger();
+    // the next kernel reads no row early that this one writes (none within 32
+    // positions of its new tokens); a call that stores lets it start behind its
+    // own wait, when the rows of the calls before it are there
+    if (tid == 0 && a.k_new == nullptr) pdl_trigger();
     // rows of cached positions more than 32 below the new tokens stream
     // before the grid-dependency wait; later tiles (a decode of the same
     // stream queued just before may still be storing the rows right below
@@ -299,6 +300,7 @@ __global__ void __maxnreg__(192)
     }
     asm volatile("" ::"l"(qr));
     pdl_wait();
+    if (tid == 0 && a.k_new != nullptr) pdl_trigger();
     __syncthreads();
     for (; issued < kDepth8 && issued < my_tiles; ++issued) issue(issued);
 

@@ -229,12 +229,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
     // every CTA is running: it waits for this grid before reading anything
     // this grid writes, except cached rows more than 32 positions below its
     // own new tokens, which the rows stored here (a decode call's at most 32
-    // new rows a stream) are not
-    if (tid == 0) pdl_trigger();
+    // new rows a stream) are not.  A call that stores lets go behind its wait,
+    // when the rows of the calls before it are there
+    if (tid == 0 && a.k_new == nullptr) pdl_trigger();
 
     if (warp < kSoftWarps) {
         // ------- softmax: row r (TMEM lane r) by two threads, keys 64 hf .. 64 hf + 63 of a tile -------
         pdl_wait();
+        if (tid == 0 && a.k_new != nullptr) pdl_trigger();
         const int r = lane + 32 * (warp & 3);
         const int hf = warp >> 2;
         const int col = col0 + r;
