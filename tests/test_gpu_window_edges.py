@@ -43,14 +43,14 @@ def test_one_workspace_for_every_length_near_a_split_s_border(fmt):
 
 
 
-def run(w, hq, q_list):
+def run(w, hq, q_list, **new):
     t = torch()
     seqs = w.seqs()
     q = dev_u16(np.concatenate(q_list))
     out = t.zeros_like(q)
     size = pkv.window_decode_ws_size(w.lay, seqs, hq, w.window, w.sinks)
     ws = t.full((max(64, size // 4),), float("nan"), dtype=t.float32, device="cuda") if size else None
-    pkv.window_decode(w.lay, seqs, 0, hq, w.window, w.sinks, q, out, ws)
+    pkv.window_decode(w.lay, seqs, 0, hq, w.window, w.sinks, q, out, ws, **new)
     return host_u16(out)
 
 
@@ -118,3 +118,35 @@ def test_e4m3_queries_beyond_fp16():
         w = Windowed(lay, ss, [2, 1], 64, 4, 16, seed=1)
         ok, report = within_tol(run(w, 8, q), w.reference(0, q))
         assert ok, (e, report)
+
+
+# calls of more CTAs than the GPU holds that the cost model leaves to clusters, in
+# waves: 384 CTAs of 8 pieces, of up to 32 columns in two passes and of 16; a few
+# streams with fewer new tokens, and one without
+@pytest.mark.parametrize("fmt,top", [(pkv.KV_BF16, 4), (pkv.KV_E4M3, 4), (pkv.KV_E4M3, 2)])
+def test_clusters_in_waves(fmt, top):
+    t = torch()
+    hq, hkv, window, sinks, idx = 16, 2, 4900, 4, 128     # pieces of some 570 keys
+    lay = pkv.layout(1, hkv, 256, idx, fmt)
+    n_new = [top] * 20 + [1, top, 0, top]
+    lens = [int(x) for x in np.linspace(4200, 6300, 22)] + [700, 5000]
+    base = streams_of([6300] * 2, hkv, idx, seed=300)          # two streams' rows, each at many lengths
+    streams = [synth.Stream(n, base[i & 1].k, base[i & 1].v, base[i & 1].ik) for i, n in enumerate(lens)]
+    for s in streams:
+        s.k, s.v, s.ik = (x[:, :s.length] for x in (s.k, s.v, s.ik))
+    q = queries_of(n_new, hq, seed=301)
+    a = Windowed(lay, streams, n_new, window, sinks, 64, seed=1, fused=True)
+    b = Windowed(lay, streams, n_new, window, sinks, 64, seed=1, fused=True)
+    pkv.store(lay, b.seqs(), 0, *b.new_rows(0))
+    k, v, ik = a.new_rows(0)
+    got = run(a, hq, q, k_new=k, v_new=v, ik_new=ik)
+    assert np.array_equal(got, run(b, hq, q))
+    assert t.equal(a.bufs[0], b.bufs[0])
+    rows = np.split(got, np.cumsum(n_new)[:-1])
+    for i in (0, 7, 20, 21, 23):
+        w = Windowed(lay, streams[i:i + 1], n_new[i:i + 1], window, sinks, 256, seed=i)
+        ok, report = within_tol(rows[i], w.reference(0, q[i:i + 1]))
+        assert ok, (i, report)
+        assert np.array_equal(run(w, hq, q[i:i + 1]), rows[i])      # alone: one cluster a KV head, or two
+    for _ in range(10):
+        assert np.array_equal(run(b, hq, q), got)
