@@ -61,8 +61,9 @@ struct DecodeMaps {
 // or -1 when none can be made (no driver entry point, or maps full).
 // bytes8: rows of 256 bytes (e4m3 codes, boxes of 128 x 16) instead of 256
 // bf16 elements (boxes of 64 x 16); tile: the 3D tile view, of code rows boxes
-// of {128, 16, 2}, of bf16 rows boxes of {64, box_rows, box_chunks} (box_rows a multiple of 16 up to 128,
-// box_chunks 1, 2 or 4).
+// of {128, 2, box_rows} (box_rows 16 or 32, box_chunks 2), of bf16 rows boxes of
+// {64, box_rows, box_chunks} (box_rows a multiple of 16 up to 128, box_chunks 1,
+// 2 or 4).
 int row_map(DecodeMaps &maps, int &n_maps, const void *base, uint64_t rows, bool bytes8,
             bool tile = false, int box_rows = 16, int box_chunks = 1);
 

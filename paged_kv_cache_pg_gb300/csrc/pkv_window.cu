@@ -770,63 +770,63 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
             }
             if constexpr (!kRuns) return;
             if (!kWide || ks_n > 1) {
-            const int cl = cg * 8 + 2 * c4;  // this lane's first column in the CTA
-            float4 *const jml = reinterpret_cast<float4 *>(smem + F::off_join_ml);  // [slice][two columns]
-            float4 *const jo = reinterpret_cast<float4 *>(smem + F::off_join) + cg * 8 * 32 + lane;
-            if (g == 0) jml[(ks * kBlockCols + cl) / 2] = make_float4(m[0], l[0], m[1], l[1]);
-            join_sync(ncg * ks_n * 32);
-            if (ks == 0) {
-                const float4 own = make_float4(m[0], l[0], m[1], l[1]);
-                for (int k = 1; k < ks_n; ++k) {
-                    const float4 ml = jml[(k * kBlockCols + cl) / 2];
-                    m[0] = fmaxf(m[0], ml.x);
-                    m[1] = fmaxf(m[1], ml.z);
-                }
-                const float w0 = m[0] == -INFINITY ? 0.f : ex2(own.x - m[0]);
-                const float w1 = m[1] == -INFINITY ? 0.f : ex2(own.z - m[1]);
-                l[0] = fmaf(w0, own.y, 0.f);
-                l[1] = fmaf(w1, own.w, 0.f);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    acc[i][0] = fmaf(w0, acc[i][0], 0.f);
-                    acc[i][1] = fmaf(w1, acc[i][1], 0.f);
-                    acc[i][2] = fmaf(w0, acc[i][2], 0.f);
-                    acc[i][3] = fmaf(w1, acc[i][3], 0.f);
-                }
-            }
-            for (int k = 1; k < ks_n; ++k) {
-                float w0 = 0.f, w1 = 0.f;
+                const int cl = cg * 8 + 2 * c4;  // this lane's first column in the CTA
+                float4 *const jml = reinterpret_cast<float4 *>(smem + F::off_join_ml);  // [slice][two columns]
+                float4 *const jo = reinterpret_cast<float4 *>(smem + F::off_join) + cg * 8 * 32 + lane;
+                if (g == 0) jml[(ks * kBlockCols + cl) / 2] = make_float4(m[0], l[0], m[1], l[1]);
+                join_sync(ncg * ks_n * 32);
                 if (ks == 0) {
-                    const float4 ml = jml[(k * kBlockCols + cl) / 2];
-                    w0 = m[0] == -INFINITY ? 0.f : ex2(ml.x - m[0]);
-                    w1 = m[1] == -INFINITY ? 0.f : ex2(ml.z - m[1]);
-                    l[0] = fmaf(w0, ml.y, l[0]);
-                    l[1] = fmaf(w1, ml.w, l[1]);
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {  // 8 tiles of 16 dims at a time
-                    if (k > 1 || h > 0) join_sync(ncg * ks_n * 32);  // the part before has been read
-                    if (ks == k) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float(&t)[4] = acc[8 * h + i];
-                            jo[i * 32] = make_float4(t[0], t[1], t[2], t[3]);
-                        }
+                    const float4 own = make_float4(m[0], l[0], m[1], l[1]);
+                    for (int k = 1; k < ks_n; ++k) {
+                        const float4 ml = jml[(k * kBlockCols + cl) / 2];
+                        m[0] = fmaxf(m[0], ml.x);
+                        m[1] = fmaxf(m[1], ml.z);
                     }
-                    join_sync(ncg * ks_n * 32);
+                    const float w0 = m[0] == -INFINITY ? 0.f : ex2(own.x - m[0]);
+                    const float w1 = m[1] == -INFINITY ? 0.f : ex2(own.z - m[1]);
+                    l[0] = fmaf(w0, own.y, 0.f);
+                    l[1] = fmaf(w1, own.w, 0.f);
+    #pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        acc[i][0] = fmaf(w0, acc[i][0], 0.f);
+                        acc[i][1] = fmaf(w1, acc[i][1], 0.f);
+                        acc[i][2] = fmaf(w0, acc[i][2], 0.f);
+                        acc[i][3] = fmaf(w1, acc[i][3], 0.f);
+                    }
+                }
+                for (int k = 1; k < ks_n; ++k) {
+                    float w0 = 0.f, w1 = 0.f;
                     if (ks == 0) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 v = jo[i * 32];
-                            float(&t)[4] = acc[8 * h + i];
-                            t[0] = fmaf(w0, v.x, t[0]);
-                            t[1] = fmaf(w1, v.y, t[1]);
-                            t[2] = fmaf(w0, v.z, t[2]);
-                            t[3] = fmaf(w1, v.w, t[3]);
+                        const float4 ml = jml[(k * kBlockCols + cl) / 2];
+                        w0 = m[0] == -INFINITY ? 0.f : ex2(ml.x - m[0]);
+                        w1 = m[1] == -INFINITY ? 0.f : ex2(ml.z - m[1]);
+                        l[0] = fmaf(w0, ml.y, l[0]);
+                        l[1] = fmaf(w1, ml.w, l[1]);
+                    }
+    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {  // 8 tiles of 16 dims at a time
+                        if (k > 1 || h > 0) join_sync(ncg * ks_n * 32);  // the part before has been read
+                        if (ks == k) {
+    #pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float(&t)[4] = acc[8 * h + i];
+                                jo[i * 32] = make_float4(t[0], t[1], t[2], t[3]);
+                            }
+                        }
+                        join_sync(ncg * ks_n * 32);
+                        if (ks == 0) {
+    #pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float4 v = jo[i * 32];
+                                float(&t)[4] = acc[8 * h + i];
+                                t[0] = fmaf(w0, v.x, t[0]);
+                                t[1] = fmaf(w1, v.y, t[1]);
+                                t[2] = fmaf(w0, v.z, t[2]);
+                                t[3] = fmaf(w1, v.w, t[3]);
+                            }
                         }
                     }
                 }
-            }
             }
             if (ks == 0) {
                 const int64_t n_part = (int64_t)sd.nsplit * a.pieces;  // of a unit
@@ -1072,7 +1072,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
     // after a wait that ran out, every copy issued lands before the memory goes
     if (failed)
         for (int j = max(0, issued - S); j < issued; ++j) mbar_wait(&x.full[j % B], (j / B) & 1, nullptr);
-    if (kRuns) return;  // window_combine merges the slices and pieces
+    if (kRuns) return;  // the slices are joined; window_combine merges the pieces
 
     // ---- merge the CTA's key slices, in order ----
     const int NC = ncg * 8;
