@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
         // of 32 new tokens could have read rows of the last call but one.
         if (tid == 0) pdl_trigger();
         uint32_t qf[16][2];
-        float qs0 = kScaleLog2, qs1 = kScaleLog2;  // e4m3: what a score of this lane's two columns is scaled by
+        float qs0, qs1;  // e4m3: what a score of this lane's two columns is scaled by
         if constexpr (kFp8) {
             // dims 64 c4 .. 64 c4 + 63 of the row, converted to f16 once.  bf16 has
             // the wider range: a power of two first takes the row's largest element
@@ -880,7 +880,6 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
 #pragma unroll
                 for (int u16 = 0; u16 < kSub; ++u16) {
                     float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-                    float ka_scl = 1.f, kb_scl = 1.f;  // e4m3: the keys' scales
                     if constexpr (kFp8) {
                         // two accumulator chains, a quarter of the dims at a time
 #pragma unroll
@@ -901,8 +900,11 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                                 mma_half((j & 1) ? sb : sa, z[j][0], z[j][1], z[j][2], z[j][3], qf[4 * i + j][0],
                                          qf[4 * i + j][1]);
                         }
-                        ka_scl = scl[16 * u16 + g];
-                        kb_scl = scl[16 * u16 + g + 8];
+                        const float ka_scl = scl[16 * u16 + g], kb_scl = scl[16 * u16 + g + 8];
+                        sa[0] = (sa[0] + sb[0]) * ka_scl * qs0;
+                        sa[1] = (sa[1] + sb[1]) * ka_scl * qs1;
+                        sa[2] = (sa[2] + sb[2]) * kb_scl * qs0;
+                        sa[3] = (sa[3] + sb[3]) * kb_scl * qs1;
                     } else {
                         // two accumulator chains, four K fragments loaded before their MMAs
                         const uint32_t kbs = s_base + slot * F::stage;
@@ -920,10 +922,11 @@ __global__ void __launch_bounds__(Cfg<kFp8>::threads, 2)
                         }
                     }
                     const int ka = pos_of(u.sp, v0) + 16 * u16 + g, kb = ka + 8;
-                    sx[u16][0] = sees(p0, ka, a.window, a.n_sink) ? ((sa[0] + sb[0]) * ka_scl) * qs0 : -INFINITY;
-                    sx[u16][1] = sees(p1, ka, a.window, a.n_sink) ? ((sa[1] + sb[1]) * ka_scl) * qs1 : -INFINITY;
-                    sx[u16][2] = sees(p0, kb, a.window, a.n_sink) ? ((sa[2] + sb[2]) * kb_scl) * qs0 : -INFINITY;
-                    sx[u16][3] = sees(p1, kb, a.window, a.n_sink) ? ((sa[3] + sb[3]) * kb_scl) * qs1 : -INFINITY;
+                    const auto score = [&](int i) { return kFp8 ? sa[i] : (sa[i] + sb[i]) * kScaleLog2; };
+                    sx[u16][0] = sees(p0, ka, a.window, a.n_sink) ? score(0) : -INFINITY;
+                    sx[u16][1] = sees(p1, ka, a.window, a.n_sink) ? score(1) : -INFINITY;
+                    sx[u16][2] = sees(p0, kb, a.window, a.n_sink) ? score(2) : -INFINITY;
+                    sx[u16][3] = sees(p1, kb, a.window, a.n_sink) ? score(3) : -INFINITY;
                 }
                 // online softmax of the two columns
                 float t0 = -INFINITY, t1 = -INFINITY;
