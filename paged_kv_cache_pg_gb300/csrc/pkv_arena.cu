@@ -202,7 +202,9 @@ extern "C" int pkv_pages_give(pkv_arena *a, const int32_t *ids, int32_t n, cudaS
     std::vector<int32_t> v;
     try {
         v.assign(ids, ids + n);
-        if (defer) a->pending.reserve(a->pending.size() + 1);
+        // room before anything changes; grown by doubling, as the list may be long
+        if (defer && a->pending.size() == a->pending.capacity())
+            a->pending.reserve(std::max<size_t>(16, 2 * a->pending.size()));
     } catch (...) {  // no host memory for the sorted list
         return PKV_EINVAL;
     }

@@ -71,3 +71,26 @@ def test_plans_in_a_row_follow_a_model():
                 owed = []
             assert a.holders(range(n)).tolist() == held.astype(int).tolist()
         a.close()
+
+
+def test_pending_gives_cost_alike_however_many_there_are():
+    import time
+    E = pkv.EventOps
+
+    def record(ctx, stream, ev):
+        ev[0] = 1
+        return 0
+
+    ops = E(E.RECORD(record), E.QUERY(lambda ctx, ev: 1), E.DESTROY(lambda ctx, ev: None), None)
+    took = {}
+    for n in (2000, 20000):
+        a = _arena(n)
+        a.set_event_ops(ops)
+        ids = a.take(n)
+        start = time.perf_counter()
+        for i in range(n):
+            a.give(ids[i:i + 1], stream=1)
+        took[n] = time.perf_counter() - start
+        assert a.holders(ids).sum() == 0 and a.info()[1] == 0
+        a.close()
+    assert took[20000] < 40 * took[2000], took     # ten times as many gives; all moved at each, it was 70 times and more
