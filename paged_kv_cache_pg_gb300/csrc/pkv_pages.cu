@@ -5,8 +5,8 @@
 // The pages of a call are cut into pieces of kPiece 16-byte units; a CTA takes
 // one piece, each of its threads kUnits units a CTA's width apart, all loaded
 // before any is stored, so an SM holds its resident CTAs' pieces in flight.
-// Measured: 96 pages of 7.9 MB (1,513 MB read and written) 226 us, 6.68 TB/s,
-// 98 % of a plain copy's rate; four pages' first 77 positions (19 MB) 5.9 us,
+// Measured: 96 pages of 7.9 MB (1,513 MB read and written) 225 us, 6.72 TB/s,
+// 99 % of a plain copy's rate; four pages' first 77 positions (19 MB) 5.9 us,
 // half of it the launch.
 // A whole page is one run of bytes.  A page's first n positions are, for each
 // layer, the first n rows of each K, V and indexer part, and the first n/4

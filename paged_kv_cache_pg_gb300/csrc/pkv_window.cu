@@ -28,11 +28,11 @@
 // not depend on its batch.
 //
 // What bounds it: the bytes of K and V where there are many (64 streams of
-// 4,096 bf16 keys: 539 MB in 86.0 us, 6.26 TB/s); whole waves of CTAs, two on
+// 4,096 bf16 keys: 539 MB in 85.7 us, 6.28 TB/s); whole waves of CTAs, two on
 // an SM, and a tile's chain of latencies below that (32 streams of 4,096 e4m3
-// keys: 137 MB in 37.1 us, 256 CTAs of two pieces on the 304 places); and for a
-// few streams the launch, the first tile's way in and the merge (one stream of
-// 128 keys 6.6 us, four of 1,024 keys 7.6 us).  Two CTAs share an SM, so one
+// keys: 137 MB in 36.7 us, 256 CTAs of two pieces on the 304 places); and for a
+// few streams the host's call, the launch, the first tile's way in and the merge
+// (one stream of 128 keys 6.6 us, four of 1,024 keys 8.2 us).  Two CTAs share an SM, so one
 // streams while the other starts or merges.
 #include <algorithm>
 #include <cuda_fp16.h>

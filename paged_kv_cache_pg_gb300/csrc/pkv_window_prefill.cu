@@ -37,7 +37,7 @@
 // 160 KB, 2,500 cycles of the memory's width beside 2,600 of the products; a
 // tile takes 3,400 (1.75 us).  Beside that the end of an item costs about a tile and a half
 // (its masked tiles, its O out, the next item's masked start).  8,192 queries at
-// a window of 1,024 (129 GFLOP that some query sees): 135 us, 956 TFLOP/s; 512
+// a window of 1,024 (129 GFLOP that some query sees): 136 us, 950 TFLOP/s; 512
 // queries at 31,000 with a window of 4,096 (34 GFLOP in 64 items, split over the
 // SMs): 53 us, 6 of them the gather and 6 the combine.
 #include <algorithm>
