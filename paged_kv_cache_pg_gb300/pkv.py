@@ -213,6 +213,7 @@ def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sin
     if _types is None:
         torch = (_current or _torch_streams())[0]
         _types = frozenset((torch.bfloat16, torch.int16, torch.uint16)), torch.int32
+    _ints(what, layer | n_q_heads | window | n_sink)
     arr, n = _seqs(seqs)
     if arr._type_ is not Seq:
         raise PkvError(EINVAL, f"{what}: the streams are not pkv_seq structures")
@@ -261,6 +262,13 @@ def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sin
         rc = lib.pkv_window_decode(lay_at, seqs_at, n, layer, n_q_heads, window, n_sink, q, k, v, ik, out, ws, ws_bytes,
                                    status, _stream(stream))
     _check(rc, what)
+
+
+def _ints(what: str, bits: int):
+    """Refuses what is negative or not a 32-bit integer (`bits`: all of them, or-ed),
+    which ctypes would cut to its low 32 bits."""
+    if bits >> 31:
+        raise PkvError(EINVAL, f"{what}: an integer that is negative or beyond 32 bits")
 
 
 def _refuse(what: str, name: str):
@@ -377,6 +385,7 @@ class Arena:
         """Share a stream's pages with a new one: (its ids, copy), where copy
         is None or (src, dst, n_pos) of the last page, which is its own."""
         import numpy as np
+        _ints("pkv_pages_fork", length)
         n_ids, ids = _host_i32("pkv_pages_fork", ids)
         out = np.empty(max(1, n_ids), dtype=np.int32)
         s, d, n = ctypes.c_int32(), ctypes.c_int32(), ctypes.c_int32()
@@ -396,6 +405,7 @@ class Arena:
         """Plan up to max_moves moves of high pages to low holes: (src, dst).
         The caller copies the pages, rewrites the tables and gives src back."""
         import numpy as np
+        _ints("pkv_arena_compact", max_moves)
         src, dst = (np.zeros(max(1, max_moves), dtype=np.int32) for _ in range(2))
         n = ctypes.c_int32()
         _check(self._lib.pkv_arena_compact(self._h, max_moves, src.ctypes.data, dst.ctypes.data,
@@ -459,6 +469,7 @@ def pages_copy(lay, page_pos: int, memory, n_pages: int, src, dst, n_pos=None, s
     n_n_pos, n_pos = (n, None) if n_pos is None else _host_i32("pkv_pages_copy", n_pos)
     if n_dst != n or n_n_pos != n:
         raise PkvError(EINVAL, "pkv_pages_copy: lists of different lengths")
+    _ints("pkv_pages_copy", page_pos | n_pages)
     base, = _here("pkv_pages_copy", memory)
     if base is not memory and memory.nbytes < 2 * n_pages * page_elems(lay, page_pos):
         raise PkvError(EINVAL, "pkv_pages_copy: the memory holds fewer pages")
@@ -523,6 +534,7 @@ def prefill(lay, seqs, layer, n_q_heads, q, out, ws, status=None, stream=None):
 
 
 def window_decode_ws_size(lay, seqs, n_q_heads, window, n_sink) -> int:
+    _ints("pkv_window_decode_ws_size", n_q_heads | window | n_sink)
     arr, n = _seqs(seqs)
     out = ctypes.c_size_t()
     _check(load().pkv_window_decode_ws_size(ctypes.byref(lay), arr, n, n_q_heads, window, n_sink,
@@ -539,6 +551,7 @@ def window_decode(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws=None, 
 
 
 def window_prefill_ws_size(lay, seqs, n_q_heads, window, n_sink) -> int:
+    _ints("pkv_window_prefill_ws_size", n_q_heads | window | n_sink)
     arr, n = _seqs(seqs)
     out = ctypes.c_size_t()
     _check(load().pkv_window_prefill_ws_size(ctypes.byref(lay), arr, n, n_q_heads, window, n_sink,
@@ -555,6 +568,7 @@ def window_prefill(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws, stat
 
 def window_dead_pages(page_pos: int, length: int, window: int, n_sink: int):
     """Logical pages [first, end) that no query at position `length` or later reads."""
+    _ints("pkv_window_dead_pages", page_pos | length | window | n_sink)
     first, end = ctypes.c_int32(), ctypes.c_int32()
     _check(load().pkv_window_dead_pages(page_pos, length, window, n_sink, ctypes.byref(first),
                                         ctypes.byref(end)), "pkv_window_dead_pages")

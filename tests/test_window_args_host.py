@@ -93,3 +93,28 @@ def test_the_streams_have_to_be_streams(call):
     with pytest.raises(pkv.PkvError) as e:
         call(pkv.layout(1, HKV, 256, IDX), (ctypes.c_int32 * 24)(), 0, HQ, 100, 4, 0x100000, 0x100000, None, stream=0)
     assert e.value.code == pkv.EINVAL
+
+
+@pytest.mark.parametrize("big", [(1 << 32) + 5, 1 << 31, (1 << 40) + 1, -1])
+def test_integers_beyond_32_bits_are_refused(big):
+    lay = pkv.layout(1, HKV, 256, IDX)
+    seqs = [pkv.seq(pkv.Pg(0x100000, 0x200000, pkv.page_elems(lay, 16), 16, 64, 50, 0), 200, 1)]
+    arena = pkv.Arena(lay, 16, 0x200000, nbytes=2 * pkv.page_elems(lay, 16) * 4)
+    rows = (0x100000, 0x100000, None)
+    calls = [lambda: pkv.window_decode(lay, seqs, 0, HQ, big, 4, *rows, stream=0),
+             lambda: pkv.window_decode(lay, seqs, 0, HQ, 100, big, *rows, stream=0),
+             lambda: pkv.window_decode(lay, seqs, big, HQ, 100, 4, *rows, stream=0),
+             lambda: pkv.window_decode(lay, seqs, 0, big, 100, 4, *rows, stream=0),
+             lambda: pkv.window_prefill(lay, seqs, 0, HQ, big, 4, *rows, stream=0),
+             lambda: pkv.window_prefill(lay, seqs, 0, HQ, 100, big, *rows, stream=0),
+             lambda: pkv.window_decode_ws_size(lay, seqs, HQ, big, 4),
+             lambda: pkv.window_prefill_ws_size(lay, seqs, HQ, 100, big),
+             lambda: pkv.window_dead_pages(16, 200, big, 4), lambda: pkv.window_dead_pages(16, big, 100, 4),
+             lambda: pkv.pages_copy(lay, 16, 0x200000, big, [0], [1], stream=0),
+             lambda: pkv.pages_copy(lay, big, 0x200000, 4, [0], [1], stream=0),
+             lambda: arena.fork([], big), lambda: arena.compact(big)]
+    for i, call in enumerate(calls):
+        with pytest.raises(pkv.PkvError) as e:
+            call()
+        assert e.value.code == pkv.EINVAL, i
+    arena.close()
