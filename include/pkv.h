@@ -287,6 +287,77 @@ int pkv_store(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int
               const void *k_new, const void *v_new, const void *ik_new, int32_t *dev_status,
               cudaStream_t stream);
 
+/* ---- rotary positions (an addition: the pages' rows come rotated) -------------
+ * A rope turns the first rot_dim elements of a row in rot_dim/2 pairs: pair i
+ * holds elements (i, i + rot_dim/2) (PKV_ROPE_HALF) or (2i, 2i + 1)
+ * (PKV_ROPE_INTERLEAVED), and becomes
+ *     (a c - b s, b c + a s),  c = scale cos(p f_i),  s = scale sin(p f_i)
+ * for position p; the row's other elements stay.  float32 arithmetic, one
+ * rounding at the end.  An angle is p times the pair's frequency in turns as a
+ * 64-bit fixed-point fraction, whose wrap-around takes off the whole turns
+ * exactly: positions as far as int32 goes lose nothing.  Rotating by -p takes
+ * a rotation by p back (scale 1), and is its gradient. */
+#define PKV_ROPE_HALF 0
+#define PKV_ROPE_INTERLEAVED 1
+/* frequencies f_i = base^(-2i/rot_dim) of a longer context (factor >= 1) */
+#define PKV_ROPE_PLAIN 0  /* as they are                                             */
+#define PKV_ROPE_LINEAR 1 /* divided by factor                                       */
+#define PKV_ROPE_NTK 2    /* of a base stretched by factor^(rot_dim / (rot_dim - 2)) */
+#define PKV_ROPE_YARN 3   /* by parts: pairs that turn more than `fast` times over the
+                             original length as they are, fewer than `slow` times
+                             divided by factor, a ramp over the pair's index between
+                             (its ends rounded outwards); scale 0.1 ln(factor) + 1   */
+#define PKV_ROPE_BANDS 4  /* the same bounds, a ramp over the number of turns        */
+
+typedef struct pkv_rope {
+    int32_t rot_dim;     /* elements that turn: even, 2 .. 256             */
+    int32_t pairs;       /* PKV_ROPE_HALF or PKV_ROPE_INTERLEAVED          */
+    float scale;         /* factor of the cosines and sines                */
+    int32_t reserved;    /* set to 0                                       */
+    uint64_t turns[128]; /* f_i / 2 pi, as fractions of a turn times 2^64  */
+} pkv_rope;
+
+/* Fill a rope.  scaling: PKV_ROPE_PLAIN .. PKV_ROPE_BANDS; fast and slow: 0 for
+ * 32 and 1 (YARN), 4 and 1 (BANDS); scale: 0 for the default (1, or YARN's).
+ * EINVAL: a rot_dim that is odd or outside 2 .. 256 (NTK: below 4), a base not
+ * above 1, a factor below 1, an original length below 1 or fast <= slow where
+ * they count, anything not finite. */
+int pkv_rope_init(int32_t rot_dim, int32_t pairs, double base, int32_t scaling, double factor,
+                  int32_t original, double fast, double slow, double scale, pkv_rope *out);
+/* The same from frequencies of the caller's own: rot_dim / 2 of them, in radians
+ * a position. */
+int pkv_rope_from_freqs(int32_t rot_dim, int32_t pairs, const double *radians, double scale,
+                        pkv_rope *out);
+
+/* Rotate the rows of the streams' new tokens: x and out [tokens][n_heads][dim]
+ * bf16, dim 256 or 128, rot_dim <= dim.  Of seqs only len and n_new are read
+ * (page descriptors may be empty).  A token's position is its place in the
+ * cache, or pos[token] (device int32, any value) where pos is not NULL.
+ * x_stride, out_stride: elements from a token's rows to the next one's, 0 for
+ * packed rows (n_heads * dim); multiples of 8, at least that.  x and out
+ * 16-byte aligned; out may be x with the same stride, and must not overlap it
+ * otherwise. */
+int pkv_rope_rows(const pkv_rope *rope, const pkv_seq *seqs, int32_t n_seqs, const int32_t *pos,
+                  int32_t n_heads, int32_t dim, const void *x, int64_t x_stride, void *out,
+                  int64_t out_stride, cudaStream_t stream);
+
+/* pkv_store with the rotation on the way: the new tokens' keys are rotated and
+ * go into their pages, values and indexer keys go there as they are, and with
+ * q non-NULL the queries [tokens][n_q_heads][256] are rotated into q_out (which
+ * may be q, as in pkv_rope_rows).  bf16 pages hold the same bytes as
+ * pkv_rope_rows of the keys and pkv_store; e4m3 pages quantize the rotated keys
+ * from float32, by pkv_store's rule (one rounding, where rotating first would
+ * be two).  Strides of a token's rows in elements, 0 for packed rows, multiples
+ * of 8: rows may be parts of one projection's output.  pos as in pkv_rope_rows;
+ * rows go to the positions len - n_new .. len - 1 of the cache all the same.
+ * n_q_heads counts only with q.  As behind pkv_store, a decode may follow
+ * directly. */
+int pkv_rope_store(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
+                   const pkv_rope *rope, const int32_t *pos, int32_t n_q_heads, const void *q,
+                   int64_t q_stride, void *q_out, int64_t q_out_stride, const void *k_new,
+                   int64_t k_stride, const void *v_new, int64_t v_stride, const void *ik_new,
+                   int64_t ik_stride, int32_t *dev_status, cudaStream_t stream);
+
 /* ---- gather (prompt-cache save: #1169 "saves and restores copy page runs
  * in the contiguous layout") -----------------------------------------------
  * Copy rows of `kind` for positions 0 .. len-1 of every stream into `out`,

@@ -221,19 +221,14 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
-// e4m3 quantization of one 256-element bf16 row spread over a warp, eight
+// e4m3 quantization of one 256-element row spread over a warp, eight
 // elements a lane in row order (#1170, commit 5c09685: a row's e4m3 codes and
 // float32 scale; the scale rule is the plainest reading): scale = max|x| / 448,
 // code = the e4m3 value nearest x / scale (float32 division with IEEE
 // rounding, ties to even, saturating); an all-zero row has scale 0 and codes 0.
 // Returns the scale (the same on every lane); *codes gets the lane's 8 codes,
 // low byte first.
-__device__ __forceinline__ float quantize_row8(const uint4 u, uint2 *codes) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        x[e] = __uint_as_float((e & 1) ? (w[e / 2] & 0xffff0000u) : (w[e / 2] << 16));
+__device__ __forceinline__ float quantize_row8f(const float (&x)[8], uint2 *codes) {
     float amax = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
@@ -249,6 +244,15 @@ __device__ __forceinline__ float quantize_row8(const uint4 u, uint2 *codes) {
     }
     *codes = make_uint2(packed[0], packed[1]);
     return scale;
+}
+// The same of a bf16 row.
+__device__ __forceinline__ float quantize_row8(const uint4 u, uint2 *codes) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        x[e] = __uint_as_float((e & 1) ? (w[e / 2] & 0xffff0000u) : (w[e / 2] << 16));
+    return quantize_row8f(x, codes);
 }
 
 // Programmatic dependent launch: wait for the previous grid's results, and

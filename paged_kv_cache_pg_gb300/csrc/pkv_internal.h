@@ -234,6 +234,20 @@ int launch_decode8(const Common &c, const DecodePlan &plan, const DecodeMaps &ma
                    const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
                    const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 
+// Rotary positions (pkv_rope.cu).
+struct RopeRows {
+    const uint16_t *q;   // or null
+    uint16_t *q_out;
+    const uint16_t *k, *v, *ik;
+    const int32_t *pos;  // device positions of the tokens, or null: their places in the cache
+    int64_t q_stride, q_out_stride, k_stride, v_stride, ik_stride;  // elements from token to token
+};
+int launch_rope_store(const Common &c, int32_t total_tokens, const pkv_rope &rope, const RopeRows &r,
+                      cudaStream_t stream);
+// rows of 256 or 128 elements (r.q to r.q_out only), c.n_q_heads of them a token
+int launch_rope_rows(const Common &c, int32_t total_tokens, const pkv_rope &rope, const RopeRows &r, int32_t dim,
+                     cudaStream_t stream);
+
 // Windowed decode (pkv_window.cu): plan and launch.
 struct WindowPlan {
     int32_t items;      // (stream, KV head, split, column block)s

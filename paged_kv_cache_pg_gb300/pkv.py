@@ -21,6 +21,8 @@ KV_BF16, KV_E4M3 = 0, 1
 OK, EINVAL, EAGAIN, ECUDA, EDEVICE = 0, 1, 2, 3, 4
 DEV_BAD_PAGE, DEV_TIMEOUT, DEV_SMEM, DEV_RANGE = 1, 2, 4, 8
 MAX_SEQS = 64
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_NTK, ROPE_YARN, ROPE_BANDS = 0, 1, 2, 3, 4
 _NAMES = {EINVAL: "PKV_EINVAL", EAGAIN: "PKV_EAGAIN", ECUDA: "PKV_ECUDA", EDEVICE: "PKV_EDEVICE"}
 
 
@@ -47,6 +49,11 @@ class Seq(ctypes.Structure):
     _fields_ = [("pg", Pg), ("len", ctypes.c_int32), ("n_new", ctypes.c_int32)]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("pairs", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128)]
+
+
 class EventOps(ctypes.Structure):
     RECORD = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                               ctypes.POINTER(ctypes.c_void_p))
@@ -68,6 +75,7 @@ EXPORTS = [
     "pkv_sparse_decode", "pkv_prefill_ws_size", "pkv_prefill", "pkv_diag_wait_runs_out",
     "pkv_diag_cta_wait_runs_out", "pkv_window_decode_ws_size", "pkv_window_decode",
     "pkv_window_prefill_ws_size", "pkv_window_prefill", "pkv_window_dead_pages",
+    "pkv_rope_init", "pkv_rope_from_freqs", "pkv_rope_rows", "pkv_rope_store",
 ]
 
 
@@ -126,6 +134,13 @@ def load(path: Optional[str] = None):
         "pkv_diag_wait_runs_out": [vp, vp],
         "pkv_diag_cta_wait_runs_out": [vp, i32, vp],
     }
+    dbl, RP = ctypes.c_double, ctypes.POINTER(Rope)
+    sig.update({
+        "pkv_rope_init": [i32, i32, dbl, i32, dbl, i32, dbl, dbl, dbl, RP],
+        "pkv_rope_from_freqs": [i32, i32, vp, dbl, RP],
+        "pkv_rope_rows": [vp, vp, i32, vp, i32, i32, vp, i64, vp, i64, vp],
+        "pkv_rope_store": [vp, vp, i32, i32, vp, vp, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp],
+    })
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.restype = ctypes.c_int
@@ -203,17 +218,15 @@ _counts = {}  # streams of a launch: reader of their new tokens
 _types = None  # types of 16-bit rows; the status word's
 
 
-def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sink: int, q, out, ws, status, stream,
-            chunk: bool, k=None, v=None, ik=None):
-    """A windowed call.  Tensors have to be contiguous, on the current device, of
-    the rows' type and as long as the launch's packed rows; rows given as ints
-    (addresses) are taken as they are.  Written out for each tensor: a small
-    call takes the GPU no longer than its arguments take here."""
+def _row_types():
     global _types
-    if _types is None:
-        torch = (_current or _torch_streams())[0]
-        _types = frozenset((torch.bfloat16, torch.int16, torch.uint16)), torch.int32
-    _ints(what, layer | n_q_heads | window | n_sink)
+    torch = (_current or _torch_streams())[0]
+    _types = frozenset((torch.bfloat16, torch.int16, torch.uint16)), torch.int32
+    return _types
+
+
+def _new_tokens(what: str, seqs):
+    """A launch's streams as an array, their number and their new tokens."""
     arr, n = _seqs(seqs)
     if arr._type_ is not Seq:
         raise PkvError(EINVAL, f"{what}: the streams are not pkv_seq structures")
@@ -221,8 +234,35 @@ def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sin
     if read is None:
         at = Seq.n_new.offset
         read = _counts[n] = struct.Struct("=" + f"{at}xi{ctypes.sizeof(Seq) - at - 4}x" * n).unpack_from
-    new = read(arr)[0] if n == 1 else sum(read(arr)) if n else 0
-    types, word = _types
+    return arr, n, read(arr)[0] if n == 1 else sum(read(arr)) if n else 0
+
+
+def _token_rows(what: str, name: str, t, dev: int, tokens: int, width: int):
+    """(address, elements from a token to the next) of 16-bit rows [tokens][...]
+    of `width` elements a token.  A token's rows have to lie together; the
+    tokens may lie apart, as in a slice of a wider tensor.  An address given as
+    an int is one of packed rows."""
+    if t is None or type(t) is int:
+        return t, 0
+    types = (_types or _row_types())[0]
+    if t.get_device() == dev and t.dtype in types:
+        if t.is_contiguous():
+            if t.numel() >= tokens * width:
+                return t.data_ptr(), 0
+        elif t.dim() >= 2 and t.shape[0] >= tokens and t[0].is_contiguous() and t[0].numel() == width:
+            return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+    raise PkvError(EINVAL, f"{what}: {name} is not a tensor of 16-bit rows, long enough, a token's rows together, on the current device")
+
+
+def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sink: int, q, out, ws, status, stream,
+            chunk: bool, k=None, v=None, ik=None):
+    """A windowed call.  Tensors have to be contiguous, on the current device, of
+    the rows' type and as long as the launch's packed rows; rows given as ints
+    (addresses) are taken as they are.  Written out for each tensor: a small
+    call takes the GPU no longer than its arguments take here."""
+    _ints(what, layer | n_q_heads | window | n_sink)
+    arr, n, new = _new_tokens(what, seqs)
+    types, word = _types or _row_types()
     dev, ws_bytes, rows = (_current or _torch_streams())[1](), 0, 512 * n_q_heads * new
     if type(q) is not int and q is not None:
         if q.get_device() != dev or q.dtype not in types or q.nbytes < rows or not q.is_contiguous():
@@ -454,6 +494,79 @@ def store(lay, seqs, layer, k_new, v_new, ik_new=None, status=None, stream=None)
     arr, n = _seqs(seqs)
     _check(load().pkv_store(ctypes.byref(lay), arr, n, layer, _ptr(k_new), _ptr(v_new),
                             _ptr(ik_new), _ptr(status), _stream(stream)), "pkv_store")
+
+
+def rope(rot_dim: int, base: float = 10000.0, pairs: int = ROPE_HALF, scaling: int = ROPE_PLAIN, factor: float = 1.0,
+         original: int = 0, fast: float = 0.0, slow: float = 0.0, scale: float = 0.0) -> Rope:
+    """Rotary positions over a row's first rot_dim elements; host memory only.
+    scaling: ROPE_LINEAR, ROPE_NTK, ROPE_YARN or ROPE_BANDS stretch the
+    frequencies by `factor` (the last two by how often a pair turns over
+    `original` positions, `fast` and `slow`; 0: 32 and 1, or 4 and 1); scale: of
+    the cosines and sines (0: 1, or ROPE_YARN's 0.1 ln(factor) + 1)."""
+    _ints("pkv_rope_init", rot_dim | pairs | scaling | original)
+    out = Rope()
+    _check(load().pkv_rope_init(rot_dim, pairs, base, scaling, factor, original, fast, slow, scale, ctypes.byref(out)),
+           "pkv_rope_init")
+    return out
+
+
+def rope_from_freqs(radians, pairs: int = ROPE_HALF, scale: float = 1.0) -> Rope:
+    """The same from frequencies of the caller's own, in radians a position."""
+    freqs = array.array("d", radians)
+    out = Rope()
+    _ints("pkv_rope_from_freqs", pairs)
+    _check(load().pkv_rope_from_freqs(2 * len(freqs), pairs, freqs.buffer_info()[0], scale, ctypes.byref(out)),
+           "pkv_rope_from_freqs")
+    return out
+
+
+def _places(what: str, pos, dev: int, tokens: int):
+    if pos is None or type(pos) is int:
+        return pos
+    if pos.get_device() != dev or pos.dtype is not (_types or _row_types())[1] or pos.numel() < tokens or not pos.is_contiguous():
+        _refuse(what, "pos")
+    return pos.data_ptr()
+
+
+def rope_rows(rope_: Rope, seqs, n_heads: int, x, out, pos=None, stream=None):
+    """Rotate rows [tokens, n_heads, dim] (dim 256 or 128, x's last) of the
+    streams' new tokens by their places in the cache, or by pos (int32 on the
+    device).  out may be x; the tokens of either may lie apart."""
+    what = "pkv_rope_rows"
+    arr, n, tokens = _new_tokens(what, seqs)
+    _ints(what, n_heads)
+    if type(rope_) is not Rope or x is None or type(x) is int:
+        raise PkvError(EINVAL, f"{what}: a rope, and rows as a tensor")
+    dev, dim = (_current or _torch_streams())[1](), x.shape[-1]
+    src, src_stride = _token_rows(what, "x", x, dev, tokens, n_heads * dim)
+    dst, dst_stride = _token_rows(what, "out", out, dev, tokens, n_heads * dim)
+    _check(load().pkv_rope_rows(ctypes.addressof(rope_), ctypes.addressof(arr), n, _places(what, pos, dev, tokens), n_heads,
+                                dim, src, src_stride, dst, dst_stride, _stream(stream)), what)
+
+
+def rope_store(lay, seqs, layer, rope_: Rope, k_new, v_new, ik_new=None, n_q_heads: int = 0, q=None, q_out=None, pos=None,
+               status=None, stream=None):
+    """Rotate the new tokens' keys into their pages, store values and indexer
+    keys, and with q rotate the queries [tokens, n_q_heads, 256] into q_out."""
+    what = "pkv_rope_store"
+    arr, n, tokens = _new_tokens(what, seqs)
+    _ints(what, layer | n_q_heads)
+    if type(rope_) is not Rope:
+        raise PkvError(EINVAL, f"{what}: not a rope")
+    dev = (_current or _torch_streams())[1]()
+    kv = 256 * lay.n_kv_heads
+    k, ks = _token_rows(what, "k_new", k_new, dev, tokens, kv)
+    v, vs = _token_rows(what, "v_new", v_new, dev, tokens, kv)
+    ik, iks = _token_rows(what, "ik_new", ik_new, dev, tokens, lay.idx_dim)
+    qa, qs = _token_rows(what, "q", q, dev, tokens, 256 * n_q_heads)
+    qo, qos = _token_rows(what, "q_out", q_out, dev, tokens, 256 * n_q_heads)
+    if status is not None and type(status) is not int:
+        if status.get_device() != dev or status.dtype is not (_types or _row_types())[1] or status.nbytes < 4:
+            _refuse(what, "the status")
+        status = status.data_ptr()
+    _check(load().pkv_rope_store(ctypes.addressof(lay), ctypes.addressof(arr), n, layer, ctypes.addressof(rope_),
+                                 _places(what, pos, dev, tokens), n_q_heads, qa, qs, qo, qos, k, ks, v, vs, ik, iks, status,
+                                 _stream(stream)), what)
 
 
 def gather(lay, seqs, layer, kind, out, status=None, stream=None):
