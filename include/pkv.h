@@ -505,6 +505,51 @@ int pkv_window_prefill(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_
 int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t n_sink,
                           int32_t *first, int32_t *end);
 
+/* ---- decode over shared pages (an addition: forks of a prompt) ------------------
+ * pkv_decode for streams that share their first pages, as pkv_pages_fork leaves
+ * them: the shared rows are read once for all the streams of a group.  The
+ * call's streams are cut, in their order, into n_groups groups of n_seqs (>= 1)
+ * streams each; the first n_pages (>= 0) logical pages of a group's streams are
+ * the same pages (of one base, page size and arena), and every stream's new
+ * tokens come behind them (len - n_new >= n_pages * page_pos).  The tables
+ * of all of them hold the shared pages' ids (which one's is read is not said).
+ * With n_pages 0, or one stream, nothing is shared.  The result is pkv_decode's,
+ * within the attention tolerance.  Both formats; n_new * (n_q_heads/H) <= 32 per
+ * stream; q, out, k_new, v_new, ik_new and the fused store as for
+ * pkv_window_decode, and so is the ordering: the shared rows too may be read
+ * before the kernel before has finished, where they lie more than 32 positions
+ * below the new tokens.
+ * Arithmetic of the shared part: tcgen05 products with float32 accumulation; Q
+ * and K in bf16 (e4m3: fp16, exact, the query behind a power of two), P and V in
+ * fp16.  So a weight has 11 significant bits; a bf16 V entry is exact for
+ * magnitudes 2^-14 to 65,280, rounded to fp16's 2^-24 grid below that, and one
+ * beyond 65,504 makes the output non-finite and sets PKV_DEV_RANGE, as does a
+ * largest score (q.k / 16) beyond 4.6e7.  e4m3 V rows of any scale from 2^-40 to
+ * 2^80 keep their precision.  A stream's own part is pkv_window_decode's.
+ * Results follow the call's shape (its groups, lengths and new tokens), not where
+ * its pages lie.
+ * ws: device, >= pkv_prefix_decode_ws_size bytes, 256-byte aligned, no
+ * initialization, one ws per in-flight call.  The size for the longest own parts
+ * (len - n_pages * page_pos) and the most new tokens covers shorter ones and
+ * fewer, whatever the shared lengths.
+ * EINVAL: groups that do not cover the streams exactly, a negative count, shared
+ * pages without a table, of streams with another base, page size or arena, past a
+ * table's end or past the cached rows, a stream of more than 2^29 positions, and
+ * as for pkv_decode. */
+typedef struct pkv_group {
+    int32_t n_seqs;  /* streams of the group                       */
+    int32_t n_pages; /* their first pages that are the same, or 0 */
+} pkv_group;
+
+int pkv_prefix_decode_ws_size(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs,
+                              const pkv_group *groups, int32_t n_groups, int32_t n_q_heads,
+                              size_t *bytes);
+int pkv_prefix_decode(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs,
+                      const pkv_group *groups, int32_t n_groups, int32_t layer, int32_t n_q_heads,
+                      const void *q, const void *k_new, const void *v_new, const void *ik_new,
+                      void *out, void *ws, size_t ws_bytes, int32_t *dev_status,
+                      cudaStream_t stream);
+
 /* ---- chunked prefill on the tensor cores (#1170, maintainer notes on the
  * Qwen slice: contiguous tensor-core attention for flat batches, a page-run
  * path for paged or mixed batches; #1169 maintainer reply: the grouped prompt

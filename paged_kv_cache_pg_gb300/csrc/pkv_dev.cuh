@@ -255,6 +255,30 @@ __device__ __forceinline__ float quantize_row8(const uint4 u, uint2 *codes) {
     return quantize_row8f(x, codes);
 }
 
+// Four e4m3 codes (low byte first) to two f16 pairs, exactly.
+__device__ __forceinline__ void f16_of_codes(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+}
+
+// ---- cluster helpers ----------------------------------------------------------
+// All threads of the cluster meet.  A warp whose lanes took different paths
+// (the producer's) may still be split behind a CTA barrier, and a warp that
+// arrives in two parts would count twice: the warp is joined first, and the
+// forms without .aligned do not need it to be.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+    return r;
+}
+
 // Programmatic dependent launch: wait for the previous grid's results, and
 // let the next grid start its prologue early.
 __device__ __forceinline__ void pdl_wait() {

@@ -1,5 +1,6 @@
 // Fifth-generation tensor core (tcgen05) wrappers and tensor-memory access for
-// M = 128 products (one CTA), shared by the chunk kernels.
+// M = 128 products (one CTA), shared by the chunk kernels, and for
+// M = 256 products of a pair of CTAs.
 #pragma once
 
 #include "pkv_dev.cuh"
@@ -56,6 +57,37 @@ __device__ __forceinline__ void tc_commit(uint64_t *bar) {
                  : "memory");
 }
 
+// ---- pairs: M = 256, cta_group::2 --------------------------------------------
+// The first CTA of a pair issues; rows 0-127 and the first half of N are its
+// own (A from its TMEM or shared memory, B's half, D in its TMEM), the others
+// its peer's, at the same offsets.
+__host__ __device__ constexpr uint32_t mma_idesc_pair(int n, bool b_mn_major, bool f16) {
+    return (mma_idesc(n, b_mn_major, f16) & ~(0x1Fu << 24)) | ((uint32_t)(2 * kM >> 4) << 24);
+}
+__device__ __forceinline__ void tc_mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tc_mma_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                               uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Arrive at this barrier of both CTAs once the products issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
 __device__ __forceinline__ void tc_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
@@ -101,6 +133,61 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
         "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
         "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+
+// Two float32 operations an instruction, each rounded as alone: the softmax and
+// edge warps' issue slots count (a prompt of 8,192 took 141.0 us with single
+// ones, 135.9 with these).
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
+}
+
+// Transpose over each four lanes: word j of lane i goes to word i of lane j.
+// Rows that lie one a lane are so read and written 64 bytes of a row at a time
+// by four lanes (16 bytes of 32 rows an instruction, as the lanes hold them,
+// kept the load and store units of an item's Q and O busy for 8,000 cycles).
+__device__ __forceinline__ uint4 shfl_xor16(const uint4 &v, int m) {
+    return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                      __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
+}
+__device__ __forceinline__ uint4 pick(bool b, const uint4 &x, const uint4 &y) {
+    return make_uint4(b ? x.x : y.x, b ? x.y : y.y, b ? x.z : y.z, b ? x.w : y.w);
+}
+__device__ __forceinline__ void quad_transpose(uint4 *v, int lane) {
+    const bool b0 = lane & 1, b1 = lane & 2;
+#pragma unroll
+    for (int p = 0; p < 4; p += 2) {
+        const uint4 got = shfl_xor16(pick(b0, v[p], v[p + 1]), 1);
+        v[p] = pick(b0, got, v[p]);
+        v[p + 1] = pick(b0, v[p + 1], got);
+    }
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const uint4 got = shfl_xor16(pick(b1, v[p], v[p + 2]), 2);
+        v[p] = pick(b1, got, v[p]);
+        v[p + 2] = pick(b1, v[p + 2], got);
+    }
 }
 
 }  // namespace pkv

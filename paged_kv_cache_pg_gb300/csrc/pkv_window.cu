@@ -134,20 +134,6 @@ static_assert(Cfg<false>::bars % kMaxSlices == 0 && Cfg<true>::bars % kMaxSlices
               "1, 2 or 4 slices, each with barriers of its own");
 
 // ---- cluster helpers ----------------------------------------------------------
-// All threads of the cluster meet.  A warp whose lanes took different paths
-// (the producer's) may still be split behind a CTA barrier, and a warp that
-// arrives in two parts would count twice: the warp is joined first, and the
-// forms without .aligned do not need it to be.
-__device__ __forceinline__ void cluster_sync() {
-    __syncwarp();
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t peer_addr(const void *p, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
 __device__ __forceinline__ float4 peer_ld4(uint32_t a) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
@@ -190,13 +176,6 @@ __device__ __forceinline__ uint32_t swz8(int r, int c) {
     return line * 128 + ((((c & 7) ^ (line & 7))) << 4);
 }
 
-// Four e4m3 codes (low byte first) to two f16 pairs, exactly.
-__device__ __forceinline__ void f16_of_codes(uint32_t four, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(four));
-}
 // D (16x8 f32) += A (16x16 f16, row) B (16x8 f16, col).  Not volatile: it only
 // reads its registers, and the compiler may place it among the conversions.
 __device__ __forceinline__ void mma_half(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -1220,7 +1199,7 @@ static int64_t most_keys(int32_t len, int32_t n_new, int32_t window, int32_t n_s
 // tokens of 8 heads, windows of 2,047 keys, 16 columns a CTA against 32: 8
 // streams 15.4 us against 21.7, 16 streams (512 CTAs against 256) 30.9 against
 // 25.0, 64 streams (which read twice the bytes from L2) 118 against 100.5.
-int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
+int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan, bool partials) {
     const int pieces = window_pieces(window, n_sink);
     const int tile = c.kv_fp8 ? Cfg<true>::tile : Cfg<false>::tile;
     bool split = false, wide = false, over8 = false;
@@ -1257,11 +1236,12 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
         floats = (floats + 63) / 64 * 64;
     }
     if (items * pieces > INT32_MAX) return PKV_EINVAL;
-    const bool some = pieces > 1 && (split || many);  // calls that may run as runs of pieces
+    // calls that may run as runs of pieces (and those have to whose partials the caller merges)
+    const bool some = partials || (pieces > 1 && (split || many));
     // the least cost: a cluster a split, or runs of pieces (which have to merge splits)
     const int64_t per = items ? keys / (items * pieces) : 0;  // keys of a piece
     const auto waves = [&](int run) { return (items * pieces / run + kCtas - 1) / kCtas; };
-    int64_t best = split ? INT64_MAX : waves(1) * (per + kStartKeys) * 10;
+    int64_t best = split || partials ? INT64_MAX : waves(1) * (per + kStartKeys) * 10;
     plan->run = 0;
     for (int run = 1; some && run <= pieces; run *= 2) {
         const int64_t cost = waves(run) * (run * per * (wide || (c.kv_fp8 && over8) ? 12 : 9) + kStartKeys * 10) + kCombKeys * 10;
@@ -1286,7 +1266,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
 
 int launch_window(const Common &c, const WindowPlan &plan, const DecodeMaps &maps, int32_t window,
                   int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
-                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream) {
+                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool partials) {
     static std::atomic<uint64_t> attr_done{0};
     if (once_per_device(attr_done, [] {
             for (int i = 0; i < 8; ++i) {
@@ -1328,7 +1308,7 @@ int launch_window(const Common &c, const WindowPlan &plan, const DecodeMaps &map
     auto *const fn = window_kernel(c.kv_fp8 != 0, !clustered, plan.wide);
     if (cudaLaunchKernelEx(&cfg, fn, c, maps, a) != cudaSuccess)
         return PKV_ECUDA;
-    if (clustered) return PKV_OK;
+    if (clustered || partials) return PKV_OK;
     return launch_status(
         launch_pdl(window_combine, static_cast<unsigned>(plan.comb), kCombThreads, 0, stream, c, a));
 }

@@ -189,61 +189,6 @@ __device__ __forceinline__ uint64_t below(int n) {
     return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1;
 }
 
-// Two float32 operations an instruction, each rounded as alone: the softmax and
-// edge warps' issue slots count (a prompt of 8,192 took 141.0 us with single
-// ones, 135.9 with these).
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-        "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
-    return d;
-}
-__device__ __forceinline__ float2 add2(float2 x, float2 y) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
-    float2 d;
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-        "mul.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-    return d;
-}
-
-// Transpose over each four lanes: word j of lane i goes to word i of lane j.
-// Rows that lie one a lane are so read and written 64 bytes of a row at a time
-// by four lanes (16 bytes of 32 rows an instruction, as the lanes hold them,
-// kept the load and store units of an item's Q and O busy for 8,000 cycles).
-__device__ __forceinline__ uint4 shfl_xor16(const uint4 &v, int m) {
-    return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
-                      __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
-}
-__device__ __forceinline__ uint4 pick(bool b, const uint4 &x, const uint4 &y) {
-    return make_uint4(b ? x.x : y.x, b ? x.y : y.y, b ? x.z : y.z, b ? x.w : y.w);
-}
-__device__ __forceinline__ void quad_transpose(uint4 *v, int lane) {
-    const bool b0 = lane & 1, b1 = lane & 2;
-#pragma unroll
-    for (int p = 0; p < 4; p += 2) {
-        const uint4 got = shfl_xor16(pick(b0, v[p], v[p + 1]), 1);
-        v[p] = pick(b0, got, v[p]);
-        v[p + 1] = pick(b0, v[p + 1], got);
-    }
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const uint4 got = shfl_xor16(pick(b1, v[p], v[p + 2]), 2);
-        v[p] = pick(b1, got, v[p]);
-        v[p + 2] = pick(b1, v[p + 2], got);
-    }
-}
-
 __global__ void __launch_bounds__(kThreads, 1)
     window_chunk(const __grid_constant__ Common c, const __grid_constant__ DecodeMaps maps,
                  const __grid_constant__ ChunkArgs a) {

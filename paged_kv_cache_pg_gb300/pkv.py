@@ -54,6 +54,10 @@ class Rope(ctypes.Structure):
                 ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128)]
 
 
+class Group(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_pages", ctypes.c_int32)]
+
+
 class EventOps(ctypes.Structure):
     RECORD = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p,
                               ctypes.POINTER(ctypes.c_void_p))
@@ -76,6 +80,7 @@ EXPORTS = [
     "pkv_diag_cta_wait_runs_out", "pkv_window_decode_ws_size", "pkv_window_decode",
     "pkv_window_prefill_ws_size", "pkv_window_prefill", "pkv_window_dead_pages",
     "pkv_rope_init", "pkv_rope_from_freqs", "pkv_rope_rows", "pkv_rope_store",
+    "pkv_prefix_decode_ws_size", "pkv_prefix_decode",
 ]
 
 
@@ -140,6 +145,10 @@ def load(path: Optional[str] = None):
         "pkv_rope_from_freqs": [i32, i32, vp, dbl, RP],
         "pkv_rope_rows": [vp, vp, i32, vp, i32, i32, vp, i64, vp, i64, vp],
         "pkv_rope_store": [vp, vp, i32, i32, vp, vp, i32, vp, i64, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp],
+    })
+    sig.update({
+        "pkv_prefix_decode_ws_size": [LP, SP, i32, vp, i32, i32, ctypes.POINTER(sz)],
+        "pkv_prefix_decode": [vp, vp, i32, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, vp, vp],
     })
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -255,8 +264,8 @@ def _token_rows(what: str, name: str, t, dev: int, tokens: int, width: int):
 
 
 def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sink: int, q, out, ws, status, stream,
-            chunk: bool, k=None, v=None, ik=None):
-    """A windowed call.  Tensors have to be contiguous, on the current device, of
+            chunk: bool, k=None, v=None, ik=None, shared=None):
+    """A windowed call, or with `shared` groups one over shared pages.  Tensors have to be contiguous, on the current device, of
     the rows' type and as long as the launch's packed rows; rows given as ints
     (addresses) are taken as they are.  Written out for each tensor: a small
     call takes the GPU no longer than its arguments take here."""
@@ -295,7 +304,10 @@ def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sin
             _refuse(what, "the status")
         status = status.data_ptr()
     lib, lay_at, seqs_at = load(), ctypes.addressof(lay), ctypes.addressof(arr)
-    if chunk:
+    if shared is not None:
+        rc = lib.pkv_prefix_decode(lay_at, seqs_at, n, ctypes.addressof(shared), len(shared), layer, n_q_heads, q, k, v, ik,
+                                   out, ws, ws_bytes, status, _stream(stream))
+    elif chunk:
         rc = lib.pkv_window_prefill(lay_at, seqs_at, n, layer, n_q_heads, window, n_sink, q, out, ws, ws_bytes, status,
                                     _stream(stream))
     else:
@@ -661,6 +673,42 @@ def window_decode(lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws=None, 
     n_sink; with k_new/v_new (and ik_new) the new rows are stored too."""
     _window("pkv_window_decode", lay, seqs, layer, n_q_heads, window, n_sink, q, out, ws, status, stream, False,
             k_new, v_new, ik_new)
+
+
+def groups(counts):
+    """(streams, shared pages) of each group of a launch's streams, in their
+    order, as one ctypes array that programs keep between calls."""
+    counts = [(int(n), int(p)) for n, p in counts]
+    for n, p in counts:
+        _ints("pkv_group", n | p)
+    return (Group * len(counts))(*counts)
+
+
+def _groups(what: str, g):
+    if isinstance(g, ctypes.Array):
+        if g._type_ is not Group:
+            raise PkvError(EINVAL, f"{what}: the groups are not pkv_group structures")
+        return g
+    return groups(g)
+
+
+def prefix_decode_ws_size(lay, seqs, groups_, n_q_heads) -> int:
+    _ints("pkv_prefix_decode_ws_size", n_q_heads)
+    g = _groups("pkv_prefix_decode_ws_size", groups_)
+    arr, n = _seqs(seqs)
+    out = ctypes.c_size_t()
+    _check(load().pkv_prefix_decode_ws_size(ctypes.byref(lay), arr, n, ctypes.addressof(g), len(g), n_q_heads,
+                                            ctypes.byref(out)), "pkv_prefix_decode_ws_size")
+    return out.value
+
+
+def prefix_decode(lay, seqs, groups_, layer, n_q_heads, q, out, ws, status=None, stream=None, k_new=None, v_new=None,
+                  ik_new=None):
+    """Decode attention for groups of streams (pairs of streams and shared pages,
+    or what groups() made of them) whose first pages are the same, which are read
+    once a group; with k_new/v_new (and ik_new) the new rows are stored too."""
+    _window("pkv_prefix_decode", lay, seqs, layer, n_q_heads, 0, 0, q, out, ws, status, stream, False, k_new, v_new, ik_new,
+            _groups("pkv_prefix_decode", groups_))
 
 
 def window_prefill_ws_size(lay, seqs, n_q_heads, window, n_sink) -> int:
