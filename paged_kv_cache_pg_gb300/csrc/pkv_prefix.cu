@@ -83,7 +83,7 @@ __device__ __forceinline__ uint32_t cta_rank() {
     return r;
 }
 __device__ __forceinline__ void arrive_first(uint64_t *bar) {  // at the first CTA's barrier
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, 0)) : "memory");
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, 0)) : "memory");
 }
 // mbar_wait for what the other CTA arrived at, too.
 __device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, uint32_t *status) {
