@@ -619,82 +619,83 @@ extern "C" int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t wind
 
 // ---- decode over shared pages ------------------------------------------------
 
-// A call's streams without their shared pages (in c), and the shared parts.
-struct PrefixCall {
-    Common c;
-    WindowPlan own;
-    PrefixPlan shared;
-    int32_t window;      // every stream's own positions
-    size_t own_floats;   // of the workspace; the shared parts' partials behind it
-    size_t ws_bytes;
-};
-
-// With `size`, groups that share nothing now are planned too, as the workspace's
-// size covers every shared length.
+// Checks of a call over shared pages, and its streams and groups: those that share
+// pages (plan->n_groups counts them and, behind them, every other stream with
+// queries alone).  *shares: whether any do; *may: whether any could.
 static int prefix_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs, const pkv_group *groups,
-                         int32_t n_groups, int32_t layer, int32_t n_q_heads, int32_t *dev_status, bool size, PrefixCall *p) {
-    Common &c = p->c;
-    int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, &c);
+                         int32_t n_groups, int32_t layer, int32_t n_q_heads, int32_t *dev_status, Common *c, PrefixPlan *plan,
+                         bool *shares, bool *may) {
+    int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, c);
     if (rc) return rc;
     if (n_groups < 0 || n_groups > n_seqs || (n_groups > 0 && !groups)) return PKV_EINVAL;
-    std::memset(&p->shared, 0, sizeof(p->shared));
-    std::memset(p->shared.of, -1, sizeof(p->shared.of));
+    std::memset(plan, 0, sizeof(*plan));
+    plan->n_seqs = n_seqs;
+    *shares = *may = false;
+    const auto add = [&](int32_t s0, int32_t n, int32_t shared) -> bool {
+        PrefixGroup &g = plan->group[plan->n_groups++];
+        const SeqDev &d = c->seq[s0];
+        g.layer_base = d.layer_base;
+        g.ps = d.ps;
+        g.ptok = d.ptok;
+        g.n_pages = d.n_pages;
+        g.shared = shared;
+        g.early = INT32_MAX;
+        g.s0 = s0;
+        g.n_seqs = n;
+        g.tok0 = d.tok_off;
+        int64_t own = 0;
+        for (int32_t s = s0; s < s0 + n; ++s) {
+            const SeqDev &e = c->seq[s];
+            plan->seq[s] = {e.table, e.len, e.n_new, e.tok_off, static_cast<int32_t>(own)};
+            if (e.n_new == 0) continue;
+            g.rows += e.n_new * c->group;
+            // a kernel just before may be writing rows at most 32 below the new tokens
+            g.early = std::min(g.early, e.len - e.n_new - 32);
+            own += (e.len - shared + 15) / 16 * 16;
+            if (own + shared > 1 << 30) return false;  // virtual keys are 32-bit
+        }
+        return true;
+    };
     int32_t s0 = 0;
     for (int32_t k = 0; k < n_groups; ++k) {
         const pkv_group &gr = groups[k];
         if (gr.n_seqs < 1 || gr.n_seqs > n_seqs - s0 || gr.n_pages < 0) return PKV_EINVAL;
-        int32_t live = 0, rows = 0;
+        int32_t live = 0;
         const pkv_pg &first = seqs[s0].pg;
         for (int32_t s = s0; s < s0 + gr.n_seqs; ++s) {
             const pkv_seq &q = seqs[s];
-            if (q.len > 1 << 29 || (int64_t)q.n_new * c.group > 32) return PKV_EINVAL;
+            if (q.len > 1 << 29 || (int64_t)q.n_new * c->group > 32) return PKV_EINVAL;
             live += q.n_new > 0;
-            rows += q.n_new * c.group;
             if (gr.n_pages == 0) continue;
             if (!q.pg.table || q.pg.base != first.base || q.pg.page_pos != first.page_pos ||
                 q.pg.n_pages != first.n_pages || gr.n_pages > q.pg.n_table ||
                 (int64_t)gr.n_pages * q.pg.page_pos > q.len - q.n_new)
                 return PKV_EINVAL;
         }
-        if (live > 1 && (gr.n_pages > 0 || size)) {
-            const SeqDev &d = c.seq[s0];
-            PrefixGroup &g = p->shared.group[p->shared.n_groups];
-            g.layer_base = d.layer_base;
-            g.table = d.table;
-            g.ps = d.ps;
-            g.ptok = d.ptok;
-            g.n_pages = d.n_pages;
-            g.len = gr.n_pages * d.ptok;
-            g.tok0 = d.tok_off;
-            g.rows = rows;
-            for (int32_t s = s0; s < s0 + gr.n_seqs; ++s) {
-                SeqDev &e = c.seq[s];
-                p->shared.of[s] = static_cast<int8_t>(p->shared.n_groups);
-                e.table += gr.n_pages;  // its own positions, from the first page behind the shared ones
-                e.n_table -= gr.n_pages;
-                e.len -= g.len;
-            }
-            ++p->shared.n_groups;
+        *may |= live > 1;
+        if (gr.n_pages > 0 && live > 1) {
+            *shares = true;
+            if (!add(s0, gr.n_seqs, gr.n_pages * first.page_pos)) return PKV_EINVAL;
+        } else {
+            for (int32_t s = s0; s < s0 + gr.n_seqs; ++s)
+                if (seqs[s].n_new > 0 && !add(s, 1, 0)) return PKV_EINVAL;
         }
         s0 += gr.n_seqs;
     }
-    if (s0 != n_seqs) return PKV_EINVAL;
-    p->window = 1;
-    for (int32_t s = 0; s < n_seqs; ++s) p->window = std::max(p->window, c.seq[s].len);
-    rc = plan_window(c, p->window, 0, &p->own, p->shared.n_groups > 0);
-    if (rc) return rc;
-    int nsm = 0;
-    rc = sm_count(&nsm);
-    if (rc) return rc;
-    plan_prefix(c, nsm, &p->shared);
-    p->own_floats = p->own.ws_bytes / 4;
-    p->ws_bytes = p->own.ws_bytes + static_cast<size_t>(p->shared.floats) * 4;
-    return PKV_OK;
+    return s0 == n_seqs ? PKV_OK : PKV_EINVAL;
 }
 
-// Tensor maps of a group's pages: whole slots of the shared part's kernel where a
-// page holds every run of 128 positions from a multiple of 128, 16-row runs where
-// it holds those.
+// The windowed decode's plan of streams that share nothing, over all their
+// positions (or those from `from` on).
+static int plan_alone(Common &c, WindowPlan *plan, int32_t *window) {
+    *window = 1;
+    for (int32_t s = 0; s < c.n_seqs; ++s) *window = std::max(*window, c.seq[s].len);
+    return plan_window(c, *window, 0, plan);
+}
+
+// Tensor maps of the groups' pages: 16-row runs where pages hold whole ones, and
+// boxes of the kernel's slots (64 K rows, 128 V rows) for rows that follow one
+// another.
 static void plan_prefix_maps(const Common &c, const pkv_layout *L, const pkv_seq *seqs, PrefixPlan &plan, DecodeMaps &maps) {
     int n_maps = 0;
     const bool fp8 = c.kv_fp8;
@@ -702,15 +703,13 @@ static void plan_prefix_maps(const Common &c, const pkv_layout *L, const pkv_seq
     for (int k = 0; k < plan.n_groups; ++k) {
         PrefixGroup &g = plan.group[k];
         g.map_k = g.map_v = g.map_run = -1;
-        int s = 0;
-        while (plan.of[s] != k) ++s;
-        const pkv_pg &pg = seqs[s].pg;
+        const pkv_pg &pg = seqs[g.s0].pg;
         const int64_t layer_off = (int64_t)c.layer * layer_elems_f(fp8, L->n_kv_heads, L->idx_dim, pg.page_pos);
         if (pg.page_pos % 16 != 0 || pg.page_elems % row != 0 || layer_off % row != 0) continue;
-        const uint64_t rows = (uint64_t)pg.n_pages * pg.page_elems / row;
+        const uint64_t rows = (uint64_t)(pg.table ? pg.n_pages : 1) * pg.page_elems / row;
         g.layer_row = layer_off / row;
         g.map_run = static_cast<int16_t>(row_map(maps, n_maps, pg.base, rows, fp8));
-        if (g.map_run < 0 || pg.page_pos % 128 != 0) continue;
+        if (g.map_run < 0 || pg.page_pos < 64) continue;  // (never 64 rows on end)
         g.map_k = static_cast<int16_t>(fp8 ? row_map(maps, n_maps, pg.base, rows, true, false, 64)
                                            : row_map(maps, n_maps, pg.base, rows, false, true, 64, 4));
         g.map_v = static_cast<int16_t>(fp8 ? row_map(maps, n_maps, pg.base, rows, true, false, 128)
@@ -721,10 +720,23 @@ static void plan_prefix_maps(const Common &c, const pkv_layout *L, const pkv_seq
 extern "C" int pkv_prefix_decode_ws_size(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs,
                                          const pkv_group *groups, int32_t n_groups, int32_t n_q_heads, size_t *bytes) {
     if (!bytes) return PKV_EINVAL;
-    PrefixCall p;
-    const int rc = prefix_common(L, seqs, n_seqs, groups, n_groups, 0, n_q_heads, nullptr, true, &p);
+    Common c;
+    PrefixPlan plan;
+    bool shares, may;
+    int rc = prefix_common(L, seqs, n_seqs, groups, n_groups, 0, n_q_heads, nullptr, &c, &plan, &shares, &may);
     if (rc) return rc;
-    *bytes = p.ws_bytes;
+    int nsm = 0;
+    rc = sm_count(&nsm);
+    if (rc) return rc;
+    const size_t shared = may ? prefix_ws_bytes(c, groups, n_groups, nsm) : 0;
+    // a call of these streams that shares nothing has their own positions only
+    for (int k = 0; k < plan.n_groups; ++k)
+        for (int s = plan.group[k].s0; s < plan.group[k].s0 + plan.group[k].n_seqs; ++s) c.seq[s].len -= plan.group[k].shared;
+    WindowPlan alone;
+    int32_t window;
+    rc = plan_alone(c, &alone, &window);
+    if (rc) return rc;
+    *bytes = std::max(shared, alone.ws_bytes);
     return PKV_OK;
 }
 
@@ -732,30 +744,48 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
                                  int32_t n_groups, int32_t layer, int32_t n_q_heads, const void *q, const void *k_new,
                                  const void *v_new, const void *ik_new, void *out, void *ws, size_t ws_bytes,
                                  int32_t *dev_status, cudaStream_t stream) {
-    PrefixCall p;
-    int rc = prefix_common(L, seqs, n_seqs, groups, n_groups, layer, n_q_heads, dev_status, false, &p);
+    Common c;
+    PrefixPlan plan;
+    bool shares, may;
+    int rc = prefix_common(L, seqs, n_seqs, groups, n_groups, layer, n_q_heads, dev_status, &c, &plan, &shares, &may);
     if (rc) return rc;
-    if (p.own.items == 0) return PKV_OK;
+    const int32_t tokens = total_new(c);
+    if (tokens == 0) return PKV_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out)) return PKV_EINVAL;
     if ((k_new == nullptr) != (v_new == nullptr)) return PKV_EINVAL;
     if (k_new) {
         if (!aligned16(k_new) || !aligned16(v_new)) return PKV_EINVAL;
         if (L->idx_dim && (!ik_new || !aligned16(ik_new))) return PKV_EINVAL;
     }
-    if (p.ws_bytes > 0 && (!ws || ws_bytes < p.ws_bytes || (reinterpret_cast<uintptr_t>(ws) & 255u))) return PKV_EINVAL;
+    const uint16_t *const kn = static_cast<const uint16_t *>(k_new), *const vn = static_cast<const uint16_t *>(v_new);
+    const uint16_t *const ikn = k_new && L->idx_dim ? static_cast<const uint16_t *>(ik_new) : nullptr;
     DecodeMaps maps;  // copied into the launch's parameters
-    plan_window_maps(p.c, L, seqs, maps);
-    float *const own = static_cast<float *>(ws), *const shared = own + p.own_floats;
-    const bool merge = p.shared.n_groups > 0;
-    rc = launch_window(p.c, p.own, maps, p.window, 0, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out), own,
-                       static_cast<const uint16_t *>(k_new), static_cast<const uint16_t *>(v_new),
-                       k_new && L->idx_dim ? static_cast<const uint16_t *>(ik_new) : nullptr, stream, merge);
-    if (rc || !merge) return rc;
-    DecodeMaps shared_maps;
-    plan_prefix_maps(p.c, L, seqs, p.shared, shared_maps);
-    rc = launch_prefix(p.c, p.shared, shared_maps, static_cast<const uint16_t *>(q), shared, stream);
+    if (!shares) {
+        WindowPlan alone;
+        int32_t window;
+        rc = plan_alone(c, &alone, &window);
+        if (rc) return rc;
+        if (alone.ws_bytes > 0 && (!ws || ws_bytes < alone.ws_bytes || (reinterpret_cast<uintptr_t>(ws) & 255u))) return PKV_EINVAL;
+        plan_window_maps(c, L, seqs, maps);
+        return launch_window(c, alone, maps, window, 0, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out),
+                             static_cast<float *>(ws), kn, vn, ikn, stream);
+    }
+    int nsm = 0;
+    rc = sm_count(&nsm);
     if (rc) return rc;
-    return launch_prefix_combine(p.c, p.shared, p.own.pieces, shared, own, static_cast<uint16_t *>(out), stream);
+    plan_prefix(c, nsm, &plan);
+    if (plan.floats > 0 &&
+        (!ws || ws_bytes < static_cast<size_t>(plan.floats) * 4 || (reinterpret_cast<uintptr_t>(ws) & 255u)))
+        return PKV_EINVAL;
+    // the new rows first, into their pages: the attention's kernel streams the
+    // shared rows meanwhile
+    if (k_new) {
+        rc = (c.kv_fp8 ? launch_store8 : launch_store)(c, tokens, kn, vn, ikn, stream);
+        if (rc) return rc;
+    }
+    plan_prefix_maps(c, L, seqs, plan, maps);
+    return launch_prefix(c, plan, maps, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out),
+                         static_cast<float *>(ws), stream);
 }
 
 extern "C" int pkv_sparse_ws_size(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs,

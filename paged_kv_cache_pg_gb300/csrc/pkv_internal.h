@@ -259,9 +259,7 @@ struct WindowPlan {
     int64_t stash_off;  // floats of partials in the workspace, before the stash
     size_t ws_bytes;
 };
-// partials: the pieces' sums stay in the workspace, O [piece of the unit][column][256]
-// of each stream from its ws_off on, then (m, l), for the caller to merge.
-int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan, bool partials = false);
+int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan);
 // Row maps of the streams (in tma): 3D boxes of 16 whole bf16 rows, or of 32
 // code rows where a page holds every run of 32 positions from a multiple of 32
 // (16 else).
@@ -269,44 +267,58 @@ __host__ __device__ inline bool window_wide(const SeqDev &d) { return d.table ==
 void plan_window_maps(Common &c, const pkv_layout *layout, const pkv_seq *seqs, DecodeMaps &maps);
 int launch_window(const Common &c, const WindowPlan &plan, const DecodeMaps &maps, int32_t window,
                   int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
-                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool partials = false);
+                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 
-// Attention over pages that streams share (pkv_prefix.cu).  A group's streams
-// follow one another in the call; its rows are their query columns, token after
-// token, n_q_heads / n_kv_heads of each KV head.
-constexpr int kMaxGroups = PKV_MAX_SEQS / 2;  // of two streams or more
+// Decode over pages that streams share (pkv_prefix.cu).  A group's streams follow
+// one another in the call; its rows are their query columns, token after token,
+// n_q_heads / n_kv_heads of each KV head; a unit is 256 of them.  A unit's keys are
+// the group's shared positions, then its streams' own ones, each padded to whole
+// runs of 16, counted through as virtual keys.
+constexpr int kUnitRows = 256;
+constexpr int kMaxUnits = PKV_MAX_SEQS + PKV_MAX_SEQS * 32 / kUnitRows;  // at most 32 columns a stream
+struct PrefixStream {
+    const int32_t *table;  // nullptr: contiguous
+    int32_t len, n_new;
+    int32_t tok;           // its first packed token
+    int32_t own;           // its own keys' place among the group's (virtual)
+};
 struct PrefixGroup {
     const uint16_t *layer_base;
-    const int32_t *table;  // of its first stream
     int64_t ps;            // elements in a page
-    int64_t ws_off;        // float offset of its partials in the workspace
     int64_t layer_row;     // map row of layer_base
     int32_t ptok, n_pages; // positions in a page, arena pages
-    int32_t len;           // shared positions
-    int32_t tok0;          // first packed token of its streams
-    int32_t rows;          // query rows of a KV head
-    int32_t work_off;      // first item (pair of CTAs)
-    int32_t nsplit, split_tiles;
+    int32_t shared;        // shared positions
+    int32_t early;         // positions below it are read before the grid-dependency wait
+    int32_t s0, n_seqs;    // its streams
+    int32_t tok0, rows;    // first packed token, rows of a KV head
+    int32_t unit0;         // its first unit
     int16_t map_k, map_v;  // whole K and V slots, or -1
     int16_t map_run;       // 16-row runs, or -1: key by key
 };
-struct PrefixPlan {
-    int32_t n_groups;
-    int32_t items;
-    int64_t floats;        // of partials
-    PrefixGroup group[kMaxGroups];
-    int8_t of[PKV_MAX_SEQS];  // each stream's group, or -1
+struct PrefixUnit {
+    int64_t ws_off;        // float offset of its partials in the workspace
+    int32_t group, row0, rows;
+    int32_t s_first;       // stream of its first row
+    int32_t keys;          // virtual keys
+    int32_t work_off;      // first item (pair of CTAs)
+    int32_t nsplit, split_tiles;
 };
-// The shared parts of a call whose plan holds each group's rows, length and
-// descriptors: splits, work and workspace (floats: the most that any shared
-// length takes).
+struct PrefixPlan {
+    int32_t n_groups, n_units, n_seqs;
+    int32_t items;
+    bool merge;            // some unit has several splits
+    int64_t floats;        // of partials
+    PrefixStream seq[PKV_MAX_SEQS];
+    PrefixGroup group[PKV_MAX_SEQS];
+    PrefixUnit unit[kMaxUnits];
+};
+// Units, splits and workspace places of a plan that holds the groups and streams.
 void plan_prefix(const Common &c, int nsm, PrefixPlan *plan);
-int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &maps, const uint16_t *q, float *ws,
+// Bytes of partials that calls of these streams' new tokens take at most, whatever
+// their lengths and whichever of the groups' pages are shared.
+size_t prefix_ws_bytes(const Common &c, const pkv_group *groups, int32_t n_groups, int nsm);
+int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &maps, const uint16_t *q, uint16_t *out, float *ws,
                   cudaStream_t stream);
-// Merge of the shared parts' partials (in ws) and of the streams' own (in
-// ws_own, as plan_window's with partials), into out.
-int launch_prefix_combine(const Common &c, const PrefixPlan &plan, int32_t pieces, const float *ws, const float *ws_own,
-                          uint16_t *out, cudaStream_t stream);
 
 // Windowed chunk attention (pkv_window_prefill.cu): plan and launch (gather,
 // chunk kernel, and the combine of split calls).

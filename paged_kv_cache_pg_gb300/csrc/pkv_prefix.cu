@@ -1,12 +1,19 @@
-// Attention of many streams' queries over pages that the streams share, on the
-// fifth-generation tensor cores: the shared rows are read once for all of them.
+// Decode attention over pages that streams share, on the fifth-generation tensor
+// cores: the shared rows are read once for all the streams of a group, and every
+// stream's own rows in the same pass.
 //
 // Rows: the query columns of a group's streams on one KV head, token after
-// token, 256 to an M-tile.  No row is masked (every query of the group comes
-// behind the shared positions).  A pair of CTAs (cta_group::2) takes an M-tile
-// and a range of keys, in tiles of 128: each CTA holds half of the rows, half of
-// a tile's K (64 keys) and half of its V (128 dims), so a tile's bytes go into
-// shared memory once for 256 rows.  Per tile:
+// token, 256 to a unit.  Its keys are the shared positions, which every row
+// reads, and then the own positions of the streams whose rows these are, stream
+// after stream, each of which only its own rows read: counted through as virtual
+// keys, in runs of 16, 128 to a tile.  The products of the masked part are idle
+// work, but a tile's rows take longer to come from memory than its products
+// take, so the own parts cost what their bytes cost, and no second kernel with
+// partials of its own is needed.
+//
+// A pair of CTAs (cta_group::2) takes a unit and a range of its tiles: each CTA
+// holds half of the rows, half of a tile's K (64 keys) and half of its V (128
+// dims), so a tile's bytes go into shared memory once for 256 rows.  Per tile:
 //   S = Q K^T -> TMEM (Q sits there too), P = softmax numerators in fp16 ->
 //   shared memory, O += P V -> TMEM
 // with V as fp16: bf16 rows are converted where they lie, e4m3 codes (K's too)
@@ -14,16 +21,18 @@
 // product takes one P part of 11 significant bits.  The scales of e4m3 rows go
 // into the scores (K) and the weights (V); the weights' reference is the running
 // maximum of score + V-scale exponent, so that they stay in fp16's range
-// wherever the scales lie.
+// wherever the scales lie.  An own V row that is not finite in fp16 (or lies
+// behind its stream's end) is multiplied as zeros, because the other streams'
+// rows meet it with a weight of 0; its stream's sums become NaN instead.
 //   warps 0-7   softmax: two threads a row, each on 64 of a tile's keys
 //   warps 8, 9  copy K and V (halves of one page, of 16-row runs, or key by key)
 //   warps 10-13 convert
 //   warp 14     first CTA: issues S; second: passes on that its K is there
 //   warp 15     first CTA: issues PV
-// The splits' O, maxima and sums go to the workspace; prefix_combine merges them
-// with the partials of the streams' own positions (pkv_window.cu).
+// The splits' O, maxima and sums go to the workspace and prefix_combine merges
+// them; a unit of one split writes its output itself.
 #include <algorithm>
-#include <cfloat>
+#include <climits>
 
 #include "pkv_tc.cuh"
 
@@ -31,7 +40,8 @@ namespace pkv {
 namespace {
 
 constexpr int kN = 128;        // keys a tile
-constexpr int kRows = 2 * kM;  // rows of an M-tile
+constexpr int kRun = 16;       // keys of a run
+static_assert(kUnitRows == 2 * kM, "a pair's rows");
 constexpr int kThreads = 512;
 constexpr int kSoftWarps = 8, kWarpK = 8, kWarpV = 9, kWarpConv = 10, kConvWarps = 4, kWarpS = 14, kWarpPv = 15;
 constexpr uint32_t kTmemCols = 512, kQCol = 0, kSCol = 128, kOCol = 256;
@@ -44,6 +54,8 @@ constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(2
 constexpr float kRescale = 8.f;          // rescale O when the reference grows by more than 2^8
 constexpr float kFarScore = 67108864.f;  // 2^26: references beyond it are reported (float32 steps of 4 there)
 
+constexpr int kInfo = 4;  // tiles whose runs' (and scales') places are kept
+
 template <bool kFp8>
 struct Lay {
     static constexpr int slots = kFp8 ? 2 : 3;      // of 16-bit K, and of V
@@ -52,8 +64,9 @@ struct Lay {
     static constexpr int off_v = off_k + slots * kSlotBytes;
     static constexpr int off_raw = off_v + slots * kSlotBytes;
     static constexpr int off_red = off_raw + raw * kRawBytes;  // [parity][half][row]
-    static constexpr int off_scl = off_red + 2 * 2 * kM * 4;   // [tile parity][K scale, V exponent, V scale][key]
-    static constexpr int off_bar = off_scl + (kFp8 ? 2 * 3 * kN * 4 : 0);
+    static constexpr int off_scl = off_red + 2 * 2 * kM * 4;   // [tile & 3][K scale, V exponent, V scale][key]
+    static constexpr int off_info = off_scl + (kFp8 ? kInfo * 3 * kN * 4 : 0);  // [tile & 3][stream, position, keys][run]
+    static constexpr int off_bar = off_info + kInfo * 3 * (kN / kRun) * 4;
     // barriers.  Of the first CTA, with arrivals from both: k_ready, v_ready,
     // q_full, s_empty, p_full.  Of each CTA: the others.
     static constexpr int k_full = 0, v_full = 3;      // copies landed (codes: the raw ring's, in k_full)
@@ -62,19 +75,22 @@ struct Lay {
     static constexpr int k_free = 15, v_free = 18;    // its products are done
     static constexpr int q_full = 21, s_full = 22, s_empty = 23, p_full = 24, o_done = 25;
     static constexpr int red = 26;                    // a row quarter's exchange (4)
-    static constexpr int scl_full = 30, scl_free = 32;
-    static constexpr int drain = 34;
-    static constexpr int bars = 36;
-    static constexpr int smem = off_bar + bars * 8 + 16;
+    static constexpr int info_full = 30, info_free = info_full + kInfo;
+    static constexpr int drain = info_free + kInfo;
+    static constexpr int bars = drain + 2;
+    static constexpr int smem = off_bar + bars * 8 + 16;  // behind the barriers: TMEM address, flags
     static_assert(smem <= 232448, "above the 227 KB a CTA may hold");
 };
 
 struct PrefixArgs {
     const uint16_t *q;
+    uint16_t *out;
     float *ws;
     uint32_t *status;
-    int32_t n_groups, n_kv_heads, n_q_heads, group;  // group: query heads of a KV head
-    PrefixGroup g[kMaxGroups];
+    int32_t n_units, n_kv_heads, n_q_heads, group;  // group: query heads of a KV head
+    PrefixStream seq[PKV_MAX_SEQS];
+    PrefixGroup g[PKV_MAX_SEQS];
+    PrefixUnit unit[kMaxUnits];
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -85,58 +101,65 @@ __device__ __forceinline__ uint32_t cta_rank() {
 __device__ __forceinline__ void arrive_first(uint64_t *bar) {  // at the first CTA's barrier
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, 0)) : "memory");
 }
-// mbar_wait for what the other CTA arrived at, too.
-__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, uint32_t *status) {
-    const auto test = [&]() -> bool {
+// A bounded wait as mbar_wait, in few instructions where it is called: sixteen
+// warps in nine roles share the instruction cache, and with each role's loop
+// written out at length a tile took 6,500 cycles, half of them waiting for
+// instructions.
+__device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t *status) {
+    const uint64_t t0 = global_ns();
+    for (uint32_t spin = 1;; ++spin) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
             "selp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity)
+            : "r"(bar), "r"(parity)
             : "memory");
-        return ok != 0;
-    };
-    if (test()) return true;
-    const uint64_t t0 = global_ns();
-    for (uint32_t spin = 0;; ++spin) {
-        if (test()) return true;
-        if ((spin & 255u) == 255u && global_ns() - t0 > kWaitLimitNs) {
+        if (ok) return true;
+        if ((spin & 255u) == 0 && global_ns() - t0 > kWaitLimitNs) {
             if (status) atomicOr(status, PKV_DEV_TIMEOUT);
             return false;
         }
     }
 }
+__device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, uint32_t *status) {
+    return mbar_try_wait(bar, parity) || wait_long(smem_u32(bar), parity, status);
+}
 
 // A pair's work.
 struct Work {
-    int g, kvh, split;
-    int first, count;  // the CTA's rows of the group
-    int key0, key1, ntiles;
+    int u, kvh, split;
+    int first, count;  // the CTA's rows of the unit
+    int key0, key1, ntiles;  // virtual keys
 };
 __device__ __forceinline__ Work work_of(const PrefixArgs &a, int item, int rank) {
     Work w;
-    w.g = find_seq(a.n_groups, item, [&](int t) { return a.g[t].work_off; });
-    const PrefixGroup &g = a.g[w.g];
-    const int mtiles = (g.rows + kRows - 1) / kRows, r = item - g.work_off, u = r / mtiles;
-    const int row0 = (r - u * mtiles) * kRows, rows = min(kRows, g.rows - row0), half = (rows + 1) >> 1;
-    w.kvh = u / g.nsplit;
-    w.split = u - w.kvh * g.nsplit;
-    w.first = row0 + rank * half;
-    w.count = rank ? rows - half : half;
-    w.key0 = w.split * g.split_tiles * kN;
-    w.key1 = min(g.len, w.key0 + g.split_tiles * kN);
+    w.u = find_seq(a.n_units, item, [&](int t) { return a.unit[t].work_off; });
+    const PrefixUnit &u = a.unit[w.u];
+    const int r = item - u.work_off, half = (u.rows + 1) >> 1;
+    w.kvh = r / u.nsplit;
+    w.split = r - w.kvh * u.nsplit;
+    w.first = rank * half;
+    w.count = rank ? u.rows - half : half;
+    w.key0 = w.split * u.split_tiles * kN;
+    w.key1 = min(u.keys, w.key0 + u.split_tiles * kN);
     w.ntiles = (w.key1 - w.key0 + kN - 1) / kN;
     return w;
 }
 
+// Stream of a unit's row (its token counted from the group's first).
+__device__ __forceinline__ int stream_of(const PrefixArgs &a, const PrefixGroup &g, int tok) {
+    return g.s0 + find_seq(g.n_seqs, g.tok0 + tok, [&](int t) { return a.seq[g.s0 + t].tok; });
+}
+
 // Where a tile's rows are.  With a map: lane i & 7 has run i of 16 rows; without,
-// lane i keys i, i + 32, i + 64, i + 96.  Keys behind the end are the last run's
-// or the last key's (their scores are masked, their rows finite).
+// lane i keys i, i + 32, i + 64, i + 96.  Keys behind a stream's end are its last
+// one's, runs behind the unit's the tile's first.
 struct Look {
     int64_t at[4];  // element offset of the page from layer_base
     int row[4];     // row in it
+    int s, pos, n;  // run lane & 7: its stream, its first position, its keys
 };
 
 template <bool kFp8>
@@ -147,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::off_bar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::bars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    uint32_t *const bad = tmem_slot + 2;  // streams (from the unit's first) with a V row that is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cta_rank());
     {
@@ -174,15 +198,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars[L::p_full], 2 * kSoftWarps);
         mbar_init(&bars[L::o_done], 1);
         for (int i = 0; i < 4; ++i) mbar_init(&bars[L::red + i], 2);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bars[L::scl_full + i], 2);
-            mbar_init(&bars[L::scl_free + i], kSoftWarps);
-            mbar_init(&bars[L::drain + i], 1);
+        for (int i = 0; i < kInfo; ++i) {
+            mbar_init(&bars[L::info_full + i], kFp8 ? 2 : 1);
+            mbar_init(&bars[L::info_free + i], kSoftWarps + kConvWarps);
         }
+        mbar_init(&bars[L::drain], 1);
+        mbar_init(&bars[L::drain + 1], 1);
         *abort_flag = 0;
+        bad[0] = bad[1] = 0u;
         fence_mbar_init();
-        // prefix_combine may start: it waits for this grid
-        pdl_trigger();
     }
     if (warp == kWarpS) {
         __syncwarp();
@@ -196,28 +220,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot, sbase = smem_u32(smem);
     const Work w = work_of(a, static_cast<int>(blockIdx.x >> 1), rank);
-    const PrefixGroup &g = a.g[w.g];
+    const PrefixUnit &u = a.unit[w.u];
+    const PrefixGroup &g = a.g[u.group];
     const int H = a.n_kv_heads, G = a.group;
+    // a tile of shared keys only, none behind their end: nothing to mask
+    const auto all_shared = [&](int n) { return w.key0 + (n + 1) * kN <= g.shared; };
+    const int *const info = reinterpret_cast<const int *>(smem + L::off_info);  // of tile n: + (n & 3) * 24
 
     auto wait = [&](int bar, uint32_t phase) -> bool {
-        const bool ok = mbar_wait(&bars[bar], phase & 1, a.status);
+        const bool ok = wait_on(&bars[bar], phase & 1, a.status);
         if (!ok) *abort_flag = 1;
         return ok;
     };
     auto wait_warp = [&](int bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
-    auto wait_both = [&](int bar, uint32_t phase) -> bool {
-        const bool ok = wait_cluster(&bars[bar], phase & 1, a.status);
-        if (!ok) *abort_flag = 1;
-        return ok;
-    };
-
-    // No grid-dependency wait before anything is read: the kernel before this one
-    // on the stream (the streams' own positions, window_partial) lets this grid
-    // start only behind its own wait, when everything queued before it is
-    // visible, and itself writes no shared row, no query and none of these
-    // partials.  Its end is waited for at this kernel's (the combine reads it).
     if (warp < kSoftWarps) {
         // ---------------- softmax ----------------
+        pdl_wait();
+        // the next kernel may start: what is older than this grid is done, and
+        // this one writes no cached row
+        if (tid == 0) pdl_trigger();
         const int r = lane + 32 * (warp & 3), hf = warp >> 2;
         const bool row_ok = r < w.count, active = 32 * (warp & 3) < w.count;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -235,10 +256,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         float qs = kScaleLog2;  // what a raw score is scaled by
+        int my = -3, qpos = 0;  // the row's stream and position
+        int64_t q_row = 0;      // its packed row
         if (active) {
-            const int gr = w.first + r, tok = row_ok ? gr / G : 0, h = row_ok ? gr - tok * G : 0;
-            const uint4 *src = reinterpret_cast<const uint4 *>(
-                a.q + (((int64_t)g.tok0 + tok) * a.n_q_heads + w.kvh * G + h) * kHeadDim + 128 * hf);
+            if (row_ok) {
+                const int gr = u.row0 + w.first + r, tok = gr / G, h = gr - tok * G;
+                my = stream_of(a, g, tok);
+                const PrefixStream &st = a.seq[my];
+                qpos = st.len - st.n_new + (g.tok0 + tok - st.tok);
+                q_row = ((int64_t)g.tok0 + tok) * a.n_q_heads + w.kvh * G + h;
+            }
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + q_row * kHeadDim + 128 * hf);
             float dn = 1.f;
             if constexpr (kFp8) {
                 // bf16 has the wider range: a power of two takes the row's largest
@@ -257,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (zeros, and rows with an infinity or NaN, stay as they are)
                 const int e = ex == 0 || ex == 0xff ? 0 : max(ex - 127 - 14, -100);
                 dn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                qs = kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                qs = 256.f * kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);  // (the codes' 2^-8)
             }
 #pragma unroll 1
             for (int h32 = 0; h32 < 2; ++h32) {
@@ -282,19 +310,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t *const p_row = smem + hf * kPRegion + r * 128;
         for (int n = 0; ok && n < w.ntiles; ++n) {
             if (!(ok = wait_warp(L::s_full, n))) break;
+            const int slot = n % kInfo;
             if (!active) {  // no row of the warp: S and P are nobody's
                 if (lane == 0) arrive_first(&bars[L::s_empty]);
                 if (n > 0 && !(ok = wait_warp(L::o_done, n - 1))) break;
                 if (lane == 0) {
                     arrive_first(&bars[L::p_full]);
-                    if (kFp8) mbar_arrive(&bars[L::scl_free + (n & 1)]);
+                    mbar_arrive(&bars[L::info_free + slot]);
                 }
                 __syncwarp();
                 continue;
             }
-            tc_fence_after();
+            const bool masked = !all_shared(n);
+            const float *const scl = reinterpret_cast<const float *>(smem + L::off_scl) + slot * 3 * kN + 64 * hf;
+            if ((kFp8 || masked) && !(ok = wait_warp(L::info_full + slot, n / kInfo))) break;
+            // the keys that the row sees, a bit each: of a run of its own stream those up
+            // to its position, of a shared run those there are
+            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+            bool any = true;
+            if (masked) {
+                see[0] = see[1] = 0u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int *const run = info + slot * 24 + 4 * hf + k;
+                    const int keys = min(run[16], run[0] == -1 ? kRun : run[0] == my ? qpos - run[8] + 1 : 0);
+                    see[k >> 1] |= (keys > 0 ? (1u << keys) - 1u : 0u) << (16 * (k & 1));
+                }
+                any = __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
+            }
             float x[64];
-            {
+            if (any) {
+                tc_fence_after();
                 uint32_t sv[64];
                 tmem_ld64(lane_base + kSCol + 64 * hf, sv);
 #pragma unroll
@@ -303,9 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_first(&bars[L::s_empty]);
-            const float *const scl = reinterpret_cast<const float *>(smem + L::off_scl) + (n & 1) * 3 * kN + 64 * hf;
-            if constexpr (kFp8) {
-                if (!(ok = wait_warp(L::scl_full + (n & 1), n >> 1))) break;
+            if (kFp8 && any) {
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 k = *reinterpret_cast<const float4 *>(scl + j);
@@ -315,17 +359,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x[j + 3] *= k.w * qs;
                 }
             }
-            const int kt = w.key0 + n * kN + 64 * hf;
-            if (kt + 64 > w.key1) {  // the prefix's end: uniform
+            if (masked && any) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
-                    if (kt + j >= w.key1) x[j] = -INFINITY;
+                    if (!(see[j >> 5] & (1u << (j & 31)))) x[j] = -INFINITY;
             }
             // this half's reference as eight interleaved chains, then the row's
             float m8[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) m8[j] = -INFINITY;
-            if constexpr (kFp8) {
+            if (!any) {
+            } else if constexpr (kFp8) {
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 e = *reinterpret_cast<const float4 *>(scl + kN + j);
@@ -367,7 +411,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // with the lazy rescale (times a V scale's mantissa below 2)
             const float m_off = m_used == -INFINITY ? 0.f : m_used;
             uint32_t p16[32];
-            if constexpr (kFp8) {
+            if (!any) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) p16[j] = 0u;
+            } else if constexpr (kFp8) {
                 float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
@@ -382,8 +429,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p16[j / 2 + 1] = pack_f16(p2 * v.z, p3 * v.w);
                 }
                 l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[L::scl_free + (n & 1)]);
+                if (masked) {  // a scale that the row does not see may be anything: 0 times it is not 0
+#pragma unroll
+                    for (int j = 0; j < 64; j += 2) {
+                        const uint32_t two = (see[j >> 5] >> (j & 31)) & 3u;
+                        p16[j / 2] &= ((two & 1u) ? 0xffffu : 0u) | ((two & 2u) ? 0xffff0000u : 0u);
+                    }
+                }
             } else {
                 const float2 scale = make_float2(kScaleLog2, kScaleLog2), off = make_float2(-m_off, -m_off);
                 float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -397,6 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars[L::info_free + slot]);
             // the P rows are free once the last tile's product is done
             if (n > 0 && !(ok = wait_warp(L::o_done, n - 1))) break;
 #pragma unroll
@@ -416,13 +470,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
         }
         if (ok && active) {
-            float *const acc = a.ws + g.ws_off;
-            float *const ml = acc + (int64_t)H * g.nsplit * g.rows * kHeadDim;
-            const int64_t prow = ((int64_t)w.kvh * g.nsplit + w.split) * g.rows + w.first + r;
-            const int64_t mine = row_ok ? prow : -1;
+            const bool single = u.nsplit == 1;
+            float *const acc = a.ws + u.ws_off;
+            float *const ml = acc + (int64_t)H * u.nsplit * u.rows * kHeadDim;
+            const int64_t prow = ((int64_t)w.kvh * u.nsplit + w.split) * u.rows + w.first + r;
+            const int64_t mine = !row_ok ? -1 : single ? q_row : prow;
             int64_t row[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) row[j] = shfl64(mine, (lane & ~3) + j);
+            // (both CTAs' converters flagged it before the products that the sums waited for)
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            bool odd_row = false;
+            if (row_ok) {
+                const int i = my - u.s_first;
+                odd_row = (reinterpret_cast<volatile uint32_t *>(bad)[i >> 5] >> (i & 31)) & 1u;
+            }
+            if (odd_row) l = __uint_as_float(0x7fffffffu);
+            const float inv = (kFp8 ? 256.f : 1.f) / l;
             float2 odd = make_float2(0.f, 0.f);  // NaN once a sum is not finite
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
@@ -432,49 +496,110 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; j += 2)
                     odd = fma2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), make_float2(0.f, 0.f), odd);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                if (single) {
                     uint4 v[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        v[j] = make_uint4(o[16 * h + 4 * j], o[16 * h + 4 * j + 1], o[16 * h + 4 * j + 2], o[16 * h + 4 * j + 3]);
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            e[k] = pack_bf16(__uint_as_float(o[8 * j + 2 * k]) * inv, __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
+                        v[j] = make_uint4(e[0], e[1], e[2], e[3]);
+                    }
                     quad_transpose(v, lane);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         if (row[j] >= 0)
-                            *(reinterpret_cast<uint4 *>(acc + row[j] * kHeadDim + 128 * hf + 32 * ch + 16 * h) + (lane & 3)) = v[j];
+                            *(reinterpret_cast<uint4 *>(a.out + row[j] * kHeadDim + 128 * hf + 32 * ch) + (lane & 3)) = v[j];
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint4 v[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t e[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                e[k] = kFp8 ? __float_as_uint(256.f * __uint_as_float(o[16 * h + 4 * j + k])) : o[16 * h + 4 * j + k];
+                            v[j] = make_uint4(e[0], e[1], e[2], e[3]);
+                        }
+                        quad_transpose(v, lane);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (row[j] >= 0)
+                                *(reinterpret_cast<uint4 *>(acc + row[j] * kHeadDim + 128 * hf + 32 * ch + 16 * h) + (lane & 3)) = v[j];
+                    }
                 }
             }
             if (row_ok) {
-                if (hf == 0) *reinterpret_cast<float2 *>(ml + 2 * prow) = make_float2(m_used, l);
-                if ((odd.x + odd.y != 0.f || (m_used != -INFINITY && fabsf(m_used) > kFarScore)) && a.status)
+                if (hf == 0 && !single) *reinterpret_cast<float2 *>(ml + 2 * prow) = make_float2(m_used, l);
+                if ((odd_row || odd.x + odd.y != 0.f || (m_used != -INFINITY && fabsf(m_used) > kFarScore)) && a.status)
                     atomicOr(a.status, PKV_DEV_RANGE);
             }
         }
     } else if (warp == kWarpK || warp == kWarpV) {
         // ---------------- copies ----------------
         const bool is_v = warp == kWarpV;
-        const int ptok = g.ptok, n_pages = g.n_pages, n_table = (g.len + ptok - 1) / ptok;
-        const int32_t *const table = g.table;
-        const uint64_t pol = policy_evict_normal();  // the other M-tiles read the same rows
+        const int ptok = g.ptok, n_pages = g.n_pages;
+        const uint64_t pol = policy_evict_normal();  // other units read the shared rows too
         const void *const map = g.map_run >= 0 ? &maps.map[g.map_run] : nullptr;
         const int whole_map = is_v ? g.map_v : g.map_k;
         const void *const map_w = whole_map >= 0 ? &maps.map[whole_map] : nullptr;
         const uint8_t *const base = reinterpret_cast<const uint8_t *>(g.layer_base);
         const bool runs = map != nullptr;
+        // The unit's streams, one and another 32 behind it a lane: a search through
+        // the launch parameters for each run took a tile of 64 streams 3 us
+        const int pad = (g.shared + kRun - 1) / kRun * kRun, n_seqs = g.s0 + g.n_seqs - u.s_first;
+        int st_own[2], st_len[2];
+        int64_t st_table[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int t = min(lane + 32 * i, n_seqs - 1);
+            const PrefixStream &st = a.seq[u.s_first + t];
+            st_own[i] = lane + 32 * i < n_seqs ? st.own : INT_MAX;
+            st_len[i] = st.len;
+            st_table[i] = reinterpret_cast<int64_t>(st.table);
+        }
+        const int own0 = __shfl_sync(0xffffffffu, st_own[0], 0);
+        const int64_t table0 = shfl64(st_table[0], 0);  // (every lane takes part in every exchange: none under a lane's condition)
         auto look = [&](int m) -> Look {
             Look k;
-            const int kt = w.key0 + m * kN;
+            const int kt = w.key0 + m * kN, v = kt + kRun * (lane & 7);
+            // run lane & 7: the last stream whose own keys begin at or before its first
+            int t = 0;
+            if (kt + kN > pad) {  // uniform
+#pragma unroll 1
+                for (int i = 0; i < 8; ++i) {
+                    const int x = kt + kRun * i - pad + own0;
+                    const int below = __popc(__ballot_sync(0xffffffffu, st_own[0] <= x)) + __popc(__ballot_sync(0xffffffffu, st_own[1] <= x));
+                    if ((lane & 7) == i) t = max(below - 1, 0);
+                }
+            }
+            const auto pick = [&](int x, int y) {
+                const int lo = __shfl_sync(0xffffffffu, x, t & 31), hi = __shfl_sync(0xffffffffu, y, t & 31);
+                return t < 32 ? lo : hi;
+            };
+            const int own = pick(st_own[0], st_own[1]), len = pick(st_len[0], st_len[1]);
+            const int64_t table_lo = shfl64(st_table[0], t & 31), table_hi = shfl64(st_table[1], t & 31);
+            const int64_t table = v < pad ? table0 : t < 32 ? table_lo : table_hi;
+            const int limit = v < pad ? g.shared : len;
+            k.s = v >= u.keys ? -2 : v < pad ? -1 : u.s_first + t;
+            k.pos = v < pad ? v : g.shared + (v - pad + own0 - own);
+            k.n = k.s == -2 ? 0 : min(kRun, limit - k.pos);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 k.at[i] = 0;
                 k.row[i] = 0;
                 if (runs && i > 0) continue;
-                const int last = runs ? w.key1 - 16 : w.key1 - 1;
-                const int key = min(kt + (runs ? 16 * (lane & 7) : 32 * i + lane), last);
-                const int page = key / ptok;
-                k.row[i] = key - page * ptok;
-                const int id = page < n_table ? __ldg(table + page) : -1;
+                // the key's run (behind the unit's last one: the tile's first), from its lane
+                int src = runs ? lane & 7 : 2 * i + (lane >> 4);
+                if (__shfl_sync(0xffffffffu, k.s, src) == -2) src = 0;
+                const int first = __shfl_sync(0xffffffffu, k.pos, src), last = __shfl_sync(0xffffffffu, limit, src) - 1;
+                const int32_t *const tab = reinterpret_cast<const int32_t *>(shfl64(table, src));
+                const int pos = runs ? first : min(first + (lane & 15), last);
+                const int page = tab ? pos / ptok : 0;
+                k.row[i] = pos - page * ptok;
+                const int id = tab ? __ldg(tab + page) : 0;
                 if (static_cast<uint32_t>(id) < static_cast<uint32_t>(n_pages)) {
                     k.at[i] = (int64_t)id * g.ps;
                 } else if (!is_v && a.status) {
@@ -506,13 +631,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         float s_now[4] = {0.f, 0.f, 0.f, 0.f};
-        Look now = look(0);
-        if constexpr (kFp8) scales(now, s_now);
+        Look now;
+        // Shared positions far enough below the new tokens stream before the kernel
+        // before this one is done (it may be storing this call's new rows)
+        bool waited = false;
         int last_q = -1;
         bool ok = true;
-        for (int m = 0; ok && m < w.ntiles; ++m) {
+        for (int m = -1; ok && m < w.ntiles; ++m) {
             Look next = now;
             if (m + 1 < w.ntiles) next = look(m + 1);
+            if (m >= 0) {
             // the slot
             const uint32_t q = kFp8 ? 2 * m + is_v : m;
             const uint32_t n_slots = kFp8 ? L::raw : L::slots, slot = q % n_slots;
@@ -525,20 +653,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int64_t rb = row_bytes(now.at[0], now.row[0]);
                 const int y = static_cast<int>(g.layer_row + rb / (kFp8 ? 256 : 512));
                 if (lane == 0) mbar_arrive_expect_tx(full, kFp8 ? kRawBytes : kSlotBytes);
-                const int y0 = __shfl_sync(0xffffffffu, y, 0);  // (and the expected bytes come first)
-                if (map_w) {
-                    // the tile lies in one page: one copy (two of K's code halves)
+                __syncwarp();  // the expected bytes come first
+                // K's 64 keys, or V's 128, row after row in memory (one page's, mostly)
+                const int run0 = is_v ? 0 : 4 * rank, n_runs = is_v ? 8 : 4;
+                const int yf = __shfl_sync(0xffffffffu, y, run0);
+                const bool in_row = (lane & 7) < run0 || (lane & 7) >= run0 + n_runs || y == yf + 16 * ((lane & 7) - run0);
+                if (map_w && __all_sync(0xffffffffu, in_row)) {
+                    // one copy (two of K's code halves)
                     if (kFp8) {
                         if (lane < (is_v ? 1 : 2))
-                            tma_load_2d(dst + lane * 8192, map_w, is_v ? 128 * rank : 128 * lane, is_v ? y0 : y0 + 64 * rank, full, pol);
+                            tma_load_2d(dst + lane * 8192, map_w, is_v ? 128 * rank : 128 * lane, yf, full, pol);
                     } else if (lane == 0) {
-                        tma_load_3d(dst, map_w, 0, is_v ? y0 : y0 + 64 * rank, is_v ? 2 * rank : 0, full, pol);
+                        tma_load_3d(dst, map_w, 0, yf, is_v ? 2 * rank : 0, full, pol);
                     }
                 } else {
                     // 16-row runs, one box a lane: K four runs of all dims, V eight of half
                     const int nc = kFp8 ? (is_v ? 1 : 2) : (is_v ? 2 : 4);  // boxes of a run
-                    const int rn = lane / nc, ch = lane - rn * nc, n_runs = is_v ? 8 : 4;
-                    const int yr = __shfl_sync(0xffffffffu, y, (is_v ? rn : 4 * rank + rn) & 7);
+                    const int rn = lane / nc, ch = lane - rn * nc;
+                    const int yr = __shfl_sync(0xffffffffu, y, (run0 + rn) & 7);
                     if (rn < n_runs) {
                         if (kFp8)
                             tma_load_2d(dst + ch * 8192 + rn * 2048, map, is_v ? 128 * rank : 128 * ch, yr, full, pol);
@@ -577,25 +709,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) mbar_arrive(full);
             }
             last_q = static_cast<int>(q);
-            if constexpr (kFp8) {
-                float *const scl = reinterpret_cast<float *>(smem + L::off_scl) + (m & 1) * 3 * kN + lane;
-                if (m >= 2 && !(ok = wait_warp(L::scl_free + (m & 1), (m >> 1) - 1))) break;
+            // the runs' places, and with e4m3 the scales
+            if (kFp8 || !is_v) {
+                const int is = m % kInfo;
+                if (m >= kInfo && !(ok = wait_warp(L::info_free + is, m / kInfo - 1))) break;
+                if (!is_v && lane < 8) {
+                    int *const to = reinterpret_cast<int *>(smem + L::off_info) + is * 24 + lane;
+                    to[0] = now.s;
+                    to[8] = now.pos;
+                    to[16] = now.n;
+                }
+                if constexpr (kFp8) {
+                    float *const scl = reinterpret_cast<float *>(smem + L::off_scl) + is * 3 * kN + lane;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!is_v) {
-                        scl[32 * i] = s_now[i];
-                    } else {
-                        // 2^e <= scale < 2^(e+1).  Between 2^-40 and 2^80 the reference follows
-                        // it; a smaller one's (values under 4e-10, or zeros) weights fade
-                        // below fp16's range, and their sums stay in float32's
-                        const int ex = static_cast<int>((__float_as_uint(s_now[i]) >> 23) & 0xffu) - 127;
-                        scl[kN + 32 * i] = static_cast<float>(min(max(ex, -40), 80));
-                        scl[2 * kN + 32 * i] = s_now[i];
+                    for (int i = 0; i < 4; ++i) {
+                        if (!is_v) {
+                            scl[32 * i] = s_now[i];
+                        } else {
+                            // 2^e <= scale < 2^(e+1).  Between 2^-40 and 2^80 the reference follows
+                            // it; a smaller one's (values under 4e-10, or zeros) weights fade
+                            // below fp16's range, and their sums stay in float32's
+                            const int ex = static_cast<int>((__float_as_uint(s_now[i]) >> 23) & 0xffu) - 127;
+                            scl[kN + 32 * i] = static_cast<float>(min(max(ex, -40), 80));
+                            scl[2 * kN + 32 * i] = s_now[i];
+                        }
                     }
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars[L::scl_full + (m & 1)]);
-                if (m + 1 < w.ntiles) scales(next, s_now);
+                if (lane == 0) mbar_arrive(&bars[L::info_full + is]);
+            }
+            }
+            if (m + 1 < w.ntiles) {
+                if (!waited && w.key0 + (m + 2) * kN > min(g.shared, g.early)) {
+                    pdl_wait();
+                    waited = true;
+                }
+                if constexpr (kFp8) scales(next, s_now);
             }
             now = next;
         }
@@ -608,26 +757,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------- conversion to fp16 ----------------
         const int t = tid - kWarpConv * 32;
         bool ok = true;
+        const auto flag = [&](int s) {  // in both CTAs: each converts half of the dims
+            const int i = s - u.s_first;
+            for (uint32_t r = 0; r < 2; ++r)
+                asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(peer_addr(bad + (i >> 5), r)),
+                             "r"(1u << (i & 31))
+                             : "memory");
+            asm volatile("fence.acq_rel.cluster;" ::: "memory");
+        };
+        // Of a tile that is not all shared: bit i is set where row `row` of run i is
+        // behind its stream's end
+        const auto behind = [&](const int *run, int row) -> uint32_t {
+            uint32_t m = 0u;
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) m |= (row >= run[16 + i] ? 1u : 0u) << i;
+            return m;
+        };
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         if constexpr (!kFp8) {
             for (int n = 0; ok && n < w.ntiles; ++n) {
                 const int slot = n % L::slots;
                 if (!(ok = wait_warp(L::v_full + slot, n / L::slots))) break;
                 uint4 *const v = reinterpret_cast<uint4 *>(smem + L::off_v + slot * kSlotBytes) + t;
+                const bool masked = !all_shared(n);
+                if (masked && !(ok = wait_warp(L::info_full + n % kInfo, n / kInfo))) break;
+                const int *const run = info + n % kInfo * 24;  // chunk i of a thread lies in run i & 7, row t >> 3
+                const uint32_t none = masked ? behind(run, t >> 3) : 0u;
+                uint32_t top = 0u;  // the largest magnitude's bits
+#pragma unroll 1
+                for (int i = 0; i < 16; i += 4) {
+                    uint4 x[4];
 #pragma unroll
-                for (int i = 0; i < 16; i += 8) {
-                    uint4 x[8];
+                    for (int j = 0; j < 4; ++j) x[j] = v[(i + j) * 128];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] = v[(i + j) * 128];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        v[(i + j) * 128] = make_uint4(pack_f16(bf16_lo(x[j].x), bf16_hi(x[j].x)), pack_f16(bf16_lo(x[j].y), bf16_hi(x[j].y)),
-                                                      pack_f16(bf16_lo(x[j].z), bf16_hi(x[j].z)), pack_f16(bf16_lo(x[j].w), bf16_hi(x[j].w)));
+                    for (int j = 0; j < 4; ++j) {
+                        if (none & (1u << ((i + j) & 7))) x[j] = zero;
+                        const uint4 y = make_uint4(pack_f16(bf16_lo(x[j].x), bf16_hi(x[j].x)), pack_f16(bf16_lo(x[j].y), bf16_hi(x[j].y)),
+                                                   pack_f16(bf16_lo(x[j].z), bf16_hi(x[j].z)), pack_f16(bf16_lo(x[j].w), bf16_hi(x[j].w)));
+                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
+                        v[(i + j) * 128] = y;
+                    }
+                }
+                if (masked && ((top & 0xffffu) >= 0x7c00u || (top >> 16) >= 0x7c00u)) {
+                    // something is not finite: chunks of own rows that have it become zeros
+#pragma unroll 1
+                    for (int i = 0; i < 16; ++i) {
+                        const uint4 y = v[i * 128];
+                        const uint32_t m = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
+                        if (run[i & 7] >= 0 && ((m & 0xffffu) >= 0x7c00u || (m >> 16) >= 0x7c00u)) {
+                            v[i * 128] = zero;
+                            flag(run[i & 7]);
+                        }
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive_first(&bars[L::v_ready + slot]);
+                if (lane == 0) {
+                    // (first: a softmax warp's arrival for a later tile comes behind v_ready's)
+                    mbar_arrive(&bars[L::info_free + n % kInfo]);
+                    arrive_first(&bars[L::v_ready + slot]);
+                }
             }
         } else {
+            // A code's bits shifted into fp16's fields are its value times 2^-8,
+            // subnormals too, but for the NaN code 0x7f (looked for beside, and put in
+            // by a second pass where there is one).  The factor goes into the scores'
+            // scale and the sums.  (cvt.rn.f16x2.e4m3x2 took 8,900 cycles a tile.)
+            const auto widen = [](uint32_t four, uint32_t &lo, uint32_t &hi) {
+                const uint32_t a0 = __byte_perm(four, 0u, 0x1404), a1 = __byte_perm(four, 0u, 0x3424);
+                lo = (a0 & 0x80008000u) | ((a0 >> 1) & 0x3f803f80u);
+                hi = (a1 & 0x80008000u) | ((a1 >> 1) & 0x3f803f80u);
+            };
+            const auto has_nan = [](const uint4 &x) -> uint32_t {
+                return (((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) | ((x.z & 0x7f7f7f7fu) + 0x01010101u) |
+                        ((x.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
+            };
+            const int odd = (t >> 2) & 1;
             for (int q = 0; ok && q < 2 * w.ntiles; ++q) {
                 const int n = q >> 1, slot = n % L::slots, raw = q % L::raw;
                 const bool is_v = q & 1;
@@ -635,30 +840,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (n >= L::slots && !(ok = wait_warp((is_v ? L::v_free : L::k_free) + slot, n / L::slots - 1))) break;
                 const uint8_t *const src = smem + L::off_raw + raw * kRawBytes;
                 uint8_t *const dst = smem + (is_v ? L::off_v : L::off_k) + slot * kSlotBytes;
+                const bool masked = is_v && !all_shared(n);
+                if (masked && !(ok = wait_warp(L::info_full + n % kInfo, n / kInfo))) break;
+                const int *const run = info + n % kInfo * 24;  // V: chunk i of a thread lies in run i
                 // eight lanes take four chunks of 16 codes of rows r and r + 4: both
                 // the reads and the writes (one order each for the two rows) then
                 // touch every bank once
                 const int quads = is_v ? 2 : 4, plane = is_v ? 0 : 8192, region = is_v ? kVRegion : kKRegion;
-                const int odd = (t >> 2) & 1;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int u = i * 16 + (t >> 3), p = u / quads, c = 4 * (u - p * quads) + (t & 3);
-                    const int r = (p >> 2) * 8 + (p & 3) + 4 * odd;
-                    const uint4 x = *reinterpret_cast<const uint4 *>(src + (c >> 3) * plane + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-                    uint4 y[2];
-                    f16_of_codes(x.x, y[0].x, y[0].y);
-                    f16_of_codes(x.y, y[0].z, y[0].w);
-                    f16_of_codes(x.z, y[1].x, y[1].y);
-                    f16_of_codes(x.w, y[1].z, y[1].w);
+                const auto where = [&](int i, int &c, int &r) {
+                    const int unit = i * 16 + (t >> 3), p = unit / quads;
+                    c = 4 * (unit - p * quads) + (t & 3);
+                    r = (p >> 2) * 8 + (p & 3) + 4 * odd;
+                };
+                const auto from = [&](int c, int r) {
+                    return reinterpret_cast<const uint4 *>(src + (c >> 3) * plane + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                };
+                const auto put = [&](int c, int r, const uint4 &y0, const uint4 &y1) {
                     uint8_t *const to = dst + (c >> 2) * region + r * 128;
                     const int c0 = (2 * c) & 7;
-                    *reinterpret_cast<uint4 *>(to + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? y[1] : y[0];
-                    *reinterpret_cast<uint4 *>(to + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? y[0] : y[1];
+                    *reinterpret_cast<uint4 *>(to + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? y1 : y0;
+                    *reinterpret_cast<uint4 *>(to + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? y0 : y1;
+                };
+                uint32_t none = 0u, nan = 0u;
+                if (masked) {
+                    int c, r;
+                    where(0, c, r);  // (a thread's rows are the same one of every run)
+                    none = behind(run, r);
+                }
+#pragma unroll 1
+                for (int i = 0; i < 8; i += 4) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        int c, r;
+                        where(i + j, c, r);
+                        x[j] = *from(c, r);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        int c, r;
+                        where(i + j, c, r);
+                        if (none & (1u << (i + j))) x[j] = zero;
+                        uint4 y0, y1;
+                        widen(x[j].x, y0.x, y0.y);
+                        widen(x[j].y, y0.z, y0.w);
+                        widen(x[j].z, y1.x, y1.y);
+                        widen(x[j].w, y1.z, y1.w);
+                        nan |= has_nan(x[j]);
+                        put(c, r, y0, y1);
+                    }
+                }
+                if (nan) {
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        int c, r;
+                        where(i, c, r);
+                        const uint4 z = *from(c, r);
+                        if (!has_nan(z) || (masked && (r & 15) >= run[16 + i])) continue;
+                        if (masked && run[i] >= 0) {
+                            put(c, r, zero, zero);
+                            flag(run[i]);
+                        } else {  // (NaN for the whole chunk's row: K's score, V's 16 dims)
+                            const uint4 no = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+                            put(c, r, no, no);
+                        }
+                    }
                 }
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(&bars[L::raw_free + raw]);
+                    if (is_v) mbar_arrive(&bars[L::info_free + n % kInfo]);
                     arrive_first(&bars[(is_v ? L::v_ready : L::k_ready) + slot]);
                 }
             }
@@ -669,17 +921,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kWarpS) {
             const uint32_t idesc = mma_idesc_pair(kN, false, kFp8);
             const uint64_t desc = smem_desc(0, 16, 1024);
-            ok = wait_both(L::q_full, 0);
+            ok = wait(L::q_full, 0);
             for (int n = 0; ok && n < w.ntiles; ++n) {
                 const int slot = n % L::slots;
-                if (n > 0 && !(ok = wait_both(L::s_empty, n - 1))) break;
+                if (n > 0 && !(ok = wait(L::s_empty, n - 1))) break;
                 if (!kFp8 && !(ok = wait(L::k_full + slot, n / L::slots))) break;
-                if (!(ok = wait_both(L::k_ready + slot, n / L::slots))) break;
+                if (!(ok = wait(L::k_ready + slot, n / L::slots))) break;
                 tc_fence_after();
                 const uint64_t dk = desc + ((sbase + L::off_k + slot * kSlotBytes) >> 4);
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    tc_mma_ts_pair(tmem + kSCol, tmem + kQCol + 8 * i, dk + (((i >> 2) * kKRegion + (i & 3) * 32) >> 4), idesc, i > 0);
+                    for (int j = 0; j < 4; ++j)
+                        tc_mma_ts_pair(tmem + kSCol, tmem + kQCol + 32 * i + 8 * j, dk + ((i * kKRegion + j * 32) >> 4), idesc, i + j > 0);
                 tc_commit_pair(&bars[L::k_free + slot]);
                 tc_commit_pair(&bars[L::s_full]);
             }
@@ -688,14 +942,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t desc_v = smem_desc(0, kVRegion, 1024), desc_p = smem_desc(sbase, 16, 1024);
             for (int n = 0; ok && n < w.ntiles; ++n) {
                 const int slot = n % L::slots;
-                if (!(ok = wait_both(L::p_full, n))) break;
-                if (!(ok = wait_both(L::v_ready + slot, n / L::slots))) break;
+                if (!(ok = wait(L::p_full, n))) break;
+                if (!(ok = wait(L::v_ready + slot, n / L::slots))) break;
                 tc_fence_after();
                 const uint64_t dv = desc_v + ((sbase + L::off_v + slot * kSlotBytes) >> 4);
+#pragma unroll 1
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    tc_mma_pair(tmem + kOCol, desc_p + (((i >> 2) * kPRegion + (i & 3) * 32) >> 4), dv + (i * 2048 >> 4), idesc,
-                                n > 0 || i > 0);
+                    for (int j = 0; j < 4; ++j)
+                        tc_mma_pair(tmem + kOCol, desc_p + ((i * kPRegion + j * 32) >> 4), dv + ((4 * i + j) * 2048 >> 4), idesc,
+                                    n + i + j > 0);
                 tc_commit_pair(&bars[L::v_free + slot]);
                 tc_commit_pair(&bars[L::o_done]);
             }
@@ -714,7 +970,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    if (tid == 0) pdl_wait();  // the kernel before is done once this grid is
     tc_fence_before();
     cluster_sync();  // both CTAs are done with each other's barriers and products
     if (warp == kWarpS) {
@@ -724,60 +979,48 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Merge of a query row's partials: the shared part's splits, then the pieces of
-// the stream's own positions, in that order.  A CTA a row; 64 threads hold its
-// 256 dims, and four such groups take every fourth partial and add up at the
-// end, so that a row of 40 partials is two rounds of loads.
+// Merge of a query row's splits, in their order.  A CTA a row; 64 threads hold
+// its 256 dims, and four such groups take every fourth split and add up at the
+// end, so that a row of 38 splits is two rounds of loads.
 constexpr int kCombThreads = 256;
 constexpr int kCombBatch = 8;
 
 struct CombineArgs {
-    const float *ws, *ws_own;
+    const float *ws;
     uint16_t *out;
-    int32_t pieces;
-    int8_t of[PKV_MAX_SEQS];  // a stream's group, or -1
-    PrefixGroup g[kMaxGroups];
+    int32_t n_groups, n_kv_heads, n_q_heads, group;
+    int32_t tok0[PKV_MAX_SEQS];   // of each group
+    int32_t unit0[PKV_MAX_SEQS];
+    struct Unit {
+        int64_t ws_off;
+        int32_t rows, nsplit;
+    } unit[kMaxUnits];
 };
 
 __global__ void __launch_bounds__(kCombThreads)
-    prefix_combine(const __grid_constant__ Common c, const __grid_constant__ CombineArgs a) {
+    prefix_combine(const __grid_constant__ CombineArgs a) {
     __shared__ float4 sh[3][64];
-    const int tok = blockIdx.x / c.n_q_heads, head = blockIdx.x - tok * c.n_q_heads;
-    const int s = find_seq(c.n_seqs, tok, [&](int t) { return c.seq[t].tok_off; });
-    const SeqDev &sd = c.seq[s];
-    const int kvh = head / c.group, h = head - kvh * c.group;
-    const int n_own = sd.nsplit * a.pieces, col = (tok - sd.tok_off) * c.group + h;
-    const float *own = a.ws_own + sd.ws_off + ((int64_t)kvh * n_own * sd.ncols + col) * kHeadDim;
-    const float *own_ml = a.ws_own + sd.ws_off + (int64_t)c.n_kv_heads * n_own * sd.ncols * kHeadDim + ((int64_t)kvh * n_own * sd.ncols + col) * 2;
-    const int64_t own_step = sd.ncols;
-    const float *sha = own, *sha_ml = own_ml;
-    int n_sha = 0;
-    int64_t sha_step = 0;
-    if (a.of[s] >= 0) {
-        const PrefixGroup &g = a.g[a.of[s]];
-        n_sha = g.nsplit;
-        sha_step = g.rows;
-        const int64_t row = (int64_t)kvh * g.nsplit * g.rows + (tok - g.tok0) * c.group + h;
-        sha = a.ws + g.ws_off + row * kHeadDim;
-        sha_ml = a.ws + g.ws_off + (int64_t)c.n_kv_heads * g.nsplit * g.rows * kHeadDim + row * 2;
-    }
-    const int np = n_sha + n_own;
+    const int tok = blockIdx.x / a.n_q_heads, head = blockIdx.x - tok * a.n_q_heads;
+    const int k = find_seq(a.n_groups, tok, [&](int t) { return a.tok0[t]; });
+    const int kvh = head / a.group, row = (tok - a.tok0[k]) * a.group + head - kvh * a.group;
+    const CombineArgs::Unit &u = a.unit[a.unit0[k] + row / kUnitRows];
+    const int np = u.nsplit;
+    const int64_t step = u.rows, first = (int64_t)kvh * np * u.rows + row % kUnitRows;
     const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 6, d = 4 * (tid & 63);
-    asm volatile("" ::"l"(own), "l"(own_ml), "l"(sha), "l"(sha_ml), "r"(np));
+    const float *const acc = a.ws + u.ws_off + first * kHeadDim + d;
+    const float *const ml = a.ws + u.ws_off + (int64_t)a.n_kv_heads * np * u.rows * kHeadDim + 2 * first;
+    asm volatile("" ::"l"(acc), "l"(ml), "r"(np));
     pdl_wait();
-    if (tid == 0) pdl_trigger();  // every kernel of the call but this one is done
-    const auto ml_of = [&](int i) -> float2 {
-        return __ldcg(reinterpret_cast<const float2 *>(i < n_sha ? sha_ml + 2 * i * sha_step : own_ml + 2 * (i - n_sha) * own_step));
-    };
-    const auto acc_of = [&](int i) -> float4 {
-        return __ldcg(reinterpret_cast<const float4 *>((i < n_sha ? sha + i * sha_step * kHeadDim : own + (i - n_sha) * own_step * kHeadDim) + d));
-    };
+    if (tid == 0) pdl_trigger();
+    if (np == 1) return;  // written where it was summed
+    const auto ml_of = [&](int i) -> float2 { return __ldcg(reinterpret_cast<const float2 *>(ml + 2 * i * step)); };
+    const auto acc_of = [&](int i) -> float4 { return __ldcg(reinterpret_cast<const float4 *>(acc + i * step * kHeadDim)); };
     const float2 none = make_float2(-INFINITY, 0.f);
     float4 v[kCombBatch];
 #pragma unroll
     for (int j = 0; j < kCombBatch; ++j)
         if (grp + 4 * j < np) v[j] = acc_of(grp + 4 * j);
-    // every warp finds the row's maximum and sum by itself: lane i has partials i, i + 32, ...
+    // every warp finds the row's maximum and sum by itself: lane i has splits i, i + 32, ...
     const float2 ml0 = lane < np ? ml_of(lane) : none, ml1 = lane + 32 < np ? ml_of(lane + 32) : none;
     float M = fmaxf(ml0.x, ml1.x);
     for (int i = lane + 64; i < np; i += 32) M = fmaxf(M, ml_of(i).x);
@@ -813,8 +1056,8 @@ __global__ void __launch_bounds__(kCombThreads)
     __syncthreads();
     if (grp) return;
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-        const float4 x = sh[k][tid];
+    for (int j = 0; j < 3; ++j) {
+        const float4 x = sh[j][tid];
         o4.x += x.x;
         o4.y += x.y;
         o4.z += x.z;
@@ -827,61 +1070,90 @@ __global__ void __launch_bounds__(kCombThreads)
 }
 
 // Split model, in hundredths of a microsecond: a pair's tile of 128 keys and 256
-// rows, its start and end, and a split's partials written and read again.
-constexpr int64_t kTileCost = 140, kPairCost = 600, kPartialCost = 6;
+// rows, its start and end, a split's partials written and read again, and the
+// merging kernel.
+constexpr int64_t kTileCost = 140, kPairCost = 600, kPartialCost = 6, kMergeCost = 400;
 
 }  // namespace
 
-// Keys are split into whole tiles, all groups by the same number, so that the
+// Keys are split into whole tiles, all units by the same number, so that the
 // pairs fill the GPU about once; the count never passes the pairs the GPU holds
 // (or one a unit), which bounds the workspace whatever the lengths.
 void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
     const int64_t H = c.n_kv_heads, slots = std::max(1, nsm / 2);
-    int64_t units = 0, most = 1, tile_rows = 0;
-    for (int i = 0; i < plan->n_groups; ++i) {
-        PrefixGroup &g = plan->group[i];
-        const int64_t mtiles = (g.rows + kRows - 1) / kRows;
-        units += H * mtiles;
-        tile_rows = std::max(tile_rows, (g.rows + mtiles - 1) / mtiles);
-        most = std::max<int64_t>(most, ((int64_t)g.len + kN - 1) / kN);
+    plan->n_units = 0;
+    int64_t most = 1;
+    for (int k = 0; k < plan->n_groups; ++k) {
+        PrefixGroup &g = plan->group[k];
+        g.unit0 = plan->n_units;
+        for (int row0 = 0; row0 < g.rows; row0 += kUnitRows) {
+            PrefixUnit &u = plan->unit[plan->n_units++];
+            u.group = k;
+            u.row0 = row0;
+            u.rows = std::min(kUnitRows, g.rows - row0);
+            const auto stream = [&](int row) {
+                int s = g.s0;
+                for (int t = g.s0; t < g.s0 + g.n_seqs; ++t)
+                    if (plan->seq[t].n_new > 0 && plan->seq[t].tok <= g.tok0 + row / c.group) s = t;
+                return s;
+            };
+            u.s_first = stream(row0);
+            const PrefixStream &last = plan->seq[stream(row0 + u.rows - 1)];
+            const auto pad = [](int n) { return (n + kRun - 1) / kRun * kRun; };
+            u.keys = pad(g.shared) + last.own + pad(last.len - g.shared) - plan->seq[u.s_first].own;
+            most = std::max<int64_t>(most, (u.keys + kN - 1) / kN);
+        }
     }
     const auto items_of = [&](int64_t per) {
         int64_t n = 0;
-        for (int i = 0; i < plan->n_groups; ++i) {
-            const PrefixGroup &g = plan->group[i];
-            n += H * ((g.rows + kRows - 1) / kRows) * ((((int64_t)g.len + kN - 1) / kN + per - 1) / per);
-        }
+        for (int i = 0; i < plan->n_units; ++i) n += H * (((plan->unit[i].keys + kN - 1) / kN + per - 1) / per);
         return n;
     };
-    const int64_t cap = std::max(units, slots);
+    const int64_t cap = std::max(H * plan->n_units, slots);
     int64_t best = INT64_MAX, chosen = most;
     for (int64_t k = 1; k <= slots; ++k) {
         const int64_t per = (most + k - 1) / k, items = items_of(per);
         if (items > cap) continue;
-        const int64_t cost = (items + slots - 1) / slots * (per * kTileCost + kPairCost) + items * kPartialCost;
+        const int64_t cost = (items + slots - 1) / slots * (per * kTileCost + kPairCost) + (k > 1 ? items * kPartialCost + kMergeCost : 0);
         if (cost < best) {
             best = cost;
             chosen = per;
         }
     }
-    // the most partial rows of `cap` pairs: more than the items' own, which are at
-    // most that many of at most tile_rows rows each
-    plan->floats = plan->n_groups ? cap * tile_rows * (kHeadDim + 2) + 64 * plan->n_groups : 0;
     int64_t floats = 0;
     plan->items = 0;
-    for (int i = 0; i < plan->n_groups; ++i) {
-        PrefixGroup &g = plan->group[i];
-        const int64_t tiles = std::max<int64_t>(1, ((int64_t)g.len + kN - 1) / kN);
-        g.work_off = plan->items;
-        g.split_tiles = static_cast<int32_t>(std::min(chosen, tiles));
-        g.nsplit = static_cast<int32_t>((tiles + g.split_tiles - 1) / g.split_tiles);
-        g.ws_off = floats;
-        plan->items += static_cast<int32_t>(H * ((g.rows + kRows - 1) / kRows) * g.nsplit);
-        floats += (H * g.nsplit * g.rows * (kHeadDim + 2) + 63) / 64 * 64;
+    plan->merge = false;
+    for (int i = 0; i < plan->n_units; ++i) {
+        PrefixUnit &u = plan->unit[i];
+        const int64_t tiles = (u.keys + kN - 1) / kN;
+        u.work_off = plan->items;
+        u.split_tiles = static_cast<int32_t>(std::min(chosen, tiles));
+        u.nsplit = static_cast<int32_t>((tiles + u.split_tiles - 1) / u.split_tiles);
+        u.ws_off = floats;
+        plan->items += static_cast<int32_t>(H * u.nsplit);
+        if (u.nsplit > 1) {
+            plan->merge = true;
+            floats += (H * u.nsplit * u.rows * (kHeadDim + 2) + 63) / 64 * 64;
+        }
     }
+    plan->floats = floats;
 }
 
-int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &maps, const uint16_t *q, float *ws,
+// At most `slots` pairs of as many rows as a unit can have (or, with more units
+// than that, one split each, which needs none).
+size_t prefix_ws_bytes(const Common &c, const pkv_group *groups, int32_t n_groups, int nsm) {
+    const int64_t slots = std::max(1, nsm / 2);
+    int64_t most = 0;
+    int s = 0;
+    for (int32_t k = 0; k < n_groups; ++k) {
+        int64_t rows = 0;
+        for (int32_t i = 0; i < groups[k].n_seqs; ++i) rows += (int64_t)c.seq[s++].n_new * c.group;
+        most = std::max(most, std::min<int64_t>(rows, kUnitRows));
+    }
+    return static_cast<size_t>((slots * most * (kHeadDim + 2) + 64 * kMaxUnits) * 4);
+}
+
+int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &maps, const uint16_t *q, uint16_t *out, float *ws,
                   cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     if (once_per_device(attr_done, [] {
@@ -892,13 +1164,16 @@ int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &map
         return PKV_ECUDA;
     PrefixArgs a;
     a.q = q;
+    a.out = out;
     a.ws = ws;
     a.status = c.status;
-    a.n_groups = plan.n_groups;
+    a.n_units = plan.n_units;
     a.n_kv_heads = c.n_kv_heads;
     a.n_q_heads = c.n_q_heads;
     a.group = c.group;
-    std::copy(plan.group, plan.group + kMaxGroups, a.g);
+    std::copy(plan.seq, plan.seq + PKV_MAX_SEQS, a.seq);
+    std::copy(plan.group, plan.group + PKV_MAX_SEQS, a.g);
+    std::copy(plan.unit, plan.unit + kMaxUnits, a.unit);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * plan.items));
     cfg.blockDim = dim3(kThreads);
@@ -913,21 +1188,23 @@ int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &map
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     auto *const fn = c.kv_fp8 ? prefix_partial<true> : prefix_partial<false>;
-    return launch_status(cudaLaunchKernelEx(&cfg, fn, maps, a));
-}
-
-int launch_prefix_combine(const Common &c, const PrefixPlan &plan, int32_t pieces, const float *ws, const float *ws_own,
-                          uint16_t *out, cudaStream_t stream) {
-    CombineArgs a;
-    a.ws = ws;
-    a.ws_own = ws_own;
-    a.out = out;
-    a.pieces = pieces;
-    std::copy(plan.of, plan.of + PKV_MAX_SEQS, a.of);
-    std::copy(plan.group, plan.group + kMaxGroups, a.g);
+    if (cudaLaunchKernelEx(&cfg, fn, maps, a) != cudaSuccess) return PKV_ECUDA;
+    if (!plan.merge) return PKV_OK;
+    CombineArgs m;
+    m.ws = ws;
+    m.out = out;
+    m.n_groups = plan.n_groups;
+    m.n_kv_heads = c.n_kv_heads;
+    m.n_q_heads = c.n_q_heads;
+    m.group = c.group;
+    for (int i = 0; i < plan.n_groups; ++i) {
+        m.tok0[i] = plan.group[i].tok0;
+        m.unit0[i] = plan.group[i].unit0;
+    }
+    for (int i = 0; i < plan.n_units; ++i) m.unit[i] = {plan.unit[i].ws_off, plan.unit[i].rows, plan.unit[i].nsplit};
     int64_t tokens = 0;
     for (int s = 0; s < c.n_seqs; ++s) tokens += c.seq[s].n_new;
-    return launch_status(launch_pdl(prefix_combine, static_cast<unsigned>(tokens * c.n_q_heads), kCombThreads, 0, stream, c, a));
+    return launch_status(launch_pdl(prefix_combine, static_cast<unsigned>(tokens * c.n_q_heads), kCombThreads, 0, stream, m));
 }
 
 }  // namespace pkv

@@ -1199,7 +1199,7 @@ static int64_t most_keys(int32_t len, int32_t n_new, int32_t window, int32_t n_s
 // tokens of 8 heads, windows of 2,047 keys, 16 columns a CTA against 32: 8
 // streams 15.4 us against 21.7, 16 streams (512 CTAs against 256) 30.9 against
 // 25.0, 64 streams (which read twice the bytes from L2) 118 against 100.5.
-int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan, bool partials) {
+int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
     const int pieces = window_pieces(window, n_sink);
     const int tile = c.kv_fp8 ? Cfg<true>::tile : Cfg<false>::tile;
     bool split = false, wide = false, over8 = false;
@@ -1236,12 +1236,11 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan, boo
         floats = (floats + 63) / 64 * 64;
     }
     if (items * pieces > INT32_MAX) return PKV_EINVAL;
-    // calls that may run as runs of pieces (and those have to whose partials the caller merges)
-    const bool some = partials || (pieces > 1 && (split || many));
+    const bool some = pieces > 1 && (split || many);  // calls that may run as runs of pieces
     // the least cost: a cluster a split, or runs of pieces (which have to merge splits)
     const int64_t per = items ? keys / (items * pieces) : 0;  // keys of a piece
     const auto waves = [&](int run) { return (items * pieces / run + kCtas - 1) / kCtas; };
-    int64_t best = split || partials ? INT64_MAX : waves(1) * (per + kStartKeys) * 10;
+    int64_t best = split ? INT64_MAX : waves(1) * (per + kStartKeys) * 10;
     plan->run = 0;
     for (int run = 1; some && run <= pieces; run *= 2) {
         const int64_t cost = waves(run) * (run * per * (wide || (c.kv_fp8 && over8) ? 12 : 9) + kStartKeys * 10) + kCombKeys * 10;
@@ -1266,7 +1265,7 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan, boo
 
 int launch_window(const Common &c, const WindowPlan &plan, const DecodeMaps &maps, int32_t window,
                   int32_t n_sink, const uint16_t *q, uint16_t *out, float *ws, const uint16_t *k_new,
-                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool partials) {
+                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream) {
     static std::atomic<uint64_t> attr_done{0};
     if (once_per_device(attr_done, [] {
             for (int i = 0; i < 8; ++i) {
@@ -1308,7 +1307,7 @@ int launch_window(const Common &c, const WindowPlan &plan, const DecodeMaps &map
     auto *const fn = window_kernel(c.kv_fp8 != 0, !clustered, plan.wide);
     if (cudaLaunchKernelEx(&cfg, fn, c, maps, a) != cudaSuccess)
         return PKV_ECUDA;
-    if (clustered || partials) return PKV_OK;
+    if (clustered) return PKV_OK;
     return launch_status(
         launch_pdl(window_combine, static_cast<unsigned>(plan.comb), kCombThreads, 0, stream, c, a));
 }

@@ -187,6 +187,25 @@ def test_not_finite(fmt, where):
     assert int(st) & ~pkv.DEV_RANGE == 0
 
 
+@pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("ptok", [64, 20])
+@pytest.mark.parametrize("where,dim", [("k", 5), ("v", 5), ("v", 200)])
+def test_not_finite_in_an_own_row(fmt, ptok, where, dim):
+    """A stream's own row that is not finite: its outputs of that KV head are not, and no other stream's change by a bit."""
+    lay = pkv.layout(1, 2, 256, 0, fmt)
+    s = Shared(lay, [([90, 40, 33], 3), ([50, 60], 2)], [1, 2, 1, 1, 3], ptok, n_q_heads=4)
+    good = bf16_values(s.call().cpu().numpy().view(np.uint16))[:-1]
+    n = s.lens[1]
+    getattr(s, where)[1][n - 15, 0, dim] = 0x7FC0
+    pkv.store(lay, [pkv.seq(s.pgs[1], n, n)], 0, s.dev(s.k[1]), s.dev(s.v[1]))
+    st = torch().zeros(1, dtype=torch().int32, device="cuda")
+    got = bf16_values(s.call(status=st).cpu().numpy().view(np.uint16))[:-1]
+    assert np.isnan(got[1:3, :2]).any(-1).all() and int(st) & ~pkv.DEV_RANGE == 0
+    rest = np.ones(got.shape, bool)
+    rest[1:3, :2] = False
+    assert np.array_equal(got[rest], good[rest])
+
+
 def test_values_beyond_fp16_are_reported():
     lay = pkv.layout(1, 1, 256, 0)
     t = torch()
