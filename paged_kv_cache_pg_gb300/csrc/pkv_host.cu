@@ -339,7 +339,7 @@ extern "C" int pkv_store(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seq
         return PKV_EINVAL;
     auto launch = c.kv_fp8 ? launch_store8 : launch_store;
     return launch(c, tok, static_cast<const uint16_t *>(k_new), static_cast<const uint16_t *>(v_new),
-                  static_cast<const uint16_t *>(ik_new), stream);
+                  static_cast<const uint16_t *>(ik_new), stream, false);
 }
 
 extern "C" int pkv_gather(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
@@ -773,6 +773,7 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
     int nsm = 0;
     rc = sm_count(&nsm);
     if (rc) return rc;
+    plan_prefix_maps(c, L, seqs, plan, maps);
     plan_prefix(c, nsm, &plan);
     if (plan.floats > 0 &&
         (!ws || ws_bytes < static_cast<size_t>(plan.floats) * 4 || (reinterpret_cast<uintptr_t>(ws) & 255u)))
@@ -780,10 +781,9 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
     // the new rows first, into their pages: the attention's kernel streams the
     // shared rows meanwhile
     if (k_new) {
-        rc = (c.kv_fp8 ? launch_store8 : launch_store)(c, tokens, kn, vn, ikn, stream);
+        rc = (c.kv_fp8 ? launch_store8 : launch_store)(c, tokens, kn, vn, ikn, stream, true);
         if (rc) return rc;
     }
-    plan_prefix_maps(c, L, seqs, plan, maps);
     return launch_prefix(c, plan, maps, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out),
                          static_cast<float *>(ws), stream);
 }

@@ -181,11 +181,13 @@ int sm_count(int *out);
 int launch_status(cudaError_t e);
 
 // Kernel launchers (one per kernel file); all return PKV_OK or PKV_ECUDA.
+// early: the next kernel may start once all older ones are done, before the rows
+// are there (one that waits before it reads any that this one writes)
 int launch_store(const Common &c, int32_t total_tokens, const uint16_t *k_new,
-                 const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
+                 const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool early = false);
 // e4m3 format: quantize the new K and V rows, copy the indexer rows
 int launch_store8(const Common &c, int32_t total_tokens, const uint16_t *k_new,
-                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
+                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool early = false);
 // e4m3 format: codes (PKV_K, PKV_V: 256 bytes a head and row) or scales
 // (PKV_KS, PKV_VS: a float32 a head and row) of positions 0 .. len-1
 int launch_gather8(const Common &c, int32_t kind, int64_t total_rows, void *out,
@@ -295,14 +297,27 @@ struct PrefixGroup {
     int16_t map_k, map_v;  // whole K and V slots, or -1
     int16_t map_run;       // 16-row runs, or -1: key by key
 };
-struct PrefixUnit {
+// A unit as the kernel sees it, with its group's fields: one or two lines of the
+// launch parameters, whose first reads cost a CTA some 600 cycles each.
+struct alignas(128) PrefixUnit {
+    const uint16_t *layer_base;
+    int64_t ps, layer_row;
     int64_t ws_off;        // float offset of its partials in the workspace
-    int32_t group, row0, rows;
+    int32_t ptok, n_pages, shared, early, s0, n_seqs, tok0;
+    int16_t map_k, map_v, map_run;
+    int32_t row0, rows;    // of the group's
     int32_t s_first;       // stream of its first row
     int32_t keys;          // virtual keys
-    int32_t work_off;      // first item (pair of CTAs)
-    int32_t nsplit, split_tiles;
+    int32_t nsplit, per;   // splits, and what each may cost (split_tile)
 };
+// First tile of split i: a tile of shared keys only costs kSharedCost, another
+// kOwnCost; `per` is at least either, so no split is empty.
+constexpr int32_t kSharedCost = 2, kOwnCost = 3;
+__host__ __device__ inline int32_t split_tile(int32_t i, int32_t per, int32_t shared_tiles, int32_t tiles) {
+    const int64_t x = (int64_t)i * per, y = x - (int64_t)kSharedCost * shared_tiles;
+    const int64_t t = y < 0 ? x / kSharedCost : shared_tiles + y / kOwnCost;
+    return static_cast<int32_t>(t < tiles ? t : tiles);
+}
 struct PrefixPlan {
     int32_t n_groups, n_units, n_seqs;
     int32_t items;
@@ -311,6 +326,7 @@ struct PrefixPlan {
     PrefixStream seq[PKV_MAX_SEQS];
     PrefixGroup group[PKV_MAX_SEQS];
     PrefixUnit unit[kMaxUnits];
+    int32_t work_off[kMaxUnits];  // each unit's first item (pair of CTAs)
 };
 // Units, splits and workspace places of a plan that holds the groups and streams.
 void plan_prefix(const Common &c, int nsm, PrefixPlan *plan);

@@ -88,9 +88,9 @@ struct PrefixArgs {
     float *ws;
     uint32_t *status;
     int32_t n_units, n_kv_heads, n_q_heads, group;  // group: query heads of a KV head
-    PrefixStream seq[PKV_MAX_SEQS];
-    PrefixGroup g[PKV_MAX_SEQS];
+    int32_t work_off[kMaxUnits];
     PrefixUnit unit[kMaxUnits];
+    PrefixStream seq[PKV_MAX_SEQS];
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -127,6 +127,19 @@ __device__ __forceinline__ bool wait_on(uint64_t *bar, uint32_t parity, uint32_t
     return mbar_try_wait(bar, parity) || wait_long(smem_u32(bar), parity, status);
 }
 
+// A phase that is known to be over, seen with the cluster's scope.
+__device__ __forceinline__ bool mbar_acquired(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
 // A pair's work.
 struct Work {
     int u, kvh, split;
@@ -135,21 +148,22 @@ struct Work {
 };
 __device__ __forceinline__ Work work_of(const PrefixArgs &a, int item, int rank) {
     Work w;
-    w.u = find_seq(a.n_units, item, [&](int t) { return a.unit[t].work_off; });
+    w.u = find_seq(a.n_units, item, [&](int t) { return a.work_off[t]; });
     const PrefixUnit &u = a.unit[w.u];
-    const int r = item - u.work_off, half = (u.rows + 1) >> 1;
+    const int r = item - a.work_off[w.u], half = (u.rows + 1) >> 1;
     w.kvh = r / u.nsplit;
     w.split = r - w.kvh * u.nsplit;
     w.first = rank * half;
     w.count = rank ? u.rows - half : half;
-    w.key0 = w.split * u.split_tiles * kN;
-    w.key1 = min(u.keys, w.key0 + u.split_tiles * kN);
+    const int tiles = (u.keys + kN - 1) / kN, st = u.shared / kN;
+    w.key0 = split_tile(w.split, u.per, st, tiles) * kN;
+    w.key1 = min(u.keys, split_tile(w.split + 1, u.per, st, tiles) * kN);
     w.ntiles = (w.key1 - w.key0 + kN - 1) / kN;
     return w;
 }
 
 // Stream of a unit's row (its token counted from the group's first).
-__device__ __forceinline__ int stream_of(const PrefixArgs &a, const PrefixGroup &g, int tok) {
+__device__ __forceinline__ int stream_of(const PrefixArgs &a, const PrefixUnit &g, int tok) {
     return g.s0 + find_seq(g.n_seqs, g.tok0 + tok, [&](int t) { return a.seq[g.s0 + t].tok; });
 }
 
@@ -157,7 +171,7 @@ __device__ __forceinline__ int stream_of(const PrefixArgs &a, const PrefixGroup 
 // lane i keys i, i + 32, i + 64, i + 96.  Keys behind a stream's end are its last
 // one's, runs behind the unit's the tile's first.
 struct Look {
-    int64_t at[4];  // element offset of the page from layer_base
+    int id[4];      // the page
     int row[4];     // row in it
     int s, pos, n;  // run lane & 7: its stream, its first position, its keys
 };
@@ -216,12 +230,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
     tc_fence_before();
-    cluster_sync();  // both CTAs' barriers and tensor memory are there
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot, sbase = smem_u32(smem);
+    __syncthreads();  // this CTA's barriers and tensor memory are there
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    // ... and its peer's, behind this: the copies, which are the CTA's own, start before
+    auto meet = [&] {
+        asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        tc_fence_after();
+    };
+    if (warp != kWarpK && warp != kWarpV) meet();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot), sbase = smem_u32(smem);
     const Work w = work_of(a, static_cast<int>(blockIdx.x >> 1), rank);
     const PrefixUnit &u = a.unit[w.u];
-    const PrefixGroup &g = a.g[u.group];
+    const PrefixUnit &g = u;  // its group's fields
     const int H = a.n_kv_heads, G = a.group;
     // a tile of shared keys only, none behind their end: nothing to mask
     const auto all_shared = [&](int n) { return w.key0 + (n + 1) * kN <= g.shared; };
@@ -467,6 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             float other = 0.f;
             ok = wait_warp(L::o_done, w.ntiles - 1) && exchange(l, other);
             l += other;
+            // (and what the peer's converters flagged before those products)
+            ok = ok && mbar_acquired(&bars[L::o_done], (w.ntiles - 1) & 1);
             tc_fence_after();
         }
         if (ok && active) {
@@ -478,8 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             int64_t row[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) row[j] = shfl64(mine, (lane & ~3) + j);
-            // (both CTAs' converters flagged it before the products that the sums waited for)
-            asm volatile("fence.acq_rel.cluster;" ::: "memory");
             bool odd_row = false;
             if (row_ok) {
                 const int i = my - u.s_first;
@@ -547,6 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const void *const map_w = whole_map >= 0 ? &maps.map[whole_map] : nullptr;
         const uint8_t *const base = reinterpret_cast<const uint8_t *>(g.layer_base);
         const bool runs = map != nullptr;
+        if (runs && lane == 0) {
+            asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+            if (map_w) asm volatile("prefetch.tensormap [%0];" ::"l"(map_w) : "memory");
+        }
         // The unit's streams, one and another 32 behind it a lane: a search through
         // the launch parameters for each run took a tile of 64 streams 3 us
         const int pad = (g.shared + kRun - 1) / kRun * kRun, n_seqs = g.s0 + g.n_seqs - u.s_first;
@@ -588,7 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             k.n = k.s == -2 ? 0 : min(kRun, limit - k.pos);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                k.at[i] = 0;
+                k.id[i] = 0;
                 k.row[i] = 0;
                 if (runs && i > 0) continue;
                 // the key's run (behind the unit's last one: the tile's first), from its lane
@@ -599,14 +623,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int pos = runs ? first : min(first + (lane & 15), last);
                 const int page = tab ? pos / ptok : 0;
                 k.row[i] = pos - page * ptok;
-                const int id = tab ? __ldg(tab + page) : 0;
-                if (static_cast<uint32_t>(id) < static_cast<uint32_t>(n_pages)) {
-                    k.at[i] = (int64_t)id * g.ps;
-                } else if (!is_v && a.status) {
-                    atomicOr(a.status, PKV_DEV_BAD_PAGE);
-                }
+                k.id[i] = tab ? __ldg(tab + page) : 0;  // (not looked at before its tile's turn)
             }
             return k;
+        };
+        // element offset of a looked-up page from layer_base; one outside the arena is
+        // reported and read as page 0
+        auto page_at = [&](int id) -> int64_t {
+            if (static_cast<uint32_t>(id) < static_cast<uint32_t>(n_pages)) return (int64_t)id * g.ps;
+            if (!is_v && a.status) atomicOr(a.status, PKV_DEV_BAD_PAGE);
+            return 0;
         };
         // byte offset of a 16-bit or code row from layer_base
         auto row_bytes = [&](int64_t at, int row) -> int64_t {
@@ -621,10 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 int row;
                 if (runs) {
                     const int src = 2 * i + (lane >> 4);
-                    at = shfl64(k.at[0], src);
+                    at = page_at(__shfl_sync(0xffffffffu, k.id[0], src));
                     row = __shfl_sync(0xffffffffu, k.row[0], src) + (lane & 15);
                 } else {
-                    at = k.at[i];
+                    at = page_at(k.id[i]);
                     row = k.row[i];
                 }
                 s[i] = __ldg(reinterpret_cast<const float *>(base + 2 * at + off8_scale(is_v, H, ptok, w.kvh, row)));
@@ -640,6 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = -1; ok && m < w.ntiles; ++m) {
             Look next = now;
             if (m + 1 < w.ntiles) next = look(m + 1);
+            if (m == 0) {
+                __syncwarp();
+                meet();
+            }
             if (m >= 0) {
             // the slot
             const uint32_t q = kFp8 ? 2 * m + is_v : m;
@@ -650,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint64_t *const full = &bars[(kFp8 || !is_v ? L::k_full : L::v_full) + slot];
             uint8_t *const dst = smem + (kFp8 ? L::off_raw + slot * kRawBytes : (is_v ? L::off_v : L::off_k) + slot * kSlotBytes);
             if (runs) {
-                const int64_t rb = row_bytes(now.at[0], now.row[0]);
+                const int64_t rb = row_bytes(page_at(now.id[0]), now.row[0]);
                 const int y = static_cast<int>(g.layer_row + rb / (kFp8 ? 256 : 512));
                 if (lane == 0) mbar_arrive_expect_tx(full, kFp8 ? kRawBytes : kSlotBytes);
                 __syncwarp();  // the expected bytes come first
@@ -684,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // key by key: 16-byte chunks through the same swizzle
                 int64_t src[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) src[i] = row_bytes(now.at[i], now.row[i]);
+                for (int i = 0; i < 4; ++i) src[i] = row_bytes(page_at(now.id[i]), now.row[i]);
                 constexpr int kChunks = kFp8 ? 16 : 32;  // of a row
                 const int per = is_v ? kChunks / 2 : kChunks, rows_pass = 32 / per, n_rows = is_v ? 128 : 64;
                 const int c = lane % per, sub = lane / per;
@@ -769,7 +799,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // behind its stream's end
         const auto behind = [&](const int *run, int row) -> uint32_t {
             uint32_t m = 0u;
-#pragma unroll 1
+#pragma unroll
             for (int i = 0; i < 8; ++i) m |= (row >= run[16 + i] ? 1u : 0u) << i;
             return m;
         };
@@ -1082,13 +1112,29 @@ constexpr int64_t kTileCost = 140, kPairCost = 600, kPartialCost = 6, kMergeCost
 void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
     const int64_t H = c.n_kv_heads, slots = std::max(1, nsm / 2);
     plan->n_units = 0;
-    int64_t most = 1;
+    int64_t most = 1;  // cost of a unit
+    const auto cost_of = [](const PrefixUnit &u) -> int64_t {
+        const int64_t tiles = (u.keys + kN - 1) / kN, shared = u.shared / kN;
+        return shared * kSharedCost + (tiles - shared) * kOwnCost;
+    };
     for (int k = 0; k < plan->n_groups; ++k) {
         PrefixGroup &g = plan->group[k];
         g.unit0 = plan->n_units;
         for (int row0 = 0; row0 < g.rows; row0 += kUnitRows) {
             PrefixUnit &u = plan->unit[plan->n_units++];
-            u.group = k;
+            u.layer_base = g.layer_base;
+            u.ps = g.ps;
+            u.layer_row = g.layer_row;
+            u.ptok = g.ptok;
+            u.n_pages = g.n_pages;
+            u.shared = g.shared;
+            u.early = g.early;
+            u.s0 = g.s0;
+            u.n_seqs = g.n_seqs;
+            u.tok0 = g.tok0;
+            u.map_k = g.map_k;
+            u.map_v = g.map_v;
+            u.map_run = g.map_run;
             u.row0 = row0;
             u.rows = std::min(kUnitRows, g.rows - row0);
             const auto stream = [&](int row) {
@@ -1101,20 +1147,21 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
             const PrefixStream &last = plan->seq[stream(row0 + u.rows - 1)];
             const auto pad = [](int n) { return (n + kRun - 1) / kRun * kRun; };
             u.keys = pad(g.shared) + last.own + pad(last.len - g.shared) - plan->seq[u.s_first].own;
-            most = std::max<int64_t>(most, (u.keys + kN - 1) / kN);
+            most = std::max(most, cost_of(u));
         }
     }
     const auto items_of = [&](int64_t per) {
         int64_t n = 0;
-        for (int i = 0; i < plan->n_units; ++i) n += H * (((plan->unit[i].keys + kN - 1) / kN + per - 1) / per);
+        for (int i = 0; i < plan->n_units; ++i) n += H * ((cost_of(plan->unit[i]) + per - 1) / per);
         return n;
     };
     const int64_t cap = std::max(H * plan->n_units, slots);
     int64_t best = INT64_MAX, chosen = most;
     for (int64_t k = 1; k <= slots; ++k) {
-        const int64_t per = (most + k - 1) / k, items = items_of(per);
+        const int64_t per = std::max<int64_t>(std::max(kSharedCost, kOwnCost), (most + k - 1) / k), items = items_of(per);
         if (items > cap) continue;
-        const int64_t cost = (items + slots - 1) / slots * (per * kTileCost + kPairCost) + (k > 1 ? items * kPartialCost + kMergeCost : 0);
+        const int64_t cost = (items + slots - 1) / slots * (per * kTileCost / kSharedCost + kPairCost) +
+                             (k > 1 ? items * kPartialCost + kMergeCost : 0);
         if (cost < best) {
             best = cost;
             chosen = per;
@@ -1125,10 +1172,9 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
     plan->merge = false;
     for (int i = 0; i < plan->n_units; ++i) {
         PrefixUnit &u = plan->unit[i];
-        const int64_t tiles = (u.keys + kN - 1) / kN;
-        u.work_off = plan->items;
-        u.split_tiles = static_cast<int32_t>(std::min(chosen, tiles));
-        u.nsplit = static_cast<int32_t>((tiles + u.split_tiles - 1) / u.split_tiles);
+        plan->work_off[i] = plan->items;
+        u.per = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(chosen, kOwnCost), INT32_MAX));
+        u.nsplit = static_cast<int32_t>((cost_of(u) + u.per - 1) / u.per);
         u.ws_off = floats;
         plan->items += static_cast<int32_t>(H * u.nsplit);
         if (u.nsplit > 1) {
@@ -1172,8 +1218,8 @@ int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &map
     a.n_q_heads = c.n_q_heads;
     a.group = c.group;
     std::copy(plan.seq, plan.seq + PKV_MAX_SEQS, a.seq);
-    std::copy(plan.group, plan.group + PKV_MAX_SEQS, a.g);
-    std::copy(plan.unit, plan.unit + kMaxUnits, a.unit);
+    std::copy(plan.unit, plan.unit + plan.n_units, a.unit);
+    std::copy(plan.work_off, plan.work_off + plan.n_units, a.work_off);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * plan.items));
     cfg.blockDim = dim3(kThreads);
