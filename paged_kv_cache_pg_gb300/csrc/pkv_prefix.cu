@@ -102,7 +102,7 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar) {  // at the first C
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(peer_addr(bar, 0)) : "memory");
 }
 // A bounded wait as mbar_wait, in few instructions where it is called: sixteen
-// warps in nine roles share the instruction cache, and with each role's loop
+// warps in six roles share the instruction cache, and with each role's loop
 // written out at length a tile took 6,500 cycles, half of them waiting for
 // instructions.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t *status) {
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (zeros, and rows with an infinity or NaN, stay as they are)
                 const int e = ex == 0 || ex == 0xff ? 0 : max(ex - 127 - 14, -100);
                 dn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-                qs = 256.f * kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);  // (the codes' 2^-8)
+                qs = kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
             }
 #pragma unroll 1
             for (int h32 = 0; h32 < 2; ++h32) {
@@ -343,24 +343,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             const bool masked = !all_shared(n);
             const float *const scl = reinterpret_cast<const float *>(smem + L::off_scl) + slot * 3 * kN + 64 * hf;
-            if ((kFp8 || masked) && !(ok = wait_warp(L::info_full + slot, n / kInfo))) break;
-            // the keys that the row sees, a bit each: of a run of its own stream those up
-            // to its position, of a shared run those there are
-            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
-            bool any = true;
-            if (masked) {
-                see[0] = see[1] = 0u;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int *const run = info + slot * 24 + 4 * hf + k;
-                    const int keys = min(run[16], run[0] == -1 ? kRun : run[0] == my ? qpos - run[8] + 1 : 0);
-                    see[k >> 1] |= (keys > 0 ? (1u << keys) - 1u : 0u) << (16 * (k & 1));
-                }
-                any = __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
-            }
+            // (S is read before anything else is looked at: the next S product waits for it)
             float x[64];
-            if (any) {
-                tc_fence_after();
+            tc_fence_after();
+            {
                 uint32_t sv[64];
                 tmem_ld64(lane_base + kSCol + 64 * hf, sv);
 #pragma unroll
@@ -369,6 +355,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) arrive_first(&bars[L::s_empty]);
+            if ((kFp8 || masked) && !(ok = wait_warp(L::info_full + slot, n / kInfo))) break;
+            // the keys that the row sees, a bit each: of a run of its own stream those up
+            // to its position, of a shared run those there are
+            uint32_t see[2] = {0xffffffffu, 0xffffffffu};
+            bool any = true;
+            if (masked) {
+                const int4 *const run = reinterpret_cast<const int4 *>(info + slot * 24) + hf;
+                const int4 s4 = run[0], p4 = run[2], n4 = run[4];  // streams, positions, keys of the half's four runs
+                const auto bits = [&](int st, int pos, int keys) -> uint32_t {
+                    const int k = min(keys, st == -1 ? kRun : st == my ? qpos - pos + 1 : 0);
+                    return k > 0 ? (1u << k) - 1u : 0u;
+                };
+                see[0] = bits(s4.x, p4.x, n4.x) | (bits(s4.y, p4.y, n4.y) << 16);
+                see[1] = bits(s4.z, p4.z, n4.z) | (bits(s4.w, p4.w, n4.w) << 16);
+                any = __any_sync(0xffffffffu, (see[0] | see[1]) != 0u);
+            }
             if (kFp8 && any) {
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 odd_row = (reinterpret_cast<volatile uint32_t *>(bad)[i >> 5] >> (i & 31)) & 1u;
             }
             if (odd_row) l = __uint_as_float(0x7fffffffu);
-            const float inv = (kFp8 ? 256.f : 1.f) / l;
+            const float inv = 1.f / l;
             float2 odd = make_float2(0.f, 0.f);  // NaN once a sum is not finite
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
@@ -536,13 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int h = 0; h < 2; ++h) {
                         uint4 v[4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t e[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                e[k] = kFp8 ? __float_as_uint(256.f * __uint_as_float(o[16 * h + 4 * j + k])) : o[16 * h + 4 * j + k];
-                            v[j] = make_uint4(e[0], e[1], e[2], e[3]);
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            v[j] = make_uint4(o[16 * h + 4 * j], o[16 * h + 4 * j + 1], o[16 * h + 4 * j + 2], o[16 * h + 4 * j + 3]);
                         quad_transpose(v, lane);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -804,6 +801,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             return m;
         };
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        // of eight fp16 values, the largest magnitudes' bits of the four low and the four
+        // high halves
+        const auto largest = [](const uint4 &v) {
+            return __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        };
+        const auto not_finite = [](uint32_t m) { return (m & 0xffffu) >= 0x7c00u || (m >> 16) >= 0x7c00u; };
         if constexpr (!kFp8) {
             for (int n = 0; ok && n < w.ntiles; ++n) {
                 const int slot = n % L::slots;
@@ -824,17 +827,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (none & (1u << ((i + j) & 7))) x[j] = zero;
                         const uint4 y = make_uint4(pack_f16(bf16_lo(x[j].x), bf16_hi(x[j].x)), pack_f16(bf16_lo(x[j].y), bf16_hi(x[j].y)),
                                                    pack_f16(bf16_lo(x[j].z), bf16_hi(x[j].z)), pack_f16(bf16_lo(x[j].w), bf16_hi(x[j].w)));
-                        top = __vmaxu2(top, __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu)));
+                        if (masked) top = __vmaxu2(top, largest(y));
                         v[(i + j) * 128] = y;
                     }
                 }
-                if (masked && ((top & 0xffffu) >= 0x7c00u || (top >> 16) >= 0x7c00u)) {
+                if (masked && not_finite(top)) {
                     // something is not finite: chunks of own rows that have it become zeros
 #pragma unroll 1
                     for (int i = 0; i < 16; ++i) {
-                        const uint4 y = v[i * 128];
-                        const uint32_t m = __vmaxu2(__vmaxu2(y.x & 0x7fff7fffu, y.y & 0x7fff7fffu), __vmaxu2(y.z & 0x7fff7fffu, y.w & 0x7fff7fffu));
-                        if (run[i & 7] >= 0 && ((m & 0xffffu) >= 0x7c00u || (m >> 16) >= 0x7c00u)) {
+                        if (run[i & 7] >= 0 && not_finite(largest(v[i * 128]))) {
                             v[i * 128] = zero;
                             flag(run[i & 7]);
                         }
@@ -849,90 +850,50 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } else {
-            // A code's bits shifted into fp16's fields are its value times 2^-8,
-            // subnormals too, but for the NaN code 0x7f (looked for beside, and put in
-            // by a second pass where there is one).  The factor goes into the scores'
-            // scale and the sums.  (cvt.rn.f16x2.e4m3x2 took 8,900 cycles a tile.)
-            const auto widen = [](uint32_t four, uint32_t &lo, uint32_t &hi) {
-                const uint32_t a0 = __byte_perm(four, 0u, 0x1404), a1 = __byte_perm(four, 0u, 0x3424);
-                lo = (a0 & 0x80008000u) | ((a0 >> 1) & 0x3f803f80u);
-                hi = (a1 & 0x80008000u) | ((a1 >> 1) & 0x3f803f80u);
-            };
-            const auto has_nan = [](const uint4 &x) -> uint32_t {
-                return (((x.x & 0x7f7f7f7fu) + 0x01010101u) | ((x.y & 0x7f7f7f7fu) + 0x01010101u) | ((x.z & 0x7f7f7f7fu) + 0x01010101u) |
-                        ((x.w & 0x7f7f7f7fu) + 0x01010101u)) & 0x80808080u;
-            };
+            // Eight lanes take four chunks of 16 codes of rows r and r + 4: both the reads
+            // and the writes (one order each for the two rows) then touch every bank
+            // once.  A thread's chunks are the same one of every 8th (K) or 16th (V) row.
             const int odd = (t >> 2) & 1;
             for (int q = 0; ok && q < 2 * w.ntiles; ++q) {
                 const int n = q >> 1, slot = n % L::slots, raw = q % L::raw;
                 const bool is_v = q & 1;
                 if (!(ok = wait_warp(L::k_full + raw, q / L::raw))) break;
                 if (n >= L::slots && !(ok = wait_warp((is_v ? L::v_free : L::k_free) + slot, n / L::slots - 1))) break;
-                const uint8_t *const src = smem + L::off_raw + raw * kRawBytes;
-                uint8_t *const dst = smem + (is_v ? L::off_v : L::off_k) + slot * kSlotBytes;
                 const bool masked = is_v && !all_shared(n);
                 if (masked && !(ok = wait_warp(L::info_full + n % kInfo, n / kInfo))) break;
-                const int *const run = info + n % kInfo * 24;  // V: chunk i of a thread lies in run i
-                // eight lanes take four chunks of 16 codes of rows r and r + 4: both
-                // the reads and the writes (one order each for the two rows) then
-                // touch every bank once
-                const int quads = is_v ? 2 : 4, plane = is_v ? 0 : 8192, region = is_v ? kVRegion : kKRegion;
-                const auto where = [&](int i, int &c, int &r) {
-                    const int unit = i * 16 + (t >> 3), p = unit / quads;
-                    c = 4 * (unit - p * quads) + (t & 3);
-                    r = (p >> 2) * 8 + (p & 3) + 4 * odd;
-                };
-                const auto from = [&](int c, int r) {
-                    return reinterpret_cast<const uint4 *>(src + (c >> 3) * plane + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-                };
-                const auto put = [&](int c, int r, const uint4 &y0, const uint4 &y1) {
-                    uint8_t *const to = dst + (c >> 2) * region + r * 128;
-                    const int c0 = (2 * c) & 7;
-                    *reinterpret_cast<uint4 *>(to + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? y1 : y0;
-                    *reinterpret_cast<uint4 *>(to + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? y0 : y1;
-                };
-                uint32_t none = 0u, nan = 0u;
-                if (masked) {
-                    int c, r;
-                    where(0, c, r);  // (a thread's rows are the same one of every run)
-                    none = behind(run, r);
-                }
+                const int *const run = info + n % kInfo * 24;  // V: a thread's chunk i lies in run i
+                const int c = 4 * ((t >> 3) & (is_v ? 1 : 3)) + (t & 3), c0 = (2 * c) & 7;
+                const int r = (is_v ? ((t >> 6) << 3) + ((t >> 4) & 3) : t >> 5) + 4 * odd, step = is_v ? 2048 : 1024;
+                const uint8_t *const src = smem + L::off_raw + raw * kRawBytes + (c >> 3) * 8192 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                uint8_t *const dst = smem + (is_v ? L::off_v + (c >> 2) * kVRegion : L::off_k + (c >> 2) * kKRegion) + slot * kSlotBytes + r * 128;
+                uint8_t *const to0 = dst + (((c0 + odd) ^ (r & 7)) << 4), *const to1 = dst + (((c0 + 1 - odd) ^ (r & 7)) << 4);
+                const uint32_t none = masked ? behind(run, r) : 0u;
+                uint32_t top = 0u;  // the largest magnitude's bits
 #pragma unroll 1
                 for (int i = 0; i < 8; i += 4) {
                     uint4 x[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        int c, r;
-                        where(i + j, c, r);
-                        x[j] = *from(c, r);
-                    }
+                    for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (i + j) * step);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        int c, r;
-                        where(i + j, c, r);
                         if (none & (1u << (i + j))) x[j] = zero;
                         uint4 y0, y1;
-                        widen(x[j].x, y0.x, y0.y);
-                        widen(x[j].y, y0.z, y0.w);
-                        widen(x[j].z, y1.x, y1.y);
-                        widen(x[j].w, y1.z, y1.w);
-                        nan |= has_nan(x[j]);
-                        put(c, r, y0, y1);
+                        f16_of_codes(x[j].x, y0.x, y0.y);
+                        f16_of_codes(x[j].y, y0.z, y0.w);
+                        f16_of_codes(x[j].z, y1.x, y1.y);
+                        f16_of_codes(x[j].w, y1.z, y1.w);
+                        if (masked) top = __vmaxu2(top, __vmaxu2(largest(y0), largest(y1)));
+                        *reinterpret_cast<uint4 *>(to0 + (i + j) * step) = odd ? y1 : y0;
+                        *reinterpret_cast<uint4 *>(to1 + (i + j) * step) = odd ? y0 : y1;
                     }
                 }
-                if (nan) {
+                if (masked && not_finite(top)) {
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
-                        int c, r;
-                        where(i, c, r);
-                        const uint4 z = *from(c, r);
-                        if (!has_nan(z) || (masked && (r & 15) >= run[16 + i])) continue;
-                        if (masked && run[i] >= 0) {
-                            put(c, r, zero, zero);
+                        uint4 *const y0 = reinterpret_cast<uint4 *>(to0 + i * step), *const y1 = reinterpret_cast<uint4 *>(to1 + i * step);
+                        if (run[i] >= 0 && not_finite(__vmaxu2(largest(*y0), largest(*y1)))) {
+                            *y0 = *y1 = zero;
                             flag(run[i]);
-                        } else {  // (NaN for the whole chunk's row: K's score, V's 16 dims)
-                            const uint4 no = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
-                            put(c, r, no, no);
                         }
                     }
                 }
