@@ -39,9 +39,8 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const __grid_constant__
                                                          int32_t total_tokens,
                                                          const uint16_t *__restrict__ k_new,
                                                          const uint16_t *__restrict__ v_new,
-                                                         const uint16_t *__restrict__ ik_new, bool early) {
+                                                         const uint16_t *__restrict__ ik_new) {
     pdl_wait();
-    if (early && threadIdx.x == 0) pdl_trigger();
     const int H = c.n_kv_heads;
     constexpr int row_chunks = kHeadDim / kChunk;  // 32
     const int kv_chunks = 2 * H * row_chunks;
@@ -191,9 +190,8 @@ __global__ void __launch_bounds__(kThreads) store8_kernel(const __grid_constant_
                                                           int64_t total_items,
                                                           const uint16_t *__restrict__ k_new,
                                                           const uint16_t *__restrict__ v_new,
-                                                          const uint16_t *__restrict__ ik_new, bool early) {
+                                                          const uint16_t *__restrict__ ik_new) {
     pdl_wait();
-    if (early && threadIdx.x == 0) pdl_trigger();
     const int H = c.n_kv_heads, lane = threadIdx.x & 31;
     const int per_tok = 2 * H + (c.idx_dim ? 1 : 0);
     const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
@@ -279,10 +277,10 @@ unsigned grid_for(int64_t work) {
 }  // namespace
 
 int launch_store(const Common &c, int32_t total_tokens, const uint16_t *k_new,
-                 const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool early) {
+                 const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream) {
     // a warp a token
     return launch_status(launch_pdl(store_kernel, grid_for((int64_t)total_tokens * 32), kThreads,
-                                    0, stream, c, total_tokens, k_new, v_new, ik_new, early));
+                                    0, stream, c, total_tokens, k_new, v_new, ik_new));
 }
 
 int launch_gather(const Common &c, int32_t kind, int64_t total_rows, uint16_t *out,
@@ -297,10 +295,10 @@ int launch_gather(const Common &c, int32_t kind, int64_t total_rows, uint16_t *o
 }
 
 int launch_store8(const Common &c, int32_t total_tokens, const uint16_t *k_new,
-                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool early) {
+                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream) {
     const int64_t items = (int64_t)total_tokens * (2 * c.n_kv_heads + (c.idx_dim ? 1 : 0));
     return launch_status(launch_pdl(store8_kernel, grid_for(items * 32), kThreads, 0, stream, c,
-                                    items, k_new, v_new, ik_new, early));
+                                    items, k_new, v_new, ik_new));
 }
 
 int launch_gather8(const Common &c, int32_t kind, int64_t total_rows, void *out,

@@ -339,7 +339,7 @@ extern "C" int pkv_store(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seq
         return PKV_EINVAL;
     auto launch = c.kv_fp8 ? launch_store8 : launch_store;
     return launch(c, tok, static_cast<const uint16_t *>(k_new), static_cast<const uint16_t *>(v_new),
-                  static_cast<const uint16_t *>(ik_new), stream, false);
+                  static_cast<const uint16_t *>(ik_new), stream);
 }
 
 extern "C" int pkv_gather(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs, int32_t layer,
@@ -781,7 +781,14 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
     // the new rows first, into their pages: the attention's kernel streams the
     // shared rows meanwhile
     if (k_new) {
-        rc = (c.kv_fp8 ? launch_store8 : launch_store)(c, tokens, kn, vn, ikn, stream, true);
+        RopeRows r;
+        std::memset(&r, 0, sizeof(r));
+        r.k = kn;
+        r.v = vn;
+        r.ik = ikn;
+        r.k_stride = r.v_stride = (int64_t)L->n_kv_heads * kHeadDim;
+        r.ik_stride = L->idx_dim;
+        rc = launch_rope_store(c, tokens, nullptr, r, stream, true);
         if (rc) return rc;
     }
     return launch_prefix(c, plan, maps, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out),

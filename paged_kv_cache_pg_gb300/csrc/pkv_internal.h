@@ -181,13 +181,11 @@ int sm_count(int *out);
 int launch_status(cudaError_t e);
 
 // Kernel launchers (one per kernel file); all return PKV_OK or PKV_ECUDA.
-// early: the next kernel may start once all older ones are done, before the rows
-// are there (one that waits before it reads any that this one writes)
 int launch_store(const Common &c, int32_t total_tokens, const uint16_t *k_new,
-                 const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool early = false);
+                 const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 // e4m3 format: quantize the new K and V rows, copy the indexer rows
 int launch_store8(const Common &c, int32_t total_tokens, const uint16_t *k_new,
-                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream, bool early = false);
+                  const uint16_t *v_new, const uint16_t *ik_new, cudaStream_t stream);
 // e4m3 format: codes (PKV_K, PKV_V: 256 bytes a head and row) or scales
 // (PKV_KS, PKV_VS: a float32 a head and row) of positions 0 .. len-1
 int launch_gather8(const Common &c, int32_t kind, int64_t total_rows, void *out,
@@ -244,8 +242,11 @@ struct RopeRows {
     const int32_t *pos;  // device positions of the tokens, or null: their places in the cache
     int64_t q_stride, q_out_stride, k_stride, v_stride, ik_stride;  // elements from token to token
 };
-int launch_rope_store(const Common &c, int32_t total_tokens, const pkv_rope &rope, const RopeRows &r,
-                      cudaStream_t stream);
+// rope null: keys are stored as they are.  early: the next kernel may start once
+// all older ones are done, before the rows are there (one that waits before it
+// reads any that this one writes).
+int launch_rope_store(const Common &c, int32_t total_tokens, const pkv_rope *rope, const RopeRows &r, cudaStream_t stream,
+                      bool early);
 // rows of 256 or 128 elements (r.q to r.q_out only), c.n_q_heads of them a token
 int launch_rope_rows(const Common &c, int32_t total_tokens, const pkv_rope &rope, const RopeRows &r, int32_t dim,
                      cudaStream_t stream);

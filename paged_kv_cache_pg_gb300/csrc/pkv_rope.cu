@@ -7,14 +7,16 @@
 // (a signed fraction of a half turn) go to sincospif.  In float32 radians a
 // position of 10^6 would leave 0.03 of the fastest pair's angle to chance.
 //
-// A CTA takes one token, or four of large calls, and computes each token's
-// cosines and sines once, into shared memory, for all of its heads (16 query
-// rows and 2 key rows use the same 32 to 128 pairs); with positions from the
-// launch parameters that happens before the grid-dependency wait.  A warp then
-// takes a row of 256 elements (two rows of 128), a lane 16 bytes of it; the
-// other elements of a lane's pairs (PKV_ROPE_HALF) are a second 16-byte load of
-// the row, which L1 has, or eight scalar ones where half of rot_dim is not a
-// multiple of 8.  Values and indexer rows are copied by the same warps.
+// A CTA takes one token, or up to four of large calls.  It finds each token's
+// stream, page and row once, by one thread (the streams' first tokens lie together
+// in the launch parameters: read from the streams' own records, 64 of them took 6
+// us of a call), and computes its cosines and sines once, into shared memory, for
+// all of its heads (16 query rows and 2 key rows use the same 32 to 128 pairs);
+// with positions from the launch parameters that happens before the
+// grid-dependency wait.  The tokens' rows come by bulk copies, all at once: held
+// in registers, two rows a warp in flight, a prompt took 47 us.  A warp then takes
+// a row of 256 elements (two of 128) at a time, a lane 16 bytes of it and, with
+// PKV_ROPE_HALF, the 16 bytes of its pairs' other elements.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -28,6 +30,7 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = kHeadDim / 2;
 constexpr int kBlockTokens = 4;  // of a CTA of large calls
+constexpr int kSegHeads = 64;    // query heads of a CTA
 
 // Cosine and sine of position p at one pair's frequency, times the scale.
 __device__ __forceinline__ float2 turn(uint64_t turns, int32_t p, float scale) {
@@ -47,165 +50,252 @@ __device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
     return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
 }
 
-// Elements 8 ch .. 8 ch + 7 of `row`, rotated, as float32.  cs: the token's
-// (cosine, sine) pairs.  Plain loads: the row may be rotated in place.
-__device__ __forceinline__ void rotated(const uint16_t *row, int ch, int rot, int interleaved, const float2 *cs,
-                                        float (&x)[8]) {
-    widen(*(reinterpret_cast<const uint4 *>(row) + ch), x);
-    const int e0 = 8 * ch, half = rot >> 1;
-    if (e0 >= rot) return;
-    if (interleaved) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2)
-            if (e0 + e < rot) {
-                const float2 t = cs[(e0 + e) >> 1];
-                const float a = x[e], b = x[e + 1];
-                x[e] = a * t.x - b * t.y;
-                x[e + 1] = b * t.x + a * t.y;
-            }
-    } else if ((half & 7) == 0) {
-        const bool first = e0 < half;
-        float y[8];
-        widen(*(reinterpret_cast<const uint4 *>(row) + (first ? ch + (half >> 3) : ch - (half >> 3))), y);
-        const float2 *const t = cs + (first ? e0 : e0 - half);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * t[e].x + (first ? -y[e] : y[e]) * t[e].y;
-    } else {
+// How a rope's pairs lie in a lane's 16 bytes of a row (chunk ch), known when
+// compiled: pairs inside it; their other elements 16 bytes of the same row; or
+// (rot_dim, or half of it, not a multiple of 8) anywhere.
+enum Mode { kStill, kInside, kApart, kAnyhow };
+int mode_of(const pkv_rope &r) {
+    return r.pairs == PKV_ROPE_INTERLEAVED ? (r.rot_dim % 8 == 0 ? kInside : kAnyhow) : (r.rot_dim % 16 == 0 ? kApart : kAnyhow);
+}
+
+// A lane's part in turning a token's rows: its elements' cosines, and the sines
+// with the sign they take, in registers over all of the token's rows.
+template <int kMode>
+struct Turner {
+    float c[8], s[8];
+    int ch, other, rot, inter;
+    bool on;  // some of its elements turn
+
+    __device__ __forceinline__ Turner(const float2 *cs, int chunk, const pkv_rope &r) {
+        ch = chunk;
+        rot = r.rot_dim;
+        inter = r.pairs;
+        const int half = rot >> 1, e0 = 8 * ch;
+        on = kMode != kStill && e0 < rot;
+        other = e0 < half ? ch + (half >> 3) : ch - (half >> 3);
+        if (!on) return;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             const int i = e0 + e;
-            if (i >= rot) continue;
-            const bool first = i < half;
-            const float y = __uint_as_float(static_cast<uint32_t>(row[first ? i + half : i - half]) << 16);
-            const float2 t = cs[first ? i : i - half];
-            x[e] = x[e] * t.x + (first ? -y : y) * t.y;
+            const bool first = kMode == kInside || (kMode == kAnyhow && inter) ? !(e & 1) : i < half;
+            const int pair = kMode == kInside || (kMode == kAnyhow && inter) ? i >> 1 : first ? i : i - half;
+            const float2 w = kMode != kAnyhow || i < rot ? cs[pair] : make_float2(1.f, 0.f);
+            c[e] = w.x;
+            s[e] = first ? -w.y : w.y;
         }
     }
+    // Its elements of a row (in shared memory), turned, as float32.
+    __device__ __forceinline__ void turn_row(const uint16_t *row, float (&x)[8]) const {
+        widen(*(reinterpret_cast<const uint4 *>(row) + ch), x);
+        if (!on) return;
+        float y[8];
+        if constexpr (kMode == kApart) {
+            widen(*(reinterpret_cast<const uint4 *>(row) + other), y);
+        } else if constexpr (kMode == kInside) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = x[e ^ 1];
+        } else {
+            const int half = rot >> 1;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = 8 * ch + e, j = inter ? i ^ 1 : i < half ? i + half : i - half;
+                y[e] = i < rot ? __uint_as_float(static_cast<uint32_t>(row[j]) << 16) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            if (kMode != kAnyhow || 8 * ch + e < rot) x[e] = x[e] * c[e] + y[e] * s[e];
+    }
+};
+
+// The streams' first tokens, and how the launch is cut.
+struct RopeTokens {
+    int32_t tok_off[PKV_MAX_SEQS];
+    int32_t total, block;  // tokens, and those of a CTA
+    int32_t segs;          // CTAs of a token: kSegHeads query heads each
+    int32_t bytes;         // of a token's rows in shared memory
+};
+// A CTA's token as its rows need it.
+struct TokenAt {
+    uint16_t *page;     // its page of the layer, or null (outside the arena)
+    int32_t row, ptok;  // its row there, positions of a page
+    int32_t pos;        // what its rows turn by
+};
+
+// Stream of a token: the streams' first tokens are compared by a warp's lanes.
+__device__ __forceinline__ int stream_of(const Common &c, const RopeTokens &tk, int32_t tok) {
+    return find_seq(c.n_seqs, tok, [&](int t) { return tk.tok_off[t]; });
 }
 
-// The tables of a CTA's tokens.
-__device__ __forceinline__ void fill_turns(const Common &c, const pkv_rope &rope, const int32_t *pos, int32_t tok0, int n,
-                                           float2 *cs) {
+// The cosines and sines of n tokens.
+__device__ __forceinline__ void fill_turns(const pkv_rope &rope, const TokenAt *at, int n, float2 *cs) {
     const int pairs = rope.rot_dim >> 1;
     for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
-        const int k = i / pairs, j = i - k * pairs, tok = tok0 + k;
-        int32_t p;
-        if (pos) {
-            p = __ldg(pos + tok);
-        } else {
-            const int s = find_seq(c.n_seqs, tok, [&](int t) { return c.seq[t].tok_off; });
-            p = c.seq[s].len - c.seq[s].n_new + (tok - c.seq[s].tok_off);
-        }
-        cs[k * kMaxPairs + j] = turn(rope.turns[j], p, rope.scale);
+        const int k = i / pairs, j = i - k * pairs;
+        cs[k * kMaxPairs + j] = turn(rope.turns[j], at[k].pos, rope.scale);
     }
-    __syncthreads();
 }
 
-// Rows of kDim elements, c.n_q_heads a token, per CTA `block` tokens.
-template <int kDim>
+// Rows of kDim elements, c.n_q_heads a token.
+template <int kDim, int kMode>
 __global__ void __launch_bounds__(kThreads)
     rope_rows(const __grid_constant__ Common c, const __grid_constant__ pkv_rope rope, const __grid_constant__ RopeRows r,
-              int32_t total_tokens, int32_t block) {
-    __shared__ float2 cs[kBlockTokens * kMaxPairs];
+              const __grid_constant__ RopeTokens tk) {
+    extern __shared__ __align__(16) uint8_t smem[];  // each token's rows
+    __shared__ __align__(16) float2 cs[kBlockTokens * kMaxPairs];
+    __shared__ TokenAt at[kBlockTokens];
+    __shared__ uint64_t full;
     constexpr int kChunks = kDim / 8, kRowsWarp = 32 / kChunks;
-    const int32_t tok0 = blockIdx.x * block;
-    const int n = min(block, total_tokens - tok0);
+    const int group = blockIdx.x / tk.segs, seg = blockIdx.x - group * tk.segs;
+    const int32_t tok0 = group * tk.block, head0 = seg * kSegHeads;
+    const int n = min(tk.block, tk.total - tok0), heads = min(kSegHeads, c.n_q_heads - head0);
+    if (threadIdx.x == 0) {
+        mbar_init(&full, 1);
+        fence_mbar_init();
+    }
     if (r.pos) pdl_wait();
-    fill_turns(c, rope, r.pos, tok0, n, cs);
-    if (!r.pos) pdl_wait();
-    if (threadIdx.x == 0) pdl_trigger();  // nothing here is read before a grid-dependency wait
-    const int lane = threadIdx.x & 31, ch = lane % kChunks, sub = lane / kChunks;
-    const int rows = n * c.n_q_heads;
-    for (int i = (threadIdx.x >> 5) * kRowsWarp; i < rows; i += kWarps * kRowsWarp) {
-        const int at = i + sub, k = at / c.n_q_heads, h = at - k * c.n_q_heads;
+    if (threadIdx.x < n) {
+        const int tok = tok0 + threadIdx.x;
+        if (r.pos) {
+            at[threadIdx.x].pos = __ldg(r.pos + tok);
+        } else {
+            const int s = stream_of(c, tk, tok);
+            at[threadIdx.x].pos = c.seq[s].len - c.seq[s].n_new + (tok - tk.tok_off[s]);
+        }
+    }
+    __syncthreads();
+    if (!r.pos && tk.block == 1) fill_turns(rope, at, n, cs);  // a small call's, beside the kernel before
+    pdl_wait();
+    if (threadIdx.x == 0) {
+        pdl_trigger();  // nothing here is read before a grid-dependency wait
+        const uint64_t pol = policy_evict_first();
+        mbar_arrive_expect_tx(&full, n * heads * kDim * 2);
+        for (int k = 0; k < n; ++k)
+            bulk_g2s(smem + k * tk.bytes, r.q + (tok0 + k) * r.q_stride + (int64_t)head0 * kDim, heads * kDim * 2, &full, pol);
+    }
+    if (r.pos || tk.block > 1) fill_turns(rope, at, n, cs);
+    __syncthreads();
+    const int lane = threadIdx.x & 31, ch = lane % kChunks, sub = lane / kChunks, ways = kWarps / tk.block;
+    const int warp = threadIdx.x >> 5, k = warp / ways, first = warp - k * ways;
+    if (!mbar_wait(&full, 0, c.status) || k >= n) return;
+    const Turner<kMode> t(cs + k * kMaxPairs, ch, rope);
+    const uint16_t *const rows = reinterpret_cast<const uint16_t *>(smem + k * tk.bytes);
+    uint16_t *const dst = r.q_out + (tok0 + k) * r.q_out_stride + (int64_t)head0 * kDim;
+    for (int h = first * kRowsWarp + sub; h < heads; h += ways * kRowsWarp) {
         float x[8];
-        if (at < rows)
-            rotated(r.q + (tok0 + k) * r.q_stride + h * kDim, ch, rope.rot_dim, rope.pairs, cs + k * kMaxPairs, x);
-        __syncwarp();  // every lane of the row has read what it turns, which may be in place
-        if (at < rows)
-            *(reinterpret_cast<uint4 *>(r.q_out + (tok0 + k) * r.q_out_stride + h * kDim) + ch) = narrow(x);
+        t.turn_row(rows + h * kDim, x);
+        *(reinterpret_cast<uint4 *>(dst + h * kDim) + ch) = narrow(x);
     }
 }
 
-// A token's rows: its queries (when given), keys, values, indexer row.
-template <bool kFp8>
+// A token's rows: its queries (when given), keys, values, indexer row.  kStill:
+// the keys are stored as they are (and there are no queries).  early: the next
+// kernel may start once all older ones are done, before the rows are there.
+template <bool kFp8, int kMode>
 __global__ void __launch_bounds__(kThreads)
     rope_store(const __grid_constant__ Common c, const __grid_constant__ pkv_rope rope, const __grid_constant__ RopeRows r,
-               int32_t total_tokens, int32_t block) {
-    __shared__ float2 cs[kBlockTokens * kMaxPairs];
-    const int32_t tok0 = blockIdx.x * block;
-    const int n = min(block, total_tokens - tok0);
-    const int H = c.n_kv_heads, nq = r.q ? c.n_q_heads : 0;
-    const int per = nq + 2 * H + (c.idx_dim ? 1 : 0);
+               const __grid_constant__ RopeTokens tk, bool early) {
+    extern __shared__ __align__(16) uint8_t smem[];  // each token's rows: queries, K and V heads, indexer row
+    __shared__ __align__(16) float2 cs[kMode != kStill ? kBlockTokens * kMaxPairs : 1];
+    __shared__ TokenAt at[kBlockTokens];
+    __shared__ uint64_t full;
+    const int group = blockIdx.x / tk.segs, seg = blockIdx.x - group * tk.segs;
+    const int32_t tok0 = group * tk.block, head0 = seg * kSegHeads;
+    const int n = min(tk.block, tk.total - tok0), H = c.n_kv_heads;
+    const int nq = kMode != kStill && r.q ? min(kSegHeads, c.n_q_heads - head0) : 0, nkv = seg == 0 ? 2 * H : 0;
+    const int idx = seg == 0 ? c.idx_dim : 0;
+    if (threadIdx.x == 0) {
+        mbar_init(&full, 1);
+        fence_mbar_init();
+    }
     if (r.pos) pdl_wait();
-    fill_turns(c, rope, r.pos, tok0, n, cs);
-    if (!r.pos) pdl_wait();
-    const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < n * per; i += kWarps) {
-        const int k = i / per;
-        int row = i - k * per;
-        const int64_t tok = tok0 + k;
-        const float2 *const t = cs + k * kMaxPairs;
-        float x[8];
-        if (row < nq) {
-            rotated(r.q + tok * r.q_stride + row * kHeadDim, lane, rope.rot_dim, rope.pairs, t, x);
-            __syncwarp();  // as in rope_rows
-            *(reinterpret_cast<uint4 *>(r.q_out + tok * r.q_out_stride + row * kHeadDim) + lane) = narrow(x);
-            continue;
-        }
-        row -= nq;
-        const int s = find_seq(c.n_seqs, tok0 + k, [&](int t) { return c.seq[t].tok_off; });
+    if (threadIdx.x < n) {
+        const int tok = tok0 + threadIdx.x, s = stream_of(c, tk, tok);
         const SeqDev &sd = c.seq[s];
-        // every lane reads the table's entry (one address); one reports it
-        int32_t in_page;
-        int64_t page = 0;
-        const int32_t place = sd.len - sd.n_new + (tok0 + k - sd.tok_off);
-        if (sd.table) {
-            const int32_t p = place / sd.ptok;
-            in_page = place - p * sd.ptok;
-            const int32_t id = __ldg(sd.table + p);
-            if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(sd.n_pages)) {
-                if (lane == 0 && c.status) atomicOr(c.status, PKV_DEV_BAD_PAGE);
+        TokenAt t;
+        const int32_t place = sd.len - sd.n_new + (tok - tk.tok_off[s]);
+        t.ptok = sd.ptok;
+        t.pos = r.pos ? __ldg(r.pos + tok) : place;
+        t.page = const_cast<uint16_t *>(sd.layer_base);
+        t.row = place;
+        if (sd.table && seg == 0) {
+            const int32_t p = place / sd.ptok, id = __ldg(sd.table + p);
+            t.row = place - p * sd.ptok;
+            if (static_cast<uint32_t>(id) < static_cast<uint32_t>(sd.n_pages)) {
+                t.page += (int64_t)id * sd.ps;
+            } else {
+                t.page = nullptr;
+                if (c.status) atomicOr(c.status, PKV_DEV_BAD_PAGE);
+            }
+        }
+        at[threadIdx.x] = t;
+    }
+    __syncthreads();
+    const bool before = kMode != kStill && !r.pos && tk.block == 1;  // a small call's turns, beside the kernel before
+    if (before) fill_turns(rope, at, n, cs);
+    pdl_wait();
+    if (threadIdx.x < 32) {
+        if (early && threadIdx.x == 0) pdl_trigger();
+        const uint64_t pol = policy_evict_first();
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&full, n * ((nq + nkv) * kHeadDim + idx) * 2);
+        __syncwarp();
+        const int k = threadIdx.x >> 2, part = threadIdx.x & 3;  // four parts a token
+        if (k < n) {
+            const int64_t tok = tok0 + k;
+            uint8_t *const to = smem + k * tk.bytes;
+            const int kv = nkv / 2 * kHeadDim * 2;  // bytes of the keys, or the values
+            if (part == 0 && nq) bulk_g2s(to, r.q + tok * r.q_stride + (int64_t)head0 * kHeadDim, nq * kHeadDim * 2, &full, pol);
+            if (part == 1 && kv) bulk_g2s(to + nq * kHeadDim * 2, r.k + tok * r.k_stride, kv, &full, pol);
+            if (part == 2 && kv) bulk_g2s(to + nq * kHeadDim * 2 + kv, r.v + tok * r.v_stride, kv, &full, pol);
+            if (part == 3 && idx) bulk_g2s(to + nq * kHeadDim * 2 + 2 * kv, r.ik + tok * r.ik_stride, idx * 2, &full, pol);
+        }
+    }
+    if (kMode != kStill && !before) fill_turns(rope, at, n, cs);
+    __syncthreads();
+    // a CTA's warps share its tokens out: eight, or fewer, to each, which take its rows in turn
+    const int lane = threadIdx.x & 31, ways = kWarps / tk.block, warp = threadIdx.x >> 5, k = warp / ways, first = warp - k * ways;
+    if (mbar_wait(&full, 0, c.status) && k < n) {
+        const Turner<kMode> t(cs + (kMode != kStill ? k * kMaxPairs : 0), lane, rope);
+        const TokenAt place = at[k];
+        const uint16_t *const rows = reinterpret_cast<const uint16_t *>(smem + k * tk.bytes);
+        uint16_t *const dst = r.q_out + (tok0 + k) * r.q_out_stride + (int64_t)head0 * kHeadDim;
+        uint8_t *const b8 = reinterpret_cast<uint8_t *>(place.page);
+        for (int i = first; i < nq + nkv + (idx ? 1 : 0); i += ways) {
+            const uint16_t *const row = rows + i * kHeadDim;
+            if (i < nq) {
+                float x[8];
+                t.turn_row(row, x);
+                *(reinterpret_cast<uint4 *>(dst + i * kHeadDim) + lane) = narrow(x);
                 continue;
             }
-            page = (int64_t)id * sd.ps;
-        } else {
-            in_page = place;
-        }
-        uint16_t *const base = const_cast<uint16_t *>(sd.layer_base) + page;
-        if (row < 2 * H) {
-            const bool v = row >= H;
-            const int head = v ? row - H : row;
-            if (v) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(r.v + tok * r.v_stride + head * kHeadDim) + lane);
-                if constexpr (!kFp8) {
-                    *(reinterpret_cast<uint4 *>(base + off_v(H, sd.ptok, head, in_page)) + lane) = u;
-                    continue;
-                }
-                widen(u, x);
-            } else {
-                rotated(r.k + tok * r.k_stride + head * kHeadDim, lane, rope.rot_dim, rope.pairs, t, x);
-            }
-            if constexpr (kFp8) {
-                uint8_t *const b8 = reinterpret_cast<uint8_t *>(base);
+            if (!place.page) break;
+            const bool v = i >= nq + H;
+            const int head = i - nq - (v ? H : 0);
+            if (i == nq + nkv) {
+                if (lane < kIdxDim / 8)
+                    *(reinterpret_cast<uint4 *>(place.page + off_ik_f(kFp8, H, c.idx_dim, place.ptok, place.row)) + lane) =
+                        *(reinterpret_cast<const uint4 *>(row) + lane);
+            } else if constexpr (kFp8) {
+                float x[8];
+                if (v || kMode == kStill) widen(*(reinterpret_cast<const uint4 *>(row) + lane), x);
+                else t.turn_row(row, x);
                 uint2 codes;
                 const float scale = quantize_row8f(x, &codes);
-                *reinterpret_cast<uint2 *>(b8 + off8_code(v, H, sd.ptok, head, in_page) + lane * 8) = codes;
-                if (lane == 0) *reinterpret_cast<float *>(b8 + off8_scale(v, H, sd.ptok, head, in_page)) = scale;
+                *reinterpret_cast<uint2 *>(b8 + off8_code(v, H, place.ptok, head, place.row) + lane * 8) = codes;
+                if (lane == 0) *reinterpret_cast<float *>(b8 + off8_scale(v, H, place.ptok, head, place.row)) = scale;
             } else {
-                *(reinterpret_cast<uint4 *>(base + off_k(sd.ptok, head, in_page)) + lane) = narrow(x);
+                uint4 u = *(reinterpret_cast<const uint4 *>(row) + lane);
+                if (!v && kMode != kStill) {
+                    float x[8];
+                    t.turn_row(row, x);
+                    u = narrow(x);
+                }
+                *(reinterpret_cast<uint4 *>(place.page + (v ? off_v(H, place.ptok, head, place.row) : off_k(place.ptok, head, place.row))) + lane) = u;
             }
-        } else if (lane < kIdxDim / 8) {
-            *(reinterpret_cast<uint4 *>(base + off_ik_f(kFp8, H, c.idx_dim, sd.ptok, in_page)) + lane) =
-                __ldg(reinterpret_cast<const uint4 *>(r.ik + tok * r.ik_stride) + lane);
         }
     }
     pdl_trigger_after_writes();  // the next decode may read these rows early
 }
-
-// Tokens a CTA: one while the CTAs of one token each fit the GPU about twice
-// over, else four.
-int block_of(int32_t tokens) { return tokens > 2048 ? kBlockTokens : 1; }
 
 bool to_turns(double radians, uint64_t *out) {
     if (!std::isfinite(radians)) return false;
@@ -223,20 +313,72 @@ bool rope_shape_ok(int32_t rot_dim, int32_t pairs, const void *out) {
 
 }  // namespace
 
-int launch_rope_rows(const Common &c, int32_t total_tokens, const pkv_rope &rope, const RopeRows &r, int32_t dim,
-                     cudaStream_t stream) {
-    const int block = block_of(total_tokens);
-    return launch_status(launch_pdl(dim == kHeadDim ? rope_rows<kHeadDim> : rope_rows<kIdxDim>,
-                                    static_cast<unsigned>((total_tokens - 1) / block + 1), kThreads, 0, stream, c, rope,
-                                    r, total_tokens, block));
+// A launch's cut, `heads` query rows and `other` bytes of a token besides: tokens
+// of a CTA one while that fits the GPU about twice over, else up to four that take
+// 48 KB, so that four CTAs of an SM have 190 KB on their way.
+static RopeTokens tokens_of(const Common &c, int32_t total, int32_t heads, int32_t row_bytes, int32_t other, unsigned *grid) {
+    RopeTokens t;
+    std::memset(&t, 0, sizeof(t));
+    for (int s = 0; s < c.n_seqs; ++s) t.tok_off[s] = c.seq[s].tok_off;
+    t.total = total;
+    t.segs = std::max(1, (heads + kSegHeads - 1) / kSegHeads);
+    t.bytes = std::min(heads, kSegHeads) * row_bytes + other;
+    t.block = 1;
+    while (total > 2048 && t.block < kBlockTokens && 2 * t.block * t.bytes <= 48 * 1024) t.block *= 2;
+    const int64_t ctas = ((int64_t)(total - 1) / t.block + 1) * t.segs;
+    *grid = ctas <= INT32_MAX ? static_cast<unsigned>(ctas) : 0;  // (none: more than a launch takes)
+    return t;
 }
 
-int launch_rope_store(const Common &c, int32_t total_tokens, const pkv_rope &rope, const RopeRows &r,
-                      cudaStream_t stream) {
-    const int block = block_of(total_tokens);
-    return launch_status(launch_pdl(c.kv_fp8 ? rope_store<true> : rope_store<false>,
-                                    static_cast<unsigned>((total_tokens - 1) / block + 1), kThreads, 0, stream, c, rope,
-                                    r, total_tokens, block));
+// A token of 64 query heads, 64 KV heads and an indexer row takes 97 KB; an SM left
+// with a small carveout could not take a CTA beside the kernel before.
+constexpr int kMaxSmem = (kSegHeads + 2 * 64) * kHeadDim * 2 + kIdxDim * 2;
+static int set_smem(const void *f) {
+    if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) return PKV_ECUDA;
+    return cuda_rc(cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared));
+}
+
+int launch_rope_rows(const Common &c, int32_t total_tokens, const pkv_rope &rope, const RopeRows &r, int32_t dim,
+                     cudaStream_t stream) {
+    unsigned grid;
+    const RopeTokens t = tokens_of(c, total_tokens, c.n_q_heads, dim * 2, 0, &grid);
+    if (grid == 0) return PKV_EINVAL;
+    using Kernel = void (*)(Common, pkv_rope, RopeRows, RopeTokens);
+    const Kernel fns[2][3] = {{rope_rows<kIdxDim, kInside>, rope_rows<kIdxDim, kApart>, rope_rows<kIdxDim, kAnyhow>},
+                              {rope_rows<kHeadDim, kInside>, rope_rows<kHeadDim, kApart>, rope_rows<kHeadDim, kAnyhow>}};
+    static std::atomic<uint64_t> attr_done{0};
+    if (once_per_device(attr_done, [&] {
+            for (const auto &of_dim : fns)
+                for (const Kernel f : of_dim)
+                    if (set_smem(reinterpret_cast<const void *>(f)) != PKV_OK) return PKV_ECUDA;
+            return PKV_OK;
+        }) != PKV_OK)
+        return PKV_ECUDA;
+    return launch_status(launch_pdl(fns[dim == kHeadDim][mode_of(rope) - kInside], grid, kThreads, t.block * t.bytes, stream, c,
+                                    rope, r, t));
+}
+
+int launch_rope_store(const Common &c, int32_t total_tokens, const pkv_rope *rope, const RopeRows &r, cudaStream_t stream,
+                      bool early) {
+    unsigned grid;
+    const RopeTokens t = tokens_of(c, total_tokens, rope && r.q ? c.n_q_heads : 0, kHeadDim * 2,
+                                   (2 * c.n_kv_heads * kHeadDim + c.idx_dim) * 2, &grid);
+    if (grid == 0) return PKV_EINVAL;
+    pkv_rope none;
+    if (!rope) std::memset(&none, 0, sizeof(none));
+    using Kernel = void (*)(Common, pkv_rope, RopeRows, RopeTokens, bool);
+    const Kernel fns[2][4] = {{rope_store<false, kStill>, rope_store<false, kInside>, rope_store<false, kApart>, rope_store<false, kAnyhow>},
+                              {rope_store<true, kStill>, rope_store<true, kInside>, rope_store<true, kApart>, rope_store<true, kAnyhow>}};
+    static std::atomic<uint64_t> attr_done{0};
+    if (once_per_device(attr_done, [&] {
+            for (const auto &of_format : fns)
+                for (const Kernel f : of_format)
+                    if (set_smem(reinterpret_cast<const void *>(f)) != PKV_OK) return PKV_ECUDA;
+            return PKV_OK;
+        }) != PKV_OK)
+        return PKV_ECUDA;
+    return launch_status(launch_pdl(fns[c.kv_fp8 != 0][rope ? mode_of(*rope) : kStill], grid, kThreads, t.block * t.bytes, stream,
+                                    c, rope ? *rope : none, r, t, early));
 }
 
 // ---- entry points -----------------------------------------------------------------
@@ -392,5 +534,5 @@ extern "C" int pkv_rope_store(const pkv_layout *L, const pkv_seq *seqs, int32_t 
     r.v = static_cast<const uint16_t *>(v_new);
     r.ik = static_cast<const uint16_t *>(ik_new);
     r.pos = pos;
-    return launch_rope_store(c, static_cast<int32_t>(tokens), *rope, r, stream);
+    return launch_rope_store(c, static_cast<int32_t>(tokens), rope, r, stream, false);
 }

@@ -110,6 +110,33 @@ def test_the_gradient_is_the_rotation_back():
     close(host(out), want, rs.turn(g, -pos, 64, HALF, f, scale)[1])
 
 
+@pytest.mark.parametrize("heads,dim,tokens", [(64, 256, 3), (65, 256, 2), (130, 128, 2), (200, 256, 1), (24, 256, 2100), (40, 128, 2053)])
+def test_many_heads(heads, dim, tokens):
+    """More heads than a CTA takes, and blocks of two and four tokens."""
+    rng = np.random.default_rng(heads)
+    lens = [(tokens + 70, tokens)]
+    x = rs.random_rows(rng, tokens, heads, dim)
+    out = torch().empty((tokens, heads, dim), dtype=torch().int16, device="cuda")
+    pkv.rope_rows(pkv.rope(64, 1e4), seqs_of(lens), heads, dev(x), out)
+    f, scale = rs.freqs(64, 1e4)
+    close(host(out), *rs.turn(rs.bf16_values(x), places(lens), 64, HALF, f, scale))
+
+
+@pytest.mark.parametrize("hkv,hq,tokens", [(64, 64, 5), (2, 130, 2), (33, 66, 3), (2, 16, 2200), (4, 16, 2050)])
+def test_store_with_many_heads(hkv, hq, tokens):
+    rng = np.random.default_rng(hkv)
+    lay, lens = pkv.layout(1, hkv, 256, 128), [(tokens + 9, tokens)]
+    a, b = Pages(lay, lens, 16, 1), Pages(lay, lens, 16, 1)
+    q, k, v = (dev(rs.random_rows(rng, tokens, h, 256)) for h in (hq, hkv, hkv))
+    ik, r = dev(rs.random_rows(rng, tokens, 128)), pkv.rope(64, 1e4, INTER)
+    k2, q2 = torch().empty_like(k), torch().empty_like(q)
+    pkv.rope_rows(r, b.seqs, hkv, k, k2)
+    pkv.rope_rows(r, b.seqs, hq, q, q2)
+    pkv.store(lay, b.seqs, 0, k2, v, ik)
+    pkv.rope_store(lay, a.seqs, 0, r, k, v, ik, n_q_heads=hq, q=q, q_out=q)      # in place
+    assert torch().equal(a.mem, b.mem) and torch().equal(q, q2)
+
+
 @pytest.mark.parametrize("pairs,rot", [(HALF, 256), (HALF, 20), (INTER, 64)])
 def test_in_place_and_strided_rows(pairs, rot):
     rng = np.random.default_rng(4)
