@@ -87,10 +87,10 @@ struct PrefixArgs {
     uint16_t *out;
     float *ws;
     uint32_t *status;
-    int32_t n_units, n_kv_heads, n_q_heads, group;  // group: query heads of a KV head
-    int32_t work_off[kMaxUnits];
+    int32_t n_units, n_seqs, n_kv_heads, n_q_heads, group;  // group: query heads of a KV head
+    alignas(16) int32_t work_off[kMaxUnits];
     PrefixUnit unit[kMaxUnits];
-    PrefixStream seq[PKV_MAX_SEQS];
+    alignas(16) PrefixStream seq[PKV_MAX_SEQS];
 };
 
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -146,25 +146,51 @@ struct Work {
     int first, count;  // the CTA's rows of the unit
     int key0, key1, ntiles;  // virtual keys
 };
-__device__ __forceinline__ Work work_of(const PrefixArgs &a, int item, int rank) {
+// The launch parameters that a CTA looks things up in, copied to shared memory
+// (where P will be) by all threads at once: read as parameters, each first use of
+// a line takes some 600 cycles, one after the other.
+struct Stash {
+    const PrefixUnit *unit;
+    const PrefixStream *seq;
+    const int32_t *work_off;
+};
+__device__ __forceinline__ uint4 load_param16(const void *p) {
+    uint4 v;
+    asm volatile("ld.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+    return v;
+}
+static_assert(sizeof(PrefixStream) == 24 && PKV_MAX_SEQS % 2 == 0 && sizeof(PrefixUnit) == 128 && kMaxUnits % 4 == 0, "whole 16 bytes");
+static_assert(offsetof(PrefixArgs, work_off) % 16 == 0 && offsetof(PrefixArgs, unit) % 16 == 0 && offsetof(PrefixArgs, seq) % 16 == 0 &&
+                  alignof(PrefixArgs) >= 16,
+              "read 16 bytes at a time");
+__device__ __forceinline__ Stash stash_params(const PrefixArgs &a, uint8_t *smem, int tid) {
+    const int units = a.n_units * 8, seqs = (a.n_seqs * 24 + 15) / 16, offs = (a.n_units + 3) / 4;
+    uint4 *const to = reinterpret_cast<uint4 *>(smem);
+    for (int i = tid; i < units + seqs + offs; i += kThreads) {
+        const uint8_t *const from = i < units ? reinterpret_cast<const uint8_t *>(a.unit) + 16 * i
+                                    : i < units + seqs ? reinterpret_cast<const uint8_t *>(a.seq) + 16 * (i - units)
+                                                       : reinterpret_cast<const uint8_t *>(a.work_off) + 16 * (i - units - seqs);
+        to[i] = load_param16(from);
+    }
+    return {reinterpret_cast<const PrefixUnit *>(smem), reinterpret_cast<const PrefixStream *>(to + units),
+            reinterpret_cast<const int32_t *>(to + units + seqs)};
+}
+static_assert(kMaxUnits * 132 + PKV_MAX_SEQS * 24 + 64 <= 2 * kPRegion, "the copies fit where P will be");
+
+__device__ __forceinline__ Work work_of(const Stash &st, int n_units, int item, int rank) {
     Work w;
-    w.u = find_seq(a.n_units, item, [&](int t) { return a.work_off[t]; });
-    const PrefixUnit &u = a.unit[w.u];
-    const int r = item - a.work_off[w.u], half = (u.rows + 1) >> 1;
+    w.u = find_seq(n_units, item, [&](int t) { return st.work_off[t]; });
+    const PrefixUnit &u = st.unit[w.u];
+    const int r = item - st.work_off[w.u], half = (u.rows + 1) >> 1;
     w.kvh = r / u.nsplit;
     w.split = r - w.kvh * u.nsplit;
     w.first = rank * half;
     w.count = rank ? u.rows - half : half;
-    const int tiles = (u.keys + kN - 1) / kN, st = u.shared / kN;
-    w.key0 = split_tile(w.split, u.per, st, tiles) * kN;
-    w.key1 = min(u.keys, split_tile(w.split + 1, u.per, st, tiles) * kN);
+    const int tiles = (u.keys + kN - 1) / kN, shared = u.shared / kN;
+    w.key0 = split_tile(w.split, u.per, shared, tiles) * kN;
+    w.key1 = min(u.keys, split_tile(w.split + 1, u.per, shared, tiles) * kN);
     w.ntiles = (w.key1 - w.key0 + kN - 1) / kN;
     return w;
-}
-
-// Stream of a unit's row (its token counted from the group's first).
-__device__ __forceinline__ int stream_of(const PrefixArgs &a, const PrefixUnit &g, int tok) {
-    return g.s0 + find_seq(g.n_seqs, g.tok0 + tok, [&](int t) { return a.seq[g.s0 + t].tok; });
 }
 
 // Where a tile's rows are.  With a map: lane i & 7 has run i of 16 rows; without,
@@ -229,17 +255,22 @@ __global__ void __launch_bounds__(kThreads, 1)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
+    const Stash stash = stash_params(a, smem, tid);
     tc_fence_before();
-    __syncthreads();  // this CTA's barriers and tensor memory are there
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    // ... and its peer's, behind this: the copies, which are the CTA's own, start before
+    __syncthreads();  // this CTA's barriers, tensor memory and copied parameters are there
+    // ... and its peer's, behind this.  Each role goes there once it has read what it
+    // needs of the copies, which P's first rows overwrite; the memory's rows, which
+    // are the CTA's own, are looked up before
+    auto arrive = [&] {
+        __syncwarp();
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    };
     auto meet = [&] {
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
         tc_fence_after();
     };
-    if (warp != kWarpK && warp != kWarpV) meet();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(tmem_slot), sbase = smem_u32(smem);
-    const Work w = work_of(a, static_cast<int>(blockIdx.x >> 1), rank);
+    const Work w = work_of(stash, a.n_units, static_cast<int>(blockIdx.x >> 1), rank);
     const PrefixUnit &u = a.unit[w.u];
     const PrefixUnit &g = u;  // its group's fields
     const int H = a.n_kv_heads, G = a.group;
@@ -255,10 +286,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto wait_warp = [&](int bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
     if (warp < kSoftWarps) {
         // ---------------- softmax ----------------
-        pdl_wait();
-        // the next kernel may start: what is older than this grid is done, and
-        // this one writes no cached row
-        if (tid == 0) pdl_trigger();
         const int r = lane + 32 * (warp & 3), hf = warp >> 2;
         const bool row_ok = r < w.count, active = 32 * (warp & 3) < w.count;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -278,14 +305,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         float qs = kScaleLog2;  // what a raw score is scaled by
         int my = -3, qpos = 0;  // the row's stream and position
         int64_t q_row = 0;      // its packed row
+        if (row_ok) {
+            const PrefixUnit &su = stash.unit[w.u];
+            const int gr = su.row0 + w.first + r, tok = su.tok0 + gr / G, h = gr % G;
+            my = su.s0 + find_seq(su.n_seqs, tok, [&](int t) { return stash.seq[su.s0 + t].tok; });
+            const PrefixStream &st = stash.seq[my];
+            qpos = st.len - st.n_new + (tok - st.tok);
+            q_row = (int64_t)tok * a.n_q_heads + w.kvh * G + h;
+        }
+        arrive();
+        meet();
+        pdl_wait();
+        // the next kernel may start: what is older than this grid is done, and
+        // this one writes no cached row
+        if (tid == 0) pdl_trigger();
         if (active) {
-            if (row_ok) {
-                const int gr = u.row0 + w.first + r, tok = gr / G, h = gr - tok * G;
-                my = stream_of(a, g, tok);
-                const PrefixStream &st = a.seq[my];
-                qpos = st.len - st.n_new + (g.tok0 + tok - st.tok);
-                q_row = ((int64_t)g.tok0 + tok) * a.n_q_heads + w.kvh * G + h;
-            }
             const uint4 *src = reinterpret_cast<const uint4 *>(a.q + q_row * kHeadDim + 128 * hf);
             float dn = 1.f;
             if constexpr (kFp8) {
@@ -375,10 +409,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 k = *reinterpret_cast<const float4 *>(scl + j);
-                    x[j] *= k.x * qs;
-                    x[j + 1] *= k.y * qs;
-                    x[j + 2] *= k.z * qs;
-                    x[j + 3] *= k.w * qs;
+                    const float2 lo = mul2(make_float2(x[j], x[j + 1]), make_float2(k.x, k.y));
+                    const float2 hi = mul2(make_float2(x[j + 2], x[j + 3]), make_float2(k.z, k.w));
+                    x[j] = lo.x;
+                    x[j + 1] = lo.y;
+                    x[j + 2] = hi.x;
+                    x[j + 3] = hi.y;
                 }
             }
             if (masked && any) {
@@ -387,6 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(see[j >> 5] & (1u << (j & 31)))) x[j] = -INFINITY;
             }
             // this half's reference as eight interleaved chains, then the row's
+            const float2 qs2 = make_float2(qs, qs);
             float m8[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) m8[j] = -INFINITY;
@@ -395,10 +432,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 e = *reinterpret_cast<const float4 *>(scl + kN + j);
-                    m8[j & 7] = fmaxf(m8[j & 7], x[j] + e.x);
-                    m8[(j + 1) & 7] = fmaxf(m8[(j + 1) & 7], x[j + 1] + e.y);
-                    m8[(j + 2) & 7] = fmaxf(m8[(j + 2) & 7], x[j + 2] + e.z);
-                    m8[(j + 3) & 7] = fmaxf(m8[(j + 3) & 7], x[j + 3] + e.w);
+                    const float2 lo = fma2(make_float2(x[j], x[j + 1]), qs2, make_float2(e.x, e.y));
+                    const float2 hi = fma2(make_float2(x[j + 2], x[j + 3]), qs2, make_float2(e.z, e.w));
+                    m8[j & 7] = fmaxf(m8[j & 7], lo.x);
+                    m8[(j + 1) & 7] = fmaxf(m8[(j + 1) & 7], lo.y);
+                    m8[(j + 2) & 7] = fmaxf(m8[(j + 2) & 7], hi.x);
+                    m8[(j + 3) & 7] = fmaxf(m8[(j + 3) & 7], hi.y);
                 }
             } else {
 #pragma unroll
@@ -437,20 +476,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) p16[j] = 0u;
             } else if constexpr (kFp8) {
-                float ps[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 off = make_float2(-m_off, -m_off);
+                float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 v = *reinterpret_cast<const float4 *>(scl + 2 * kN + j);
-                    const float p0 = ex2(x[j] - m_off), p1 = ex2(x[j + 1] - m_off);
-                    const float p2 = ex2(x[j + 2] - m_off), p3 = ex2(x[j + 3] - m_off);
-                    ps[0] += p0;
-                    ps[1] += p1;
-                    ps[2] += p2;
-                    ps[3] += p3;
-                    p16[j / 2] = pack_f16(p0 * v.x, p1 * v.y);
-                    p16[j / 2 + 1] = pack_f16(p2 * v.z, p3 * v.w);
+                    float2 lo = fma2(make_float2(x[j], x[j + 1]), qs2, off), hi = fma2(make_float2(x[j + 2], x[j + 3]), qs2, off);
+                    lo.x = ex2(lo.x);
+                    lo.y = ex2(lo.y);
+                    hi.x = ex2(hi.x);
+                    hi.y = ex2(hi.y);
+                    ps[0] = add2(ps[0], lo);
+                    ps[1] = add2(ps[1], hi);
+                    lo = mul2(lo, make_float2(v.x, v.y));
+                    hi = mul2(hi, make_float2(v.z, v.w));
+                    p16[j / 2] = pack_f16(lo.x, lo.y);
+                    p16[j / 2 + 1] = pack_f16(hi.x, hi.y);
                 }
-                l += (ps[0] + ps[1]) + (ps[2] + ps[3]);
+                l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
                 if (masked) {  // a scale that the row does not see may be anything: 0 times it is not 0
 #pragma unroll
                     for (int j = 0; j < 64; j += 2) {
@@ -510,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (odd_row) l = __uint_as_float(0x7fffffffu);
             const float inv = 1.f / l;
             float2 odd = make_float2(0.f, 0.f);  // NaN once a sum is not finite
-#pragma unroll 1
+#pragma unroll 2
             for (int ch = 0; ch < 4; ++ch) {
                 uint32_t o[32];
                 __syncwarp();
@@ -557,12 +600,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kWarpK || warp == kWarpV) {
         // ---------------- copies ----------------
         const bool is_v = warp == kWarpV;
-        const int ptok = g.ptok, n_pages = g.n_pages;
+        const PrefixUnit &su = stash.unit[w.u];
+        const int ptok = su.ptok, n_pages = su.n_pages, shared = su.shared, keys = su.keys, s_first = su.s_first;
+        const int64_t page_elems = su.ps;
         const uint64_t pol = policy_evict_normal();  // other units read the shared rows too
-        const void *const map = g.map_run >= 0 ? &maps.map[g.map_run] : nullptr;
-        const int whole_map = is_v ? g.map_v : g.map_k;
+        const void *const map = su.map_run >= 0 ? &maps.map[su.map_run] : nullptr;
+        const int whole_map = is_v ? su.map_v : su.map_k;
         const void *const map_w = whole_map >= 0 ? &maps.map[whole_map] : nullptr;
-        const uint8_t *const base = reinterpret_cast<const uint8_t *>(g.layer_base);
+        const uint8_t *const base = reinterpret_cast<const uint8_t *>(su.layer_base);
         const bool runs = map != nullptr;
         if (runs && lane == 0) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
@@ -570,17 +615,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // The unit's streams, one and another 32 behind it a lane: a search through
         // the launch parameters for each run took a tile of 64 streams 3 us
-        const int pad = (g.shared + kRun - 1) / kRun * kRun, n_seqs = g.s0 + g.n_seqs - u.s_first;
+        const int pad = (shared + kRun - 1) / kRun * kRun, n_seqs = su.s0 + su.n_seqs - s_first;
         int st_own[2], st_len[2];
         int64_t st_table[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int t = min(lane + 32 * i, n_seqs - 1);
-            const PrefixStream &st = a.seq[u.s_first + t];
+            const PrefixStream &st = stash.seq[s_first + t];
             st_own[i] = lane + 32 * i < n_seqs ? st.own : INT_MAX;
             st_len[i] = st.len;
             st_table[i] = reinterpret_cast<int64_t>(st.table);
         }
+        const int layer_row = static_cast<int>(su.layer_row), early = min(shared, su.early);
+        arrive();
         const int own0 = __shfl_sync(0xffffffffu, st_own[0], 0);
         const int64_t table0 = shfl64(st_table[0], 0);  // (every lane takes part in every exchange: none under a lane's condition)
         auto look = [&](int m) -> Look {
@@ -603,9 +650,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int own = pick(st_own[0], st_own[1]), len = pick(st_len[0], st_len[1]);
             const int64_t table_lo = shfl64(st_table[0], t & 31), table_hi = shfl64(st_table[1], t & 31);
             const int64_t table = v < pad ? table0 : t < 32 ? table_lo : table_hi;
-            const int limit = v < pad ? g.shared : len;
-            k.s = v >= u.keys ? -2 : v < pad ? -1 : u.s_first + t;
-            k.pos = v < pad ? v : g.shared + (v - pad + own0 - own);
+            const int limit = v < pad ? shared : len;
+            k.s = v >= keys ? -2 : v < pad ? -1 : s_first + t;
+            k.pos = v < pad ? v : shared + (v - pad + own0 - own);
             k.n = k.s == -2 ? 0 : min(kRun, limit - k.pos);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -627,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // element offset of a looked-up page from layer_base; one outside the arena is
         // reported and read as page 0
         auto page_at = [&](int id) -> int64_t {
-            if (static_cast<uint32_t>(id) < static_cast<uint32_t>(n_pages)) return (int64_t)id * g.ps;
+            if (static_cast<uint32_t>(id) < static_cast<uint32_t>(n_pages)) return (int64_t)id * page_elems;
             if (!is_v && a.status) atomicOr(a.status, PKV_DEV_BAD_PAGE);
             return 0;
         };
@@ -663,10 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int m = -1; ok && m < w.ntiles; ++m) {
             Look next = now;
             if (m + 1 < w.ntiles) next = look(m + 1);
-            if (m == 0) {
-                __syncwarp();
-                meet();
-            }
+            if (m == 0) meet();
             if (m >= 0) {
             // the slot
             const uint32_t q = kFp8 ? 2 * m + is_v : m;
@@ -678,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t *const dst = smem + (kFp8 ? L::off_raw + slot * kRawBytes : (is_v ? L::off_v : L::off_k) + slot * kSlotBytes);
             if (runs) {
                 const int64_t rb = row_bytes(page_at(now.id[0]), now.row[0]);
-                const int y = static_cast<int>(g.layer_row + rb / (kFp8 ? 256 : 512));
+                const int y = layer_row + static_cast<int>(rb / (kFp8 ? 256 : 512));
                 if (lane == 0) mbar_arrive_expect_tx(full, kFp8 ? kRawBytes : kSlotBytes);
                 __syncwarp();  // the expected bytes come first
                 // K's 64 keys, or V's 128, row after row in memory (one page's, mostly)
@@ -767,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             }
             if (m + 1 < w.ntiles) {
-                if (!waited && w.key0 + (m + 2) * kN > min(g.shared, g.early)) {
+                if (!waited && w.key0 + (m + 2) * kN > early) {
                     pdl_wait();
                     waited = true;
                 }
@@ -782,6 +826,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kWarpConv && warp < kWarpConv + kConvWarps) {
         // ---------------- conversion to fp16 ----------------
+        arrive();
+        meet();
         const int t = tid - kWarpConv * 32;
         bool ok = true;
         const auto flag = [&](int s) {  // in both CTAs: each converts half of the dims
@@ -906,7 +952,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         }
-    } else if (rank == 0 && lane == 0) {
+    } else {
+        arrive();
+        meet();
+    }
+    if (warp >= kWarpS && rank == 0 && lane == 0) {
         // ---------------- products ----------------
         bool ok = true;
         if (warp == kWarpS) {
@@ -952,7 +1002,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_commit_pair(&bars[drain]);
             mbar_wait(&bars[drain], 0, nullptr);
         }
-    } else if (!kFp8 && rank == 1 && warp == kWarpS && lane == 0) {
+    }
+    if (!kFp8 && rank == 1 && warp == kWarpS && lane == 0) {
         // the second CTA's K rows are there
         for (int n = 0; n < w.ntiles; ++n) {
             if (!wait(L::k_full + n % L::slots, n / L::slots)) break;
@@ -1175,6 +1226,7 @@ int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &map
     a.ws = ws;
     a.status = c.status;
     a.n_units = plan.n_units;
+    a.n_seqs = plan.n_seqs;
     a.n_kv_heads = c.n_kv_heads;
     a.n_q_heads = c.n_q_heads;
     a.group = c.group;
