@@ -315,9 +315,10 @@ struct alignas(128) PrefixUnit {
 // kOwnCost; `per` is at least either, so no split is empty.
 constexpr int32_t kSharedCost = 2, kOwnCost = 3;
 __host__ __device__ inline int32_t split_tile(int32_t i, int32_t per, int32_t shared_tiles, int32_t tiles) {
-    const int64_t x = (int64_t)i * per, y = x - (int64_t)kSharedCost * shared_tiles;
-    const int64_t t = y < 0 ? x / kSharedCost : shared_tiles + y / kOwnCost;
-    return static_cast<int32_t>(t < tiles ? t : tiles);
+    // (a unit has at most 2^23 tiles: 32 bits hold all of it)
+    const uint32_t x = (uint32_t)i * (uint32_t)per, s = (uint32_t)kSharedCost * (uint32_t)shared_tiles;
+    const uint32_t t = x < s ? x / kSharedCost : (uint32_t)shared_tiles + (x - s) / kOwnCost;
+    return static_cast<int32_t>(t < (uint32_t)tiles ? t : (uint32_t)tiles);
 }
 struct PrefixPlan {
     int32_t n_groups, n_units, n_seqs;

@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars[L::drain + 1], 1);
         *abort_flag = 0;
         bad[0] = bad[1] = 0u;
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");  // (the peer sets bits of `bad`)
         fence_mbar_init();
     }
     if (warp == kWarpS) {
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // are the CTA's own, are looked up before
     auto arrive = [&] {
         __syncwarp();
-        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");  // (the barriers' fence_mbar_init released them)
     };
     auto meet = [&] {
         asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
@@ -307,8 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int64_t q_row = 0;      // its packed row
         if (row_ok) {
             const PrefixUnit &su = stash.unit[w.u];
-            const int gr = su.row0 + w.first + r, tok = su.tok0 + gr / G, h = gr % G;
-            my = su.s0 + find_seq(su.n_seqs, tok, [&](int t) { return stash.seq[su.s0 + t].tok; });
+            const int gr = su.row0 + w.first + r, t = gr / G, tok = su.tok0 + t, h = gr - t * G;
+            my = su.s0 + find_seq(su.n_seqs, tok, [&](int i) { return stash.seq[su.s0 + i].tok; });
             const PrefixStream &st = stash.seq[my];
             qpos = st.len - st.n_new + (tok - st.tok);
             q_row = (int64_t)tok * a.n_q_heads + w.kvh * G + h;
@@ -561,7 +562,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; j += 2)
                     odd = fma2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), make_float2(0.f, 0.f), odd);
-                if (single) {
+                if (!single && w.count <= 32) {
+                    // few rows: a lane writes its own (64 bytes of a row by four lanes, below,
+                    // halve the sectors that L2 takes, but the exchange takes one warp 1 us)
+                    if (row_ok)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *(reinterpret_cast<uint4 *>(acc + prow * kHeadDim + 128 * hf + 32 * ch) + j) =
+                                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                } else if (single) {
                     uint4 v[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -1185,7 +1194,7 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
     for (int i = 0; i < plan->n_units; ++i) {
         PrefixUnit &u = plan->unit[i];
         plan->work_off[i] = plan->items;
-        u.per = static_cast<int32_t>(std::min<int64_t>(std::max<int64_t>(chosen, kOwnCost), INT32_MAX));
+        u.per = static_cast<int32_t>(std::max<int64_t>(chosen, kOwnCost));
         u.nsplit = static_cast<int32_t>((cost_of(u) + u.per - 1) / u.per);
         u.ws_off = floats;
         plan->items += static_cast<int32_t>(H * u.nsplit);
