@@ -693,27 +693,33 @@ static int plan_alone(Common &c, WindowPlan *plan, int32_t *window) {
     return plan_window(c, *window, 0, plan);
 }
 
-// Tensor maps of the groups' pages: 16-row runs where pages hold whole ones, and
-// boxes of the kernel's slots (64 K rows, 128 V rows) for rows that follow one
-// another.
+// Tensor maps of the groups' pages, for the planned units: 16-row runs where pages
+// hold whole ones, and boxes of the kernel's slots (64 K rows, 128 V rows) for rows
+// that follow one another.
 static void plan_prefix_maps(const Common &c, const pkv_layout *L, const pkv_seq *seqs, PrefixPlan &plan, DecodeMaps &maps) {
     int n_maps = 0;
     const bool fp8 = c.kv_fp8;
     const int64_t row = fp8 ? 128 : 256;  // 16-bit elements of a row
     for (int k = 0; k < plan.n_groups; ++k) {
-        PrefixGroup &g = plan.group[k];
-        g.map_k = g.map_v = g.map_run = -1;
+        const PrefixGroup &g = plan.group[k];
         const pkv_pg &pg = seqs[g.s0].pg;
         const int64_t layer_off = (int64_t)c.layer * layer_elems_f(fp8, L->n_kv_heads, L->idx_dim, pg.page_pos);
         if (pg.page_pos % 16 != 0 || pg.page_elems % row != 0 || layer_off % row != 0) continue;
         const uint64_t rows = (uint64_t)(pg.table ? pg.n_pages : 1) * pg.page_elems / row;
-        g.layer_row = layer_off / row;
-        g.map_run = static_cast<int16_t>(row_map(maps, n_maps, pg.base, rows, fp8));
-        if (g.map_run < 0 || pg.page_pos < 64) continue;  // (never 64 rows on end)
-        g.map_k = static_cast<int16_t>(fp8 ? row_map(maps, n_maps, pg.base, rows, true, false, 64)
-                                           : row_map(maps, n_maps, pg.base, rows, false, true, 64, 4));
-        g.map_v = static_cast<int16_t>(fp8 ? row_map(maps, n_maps, pg.base, rows, true, false, 128)
-                                           : row_map(maps, n_maps, pg.base, rows, false, true, 128, 2));
+        const int run = row_map(maps, n_maps, pg.base, rows, fp8);
+        int map_k = -1, map_v = -1;
+        if (run >= 0 && pg.page_pos >= 64) {  // (else never 64 rows on end)
+            map_k = fp8 ? row_map(maps, n_maps, pg.base, rows, true, false, 64) : row_map(maps, n_maps, pg.base, rows, false, true, 64, 4);
+            map_v = fp8 ? row_map(maps, n_maps, pg.base, rows, true, false, 128) : row_map(maps, n_maps, pg.base, rows, false, true, 128, 2);
+        }
+        const int end = k + 1 < plan.n_groups ? plan.group[k + 1].unit0 : plan.n_units;
+        for (int i = g.unit0; i < end; ++i) {
+            PrefixUnit &u = plan.unit[i];
+            u.layer_row = layer_off / row;
+            u.map_run = static_cast<int16_t>(run);
+            u.map_k = static_cast<int16_t>(map_k);
+            u.map_v = static_cast<int16_t>(map_v);
+        }
     }
 }
 
@@ -760,24 +766,38 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
     const uint16_t *const kn = static_cast<const uint16_t *>(k_new), *const vn = static_cast<const uint16_t *>(v_new);
     const uint16_t *const ikn = k_new && L->idx_dim ? static_cast<const uint16_t *>(ik_new) : nullptr;
     DecodeMaps maps;  // copied into the launch's parameters
-    if (!shares) {
-        WindowPlan alone;
-        int32_t window;
-        rc = plan_alone(c, &alone, &window);
+    // Together or alone: a call that shares nothing, and one whose shared rows are so
+    // few that each stream reads them sooner by itself.  16 query and 2 KV heads, 100
+    // own positions a stream, alone against together: 2 streams of 512 shared positions
+    // 6.4 us against 14.5, of 4,096: 15.0, 13.7; 8 streams of 2,048: 11.1, 15.6, of
+    // 16,384: 33.2, 23.8; 64 streams of 512: 21.9, 24.6, of 2,048: 37.1, 25.9.  (Of 130
+    // calls the worst choice costs a quarter.)  Not where it needs more workspace than
+    // the size that was told.
+    int nsm = 0;
+    bool together = shares;
+    Common ca = c;
+    WindowPlan alone;
+    int32_t window;
+    rc = plan_alone(ca, &alone, &window);
+    if (shares) {
+        const bool no_plan = rc != PKV_OK;
+        rc = sm_count(&nsm);
         if (rc) return rc;
+        plan_prefix(c, nsm, &plan);
+        together = no_plan || plan.cost <= alone_cost(ca, alone) || alone.ws_bytes > prefix_ws_bytes(c, groups, n_groups, nsm);
+    } else if (rc) {
+        return rc;
+    }
+    if (!together) {
         if (alone.ws_bytes > 0 && (!ws || ws_bytes < alone.ws_bytes || (reinterpret_cast<uintptr_t>(ws) & 255u))) return PKV_EINVAL;
-        plan_window_maps(c, L, seqs, maps);
-        return launch_window(c, alone, maps, window, 0, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out),
+        plan_window_maps(ca, L, seqs, maps);
+        return launch_window(ca, alone, maps, window, 0, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out),
                              static_cast<float *>(ws), kn, vn, ikn, stream);
     }
-    int nsm = 0;
-    rc = sm_count(&nsm);
-    if (rc) return rc;
-    plan_prefix_maps(c, L, seqs, plan, maps);
-    plan_prefix(c, nsm, &plan);
     if (plan.floats > 0 &&
         (!ws || ws_bytes < static_cast<size_t>(plan.floats) * 4 || (reinterpret_cast<uintptr_t>(ws) & 255u)))
         return PKV_EINVAL;
+    plan_prefix_maps(c, L, seqs, plan, maps);
     // the new rows first, into their pages: the attention's kernel streams the
     // shared rows meanwhile
     if (k_new) {

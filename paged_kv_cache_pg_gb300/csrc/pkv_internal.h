@@ -261,6 +261,7 @@ struct WindowPlan {
     bool wide;          // a CTA takes all of a KV head's columns
     int64_t stash_off;  // floats of partials in the workspace, before the stash
     size_t ws_bytes;
+    int64_t cost, keys; // of the plan, in tenths of a key's time; keys that its CTAs read
 };
 int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan);
 // Row maps of the streams (in tma): 3D boxes of 16 whole bf16 rows, or of 32
@@ -288,24 +289,23 @@ struct PrefixStream {
 struct PrefixGroup {
     const uint16_t *layer_base;
     int64_t ps;            // elements in a page
-    int64_t layer_row;     // map row of layer_base
     int32_t ptok, n_pages; // positions in a page, arena pages
     int32_t shared;        // shared positions
     int32_t early;         // positions below it are read before the grid-dependency wait
     int32_t s0, n_seqs;    // its streams
     int32_t tok0, rows;    // first packed token, rows of a KV head
     int32_t unit0;         // its first unit
-    int16_t map_k, map_v;  // whole K and V slots, or -1
-    int16_t map_run;       // 16-row runs, or -1: key by key
 };
 // A unit as the kernel sees it, with its group's fields: one or two lines of the
 // launch parameters, whose first reads cost a CTA some 600 cycles each.
 struct alignas(128) PrefixUnit {
     const uint16_t *layer_base;
-    int64_t ps, layer_row;
+    int64_t ps;
+    int64_t layer_row;     // map row of layer_base
     int64_t ws_off;        // float offset of its partials in the workspace
     int32_t ptok, n_pages, shared, early, s0, n_seqs, tok0;
-    int16_t map_k, map_v, map_run;
+    int16_t map_k, map_v;  // whole K and V slots, or -1
+    int16_t map_run;       // 16-row runs, or -1: key by key
     int32_t row0, rows;    // of the group's
     int32_t s_first;       // stream of its first row
     int32_t keys;          // virtual keys
@@ -325,6 +325,7 @@ struct PrefixPlan {
     int32_t items;
     bool merge;            // some unit has several splits
     int64_t floats;        // of partials
+    int64_t cost;          // nanoseconds, as modelled
     PrefixStream seq[PKV_MAX_SEQS];
     PrefixGroup group[PKV_MAX_SEQS];
     PrefixUnit unit[kMaxUnits];
@@ -332,6 +333,7 @@ struct PrefixPlan {
 };
 // Units, splits and workspace places of a plan that holds the groups and streams.
 void plan_prefix(const Common &c, int nsm, PrefixPlan *plan);
+int64_t alone_cost(const Common &c, const WindowPlan &plan);
 // Bytes of partials that calls of these streams' new tokens take at most, whatever
 // their lengths and whichever of the groups' pages are shared.
 size_t prefix_ws_bytes(const Common &c, const pkv_group *groups, int32_t n_groups, int nsm);

@@ -1120,10 +1120,16 @@ __global__ void __launch_bounds__(kCombThreads)
     *reinterpret_cast<uint2 *>(a.out + (int64_t)blockIdx.x * kHeadDim + d) = pk;
 }
 
-// Split model, in hundredths of a microsecond: a pair's tile of 128 keys and 256
-// rows, its start and end, a split's partials written and read again, and the
-// merging kernel.
-constexpr int64_t kTileCost = 140, kPairCost = 600, kPartialCost = 6, kMergeCost = 400;
+// Cost model in nanoseconds, fitted to 130 calls of 2 to 64 streams (128 to 31,000
+// shared positions, 100 to 2,000 own, 1 or 4 new tokens, 1 or 2 KV heads of 8
+// columns; within 10 % of most of them, 25 % of the worst): a pair's tile of 128
+// shared keys (bf16, e4m3), its start and end, two rows of partials written and
+// read again, and the merging kernel.
+constexpr int64_t kTileCost[2] = {1650, 2460}, kPairCost = 7200, kTwoRowsCost = 1, kMergeCost[2] = {4500, 6000};
+// ... and of the streams decoded alone: start, a thousand units of the windowed
+// plan's cost, a million keys; twice and more of that for
+// more than eight e4m3 columns.
+constexpr int64_t kAloneCost[2] = {0, 10000}, kAloneUnits[2] = {2060, 630}, kAloneKeys[2] = {28500, 78500}, kAloneWide = 178000;
 
 }  // namespace
 
@@ -1145,7 +1151,6 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
             PrefixUnit &u = plan->unit[plan->n_units++];
             u.layer_base = g.layer_base;
             u.ps = g.ps;
-            u.layer_row = g.layer_row;
             u.ptok = g.ptok;
             u.n_pages = g.n_pages;
             u.shared = g.shared;
@@ -1153,9 +1158,7 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
             u.s0 = g.s0;
             u.n_seqs = g.n_seqs;
             u.tok0 = g.tok0;
-            u.map_k = g.map_k;
-            u.map_v = g.map_v;
-            u.map_run = g.map_run;
+            u.map_k = u.map_v = u.map_run = -1;  // (plan_prefix_maps gives it its maps)
             u.row0 = row0;
             u.rows = std::min(kUnitRows, g.rows - row0);
             const auto stream = [&](int row) {
@@ -1171,20 +1174,23 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
             most = std::max(most, cost_of(u));
         }
     }
-    const auto items_of = [&](int64_t per) {
-        int64_t n = 0;
-        for (int i = 0; i < plan->n_units; ++i) n += H * ((cost_of(plan->unit[i]) + per - 1) / per);
-        return n;
-    };
     const int64_t cap = std::max(H * plan->n_units, slots);
-    int64_t best = INT64_MAX, chosen = most;
+    const int fp8 = c.kv_fp8 ? 1 : 0;
+    int64_t chosen = most;
+    plan->cost = INT64_MAX;
     for (int64_t k = 1; k <= slots; ++k) {
-        const int64_t per = std::max<int64_t>(std::max(kSharedCost, kOwnCost), (most + k - 1) / k), items = items_of(per);
+        const int64_t per = std::max<int64_t>(std::max(kSharedCost, kOwnCost), (most + k - 1) / k);
+        int64_t items = 0, rows = 0;
+        for (int i = 0; i < plan->n_units; ++i) {
+            const int64_t n = H * ((cost_of(plan->unit[i]) + per - 1) / per);
+            items += n;
+            rows += n * plan->unit[i].rows;
+        }
         if (items > cap) continue;
-        const int64_t cost = (items + slots - 1) / slots * (per * kTileCost / kSharedCost + kPairCost) +
-                             (k > 1 ? items * kPartialCost + kMergeCost : 0);
-        if (cost < best) {
-            best = cost;
+        const int64_t cost = (items + slots - 1) / slots * (per * kTileCost[fp8] / kSharedCost + kPairCost) +
+                             (k > 1 ? rows * kTwoRowsCost / 2 + kMergeCost[fp8] : 0);
+        if (cost < plan->cost) {
+            plan->cost = cost;
             chosen = per;
         }
     }
@@ -1204,6 +1210,15 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
         }
     }
     plan->floats = floats;
+}
+
+// Nanoseconds of the streams' windowed decode over all their positions.
+int64_t alone_cost(const Common &c, const WindowPlan &plan) {
+    const int fp8 = c.kv_fp8 ? 1 : 0;
+    bool over8 = false;
+    for (int s = 0; s < c.n_seqs; ++s) over8 |= c.seq[s].n_new * c.group > 8;
+    return kAloneCost[fp8] + plan.cost * kAloneUnits[fp8] / 1000 +
+           plan.keys * (kAloneKeys[fp8] + (fp8 && over8 ? kAloneWide : 0)) / 1000000;
 }
 
 // At most `slots` pairs of as many rows as a unit can have (or, with more units

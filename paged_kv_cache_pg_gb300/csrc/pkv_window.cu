@@ -1250,6 +1250,8 @@ int plan_window(Common &c, int32_t window, int32_t n_sink, WindowPlan *plan) {
         }
     }
     const bool combine = plan->run > 0;
+    plan->cost = best;
+    plan->keys = keys;
     plan->items = static_cast<int32_t>(items);
     plan->comb = combine ? static_cast<int32_t>(cols) : 0;
     plan->pieces = pieces;
