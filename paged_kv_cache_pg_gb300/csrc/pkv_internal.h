@@ -313,7 +313,7 @@ struct alignas(128) PrefixUnit {
 };
 // First tile of split i: a tile of shared keys only costs kSharedCost, another
 // kOwnCost; `per` is at least either, so no split is empty.
-constexpr int32_t kSharedCost = 2, kOwnCost = 3;
+constexpr int32_t kSharedCost = 5, kOwnCost = 6;
 __host__ __device__ inline int32_t split_tile(int32_t i, int32_t per, int32_t shared_tiles, int32_t tiles) {
     // (a unit has at most 2^23 tiles: 32 bits hold all of it)
     const uint32_t x = (uint32_t)i * (uint32_t)per, s = (uint32_t)kSharedCost * (uint32_t)shared_tiles;
@@ -322,7 +322,7 @@ __host__ __device__ inline int32_t split_tile(int32_t i, int32_t per, int32_t sh
 }
 struct PrefixPlan {
     int32_t n_groups, n_units, n_seqs;
-    int32_t items;
+    int32_t items, nsm;
     bool merge;            // some unit has several splits
     int64_t floats;        // of partials
     int64_t cost;          // nanoseconds, as modelled

@@ -54,6 +54,9 @@ constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(2
 constexpr float kRescale = 8.f;          // rescale O when the reference grows by more than 2^8
 constexpr float kFarScore = 67108864.f;  // 2^26: references beyond it are reported (float32 steps of 4 there)
 
+constexpr int kHalfRow = 512, kHalfOut = 256;  // bytes of 128 of a row's float32 sums, of its outputs
+constexpr int kMaxSplits = 128;
+
 constexpr int kInfo = 4;  // tiles whose runs' (and scales') places are kept
 
 template <bool kFp8>
@@ -80,6 +83,7 @@ struct Lay {
     static constexpr int bars = drain + 2;
     static constexpr int smem = off_bar + bars * 8 + 16;  // behind the barriers: TMEM address, flags
     static_assert(smem <= 232448, "above the 227 KB a CTA may hold");
+    static_assert(off_k + kSoftWarps * 32 * kHalfRow <= off_red, "the sums fit in the slots");
 };
 
 struct PrefixArgs {
@@ -138,6 +142,15 @@ __device__ __forceinline__ bool mbar_acquired(uint64_t *bar, uint32_t parity) {
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
+}
+
+// One bulk copy shared -> global (16-byte aligned, whole 16 bytes), and the wait for
+// the thread's copies.
+__device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_stores_done() {
+    asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // A pair's work.
@@ -245,9 +258,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bars[L::drain], 1);
         mbar_init(&bars[L::drain + 1], 1);
         *abort_flag = 0;
-        bad[0] = bad[1] = 0u;
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");  // (the peer sets bits of `bad`)
         fence_mbar_init();
+    }
+    if (tid == kThreads - 1) {
+        bad[0] = bad[1] = 0u;
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");  // (the peer sets bits of it)
     }
     if (warp == kWarpS) {
         __syncwarp();
@@ -321,18 +336,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         // this one writes no cached row
         if (tid == 0) pdl_trigger();
         if (active) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + q_row * kHeadDim + 128 * hf);
+            // Eight lanes read a row's 128 bytes; the rows are turned to their threads
+            // where P will be, 64 dims at a time (16 bytes of 32 rows an instruction took
+            // 13,600 cycles with 128 e4m3 rows, whose loads miss what is left of L1)
+            uint4 v[16];
+            const uint4 *const q0 = reinterpret_cast<const uint4 *>(a.q + 128 * hf) + (lane & 7);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int64_t at = shfl64(row_ok ? q_row : -1, 4 * i + (lane >> 3));
+                v[i] = at >= 0 ? __ldg(q0 + at * (kHeadDim / 8)) : make_uint4(0, 0, 0, 0);
+                v[8 + i] = at >= 0 ? __ldg(q0 + at * (kHeadDim / 8) + 8) : make_uint4(0, 0, 0, 0);
+            }
+            uint4 *const turn = reinterpret_cast<uint4 *>(smem) + warp * 256;
+#pragma unroll
+            for (int h = 0; h < 16; h += 8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int to = 4 * i + (lane >> 3);
+                    turn[8 * to + ((lane & 7) ^ (to & 7))] = v[h + i];
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[h + i] = turn[8 * lane + (i ^ (lane & 7))];
+                __syncwarp();
+            }
             float dn = 1.f;
             if constexpr (kFp8) {
                 // bf16 has the wider range: a power of two takes the row's largest
                 // element to 2^14 .. 2^15, exactly, and goes into the scores' scale
                 uint32_t top = 0u;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint4 v = row_ok ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
-                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                                 __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
-                }
+                for (int i = 0; i < 16; ++i)
+                    top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu),
+                                                 __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu)));
                 const uint32_t mine = max(top >> 16, top & 0xffffu);
                 float other = 0.f;
                 ok = exchange(__uint_as_float(mine), other);
@@ -342,13 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 dn = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
                 qs = kScaleLog2 * __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
             }
-#pragma unroll 1
+#pragma unroll
             for (int h32 = 0; h32 < 2; ++h32) {
                 uint32_t qv[32];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const uint4 v = row_ok ? __ldg(src + 8 * h32 + i) : make_uint4(0, 0, 0, 0);
-                    const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+                    const uint32_t e[4] = {v[8 * h32 + i].x, v[8 * h32 + i].y, v[8 * h32 + i].z, v[8 * h32 + i].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         qv[4 * i + k] = kFp8 ? pack_f16(dn * bf16_lo(e[k]), dn * bf16_hi(e[k])) : e[k];
@@ -538,14 +573,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
         }
         if (ok && active) {
+            // Through the slots, whose products are done, and out by bulk copies: 16
+            // bytes a lane at a time straight from the registers took 3,000 cycles.
+            // A split's partials are [half][row][128], a row's 16-byte chunks exchanged
+            // by its number's low bits (no two of eight lanes in one bank), so that a
+            // warp's 32 rows go as one copy; a unit's outputs are a copy a lane, its rows 16
+            // bytes apart.
             const bool single = u.nsplit == 1;
-            float *const acc = a.ws + u.ws_off;
-            float *const ml = acc + (int64_t)H * u.nsplit * u.rows * kHeadDim;
-            const int64_t prow = ((int64_t)w.kvh * u.nsplit + w.split) * u.rows + w.first + r;
-            const int64_t mine = !row_ok ? -1 : single ? q_row : prow;
-            int64_t row[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) row[j] = shfl64(mine, (lane & ~3) + j);
+            const int wr = 32 * (warp & 3), key = (w.first + r) & 7;
+            uint8_t *const stage = smem + L::off_k + warp * 32 * kHalfRow, *const mine = stage + lane * (single ? kHalfOut + 16 : kHalfRow);
             bool odd_row = false;
             if (row_ok) {
                 const int i = my - u.s_first;
@@ -554,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (odd_row) l = __uint_as_float(0x7fffffffu);
             const float inv = 1.f / l;
             float2 odd = make_float2(0.f, 0.f);  // NaN once a sum is not finite
-#pragma unroll 2
+#pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
                 uint32_t o[32];
                 __syncwarp();
@@ -562,49 +598,38 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 32; j += 2)
                     odd = fma2(make_float2(__uint_as_float(o[j]), __uint_as_float(o[j + 1])), make_float2(0.f, 0.f), odd);
-                if (!single && w.count <= 32) {
-                    // few rows: a lane writes its own (64 bytes of a row by four lanes, below,
-                    // halve the sectors that L2 takes, but the exchange takes one warp 1 us)
-                    if (row_ok)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *(reinterpret_cast<uint4 *>(acc + prow * kHeadDim + 128 * hf + 32 * ch) + j) =
-                                make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-                } else if (single) {
-                    uint4 v[4];
+                if (single) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         uint32_t e[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             e[k] = pack_bf16(__uint_as_float(o[8 * j + 2 * k]) * inv, __uint_as_float(o[8 * j + 2 * k + 1]) * inv);
-                        v[j] = make_uint4(e[0], e[1], e[2], e[3]);
+                        *reinterpret_cast<uint4 *>(mine + 16 * (4 * ch + j)) = make_uint4(e[0], e[1], e[2], e[3]);
                     }
-                    quad_transpose(v, lane);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (row[j] >= 0)
-                            *(reinterpret_cast<uint4 *>(a.out + row[j] * kHeadDim + 128 * hf + 32 * ch) + (lane & 3)) = v[j];
                 } else {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint4 v[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            v[j] = make_uint4(o[16 * h + 4 * j], o[16 * h + 4 * j + 1], o[16 * h + 4 * j + 2], o[16 * h + 4 * j + 3]);
-                        quad_transpose(v, lane);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (row[j] >= 0)
-                                *(reinterpret_cast<uint4 *>(acc + row[j] * kHeadDim + 128 * hf + 32 * ch + 16 * h) + (lane & 3)) = v[j];
-                    }
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4 *>(mine + 16 * ((8 * ch + j) ^ key)) =
+                            make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
                 }
             }
+            fence_async_smem();
+            __syncwarp();
+            const int64_t split = (int64_t)w.kvh * u.nsplit + w.split;
+            float *const acc = a.ws + u.ws_off + split * u.rows * kHeadDim + (int64_t)hf * u.rows * (kHeadDim / 2);
+            float *const ml = a.ws + u.ws_off + (int64_t)H * u.nsplit * u.rows * kHeadDim + split * u.rows * 2;
+            if (single) {
+                if (row_ok) bulk_s2g(a.out + q_row * kHeadDim + 128 * hf, mine, kHalfOut);
+            } else if (lane == 0) {
+                bulk_s2g(acc + (w.first + wr) * (kHeadDim / 2), stage, min(32, w.count - wr) * kHalfRow);
+            }
             if (row_ok) {
-                if (hf == 0 && !single) *reinterpret_cast<float2 *>(ml + 2 * prow) = make_float2(m_used, l);
+                if (hf == 0 && !single) *reinterpret_cast<float2 *>(ml + 2 * (w.first + r)) = make_float2(m_used, l);
                 if ((odd_row || odd.x + odd.y != 0.f || (m_used != -INFINITY && fabsf(m_used) > kFarScore)) && a.status)
                     atomicOr(a.status, PKV_DEV_RANGE);
             }
+            bulk_stores_done();
         }
     } else if (warp == kWarpK || warp == kWarpV) {
         // ---------------- copies ----------------
@@ -710,17 +735,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         float s_now[4] = {0.f, 0.f, 0.f, 0.f};
-        Look now;
         // Shared positions far enough below the new tokens stream before the kernel
         // before this one is done (it may be storing this call's new rows)
         bool waited = false;
         int last_q = -1;
         bool ok = true;
-        for (int m = -1; ok && m < w.ntiles; ++m) {
-            Look next = now;
-            if (m + 1 < w.ntiles) next = look(m + 1);
+        for (int m = 0; ok && m < w.ntiles; ++m) {
+            // looked up while the slot is still being multiplied
+            const Look now = look(m);
+            if (!waited && w.key0 + (m + 1) * kN > early) {
+                pdl_wait();
+                waited = true;
+            }
+            if constexpr (kFp8) scales(now, s_now);
             if (m == 0) meet();
-            if (m >= 0) {
             // the slot
             const uint32_t q = kFp8 ? 2 * m + is_v : m;
             const uint32_t n_slots = kFp8 ? L::raw : L::slots, slot = q % n_slots;
@@ -818,15 +846,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[L::info_full + is]);
             }
-            }
-            if (m + 1 < w.ntiles) {
-                if (!waited && w.key0 + (m + 2) * kN > early) {
-                    pdl_wait();
-                    waited = true;
-                }
-                if constexpr (kFp8) scales(next, s_now);
-            }
-            now = next;
         }
         if (!ok) {  // what was copied lands before the memory goes
             const int n_slots = kFp8 ? L::raw : L::slots, step = kFp8 ? 2 : 1;
@@ -1031,9 +1050,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Merge of a query row's splits, in their order.  A CTA a row; 64 threads hold
-// its 256 dims, and four such groups take every fourth split and add up at the
-// end, so that a row of 38 splits is two rounds of loads.
+// its 256 dims, and four such groups (two, where the GPU does not hold four of all
+// rows at once) take every fourth (second) split and add up at the end.
 constexpr int kCombThreads = 256;
+constexpr int kCombCtas = 4;  // of kCombThreads an SM holds
 constexpr int kCombBatch = 8;
 
 struct CombineArgs {
@@ -1048,55 +1068,59 @@ struct CombineArgs {
     } unit[kMaxUnits];
 };
 
-__global__ void __launch_bounds__(kCombThreads)
+__global__ void __launch_bounds__(kCombThreads, kCombCtas)
     prefix_combine(const __grid_constant__ CombineArgs a) {
+    __shared__ float weight[kMaxSplits];
     __shared__ float4 sh[3][64];
     const int tok = blockIdx.x / a.n_q_heads, head = blockIdx.x - tok * a.n_q_heads;
     const int k = find_seq(a.n_groups, tok, [&](int t) { return a.tok0[t]; });
     const int kvh = head / a.group, row = (tok - a.tok0[k]) * a.group + head - kvh * a.group;
     const CombineArgs::Unit &u = a.unit[a.unit0[k] + row / kUnitRows];
-    const int np = u.nsplit;
-    const int64_t step = u.rows, first = (int64_t)kvh * np * u.rows + row % kUnitRows;
-    const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 6, d = 4 * (tid & 63);
-    const float *const acc = a.ws + u.ws_off + first * kHeadDim + d;
-    const float *const ml = a.ws + u.ws_off + (int64_t)a.n_kv_heads * np * u.rows * kHeadDim + 2 * first;
+    const int np = u.nsplit, groups = blockDim.x >> 6;
+    const int64_t first = (int64_t)kvh * np * u.rows;
+    const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 6, ur = row % kUnitRows;
+    const int step = u.rows * kHeadDim;
+    const float *const acc = a.ws + u.ws_off + first * kHeadDim + ((tid & 63) >> 5) * u.rows * (kHeadDim / 2) + ur * (kHeadDim / 2) +
+                             4 * (lane ^ (ur & 7));
+    const float2 *const ml = reinterpret_cast<const float2 *>(a.ws + u.ws_off + (int64_t)a.n_kv_heads * np * u.rows * kHeadDim) + first + ur;
     asm volatile("" ::"l"(acc), "l"(ml), "r"(np));
     pdl_wait();
     if (tid == 0) pdl_trigger();
     if (np == 1) return;  // written where it was summed
-    const auto ml_of = [&](int i) -> float2 { return __ldcg(reinterpret_cast<const float2 *>(ml + 2 * i * step)); };
-    const auto acc_of = [&](int i) -> float4 { return __ldcg(reinterpret_cast<const float4 *>(acc + i * step * kHeadDim)); };
-    const float2 none = make_float2(-INFINITY, 0.f);
     float4 v[kCombBatch];
+    const auto load = [&](int b) {
 #pragma unroll
-    for (int j = 0; j < kCombBatch; ++j)
-        if (grp + 4 * j < np) v[j] = acc_of(grp + 4 * j);
+        for (int j = 0; j < kCombBatch; ++j)
+            if (b + groups * j < np) v[j] = __ldcg(reinterpret_cast<const float4 *>(acc + (int64_t)(b + groups * j) * step));
+    };
+    load(grp);
     // every warp finds the row's maximum and sum by itself: lane i has splits i, i + 32, ...
-    const float2 ml0 = lane < np ? ml_of(lane) : none, ml1 = lane + 32 < np ? ml_of(lane + 32) : none;
-    float M = fmaxf(ml0.x, ml1.x);
-    for (int i = lane + 64; i < np; i += 32) M = fmaxf(M, ml_of(i).x);
+    float2 x[kMaxSplits / 32];
+    float M = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxSplits / 32; ++j) {
+        x[j] = lane + 32 * j < np ? __ldcg(ml + (int64_t)(lane + 32 * j) * u.rows) : make_float2(-INFINITY, 0.f);
+        M = fmaxf(M, x[j].x);
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const auto weight = [&](float m) { return M == -INFINITY ? 0.f : ex2(m - M); };
-    const float w0 = weight(ml0.x), w1 = weight(ml1.x);
-    float sum = w0 * ml0.y + w1 * ml1.y;
-    for (int i = lane + 64; i < np; i += 32) {
-        const float2 x = ml_of(i);
-        sum += weight(x.x) * x.y;
+#pragma unroll
+    for (int j = 0; j < kMaxSplits / 32; ++j) {
+        const float w = M == -INFINITY ? 0.f : ex2(x[j].x - M);
+        if (tid < 32) weight[lane + 32 * j] = w;
+        sum += w * x[j].y;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncthreads();
     float4 o4 = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = grp; b < np; b += 4 * kCombBatch) {
-        if (b > grp)
-#pragma unroll
-            for (int j = 0; j < kCombBatch; ++j)
-                if (b + 4 * j < np) v[j] = acc_of(b + 4 * j);
+#pragma unroll 1
+    for (int b = grp; b < np; b += groups * kCombBatch) {
+        if (b > grp) load(b);
 #pragma unroll
         for (int j = 0; j < kCombBatch; ++j) {
-            const int i = b + 4 * j;
-            if (i >= np) break;  // uniform in the warp
-            const float w = i < 64 ? __shfl_sync(0xffffffffu, i < 32 ? w0 : w1, i & 31) : weight(ml_of(i).x);
+            if (b + groups * j >= np) break;
+            const float w = weight[b + groups * j];
             o4.x = fmaf(w, v[j].x, o4.x);
             o4.y = fmaf(w, v[j].y, o4.y);
             o4.z = fmaf(w, v[j].z, o4.z);
@@ -1106,18 +1130,18 @@ __global__ void __launch_bounds__(kCombThreads)
     if (grp) sh[grp - 1][tid & 63] = o4;
     __syncthreads();
     if (grp) return;
-#pragma unroll
-    for (int j = 0; j < 3; ++j) {
-        const float4 x = sh[j][tid];
-        o4.x += x.x;
-        o4.y += x.y;
-        o4.z += x.z;
-        o4.w += x.w;
+#pragma unroll 1
+    for (int j = 0; j < groups - 1; ++j) {
+        const float4 y = sh[j][tid];
+        o4.x += y.x;
+        o4.y += y.y;
+        o4.z += y.z;
+        o4.w += y.w;
     }
     uint2 pk;
     pk.x = pack_bf16(__fdiv_rn(o4.x, sum), __fdiv_rn(o4.y, sum));
     pk.y = pack_bf16(__fdiv_rn(o4.z, sum), __fdiv_rn(o4.w, sum));
-    *reinterpret_cast<uint2 *>(a.out + (int64_t)blockIdx.x * kHeadDim + d) = pk;
+    *reinterpret_cast<uint2 *>(a.out + (int64_t)blockIdx.x * kHeadDim + 4 * (tid & 63)) = pk;
 }
 
 // Cost model in nanoseconds, fitted to 130 calls of 2 to 64 streams (128 to 31,000
@@ -1139,6 +1163,7 @@ constexpr int64_t kAloneCost[2] = {0, 10000}, kAloneUnits[2] = {2060, 630}, kAlo
 void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
     const int64_t H = c.n_kv_heads, slots = std::max(1, nsm / 2);
     plan->n_units = 0;
+    plan->nsm = nsm;
     int64_t most = 1;  // cost of a unit
     const auto cost_of = [](const PrefixUnit &u) -> int64_t {
         const int64_t tiles = (u.keys + kN - 1) / kN, shared = u.shared / kN;
@@ -1178,7 +1203,7 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
     const int fp8 = c.kv_fp8 ? 1 : 0;
     int64_t chosen = most;
     plan->cost = INT64_MAX;
-    for (int64_t k = 1; k <= slots; ++k) {
+    for (int64_t k = 1; k <= std::min<int64_t>(slots, kMaxSplits); ++k) {
         const int64_t per = std::max<int64_t>(std::max(kSharedCost, kOwnCost), (most + k - 1) / k);
         int64_t items = 0, rows = 0;
         for (int i = 0; i < plan->n_units; ++i) {
@@ -1287,7 +1312,9 @@ int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &map
     for (int i = 0; i < plan.n_units; ++i) m.unit[i] = {plan.unit[i].ws_off, plan.unit[i].rows, plan.unit[i].nsplit};
     int64_t tokens = 0;
     for (int s = 0; s < c.n_seqs; ++s) tokens += c.seq[s].n_new;
-    return launch_status(launch_pdl(prefix_combine, static_cast<unsigned>(tokens * c.n_q_heads), kCombThreads, 0, stream, m));
+    const int64_t rows = tokens * c.n_q_heads;
+    const int threads = rows <= (int64_t)kCombCtas * plan.nsm ? kCombThreads : kCombThreads / 2;
+    return launch_status(launch_pdl(prefix_combine, static_cast<unsigned>(rows), threads, 0, stream, m));
 }
 
 }  // namespace pkv
