@@ -575,13 +575,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && active) {
             // Through the slots, whose products are done, and out by bulk copies: 16
             // bytes a lane at a time straight from the registers took 3,000 cycles.
-            // A split's partials are [half][row][128], a row's 16-byte chunks exchanged
-            // by its number's low bits (no two of eight lanes in one bank), so that a
-            // warp's 32 rows go as one copy; a unit's outputs are a copy a lane, its rows 16
-            // bytes apart.
+            // A split's partials are [32 dims][row][32], a row's 16-byte chunks exchanged
+            // by its number's low bits (no two of eight lanes in one bank), so that 32 dims
+            // of a warp's 32 rows go as one copy while the next ones are read; a unit's
+            // outputs are a copy a lane, its rows 16 bytes apart.
             const bool single = u.nsplit == 1;
             const int wr = 32 * (warp & 3), key = (w.first + r) & 7;
-            uint8_t *const stage = smem + L::off_k + warp * 32 * kHalfRow, *const mine = stage + lane * (single ? kHalfOut + 16 : kHalfRow);
+            uint8_t *const stage = smem + L::off_k + warp * 32 * kHalfRow, *const mine = stage + lane * (single ? kHalfOut + 16 : 128);
             bool odd_row = false;
             if (row_ok) {
                 const int i = my - u.s_first;
@@ -589,6 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (odd_row) l = __uint_as_float(0x7fffffffu);
             const float inv = 1.f / l;
+            const int64_t split = (int64_t)w.kvh * u.nsplit + w.split;
+            float *const acc = a.ws + u.ws_off + split * u.rows * kHeadDim + (int64_t)hf * u.rows * (kHeadDim / 2) + (w.first + wr) * 32;
+            float *const ml = a.ws + u.ws_off + (int64_t)H * u.nsplit * u.rows * kHeadDim + split * u.rows * 2;
             float2 odd = make_float2(0.f, 0.f);  // NaN once a sum is not finite
 #pragma unroll 1
             for (int ch = 0; ch < 4; ++ch) {
@@ -610,19 +613,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        *reinterpret_cast<uint4 *>(mine + 16 * ((8 * ch + j) ^ key)) =
+                        *reinterpret_cast<uint4 *>(mine + 4096 * ch + 16 * (j ^ key)) =
                             make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) bulk_s2g(acc + (int64_t)ch * u.rows * 32, stage + 4096 * ch, min(32, w.count - wr) * 128);
                 }
             }
-            fence_async_smem();
-            __syncwarp();
-            const int64_t split = (int64_t)w.kvh * u.nsplit + w.split;
-            float *const acc = a.ws + u.ws_off + split * u.rows * kHeadDim + (int64_t)hf * u.rows * (kHeadDim / 2);
-            float *const ml = a.ws + u.ws_off + (int64_t)H * u.nsplit * u.rows * kHeadDim + split * u.rows * 2;
-            if (single) {
-                if (row_ok) bulk_s2g(a.out + q_row * kHeadDim + 128 * hf, mine, kHalfOut);
-            } else if (lane == 0) {
-                bulk_s2g(acc + (w.first + wr) * (kHeadDim / 2), stage, min(32, w.count - wr) * kHalfRow);
+            if (single && row_ok) {
+                fence_async_smem();
+                bulk_s2g(a.out + q_row * kHeadDim + 128 * hf, mine, kHalfOut);
             }
             if (row_ok) {
                 if (hf == 0 && !single) *reinterpret_cast<float2 *>(ml + 2 * (w.first + r)) = make_float2(m_used, l);
@@ -1080,8 +1080,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas)
     const int64_t first = (int64_t)kvh * np * u.rows;
     const int tid = threadIdx.x, lane = tid & 31, grp = tid >> 6, ur = row % kUnitRows;
     const int step = u.rows * kHeadDim;
-    const float *const acc = a.ws + u.ws_off + first * kHeadDim + ((tid & 63) >> 5) * u.rows * (kHeadDim / 2) + ur * (kHeadDim / 2) +
-                             4 * (lane ^ (ur & 7));
+    const float *const acc = a.ws + u.ws_off + first * kHeadDim + (((tid & 63) >> 3) * u.rows + ur) * 32 + 4 * ((tid ^ ur) & 7);
     const float2 *const ml = reinterpret_cast<const float2 *>(a.ws + u.ws_off + (int64_t)a.n_kv_heads * np * u.rows * kHeadDim) + first + ur;
     asm volatile("" ::"l"(acc), "l"(ml), "r"(np));
     pdl_wait();
