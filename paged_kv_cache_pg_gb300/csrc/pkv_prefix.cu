@@ -1145,13 +1145,13 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas)
 
 // Cost model in nanoseconds, fitted to 130 calls of 2 to 64 streams (128 to 31,000
 // shared positions, 100 to 2,000 own, 1 or 4 new tokens, 1 or 2 KV heads of 8
-// columns; within 10 % of most of them, 25 % of the worst): a pair's tile of 128
-// shared keys (bf16, e4m3), its start and end, two rows of partials written and
-// read again, and the merging kernel.
-constexpr int64_t kTileCost[2] = {1650, 2460}, kPairCost = 7200, kTwoRowsCost = 1, kMergeCost[2] = {4500, 6000};
+// columns; within 14 % of each): a pair's tile of 128 shared keys (bf16, e4m3), its
+// start and end, a hundred rows of partials written and read again, and the merging
+// kernel.
+constexpr int64_t kTileCost[2] = {2200, 3000}, kPairCost = 7200, kRowsCost = 22, kMergeCost[2] = {4500, 5300};
 // ... and of the streams decoded alone: start, a thousand units of the windowed
-// plan's cost, a million keys; twice and more of that for
-// more than eight e4m3 columns.
+// plan's cost, a million keys, and what those take more with more than eight e4m3
+// columns.
 constexpr int64_t kAloneCost[2] = {0, 10000}, kAloneUnits[2] = {2060, 630}, kAloneKeys[2] = {28500, 78500}, kAloneWide = 178000;
 
 }  // namespace
@@ -1212,7 +1212,7 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
         }
         if (items > cap) continue;
         const int64_t cost = (items + slots - 1) / slots * (per * kTileCost[fp8] / kSharedCost + kPairCost) +
-                             (k > 1 ? rows * kTwoRowsCost / 2 + kMergeCost[fp8] : 0);
+                             (k > 1 ? rows * kRowsCost / 100 + kMergeCost[fp8] : 0);
         if (cost < plan->cost) {
             plan->cost = cost;
             chosen = per;
