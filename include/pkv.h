@@ -507,25 +507,30 @@ int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t
 
 /* ---- decode over shared pages (an addition: forks of a prompt) ------------------
  * pkv_decode for streams that share their first pages, as pkv_pages_fork leaves
- * them: the shared rows are read once for all the streams of a group.  The
- * call's streams are cut, in their order, into n_groups groups of n_seqs (>= 1)
- * streams each; the first n_pages (>= 0) logical pages of a group's streams are
- * the same pages (of one base, page size and arena), and every stream's new
- * tokens come behind them (len - n_new >= n_pages * page_pos).  The tables
- * of all of them hold the shared pages' ids (which one's is read is not said).
- * With n_pages 0, or one stream, nothing is shared.  The result is pkv_decode's,
- * within the attention tolerance.  Both formats; n_new * (n_q_heads/H) <= 32 per
- * stream; q, out, k_new, v_new, ik_new and the fused store as for
- * pkv_window_decode, and so is the ordering: the shared rows too may be read
- * before the kernel before has finished, where they lie more than 32 positions
- * below the new tokens.
- * Arithmetic of the shared part: tcgen05 products with float32 accumulation; Q
- * and K in bf16 (e4m3: fp16, exact, the query behind a power of two), P and V in
- * fp16.  So a weight has 11 significant bits; a bf16 V entry is exact for
- * magnitudes 2^-14 to 65,280, rounded to fp16's 2^-24 grid below that, and one
- * beyond 65,504 makes the output non-finite and sets PKV_DEV_RANGE, as does a
- * largest score (q.k / 16) beyond 4.6e7.  e4m3 V rows of any scale from 2^-40 to
- * 2^80 keep their precision.  A stream's own part is pkv_window_decode's.
+ * them: the shared rows are read once for all the streams of a group, and in the
+ * same pass each stream's own rows.  The call's streams are cut, in their order,
+ * into n_groups groups of n_seqs (>= 1) streams each; the first n_pages (>= 0)
+ * logical pages of a group's streams are the same pages (of one base, page size
+ * and arena), and every stream's new tokens come behind them (len - n_new >=
+ * n_pages * page_pos).  The tables of all of them hold the shared pages' ids
+ * (which one's is read is not said).  With n_pages 0, or one stream, nothing is
+ * shared.  The result is pkv_decode's, within the attention tolerance.  Both
+ * formats; n_new * (n_q_heads/H) <= 32 per stream; q, out, k_new, v_new, ik_new
+ * and the fused store as for pkv_window_decode, and so is the ordering: the
+ * shared rows too may be read before the kernel before has finished, where they
+ * lie more than 32 positions below the new tokens.
+ * A call that shares nothing, or whose shared rows are so few that its streams
+ * read them sooner each by itself (a rule on the streams' numbers, lengths and
+ * heads), has pkv_window_decode's arithmetic, of a window of all positions.
+ * Arithmetic of the others: tcgen05 products with float32 accumulation; Q and K
+ * in bf16 (e4m3: fp16, exact, the query behind a power of two), P and V in fp16.
+ * So a weight has 11 significant bits down to 2^-14 of the largest (below, it is
+ * rounded to 2^-25 of that); a bf16 V entry is exact for magnitudes 2^-14 to
+ * 65,280 and rounded to fp16's 2^-24 grid below that.  A V entry beyond 65,504,
+ * or not finite, makes outputs of its KV head that are not finite, for every
+ * stream that reads it and no other, and sets PKV_DEV_RANGE, as does a largest
+ * score (q.k / 16) beyond 4.6e7.  e4m3 V rows of any scale from 2^-40 to 2^80
+ * keep their precision.
  * Results follow the call's shape (its groups, lengths and new tokens), not where
  * its pages lie.
  * ws: device, >= pkv_prefix_decode_ws_size bytes, 256-byte aligned, no

@@ -685,8 +685,8 @@ static int prefix_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seq
     return s0 == n_seqs ? PKV_OK : PKV_EINVAL;
 }
 
-// The windowed decode's plan of streams that share nothing, over all their
-// positions (or those from `from` on).
+// The windowed decode's plan of the streams, each by itself, over all their
+// positions.
 static int plan_alone(Common &c, WindowPlan *plan, int32_t *window) {
     *window = 1;
     for (int32_t s = 0; s < c.n_seqs; ++s) *window = std::max(*window, c.seq[s].len);

@@ -265,10 +265,11 @@ def _token_rows(what: str, name: str, t, dev: int, tokens: int, width: int):
 
 def _window(what: str, lay, seqs, layer: int, n_q_heads: int, window: int, n_sink: int, q, out, ws, status, stream,
             chunk: bool, k=None, v=None, ik=None, shared=None):
-    """A windowed call, or with `shared` groups one over shared pages.  Tensors have to be contiguous, on the current device, of
-    the rows' type and as long as the launch's packed rows; rows given as ints
-    (addresses) are taken as they are.  Written out for each tensor: a small
-    call takes the GPU no longer than its arguments take here."""
+    """A windowed call, or with `shared` groups one over shared pages.  Tensors
+    have to be contiguous, on the current device, of the rows' type and as long
+    as the launch's packed rows; rows given as ints (addresses) are taken as
+    they are.  Written out for each tensor: a small call takes the GPU no longer
+    than its arguments take here."""
     _ints(what, layer | n_q_heads | window | n_sink)
     arr, n, new = _new_tokens(what, seqs)
     types, word = _types or _row_types()

@@ -74,6 +74,15 @@ def test_row_counts(rows_streams, new, hq, ballast):
     s.check(s.call())
 
 
+@pytest.mark.parametrize("fmt", [BF, E4])
+def test_largest(fmt):
+    """All streams with all the columns a call takes: eight units of 256 rows; and 64 KV heads."""
+    s = Shared(pkv.layout(1, 2, 256, 0, fmt), [([4 + 3 * i for i in range(64)], 8)], 4, 128, n_q_heads=16, fused=True)
+    s.check(s.call())
+    s = Shared(pkv.layout(1, 64, 256, 0, fmt), [([5, 20, 33], 2)], 2, 64, n_q_heads=64, fused=True, ballast=24)
+    s.check(s.call())
+
+
 @TOGETHER
 @pytest.mark.parametrize("fmt", [BF, E4])
 @pytest.mark.parametrize("gain", [8.0, 16.0, 64.0])
