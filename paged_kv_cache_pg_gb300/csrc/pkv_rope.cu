@@ -7,15 +7,20 @@
 // (a signed fraction of a half turn) go to sincospif.  In float32 radians a
 // position of 10^6 would leave 0.03 of the fastest pair's angle to chance.
 //
-// A CTA takes one token, or up to four of large calls.  It finds each token's
-// stream, page and row once, by one thread (the streams' first tokens lie together
-// in the launch parameters: read from the streams' own records, 64 of them took 6
-// us of a call), and computes its cosines and sines once, into shared memory, for
-// all of its heads (16 query rows and 2 key rows use the same 32 to 128 pairs);
-// with positions from the launch parameters that happens before the
-// grid-dependency wait.  The tokens' rows come by bulk copies, all at once: held
-// in registers, two rows a warp in flight, a prompt took 47 us.  A warp then takes
-// a row of 256 elements (two of 128) at a time, a lane 16 bytes of it and, with
+// A small call has a CTA a token.  A large one is cut into units of up to four
+// tokens, and as many CTAs as the GPU holds take every so many-th, the next unit's
+// rows on their way while one's are turned: a prompt of 8,192 tokens of 16 query and
+// 2 KV heads (172 MB) takes 32.9 us, 77 % of the copy rate, where CTAs of a unit
+// each took 34.1, 36.7 with units of 48 KB and two CTAs an SM.  (What is left: the
+// first rows' way in and the last ones' way out, and 7 units of 6.7 a CTA.)  A
+// unit's tokens' streams, pages and rows are found once, by a thread a token (the
+// streams' first tokens lie together in the launch parameters: read from the
+// streams' own records, 64 of them took 6 us of a call), and their cosines and sines
+// computed once, into shared memory, for all of their heads (16 query rows and 2 key
+// rows use the same 32 to 128 pairs); a small call's, with positions from the launch
+// parameters, before the grid-dependency wait.  Rows come by bulk copies: held in
+// registers, two rows a warp in flight, a prompt took 47 us.  A warp takes a row of
+// 256 elements (two of 128) at a time, a lane 16 bytes of it and, with
 // PKV_ROPE_HALF, the 16 bytes of its pairs' other elements.
 #include <algorithm>
 #include <cmath>
@@ -29,8 +34,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxPairs = kHeadDim / 2;
-constexpr int kBlockTokens = 4;  // of a CTA of large calls
-constexpr int kSegHeads = 64;    // query heads of a CTA
+constexpr int kBlockTokens = 4;  // of a unit of large calls
+constexpr int kSegHeads = 64;    // query heads of a unit
+constexpr int kStageBytes = 24 * 1024;  // of a unit of several tokens
+constexpr int kSmBytes = 228 * 1024, kStaticBytes = 6 * 1024, kCtas = 4;  // of an SM, of a CTA besides its stages, CTAs of an SM
 
 // Cosine and sine of position p at one pair's frequency, times the scale.
 __device__ __forceinline__ float2 turn(uint64_t turns, int32_t p, float scale) {
@@ -111,9 +118,21 @@ struct Turner {
 // The streams' first tokens, and how the launch is cut.
 struct RopeTokens {
     int32_t tok_off[PKV_MAX_SEQS];
-    int32_t total, block;  // tokens, and those of a CTA
-    int32_t segs;          // CTAs of a token: kSegHeads query heads each
+    int32_t total, block;  // tokens, and those of a unit
+    int32_t segs;          // units of a token: kSegHeads query heads each
     int32_t bytes;         // of a token's rows in shared memory
+    int32_t units, ctas;
+};
+// What a CTA works on at a time.
+struct RopeUnit {
+    int32_t tok0;
+    int n, seg;  // tokens; which of their heads
+    __device__ __forceinline__ RopeUnit(const RopeTokens &tk, int u) {
+        const int group = u / tk.segs;
+        seg = u - group * tk.segs;
+        tok0 = group * tk.block;
+        n = min(tk.block, tk.total - tok0);
+    }
 };
 // A CTA's token as its rows need it.
 struct TokenAt {
@@ -136,81 +155,133 @@ __device__ __forceinline__ void fill_turns(const pkv_rope &rope, const TokenAt *
     }
 }
 
-// Rows of kDim elements, c.n_q_heads a token.
-template <int kDim, int kMode>
-__global__ void __launch_bounds__(kThreads)
-    rope_rows(const __grid_constant__ Common c, const __grid_constant__ pkv_rope rope, const __grid_constant__ RopeRows r,
-              const __grid_constant__ RopeTokens tk) {
-    extern __shared__ __align__(16) uint8_t smem[];  // each token's rows
-    __shared__ __align__(16) float2 cs[kBlockTokens * kMaxPairs];
-    __shared__ TokenAt at[kBlockTokens];
-    __shared__ uint64_t full;
-    constexpr int kChunks = kDim / 8, kRowsWarp = 32 / kChunks;
-    const int group = blockIdx.x / tk.segs, seg = blockIdx.x - group * tk.segs;
-    const int32_t tok0 = group * tk.block, head0 = seg * kSegHeads;
-    const int n = min(tk.block, tk.total - tok0), heads = min(kSegHeads, c.n_q_heads - head0);
+// A CTA's way through its units, every tk.ctas-th: the next one's rows come while
+// this one's are turned.  load(unit, stage) and place(unit, places) start a unit's
+// copies (by the first warp) and find its tokens; rows(unit, stage) turns them.
+template <bool kTurns, typename Load, typename Place, typename Rows>
+__device__ __forceinline__ void through_units(const pkv_rope &rope, const RopeTokens &tk, bool pos_given, bool early,
+                                              uint64_t (&full)[2], TokenAt (&at)[2][kBlockTokens], float2 *cs, uint32_t *status,
+                                              const Load &load, const Place &place, const Rows &rows) {
     if (threadIdx.x == 0) {
-        mbar_init(&full, 1);
+        mbar_init(&full[0], 1);
+        mbar_init(&full[1], 1);
         fence_mbar_init();
     }
-    if (r.pos) pdl_wait();
-    if (threadIdx.x < n) {
-        const int tok = tok0 + threadIdx.x;
-        if (r.pos) {
-            at[threadIdx.x].pos = __ldg(r.pos + tok);
-        } else {
-            const int s = stream_of(c, tk, tok);
-            at[threadIdx.x].pos = c.seq[s].len - c.seq[s].n_new + (tok - tk.tok_off[s]);
+    int u = blockIdx.x;
+    RopeUnit now(tk, u), next = now;
+    if (pos_given) pdl_wait();
+    place(now, at[0]);
+    __syncthreads();
+    const bool before = kTurns && !pos_given && tk.block == 1;  // a small call's turns, beside the kernel before
+    if (before) fill_turns(rope, at[0], now.n, cs);
+    pdl_wait();
+    if (early && threadIdx.x == 0) pdl_trigger();
+    load(now, 0);
+    u += tk.ctas;
+    bool more = u < tk.units;
+    if (more) {
+        next = RopeUnit(tk, u);
+        load(next, 1);
+        place(next, at[1]);
+    }
+    for (int it = 0;; ++it) {
+        const int s = it & 1;
+        if (kTurns && !(before && it == 0)) fill_turns(rope, at[s], now.n, cs);
+        __syncthreads();
+        if (mbar_wait(&full[s], (it >> 1) & 1, status)) rows(now, s);
+        if (!more) return;
+        __syncthreads();  // the stage, its places and the turns are done with
+        now = next;
+        u += tk.ctas;
+        more = u < tk.units;
+        if (more) {
+            next = RopeUnit(tk, u);
+            load(next, s);
+            place(next, at[s]);
         }
     }
-    __syncthreads();
-    if (!r.pos && tk.block == 1) fill_turns(rope, at, n, cs);  // a small call's, beside the kernel before
-    pdl_wait();
-    if (threadIdx.x == 0) {
-        pdl_trigger();  // nothing here is read before a grid-dependency wait
+}
+
+// Rows of kDim elements, c.n_q_heads a token.
+template <int kDim, int kMode>
+__global__ void __launch_bounds__(kThreads, kCtas)
+    rope_rows(const __grid_constant__ Common c, const __grid_constant__ pkv_rope rope, const __grid_constant__ RopeRows r,
+              const __grid_constant__ RopeTokens tk) {
+    extern __shared__ __align__(16) uint8_t smem[];  // one or two stages of each token's rows
+    __shared__ __align__(16) float2 cs[kBlockTokens * kMaxPairs];
+    __shared__ TokenAt at[2][kBlockTokens];
+    __shared__ uint64_t full[2];
+    constexpr int kChunks = kDim / 8, kRowsWarp = 32 / kChunks;
+    const int stage_bytes = tk.block * tk.bytes;
+    const auto heads_of = [&](const RopeUnit &u) { return min(kSegHeads, c.n_q_heads - u.seg * kSegHeads); };
+    const auto load = [&](const RopeUnit &u, int stage) {
+        if (threadIdx.x) return;
         const uint64_t pol = policy_evict_first();
-        mbar_arrive_expect_tx(&full, n * heads * kDim * 2);
-        for (int k = 0; k < n; ++k)
-            bulk_g2s(smem + k * tk.bytes, r.q + (tok0 + k) * r.q_stride + (int64_t)head0 * kDim, heads * kDim * 2, &full, pol);
-    }
-    if (r.pos || tk.block > 1) fill_turns(rope, at, n, cs);
-    __syncthreads();
+        const int bytes = heads_of(u) * kDim * 2;
+        mbar_arrive_expect_tx(&full[stage], u.n * bytes);
+        for (int k = 0; k < u.n; ++k)
+            bulk_g2s(smem + stage * stage_bytes + k * tk.bytes, r.q + (u.tok0 + k) * r.q_stride + (int64_t)u.seg * kSegHeads * kDim, bytes,
+                     &full[stage], pol);
+    };
+    const auto place = [&](const RopeUnit &u, TokenAt *to) {
+        if (threadIdx.x >= u.n) return;
+        const int tok = u.tok0 + threadIdx.x;
+        if (r.pos) {
+            to[threadIdx.x].pos = __ldg(r.pos + tok);
+        } else {
+            const int s = stream_of(c, tk, tok);
+            to[threadIdx.x].pos = c.seq[s].len - c.seq[s].n_new + (tok - tk.tok_off[s]);
+        }
+    };
     const int lane = threadIdx.x & 31, ch = lane % kChunks, sub = lane / kChunks, ways = kWarps / tk.block;
     const int warp = threadIdx.x >> 5, k = warp / ways, first = warp - k * ways;
-    if (!mbar_wait(&full, 0, c.status) || k >= n) return;
-    const Turner<kMode> t(cs + k * kMaxPairs, ch, rope);
-    const uint16_t *const rows = reinterpret_cast<const uint16_t *>(smem + k * tk.bytes);
-    uint16_t *const dst = r.q_out + (tok0 + k) * r.q_out_stride + (int64_t)head0 * kDim;
-    for (int h = first * kRowsWarp + sub; h < heads; h += ways * kRowsWarp) {
-        float x[8];
-        t.turn_row(rows + h * kDim, x);
-        *(reinterpret_cast<uint4 *>(dst + h * kDim) + ch) = narrow(x);
-    }
+    const auto rows = [&](const RopeUnit &u, int stage) {
+        if (k >= u.n) return;
+        const Turner<kMode> t(cs + k * kMaxPairs, ch, rope);
+        const uint16_t *const src = reinterpret_cast<const uint16_t *>(smem + stage * stage_bytes + k * tk.bytes);
+        uint16_t *const dst = r.q_out + (u.tok0 + k) * r.q_out_stride + (int64_t)u.seg * kSegHeads * kDim;
+        for (int h = first * kRowsWarp + sub; h < heads_of(u); h += ways * kRowsWarp) {
+            float x[8];
+            t.turn_row(src + h * kDim, x);
+            *(reinterpret_cast<uint4 *>(dst + h * kDim) + ch) = narrow(x);
+        }
+    };
+    // (nothing here is read before a grid-dependency wait: the next kernel may start)
+    through_units<true>(rope, tk, r.pos != nullptr, true, full, at, cs, c.status, load, place, rows);
 }
 
 // A token's rows: its queries (when given), keys, values, indexer row.  kStill:
 // the keys are stored as they are (and there are no queries).  early: the next
 // kernel may start once all older ones are done, before the rows are there.
 template <bool kFp8, int kMode>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
     rope_store(const __grid_constant__ Common c, const __grid_constant__ pkv_rope rope, const __grid_constant__ RopeRows r,
                const __grid_constant__ RopeTokens tk, bool early) {
-    extern __shared__ __align__(16) uint8_t smem[];  // each token's rows: queries, K and V heads, indexer row
+    extern __shared__ __align__(16) uint8_t smem[];  // one or two stages of each token's queries, K and V heads, indexer row
     __shared__ __align__(16) float2 cs[kMode != kStill ? kBlockTokens * kMaxPairs : 1];
-    __shared__ TokenAt at[kBlockTokens];
-    __shared__ uint64_t full;
-    const int group = blockIdx.x / tk.segs, seg = blockIdx.x - group * tk.segs;
-    const int32_t tok0 = group * tk.block, head0 = seg * kSegHeads;
-    const int n = min(tk.block, tk.total - tok0), H = c.n_kv_heads;
-    const int nq = kMode != kStill && r.q ? min(kSegHeads, c.n_q_heads - head0) : 0, nkv = seg == 0 ? 2 * H : 0;
-    const int idx = seg == 0 ? c.idx_dim : 0;
-    if (threadIdx.x == 0) {
-        mbar_init(&full, 1);
-        fence_mbar_init();
-    }
-    if (r.pos) pdl_wait();
-    if (threadIdx.x < n) {
-        const int tok = tok0 + threadIdx.x, s = stream_of(c, tk, tok);
+    __shared__ TokenAt at[2][kBlockTokens];
+    __shared__ uint64_t full[2];
+    const int stage_bytes = tk.block * tk.bytes, H = c.n_kv_heads;
+    const auto queries = [&](const RopeUnit &u) { return kMode != kStill && r.q ? min(kSegHeads, c.n_q_heads - u.seg * kSegHeads) : 0; };
+    const auto load = [&](const RopeUnit &u, int stage) {
+        if (threadIdx.x >= 32) return;
+        const uint64_t pol = policy_evict_first();
+        const int q = queries(u) * kHeadDim * 2, kv = u.seg == 0 ? H * kHeadDim * 2 : 0, ik = u.seg == 0 ? c.idx_dim * 2 : 0;  // bytes
+        if (threadIdx.x == 0) mbar_arrive_expect_tx(&full[stage], u.n * (q + 2 * kv + ik));
+        __syncwarp();
+        const int k = threadIdx.x >> 2, part = threadIdx.x & 3;  // four parts a token
+        if (k < u.n) {
+            const int64_t tok = u.tok0 + k;
+            uint8_t *const to = smem + stage * stage_bytes + k * tk.bytes;
+            if (part == 0 && q) bulk_g2s(to, r.q + tok * r.q_stride + (int64_t)u.seg * kSegHeads * kHeadDim, q, &full[stage], pol);
+            if (part == 1 && kv) bulk_g2s(to + q, r.k + tok * r.k_stride, kv, &full[stage], pol);
+            if (part == 2 && kv) bulk_g2s(to + q + kv, r.v + tok * r.v_stride, kv, &full[stage], pol);
+            if (part == 3 && ik) bulk_g2s(to + q + 2 * kv, r.ik + tok * r.ik_stride, ik, &full[stage], pol);
+        }
+    };
+    const auto place = [&](const RopeUnit &u, TokenAt *to) {
+        if (threadIdx.x >= u.n) return;
+        const int tok = u.tok0 + threadIdx.x, s = stream_of(c, tk, tok);
         const SeqDev &sd = c.seq[s];
         TokenAt t;
         const int32_t place = sd.len - sd.n_new + (tok - tk.tok_off[s]);
@@ -218,7 +289,7 @@ __global__ void __launch_bounds__(kThreads)
         t.pos = r.pos ? __ldg(r.pos + tok) : place;
         t.page = const_cast<uint16_t *>(sd.layer_base);
         t.row = place;
-        if (sd.table && seg == 0) {
+        if (sd.table && u.seg == 0) {
             const int32_t p = place / sd.ptok, id = __ldg(sd.table + p);
             t.row = place - p * sd.ptok;
             if (static_cast<uint32_t>(id) < static_cast<uint32_t>(sd.n_pages)) {
@@ -228,40 +299,21 @@ __global__ void __launch_bounds__(kThreads)
                 if (c.status) atomicOr(c.status, PKV_DEV_BAD_PAGE);
             }
         }
-        at[threadIdx.x] = t;
-    }
-    __syncthreads();
-    const bool before = kMode != kStill && !r.pos && tk.block == 1;  // a small call's turns, beside the kernel before
-    if (before) fill_turns(rope, at, n, cs);
-    pdl_wait();
-    if (threadIdx.x < 32) {
-        if (early && threadIdx.x == 0) pdl_trigger();
-        const uint64_t pol = policy_evict_first();
-        if (threadIdx.x == 0) mbar_arrive_expect_tx(&full, n * ((nq + nkv) * kHeadDim + idx) * 2);
-        __syncwarp();
-        const int k = threadIdx.x >> 2, part = threadIdx.x & 3;  // four parts a token
-        if (k < n) {
-            const int64_t tok = tok0 + k;
-            uint8_t *const to = smem + k * tk.bytes;
-            const int kv = nkv / 2 * kHeadDim * 2;  // bytes of the keys, or the values
-            if (part == 0 && nq) bulk_g2s(to, r.q + tok * r.q_stride + (int64_t)head0 * kHeadDim, nq * kHeadDim * 2, &full, pol);
-            if (part == 1 && kv) bulk_g2s(to + nq * kHeadDim * 2, r.k + tok * r.k_stride, kv, &full, pol);
-            if (part == 2 && kv) bulk_g2s(to + nq * kHeadDim * 2 + kv, r.v + tok * r.v_stride, kv, &full, pol);
-            if (part == 3 && idx) bulk_g2s(to + nq * kHeadDim * 2 + 2 * kv, r.ik + tok * r.ik_stride, idx * 2, &full, pol);
-        }
-    }
-    if (kMode != kStill && !before) fill_turns(rope, at, n, cs);
-    __syncthreads();
+        to[threadIdx.x] = t;
+    };
     // a CTA's warps share its tokens out: eight, or fewer, to each, which take its rows in turn
     const int lane = threadIdx.x & 31, ways = kWarps / tk.block, warp = threadIdx.x >> 5, k = warp / ways, first = warp - k * ways;
-    if (mbar_wait(&full, 0, c.status) && k < n) {
+    const auto rows = [&](const RopeUnit &u, int stage) {
+        if (k >= u.n) return;
+        const int nq = queries(u), nkv = u.seg == 0 ? 2 * H : 0;
+        const bool idx = u.seg == 0 && c.idx_dim;
         const Turner<kMode> t(cs + (kMode != kStill ? k * kMaxPairs : 0), lane, rope);
-        const TokenAt place = at[k];
-        const uint16_t *const rows = reinterpret_cast<const uint16_t *>(smem + k * tk.bytes);
-        uint16_t *const dst = r.q_out + (tok0 + k) * r.q_out_stride + (int64_t)head0 * kHeadDim;
+        const TokenAt place = at[stage][k];
+        const uint16_t *const src = reinterpret_cast<const uint16_t *>(smem + stage * stage_bytes + k * tk.bytes);
+        uint16_t *const dst = r.q_out + (u.tok0 + k) * r.q_out_stride + (int64_t)u.seg * kSegHeads * kHeadDim;
         uint8_t *const b8 = reinterpret_cast<uint8_t *>(place.page);
         for (int i = first; i < nq + nkv + (idx ? 1 : 0); i += ways) {
-            const uint16_t *const row = rows + i * kHeadDim;
+            const uint16_t *const row = src + i * kHeadDim;
             if (i < nq) {
                 float x[8];
                 t.turn_row(row, x);
@@ -284,16 +336,17 @@ __global__ void __launch_bounds__(kThreads)
                 *reinterpret_cast<uint2 *>(b8 + off8_code(v, H, place.ptok, head, place.row) + lane * 8) = codes;
                 if (lane == 0) *reinterpret_cast<float *>(b8 + off8_scale(v, H, place.ptok, head, place.row)) = scale;
             } else {
-                uint4 u = *(reinterpret_cast<const uint4 *>(row) + lane);
+                uint4 o = *(reinterpret_cast<const uint4 *>(row) + lane);
                 if (!v && kMode != kStill) {
                     float x[8];
                     t.turn_row(row, x);
-                    u = narrow(x);
+                    o = narrow(x);
                 }
-                *(reinterpret_cast<uint4 *>(place.page + (v ? off_v(H, place.ptok, head, place.row) : off_k(place.ptok, head, place.row))) + lane) = u;
+                *(reinterpret_cast<uint4 *>(place.page + (v ? off_v(H, place.ptok, head, place.row) : off_k(place.ptok, head, place.row))) + lane) = o;
             }
         }
-    }
+    };
+    through_units<kMode != kStill>(rope, tk, r.pos != nullptr, early, full, at, cs, c.status, load, place, rows);
     pdl_trigger_after_writes();  // the next decode may read these rows early
 }
 
@@ -313,10 +366,10 @@ bool rope_shape_ok(int32_t rot_dim, int32_t pairs, const void *out) {
 
 }  // namespace
 
-// A launch's cut, `heads` query rows and `other` bytes of a token besides: tokens
-// of a CTA one while that fits the GPU about twice over, else up to four that take
-// 48 KB, so that four CTAs of an SM have 190 KB on their way.
-static RopeTokens tokens_of(const Common &c, int32_t total, int32_t heads, int32_t row_bytes, int32_t other, unsigned *grid) {
+// A launch's cut, `heads` query rows and `other` bytes of a token besides.  Large
+// calls: units of up to four tokens, as many CTAs as the GPU holds with two stages
+// of them each.
+static RopeTokens tokens_of(const Common &c, int32_t total, int32_t heads, int32_t row_bytes, int32_t other, int nsm, size_t *smem) {
     RopeTokens t;
     std::memset(&t, 0, sizeof(t));
     for (int s = 0; s < c.n_seqs; ++s) t.tok_off[s] = c.seq[s].tok_off;
@@ -324,15 +377,18 @@ static RopeTokens tokens_of(const Common &c, int32_t total, int32_t heads, int32
     t.segs = std::max(1, (heads + kSegHeads - 1) / kSegHeads);
     t.bytes = std::min(heads, kSegHeads) * row_bytes + other;
     t.block = 1;
-    while (total > 2048 && t.block < kBlockTokens && 2 * t.block * t.bytes <= 48 * 1024) t.block *= 2;
-    const int64_t ctas = ((int64_t)(total - 1) / t.block + 1) * t.segs;
-    *grid = ctas <= INT32_MAX ? static_cast<unsigned>(ctas) : 0;  // (none: more than a launch takes)
+    while (total > 2048 && t.block < kBlockTokens && 2 * t.block * t.bytes <= kStageBytes) t.block *= 2;
+    const int64_t units = ((int64_t)(total - 1) / t.block + 1) * t.segs;
+    t.units = units <= INT32_MAX / 2 ? static_cast<int32_t>(units) : 0;  // (none: more than a launch takes)
+    const int holds = std::min(kCtas, kSmBytes / (2 * t.block * t.bytes + kStaticBytes));
+    t.ctas = t.block == 1 ? t.units : std::min(t.units, nsm * std::max(1, holds));
+    *smem = static_cast<size_t>(t.ctas < t.units ? 2 : 1) * t.block * t.bytes;
     return t;
 }
 
 // A token of 64 query heads, 64 KV heads and an indexer row takes 97 KB; an SM left
 // with a small carveout could not take a CTA beside the kernel before.
-constexpr int kMaxSmem = (kSegHeads + 2 * 64) * kHeadDim * 2 + kIdxDim * 2;
+constexpr int kMaxSmem = std::max((kSegHeads + 2 * 64) * kHeadDim * 2 + kIdxDim * 2, 2 * kStageBytes);
 static int set_smem(const void *f) {
     if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem) != cudaSuccess) return PKV_ECUDA;
     return cuda_rc(cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared));
@@ -340,9 +396,12 @@ static int set_smem(const void *f) {
 
 int launch_rope_rows(const Common &c, int32_t total_tokens, const pkv_rope &rope, const RopeRows &r, int32_t dim,
                      cudaStream_t stream) {
-    unsigned grid;
-    const RopeTokens t = tokens_of(c, total_tokens, c.n_q_heads, dim * 2, 0, &grid);
-    if (grid == 0) return PKV_EINVAL;
+    int nsm = 0;
+    const int rc = sm_count(&nsm);
+    if (rc) return rc;
+    size_t smem;
+    const RopeTokens t = tokens_of(c, total_tokens, c.n_q_heads, dim * 2, 0, nsm, &smem);
+    if (t.units == 0) return PKV_EINVAL;
     using Kernel = void (*)(Common, pkv_rope, RopeRows, RopeTokens);
     const Kernel fns[2][3] = {{rope_rows<kIdxDim, kInside>, rope_rows<kIdxDim, kApart>, rope_rows<kIdxDim, kAnyhow>},
                               {rope_rows<kHeadDim, kInside>, rope_rows<kHeadDim, kApart>, rope_rows<kHeadDim, kAnyhow>}};
@@ -354,16 +413,19 @@ int launch_rope_rows(const Common &c, int32_t total_tokens, const pkv_rope &rope
             return PKV_OK;
         }) != PKV_OK)
         return PKV_ECUDA;
-    return launch_status(launch_pdl(fns[dim == kHeadDim][mode_of(rope) - kInside], grid, kThreads, t.block * t.bytes, stream, c,
+    return launch_status(launch_pdl(fns[dim == kHeadDim][mode_of(rope) - kInside], t.ctas, kThreads, smem, stream, c,
                                     rope, r, t));
 }
 
 int launch_rope_store(const Common &c, int32_t total_tokens, const pkv_rope *rope, const RopeRows &r, cudaStream_t stream,
                       bool early) {
-    unsigned grid;
+    int nsm = 0;
+    const int rc = sm_count(&nsm);
+    if (rc) return rc;
+    size_t smem;
     const RopeTokens t = tokens_of(c, total_tokens, rope && r.q ? c.n_q_heads : 0, kHeadDim * 2,
-                                   (2 * c.n_kv_heads * kHeadDim + c.idx_dim) * 2, &grid);
-    if (grid == 0) return PKV_EINVAL;
+                                   (2 * c.n_kv_heads * kHeadDim + c.idx_dim) * 2, nsm, &smem);
+    if (t.units == 0) return PKV_EINVAL;
     pkv_rope none;
     if (!rope) std::memset(&none, 0, sizeof(none));
     using Kernel = void (*)(Common, pkv_rope, RopeRows, RopeTokens, bool);
@@ -377,7 +439,7 @@ int launch_rope_store(const Common &c, int32_t total_tokens, const pkv_rope *rop
             return PKV_OK;
         }) != PKV_OK)
         return PKV_ECUDA;
-    return launch_status(launch_pdl(fns[c.kv_fp8 != 0][rope ? mode_of(*rope) : kStill], grid, kThreads, t.block * t.bytes, stream,
+    return launch_status(launch_pdl(fns[c.kv_fp8 != 0][rope ? mode_of(*rope) : kStill], t.ctas, kThreads, smem, stream,
                                     c, rope ? *rope : none, r, t, early));
 }
 

@@ -137,6 +137,31 @@ def test_store_with_many_heads(hkv, hq, tokens):
     assert torch().equal(a.mem, b.mem) and torch().equal(q, q2)
 
 
+@pytest.mark.parametrize("fmt", [pkv.KV_BF16, pkv.KV_E4M3])
+@pytest.mark.parametrize("given", [False, True])
+def test_a_large_call_is_its_small_ones(fmt, given):
+    """Units one after another in a CTA: the bits of calls of a CTA a token, positions of the cache's or given."""
+    rng, t = np.random.default_rng(21), torch()
+    lay, lens = pkv.layout(1, 2, 256, 128, fmt), [(6100, 6003), (3000, 2998), (40, 2)]
+    a, b = Pages(lay, lens, 48, 1), Pages(lay, lens, 48, 1)
+    tokens = sum(m for _, m in lens)
+    q, k, v = (dev(rs.random_rows(rng, tokens, h, 256)) for h in (6, 2, 2))
+    ik, r = dev(rs.random_rows(rng, tokens, 128)), pkv.rope(64, 1e4)
+    pos = t.randint(-50000, 50000, (tokens,), dtype=t.int32, device="cuda") if given else None
+    out, rows, small = t.empty_like(q), t.empty_like(q), t.empty_like(q)
+    pkv.rope_store(lay, a.seqs, 0, r, k, v, ik, n_q_heads=6, q=q, q_out=out, pos=pos)
+    pkv.rope_rows(r, a.seqs, 6, q, rows, pos=pos)
+    at = 0
+    for g, (n, m) in zip([x.pg for x in b.seqs], lens):
+        for first in range(0, m, 1000):
+            step = min(1000, m - first)
+            s = slice(at + first, at + first + step)
+            pkv.rope_store(lay, [pkv.seq(g, n - m + first + step, step)], 0, r, k[s], v[s], ik[s], n_q_heads=6, q=q[s], q_out=small[s],
+                           pos=pos[s] if given else None)
+        at += m
+    assert t.equal(a.mem, b.mem) and t.equal(out, small) and t.equal(rows, small)
+
+
 @pytest.mark.parametrize("pairs,rot", [(HALF, 256), (HALF, 20), (INTER, 64)])
 def test_in_place_and_strided_rows(pairs, rot):
     rng = np.random.default_rng(4)
