@@ -30,12 +30,13 @@
  *     and wait for it before touching anything it may write.  Two things are
  *     read before that wait: page tables, and the rows of cached positions
  *     more than 32 below a stream's new tokens (below len - n_new - 32) in
- *     pkv_decode / pkv_decode_static / pkv_window_decode.  So those must not
- *     be written by the kernel immediately before on the stream, unless that
- *     kernel is pkv_store, pkv_pages_copy or pkv_tables_remap, which make
- *     what they write visible before letting the next kernel start.  A
- *     pkv_decode or pkv_window_decode with k_new writes only its own new
- *     rows (at most 32 a stream), which for a stream decoding in order lie
+ *     pkv_decode / pkv_decode_static / pkv_window_decode / pkv_prefix_decode.
+ *     So those must not be written by the kernel immediately before on the
+ *     stream, unless that kernel is pkv_store, pkv_rope_store, pkv_pages_copy
+ *     or pkv_tables_remap, which make what they write visible before letting
+ *     the next kernel start.  A pkv_decode, pkv_window_decode or
+ *     pkv_prefix_decode with k_new writes only its own new rows (at most 32 a
+ *     stream), which for a stream decoding in order lie
  *     within the 32 positions below the next call's new tokens, so decode
  *     calls of the same stream and layer may follow each other directly.
  *     Rows, tables and inputs written earlier on the stream, or by a copy or
