@@ -77,11 +77,12 @@ extern "C" {
 #define PKV_DEV_SMEM 4u     /* a kernel's shared memory was not at the
                                alignment its layout needs; it did nothing  */
 #define PKV_DEV_RANGE 8u    /* the tensor-core attention (pkv_prefill, a decode
-                               call's tensor-core route, pkv_window_prefill)
-                               summed a non-finite value: a V entry beyond
-                               fp16's range (|v| > 65,504) in a call whose PV
-                               product runs in fp16, or non-finite inputs; or
-                               pkv_window_prefill met scores beyond 4.6e7  */
+                               call's tensor-core route, pkv_window_prefill,
+                               pkv_prefix_decode) summed a non-finite value: a
+                               V entry beyond fp16's range (|v| > 65,504) in a
+                               call whose PV product runs in fp16, or
+                               non-finite inputs; or one of the last two met
+                               scores beyond 4.6e7                         */
 
 /* kinds of rows (pkv_pg_row, pkv_gather) */
 #define PKV_K 0

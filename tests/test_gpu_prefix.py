@@ -340,6 +340,30 @@ def test_a_graph_and_calls_in_a_row(ballast):
     assert int(st) == 0
 
 
+@TOGETHER
+@pytest.mark.parametrize("fmt", [BF, E4])
+def test_storing_calls_in_a_row(fmt, ballast):
+    """Thirty tokens of each stream, stored by the calls, one call behind another: the bits of calls whose rows were there before."""
+    t, lay, hq, steps = torch(), pkv.layout(1, 2, 256, 128, fmt), 16, 30
+    s = Shared(lay, [([60, 90, 75], 9), ([40], 0)], 1, 64, n_q_heads=hq, ballast=ballast)
+    mem, nan = s.mem.clone(), t.full((4 * steps, 2, 256), 0x7FC1, dtype=t.int16, device="cuda")
+    pgs = [pkv.pg(mem, x, s.ps, 64, s.n_pages) for x in s.dev_tables]
+    pkv.store(lay, [pkv.seq(g, n, steps) for g, n in zip(pgs[:4], s.lens)], 0, nan, nan, nan[:, 0, :128].contiguous())
+    ik, ws = t.zeros((4 + ballast, 128), dtype=t.int16, device="cuda"), s.ws()
+    st = t.zeros(1, dtype=t.int32, device="cuda")
+    calls = []
+    for step in range(steps):
+        lens = [n - steps + 1 + step if i < 4 else n for i, n in enumerate(s.lens)]
+        new = [t.cat([s.dev(np.stack([x[i][lens[i] - 1] for i in range(4)])), y[4:]]) for x, y in ((s.k, s.k_new), (s.v, s.v_new))]
+        calls.append((lens, new, t.full_like(s.dq, 77), t.full_like(s.dq, 77)))
+    t.cuda.synchronize()
+    for lens, (k, v), out, _ in calls:
+        pkv.prefix_decode(lay, [pkv.seq(g, n, 1) for g, n in zip(pgs, lens)], s.groups, 0, hq, s.dq, out, ws, status=st, k_new=k, v_new=v, ik_new=ik)
+    for lens, _, _, out in calls:
+        pkv.prefix_decode(lay, [pkv.seq(g, n, 1) for g, n in zip(s.pgs, lens)], s.groups, 0, hq, s.dq, out, ws, status=st)
+    assert int(st) == 0 and all(t.equal(a, b) for _, _, a, b in calls)
+
+
 @pytest.mark.parametrize("forks,n", [(5, 1000), (47, 4000)])
 def test_forks_decoding_token_by_token(forks, n):
     """As it is used: a prompt stored and forked, its page copied, then steps of rope_store and prefix_decode of all forks, against
