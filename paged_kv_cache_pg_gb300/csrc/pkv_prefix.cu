@@ -62,6 +62,7 @@ constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(2
 constexpr float kRescale = 8.f;          // rescale O when the reference grows by more than 2^8
 constexpr float kFarScore = 67108864.f;  // 2^26: references beyond it are reported (float32 steps of 4 there)
 
+constexpr int kNear = 3;  // V exponents of a tile this near each other count as their largest
 constexpr int kHalfRow = 512, kHalfOut = 256;  // bytes of 128 of a row's float32 sums, of its outputs
 constexpr int kMaxSplits = 128;
 
@@ -77,7 +78,8 @@ struct Lay {
     static constexpr int off_red = off_raw + raw * kRawBytes;  // [parity][half][row]
     static constexpr int off_scl = off_red + 2 * 2 * kM * 4;   // [tile & 3][K scale, V exponent, V scale][key]
     static constexpr int off_info = off_scl + (kFp8 ? kInfo * 3 * kN * 4 : 0);  // [tile & 3][stream, position, keys][run]
-    static constexpr int off_bar = off_info + kInfo * 3 * (kN / kRun) * 4;
+    static constexpr int off_top = off_info + kInfo * 3 * (kN / kRun) * 4;  // [tile & 3]: the largest V exponent
+    static constexpr int off_bar = off_top + (kFp8 ? kInfo * 4 : 0);
     // barriers.  Of the first CTA, with arrivals from both: k_ready, v_ready,
     // q_full, s_empty, p_full.  Of each CTA: the others.
     static constexpr int k_full = 0, v_full = 3;      // copies landed (codes: the raw ring's, in k_full)
@@ -161,6 +163,17 @@ __device__ __forceinline__ void bulk_stores_done() {
     asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
 }
 
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
 // A pair's work.
 struct Work {
     int u, kvh, split;
@@ -223,7 +236,12 @@ struct Look {
     int s, pos, n;  // run lane & 7: its stream, its first position, its keys
 };
 
-template <bool kFp8>
+// kRuns: every unit has maps.  The roles share the instruction cache, and code that
+// a call does not need costs it: without the copies key by key (16 KB) e4m3 pages of
+// 128 took 36.5 us for 38.3, with a loop of its own for the masked tiles' conversion
+// and O corrected 16 columns at a time 35.3, with V exponents that lie near each
+// other taken as one 34.6.
+template <bool kFp8, bool kRuns>
 __global__ void __launch_bounds__(kThreads, 1)
     prefix_partial(const __grid_constant__ DecodeMaps maps, const __grid_constant__ PrefixArgs a) {
     using L = Lay<kFp8>;
@@ -466,13 +484,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int j = 0; j < 64; ++j)
                     if (!(see[j >> 5] & (1u << (j & 31)))) x[j] = -INFINITY;
             }
-            // this half's reference as eight interleaved chains, then the row's
+            // this half's reference as eight interleaved chains, then the row's.  V
+            // exponents near each other (a tile's mostly are) count as their largest: at
+            // most 3 of fp16's binades, for a third of the scales' reads
             const float2 qs2 = make_float2(qs, qs);
             float m8[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) m8[j] = -INFINITY;
+            const float top = kFp8 ? reinterpret_cast<const float *>(smem + L::off_top)[slot] : 0.f;
             if (!any) {
-            } else if constexpr (kFp8) {
+            } else if (kFp8 && top == INFINITY) {
 #pragma unroll
                 for (int j = 0; j < 64; j += 4) {
                     const float4 e = *reinterpret_cast<const float4 *>(scl + kN + j);
@@ -487,7 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 64; ++j) m8[j & 7] = fmaxf(m8[j & 7], x[j]);
             }
-            const float lmx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+            float lmx = fmaxf(fmaxf(fmaxf(m8[0], m8[1]), fmaxf(m8[2], m8[3])), fmaxf(fmaxf(m8[4], m8[5]), fmaxf(m8[6], m8[7])));
+            if (kFp8 && top != INFINITY) lmx = fmaf(lmx, qs, top);
             float omx = 0.f;
             if (!(ok = exchange(lmx, omx))) break;
             const float mx = fmaxf(lmx, omx) * (kFp8 ? 1.f : kScaleLog2);  // log2 units
@@ -499,12 +521,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float m_new = fmaxf(m_used, mx);
                 const float alpha = m_used == -INFINITY ? 0.f : ex2(m_used - m_new);
 #pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t o[32];
-                    tmem_ld32(lane_base + kOCol + 128 * hf + ch * 32, o);
+                for (int ch = 0; ch < 8; ++ch) {
+                    uint32_t o[16];
+                    tmem_ld16(lane_base + kOCol + 128 * hf + ch * 16, o);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                    tmem_st32(lane_base + kOCol + 128 * hf + ch * 32, o);
+                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                    tmem_st16(lane_base + kOCol + 128 * hf + ch * 16, o);
                 }
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 l *= alpha;
@@ -538,13 +560,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     p16[j / 2 + 1] = pack_f16(hi.x, hi.y);
                 }
                 l += (ps[0].x + ps[1].x) + (ps[0].y + ps[1].y);
-                if (masked) {  // a scale that the row does not see may be anything: 0 times it is not 0
-#pragma unroll
-                    for (int j = 0; j < 64; j += 2) {
-                        const uint32_t two = (see[j >> 5] >> (j & 31)) & 3u;
-                        p16[j / 2] &= ((two & 1u) ? 0xffffu : 0u) | ((two & 2u) ? 0xffff0000u : 0u);
-                    }
-                }
             } else {
                 const float2 scale = make_float2(kScaleLog2, kScaleLog2), off = make_float2(-m_off, -m_off);
                 float2 ps[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
@@ -646,11 +661,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ptok = su.ptok, n_pages = su.n_pages, shared = su.shared, keys = su.keys, s_first = su.s_first;
         const int64_t page_elems = su.ps;
         const uint64_t pol = policy_evict_normal();  // other units read the shared rows too
-        const void *const map = su.map_run >= 0 ? &maps.map[su.map_run] : nullptr;
+        const void *const map = kRuns || su.map_run >= 0 ? &maps.map[su.map_run] : nullptr;
         const int whole_map = is_v ? su.map_v : su.map_k;
         const void *const map_w = whole_map >= 0 ? &maps.map[whole_map] : nullptr;
         const uint8_t *const base = reinterpret_cast<const uint8_t *>(su.layer_base);
-        const bool runs = map != nullptr;
+        const bool runs = kRuns || map != nullptr;
         if (runs && lane == 0) {
             asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
             if (map_w) asm volatile("prefetch.tensormap [%0];" ::"l"(map_w) : "memory");
@@ -837,18 +852,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if constexpr (kFp8) {
                     float *const scl = reinterpret_cast<float *>(smem + L::off_scl) + is * 3 * kN + lane;
+                    int most = -127, least = 128;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         if (!is_v) {
                             scl[32 * i] = s_now[i];
                         } else {
+                            // Other streams' rows meet an own row with a weight of 0, which a
+                            // scale that is not finite must not make NaN: it counts as 0, and
+                            // flags its stream.  Behind the run's keys it may be anything.
+                            const int run = 2 * i + (lane >> 4);
+                            const int st = __shfl_sync(0xffffffffu, now.s, run), n = __shfl_sync(0xffffffffu, now.n, run);
+                            if ((lane & 15) >= n) {
+                                s_now[i] = 0.f;
+                            } else if (st >= 0 && !(fabsf(s_now[i]) < INFINITY)) {
+                                s_now[i] = 0.f;
+                                atomicOr(bad + ((st - s_first) >> 5), 1u << ((st - s_first) & 31));
+                            }
                             // 2^e <= scale < 2^(e+1).  Between 2^-40 and 2^80 the reference follows
                             // it; a smaller one's (values under 4e-10, or zeros) weights fade
                             // below fp16's range, and their sums stay in float32's
                             const int ex = static_cast<int>((__float_as_uint(s_now[i]) >> 23) & 0xffu) - 127;
-                            scl[kN + 32 * i] = static_cast<float>(min(max(ex, -40), 80));
+                            const int e = min(max(ex, -40), 80);
+                            scl[kN + 32 * i] = static_cast<float>(e);
                             scl[2 * kN + 32 * i] = s_now[i];
+                            most = max(most, e);
+                            least = min(least, e);
                         }
+                    }
+                    if (is_v) {
+                        most = __reduce_max_sync(0xffffffffu, most);
+                        least = __reduce_min_sync(0xffffffffu, least);
+                        if (lane == 0)
+                            reinterpret_cast<float *>(smem + L::off_top)[is] = most - least <= kNear ? static_cast<float>(most) : INFINITY;
                     }
                 }
                 __syncwarp();
@@ -951,6 +987,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *const to0 = dst + (((c0 + odd) ^ (r & 7)) << 4), *const to1 = dst + (((c0 + 1 - odd) ^ (r & 7)) << 4);
                 const uint32_t none = masked ? behind(run, r) : 0u;
                 uint32_t top = 0u;  // the largest magnitude's bits
+                if (!masked) {
 #pragma unroll 1
                 for (int i = 0; i < 8; i += 4) {
                     uint4 x[4];
@@ -958,16 +995,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (i + j) * step);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
+                        uint4 y0, y1;
+                        f16_of_codes(x[j].x, y0.x, y0.y);
+                        f16_of_codes(x[j].y, y0.z, y0.w);
+                        f16_of_codes(x[j].z, y1.x, y1.y);
+                        f16_of_codes(x[j].w, y1.z, y1.w);
+                        *reinterpret_cast<uint4 *>(to0 + (i + j) * step) = odd ? y1 : y0;
+                        *reinterpret_cast<uint4 *>(to1 + (i + j) * step) = odd ? y0 : y1;
+                    }
+                }
+                } else {
+#pragma unroll 1
+                for (int i = 0; i < 8; i += 2) {
+                    uint4 x[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (i + j) * step);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
                         if (none & (1u << (i + j))) x[j] = zero;
                         uint4 y0, y1;
                         f16_of_codes(x[j].x, y0.x, y0.y);
                         f16_of_codes(x[j].y, y0.z, y0.w);
                         f16_of_codes(x[j].z, y1.x, y1.y);
                         f16_of_codes(x[j].w, y1.z, y1.w);
-                        if (masked) top = __vmaxu2(top, __vmaxu2(largest(y0), largest(y1)));
+                        top = __vmaxu2(top, __vmaxu2(largest(y0), largest(y1)));
                         *reinterpret_cast<uint4 *>(to0 + (i + j) * step) = odd ? y1 : y0;
                         *reinterpret_cast<uint4 *>(to1 + (i + j) * step) = odd ? y0 : y1;
                     }
+                }
                 }
                 if (masked && not_finite(top)) {
 #pragma unroll 1
@@ -1269,11 +1324,15 @@ size_t prefix_ws_bytes(const Common &c, const pkv_group *groups, int32_t n_group
 
 int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &maps, const uint16_t *q, uint16_t *out, float *ws,
                   cudaStream_t stream) {
+    using Kernel = void (*)(DecodeMaps, PrefixArgs);
+    const Kernel fns[2][2] = {{prefix_partial<false, false>, prefix_partial<false, true>}, {prefix_partial<true, false>, prefix_partial<true, true>}};
     static std::atomic<uint64_t> attr_done{0};
-    if (once_per_device(attr_done, [] {
-            const cudaError_t e = cudaFuncSetAttribute(prefix_partial<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<false>::smem);
-            if (e != cudaSuccess) return PKV_ECUDA;
-            return cuda_rc(cudaFuncSetAttribute(prefix_partial<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay<true>::smem));
+    if (once_per_device(attr_done, [&] {
+            for (int i = 0; i < 4; ++i)
+                if (cudaFuncSetAttribute(fns[i >> 1][i & 1], cudaFuncAttributeMaxDynamicSharedMemorySize, i >> 1 ? Lay<true>::smem : Lay<false>::smem) !=
+                    cudaSuccess)
+                    return PKV_ECUDA;
+            return PKV_OK;
         }) != PKV_OK)
         return PKV_ECUDA;
     PrefixArgs a;
@@ -1302,8 +1361,9 @@ int launch_prefix(const Common &c, const PrefixPlan &plan, const DecodeMaps &map
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    auto *const fn = c.kv_fp8 ? prefix_partial<true> : prefix_partial<false>;
-    if (cudaLaunchKernelEx(&cfg, fn, maps, a) != cudaSuccess) return PKV_ECUDA;
+    bool runs = true;
+    for (int i = 0; i < plan.n_units; ++i) runs &= plan.unit[i].map_run >= 0;
+    if (cudaLaunchKernelEx(&cfg, fns[c.kv_fp8 != 0][runs], maps, a) != cudaSuccess) return PKV_ECUDA;
     if (!plan.merge) return PKV_OK;
     CombineArgs m;
     m.ws = ws;

@@ -248,6 +248,25 @@ def test_not_finite_in_an_own_row(fmt, ptok, where, dim, ballast):
 
 
 @TOGETHER
+@pytest.mark.parametrize("ptok", [64, 20])
+@pytest.mark.parametrize("bits", [0x7F80, 0x7FC0, 0xFF80])
+def test_not_finite_scale_of_an_own_row(ptok, bits, ballast):
+    """... of an e4m3 value row: its stream's outputs of that KV head are not finite, no other's change by a bit."""
+    lay = pkv.layout(1, 2, 256, 0, E4)
+    s = Shared(lay, [([90, 40, 33], 3), ([50, 60], 2)], [1, 2, 1, 1, 3], ptok, n_q_heads=4, ballast=ballast)
+    good = s.call()
+    at = pkv.pg_row(lay, s.pgs[1], s.tables[1], 0, pkv.VS, 1, s.lens[1] - 15)
+    s.mem.view(-1)[at // 2:at // 2 + 2] = s.dev(np.array([0, bits], np.uint16))   # (e4m3 offsets are in bytes)
+    st = torch().zeros(1, dtype=torch().int32, device="cuda")
+    got = s.call(status=st)
+    a, b = (bf16_values(x.cpu().numpy().view(np.uint16))[:-1] for x in (got, good))
+    assert (~np.isfinite(a[1:3, 2:])).any(-1).all() and int(st) & ~pkv.DEV_RANGE == 0
+    rest = np.ones(a.shape, bool)
+    rest[1:3, 2:] = False
+    assert np.array_equal(a[rest], b[rest])
+
+
+@TOGETHER
 def test_values_beyond_fp16_are_reported(ballast):
     """... where shared rows are read together: a stream alone is exact over bf16's range."""
     lay = pkv.layout(1, 1, 256, 0)
