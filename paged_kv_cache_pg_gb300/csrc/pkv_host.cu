@@ -770,7 +770,7 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
     // few that each stream reads them sooner by itself.  16 query and 2 KV heads, 100
     // own positions a stream, alone against together: 2 streams of 512 shared positions
     // 6.5 us against 13.1, of 4,096: 14.9, 14.4; 8 streams of 2,048: 11.3, 14.8, of
-    // 16,384: 33.4, 23.8; 64 streams of 512: 21.8, 22.0, of 2,048: 37.1, 23.0.  (Of 130
+    // 16,384: 33.4, 23.8; 64 streams of 512: 21.8, 22.0, of 2,048: 37.1, 23.0.  (Of 124
     // calls the worst choice costs a quarter.)  Not where it needs more workspace than
     // the size that was told.
     int nsm = 0;

@@ -312,7 +312,7 @@ struct alignas(128) PrefixUnit {
     int32_t nsplit, per;   // splits, and what each may cost (split_tile)
 };
 // First tile of split i: a tile of shared keys only costs kSharedCost, another
-// kOwnCost (1.39 and 1.68 us with 256 bf16 rows, 2.3 and 2.75 with e4m3 ones);
+// kOwnCost (1.39 and 1.68 us with 256 rows and bf16 pages, 1.75 and 2.1 with e4m3);
 // `per` is at least either, so no split is empty.
 constexpr int32_t kSharedCost = 5, kOwnCost = 6;
 __host__ __device__ inline int32_t split_tile(int32_t i, int32_t per, int32_t shared_tiles, int32_t tiles) {

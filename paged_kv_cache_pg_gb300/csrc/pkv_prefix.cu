@@ -33,12 +33,12 @@
 // them; a unit of one split writes its output itself.
 //
 // Of 64 streams on 31,000 shared positions (16 query and 2 KV heads, up to 1,000 own
-// positions each; 148 MB, 33.2 GFLOP) a call takes 53.3 us, 622 TFLOP/s: 23 tiles a
+// positions each; 148 MB, 33.2 GFLOP) a call takes 53.1 us, 624 TFLOP/s: 23 tiles a
 // pair of 2,950 cycles, whose 24 products alone take the tensor core 2,620 (16 of N =
 // 128 at 96, 8 of N = 256 at 135), 6 us to the first tile, 4.5 for the sums' way out
-// and 6 for the merge.  32 streams on 24,000 positions of e4m3 pages take 38.3 us:
-// tiles of 4,500 cycles, in which the softmax, its scales and the conversion of the
-// codes share the issue slots.
+// for the merge.  32 streams on 24,000 positions of e4m3 pages take 34.5 us: tiles
+// of 3,600 cycles, in which the conversion of 64 KB of codes by four warps is the
+// longest chain.
 #include <algorithm>
 #include <climits>
 
@@ -989,40 +989,40 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t top = 0u;  // the largest magnitude's bits
                 if (!masked) {
 #pragma unroll 1
-                for (int i = 0; i < 8; i += 4) {
-                    uint4 x[4];
+                    for (int i = 0; i < 8; i += 4) {
+                        uint4 x[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (i + j) * step);
+                        for (int j = 0; j < 4; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (i + j) * step);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint4 y0, y1;
-                        f16_of_codes(x[j].x, y0.x, y0.y);
-                        f16_of_codes(x[j].y, y0.z, y0.w);
-                        f16_of_codes(x[j].z, y1.x, y1.y);
-                        f16_of_codes(x[j].w, y1.z, y1.w);
-                        *reinterpret_cast<uint4 *>(to0 + (i + j) * step) = odd ? y1 : y0;
-                        *reinterpret_cast<uint4 *>(to1 + (i + j) * step) = odd ? y0 : y1;
+                        for (int j = 0; j < 4; ++j) {
+                            uint4 y0, y1;
+                            f16_of_codes(x[j].x, y0.x, y0.y);
+                            f16_of_codes(x[j].y, y0.z, y0.w);
+                            f16_of_codes(x[j].z, y1.x, y1.y);
+                            f16_of_codes(x[j].w, y1.z, y1.w);
+                            *reinterpret_cast<uint4 *>(to0 + (i + j) * step) = odd ? y1 : y0;
+                            *reinterpret_cast<uint4 *>(to1 + (i + j) * step) = odd ? y0 : y1;
+                        }
                     }
-                }
-                } else {
+                } else {  // in a loop of its own, so that the first one is small
 #pragma unroll 1
-                for (int i = 0; i < 8; i += 2) {
-                    uint4 x[2];
+                    for (int i = 0; i < 8; i += 2) {
+                        uint4 x[2];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (i + j) * step);
+                        for (int j = 0; j < 2; ++j) x[j] = *reinterpret_cast<const uint4 *>(src + (i + j) * step);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        if (none & (1u << (i + j))) x[j] = zero;
-                        uint4 y0, y1;
-                        f16_of_codes(x[j].x, y0.x, y0.y);
-                        f16_of_codes(x[j].y, y0.z, y0.w);
-                        f16_of_codes(x[j].z, y1.x, y1.y);
-                        f16_of_codes(x[j].w, y1.z, y1.w);
-                        top = __vmaxu2(top, __vmaxu2(largest(y0), largest(y1)));
-                        *reinterpret_cast<uint4 *>(to0 + (i + j) * step) = odd ? y1 : y0;
-                        *reinterpret_cast<uint4 *>(to1 + (i + j) * step) = odd ? y0 : y1;
+                        for (int j = 0; j < 2; ++j) {
+                            if (none & (1u << (i + j))) x[j] = zero;
+                            uint4 y0, y1;
+                            f16_of_codes(x[j].x, y0.x, y0.y);
+                            f16_of_codes(x[j].y, y0.z, y0.w);
+                            f16_of_codes(x[j].z, y1.x, y1.y);
+                            f16_of_codes(x[j].w, y1.z, y1.w);
+                            top = __vmaxu2(top, __vmaxu2(largest(y0), largest(y1)));
+                            *reinterpret_cast<uint4 *>(to0 + (i + j) * step) = odd ? y1 : y0;
+                            *reinterpret_cast<uint4 *>(to1 + (i + j) * step) = odd ? y0 : y1;
+                        }
                     }
-                }
                 }
                 if (masked && not_finite(top)) {
 #pragma unroll 1
@@ -1213,9 +1213,9 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas)
 // kernel.
 constexpr int64_t kTileCost[2] = {2200, 3000}, kPairCost = 7200, kRowsCost = 22, kMergeCost[2] = {4500, 5300};
 // ... and of the streams decoded alone: start, a thousand units of the windowed
-// plan's cost, a million keys, and what those take more with more than eight e4m3
-// columns.
-constexpr int64_t kAloneCost[2] = {0, 10000}, kAloneUnits[2] = {2060, 630}, kAloneKeys[2] = {28500, 78500}, kAloneWide = 178000;
+// plan's cost, a million keys, and what those take more with more than eight columns
+// a stream.
+constexpr int64_t kAloneCost[2] = {-800, 10000}, kAloneUnits[2] = {2200, 610}, kAloneKeys[2] = {22900, 79600}, kAloneWide[2] = {119000, 178000};
 
 }  // namespace
 
@@ -1305,7 +1305,7 @@ int64_t alone_cost(const Common &c, const WindowPlan &plan) {
     bool over8 = false;
     for (int s = 0; s < c.n_seqs; ++s) over8 |= c.seq[s].n_new * c.group > 8;
     return kAloneCost[fp8] + plan.cost * kAloneUnits[fp8] / 1000 +
-           plan.keys * (kAloneKeys[fp8] + (fp8 && over8 ? kAloneWide : 0)) / 1000000;
+           plan.keys * (kAloneKeys[fp8] + (over8 ? kAloneWide[fp8] : 0)) / 1000000;
 }
 
 // At most `slots` pairs of as many rows as a unit can have (or, with more units
