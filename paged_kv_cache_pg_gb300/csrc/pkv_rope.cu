@@ -10,9 +10,9 @@
 // A small call has a CTA a token.  A large one is cut into units of up to four
 // tokens, and as many CTAs as the GPU holds take every so many-th, the next unit's
 // rows on their way while one's are turned: a prompt of 8,192 tokens of 16 query and
-// 2 KV heads (172 MB) takes 32.9 us, 77 % of the copy rate, where CTAs of a unit
-// each took 34.1, 36.7 with units of 48 KB and two CTAs an SM.  (What is left: the
-// first rows' way in and the last ones' way out, and 7 units of 6.7 a CTA.)  A
+// 2 KV heads (172 MB) takes 31.6 us, 80 % of the copy rate (CTAs of a unit each took
+// 1.2 us longer, units of 48 KB and two CTAs an SM 3.8).  What is left: the first
+// rows' way in and the last ones' way out, and 7 units of 6.7 a CTA.  A
 // unit's tokens' streams, pages and rows are found once, by a thread a token (the
 // streams' first tokens lie together in the launch parameters: read from the
 // streams' own records, 64 of them took 6 us of a call), and their cosines and sines
@@ -37,7 +37,7 @@ constexpr int kMaxPairs = kHeadDim / 2;
 constexpr int kBlockTokens = 4;  // of a unit of large calls
 constexpr int kSegHeads = 64;    // query heads of a unit
 constexpr int kStageBytes = 24 * 1024;  // of a unit of several tokens
-constexpr int kSmBytes = 228 * 1024, kStaticBytes = 6 * 1024, kCtas = 4;  // of an SM, of a CTA besides its stages, CTAs of an SM
+constexpr int kSmBytes = 228 * 1024, kStaticBytes = 7 * 1024, kCtas = 4;  // of an SM, of a CTA besides its stages, CTAs of an SM
 
 // Cosine and sine of position p at one pair's frequency, times the scale.
 __device__ __forceinline__ float2 turn(uint64_t turns, int32_t p, float scale) {
@@ -146,12 +146,29 @@ __device__ __forceinline__ int stream_of(const Common &c, const RopeTokens &tk, 
     return find_seq(c.n_seqs, tok, [&](int t) { return tk.tok_off[t]; });
 }
 
-// The cosines and sines of n tokens.
-__device__ __forceinline__ void fill_turns(const pkv_rope &rope, const TokenAt *at, int n, float2 *cs) {
-    const int pairs = rope.rot_dim >> 1;
-    for (int i = threadIdx.x; i < n * pairs; i += kThreads) {
-        const int k = i / pairs, j = i - k * pairs;
-        cs[k * kMaxPairs + j] = turn(rope.turns[j], at[k].pos, rope.scale);
+// The cosines and sines of n tokens: a thread a pair, as many tokens at once as
+// that leaves threads for.
+struct Filler {
+    int pair, first, step;  // this thread's pair, its first token, and from one to the next (none: first >= kThreads)
+    __device__ __forceinline__ explicit Filler(int pairs) {
+        step = kThreads / pairs;
+        first = threadIdx.x / pairs;
+        pair = threadIdx.x - first * pairs;
+        if (first >= step) first = kThreads;
+    }
+    __device__ __forceinline__ void operator()(const uint64_t *turns, float scale, const TokenAt *at, int n, float2 *cs) const {
+        for (int k = first; k < n; k += step) cs[k * kMaxPairs + pair] = turn(turns[pair], at[k].pos, scale);
+    }
+};
+// The frequencies of the launch parameters, each by one thread, into shared memory:
+// read where they are, a warp's 32 different ones were as many reads one after the
+// other for every token (the prompt 32.8 us, 4,096 tokens' indexer queries 8.4 for
+// 7.4).
+__device__ __forceinline__ void copy_turns(const pkv_rope &rope, uint64_t *turns) {
+    if (threadIdx.x < rope.rot_dim >> 1) {
+        uint64_t v;
+        asm volatile("ld.u64 %0, [%1];" : "=l"(v) : "l"(rope.turns + threadIdx.x));
+        turns[threadIdx.x] = v;
     }
 }
 
@@ -160,7 +177,7 @@ __device__ __forceinline__ void fill_turns(const pkv_rope &rope, const TokenAt *
 // copies (by the first warp) and find its tokens; rows(unit, stage) turns them.
 template <bool kTurns, typename Load, typename Place, typename Rows>
 __device__ __forceinline__ void through_units(const pkv_rope &rope, const RopeTokens &tk, bool pos_given, bool early,
-                                              uint64_t (&full)[2], TokenAt (&at)[2][kBlockTokens], float2 *cs, uint32_t *status,
+                                              uint64_t (&full)[2], TokenAt (&at)[2][kBlockTokens], uint64_t *turns, float2 *cs, uint32_t *status,
                                               const Load &load, const Place &place, const Rows &rows) {
     if (threadIdx.x == 0) {
         mbar_init(&full[0], 1);
@@ -169,11 +186,13 @@ __device__ __forceinline__ void through_units(const pkv_rope &rope, const RopeTo
     }
     int u = blockIdx.x;
     RopeUnit now(tk, u), next = now;
+    if (kTurns) copy_turns(rope, turns);
+    const Filler fill(kTurns ? rope.rot_dim >> 1 : kMaxPairs);
     if (pos_given) pdl_wait();
     place(now, at[0]);
     __syncthreads();
     const bool before = kTurns && !pos_given && tk.block == 1;  // a small call's turns, beside the kernel before
-    if (before) fill_turns(rope, at[0], now.n, cs);
+    if (before) fill(turns, rope.scale, at[0], now.n, cs);
     pdl_wait();
     if (early && threadIdx.x == 0) pdl_trigger();
     load(now, 0);
@@ -186,7 +205,7 @@ __device__ __forceinline__ void through_units(const pkv_rope &rope, const RopeTo
     }
     for (int it = 0;; ++it) {
         const int s = it & 1;
-        if (kTurns && !(before && it == 0)) fill_turns(rope, at[s], now.n, cs);
+        if (kTurns && !(before && it == 0)) fill(turns, rope.scale, at[s], now.n, cs);
         __syncthreads();
         if (mbar_wait(&full[s], (it >> 1) & 1, status)) rows(now, s);
         if (!more) return;
@@ -209,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
               const __grid_constant__ RopeTokens tk) {
     extern __shared__ __align__(16) uint8_t smem[];  // one or two stages of each token's rows
     __shared__ __align__(16) float2 cs[kBlockTokens * kMaxPairs];
+    __shared__ uint64_t turns[kMaxPairs];
     __shared__ TokenAt at[2][kBlockTokens];
     __shared__ uint64_t full[2];
     constexpr int kChunks = kDim / 8, kRowsWarp = 32 / kChunks;
@@ -247,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
         }
     };
     // (nothing here is read before a grid-dependency wait: the next kernel may start)
-    through_units<true>(rope, tk, r.pos != nullptr, true, full, at, cs, c.status, load, place, rows);
+    through_units<true>(rope, tk, r.pos != nullptr, true, full, at, turns, cs, c.status, load, place, rows);
 }
 
 // A token's rows: its queries (when given), keys, values, indexer row.  kStill:
@@ -259,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
                const __grid_constant__ RopeTokens tk, bool early) {
     extern __shared__ __align__(16) uint8_t smem[];  // one or two stages of each token's queries, K and V heads, indexer row
     __shared__ __align__(16) float2 cs[kMode != kStill ? kBlockTokens * kMaxPairs : 1];
+    __shared__ uint64_t turns[kMode != kStill ? kMaxPairs : 1];
     __shared__ TokenAt at[2][kBlockTokens];
     __shared__ uint64_t full[2];
     const int stage_bytes = tk.block * tk.bytes, H = c.n_kv_heads;
@@ -346,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, kCtas)
             }
         }
     };
-    through_units<kMode != kStill>(rope, tk, r.pos != nullptr, early, full, at, cs, c.status, load, place, rows);
+    through_units<kMode != kStill>(rope, tk, r.pos != nullptr, early, full, at, turns, cs, c.status, load, place, rows);
     pdl_trigger_after_writes();  // the next decode may read these rows early
 }
 
