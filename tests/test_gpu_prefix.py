@@ -361,6 +361,31 @@ def test_a_graph_and_calls_in_a_row(ballast):
 
 @TOGETHER
 @pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("other", [20, 48, 128])
+def test_arenas_of_their_own(fmt, other, ballast):
+    """Groups of two arenas with pages of their own size, and a contiguous stream between them, in one call."""
+    t, lay, hq = torch(), pkv.layout(1, 2, 256, 0, fmt), 8
+    a = Shared(lay, [([9, 70], 7)], [1, 2], other, n_q_heads=hq, seed=1)
+    c = Shared(lay, [([333], 0)], 3, 64, n_q_heads=hq, seed=2)
+    b = Shared(lay, [([33, 4, 150], 5), ([20, 21], 1)], 2, 64, n_q_heads=hq, seed=3, ballast=ballast)
+    flat = t.full((1, pkv.page_elems(lay, 336)), 0x7FC1, dtype=t.int16, device="cuda")
+    alone = pkv.Pg(flat.data_ptr(), None, flat.shape[1], 336, 1, 1, 0)
+    pkv.store(lay, [pkv.seq(alone, 333, 333)], 0, c.dev(c.k[0]), c.dev(c.v[0]))
+    seqs, groups = a.seqs + [pkv.seq(alone, 333, 3)] + b.seqs, a.groups + [(1, 0)] + b.groups
+    q, st = t.cat([a.dq, c.dq, b.dq]), t.zeros(1, dtype=t.int32, device="cuda")
+    ws = t.full((max(64, pkv.prefix_decode_ws_size(lay, seqs, groups, hq) // 4),), float("nan"), device="cuda")
+    out = t.full((q.shape[0] + 1, hq, 256), 77, dtype=t.int16, device="cuda")
+    pkv.prefix_decode(lay, seqs, groups, 0, hq, q, out, ws, status=st)
+    assert int(st) == 0
+    end, at = out[-1:], 0
+    for s in (a, c, b):
+        n = s.dq.shape[0]
+        s.check(t.cat([out[at:at + n], end]))
+        at += n
+
+
+@TOGETHER
+@pytest.mark.parametrize("fmt", [BF, E4])
 def test_storing_calls_in_a_row(fmt, ballast):
     """Thirty tokens of each stream, stored by the calls, one call behind another: the bits of calls whose rows were there before."""
     t, lay, hq, steps = torch(), pkv.layout(1, 2, 256, 128, fmt), 16, 30
