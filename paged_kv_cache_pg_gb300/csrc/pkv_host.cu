@@ -628,7 +628,7 @@ static int prefix_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seq
     int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, c);
     if (rc) return rc;
     if (n_groups < 0 || n_groups > n_seqs || (n_groups > 0 && !groups)) return PKV_EINVAL;
-    std::memset(plan, 0, sizeof(*plan));
+    plan->n_groups = 0;
     plan->n_seqs = n_seqs;
     *shares = *may = false;
     const auto add = [&](int32_t s0, int32_t n, int32_t shared) -> bool {
@@ -643,6 +643,7 @@ static int prefix_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seq
         g.s0 = s0;
         g.n_seqs = n;
         g.tok0 = d.tok_off;
+        g.rows = 0;
         int64_t own = 0;
         for (int32_t s = s0; s < s0 + n; ++s) {
             const SeqDev &e = c->seq[s];
@@ -775,23 +776,22 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
     // the size that was told.
     int nsm = 0;
     bool together = shares;
-    Common ca = c;
     WindowPlan alone;
     int32_t window;
-    rc = plan_alone(ca, &alone, &window);
+    rc = plan_alone(c, &alone, &window);
     if (shares) {
         const bool no_plan = rc != PKV_OK;
         rc = sm_count(&nsm);
         if (rc) return rc;
         plan_prefix(c, nsm, &plan);
-        together = no_plan || plan.cost <= alone_cost(ca, alone) || alone.ws_bytes > prefix_ws_bytes(c, groups, n_groups, nsm);
+        together = no_plan || plan.cost <= alone_cost(c, alone) || alone.ws_bytes > prefix_ws_bytes(c, groups, n_groups, nsm);
     } else if (rc) {
         return rc;
     }
     if (!together) {
         if (alone.ws_bytes > 0 && (!ws || ws_bytes < alone.ws_bytes || (reinterpret_cast<uintptr_t>(ws) & 255u))) return PKV_EINVAL;
-        plan_window_maps(ca, L, seqs, maps);
-        return launch_window(ca, alone, maps, window, 0, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out),
+        plan_window_maps(c, L, seqs, maps);
+        return launch_window(c, alone, maps, window, 0, static_cast<const uint16_t *>(q), static_cast<uint16_t *>(out),
                              static_cast<float *>(ws), kn, vn, ikn, stream);
     }
     if (plan.floats > 0 &&

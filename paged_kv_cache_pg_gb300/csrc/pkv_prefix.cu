@@ -1246,6 +1246,7 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
             u.n_seqs = g.n_seqs;
             u.tok0 = g.tok0;
             u.map_k = u.map_v = u.map_run = -1;  // (plan_prefix_maps gives it its maps)
+            u.layer_row = 0;
             u.row0 = row0;
             u.rows = std::min(kUnitRows, g.rows - row0);
             const auto stream = [&](int row) {
@@ -1265,15 +1266,17 @@ void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
     const int fp8 = c.kv_fp8 ? 1 : 0;
     int64_t chosen = most;
     plan->cost = INT64_MAX;
-    for (int64_t k = 1; k <= std::min<int64_t>(slots, kMaxSplits); ++k) {
+    for (int64_t k = 1, last = 0; k <= std::min<int64_t>(slots, kMaxSplits); ++k) {
         const int64_t per = std::max<int64_t>(std::max(kSharedCost, kOwnCost), (most + k - 1) / k);
+        if (per == last) continue;
+        last = per;
         int64_t items = 0, rows = 0;
         for (int i = 0; i < plan->n_units; ++i) {
             const int64_t n = H * ((cost_of(plan->unit[i]) + per - 1) / per);
             items += n;
             rows += n * plan->unit[i].rows;
         }
-        if (items > cap) continue;
+        if (items > cap) break;  // (more splits have no fewer)
         const int64_t cost = (items + slots - 1) / slots * (per * kTileCost[fp8] / kSharedCost + kPairCost) +
                              (k > 1 ? rows * kRowsCost / 100 + kMergeCost[fp8] : 0);
         if (cost < plan->cost) {
