@@ -7,9 +7,8 @@
 // reads, and then the own positions of the streams whose rows these are, stream
 // after stream, each of which only its own rows read: counted through as virtual
 // keys, in runs of 16, 128 to a tile.  The products of the masked part are idle
-// work, but a tile's rows take longer to come from memory than its products
-// take, so the own parts cost what their bytes cost, and no second kernel with
-// partials of its own is needed.
+// work, a fifth more a tile than a shared one takes; a second kernel for the own
+// parts would need partials of its own, and a merge of both.
 //
 // A pair of CTAs (cta_group::2) takes a unit and a range of its tiles: each CTA
 // holds half of the rows, half of a tile's K (64 keys) and half of its V (128
@@ -36,8 +35,8 @@
 // positions each; 148 MB, 33.2 GFLOP) a call takes 53.1 us, 624 TFLOP/s: 23 tiles a
 // pair of 2,950 cycles, whose 24 products alone take the tensor core 2,620 (16 of N =
 // 128 at 96, 8 of N = 256 at 135), 6 us to the first tile, 4.5 for the sums' way out
-// for the merge.  32 streams on 24,000 positions of e4m3 pages take 34.5 us: tiles
-// of 3,600 cycles, in which the conversion of 64 KB of codes by four warps is the
+// and 6 for the merge.  32 streams on 24,000 positions of e4m3 pages take 34.5 us:
+// tiles of 3,600 cycles, in which the conversion of 64 KB of codes by four warps is the
 // longest chain.
 #include <algorithm>
 #include <climits>
@@ -1206,7 +1205,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas)
     *reinterpret_cast<uint2 *>(a.out + (int64_t)blockIdx.x * kHeadDim + 4 * (tid & 63)) = pk;
 }
 
-// Cost model in nanoseconds, fitted to 130 calls of 2 to 64 streams (128 to 31,000
+// Cost model in nanoseconds, fitted to 124 calls of 2 to 64 streams (128 to 31,000
 // shared positions, 100 to 2,000 own, 1 or 4 new tokens, 1 or 2 KV heads of 8
 // columns; within 14 % of each): a pair's tile of 128 shared keys (bf16, e4m3), its
 // start and end, a hundred rows of partials written and read again, and the merging
