@@ -159,7 +159,7 @@ __device__ __forceinline__ void bulk_s2g(void *dst, const void *src, uint32_t by
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void bulk_stores_done() {
-    asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
+    asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group.read 0;" ::: "memory");
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
     };
     auto wait_warp = [&](int bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
+    bool settled = false;  // each of the warp's arrivals at the first CTA's barriers has been waited for
     if (warp < kSoftWarps) {
         // ---------------- softmax ----------------
         const int r = lane + 32 * (warp & 3), hf = warp >> 2;
@@ -449,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_first(&bars[L::s_empty]);
+            if (lane == 0 && n + 1 < w.ntiles) arrive_first(&bars[L::s_empty]);
             if ((kFp8 || masked) && !(ok = wait_warp(L::info_full + slot, n / kInfo))) break;
             // the keys that the row sees, a bit each: of a run of its own stream those up
             // to its position, of a shared run those there are
@@ -652,6 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     atomicOr(a.status, PKV_DEV_RANGE);
             }
             bulk_stores_done();
+            settled = true;
         }
     } else if (warp == kWarpK || warp == kWarpV) {
         // ---------------- copies ----------------
@@ -1103,7 +1105,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     tc_fence_before();
-    cluster_sync();  // both CTAs are done with each other's barriers and products
+    // both CTAs are done with each other's barriers and products (a warp that has
+    // settled has nothing to release but its sums, which the kernel's end does)
+    __syncwarp();
+    if (settled)
+        asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+    else
+        asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     if (warp == kWarpS) {
         __syncwarp();
         tc_fence_after();
