@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return;
         }
     }
-    if (tid == 0) {
+    if (tid == 32 * (kWarpS - 1)) {  // (a warp that copies no parameters below)
         for (int i = 0; i < 3; ++i) {
             mbar_init(&bars[L::k_full + i], 1);
             mbar_init(&bars[L::v_full + i], 1);
