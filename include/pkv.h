@@ -526,9 +526,10 @@ int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t
  * heads), has pkv_window_decode's arithmetic, of a window of all positions.
  * Arithmetic of the others: tcgen05 products with float32 accumulation; Q and K
  * in bf16 (e4m3: fp16, exact, the query behind a power of two), P and V in fp16.
- * So a weight has 11 significant bits down to 2^-14 of the largest (below, it is
- * rounded to 2^-25 of that); a bf16 V entry is exact for magnitudes 2^-14 to
- * 65,280 and rounded to fp16's 2^-24 grid below that.  A V entry beyond 65,504,
+ * So a weight has 11 significant bits down to 2^-14 of the largest, and is
+ * rounded to a multiple of 2^-24 of that below (e4m3: weight times V scale, to
+ * 2^-23); a bf16 V entry is exact for magnitudes 2^-14 to 65,280 and rounded to
+ * fp16's 2^-24 grid below that.  A V entry beyond 65,504,
  * or not finite, makes outputs of its KV head that are not finite, for every
  * stream that reads it and no other, and sets PKV_DEV_RANGE, as does a largest
  * score (q.k / 16) beyond 4.6e7.  e4m3 V rows of any scale from 2^-40 to 2^80

@@ -61,7 +61,7 @@ constexpr float kScaleLog2 = 0.0625f * 1.4426950408889634f;  // log2(e) / sqrt(2
 constexpr float kRescale = 8.f;          // rescale O when the reference grows by more than 2^8
 constexpr float kFarScore = 67108864.f;  // 2^26: references beyond it are reported (float32 steps of 4 there)
 
-constexpr int kNear = 3;  // V exponents of a tile this near each other count as their largest
+constexpr int kNear = 1;  // V exponents of a tile this near each other count as their largest
 constexpr int kHalfRow = 512, kHalfOut = 256;  // bytes of 128 of a row's float32 sums, of its outputs
 constexpr int kMaxSplits = 128;
 
@@ -238,7 +238,7 @@ struct Look {
 // kRuns: every unit has maps.  The roles share the instruction cache, and code that
 // a call does not need costs it: without the copies key by key (16 KB) e4m3 pages of
 // 128 took 36.5 us for 38.3, with a loop of its own for the masked tiles' conversion
-// and O corrected 16 columns at a time 35.3, with V exponents that lie near each
+// and O corrected 16 columns at a time 35.3, with V exponents next to each
 // other taken as one 34.6.
 template <bool kFp8, bool kRuns>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -485,8 +485,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!(see[j >> 5] & (1u << (j & 31)))) x[j] = -INFINITY;
             }
             // this half's reference as eight interleaved chains, then the row's.  V
-            // exponents near each other (a tile's mostly are) count as their largest: at
-            // most 3 of fp16's binades, for a third of the scales' reads
+            // exponents next to each other (a tile's mostly are) count as the larger: one of
+            // fp16's binades, for a third of the scales' reads
             const float2 qs2 = make_float2(qs, qs);
             float m8[8];
 #pragma unroll

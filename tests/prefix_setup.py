@@ -113,11 +113,13 @@ class Shared:
         return out
 
     def reference(self):
-        """(outputs, sums of weight x |value|) in float64: [tokens][heads][256]."""
+        """In float64, [tokens][heads][256]: outputs, sums of weight x |value|, and the part of the bound that fp16's
+        grid of 2^-24 takes: the same sums with each weight (times the row's scale, e4m3) no more than 2^-23 of the
+        largest, and bf16 values below 2^-14 half a step off."""
         t = torch()
         fmt, h, d, grp = self.lay.kv_format, self.lay.n_kv_heads, 256, self.n_q_heads // self.lay.n_kv_heads
         q = t.from_numpy(bf16_values(self.q)).cuda()
-        out, size, tok = t.zeros_like(q), t.zeros_like(q), 0
+        out, size, small, tok = t.zeros_like(q), t.zeros_like(q), t.zeros_like(q), 0
 
         for i, m in enumerate(self.new[:len(self.k)]):
             if m == 0:
@@ -128,19 +130,26 @@ class Shared:
             pos = t.arange(n - m, n, device="cuda").repeat_interleave(grp)
             x = x.masked_fill(t.arange(n, device="cuda")[None, :] > pos[:, None], float("-inf"))
             p = t.softmax(x, -1)
-            for to, val in ((out, v), (size, v.abs())):
-                to[tok:tok + m] = (p @ val).view(h, m, grp, d).permute(1, 0, 2, 3).reshape(m, self.n_q_heads, d)
+            top = v.abs().amax(-1, keepdim=True).clamp_min(1e-300) if fmt == pkv.KV_E4M3 else t.ones_like(v[..., :1])   # a row's scale x 448
+            w = p * top.transpose(1, 2)
+            off = (v.abs() < 2.0 ** -14).double() * 2.0 ** -25 if fmt == pkv.KV_BF16 else t.zeros_like(v)
+            low = t.minimum(w, 2.0 ** -23 * w.amax(-1, keepdim=True))
+            for to, val in ((out, p @ v), (size, p @ v.abs()), (small, low @ (v.abs() / top) + p @ off)):
+                to[tok:tok + m] = val.view(h, m, grp, d).permute(1, 0, 2, 3).reshape(m, self.n_q_heads, d)
             tok += m
-        return out.cpu().numpy(), size.cpu().numpy()
+        return out.cpu().numpy(), size.cpu().numpy(), small.cpu().numpy()
 
     def check(self, out):
-        """A weight of the shared part has 11 significant bits (2^-11 of it at most; the own part's two bf16
-        parts 2^-15): that much of the sum of weight x |value|; float32 scores and sums of a few thousand
-        terms stay below 2^-14 of it; the output is rounded to bf16."""
+        """A weight has 11 significant bits (2^-11 of it at most): that much of the sum of weight x |value|; float32
+        scores and sums of a few thousand terms stay below 2^-14 of it; the output is rounded to bf16.  A weight
+        under 2^-14 of fp16's one, near which the largest lies or above (e4m3: weight x scale, no less than half of
+        it below), is rounded to the grid of 2^-24: no more than itself off, nor than 2^-25 of the largest (e4m3:
+        four times that, as the largest times its scale may be half of one, and a scale's mantissa is below 2).  A bf16
+        value below 2^-14 is rounded to that grid too: 2^-25 off."""
         got = bf16_values(out.cpu().numpy().view(np.uint16))
-        want, size = self.reference()
+        want, size, small = self.reference()
         assert np.isfinite(got[:-1]).all()
         got = got[:self.checked]
-        err = np.abs(got - want) - (2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14) * size + 1e-30)
+        err = np.abs(got - want) - (2.0 ** -8 * np.abs(want) + (2.0 ** -11 + 2.0 ** -14) * size + small + 1e-30)
         assert (err <= 0).all(), (err.max(), np.unravel_index(err.argmax(), err.shape))
         assert (out[-1] == 77).all()
