@@ -258,8 +258,15 @@ def _token_rows(what: str, name: str, t, dev: int, tokens: int, width: int):
         if t.is_contiguous():
             if t.numel() >= tokens * width:
                 return t.data_ptr(), 0
-        elif t.dim() >= 2 and t.shape[0] >= tokens and t[0].is_contiguous() and t[0].numel() == width:
-            return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0
+        else:  # (views made to ask them would take longer than the call)
+            n, shape, strides = 1, t.shape, t.stride()
+            for size, stride in zip(shape[:0:-1], strides[:0:-1]):
+                if size != 1 and stride != n:
+                    n = -1
+                    break
+                n *= size
+            if n == width and shape[0] >= tokens and (strides[0] or tokens <= 1):   # (0: one row, expanded)
+                return t.data_ptr(), strides[0] if tokens > 1 else 0
     raise PkvError(EINVAL, f"{what}: {name} is not a tensor of 16-bit rows, long enough, a token's rows together, on the current device")
 
 

@@ -124,3 +124,21 @@ def test_python_refuses_what_ctypes_would_cut():
         with pytest.raises(pkv.PkvError) as e:
             call()
         assert e.value.code == pkv.EINVAL
+
+
+def test_rows_that_lie_apart():
+    """Slices of wider rows are taken with their stride; what does not lie together, is too short or is one row expanded is refused."""
+    torch = pytest.importorskip("torch")
+    rows = lambda t, tokens, width: pkv._token_rows("x", "x", t, -1, tokens, width)  # noqa: E731
+    wide = torch.zeros((6, 40, 8), dtype=torch.int16)
+    part = wide[:, 3:19]
+    assert rows(part, 6, 128) == (part.data_ptr(), 320) and rows(part, 4, 128) == (part.data_ptr(), 320)
+    assert rows(part.flatten(1), 6, 128) == (part.data_ptr(), 320)      # (still a view)
+    assert rows(wide[::2, :16], 3, 128) == (wide.data_ptr(), 640) and rows(wide, 6, 320) == (wide.data_ptr(), 0)
+    one = torch.zeros((4, 8), dtype=torch.int16)
+    assert rows(one.expand(5, 4, 8), 1, 32) == (one.data_ptr(), 0)
+    assert rows(wide[:1, 3:19], 1, 128)[1] == 0 and rows(wide[:0, 3:19], 0, 128)[1] == 0
+    for bad, tokens, width in ((one.expand(5, 4, 8), 5, 32), (part, 7, 128), (part, 6, 120), (wide[:, ::2], 6, 160), (wide[..., :4], 6, 160),
+                               (wide.transpose(0, 1), 6, 48), (part.float(), 6, 128), (torch.zeros(40, dtype=torch.int16)[::2], 4, 5)):
+        with pytest.raises(pkv.PkvError):
+            rows(bad, tokens, width)
