@@ -813,25 +813,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             } else {
-                // key by key: 16-byte chunks through the same swizzle
+                // key by key: 16-byte chunks through the same swizzle, the row's place by one
+                // exchange (four, with the selects behind them, took a tile 3 us longer)
                 int64_t src[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) src[i] = row_bytes(page_at(now.id[i]), now.row[i]);
                 constexpr int kChunks = kFp8 ? 16 : 32;  // of a row
-                const int per = is_v ? kChunks / 2 : kChunks, rows_pass = 32 / per, n_rows = is_v ? 128 : 64;
+                const int per = is_v ? kChunks / 2 : kChunks, rows_pass = 32 / per, n_groups = is_v ? 4 : 2;
                 const int c = lane % per, sub = lane / per;
                 const int region = is_v ? 128 * 128 : 64 * 128;
+                const uint8_t *const chunk = base + 16 * ((is_v ? per * rank : 0) + c);
+#pragma unroll 1
+                for (int g = 0; g < n_groups; ++g) {
+                    // the group's 32 keys are src[at]'s (by selects: an index would put them in memory)
+                    const int at = is_v ? g : 2 * rank + g;
+                    const int64_t mine = at == 0 ? src[0] : at == 1 ? src[1] : at == 2 ? src[2] : src[3];
+                    uint8_t *const to = dst + (c >> 3) * region + 32 * g * 128;
 #pragma unroll 4
-                for (int r0 = 0; r0 < n_rows; r0 += rows_pass) {
-                    const int r = r0 + sub, key = (is_v ? 0 : 64 * rank) + r, i = key >> 5;
-                    // (the four values by selects: an index would put them in memory)
-                    const int64_t s0 = shfl64(src[0], key & 31), s1 = shfl64(src[1], key & 31);
-                    const int64_t s2 = shfl64(src[2], key & 31), s3 = shfl64(src[3], key & 31);
-                    const int64_t s = i == 0 ? s0 : i == 1 ? s1 : i == 2 ? s2 : s3;
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
-                                     smem_u32(dst + (c >> 3) * region + r * 128 + (((c & 7) ^ (r & 7)) << 4))),
-                                 "l"(base + s + 16 * ((is_v ? per * rank : 0) + c))
-                                 : "memory");
+                    for (int r0 = 0; r0 < 32; r0 += rows_pass) {
+                        const int r = r0 + sub;
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                                         smem_u32(to + r * 128 + (((c & 7) ^ (r & 7)) << 4))),
+                                     "l"(chunk + shfl64(mine, r))
+                                     : "memory");
+                    }
                 }
                 // the tensor cores read K through the async proxy: each lane waits
                 // for its copies and fences before the warp's arrival
