@@ -764,6 +764,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool waited = false;
         int last_q = -1;
         bool ok = true;
+        // Key by key, a bf16 tile's copies are on their way while the next one's are
+        // issued, and it is told of after that (45 streams on 6,168 positions, pages of
+        // 4: 68.4 us for 73.2; the codes' three slots are too few: 28.5 for 26.8 there).
+        // The tensor cores read K through the async proxy: each lane waits for its
+        // copies and fences before the warp's arrival.
+        uint64_t *held = nullptr;
+        auto landed = [&] {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(held);
+            held = nullptr;
+        };
         for (int m = 0; ok && m < w.ntiles; ++m) {
             // looked up while the slot is still being multiplied
             const Look now = look(m);
@@ -776,9 +788,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             // the slot
             const uint32_t q = kFp8 ? 2 * m + is_v : m;
             const uint32_t n_slots = kFp8 ? L::raw : L::slots, slot = q % n_slots;
-            if (q >= n_slots &&
-                !(ok = wait_warp((kFp8 ? L::raw_free : is_v ? L::v_free : L::k_free) + slot, q / n_slots - 1)))
-                break;
+            if (q >= n_slots) {
+                const int free = (kFp8 ? L::raw_free : is_v ? L::v_free : L::k_free) + slot;
+                const uint32_t phase = q / n_slots - 1;
+                // (nothing is held back from those who would free it)
+                if (held && !__all_sync(0xffffffffu, mbar_acquired(&bars[free], phase & 1))) {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    landed();
+                }
+                if (!(ok = wait_warp(free, phase))) break;
+            }
             uint64_t *const full = &bars[(kFp8 || !is_v ? L::k_full : L::v_full) + slot];
             uint8_t *const dst = smem + (kFp8 ? L::off_raw + slot * kRawBytes : (is_v ? L::off_v : L::off_k) + slot * kSlotBytes);
             if (runs) {
@@ -838,12 +857,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                      : "memory");
                     }
                 }
-                // the tensor cores read K through the async proxy: each lane waits
-                // for its copies and fences before the warp's arrival
-                asm volatile("cp.async.commit_group;\ncp.async.wait_group 0;" ::: "memory");
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (!kFp8 && held) {
+                    asm volatile("cp.async.wait_group 1;" ::: "memory");
+                    landed();
+                }
+                held = full;
+                if (kFp8) {
+                    asm volatile("cp.async.wait_group 0;" ::: "memory");
+                    landed();
+                }
             }
             last_q = static_cast<int>(q);
             // the runs' places, and with e4m3 the scales
@@ -896,6 +919,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars[L::info_full + is]);
             }
+        }
+        if (held) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+            landed();
         }
         if (!ok) {  // what was copied lands before the memory goes
             const int n_slots = kFp8 ? L::raw : L::slots, step = kFp8 ? 2 : 1;

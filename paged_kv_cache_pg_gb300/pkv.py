@@ -260,11 +260,16 @@ def _token_rows(what: str, name: str, t, dev: int, tokens: int, width: int):
                 return t.data_ptr(), 0
         else:  # (views made to ask them would take longer than the call)
             n, shape, strides = 1, t.shape, t.stride()
-            for size, stride in zip(shape[:0:-1], strides[:0:-1]):
-                if size != 1 and stride != n:
-                    n = -1
-                    break
-                n *= size
+            if len(strides) == 2 and strides[1] == 1:
+                n = shape[1]
+            elif len(strides) == 3 and strides[2] == 1 and strides[1] == shape[2]:
+                n = shape[1] * shape[2]
+            else:
+                for size, stride in zip(shape[:0:-1], strides[:0:-1]):
+                    if size != 1 and stride != n:
+                        n = -1
+                        break
+                    n *= size
             if n == width and shape[0] >= tokens and (strides[0] or tokens <= 1):   # (0: one row, expanded)
                 return t.data_ptr(), strides[0] if tokens > 1 else 0
     raise PkvError(EINVAL, f"{what}: {name} is not a tensor of 16-bit rows, long enough, a token's rows together, on the current device")
