@@ -325,6 +325,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         return ok;
     };
     auto wait_warp = [&](int bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
+    // The arrivals of the last products at the slots' barriers, which come to both CTAs
+    // of the pair whether or not a copy waits for the slot: neither CTA leaves before.
+    auto slots_free = [&](int bar) -> bool {
+        bool ok = true;
+        for (int n = max(0, w.ntiles - L::slots); ok && n < w.ntiles; ++n) ok = wait_warp(bar + n % L::slots, n / L::slots);
+        return ok;
+    };
     bool settled = false;  // each of the warp's arrivals at the first CTA's barriers has been waited for
     if (warp < kSoftWarps) {
         // ---------------- softmax ----------------
@@ -586,10 +593,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) arrive_first(&bars[L::p_full]);
         }
+        // The last products' arrival comes to both CTAs: warps without rows wait for it
+        // too, so that a CTA that has none is still there when it does
+        ok = ok && wait_warp(L::o_done, w.ntiles - 1);
         // ---------------- the split's sums to the workspace ----------------
         if (ok && active) {
             float other = 0.f;
-            ok = wait_warp(L::o_done, w.ntiles - 1) && exchange(l, other);
+            ok = exchange(l, other);
             l += other;
             // (and what the peer's converters flagged before those products)
             ok = ok && mbar_acquired(&bars[L::o_done], (w.ntiles - 1) & 1);
@@ -654,6 +664,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             bulk_stores_done();
             settled = true;
+        }
+        if (!ok && rank == 1 && warp == 0 && lane == 0) {  // (the first CTA's issuers gave up, or soon will)
+            wait_on(&bars[L::drain], 0, nullptr);
+            wait_on(&bars[L::drain + 1], 0, nullptr);
         }
     } else if (warp == kWarpK || warp == kWarpV) {
         // ---------------- copies ----------------
@@ -924,6 +938,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("cp.async.wait_group 0;" ::: "memory");
             landed();
         }
+        if constexpr (!kFp8) ok = ok && slots_free(is_v ? L::v_free : L::k_free);
         if (!ok) {  // what was copied lands before the memory goes
             const int n_slots = kFp8 ? L::raw : L::slots, step = kFp8 ? 2 : 1;
             for (int k = last_q; k >= 0 && k > last_q - n_slots; k -= step)
@@ -1075,6 +1090,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     arrive_first(&bars[(is_v ? L::v_ready : L::k_ready) + slot]);
                 }
             }
+            if (ok && warp == kWarpConv && slots_free(L::k_free)) slots_free(L::v_free);
         }
     } else {
         arrive();

@@ -1,0 +1,54 @@
+"""Decode over shared pages on the GPU: units of odd shapes, rows that some tokens must not see, workspaces, routes."""
+import numpy as np
+import pytest
+
+from paged_kv_cache_pg_gb300 import pkv
+
+from gpu_setup import torch
+from prefix_setup import Shared
+
+pytestmark = pytest.mark.gpu
+
+BF, E4 = pkv.KV_BF16, pkv.KV_E4M3
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from paged_kv_cache_pg_gb300 import build
+    build.build()
+    pkv.load()
+
+
+def decoded_alone(s, out):
+    """Whether these are the bits of pkv_window_decode over all positions, each stream by itself (its rows are stored by now)."""
+    t, n = torch(), max(s.lens)
+    ws = t.empty(max(64, pkv.window_decode_ws_size(s.lay, s.seqs, s.n_q_heads, n, 0) // 4), device="cuda")
+    alone = t.full_like(out, 77)
+    pkv.window_decode(s.lay, s.seqs, s.layer, s.n_q_heads, n, 0, s.dq, alone, ws)
+    return t.equal(out, alone)
+
+
+@pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("ptok", [64, 20])
+@pytest.mark.parametrize("own", [1, 130, 700])
+def test_units_of_one_row(fmt, ptok, own):
+    """A stream of one query head a KV head that shares nothing, beside groups that do: the second CTA of its pair has no row.
+    Splits of one tile and of several, calls in a row."""
+    lay = pkv.layout(1, 1, 256, 0, fmt)
+    s = Shared(lay, [([own], 0), ([3, 40], 700 // ptok), ([own], 2)], 1, ptok, n_q_heads=1, seed=own, ballast=24)
+    ws = s.ws()
+    outs = [s.call(ws=ws) for _ in range(4)]
+    s.check(outs[0])
+    assert not decoded_alone(s, outs[0])
+    assert all(torch().equal(outs[0], x) for x in outs[1:])
+
+
+@pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("ptok", [128, 20])
+def test_a_unit_of_256_rows_and_one_of_one(fmt, ptok):
+    """63 streams of four columns and one of five: the second unit is one row, whose stream's other rows are the first unit's."""
+    lay = pkv.layout(1, 1, 256, 0, fmt)
+    s = Shared(lay, [([5 + i for i in range(64)], 4096 // ptok)], [4] * 63 + [5], ptok, n_q_heads=1, fused=True)
+    out = s.call()
+    s.check(out)
+    assert not decoded_alone(s, out)
