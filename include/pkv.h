@@ -346,7 +346,8 @@ int pkv_rope_rows(const pkv_rope *rope, const pkv_seq *seqs, int32_t n_seqs, con
 /* pkv_store with the rotation on the way: the new tokens' keys are rotated and
  * go into their pages, values and indexer keys go there as they are, and with
  * q non-NULL the queries [tokens][n_q_heads][256] are rotated into q_out (which
- * may be q, as in pkv_rope_rows).  bf16 pages hold the same bytes as
+ * may be q, as in pkv_rope_rows, and must not overlap the rows of k_new, v_new
+ * and ik_new: EINVAL).  bf16 pages hold the same bytes as
  * pkv_rope_rows of the keys and pkv_store; e4m3 pages quantize the rotated keys
  * from float32, by pkv_store's rule (one rounding, where rotating first would
  * be two).  Strides of a token's rows in elements, 0 for packed rows, multiples

@@ -484,15 +484,17 @@ static bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_byt
     return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
 }
 
-// Rows read and written: the same ones in place, or apart (rows of other heads
-// between a token's rows, as in one projection's output, may interleave).
-static bool in_place_ok(const void *x, int64_t xs, const void *out, int64_t os, int64_t width, int64_t tokens) {
-    if (x == out) return xs == os;
+// Rows read and written: apart (rows of other heads between a token's rows, as in
+// one projection's output, may interleave), or the same ones in place.
+static bool rows_apart(const void *x, int64_t xs, int64_t x_width, const void *out, int64_t os, int64_t out_width, int64_t tokens) {
     const int64_t gap = (static_cast<const char *>(out) - static_cast<const char *>(x)) / 2;
-    if (!overlap(x, 2 * ((tokens - 1) * xs + width), out, 2 * ((tokens - 1) * os + width))) return true;
-    if (xs != os) return false;
+    if (!overlap(x, 2 * ((tokens - 1) * xs + x_width), out, 2 * ((tokens - 1) * os + out_width))) return true;
+    if (xs != os || tokens == 1) return false;
     const int64_t m = ((gap % xs) + xs) % xs;  // out's place among x's rows
-    return m >= width && m + width <= xs;
+    return m >= x_width && m + out_width <= xs;
+}
+static bool in_place_ok(const void *x, int64_t xs, const void *out, int64_t os, int64_t width, int64_t tokens) {
+    return x == out ? xs == os : rows_apart(x, xs, width, out, os, width, tokens);
 }
 
 }  // namespace pkv
@@ -611,6 +613,14 @@ extern "C" int pkv_rope_store(const pkv_layout *L, const pkv_seq *seqs, int32_t 
     if (tokens == 0) return PKV_OK;
     if (!k_new || !v_new || (L->idx_dim && !ik_new)) return PKV_EINVAL;
     if (!aligned16(k_new) || !aligned16(v_new) || (L->idx_dim && !aligned16(ik_new))) return PKV_EINVAL;
+    // a token's queries are written while other tokens' keys and values are still read
+    if (q) {
+        const int64_t width = (int64_t)n_q_heads * kHeadDim;
+        if (!rows_apart(k_new, r.k_stride, kv, q_out, r.q_out_stride, width, tokens) ||
+            !rows_apart(v_new, r.v_stride, kv, q_out, r.q_out_stride, width, tokens) ||
+            (L->idx_dim && !rows_apart(ik_new, r.ik_stride, L->idx_dim, q_out, r.q_out_stride, width, tokens)))
+            return PKV_EINVAL;
+    }
     r.q = static_cast<const uint16_t *>(q);
     r.q_out = static_cast<uint16_t *>(q_out);
     r.k = static_cast<const uint16_t *>(k_new);

@@ -359,3 +359,19 @@ def test_captured_on_another_stream_then_decoded():
             pkv.decode(lay, b.seqs, 0, hq, q2, out, ws)
             side.synchronize()
             assert t.equal(got, out)
+
+
+@pytest.mark.parametrize("tokens,spare", [(1, 0), (3, 0), (3, 8), (2500, 0)])
+def test_queries_turned_where_one_projection_has_them(tokens, spare):
+    """q_out beside the keys, values and indexer rows of the same projection's rows: these go into the pages as ever."""
+    rng, t = np.random.default_rng(tokens), torch()
+    lay, lens = pkv.layout(1, 2, 256, 128), [(tokens + 50, tokens)]
+    a, b = Pages(lay, lens, 16, 1), Pages(lay, lens, 16, 1)
+    flat = dev(rs.random_rows(rng, tokens, 6 * 256 + 2 * 512 + 128 + spare))
+    cut = lambda x: x[:, :6 * 256 + 2 * 512 + 128].split([6 * 256, 512, 512, 128], 1)  # noqa: E731
+    parts, r = [x.contiguous() for x in cut(flat)], pkv.rope(64, 1e4)
+    want, before = t.empty_like(parts[0]), flat.clone()
+    pkv.rope_store(lay, b.seqs, 0, r, *parts[1:], n_q_heads=6, q=parts[0], q_out=want)
+    q, k, v, ik = cut(flat)
+    pkv.rope_store(lay, a.seqs, 0, r, k, v, ik, n_q_heads=6, q=q, q_out=q)
+    assert t.equal(a.mem, b.mem) and t.equal(q, want) and t.equal(flat[:, 6 * 256:], before[:, 6 * 256:])

@@ -114,6 +114,18 @@ def test_store_refuses(lib):
     assert _store(lib, q=None, qs=4, n_new=0) == pkv.OK
 
 
+@pytest.mark.parametrize("n_new", [1, 2])
+@pytest.mark.parametrize("bad", [
+    dict(qo=0x300000), dict(qo=0x300000 + 512), dict(qo=0x400000 - 1024), dict(qo=0x500000 - 2048 + 16), dict(qo=0x500000 + 128),
+    dict(qo=0x400000, q=0x400000),                                                         # the queries and the values are the same rows
+    # one projection's rows of 2,304 elements (4 query heads, 2 of keys and of values, 128 indexer elements and 128 unused):
+    # queries out over the keys, over the end of the keys' and the indexer's row
+    *(dict(q=0x100000, qs=2304, qos=2304, k=0x100000 + 2048, ks=2304, v=0x100000 + 3072, vs=2304, ik=0x100000 + 4096, iks=2304, qo=0x100000 + at)
+      for at in (2048, 3072 - 16, 4096 + 240))])
+def test_store_refuses_queries_written_over_its_other_rows(lib, bad, n_new):
+    assert _store(lib, n_new=n_new, **bad) == pkv.EINVAL
+
+
 def test_python_refuses_what_ctypes_would_cut():
     lay = pkv.layout(1, 2)
     for call in (lambda: pkv.rope_store(lay, [], 1 << 32, pkv.rope(64), None, None),
