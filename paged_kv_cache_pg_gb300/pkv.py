@@ -246,17 +246,32 @@ def _new_tokens(what: str, seqs):
     return arr, n, read(arr)[0] if n == 1 else sum(read(arr)) if n else 0
 
 
+def _packed(shape, width: int) -> bool:
+    """Whether a contiguous tensor's shape is that of rows of `width` elements a
+    token: its last dimensions make up a token's row, or there is one dimension,
+    or two that are all tokens' heads and a head's row."""
+    n = 1
+    for size in shape[:0:-1]:
+        n *= size
+        if n == width:
+            return True
+    return len(shape) == 1 or width == 0 or len(shape) == 2 and n in (128, 256)
+
+
 def _token_rows(what: str, name: str, t, dev: int, tokens: int, width: int):
     """(address, elements from a token to the next) of 16-bit rows [tokens][...]
     of `width` elements a token.  A token's rows have to lie together; the
-    tokens may lie apart, as in a slice of a wider tensor.  An address given as
-    an int is one of packed rows."""
+    tokens may lie apart, as in a slice of a wider tensor.  A contiguous tensor
+    may have more tokens than the launch, of that width (a wider token's rows read
+    as packed ones would be other tokens').  An address given as an int is one of
+    packed rows."""
     if t is None or type(t) is int:
         return t, 0
     types = (_types or _row_types())[0]
     if t.get_device() == dev and t.dtype in types:
         if t.is_contiguous():
-            if t.numel() >= tokens * width:
+            have = t.numel()
+            if have == tokens * width or have > tokens * width and (tokens <= 1 or _packed(t.shape, width)):
                 return t.data_ptr(), 0
         else:  # (views made to ask them would take longer than the call)
             n, shape, strides = 1, t.shape, t.stride()

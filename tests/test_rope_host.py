@@ -154,3 +154,24 @@ def test_rows_that_lie_apart():
                                (wide.transpose(0, 1), 6, 48), (part.float(), 6, 128), (torch.zeros(40, dtype=torch.int16)[::2], 4, 5)):
         with pytest.raises(pkv.PkvError):
             rows(bad, tokens, width)
+
+
+def test_contiguous_rows_of_another_width():
+    """A longer contiguous tensor is packed rows where its shape says so; wider or narrower tokens are refused, as their slices are."""
+    torch = pytest.importorskip("torch")
+    rows = lambda t, tokens, width: pkv._token_rows("x", "x", t, -1, tokens, width)  # noqa: E731
+    z = lambda *shape: torch.zeros(shape, dtype=torch.int16)  # noqa: E731
+    for good, tokens, width in ((z(9, 16, 256), 6, 4096), (z(9, 4096), 6, 4096), (z(2, 3, 16, 256), 6, 4096), (z(3, 3, 16, 256), 6, 4096),
+                                (z(1, 9, 16, 256), 6, 4096), (z(9, 1, 256), 6, 256), (z(9 * 16, 256), 6, 4096), (z(9 * 4096), 6, 4096),
+                                (z(9, 128), 6, 128), (z(9 * 4, 128), 6, 512), (z(9, 16, 256), 1, 2048), (z(9, 16, 256), 0, 2048),
+                                (z(9, 128), 6, 0), (z(12, 8, 256), 6, 4096), (z(8, 16, 256)[:6], 6, 4096)):
+        assert rows(good, tokens, width) == (good.data_ptr(), 0), (good.shape, tokens, width)
+    for bad, tokens, width in ((z(6, 16, 256), 6, 2048), (z(9, 4096), 6, 2048), (z(13, 8, 256), 6, 4096), (z(9, 3, 128), 6, 256), (z(9, 2, 128), 4, 512),
+                               (z(6, 4096 + 8), 6, 4096), (z(6, 2, 16, 256), 6, 2048), (z(6, 256), 6, 128 * 3)):
+        with pytest.raises(pkv.PkvError):
+            rows(bad, tokens, width)
+    # as it is called: queries of 16 heads told to be of 8, 6 tokens
+    pkv_rows = lambda heads: pkv._token_rows("pkv_rope_rows", "x", z(6, 16, 256), -1, 6, heads * 256)  # noqa: E731
+    assert pkv_rows(16)[1] == 0
+    with pytest.raises(pkv.PkvError):
+        pkv_rows(8)
