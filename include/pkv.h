@@ -524,7 +524,9 @@ int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t
  * lie more than 32 positions below the new tokens.
  * A call that shares nothing, or whose shared rows are so few that its streams
  * read them sooner each by itself (a rule on the streams' numbers, lengths and
- * heads), has pkv_window_decode's arithmetic, of a window of all positions.
+ * heads), has pkv_window_decode's arithmetic, of a window of all positions (but
+ * not where a group of several streams has shared pages and one stream with new
+ * tokens, and that arithmetic takes more workspace than reading together).
  * Arithmetic of the others: tcgen05 products with float32 accumulation; Q and K
  * in bf16 (e4m3: fp16, exact, the query behind a power of two), P and V in fp16.
  * So a weight has 11 significant bits down to 2^-14 of the largest, and is
@@ -539,8 +541,9 @@ int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t
  * its pages lie.
  * ws: device, >= pkv_prefix_decode_ws_size bytes, 256-byte aligned, no
  * initialization, one ws per in-flight call.  The size for the longest own parts
- * (len - n_pages * page_pos) and the most new tokens covers shorter ones and
- * fewer, whatever the shared lengths.
+ * (len - n_pages * page_pos; in a group of one stream, which shares nothing, len)
+ * and the most new tokens covers shorter ones and fewer, whatever the shared
+ * lengths, also where one stream of a group alone still has new tokens.
  * EINVAL: groups that do not cover the streams exactly, a negative count, shared
  * pages without a table, of streams with another base, page size or arena, past a
  * table's end or past the cached rows, a stream of more than 2^29 positions, and

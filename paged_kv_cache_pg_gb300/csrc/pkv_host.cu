@@ -619,18 +619,25 @@ extern "C" int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t wind
 
 // ---- decode over shared pages ------------------------------------------------
 
+// What a call over shared pages shares.
+struct Sharing {
+    bool any;   // some streams' pages
+    bool may;   // some streams could
+    bool lone;  // a stream with queries has shared pages, and no other of its group queries
+};
+
 // Checks of a call over shared pages, and its streams and groups: those that share
 // pages (plan->n_groups counts them and, behind them, every other stream with
-// queries alone).  *shares: whether any do; *may: whether any could.
+// queries alone).
 static int prefix_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seqs, const pkv_group *groups,
                          int32_t n_groups, int32_t layer, int32_t n_q_heads, int32_t *dev_status, Common *c, PrefixPlan *plan,
-                         bool *shares, bool *may) {
+                         Sharing *sharing) {
     int rc = fill_common(L, seqs, n_seqs, layer, n_q_heads, dev_status, c);
     if (rc) return rc;
     if (n_groups < 0 || n_groups > n_seqs || (n_groups > 0 && !groups)) return PKV_EINVAL;
     plan->n_groups = 0;
     plan->n_seqs = n_seqs;
-    *shares = *may = false;
+    *sharing = {false, false, false};
     const auto add = [&](int32_t s0, int32_t n, int32_t shared) -> bool {
         PrefixGroup &g = plan->group[plan->n_groups++];
         const SeqDev &d = c->seq[s0];
@@ -673,9 +680,10 @@ static int prefix_common(const pkv_layout *L, const pkv_seq *seqs, int32_t n_seq
                 (int64_t)gr.n_pages * q.pg.page_pos > q.len - q.n_new)
                 return PKV_EINVAL;
         }
-        *may |= live > 1;
+        sharing->may |= gr.n_seqs > 1 && live > 0;
+        sharing->lone |= gr.n_seqs > 1 && live == 1 && gr.n_pages > 0;
         if (gr.n_pages > 0 && live > 1) {
-            *shares = true;
+            sharing->any = true;
             if (!add(s0, gr.n_seqs, gr.n_pages * first.page_pos)) return PKV_EINVAL;
         } else {
             for (int32_t s = s0; s < s0 + gr.n_seqs; ++s)
@@ -729,16 +737,18 @@ extern "C" int pkv_prefix_decode_ws_size(const pkv_layout *L, const pkv_seq *seq
     if (!bytes) return PKV_EINVAL;
     Common c;
     PrefixPlan plan;
-    bool shares, may;
-    int rc = prefix_common(L, seqs, n_seqs, groups, n_groups, 0, n_q_heads, nullptr, &c, &plan, &shares, &may);
+    Sharing sharing;
+    int rc = prefix_common(L, seqs, n_seqs, groups, n_groups, 0, n_q_heads, nullptr, &c, &plan, &sharing);
     if (rc) return rc;
     int nsm = 0;
     rc = sm_count(&nsm);
     if (rc) return rc;
-    const size_t shared = may ? prefix_ws_bytes(c, groups, n_groups, nsm) : 0;
-    // a call of these streams that shares nothing has their own positions only
-    for (int k = 0; k < plan.n_groups; ++k)
-        for (int s = plan.group[k].s0; s < plan.group[k].s0 + plan.group[k].n_seqs; ++s) c.seq[s].len -= plan.group[k].shared;
+    const size_t shared = sharing.may ? prefix_ws_bytes(c, groups, n_groups, nsm) : 0;
+    // a call of these streams that shares nothing has their own positions only (a group
+    // of one stream, all of its positions)
+    for (int32_t k = 0, s = 0; k < n_groups; ++k)
+        for (const int32_t end = s + groups[k].n_seqs; s < end; ++s)
+            if (groups[k].n_seqs > 1) c.seq[s].len -= groups[k].n_pages * seqs[s].pg.page_pos;
     WindowPlan alone;
     int32_t window;
     rc = plan_alone(c, &alone, &window);
@@ -753,8 +763,8 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
                                  int32_t *dev_status, cudaStream_t stream) {
     Common c;
     PrefixPlan plan;
-    bool shares, may;
-    int rc = prefix_common(L, seqs, n_seqs, groups, n_groups, layer, n_q_heads, dev_status, &c, &plan, &shares, &may);
+    Sharing sharing;
+    int rc = prefix_common(L, seqs, n_seqs, groups, n_groups, layer, n_q_heads, dev_status, &c, &plan, &sharing);
     if (rc) return rc;
     const int32_t tokens = total_new(c);
     if (tokens == 0) return PKV_OK;
@@ -772,19 +782,21 @@ extern "C" int pkv_prefix_decode(const pkv_layout *L, const pkv_seq *seqs, int32
     // own positions a stream, alone against together: 2 streams of 512 shared positions
     // 6.5 us against 13.1, of 4,096: 14.9, 14.4; 8 streams of 2,048: 11.3, 14.8, of
     // 16,384: 33.4, 23.8; 64 streams of 512: 21.8, 22.0, of 2,048: 37.1, 23.0.  (Of 124
-    // calls the worst choice costs a quarter.)  Not where it needs more workspace than
-    // the size that was told.
+    // calls the worst choice costs a quarter.)  Alone not where it needs more workspace
+    // than the size that was told, nor where the one stream of a group that queries does
+    // over the pages that it would share.
     int nsm = 0;
-    bool together = shares;
+    bool together = sharing.any;
     WindowPlan alone;
     int32_t window;
     rc = plan_alone(c, &alone, &window);
-    if (shares) {
+    if (sharing.any || sharing.lone) {
         const bool no_plan = rc != PKV_OK;
         rc = sm_count(&nsm);
         if (rc) return rc;
-        plan_prefix(c, nsm, &plan);
-        together = no_plan || plan.cost <= alone_cost(c, alone) || alone.ws_bytes > prefix_ws_bytes(c, groups, n_groups, nsm);
+        together = no_plan || alone.ws_bytes > prefix_ws_bytes(c, groups, n_groups, nsm);
+        if (together || sharing.any) plan_prefix(c, nsm, &plan);
+        together |= sharing.any && plan.cost <= alone_cost(c, alone);
     } else if (rc) {
         return rc;
     }

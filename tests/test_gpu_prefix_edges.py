@@ -52,3 +52,18 @@ def test_a_unit_of_256_rows_and_one_of_one(fmt, ptok):
     out = s.call()
     s.check(out)
     assert not decoded_alone(s, out)
+
+
+@pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("hkv,hq,new,pages", [(40, 40, 1, 11), (8, 16, 2, 190), (2, 16, 1, 830)])
+def test_the_told_workspace_covers_one_stream_left(fmt, hkv, hq, new, pages):
+    """Streams of a group end one after another; the size told while all decode, over less, is enough for the last one alone."""
+    t, lay, ptok = torch(), pkv.layout(1, hkv, 256, 0, fmt), 64
+    first = Shared(lay, [([20, 9], 1), ([30], 0)], new, ptok, n_q_heads=hq)
+    size = pkv.prefix_decode_ws_size(lay, first.seqs, first.groups, hq) // 4
+    for live in ([new, new, new], [0, new, 0], [new, 0, new], [1, 0, 0]):
+        s = Shared(lay, [([20, 9], pages), ([30], 0)], live, ptok, n_q_heads=hq)
+        assert pkv.prefix_decode_ws_size(lay, s.seqs, s.groups, hq) <= 4 * size
+        ws = t.full((size + 64,), 3.0, device="cuda")
+        s.check(s.call(ws=ws[:size]))
+        assert (ws[size:] == 3.0).all()
