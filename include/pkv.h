@@ -533,9 +533,11 @@ int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t
  * rounded to a multiple of 2^-24 of that below (e4m3: weight times V scale, to
  * 2^-23); a bf16 V entry is exact for magnitudes 2^-14 to 65,280 and rounded to
  * fp16's 2^-24 grid below that.  A V entry beyond 65,504,
- * or not finite, makes outputs of its KV head that are not finite, for every
- * stream that reads it and no other, and sets PKV_DEV_RANGE, as does a largest
- * score (q.k / 16) beyond 4.6e7.  e4m3 V rows of any scale from 2^-40 to 2^80
+ * or not finite, makes outputs of its KV head that are not finite, for every new
+ * token that reads it and no other, and sets PKV_DEV_RANGE, as does a largest
+ * score (q.k / 16) beyond 4.6e7.  (Streams that are decoded alone follow
+ * pkv_window_decode here too: a row that some of a stream's new tokens read and
+ * others do not must hold finite values.)  e4m3 V rows of any scale from 2^-40 to 2^80
  * keep their precision.
  * Results follow the call's shape (its groups, lengths and new tokens), not where
  * its pages lie.

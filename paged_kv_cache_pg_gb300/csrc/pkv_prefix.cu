@@ -22,7 +22,8 @@
 // maximum of score + V-scale exponent, so that they stay in fp16's range
 // wherever the scales lie.  An own V row that is not finite in fp16 (or lies
 // behind its stream's end) is multiplied as zeros, because the other streams'
-// rows meet it with a weight of 0; its stream's sums become NaN instead.
+// rows meet it with a weight of 0; the sums of its stream's rows that read it become
+// NaN instead.
 //   warps 0-7   softmax: two threads a row, each on 64 of a tile's keys
 //   warps 8, 9  copy K and V (halves of one page, of 16-row runs, or key by key)
 //   warps 10-13 convert
@@ -90,7 +91,7 @@ struct Lay {
     static constexpr int info_full = 30, info_free = info_full + kInfo;
     static constexpr int drain = info_free + kInfo;
     static constexpr int bars = drain + 2;
-    static constexpr int smem = off_bar + bars * 8 + 16;  // behind the barriers: TMEM address, flags
+    static constexpr int smem = off_bar + bars * 8 + 16 + PKV_MAX_SEQS * 4;  // behind the barriers: TMEM address, flag, positions
     static_assert(smem <= 232448, "above the 227 KB a CTA may hold");
     static_assert(off_k + kSoftWarps * 32 * kHalfRow <= off_red, "the sums fit in the slots");
 };
@@ -248,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::off_bar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::bars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    uint32_t *const bad = tmem_slot + 2;  // streams (from the unit's first) with a V row that is not finite
+    int *const bad = reinterpret_cast<int *>(tmem_slot + 4);  // of each stream (from the unit's first): its first V row that is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cta_rank());
     {
@@ -285,9 +286,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (tid == kThreads - 1) {
-        bad[0] = bad[1] = 0u;
-        asm volatile("fence.acq_rel.cluster;" ::: "memory");  // (the peer sets bits of it)
+    if (warp == kWarpPv) {
+        bad[lane] = bad[lane + 32] = INT_MAX;
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");  // (the peer lowers them)
     }
     if (warp == kWarpS) {
         __syncwarp();
@@ -615,11 +616,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool single = u.nsplit == 1;
             const int wr = 32 * (warp & 3), key = (w.first + r) & 7;
             uint8_t *const stage = smem + L::off_k + warp * 32 * kHalfRow, *const mine = stage + lane * (single ? kHalfOut + 16 : 128);
-            bool odd_row = false;
-            if (row_ok) {
-                const int i = my - u.s_first;
-                odd_row = (reinterpret_cast<volatile uint32_t *>(bad)[i >> 5] >> (i & 31)) & 1u;
-            }
+            // (a new token does not read its stream's later ones)
+            const bool odd_row = row_ok && reinterpret_cast<volatile int *>(bad)[my - u.s_first] <= qpos;
             if (odd_row) l = __uint_as_float(0x7fffffffu);
             const float inv = 1.f / l;
             const int64_t split = (int64_t)w.kvh * u.nsplit + w.split;
@@ -903,14 +901,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
                             // Other streams' rows meet an own row with a weight of 0, which a
                             // scale that is not finite must not make NaN: it counts as 0, and
-                            // flags its stream.  Behind the run's keys it may be anything.
+                            // its place is kept.  Behind the run's keys it may be anything.
                             const int run = 2 * i + (lane >> 4);
                             const int st = __shfl_sync(0xffffffffu, now.s, run), n = __shfl_sync(0xffffffffu, now.n, run);
+                            const int pos = __shfl_sync(0xffffffffu, now.pos, run) + (lane & 15);
                             if ((lane & 15) >= n) {
                                 s_now[i] = 0.f;
                             } else if (st >= 0 && !(fabsf(s_now[i]) < INFINITY)) {
                                 s_now[i] = 0.f;
-                                atomicOr(bad + ((st - s_first) >> 5), 1u << ((st - s_first) & 31));
+                                atomicMin(bad + (st - s_first), pos);
                             }
                             // 2^e <= scale < 2^(e+1).  Between 2^-40 and 2^80 the reference follows
                             // it; a smaller one's (values under 4e-10, or zeros) weights fade
@@ -950,11 +949,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         meet();
         const int t = tid - kWarpConv * 32;
         bool ok = true;
-        const auto flag = [&](int s) {  // in both CTAs: each converts half of the dims
-            const int i = s - u.s_first;
+        const auto flag = [&](int s, int pos) {  // in both CTAs: each converts half of the dims
             for (uint32_t r = 0; r < 2; ++r)
-                asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(peer_addr(bad + (i >> 5), r)),
-                             "r"(1u << (i & 31))
+                asm volatile("red.relaxed.cluster.shared::cluster.min.s32 [%0], %1;" ::"r"(peer_addr(bad + (s - u.s_first), r)), "r"(pos)
                              : "memory");
             asm volatile("fence.acq_rel.cluster;" ::: "memory");
         };
@@ -1003,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 16; ++i) {
                         if (run[i & 7] >= 0 && not_finite(largest(v[i * 128]))) {
                             v[i * 128] = zero;
-                            flag(run[i & 7]);
+                            flag(run[i & 7], run[8 + (i & 7)] + (t >> 3));
                         }
                     }
                 }
@@ -1078,7 +1075,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint4 *const y0 = reinterpret_cast<uint4 *>(to0 + i * step), *const y1 = reinterpret_cast<uint4 *>(to1 + i * step);
                         if (run[i] >= 0 && not_finite(__vmaxu2(largest(*y0), largest(*y1)))) {
                             *y0 = *y1 = zero;
-                            flag(run[i]);
+                            flag(run[i], run[8 + i] + r);
                         }
                     }
                 }

@@ -6,6 +6,7 @@ from paged_kv_cache_pg_gb300 import pkv
 
 from gpu_setup import torch
 from prefix_setup import Shared
+from rope_setup import bf16_bits, bf16_values
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,48 @@ def test_the_told_workspace_covers_one_stream_left(fmt, hkv, hq, new, pages):
         ws = t.full((size + 64,), 3.0, device="cuda")
         s.check(s.call(ws=ws[:size]))
         assert (ws[size:] == 3.0).all()
+
+
+@pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("ptok", [64, 20])
+@pytest.mark.parametrize("where,value", [("k", np.nan), ("v", np.nan), ("v", np.inf), ("v", 70000.0)])
+@pytest.mark.parametrize("back", [1, 2, 3])
+def test_a_draft_token_does_not_read_later_rows_that_are_not_finite(fmt, ptok, where, value, back):
+    """The row `back` before the end of a stream of four draft tokens: those before it keep their bits, as all other streams."""
+    t, lay = torch(), pkv.layout(1, 2, 256, 0, fmt)
+    s = Shared(lay, [([90, 40, 33], 3), ([20], 0)], [1, 4, 4, 2], ptok, n_q_heads=4, ballast=24)
+    good = s.call()
+    assert not decoded_alone(s, good)
+    n = s.lens[1]
+    getattr(s, where)[1][n - back, 0, [5, 200]] = bf16_bits(np.array([value]))[0]
+    pkv.store(lay, [pkv.seq(s.pgs[1], n, n)], 0, s.dev(s.k[1]), s.dev(s.v[1]))
+    st = t.zeros(1, dtype=t.int32, device="cuda")
+    out = s.call(status=st)
+    a, b = (bf16_values(x.cpu().numpy().view(np.uint16))[:-1] for x in (out, good))
+    if fmt == E4 and value == 70000.0:
+        # A row of 70,000 is finite there: codes of up to 448 with a scale of 70000 / 448.  The reference that a tile's
+        # weights are rounded against follows its scales, so others' bits may change: all of it against the definition.
+        assert int(st) == 0
+        s.check(out)
+        return
+    reads = np.zeros(a.shape, bool)
+    reads[5 - back:5, :2] = True      # tokens 1 .. 4 are the stream's
+    assert np.array_equal(a[~reads], b[~reads])
+    assert (~np.isfinite(a[5 - back:5, :2])).any(-1).all() and int(st) & ~pkv.DEV_RANGE == 0
+    assert where == "k" or int(st) == pkv.DEV_RANGE
+
+
+@pytest.mark.parametrize("ptok", [64, 20])
+@pytest.mark.parametrize("bits", [0x7F80, 0x7FC0])
+def test_nor_later_scales_that_are_not_finite(ptok, bits):
+    """... of an e4m3 value row."""
+    lay = pkv.layout(1, 2, 256, 0, E4)
+    s = Shared(lay, [([90, 40, 33], 3)], [1, 4, 4], ptok, n_q_heads=4, ballast=24)
+    good = s.call()
+    at = pkv.pg_row(lay, s.pgs[1], s.tables[1], 0, pkv.VS, 1, s.lens[1] - 2)
+    s.mem.view(-1)[at // 2:at // 2 + 2] = s.dev(np.array([0, bits], np.uint16))   # (e4m3 offsets are in bytes)
+    st = torch().zeros(1, dtype=torch().int32, device="cuda")
+    a, b = (bf16_values(x.cpu().numpy().view(np.uint16))[:-1] for x in (s.call(status=st), good))
+    reads = np.zeros(a.shape, bool)
+    reads[3:5, 2:] = True
+    assert np.array_equal(a[~reads], b[~reads]) and (~np.isfinite(a[3:5, 2:])).any(-1).all() and int(st) == pkv.DEV_RANGE
