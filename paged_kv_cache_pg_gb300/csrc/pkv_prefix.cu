@@ -91,7 +91,7 @@ struct Lay {
     static constexpr int info_full = 30, info_free = info_full + kInfo;
     static constexpr int drain = info_free + kInfo;
     static constexpr int bars = drain + 2;
-    static constexpr int smem = off_bar + bars * 8 + 16 + PKV_MAX_SEQS * 4;  // behind the barriers: TMEM address, flag, positions
+    static constexpr int smem = off_bar + bars * 8 + 4 + PKV_MAX_SEQS * 4;  // behind the barriers: TMEM address, positions
     static_assert(smem <= 232448, "above the 227 KB a CTA may hold");
     static_assert(off_k + kSoftWarps * 32 * kHalfRow <= off_red, "the sums fit in the slots");
 };
@@ -118,7 +118,8 @@ __device__ __forceinline__ void arrive_first(uint64_t *bar) {  // at the first C
 // A bounded wait as mbar_wait, in few instructions where it is called: sixteen
 // warps in six roles share the instruction cache, and with each role's loop
 // written out at length a tile took 6,500 cycles, half of them waiting for
-// instructions.
+// instructions.  A role whose wait ran out leaves, and the roles that wait for it,
+// in both CTAs, run into the same limit in their turn.
 __device__ __noinline__ bool wait_long(uint32_t bar, uint32_t parity, uint32_t *status) {
     const uint64_t t0 = global_ns();
     for (uint32_t spin = 1;; ++spin) {
@@ -248,8 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::off_bar);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::bars);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
-    int *const bad = reinterpret_cast<int *>(tmem_slot + 4);  // of each stream (from the unit's first): its first V row that is not finite
+    int *const bad = reinterpret_cast<int *>(tmem_slot + 1);  // of each stream (from the unit's first): its first V row that is not finite
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int rank = static_cast<int>(cta_rank());
     {
@@ -283,7 +283,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mbar_init(&bars[L::drain], 1);
         mbar_init(&bars[L::drain + 1], 1);
-        *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == kWarpPv) {
@@ -320,11 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto all_shared = [&](int n) { return w.key0 + (n + 1) * kN <= g.shared; };
     const int *const info = reinterpret_cast<const int *>(smem + L::off_info);  // of tile n: + (n & 3) * 24
 
-    auto wait = [&](int bar, uint32_t phase) -> bool {
-        const bool ok = wait_on(&bars[bar], phase & 1, a.status);
-        if (!ok) *abort_flag = 1;
-        return ok;
-    };
+    auto wait = [&](int bar, uint32_t phase) -> bool { return wait_on(&bars[bar], phase & 1, a.status); };
     auto wait_warp = [&](int bar, uint32_t phase) -> bool { return __all_sync(0xffffffffu, wait(bar, phase)); };
     // The arrivals of the last products at the slots' barriers, which come to both CTAs
     // of the pair whether or not a copy waits for the slot: neither CTA leaves before.
