@@ -113,3 +113,60 @@ def test_nor_later_scales_that_are_not_finite(ptok, bits):
     reads = np.zeros(a.shape, bool)
     reads[3:5, 2:] = True
     assert np.array_equal(a[~reads], b[~reads]) and (~np.isfinite(a[3:5, 2:])).any(-1).all() and int(st) == pkv.DEV_RANGE
+
+
+SMALL = [([9, 4], 3), ([5, 7], 2)]
+ODD = [([90, 40, 33], 3), ([50, 60], 2)]
+SHAPES = [   # layers, KV heads, indexer dims, groups, new tokens, page size, query heads, small calls' ballast
+    *((2, 2, 128, [([3, 40], pages)], 1, ptok, 8, 24) for ptok, pages in ((128, 1), (256, 3), (16, 5), (48, 9), (64, 4), (4, 1), (4, 67), (20, 20))),
+    *((1, hkv, 0, [([new, 70, 33], 700 // ptok), ([90], 5), ([21, 300], 0), ([15, 16, 17, 18, 500], 1300 // ptok), ([64, 9], 2)],
+       [new, new, 0, new, new, new, 0, new, new, 0, new, new, 0], ptok, hq, 24)
+      for ptok in (16, 20, 128) for hkv, hq, new in ((1, 4, 1), (2, 16, 2), (1, 32, 1), (3, 3, 4), (4, 20, 3))),
+    *((1, 1, 0, [([new + 2 * i for i in range(n)], 3)], new, 64, hq, 20) for n, new, hq in ((2, 1, 1), (33, 1, 1), (43, 3, 1), (2, 4, 8), (9, 1, 29))),
+    *((1, 2, 128, [([400, 5, 1, 77, 128, 129, 250, 31], 9000 // ptok)], 1, ptok, 16, 24) for ptok in (256, 48, 128, 4)),
+    *((1, 2, 0, [([40, 60, 7], 12)], new, 128, hq, 24) for new, hq in ((2, 8), (1, 2))),
+    (1, 2, 0, [([9, 4], 6)], 1, 128, 8, 24), (1, 1, 0, [([9, 4], 4)], 1, 128, 4, 24), (1, 1, 0, [([9, 4], 3)], 1, 64, 4, 24),
+    *((2, 2, 128, [([3, 40, 17], 8), ([33, 5], 0)], [1, 2, 3, 1, 4], ptok, 16, 24) for ptok in (16, 20, 128)),
+    *((1, 2, idx, [([30, 7, 200], 20)], 1, ptok, 16, 24) for idx, ptok in ((128, 48), (128, 64))),
+    *((1, 2, 0, [(own, pages)], new, 64, 16, 24) for own, pages, new in (([700, 3, 650], 40, 3), ([1, 1, 1], 90, 1), ([640, 641, 4], 1, 4), ([100, 90, 80], 7, 2))),
+    *((1, 2, 0, groups, new, ptok, 4, 24) for groups, new, ptok in ((SMALL, 1, 64), (ODD, [1, 2, 1, 1, 3], 64), (ODD, [1, 2, 1, 1, 3], 20))),
+    *((1, 1, 0, [([9, 4], 3), ([5, 7], 6)], 1, ptok, 4, 24) for ptok in (64, 128, 20)),
+    (1, 2, 128, [([60, 90, 75], 9), ([40], 0)], 1, 64, 16, 24),
+]
+
+
+@pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("shape", range(len(SHAPES)))
+def test_calls_meant_to_read_together_do(fmt, shape):
+    """The shapes that stand for calls whose streams are read together, beside a large group, are: not the windowed decode's bits."""
+    layers, hkv, idx, groups, new, ptok, hq, ballast = SHAPES[shape]
+    s = Shared(pkv.layout(layers, hkv, 256, idx, fmt), groups, new, ptok, n_q_heads=hq, ballast=ballast)
+    assert not decoded_alone(s, s.call())
+
+
+@pytest.mark.parametrize("fmt", [BF, E4])
+@pytest.mark.parametrize("ptok", [64, 128, 16])
+@pytest.mark.parametrize("last", [False, True], ids=["before", "behind"])
+def test_more_bases_than_a_call_has_maps(fmt, ptok, last):
+    """Eighteen contiguous streams, each of a buffer of its own, before (behind) groups that share: the groups (the last streams) go key by key."""
+    t, lay, hq, n = torch(), pkv.layout(1, 2, 256, 0, fmt), 8, 18
+    a = Shared(lay, [([100 + 5 * i], 0) for i in range(n)], [1 + i % 3 for i in range(n)], ptok, n_q_heads=hq, seed=1)
+    b = Shared(lay, [([33, 4, 150], 5), ([20, 21], 3)], 2, ptok, n_q_heads=hq, seed=2, ballast=24)
+    buffers = [t.full((1, pkv.page_elems(lay, 192)), 0x7FC1, dtype=t.int16, device="cuda") for _ in range(n)]
+    lone = []
+    for i, x in enumerate(buffers):
+        g, length = pkv.Pg(x.data_ptr(), None, x.shape[1], 192, 1, 1, 0), a.lens[i]
+        pkv.store(lay, [pkv.seq(g, length, length)], 0, a.dev(a.k[i]), a.dev(a.v[i]))
+        lone.append(pkv.seq(g, length, a.new[i]))
+    order = (b, a) if last else (a, b)
+    seqs = b.seqs + lone if last else lone + b.seqs
+    groups = b.groups + a.groups if last else a.groups + b.groups
+    q, st = t.cat([s.dq for s in order]), t.zeros(1, dtype=t.int32, device="cuda")
+    ws = t.full((max(64, pkv.prefix_decode_ws_size(lay, seqs, groups, hq) // 4),), float("nan"), device="cuda")
+    out = t.full((q.shape[0] + 1, hq, 256), 77, dtype=t.int16, device="cuda")
+    pkv.prefix_decode(lay, seqs, groups, 0, hq, q, out, ws, status=st)
+    assert int(st) == 0
+    at = 0
+    for s in order:
+        s.check(t.cat([out[at:at + s.dq.shape[0]], out[-1:]]))
+        at += s.dq.shape[0]

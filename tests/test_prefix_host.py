@@ -77,3 +77,9 @@ def test_python_refuses():
         with pytest.raises(pkv.PkvError) as e:
             pkv.prefix_decode_ws_size(lay, seqs, groups, 4)
         assert e.value.code == pkv.EINVAL
+
+
+def test_nothing_to_do_needs_no_gpu(lib):
+    """A call without new tokens, or without streams, returns before it asks for a GPU."""
+    assert _call(lib, seqs=((100, 0, 0), (90, 0, 0)), q=None, out=None, ws=None, ws_bytes=0) == pkv.OK
+    assert _call(lib, seqs=(), groups=(), q=None, out=None, ws=None, ws_bytes=0) == pkv.OK
