@@ -297,7 +297,8 @@ int pkv_store(const pkv_layout *layout, const pkv_seq *seqs, int32_t n_seqs, int
  * for position p; the row's other elements stay.  float32 arithmetic, one
  * rounding at the end.  An angle is p times the pair's frequency in turns as a
  * 64-bit fixed-point fraction, whose wrap-around takes off the whole turns
- * exactly: positions as far as int32 goes lose nothing.  Rotating by -p takes
+ * exactly.  The frequencies are computed in float64: at a position of 2^31 that
+ * leaves an angle less than 2^-22 of a turn off.  Rotating by -p takes
  * a rotation by p back (scale 1), and is its gradient. */
 #define PKV_ROPE_HALF 0
 #define PKV_ROPE_INTERLEAVED 1
@@ -540,7 +541,14 @@ int pkv_window_dead_pages(int32_t page_pos, int32_t len, int32_t window, int32_t
  * others do not must hold finite values.)  e4m3 V rows of any scale from 2^-40 to 2^80
  * keep their precision.
  * Results follow the call's shape (its groups, lengths and new tokens), not where
- * its pages lie.
+ * its pages lie.  Read together, a stream's roundings also follow the rows of the
+ * group's other streams, within the attention tolerance.
+ * Pages that hold whole runs of 16 positions are copied by tensor maps, others key
+ * by key, several times as slow: positions a multiple of 16, and a page's and a
+ * layer's bytes multiples of 512 (e4m3: of 256; without indexer rows a page of 16
+ * positions and one KV head is not).  A call holds 16 maps, one a base and up to
+ * three where pages hold 64 positions, taken in the groups' order: with more bases
+ * than that the last groups go key by key.
  * ws: device, >= pkv_prefix_decode_ws_size bytes, 256-byte aligned, no
  * initialization, one ws per in-flight call.  The size for the longest own parts
  * (len - n_pages * page_pos; in a group of one stream, which shares nothing, len)

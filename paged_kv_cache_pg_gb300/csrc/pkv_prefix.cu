@@ -1256,9 +1256,14 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtas)
 
 // Cost model in nanoseconds, fitted to 124 calls of 2 to 64 streams (128 to 31,000
 // shared positions, 100 to 2,000 own, 1 or 4 new tokens, 1 or 2 KV heads of 8
-// columns; within 14 % of each): a pair's tile of 128 shared keys (bf16, e4m3), its
-// start and end, a hundred rows of partials written and read again, and the merging
-// kernel.
+// columns): a coefficient for a pair's tile of 128 shared keys (bf16, e4m3), one for
+// its start and end, for a hundred rows of partials written and read again, and for
+// the merging kernel.  Within 14 % of each of those calls as the kernel was then.  It
+// has become faster since, and a tile's coefficient is above a tile's time: 64
+// streams on 31,000 positions 66.6 us modelled, 52.6 measured; 32 of e4m3 pages on
+// 24,000 41.4, 34.4; four prompts 32.1, 26.0; eight samples 18.5, 20.0.  Where the
+// model is far off, decoding alone costs twice as much and more (60 us for the four
+// prompts), so the choice does not hang on it.
 constexpr int64_t kTileCost[2] = {2200, 3000}, kPairCost = 7200, kRowsCost = 22, kMergeCost[2] = {4500, 5300};
 // ... and of the streams decoded alone: start, a thousand units of the windowed
 // plan's cost, a million keys, and what those take more with more than eight columns
@@ -1267,9 +1272,11 @@ constexpr int64_t kAloneCost[2] = {-800, 10000}, kAloneUnits[2] = {2200, 610}, k
 
 }  // namespace
 
-// Keys are split into whole tiles, all units by the same number, so that the
-// pairs fill the GPU about once; the count never passes the pairs the GPU holds
-// (or one a unit), which bounds the workspace whatever the lengths.
+// Keys are split into whole tiles, each split of any unit up to the same cost `per`,
+// so that the pairs fill the GPU about once; the count of splits never passes the
+// pairs the GPU holds (or one a unit), which bounds the workspace whatever the
+// lengths.  (Units that do not divide the pairs leave some empty: five equal prompts
+// at 8 KV heads are 40 splits for 76 pairs.)
 void plan_prefix(const Common &c, int nsm, PrefixPlan *plan) {
     const int64_t H = c.n_kv_heads, slots = std::max(1, nsm / 2);
     plan->n_units = 0;

@@ -2,9 +2,10 @@
 // (pkv_rope_rows) or on the way into the pages (pkv_rope_store).
 //
 // Pair i of a row at position p turns by p f_i.  The frequencies come as
-// fractions of a turn times 2^64, so p times one, modulo 2^64, is the angle
-// without its whole turns, exact to 2^-64 of a turn a position; its top 32 bits
-// (a signed fraction of a half turn) go to sincospif.  In float32 radians a
+// fractions of a turn times 2^64, so p times one, modulo 2^64, is that product
+// without its whole turns, exactly (the frequency itself is a float64's: 2^-22 of a
+// turn at most at a position of 2^31); its top 32 bits (a signed fraction of a half
+// turn) go to sincospif.  In float32 radians a
 // position of 10^6 would leave 0.03 of the fastest pair's angle to chance.
 //
 // A small call has a CTA a token.  A large one is cut into units of up to four
@@ -141,7 +142,7 @@ struct TokenAt {
     int32_t pos;        // what its rows turn by
 };
 
-// Stream of a token: the streams' first tokens are compared by a warp's lanes.
+// Stream of a token, found by one thread.
 __device__ __forceinline__ int stream_of(const Common &c, const RopeTokens &tk, int32_t tok) {
     return find_seq(c.n_seqs, tok, [&](int t) { return tk.tok_off[t]; });
 }
