@@ -208,9 +208,19 @@ __device__ __forceinline__ void through_units(const pkv_rope &rope, const RopeTo
         const int s = it & 1;
         if (kTurns && !(before && it == 0)) fill(turns, rope.scale, at[s], now.n, cs);
         __syncthreads();
-        if (mbar_wait(&full[s], (it >> 1) & 1, status)) rows(now, s);
-        if (!more) return;
-        __syncthreads();  // the stage, its places and the turns are done with
+        const bool there = mbar_wait(&full[s], (it >> 1) & 1, status);
+        if (there) rows(now, s);
+        // Where a wait ran out no barrier is used again, and what is on its way lands
+        // (or another limit passes) before the memory goes
+        if (!more) {
+            if (!there) mbar_wait(&full[s], (it >> 1) & 1, nullptr);
+            return;
+        }
+        if (__syncthreads_or(!there)) {  // (the stage, its places and the turns are done with)
+            mbar_wait(&full[s], (it >> 1) & 1, nullptr);
+            mbar_wait(&full[s ^ 1], ((it + 1) >> 1) & 1, nullptr);
+            return;
+        }
         now = next;
         u += tk.ctas;
         more = u < tk.units;
