@@ -328,7 +328,8 @@ typedef struct pkv_rope {
 int pkv_rope_init(int32_t rot_dim, int32_t pairs, double base, int32_t scaling, double factor,
                   int32_t original, double fast, double slow, double scale, pkv_rope *out);
 /* The same from frequencies of the caller's own: rot_dim / 2 of them, in radians
- * a position. */
+ * a position, and the scale as it is given (0 makes rows of zeros).  EINVAL: the
+ * same of rot_dim and pairs, anything not finite. */
 int pkv_rope_from_freqs(int32_t rot_dim, int32_t pairs, const double *radians, double scale,
                         pkv_rope *out);
 
