@@ -33,7 +33,7 @@
 // them; a unit of one split writes its output itself.
 //
 // Of 64 streams on 31,000 shared positions (16 query and 2 KV heads, up to 1,000 own
-// positions each; 148 MB, 33.2 GFLOP) a call takes 53.1 us, 624 TFLOP/s: 23 tiles a
+// positions each; 148 MB, 33.2 GFLOP) a call takes 52.5 us, 632 TFLOP/s: 23 tiles a
 // pair of 2,950 cycles, whose 24 products alone take the tensor core 2,620 (16 of N =
 // 128 at 96, 8 of N = 256 at 135), 6 us to the first tile, 4.5 for the sums' way out
 // and 6 for the merge.  32 streams on 24,000 positions of e4m3 pages take 34.5 us:

@@ -11,7 +11,7 @@
 // A small call has a CTA a token.  A large one is cut into units of up to four
 // tokens, and as many CTAs as the GPU holds take every so many-th, the next unit's
 // rows on their way while one's are turned: a prompt of 8,192 tokens of 16 query and
-// 2 KV heads (172 MB) takes 30.9 us, 82 % of the copy rate (CTAs of a unit each took
+// 2 KV heads (172 MB) takes 31.7 us, 80 % of the copy rate (CTAs of a unit each took
 // 1.2 us longer, units of 48 KB and two CTAs an SM 3.8).  What is left: the first
 // rows' way in and the last ones' way out, and 7 units of 6.7 a CTA.  A
 // unit's tokens' streams, pages and rows are found once, by a thread a token (the
