@@ -118,10 +118,10 @@ def test_store_refuses(lib):
 @pytest.mark.parametrize("bad", [
     dict(qo=0x300000), dict(qo=0x300000 + 512), dict(qo=0x400000 - 1024), dict(qo=0x500000 - 2048 + 16), dict(qo=0x500000 + 128),
     dict(qo=0x400000, q=0x400000),                                                         # the queries and the values are the same rows
-    # one projection's rows of 2,304 elements (4 query heads, 2 of keys and of values, 128 indexer elements and 128 unused):
-    # queries out over the keys, over the end of the keys' and the indexer's row
-    *(dict(q=0x100000, qs=2304, qos=2304, k=0x100000 + 2048, ks=2304, v=0x100000 + 3072, vs=2304, ik=0x100000 + 4096, iks=2304, qo=0x100000 + at)
-      for at in (2048, 3072 - 16, 4096 + 240))])
+    # one projection's rows of 2,304 elements (1,024 of queries, 2 heads of keys, 64 unused, 2 of values, 128 indexer elements, 64 unused):
+    # queries out over the keys, the values' first elements and the indexer's last ones
+    *(dict(q=0x700000, qos=2304, k=0x100000 + 2048, ks=2304, v=0x100000 + 3200, vs=2304, ik=0x100000 + 4224, iks=2304, qo=0x100000 + at)
+      for at in (2048, 3200 - 2048 + 16, 4224 + 240))])
 def test_store_refuses_queries_written_over_its_other_rows(lib, bad, n_new):
     assert _store(lib, n_new=n_new, **bad) == pkv.EINVAL
 
