@@ -170,3 +170,15 @@ def test_more_bases_than_a_call_has_maps(fmt, ptok, last):
     for s in order:
         s.check(t.cat([out[at:at + s.dq.shape[0]], out[-1:]]))
         at += s.dq.shape[0]
+
+
+@pytest.mark.parametrize("fmt", [BF, E4])
+def test_one_stream_left_stores_its_rows(fmt):
+    """... beyond the windowed decode's workspace, with the new rows stored by the call: pages and bits as by a store before it."""
+    t, lay = torch(), pkv.layout(1, 40, 256, 128, fmt)
+    a, b = (Shared(lay, [([20, 9, 30], 11), ([30], 0)], [0, 2, 0, 1], 64, n_q_heads=40, fused=True) for _ in range(2))
+    pkv.store(lay, b.seqs, 0, b.k_new, b.v_new, b.ik_new)
+    b.fused = False
+    one, two = a.call(), b.call()
+    a.check(one)
+    assert t.equal(a.mem, b.mem) and t.equal(one, two) and not decoded_alone(a, one)
